@@ -459,6 +459,135 @@ RM_API rm_status rm_token_mix(const void *X, void *Y, int B, int T, int D, int H
  * overlapping.  Runs on the current device; asynchronous on `stream`. */
 RM_API rm_status rm_debug_mix_residual(const void *X, int from_z, float *Y, int B, int T, int D, void *stream);
 
+/* ---- 8-bit operands and checkpoints ------------------------------------
+ *
+ * An 8-bit tensor holds codes of one byte (e4m3: largest value 448; e5m2:
+ * 57344) and one exponent byte E per block of 128 consecutive values of a row
+ * (activations) or per block of 128 x 128 values (weights); a value is
+ * code * 2^(E - 127).  The calls below that make such tensors choose, for every
+ * block, the smallest E for which the block's largest finite magnitude is at
+ * most the format's largest value (at least 1; 127 for a block of zeros), and
+ * round value / 2^(E - 127) to the nearest code, ties to even.  Infinities and
+ * NaN become NaN codes and do not count for E.  A power-of-two scale loses no
+ * bits of its own: restoring a code is exact in float32 (and in bf16, except
+ * below 2^-133), and the tensor cores apply it without a rounding.  E = 255
+ * stands for NaN.
+ *   Activations: row-major [B][T][cols]; row r = b T + t has its codes at
+ *     codes + r ld (ld >= cols, a multiple of 16) and the byte of its block j
+ *     at scales + r lds + j (lds >= ceil(cols / 128), a multiple of 4).
+ *   Weights: [T][K][N] in the layout of rm_layer_params (y = x W); row r =
+ *     t K + k of codes as above, and the byte of the block (i, j) of token t's
+ *     matrix at scales + (t ceil(K / 128) + i) lds + j.  One copy serves the
+ *     forward product and, through transpose_w, the data gradient.
+ * codes must be 16-byte, scales 4-byte aligned.  Rows are padded: bytes past
+ * cols (codes) and past the last block (scales) are never interpreted.
+ *
+ * These calls need no context: they run on the current device, which must own
+ * the buffers, on `stream`, allocate nothing, keep nothing between calls and
+ * may be captured into a CUDA graph.  Calls on different streams are
+ * independent when their buffers (and workspaces) are.  Device-side errors (a
+ * bounded wait that ran out) are latched per device and reported by
+ * rm_fp8_sync_status. */
+typedef enum rm_fp8_format {
+    RM_E4M3 = 0,
+    RM_E5M2 = 1
+} rm_fp8_format;
+
+typedef struct rm_fp8_tensor {
+    void *codes;             /* device */
+    unsigned char *scales;   /* device */
+    long long ld;            /* bytes between rows of codes */
+    long long lds;           /* bytes between rows of scales */
+    rm_fp8_format format;
+} rm_fp8_tensor;
+
+/* Save rows in 8 bits: X device [rows][ldx] of dtype (only the element's own
+ * alignment is needed; rows that are 16-byte aligned run faster), cols values
+ * of each row.  rows = B T. */
+RM_API rm_status rm_fp8_quantize(const void *X, rm_dtype dtype, long long rows, int cols, long long ldx,
+                                 const rm_fp8_tensor *out, void *stream);
+
+/* The same for weights W device [T][K][N] (contiguous): blocks of 128 x 128. */
+RM_API rm_status rm_fp8_quantize_weight(const void *W, rm_dtype dtype, int T, int K, int N, const rm_fp8_tensor *out,
+                                        void *stream);
+
+/* Restore rows kept in 8 bits: Y device [rows][ldy] of dtype. */
+RM_API rm_status rm_fp8_dequantize(const rm_fp8_tensor *in, long long rows, int cols, void *Y, rm_dtype dtype,
+                                   long long ldy, void *stream);
+
+/* Per-token product of 8-bit operands,
+ *   Y[b][t][n] = sum_k x[b][t][k] W[t][k][n] + bias[t][n]
+ * (transpose_w: W is [T][N][K] and the sum runs over its last index: the data
+ * gradient of the forward product).  x: [B][T][K], either format; W: e4m3;
+ * bias (nullable): device float32 [T][N]; Y: device [B][T][N] of dtype,
+ * contiguous.  Products and sums in float32, one rounding to dtype. */
+RM_API rm_status rm_fp8_matmul(const rm_fp8_tensor *x, const rm_fp8_tensor *W, const float *bias, void *Y,
+                               rm_dtype dtype, int B, int T, int K, int N, int transpose_w, void *stream);
+
+/* Gradients of a per-token linear layer from its input kept in 8 bits:
+ *   dW[t][k][n] = sum_b x[b][t][k] dY[b][t][n],  db[t][n] = sum_b dY[b][t][n].
+ * x: [B][T][K], e4m3; dY: device bf16 [B][T][N], contiguous, N a multiple of 8
+ * (RM_ERR_UNSUPPORTED otherwise); dW [T][K][N] and db [T][N] (either may be
+ * NULL): device, of dtype, overwritten.  Sums in float32, in an order that
+ * depends on the sizes alone. */
+RM_API rm_status rm_fp8_wgrad(const rm_fp8_tensor *x, const void *dY, void *dW, void *db, rm_dtype dtype, int B, int T,
+                              int K, int N, void *stream);
+
+/* A per-token FFN ("RankMixer" section 3.3.2 Eq. 6-9) with 8-bit weights:
+ * W1 [T][D][F] and W2 [T][F][D] in e4m3, b1 [T][F] and b2 [T][D] float32.
+ * D and F multiples of 16 (RM_ERR_UNSUPPORTED otherwise). */
+typedef struct rm_fp8_pffn {
+    rm_fp8_tensor W1, W2;
+    const float *b1, *b2;
+    int T, D, F;
+} rm_fp8_pffn;
+
+/* What a training forward keeps for the backward pass, 8-bit activations that
+ * the caller allocates: the input x [B][T][D], the hidden pre-activation u and
+ * the hidden activation a [B][T][F], all e4m3: D + 2 F bytes per row (and 1 in
+ * 128 for the scales). */
+typedef struct rm_fp8_kept {
+    rm_fp8_tensor x, u, a;
+} rm_fp8_kept;
+
+/* Gradients, device buffers of dtype, overwritten: dW1 [T][D][F], db1 [T][F],
+ * dW2 [T][F][D], db2 [T][D]. */
+typedef struct rm_fp8_grads {
+    void *dW1, *db1, *dW2, *db2;
+    rm_dtype dtype;
+} rm_fp8_grads;
+
+/* Bytes of device workspace (16-byte aligned) that a call with batch B needs:
+ * the forward without kept activations (serving), or with them, or the backward. */
+typedef enum rm_fp8_pass {
+    RM_FP8_SERVE = 0,
+    RM_FP8_TRAIN = 1,
+    RM_FP8_BACKWARD = 2
+} rm_fp8_pass;
+RM_API rm_status rm_fp8_pffn_workspace(const rm_fp8_pffn *p, int B, rm_fp8_pass pass, long long *bytes);
+
+/* Forward: with Q the 8-bit rounding above,
+ *   x = Q(X), u = x W1 + b1, a = Q(Gelu(u)), V = a W2 + b2.
+ * X: device [B][T][D] of x_dtype; V: device [B][T][D] of v_dtype.  keep NULL:
+ * serving (RM_FP8_SERVE workspace); else x, Q(u) and a are kept (RM_FP8_TRAIN). */
+RM_API rm_status rm_fp8_pffn_forward(const rm_fp8_pffn *p, const void *X, rm_dtype x_dtype, void *V, rm_dtype v_dtype,
+                                     const rm_fp8_kept *keep, int B, void *work, long long work_bytes, void *stream);
+
+/* Backward from the kept activations, for the gradient dV at V:
+ *   dU = (Q(dV) W2^T) Gelu'(u),  dX = Q(dU) W1^T,
+ *   dW2 = a^T dV, db2 = sum dV,  dW1 = x^T dU, db1 = sum dU   (sums over b).
+ * dV: device [B][T][D] of dv_dtype; dX (nullable): device [B][T][D] of
+ * dx_dtype.  The weight gradients take dV and dU rounded to bf16.  kept is
+ * read only: a second backward from it gives the same values. */
+RM_API rm_status rm_fp8_pffn_backward(const rm_fp8_pffn *p, const void *dV, rm_dtype dv_dtype, const rm_fp8_kept *kept,
+                                      void *dX, rm_dtype dx_dtype, const rm_fp8_grads *grads, int B, void *work,
+                                      long long work_bytes, void *stream);
+
+/* Synchronise `stream`, then report and clear the current device's error word
+ * of the calls above: RM_OK, RM_ERR_TIMEOUT or RM_ERR_DEVICE (RM_ERR_CUDA if
+ * the synchronisation itself failed). */
+RM_API rm_status rm_fp8_sync_status(void *stream);
+
 /* Synchronise `stream`, then report and clear the context's device error
  * word: RM_OK, RM_ERR_TIMEOUT or RM_ERR_DEVICE (or RM_ERR_CUDA if the
  * synchronisation itself failed). */

@@ -35,6 +35,13 @@ RM_PATH_AUTO = 0
 RM_PATH_SIMT = 1
 RM_PATH_TCGEN05 = 2
 
+# rm_fp8_format, rm_fp8_pass
+RM_E4M3 = 0
+RM_E5M2 = 1
+RM_FP8_SERVE = 0
+RM_FP8_TRAIN = 1
+RM_FP8_BACKWARD = 2
+
 # rm_kernel_kind
 KERNEL_KINDS = ["mix_ln1", "gemm1", "gemm2", "ln2_out", "pool", "rowstats", "moe_route", "moe_gemm1",
                 "moe_gemm2", "misc", "moe_combine", "bwd_recompute", "bwd_dgrad", "bwd_wgrad", "bwd_rows",
@@ -48,7 +55,9 @@ EXPORTED = ["rm_create", "rm_destroy", "rm_block_forward", "rm_stack_forward", "
             "rm_debug_gelu_grad", "rm_stack_forward_train", "rm_stack_backward_saved", "rm_head_forward",
             "rm_set_tokenizer", "rm_tokenize", "rm_score", "rm_moe_pffn_forward_train", "rm_tokenize_backward",
             "rm_set_unimixing", "rm_unimixing_weights", "rm_unimixing", "rm_debug_mix_residual",
-            "rm_debug_fail_alloc", "rm_debug_alloc_stats", "rm_stack_forward_host_async", "rm_host_wait"]
+            "rm_debug_fail_alloc", "rm_debug_alloc_stats", "rm_stack_forward_host_async", "rm_host_wait",
+            "rm_fp8_quantize", "rm_fp8_quantize_weight", "rm_fp8_dequantize", "rm_fp8_matmul", "rm_fp8_wgrad",
+            "rm_fp8_pffn_workspace", "rm_fp8_pffn_forward", "rm_fp8_pffn_backward", "rm_fp8_sync_status"]
 
 
 class rm_config(ctypes.Structure):
@@ -81,6 +90,25 @@ class rm_kernel_stat(ctypes.Structure):
     _fields_ = [("launches", ctypes.c_longlong), ("total_ms", ctypes.c_double)]
 
 
+class rm_fp8_tensor(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("ld", ctypes.c_longlong),
+                ("lds", ctypes.c_longlong), ("format", ctypes.c_int)]
+
+
+class rm_fp8_pffn(ctypes.Structure):
+    _fields_ = [("W1", rm_fp8_tensor), ("W2", rm_fp8_tensor), ("b1", ctypes.c_void_p), ("b2", ctypes.c_void_p),
+                ("T", ctypes.c_int), ("D", ctypes.c_int), ("F", ctypes.c_int)]
+
+
+class rm_fp8_kept(ctypes.Structure):
+    _fields_ = [("x", rm_fp8_tensor), ("u", rm_fp8_tensor), ("a", rm_fp8_tensor)]
+
+
+class rm_fp8_grads(ctypes.Structure):
+    _fields_ = [("dW1", ctypes.c_void_p), ("db1", ctypes.c_void_p), ("dW2", ctypes.c_void_p),
+                ("db2", ctypes.c_void_p), ("dtype", ctypes.c_int)]
+
+
 class RankMixerError(RuntimeError):
     def __init__(self, status: int, where: str, msg: str):
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}: {msg}")
@@ -101,6 +129,8 @@ def load() -> ctypes.CDLL:
                            f"g.build()'` (there is no non-CUDA fallback)")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i, st = ctypes.c_void_p, ctypes.c_int, ctypes.c_int
+    ll, t8 = ctypes.c_longlong, ctypes.POINTER(rm_fp8_tensor)
+    ffn8, kept8 = ctypes.POINTER(rm_fp8_pffn), ctypes.POINTER(rm_fp8_kept)
     sig = {
         "rm_create": (st, [ctypes.POINTER(rm_config), ctypes.POINTER(rm_layer_params), i, ctypes.POINTER(vp)]),
         "rm_destroy": (st, [vp]),
@@ -137,6 +167,15 @@ def load() -> ctypes.CDLL:
         "rm_debug_mix_residual": (st, [vp, i, vp, i, i, i, vp]),
         "rm_debug_fail_alloc": (st, [ctypes.c_longlong]),
         "rm_debug_alloc_stats": (st, [ctypes.POINTER(ctypes.c_longlong)] * 3),
+        "rm_fp8_quantize": (st, [vp, i, ll, i, ll, t8, vp]),
+        "rm_fp8_quantize_weight": (st, [vp, i, i, i, i, t8, vp]),
+        "rm_fp8_dequantize": (st, [t8, ll, i, vp, i, ll, vp]),
+        "rm_fp8_matmul": (st, [t8, t8, vp, vp, i, i, i, i, i, i, vp]),
+        "rm_fp8_wgrad": (st, [t8, vp, vp, vp, i, i, i, i, i, vp]),
+        "rm_fp8_pffn_workspace": (st, [ffn8, i, i, ctypes.POINTER(ll)]),
+        "rm_fp8_pffn_forward": (st, [ffn8, vp, i, vp, i, kept8, i, vp, ll, vp]),
+        "rm_fp8_pffn_backward": (st, [ffn8, vp, i, kept8, vp, i, ctypes.POINTER(rm_fp8_grads), i, vp, ll, vp]),
+        "rm_fp8_sync_status": (st, [vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -303,6 +342,51 @@ def rm_debug_alloc_stats() -> tuple[int, int, int]:
     v = [ctypes.c_longlong() for _ in range(3)]
     check(load().rm_debug_alloc_stats(*[ctypes.byref(x) for x in v]), "rm_debug_alloc_stats")
     return v[0].value, v[1].value, v[2].value
+
+
+def rm_fp8_quantize(X: int, dtype: int, rows: int, cols: int, ldx: int, out: rm_fp8_tensor, stream: int) -> None:
+    check(load().rm_fp8_quantize(X, dtype, rows, cols, ldx, out, stream), "rm_fp8_quantize")
+
+
+def rm_fp8_quantize_weight(W: int, dtype: int, T: int, K: int, N: int, out: rm_fp8_tensor, stream: int) -> None:
+    check(load().rm_fp8_quantize_weight(W, dtype, T, K, N, out, stream), "rm_fp8_quantize_weight")
+
+
+def rm_fp8_dequantize(q: rm_fp8_tensor, rows: int, cols: int, Y: int, dtype: int, ldy: int, stream: int) -> None:
+    check(load().rm_fp8_dequantize(q, rows, cols, Y, dtype, ldy, stream), "rm_fp8_dequantize")
+
+
+def rm_fp8_matmul(x: rm_fp8_tensor, W: rm_fp8_tensor, bias: int | None, Y: int, dtype: int, B: int, T: int, K: int,
+                  N: int, transpose_w: bool, stream: int) -> None:
+    check(load().rm_fp8_matmul(x, W, bias, Y, dtype, B, T, K, N, 1 if transpose_w else 0, stream), "rm_fp8_matmul")
+
+
+def rm_fp8_wgrad(x: rm_fp8_tensor, dY: int, dW: int | None, db: int | None, dtype: int, B: int, T: int, K: int, N: int,
+                 stream: int) -> None:
+    check(load().rm_fp8_wgrad(x, dY, dW, db, dtype, B, T, K, N, stream), "rm_fp8_wgrad")
+
+
+def rm_fp8_pffn_workspace(p: rm_fp8_pffn, B: int, pass_: int) -> int:
+    n = ctypes.c_longlong()
+    check(load().rm_fp8_pffn_workspace(p, B, pass_, ctypes.byref(n)), "rm_fp8_pffn_workspace")
+    return n.value
+
+
+def rm_fp8_pffn_forward(p: rm_fp8_pffn, X: int, x_dtype: int, V: int, v_dtype: int, keep: rm_fp8_kept | None, B: int,
+                        work: int | None, work_bytes: int, stream: int) -> None:
+    check(load().rm_fp8_pffn_forward(p, X, x_dtype, V, v_dtype, keep, B, work, work_bytes, stream),
+          "rm_fp8_pffn_forward")
+
+
+def rm_fp8_pffn_backward(p: rm_fp8_pffn, dV: int, dv_dtype: int, kept: rm_fp8_kept, dX: int | None, dx_dtype: int,
+                         grads: rm_fp8_grads, B: int, work: int | None, work_bytes: int, stream: int) -> None:
+    check(load().rm_fp8_pffn_backward(p, dV, dv_dtype, kept, dX, dx_dtype, grads, B, work, work_bytes, stream),
+          "rm_fp8_pffn_backward")
+
+
+def rm_fp8_sync_status(stream: int) -> int:
+    """Returns the raw status (RM_OK, RM_ERR_TIMEOUT, ...) without raising."""
+    return load().rm_fp8_sync_status(stream)
 
 
 def rm_debug_gelu_grad(u: int, out: int, n: int, stream: int) -> None:

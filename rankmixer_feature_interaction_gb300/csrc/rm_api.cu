@@ -49,6 +49,15 @@ thread_local const char* t_bounds_what = nullptr;
 
 }  // namespace
 
+void rm::set_last_error(const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+}
+
 cudaError_t rm::debug_bounds_fail(const char* what) {
     t_bounds_what = what;
     return cudaErrorInvalidValue;

@@ -36,6 +36,9 @@ cudaError_t debug_bounds_fail(const char* what);
         if (::rm::kDebugBounds && !(cond)) return ::rm::debug_bounds_fail(#cond); \
     } while (0)
 
+// Set what rm_last_error() returns on this host thread (printf-style).
+void set_last_error(const char* fmt, ...);
+
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) acts on the current device:
 // set it once per (kernel, device), so that a process driving several GPUs
 // gets it on each.
