@@ -32,21 +32,38 @@ cudaError_t launch_fp8_dequantize(const Fp8View& in, long long rows, int cols, v
 // float or bf16, in a fixed order.
 cudaError_t launch_fp8_colsum(const void* Y, void* out, bool out_f32, int B, int T, int N, cudaStream_t s);
 
-// Y[b][t][n] = sum_k x[b][t][k] W[t][k][n] (trans: W[t][n][k]) + bias[t][n].
-cudaError_t launch_fp8_matmul(const Fp8View& x, const Fp8View& w, bool trans, const float* bias, void* Y, bool y_f32,
-                              int B, int T, int K, int N, cudaStream_t s);
+// What the tensor-core kernels need of the current device: its SM count, the
+// error word that bounded waits latch and their bound.
+struct Fp8Device {
+    int num_sms;
+    int* err;
+    unsigned long long timeout_ns;
+};
+
+// acc[b][t][n] = sum_k x[b][t][k] W[t][k][n] (trans: W[t][n][k]), then
+//   FP8_OUT_*:  y = acc + bias (bias nullable)
+//   FP8_GELU:   u = acc + bias; o0 = Q(Gelu(u)) and, where o1.codes is not null, o1 = Q(u)
+//   FP8_DGELU:  dU = acc Gelu'(u) with u read from o1; o0 = Q(dU), y = dU in bf16, and its
+//               sums over 32 rows in colpart [T][fp8_colpart_rows(B)][N]
+enum Fp8Epilogue { FP8_OUT_BF16, FP8_OUT_F32, FP8_GELU, FP8_DGELU };
+struct Fp8Product {
+    Fp8Epilogue epi;
+    Fp8View x, w;
+    bool trans;
+    const float* bias;
+    void* y;
+    Fp8View o0, o1;
+    float* colpart;
+    int B, T, K, N;
+};
+int fp8_colpart_rows(int B);
+cudaError_t launch_fp8_product(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s);
+
+// out[t][n] = sum over r < R of part[t][r][n], of float or bf16, in a fixed order.
+cudaError_t launch_fp8_sum_parts(const float* part, void* out, bool out_f32, int R, int T, int N, cudaStream_t s);
 
 // dW[t][k][n] = sum_b x[b][t][k] dY[b][t][n], dY bf16 [B][T][N].
 cudaError_t launch_fp8_wgrad(const Fp8View& x, const void* dY, void* dW, bool w_f32, int B, int T, int K, int N,
-                             cudaStream_t s);
-
-// From u = x W1 + b1 [rows][cols] in float: a = Q(Gelu(u)) and, where u8.codes
-// is not null, u8 = Q(u).
-cudaError_t launch_fp8_gelu(const float* u, long long rows, int cols, const Fp8View& a, const Fp8View& u8,
-                            cudaStream_t s);
-
-// From dA [rows][cols] in float and the kept u8: dU = dA Gelu'(u) as d8 = Q(dU) and in bf16.
-cudaError_t launch_fp8_dgelu(const float* dA, long long rows, int cols, const Fp8View& u8, const Fp8View& d8, void* dU,
                              cudaStream_t s);
 
 }  // namespace rm

@@ -42,6 +42,33 @@ Fp8View view(const rm_fp8_tensor& t) {
 // rows are limited so that row and block numbers of every kernel fit 32-bit grids
 constexpr long long kMaxRows = 1ll << 31;
 
+constexpr unsigned long long kWaitTimeoutNs = 2000000000ull;    // bound of every device-side wait
+
+// The error word of the tensor-core kernels, one per device that loads the library.
+__device__ int g_fp8_error;
+
+// SM count and error word of the current device, looked up once per device.
+rm_status device_info(Fp8Device* out) {
+    static std::mutex mu;
+    static Fp8Device known_devices[64];
+    int d = 0;
+    RM_CHECK_CUDA(cudaGetDevice(&d), "cudaGetDevice");
+    if (d < 0 || d >= 64) return fail(RM_ERR_UNSUPPORTED, "device %d", d);
+    std::lock_guard<std::mutex> lk(mu);
+    Fp8Device& k = known_devices[d];
+    if (!k.err) {
+        int n = 0;
+        void* p = nullptr;
+        RM_CHECK_CUDA(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d), "SM count");
+        RM_CHECK_CUDA(cudaGetSymbolAddress(&p, g_fp8_error), "error word");
+        k.num_sms = n;
+        k.timeout_ns = kWaitTimeoutNs;
+        k.err = (int*)p;
+    }
+    *out = k;
+    return RM_OK;
+}
+
 rm_status check_tensor(const rm_fp8_tensor* t, int cols, const char* name, bool e4m3_only) {
     if (!t) return fail(RM_ERR_INVALID_ARG, "%s is NULL", name);
     if (!t->codes || !t->scales) return fail(RM_ERR_INVALID_ARG, "%s has NULL codes or scales", name);
@@ -105,7 +132,6 @@ struct Carver {
 
 struct ForwardWork {
     rm_fp8_kept kept;
-    float* u;
     long long bytes;
 };
 ForwardWork forward_work(const rm_fp8_pffn* p, int B, const rm_fp8_kept* keep, bool train, void* base) {
@@ -118,7 +144,6 @@ ForwardWork forward_work(const rm_fp8_pffn* p, int B, const rm_fp8_kept* keep, b
         w.kept.x = c.tensor(rows, p->D);
         w.kept.a = c.tensor(rows, p->F);
     }
-    w.u = (float*)c.take(rows * p->F * 4);
     w.bytes = c.used;
     return w;
 }
@@ -126,7 +151,7 @@ ForwardWork forward_work(const rm_fp8_pffn* p, int B, const rm_fp8_kept* keep, b
 struct BackwardWork {
     rm_fp8_tensor dv, du;
     void *dv16, *du16;
-    float* da;
+    float* colpart;
     long long bytes;
 };
 BackwardWork backward_work(const rm_fp8_pffn* p, int B, void* base) {
@@ -137,7 +162,7 @@ BackwardWork backward_work(const rm_fp8_pffn* p, int B, void* base) {
     w.du = c.tensor(rows, p->F);
     w.dv16 = c.take(rows * p->D * 2);
     w.du16 = c.take(rows * p->F * 2);
-    w.da = (float*)c.take(rows * p->F * 4);
+    w.colpart = (float*)c.take((long long)p->T * fp8_colpart_rows(B) * p->F * 4);
     w.bytes = c.used;
     return w;
 }
@@ -147,6 +172,15 @@ rm_status check_work(const void* work, long long have, long long need) {
     if (!aligned(work, 16)) return fail(RM_ERR_INVALID_ARG, "work must be 16-byte aligned");
     if (have < need) return fail(RM_ERR_INVALID_ARG, "work_bytes (%lld) is below the %lld needed", have, need);
     return RM_OK;
+}
+
+Fp8Product product(rm_dtype dtype, const rm_fp8_tensor& x, const rm_fp8_tensor& w, bool trans, const float* bias,
+                   void* y, int B, int T, int K, int N) {
+    Fp8Product p{};
+    p.epi = dtype == RM_F32 ? FP8_OUT_F32 : FP8_OUT_BF16;
+    p.x = view(x), p.w = view(w), p.trans = trans, p.bias = bias, p.y = y;
+    p.B = B, p.T = T, p.K = K, p.N = N;
+    return p;
 }
 
 }  // namespace
@@ -199,8 +233,9 @@ rm_status rm_fp8_matmul(const rm_fp8_tensor* x, const rm_fp8_tensor* W, const fl
     RM_CHECK(check_tensor(W, transpose_w ? K : N, "W", true));
     if (!aligned(Y, 16) || (bias && !aligned(bias, 16)))
         return fail(RM_ERR_INVALID_ARG, "Y and bias must be 16-byte aligned");
-    RM_CHECK_CUDA(launch_fp8_matmul(view(*x), view(*W), transpose_w != 0, bias, Y, dtype == RM_F32, B, T, K, N,
-                                    as_stream(stream)),
+    Fp8Device dev;
+    RM_CHECK(device_info(&dev));
+    RM_CHECK_CUDA(launch_fp8_product(product(dtype, *x, *W, transpose_w != 0, bias, Y, B, T, K, N), dev, as_stream(stream)),
                   "8-bit product");
     return RM_OK;
 }
@@ -248,10 +283,15 @@ rm_status rm_fp8_pffn_forward(const rm_fp8_pffn* p, const void* X, rm_dtype x_dt
     const int T = p->T, D = p->D, F = p->F;
     const long long rows = (long long)B * T;
     const cudaStream_t s = as_stream(stream);
+    Fp8Device dev;
+    RM_CHECK(device_info(&dev));
     RM_CHECK_CUDA(launch_fp8_quantize(x_dtype == RM_F32, X, rows, D, D, view(w.kept.x), nullptr, s), "quantize");
-    RM_CHECK_CUDA(launch_fp8_matmul(view(w.kept.x), view(p->W1), false, p->b1, w.u, true, B, T, D, F, s), "8-bit layer 1");
-    RM_CHECK_CUDA(launch_fp8_gelu(w.u, rows, F, view(w.kept.a), keep ? view(w.kept.u) : Fp8View{}, s), "gelu");
-    RM_CHECK_CUDA(launch_fp8_matmul(view(w.kept.a), view(p->W2), false, p->b2, V, v_dtype == RM_F32, B, T, F, D, s),
+    Fp8Product g = product(RM_BF16, w.kept.x, p->W1, false, p->b1, nullptr, B, T, D, F);
+    g.epi = FP8_GELU;
+    g.o0 = view(w.kept.a);
+    if (keep) g.o1 = view(w.kept.u);
+    RM_CHECK_CUDA(launch_fp8_product(g, dev, s), "8-bit layer 1");
+    RM_CHECK_CUDA(launch_fp8_product(product(v_dtype, w.kept.a, p->W2, false, p->b2, V, B, T, F, D), dev, s),
                   "8-bit layer 2");
     return RM_OK;
 }
@@ -276,22 +316,35 @@ rm_status rm_fp8_pffn_backward(const rm_fp8_pffn* p, const void* dV, rm_dtype dv
     const long long rows = (long long)B * T;
     const bool f32 = dv_dtype == RM_F32, g32 = grads->dtype == RM_F32;
     const cudaStream_t s = as_stream(stream);
+    Fp8Device dev;
+    RM_CHECK(device_info(&dev));
     const void* dv16 = f32 ? w.dv16 : dV;
     RM_CHECK_CUDA(launch_fp8_quantize(f32, dV, rows, D, D, view(w.dv), f32 ? w.dv16 : nullptr, s), "quantize dV");
-    RM_CHECK_CUDA(launch_fp8_matmul(view(w.dv), view(p->W2), true, nullptr, w.da, true, B, T, D, F, s), "dA");
-    RM_CHECK_CUDA(launch_fp8_dgelu(w.da, rows, F, view(kept->u), view(w.du), w.du16, s), "dU");
+    Fp8Product g = product(RM_BF16, w.dv, p->W2, true, nullptr, w.du16, B, T, D, F);
+    g.epi = FP8_DGELU;
+    g.o0 = view(w.du);
+    g.o1 = view(kept->u);
+    g.colpart = w.colpart;
+    RM_CHECK_CUDA(launch_fp8_product(g, dev, s), "dU");
     if (dX)
-        RM_CHECK_CUDA(launch_fp8_matmul(view(w.du), view(p->W1), true, nullptr, dX, dx_dtype == RM_F32, B, T, F, D, s),
-                      "dX");
+        RM_CHECK_CUDA(launch_fp8_product(product(dx_dtype, w.du, p->W1, true, nullptr, dX, B, T, F, D), dev, s), "dX");
     RM_CHECK_CUDA(launch_fp8_wgrad(view(kept->a), dv16, grads->dW2, g32, B, T, F, D, s), "dW2");
     RM_CHECK_CUDA(launch_fp8_colsum(dv16, grads->db2, g32, B, T, D, s), "db2");
     RM_CHECK_CUDA(launch_fp8_wgrad(view(kept->x), w.du16, grads->dW1, g32, B, T, D, F, s), "dW1");
-    RM_CHECK_CUDA(launch_fp8_colsum(w.du16, grads->db1, g32, B, T, F, s), "db1");
+    RM_CHECK_CUDA(launch_fp8_sum_parts(w.colpart, grads->db1, g32, fp8_colpart_rows(B), T, F, s), "db1");
     return RM_OK;
 }
 
 rm_status rm_fp8_sync_status(void* stream) {
-    const cudaError_t e = cudaStreamSynchronize(as_stream(stream));
+    cudaError_t e = cudaStreamSynchronize(as_stream(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rm_fp8_sync_status");
-    return RM_OK;
+    Fp8Device dev;
+    RM_CHECK(device_info(&dev));
+    int v = 0;
+    const int zero = 0;
+    RM_CHECK_CUDA(cudaMemcpy(&v, dev.err, sizeof v, cudaMemcpyDeviceToHost), "error word");
+    if (v == 0) return RM_OK;
+    RM_CHECK_CUDA(cudaMemcpy(dev.err, &zero, sizeof zero, cudaMemcpyHostToDevice), "error word");
+    return v == kDevErrTimeout ? fail(RM_ERR_TIMEOUT, "a device-side wait of an 8-bit operator ran out")
+                               : fail(RM_ERR_DEVICE, "device error %d in an 8-bit operator", v);
 }

@@ -7,7 +7,6 @@
 // per half warp are loaded before the first is used.
 #include "rm_common.cuh"
 #include "rm_fp8.cuh"
-#include "rm_train_math.cuh"
 
 namespace rm {
 namespace {
@@ -233,54 +232,21 @@ colsum_kernel(const __nv_bfloat16* __restrict__ Y, OUT* __restrict__ out, int B,
     }
 }
 
-__global__ void __launch_bounds__(kThreads)
-gelu_kernel(const float* __restrict__ U, unsigned long long blocks, int cols, int nb, Fp8View a, Fp8View u8) {
-    const int l16 = threadIdx.x & 15;
-    const unsigned long long id = (unsigned long long)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
-    const bool here = id < blocks;
-    const unsigned long long row = here ? id / (unsigned)nb : 0;
-    const int c0 = here ? (int)(id - row * (unsigned)nb) * kFp8Block : 0, col = c0 + 8 * l16;
-    const int n = here ? cols - col : 0;
-    float v[8];
-    load8<float, true>(U + row * (unsigned long long)cols + col, n, v);
-    if (u8.codes)
-        save_block<false>(v, here ? cols - c0 : 0, l16, u8.codes + row * (unsigned long long)u8.ld + col,
-                          u8.scales + row * (unsigned long long)u8.lds + col / kFp8Block, n);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? gelu_with_grad(v[j]).value : 0.f;
-    save_block<false>(v, here ? cols - c0 : 0, l16, a.codes + row * (unsigned long long)a.ld + col,
-                      a.scales + row * (unsigned long long)a.lds + col / kFp8Block, n);
-}
-
-__global__ void __launch_bounds__(kThreads)
-dgelu_kernel(const float* __restrict__ dA, unsigned long long blocks, int cols, int nb, Fp8View u8, Fp8View d8,
-             __nv_bfloat16* __restrict__ dU) {
-    const int l16 = threadIdx.x & 15;
-    const unsigned long long id = (unsigned long long)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
-    const bool here = id < blocks;
-    const unsigned long long row = here ? id / (unsigned)nb : 0;
-    const int c0 = here ? (int)(id - row * (unsigned)nb) * kFp8Block : 0, col = c0 + 8 * l16;
-    const int n = here ? cols - col : 0;
-    float v[8];
-    load8<float, true>(dA + row * (unsigned long long)cols + col, n, v);
-    if (n >= 8) {
-        const uint2 w = *reinterpret_cast<const uint2*>(u8.codes + row * (unsigned long long)u8.ld + col);
-        const float s = fp8_scale(u8.scales[row * (unsigned long long)u8.lds + col / kFp8Block]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = fp8_unpack2<false>((j < 2 ? w.x : w.y) >> (16 * (j & 1)));
-            v[2 * j] *= gelu_with_grad(f.x * s).grad;
-            v[2 * j + 1] *= gelu_with_grad(f.y * s).grad;
-        }
-        uint4 o;
-        o.x = pack_bf16x2(v[0], v[1]);
-        o.y = pack_bf16x2(v[2], v[3]);
-        o.z = pack_bf16x2(v[4], v[5]);
-        o.w = pack_bf16x2(v[6], v[7]);
-        *reinterpret_cast<uint4*>(dU + row * (unsigned long long)cols + col) = o;
+// One thread per 4 columns (N is a multiple of 4), rows in order.
+template <typename OUT>
+__global__ void __launch_bounds__(128)
+sum_parts_kernel(const float* __restrict__ part, OUT* __restrict__ out, int R, int N) {
+    const int t = blockIdx.y, n = 4 * (blockIdx.x * 128 + threadIdx.x);
+    if (n >= N) return;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* p = part + (size_t)t * R * N + n;
+#pragma unroll 8
+    for (int r = 0; r < R; ++r) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(p + (size_t)r * N));
+        a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
     }
-    save_block<false>(v, here ? cols - c0 : 0, l16, d8.codes + row * (unsigned long long)d8.ld + col,
-                      d8.scales + row * (unsigned long long)d8.lds + col / kFp8Block, n);
+    OUT* o = out + (size_t)t * N + n;
+    o[0] = from_f32<OUT>(a.x), o[1] = from_f32<OUT>(a.y), o[2] = from_f32<OUT>(a.z), o[3] = from_f32<OUT>(a.w);
 }
 
 bool aligned16p(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -367,19 +333,12 @@ cudaError_t launch_fp8_colsum(const void* Y, void* out, bool out_f32, int B, int
     return cudaGetLastError();
 }
 
-cudaError_t launch_fp8_gelu(const float* u, long long rows, int cols, const Fp8View& a, const Fp8View& u8,
-                            cudaStream_t s) {
-    const int nb = (cols + kFp8Block - 1) / kFp8Block;
-    const unsigned long long blocks = (unsigned long long)rows * nb;
-    gelu_kernel<<<(unsigned)((blocks + 15) / 16), kThreads, 0, s>>>(u, blocks, cols, nb, a, u8);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_fp8_dgelu(const float* dA, long long rows, int cols, const Fp8View& u8, const Fp8View& d8, void* dU,
-                             cudaStream_t s) {
-    const int nb = (cols + kFp8Block - 1) / kFp8Block;
-    const unsigned long long blocks = (unsigned long long)rows * nb;
-    dgelu_kernel<<<(unsigned)((blocks + 15) / 16), kThreads, 0, s>>>(dA, blocks, cols, nb, u8, d8, (__nv_bfloat16*)dU);
+cudaError_t launch_fp8_sum_parts(const float* part, void* out, bool out_f32, int R, int T, int N, cudaStream_t s) {
+    const dim3 grid((N + 511) / 512, T);
+    if (out_f32)
+        sum_parts_kernel<float><<<grid, 128, 0, s>>>(part, (float*)out, R, N);
+    else
+        sum_parts_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(part, (__nv_bfloat16*)out, R, N);
     return cudaGetLastError();
 }
 

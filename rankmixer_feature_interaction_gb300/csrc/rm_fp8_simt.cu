@@ -1,4 +1,4 @@
-// The products of the 8-bit operators on the CUDA cores, 64 x 64 tiles with
+// The weight-gradient product of the 8-bit operators on the CUDA cores, 64 x 64 tiles with
 // operands restored to float32 in shared memory.
 #include "rm_common.cuh"
 #include "rm_fp8.cuh"
@@ -24,29 +24,10 @@ struct ColsX {      // A(m = k, b) = x[b][t][k]
     RowsX x;
     __device__ float operator()(int t, int k, int b) const { return x(t, b, k); }
 };
-struct Weight {     // B(k, n) = W[t][k][n], or W[t][n][k]
-    Fp8View w;
-    int R, KB;      // rows per token, and blocks of them
-    bool trans;
-    __device__ float operator()(int t, int k, int n) const {
-        const int r = trans ? n : k, c = trans ? k : n;
-        return code_value(w.codes[((size_t)t * R + r) * w.ld + c], w.e5m2) *
-               fp8_scale(w.scales[((size_t)t * KB + r / kFp8Block) * w.lds + c / kFp8Block]);
-    }
-};
 struct RowsY {      // B(b, n) = dY[b][t][n]
     const __nv_bfloat16* y;
     int T, N;
     __device__ float operator()(int t, int b, int n) const { return to_f32(y[((size_t)b * T + t) * N + n]); }
-};
-template <typename OUT>
-struct ToY {        // Y[b][t][n]
-    OUT* y;
-    const float* bias;
-    int T, N;
-    __device__ void operator()(int t, int b, int n, float v) const {
-        y[((size_t)b * T + t) * N + n] = from_f32<OUT>(bias ? v + bias[(size_t)t * N + n] : v);
-    }
 };
 template <typename OUT>
 struct ToW {        // dW[t][k][n]
@@ -93,15 +74,6 @@ cudaError_t run(const A& a, const B& b, const C& c, int T, int M, int N, int K, 
 }
 
 }  // namespace
-
-cudaError_t launch_fp8_matmul(const Fp8View& x, const Fp8View& w, bool trans, const float* bias, void* Y, bool y_f32,
-                              int B, int T, int K, int N, cudaStream_t s) {
-    const RowsX a{x, T};
-    const int R = trans ? N : K;
-    const Weight b{w, R, (R + kFp8Block - 1) / kFp8Block, trans};
-    if (y_f32) return run(a, b, ToY<float>{(float*)Y, bias, T, N}, T, B, N, K, s);
-    return run(a, b, ToY<__nv_bfloat16>{(__nv_bfloat16*)Y, bias, T, N}, T, B, N, K, s);
-}
 
 cudaError_t launch_fp8_wgrad(const Fp8View& x, const void* dY, void* dW, bool w_f32, int B, int T, int K, int N,
                              cudaStream_t s) {

@@ -1,0 +1,84 @@
+// tcgen05 forms that the 8-bit kernels add to rm_common.cuh: block-scaled MMA
+// on 8-bit operands, the copy of scales into tensor memory, and the shared-
+// memory descriptors of 128-byte swizzled operands in both majors.
+#pragma once
+
+#include "rm_common.cuh"
+
+namespace rm {
+
+// Operand tile of 128-byte rows written by TMA with the 128-byte swizzle
+// (layout type 2, descriptor version 1), base 1024-byte aligned.  K-major: a row
+// holds 128 bytes of K of one M (or N) index.  MN-major: a row holds 128 bytes
+// of M (or N) of one K index; lbo is the distance between such runs.  In both,
+// groups of eight rows lie 1024 bytes apart (stride byte offset).
+__device__ __forceinline__ uint64_t sw128_operand(uint32_t saddr, uint32_t lbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+// 512 bytes of scales (32 rows of 16 bytes, no swizzle): eight-row groups are
+// 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(128u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    return d;
+}
+
+// Instruction descriptor of kind::mxf8f6f4: operand formats (0 e4m3, 1 e5m2) at
+// bits 7 and 10, majors (1: MN) at 15 and 16, N >> 3 at 17, exponent-only
+// scales at 23, M >> 4 at 24.  with_scale_id selects the byte of the 32-bit
+// scale words, at bits 4 (B) and 29 (A).
+__host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, bool a_mn, bool b_mn) {
+    return ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t with_scale_id(uint32_t idesc, uint32_t id) { return idesc | (id << 4) | (id << 29); }
+
+template <bool PAIR>
+__device__ __forceinline__ void umma_mxf8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+            : "memory");
+}
+
+// Scales of 128 rows (one 32-bit word each: row r at 16 (r % 32) + 4 (r / 32))
+// into four columns of tensor memory, repeated for the four lane quarters.  As
+// a pair, each CTA's tensor memory takes its own shared memory's scales.
+template <bool PAIR>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+}  // namespace rm
