@@ -64,6 +64,6 @@ cudaError_t launch_fp8_sum_parts(const float* part, void* out, bool out_f32, int
 
 // dW[t][k][n] = sum_b x[b][t][k] dY[b][t][n], dY bf16 [B][T][N].
 cudaError_t launch_fp8_wgrad(const Fp8View& x, const void* dY, void* dW, bool w_f32, int B, int T, int K, int N,
-                             cudaStream_t s);
+                             const Fp8Device& dev, cudaStream_t s);
 
 }  // namespace rm

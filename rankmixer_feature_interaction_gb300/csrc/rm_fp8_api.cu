@@ -251,7 +251,9 @@ rm_status rm_fp8_wgrad(const rm_fp8_tensor* x, const void* dY, void* dW, void* d
     if (!aligned(dY, 16) || (dW && !aligned(dW, 16)) || (db && !aligned(db, 16)))
         return fail(RM_ERR_INVALID_ARG, "dY, dW and db must be 16-byte aligned");
     const cudaStream_t s = as_stream(stream);
-    if (dW) RM_CHECK_CUDA(launch_fp8_wgrad(view(*x), dY, dW, dtype == RM_F32, B, T, K, N, s), "weight gradient");
+    Fp8Device dev;
+    RM_CHECK(device_info(&dev));
+    if (dW) RM_CHECK_CUDA(launch_fp8_wgrad(view(*x), dY, dW, dtype == RM_F32, B, T, K, N, dev, s), "weight gradient");
     if (db) RM_CHECK_CUDA(launch_fp8_colsum(dY, db, dtype == RM_F32, B, T, N, s), "bias gradient");
     return RM_OK;
 }
@@ -328,9 +330,9 @@ rm_status rm_fp8_pffn_backward(const rm_fp8_pffn* p, const void* dV, rm_dtype dv
     RM_CHECK_CUDA(launch_fp8_product(g, dev, s), "dU");
     if (dX)
         RM_CHECK_CUDA(launch_fp8_product(product(dx_dtype, w.du, p->W1, true, nullptr, dX, B, T, F, D), dev, s), "dX");
-    RM_CHECK_CUDA(launch_fp8_wgrad(view(kept->a), dv16, grads->dW2, g32, B, T, F, D, s), "dW2");
+    RM_CHECK_CUDA(launch_fp8_wgrad(view(kept->a), dv16, grads->dW2, g32, B, T, F, D, dev, s), "dW2");
     RM_CHECK_CUDA(launch_fp8_colsum(dv16, grads->db2, g32, B, T, D, s), "db2");
-    RM_CHECK_CUDA(launch_fp8_wgrad(view(kept->x), w.du16, grads->dW1, g32, B, T, D, F, s), "dW1");
+    RM_CHECK_CUDA(launch_fp8_wgrad(view(kept->x), w.du16, grads->dW1, g32, B, T, D, F, dev, s), "dW1");
     RM_CHECK_CUDA(launch_fp8_sum_parts(w.colpart, grads->db1, g32, fp8_colpart_rows(B), T, F, s), "db1");
     return RM_OK;
 }

@@ -525,10 +525,9 @@ bool get_encoder() {
 
 }  // namespace f8
 
-bool fp8_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int esz, const void* ptr, long long inner, long long rows,
+bool fp8_tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, long long inner, long long rows,
                     long long groups, long long row_bytes, long long group_bytes, int box_inner, int box_rows) {
     if (!f8::get_encoder()) return false;
-    (void)esz;
     cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)groups};
     cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)group_bytes};
     cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1u};
@@ -592,15 +591,15 @@ cudaError_t launch_fp8_product(const Fp8Product& p, const Fp8Device& dev, cudaSt
     a.timeout_ns = dev.timeout_ns;
     CUtensorMap mx, mw, m0, m1;
     const auto u8t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    if (!fp8_tensor_map(&mx, u8t, 1, p.x.codes, p.K, p.B, p.T, p.T * p.x.ld, p.x.ld, BK, BM) ||
-        !fp8_tensor_map(&mw, u8t, 1, p.w.codes, wc, wr, p.T, p.w.ld, (long long)wr * p.w.ld, 128, 128))
+    if (!fp8_tensor_map(&mx, u8t, p.x.codes, p.K, p.B, p.T, p.T * p.x.ld, p.x.ld, BK, BM) ||
+        !fp8_tensor_map(&mw, u8t, p.w.codes, wc, wr, p.T, p.w.ld, (long long)wr * p.w.ld, 128, 128))
         return cudaErrorInvalidValue;
     m0 = m1 = mx;
     auto map8 = [&](CUtensorMap* m, const Fp8View& q) {
-        return fp8_tensor_map(m, u8t, 1, q.codes, p.N, p.B, p.T, p.T * q.ld, q.ld, 128, 32);
+        return fp8_tensor_map(m, u8t, q.codes, p.N, p.B, p.T, p.T * q.ld, q.ld, 128, 32);
     };
     auto map16 = [&](CUtensorMap* m, void* q) {
-        return fp8_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q, p.N, p.B, p.T, 2ll * p.T * p.N, 2ll * p.N, 64, 32);
+        return fp8_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, p.N, p.B, p.T, 2ll * p.T * p.N, 2ll * p.N, 64, 32);
     };
     switch (p.epi) {
         case FP8_OUT_BF16:
@@ -609,7 +608,7 @@ cudaError_t launch_fp8_product(const Fp8Product& p, const Fp8Device& dev, cudaSt
             return run_either<EPI_BF16>(p.trans, mx, mw, m0, m1, a, dev.num_sms, s);
         case FP8_OUT_F32:
             a.direct = p.N % 4 != 0;
-            if (!a.direct && !fp8_tensor_map(&m0, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.y, p.N, p.B, p.T,
+            if (!a.direct && !fp8_tensor_map(&m0, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.y, p.N, p.B, p.T,
                                              4ll * p.T * p.N, 4ll * p.N, 32, 32))
                 return cudaErrorInvalidValue;
             return run_either<EPI_F32>(p.trans, mx, mw, m0, m1, a, dev.num_sms, s);

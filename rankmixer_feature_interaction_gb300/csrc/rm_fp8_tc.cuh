@@ -7,6 +7,12 @@
 
 namespace rm {
 
+// 3-D tensor map {inner, rows, groups} with boxes of box_inner x box_rows
+// elements (128 bytes wide) and the 128-byte swizzle; what lies outside reads
+// as zero and is not written.
+bool fp8_tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, long long inner, long long rows,
+                    long long groups, long long row_bytes, long long group_bytes, int box_inner, int box_rows);
+
 // Operand tile of 128-byte rows written by TMA with the 128-byte swizzle
 // (layout type 2, descriptor version 1), base 1024-byte aligned.  K-major: a row
 // holds 128 bytes of K of one M (or N) index.  MN-major: a row holds 128 bytes

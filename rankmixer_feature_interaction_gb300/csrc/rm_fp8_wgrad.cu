@@ -1,0 +1,407 @@
+// Weight gradient of a per-token linear layer from its input kept in 8 bits,
+//   dW[t][k][n] = sum_b x[b][t][k] dY[b][t][n]   (dY bf16),
+// on the 5th-generation tensor cores.  The scales of x belong to the summed
+// index (one per sample and 128 values of k), so they cannot be applied by a
+// block-scaled MMA, whose scales run along the sum in blocks: x's codes are
+// restored on the way, in shared memory.  A code times a power of two is exact
+// in bf16, so the product is the bf16 product of the restored activation and
+// dY, without that activation ever being written to memory: x costs one byte a
+// value, and no pass of its own.
+//
+// Kernel: one persistent pair of CTAs per 256 (k) x 256 (n) tile of one token;
+// per 64 samples each CTA holds 128 of x's columns and 128 of dY's.
+//   warp 0        TMA producer of dY (MN-major: boxes of 64 columns x 64 samples)
+//   warp 1        MMA issuer (the even CTA's): kind::f16 on bf16, M = N = 256
+//   warp 2        TMA producer of x's codes (64 samples x 128 bytes)
+//   warps 4-11    epilogue
+//   warps 12-15   restore codes to bf16: MN-major operand rows are samples, so
+//                 16 codes of a row become two 16-byte pieces of the same row.
+//                 Two codes at a time: the bits of e4m3, moved to bf16's
+//                 exponent and mantissa, are the code times 2^-120 (also for
+//                 subnormal codes); two packed products restore it and apply
+//                 the scale.  About 6 instructions for two codes: 192 of the
+//                 512 tensor cycles that 64 samples take.
+// Every mbarrier wait is bounded in time; on expiry the CTA latches an error
+// word and all roles unwind.
+#include <cudaTypedefs.h>
+
+#include "rm_fp8.cuh"
+#include "rm_fp8_tc.cuh"
+
+namespace rm {
+namespace f8w {
+
+constexpr int BM = 128, BN = 256, BK = 64;
+constexpr int RAW_BYTES = BK * BM;           // 64 samples x 128 codes
+constexpr int A_BYTES = BK * BM * 2;         // the same in bf16: two boxes of 64 columns x 64 samples
+constexpr int B_BYTES = BK * (BN / 2) * 2;   // dY: two boxes of 64 columns x 64 samples
+constexpr int BOX_BYTES = 64 * BK * 2;
+constexpr int STAGES = 5, RAWS = 4;
+constexpr int EPI_WARPS = 8, CONV_WARPS = 4;
+constexpr int STAGING = 4096;
+constexpr int THREADS = 128 + 32 * (EPI_WARPS + CONV_WARPS);
+constexpr int SMEM_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES) + RAWS * RAW_BYTES + EPI_WARPS * STAGING + 256;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+
+struct Args {
+    int B, T, K, N;
+    int m_tiles, n_tiles, kblocks;
+    long long tiles;
+    const uint8_t* xs;
+    long long xs_ld;
+    int* err;
+    unsigned long long timeout_ns;
+};
+
+struct Tile {
+    int t, m0, n0;
+};
+__device__ __forceinline__ Tile tile_of(long long i, const Args& a) {
+    const int per = a.m_tiles * a.n_tiles;
+    Tile r;
+    r.t = (int)(i / per);
+    const int rem = (int)(i - (long long)r.t * per), nb = rem / a.m_tiles;
+    r.m0 = (rem - nb * a.m_tiles) * 2 * BM;
+    r.n0 = nb * BN;
+    return r;
+}
+
+// kind::f16: D f32, A and B bf16, both MN-major, N >> 3, M >> 4.
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | ((uint32_t)(BN >> 3) << 17) |
+                            ((uint32_t)(2 * BM >> 4) << 24);
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Four codes (one word) to four bf16 of code * s, s = 2^(E - 127) in both halves.
+__device__ __forceinline__ void restore4(uint32_t w, uint32_t s, uint32_t& lo, uint32_t& hi) {
+    constexpr uint32_t up = 0x7b807b80u;                        // 2^120
+    uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);   // bytes 0, 1 and 2, 3 at the tops of halves
+    a = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
+    b = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
+    lo = mul_bf16x2(mul_bf16x2(a, up), s);
+    hi = mul_bf16x2(mul_bf16x2(b, up), s);
+    // the NaN codes, magnitude 0x7f
+    const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    if (nan) {
+        if (nan & 0x00000080u) lo |= 0x00007fffu;
+        if (nan & 0x00008000u) lo |= 0x7fff0000u;
+        if (nan & 0x00800000u) hi |= 0x00007fffu;
+        if (nan & 0x80000000u) hi |= 0x7fff0000u;
+    }
+}
+
+// E's power of two as a bf16 pair (255: NaN, 0: 2^-127).
+__device__ __forceinline__ uint32_t scale_pair(uint32_t E) {
+    const uint32_t h = E == 0u ? 0x0040u : E == 255u ? 0x7fc0u : E << 7;
+    return h | (h << 16);
+}
+
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(THREADS, 1)
+fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY,
+                 const __grid_constant__ CUtensorMap tmW, const Args args) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t* base_ptr = smem_raw + (base - raw_addr);
+    const uint32_t sA = base, sB = sA + STAGES * A_BYTES, sRaw = sB + STAGES * B_BYTES;
+    const uint32_t sEpi = sRaw + RAWS * RAW_BYTES;
+    const uint32_t bar0 = sEpi + EPI_WARPS * STAGING;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto rfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
+    auto rempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + RAWS + s); };
+    auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * RAWS + x); };
+    auto tempty_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * RAWS + 2 + x); };
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + 8 * (2 * STAGES + 2 * RAWS + 4));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const long long unit = blockIdx.x >> 1, nunits = gridDim.x >> 1;
+
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmY);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 1 + 2 * CONV_WARPS);   // the even CTA's: dY's bytes of both CTAs, both CTAs' restorers
+            mbar_init(empty_bar(s), 1);                   // multicast commit
+        }
+        for (int s = 0; s < RAWS; ++s) {
+            mbar_init(rfull_bar(s), 1);
+            mbar_init(rempty_bar(s), CONV_WARPS);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(tfull_bar(x), 1);                   // multicast commit
+            mbar_init(tempty_bar(x), 2 * EPI_WARPS);      // the even CTA's: every epilogue warp of both CTAs
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 3) {
+        tmem_alloc_pair(smem_u32(tmem_holder), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
+    const int kblocks = args.kblocks;
+
+    if (warp == 0) {
+        // ------------------------------ dY producer -------------------------------
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (long long i = unit; ok && i < args.tiles; i += nunits) {
+            const Tile tl = tile_of(i, args);
+            const int col = tl.n0 + BN / 2 * (int)rank;
+            for (int kb = 0; kb < kblocks; ++kb) {
+                if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const uint32_t fb = mapa_shared(full_bar(stage), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2u * B_BYTES);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        tma_load_3d_pair(&tmY, sB + stage * B_BYTES + j * BOX_BYTES, fb, col + 64 * j, kb * BK, tl.t);
+                }
+                __syncwarp();
+                if (++stage == STAGES) stage = 0, phase ^= 1u;
+            }
+        }
+    } else if (warp == 2) {
+        // ------------------------------ x producer --------------------------------
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (long long i = unit; ok && i < args.tiles; i += nunits) {
+            const Tile tl = tile_of(i, args);
+            for (int kb = 0; kb < kblocks; ++kb) {
+                if (!mbar_wait_bounded(rempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(rfull_bar(slot), RAW_BYTES);
+                    tma_load_3d(&tmX, sRaw + slot * RAW_BYTES, rfull_bar(slot), tl.m0 + BM * (int)rank, kb * BK, tl.t);
+                }
+                __syncwarp();
+                if (++slot == RAWS) slot = 0, phase ^= 1u;
+            }
+        }
+    } else if (warp == 1 && rank == 0) {
+        // ------------------------------ MMA issuer --------------------------------
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool ok = true;
+        for (long long i = unit; ok && i < args.tiles; i += nunits) {
+            if (!mbar_wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
+            tc_fence_after();
+            const uint32_t d = tmem_base + (uint32_t)(acc * BN);
+            for (int kb = 0; kb < kblocks; ++kb) {
+                if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, args.err, args.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t a0 = sA + stage * A_BYTES, b0 = sB + stage * B_BYTES;
+#pragma unroll
+                    for (int k = 0; k < BK / 16; ++k)        // 16 samples: 16 rows of 128 bytes
+                        umma_f16_pair(d, sw128_operand(a0 + 2048u * k, BOX_BYTES), sw128_operand(b0 + 2048u * k, BOX_BYTES),
+                                      kIdesc, (kb | k) != 0 ? 1u : 0u);
+                    umma_commit_pair_mc(empty_bar(stage), (uint16_t)0x3);
+                }
+                __syncwarp();
+                if (++stage == STAGES) stage = 0, phase ^= 1u;
+            }
+            if (!ok) break;
+            if (lane == 0) umma_commit_pair_mc(tfull_bar(acc), (uint16_t)0x3);
+            __syncwarp();
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+    } else if (warp >= 12) {
+        // ------------------------------ restorers ---------------------------------
+        // Lane's 16-byte chunks: column chunk c and, per step, one of its warp's 16
+        // rows.  The two rows of a group of eight lanes differ by 5 in their low
+        // three bits, which keeps both the reads (chunk c of row r at c ^ (r % 8))
+        // and the writes (pieces 2 (c % 4), + 1 at ^ (r % 8)) free of bank conflicts.
+        const int cw = warp - 12;
+        const int c = (lane & 3) | ((lane >> 1) & 4);
+        const int flip = (lane & 4) ? 5 : 0, rep0 = lane >> 4;
+        int row[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) row[j] = 16 * cw + 8 * (j >> 1) + ((rep0 | ((j & 1) << 1)) ^ flip);
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, rphase = 0;
+        bool ok = true;
+        for (long long i = unit; ok && i < args.tiles; i += nunits) {
+            const Tile tl = tile_of(i, args);
+            const int k0 = tl.m0 + BM * (int)rank;
+            const uint8_t* sp = args.xs + (size_t)tl.t * (size_t)args.xs_ld + k0 / kFp8Block;
+            const size_t step = (size_t)args.T * (size_t)args.xs_ld;
+            // exponent bytes two k-blocks ahead
+            auto exponents = [&](int kb) {
+                uint32_t w = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int b = kb * BK + row[j];
+                    const uint32_t E = b < args.B && k0 < args.K ? __ldg(sp + (size_t)b * step) : 127u;
+                    w |= E << (8 * j);
+                }
+                return w;
+            };
+            uint32_t now = exponents(0), next = exponents(1);
+            for (int kb = 0; kb < kblocks; ++kb) {
+                const uint32_t later = exponents(kb + 2);
+                if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns) ||
+                    !mbar_wait_bounded(rfull_bar(slot), rphase, abort_flag, args.err, args.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t src = sRaw + slot * RAW_BYTES, dst = sA + stage * A_BYTES + (uint32_t)(c >> 2) * BOX_BYTES;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t r = (uint32_t)row[j], x7 = r & 7u;
+                    const uint4 w = ld_shared_u4(src + 128u * r + 16u * ((uint32_t)c ^ x7));
+                    const uint32_t s = scale_pair((now >> (8 * j)) & 0xffu);
+                    uint32_t o[8];
+                    restore4(w.x, s, o[0], o[1]);
+                    restore4(w.y, s, o[2], o[3]);
+                    restore4(w.z, s, o[4], o[5]);
+                    restore4(w.w, s, o[6], o[7]);
+                    const uint32_t p = 2u * (uint32_t)(c & 3);
+                    st_shared_v4(dst + 128u * r + 16u * (p ^ x7), o[0], o[1], o[2], o[3]);
+                    st_shared_v4(dst + 128u * r + 16u * ((p + 1u) ^ x7), o[4], o[5], o[6], o[7]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_cluster(mapa_shared(full_bar(stage), 0));
+                    mbar_arrive(rempty_bar(slot));
+                }
+                now = next;
+                next = later;
+                if (++stage == STAGES) stage = 0, phase ^= 1u;
+                if (++slot == RAWS) slot = 0, rphase ^= 1u;
+            }
+        }
+    } else if (warp >= 4) {
+        // ------------------------------ epilogue ----------------------------------
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t stage = sEpi + (uint32_t)(warp - 4) * STAGING;
+        constexpr int PIECE = F32 ? 32 : 64;                 // columns of 128 bytes
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (long long i = unit; i < args.tiles; i += nunits) {
+            const Tile tl = tile_of(i, args);
+            const int m = tl.m0 + BM * (int)rank + 32 * quad, n = tl.n0 + 128 * half;
+            if (!mbar_wait_bounded(tfull_bar(acc), acc_phase, abort_flag, args.err, args.timeout_ns)) break;
+            tc_fence_after();
+            const uint32_t tcol = tmem_base + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * BN) + 128u * half;
+#pragma unroll
+            for (int h = 0; h < 128 / PIECE; ++h) {
+                uint32_t r[PIECE];
+#pragma unroll
+                for (int q = 0; q < PIECE / 32; ++q)
+                    tmem_ld32_nowait(tcol + PIECE * h + 32 * q, reinterpret_cast<uint32_t(&)[32]>(r[32 * q]));
+                tmem_wait_ld();
+                if (lane == 0) bulk_wait_group_read<0>();
+                __syncwarp();
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        w[q] = F32 ? r[4 * p + q]
+                                   : pack_bf16x2(__uint_as_float(r[(8 * p + 2 * q) % PIECE]),
+                                                 __uint_as_float(r[(8 * p + 2 * q + 1) % PIECE]));
+                    st_shared_v4(stage + 128u * lane + 16u * (uint32_t)(p ^ (lane & 7)), w[0], w[1], w[2], w[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (m < args.K && n + PIECE * h < args.N) tma_store_3d(&tmW, stage, n + PIECE * h, m, tl.t);
+                    bulk_commit_group();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+        if (lane == 0) bulk_wait_group<0>();                 // this warp's tensor stores have landed
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();    // no CTA leaves while its peer may still touch its memory
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+template <bool F32>
+cudaError_t run(const CUtensorMap& mx, const CUtensorMap& my, const CUtensorMap& mw, const Args& a, int num_sms,
+                cudaStream_t s) {
+    auto k = fp8_wgrad_kernel<F32>;
+    cudaError_t e = smem_attr_once((const void*)k, SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    const long long pairs = num_sms / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * (a.tiles < pairs ? a.tiles : pairs)));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k, mx, my, mw, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace f8w
+
+cudaError_t launch_fp8_wgrad(const Fp8View& x, const void* dY, void* dW, bool w_f32, int B, int T, int K, int N,
+                             const Fp8Device& dev, cudaStream_t s) {
+    using namespace f8w;
+    Args a{};
+    a.B = B, a.T = T, a.K = K, a.N = N;
+    a.m_tiles = (K + 2 * BM - 1) / (2 * BM);
+    a.n_tiles = (N + BN - 1) / BN;
+    a.kblocks = (B + BK - 1) / BK;
+    a.tiles = (long long)T * a.m_tiles * a.n_tiles;
+    a.xs = x.scales, a.xs_ld = x.lds;
+    a.err = dev.err;
+    a.timeout_ns = dev.timeout_ns;
+    CUtensorMap mx, my, mw;
+    if (!fp8_tensor_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, x.codes, K, B, T, T * x.ld, x.ld, BM, BK) ||
+        !fp8_tensor_map(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, N, B, T, 2ll * T * N, 2ll * N, 64, BK) ||
+        !fp8_tensor_map(&mw, w_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dW, N, K, T,
+                        (w_f32 ? 4ll : 2ll) * N, (w_f32 ? 4ll : 2ll) * K * N, w_f32 ? 32 : 64, 32))
+        return cudaErrorInvalidValue;
+    return w_f32 ? run<true>(mx, my, mw, a, dev.num_sms, s) : run<false>(mx, my, mw, a, dev.num_sms, s);
+}
+
+}  // namespace rm
