@@ -78,6 +78,14 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
         asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
+// Arrive on the pair's barrier (a shared::cluster address) after writes to this
+// CTA's own shared memory that fence_proxy_async_smem has ordered before the
+// tensor core's reads of it.  The fence carries the data; the arrival needs no
+// cluster-wide release of its own, whose memory barrier costs about 1000 cycles.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));

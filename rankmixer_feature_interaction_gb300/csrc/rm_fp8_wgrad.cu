@@ -14,13 +14,14 @@
 //   warp 1        MMA issuer (the even CTA's): kind::f16 on bf16, M = N = 256
 //   warp 2        TMA producer of x's codes (64 samples x 128 bytes)
 //   warps 4-11    epilogue
-//   warps 12-15   restore codes to bf16: MN-major operand rows are samples, so
+//   warp 3        x's exponent bytes into shared memory, eight k-blocks' loads
+//                 at a time so that their latency is paid once in eight
+//   warps 12-19   restore codes to bf16: MN-major operand rows are samples, so
 //                 16 codes of a row become two 16-byte pieces of the same row.
 //                 Two codes at a time: the bits of e4m3, moved to bf16's
 //                 exponent and mantissa, are the code times 2^-120 (also for
-//                 subnormal codes); two packed products restore it and apply
-//                 the scale.  About 6 instructions for two codes: 192 of the
-//                 512 tensor cycles that 64 samples take.
+//                 subnormal codes), so one packed product by 2^120 times the
+//                 scale restores it: 4 instructions for two codes
 // Every mbarrier wait is bounded in time; on expiry the CTA latches an error
 // word and all roles unwind.
 #include <cudaTypedefs.h>
@@ -37,15 +38,23 @@ constexpr int A_BYTES = BK * BM * 2;         // the same in bf16: two boxes of 6
 constexpr int B_BYTES = BK * (BN / 2) * 2;   // dY: two boxes of 64 columns x 64 samples
 constexpr int BOX_BYTES = 64 * BK * 2;
 constexpr int STAGES = 5, RAWS = 4;
-constexpr int EPI_WARPS = 8, CONV_WARPS = 4;
+constexpr int EPI_WARPS = 8, CONV_WARPS = 8;
+constexpr int CONV_GROUP = 2;                // restoring warps per k-block
+constexpr int AHEAD = 8;                     // k-blocks whose exponent bytes are loaded together
+// Float32 gradients of more samples are summed in chunks of this many: a chunk's
+// sum leaves the tensor cores' accumulator (which truncates each addition) and
+// is added to dW in memory with rounding to nearest.
+constexpr int CHUNK = 2048;
 constexpr int STAGING = 4096;
 constexpr int THREADS = 128 + 32 * (EPI_WARPS + CONV_WARPS);
-constexpr int SMEM_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES) + RAWS * RAW_BYTES + EPI_WARPS * STAGING + 256;
+constexpr int SMEM_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES) + RAWS * (RAW_BYTES + BK) + EPI_WARPS * STAGING + 256;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+static_assert(RAWS * CONV_GROUP == CONV_WARPS && RAWS < STAGES, "a raw slot per group of restorers");
 
 struct Args {
     int B, T, K, N;
     int m_tiles, n_tiles, kblocks;
+    int chunks, chunk_blocks;            // the sum over samples: chunks of that many k-blocks
     long long tiles;
     const uint8_t* xs;
     long long xs_ld;
@@ -76,34 +85,66 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Four codes (one word) to four bf16 of code * s, s = 2^(E - 127) in both halves.
-__device__ __forceinline__ void restore4(uint32_t w, uint32_t s, uint32_t& lo, uint32_t& hi) {
-    constexpr uint32_t up = 0x7b807b80u;                        // 2^120
-    uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);   // bytes 0, 1 and 2, 3 at the tops of halves
-    a = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
-    b = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
-    lo = mul_bf16x2(mul_bf16x2(a, up), s);
-    hi = mul_bf16x2(mul_bf16x2(b, up), s);
-    // the NaN codes, magnitude 0x7f
-    const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-    if (nan) {
-        if (nan & 0x00000080u) lo |= 0x00007fffu;
-        if (nan & 0x00008000u) lo |= 0x7fff0000u;
-        if (nan & 0x00800000u) hi |= 0x00007fffu;
-        if (nan & 0x80000000u) hi |= 0x7fff0000u;
-    }
+// Two codes (bytes of w) to bf16 times 2^-120: the selector spreads them to
+// halves with their sign bits repeated above (prmt's sign mode), which leaves
+// the sign at bit 15 and the magnitude's seven bits at bit 4 after the shift.
+__device__ __forceinline__ uint32_t spread2(uint32_t w, uint32_t selector) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "r"(selector));
+    return (r << 4) & 0x87f087f0u;
 }
 
-// E's power of two as a bf16 pair (255: NaN, 0: 2^-127).
-__device__ __forceinline__ uint32_t scale_pair(uint32_t E) {
-    const uint32_t h = E == 0u ? 0x0040u : E == 255u ? 0x7fc0u : E << 7;
-    return h | (h << 16);
+// 16 codes to 16 bf16 of code * 2^(E - 127): exact where bf16 is normal, else
+// rounded once.
+__device__ __forceinline__ void restore16(const uint4& q, uint32_t E, uint32_t (&o)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o[2 * i] = spread2(w[i], 0x9180u);
+        o[2 * i + 1] = spread2(w[i], 0xb3a2u);
+    }
+    if (E <= 134u) {                                   // 2^120 2^(E - 127) is a bf16
+        const uint32_t h = (E + 120u) << 7, s = h | (h << 16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], s);
+    } else {                                           // blocks above 57344: in two steps, the first exact
+        const uint32_t h = E == 255u ? 0x7fc0u : E << 7, s = h | (h << 16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(mul_bf16x2(o[i], 0x7b807b80u), s);
+    }
+    uint32_t nan = 0;                                  // codes of magnitude 0x7f
+#pragma unroll
+    for (int i = 0; i < 4; ++i) nan |= ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    if (nan) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t m = ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+            o[2 * i] |= (m & 0x80u ? 0x7fffu : 0u) | (m & 0x8000u ? 0x7fff0000u : 0u);
+            o[2 * i + 1] |= (m & 0x800000u ? 0x7fffu : 0u) | (m & 0x80000000u ? 0x7fff0000u : 0u);
+        }
+    }
 }
 
 __device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Tiled add of float32 shared -> global (bulk async group).
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* m, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(m)), "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
 }
 
 template <bool F32>
@@ -115,8 +156,8 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
     uint8_t* base_ptr = smem_raw + (base - raw_addr);
     const uint32_t sA = base, sB = sA + STAGES * A_BYTES, sRaw = sB + STAGES * B_BYTES;
-    const uint32_t sEpi = sRaw + RAWS * RAW_BYTES;
-    const uint32_t bar0 = sEpi + EPI_WARPS * STAGING;
+    const uint32_t sEpi = sRaw + RAWS * RAW_BYTES, sExp = sEpi + EPI_WARPS * STAGING;
+    const uint32_t bar0 = sExp + RAWS * BK;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
     auto rfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
@@ -134,12 +175,12 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         tma_prefetch_desc(&tmX);
         tma_prefetch_desc(&tmY);
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full_bar(s), 1 + 2 * CONV_WARPS);   // the even CTA's: dY's bytes of both CTAs, both CTAs' restorers
+            mbar_init(full_bar(s), 1 + 2 * CONV_GROUP);   // the even CTA's: dY's bytes of both CTAs, both CTAs' restorers
             mbar_init(empty_bar(s), 1);                   // multicast commit
         }
         for (int s = 0; s < RAWS; ++s) {
-            mbar_init(rfull_bar(s), 1);
-            mbar_init(rempty_bar(s), CONV_WARPS);
+            mbar_init(rfull_bar(s), 2);                   // x's bytes, its exponents
+            mbar_init(rempty_bar(s), CONV_GROUP);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(tfull_bar(x), 1);                   // multicast commit
@@ -209,10 +250,14 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true;
         for (long long i = unit; ok && i < args.tiles; i += nunits) {
-            if (!mbar_wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
-            tc_fence_after();
-            const uint32_t d = tmem_base + (uint32_t)(acc * BN);
+            int in_chunk = 0;
             for (int kb = 0; kb < kblocks; ++kb) {
+                if (in_chunk == 0 &&
+                    !mbar_wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t d = tmem_base + (uint32_t)(acc * BN);
                 if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, args.err, args.timeout_ns)) {
                     ok = false;
                     break;
@@ -223,82 +268,97 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
 #pragma unroll
                     for (int k = 0; k < BK / 16; ++k)        // 16 samples: 16 rows of 128 bytes
                         umma_f16_pair(d, sw128_operand(a0 + 2048u * k, BOX_BYTES), sw128_operand(b0 + 2048u * k, BOX_BYTES),
-                                      kIdesc, (kb | k) != 0 ? 1u : 0u);
+                                      kIdesc, (in_chunk | k) != 0 ? 1u : 0u);
                     umma_commit_pair_mc(empty_bar(stage), (uint16_t)0x3);
                 }
                 __syncwarp();
                 if (++stage == STAGES) stage = 0, phase ^= 1u;
+                if (++in_chunk == args.chunk_blocks || kb + 1 == kblocks) {
+                    if (lane == 0) umma_commit_pair_mc(tfull_bar(acc), (uint16_t)0x3);
+                    __syncwarp();
+                    in_chunk = 0;
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
+                }
             }
-            if (!ok) break;
-            if (lane == 0) umma_commit_pair_mc(tfull_bar(acc), (uint16_t)0x3);
-            __syncwarp();
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1u;
         }
-    } else if (warp >= 12) {
-        // ------------------------------ restorers ---------------------------------
-        // Lane's 16-byte chunks: column chunk c and, per step, one of its warp's 16
-        // rows.  The two rows of a group of eight lanes differ by 5 in their low
-        // three bits, which keeps both the reads (chunk c of row r at c ^ (r % 8))
-        // and the writes (pieces 2 (c % 4), + 1 at ^ (r % 8)) free of bank conflicts.
-        const int cw = warp - 12;
-        const int c = (lane & 3) | ((lane >> 1) & 4);
-        const int flip = (lane & 4) ? 5 : 0, rep0 = lane >> 4;
-        int row[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) row[j] = 16 * cw + 8 * (j >> 1) + ((rep0 | ((j & 1) << 1)) ^ flip);
-        int stage = 0, slot = 0;
-        uint32_t phase = 0, rphase = 0;
+    } else if (warp == 3) {
+        // ------------------------------ exponents ---------------------------------
+        int slot = 0;
+        uint32_t phase = 0;
         bool ok = true;
         for (long long i = unit; ok && i < args.tiles; i += nunits) {
             const Tile tl = tile_of(i, args);
             const int k0 = tl.m0 + BM * (int)rank;
             const uint8_t* sp = args.xs + (size_t)tl.t * (size_t)args.xs_ld + k0 / kFp8Block;
             const size_t step = (size_t)args.T * (size_t)args.xs_ld;
-            // exponent bytes two k-blocks ahead
-            auto exponents = [&](int kb) {
-                uint32_t w = 0;
+            for (int kb0 = 0; ok && kb0 < kblocks; kb0 += AHEAD) {
+                uint32_t E[AHEAD][2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int b = kb * BK + row[j];
-                    const uint32_t E = b < args.B && k0 < args.K ? __ldg(sp + (size_t)b * step) : 127u;
-                    w |= E << (8 * j);
+                for (int q = 0; q < AHEAD; ++q)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int b = (kb0 + q) * BK + 32 * j + lane;
+                        E[q][j] = b < args.B && k0 < args.K ? __ldg(sp + (size_t)b * step) : 127u;
+                    }
+#pragma unroll
+                for (int q = 0; q < AHEAD; ++q) {
+                    if (ok && kb0 + q < kblocks) {
+                        ok = mbar_wait_bounded(rempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns);
+                        if (ok) {
+                            st_shared_u8(sExp + BK * slot + lane, E[q][0]);
+                            st_shared_u8(sExp + BK * slot + 32 + lane, E[q][1]);
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(rfull_bar(slot));
+                            if (++slot == RAWS) slot = 0, phase ^= 1u;
+                        }
+                    }
                 }
-                return w;
-            };
-            uint32_t now = exponents(0), next = exponents(1);
-            for (int kb = 0; kb < kblocks; ++kb) {
-                const uint32_t later = exponents(kb + 2);
+            }
+        }
+    } else if (warp >= 12) {
+        // ------------------------------ restorers ---------------------------------
+        // Four groups of two warps, each with every fourth k-block (and the raw slot
+        // of that number), so that four k-blocks' latencies overlap.  Lane's 16-byte
+        // chunks: column chunk c of eight of its warp's 32 rows.  The two rows that a
+        // group of eight lanes reads at a time differ by 5 in their low three bits,
+        // which keeps both the reads (chunk c of row r at c ^ (r % 8)) and the writes
+        // (pieces 2 (c % 4), + 1 at ^ (r % 8)) free of bank conflicts.
+        const uint32_t cw = warp - 12, slot = cw >> 1;
+        const uint32_t c = (lane & 3) | ((lane >> 1) & 4), p = 2u * (c & 3u);
+        const uint32_t flip = (lane & 4) ? 5 : 0, rep0 = lane >> 4;
+        const uint32_t src = sRaw + slot * RAW_BYTES, exps = sExp + BK * slot;
+        uint32_t rphase = 0;
+        long long done = 0;                          // k-blocks before this tile
+        int stage = (int)slot % STAGES;              // of the group's next k-block
+        uint32_t phase = 0;
+        long long next = slot;
+        bool ok = true;
+        for (long long i = unit; ok && i < args.tiles; i += nunits, done += kblocks) {
+            for (; next < done + kblocks; next += RAWS) {
                 if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns) ||
                     !mbar_wait_bounded(rfull_bar(slot), rphase, abort_flag, args.err, args.timeout_ns)) {
                     ok = false;
                     break;
                 }
-                const uint32_t src = sRaw + slot * RAW_BYTES, dst = sA + stage * A_BYTES + (uint32_t)(c >> 2) * BOX_BYTES;
+                rphase ^= 1u;
+                const uint32_t dst = sA + stage * A_BYTES + (c >> 2) * BOX_BYTES;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t r = (uint32_t)row[j], x7 = r & 7u;
-                    const uint4 w = ld_shared_u4(src + 128u * r + 16u * ((uint32_t)c ^ x7));
-                    const uint32_t s = scale_pair((now >> (8 * j)) & 0xffu);
+                for (uint32_t j = 0; j < 8; ++j) {
+                    const uint32_t x7 = (rep0 | ((j & 1u) << 1)) ^ flip, r = 32u * (cw & 1u) + 8u * (j >> 1) + x7;
                     uint32_t o[8];
-                    restore4(w.x, s, o[0], o[1]);
-                    restore4(w.y, s, o[2], o[3]);
-                    restore4(w.z, s, o[4], o[5]);
-                    restore4(w.w, s, o[6], o[7]);
-                    const uint32_t p = 2u * (uint32_t)(c & 3);
+                    restore16(ld_shared_u4(src + 128u * r + 16u * (c ^ x7)), ld_shared_u8(exps + r), o);
                     st_shared_v4(dst + 128u * r + 16u * (p ^ x7), o[0], o[1], o[2], o[3]);
                     st_shared_v4(dst + 128u * r + 16u * ((p + 1u) ^ x7), o[4], o[5], o[6], o[7]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive_cluster(mapa_shared(full_bar(stage), 0));
+                    mbar_arrive_pair(mapa_shared(full_bar(stage), 0));
                     mbar_arrive(rempty_bar(slot));
                 }
-                now = next;
-                next = later;
-                if (++stage == STAGES) stage = 0, phase ^= 1u;
-                if (++slot == RAWS) slot = 0, rphase ^= 1u;
+                stage += RAWS;
+                if (stage >= STAGES) stage -= STAGES, phase ^= 1u;
             }
         }
     } else if (warp >= 4) {
@@ -308,10 +368,15 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         constexpr int PIECE = F32 ? 32 : 64;                 // columns of 128 bytes
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (long long i = unit; i < args.tiles; i += nunits) {
-            const Tile tl = tile_of(i, args);
+        bool ok = true;
+        for (long long i = unit; ok && i < args.tiles; i += nunits) {
+          const Tile tl = tile_of(i, args);
+          for (int chunk = 0; chunk < args.chunks; ++chunk) {
             const int m = tl.m0 + BM * (int)rank + 32 * quad, n = tl.n0 + 128 * half;
-            if (!mbar_wait_bounded(tfull_bar(acc), acc_phase, abort_flag, args.err, args.timeout_ns)) break;
+            if (!mbar_wait_bounded(tfull_bar(acc), acc_phase, abort_flag, args.err, args.timeout_ns)) {
+                ok = false;
+                break;
+            }
             tc_fence_after();
             const uint32_t tcol = tmem_base + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * BN) + 128u * half;
 #pragma unroll
@@ -321,7 +386,12 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 for (int q = 0; q < PIECE / 32; ++q)
                     tmem_ld32_nowait(tcol + PIECE * h + 32 * q, reinterpret_cast<uint32_t(&)[32]>(r[32 * q]));
                 tmem_wait_ld();
-                if (lane == 0) bulk_wait_group_read<0>();
+                if (lane == 0) {
+                    if (F32 && chunk > 0)
+                        bulk_wait_group<0>();        // the chunk before is in memory
+                    else
+                        bulk_wait_group_read<0>();
+                }
                 __syncwarp();
 #pragma unroll
                 for (int p = 0; p < 8; ++p) {
@@ -336,7 +406,12 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (m < args.K && n + PIECE * h < args.N) tma_store_3d(&tmW, stage, n + PIECE * h, m, tl.t);
+                    if (m < args.K && n + PIECE * h < args.N) {
+                        if (F32 && chunk > 0)
+                            tma_add_3d(&tmW, stage, n + PIECE * h, m, tl.t);
+                        else
+                            tma_store_3d(&tmW, stage, n + PIECE * h, m, tl.t);
+                    }
                     bulk_commit_group();
                 }
             }
@@ -345,6 +420,7 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
+          }
         }
         if (lane == 0) bulk_wait_group<0>();                 // this warp's tensor stores have landed
     }
@@ -392,6 +468,8 @@ cudaError_t launch_fp8_wgrad(const Fp8View& x, const void* dY, void* dW, bool w_
     a.n_tiles = (N + BN - 1) / BN;
     a.kblocks = (B + BK - 1) / BK;
     a.tiles = (long long)T * a.m_tiles * a.n_tiles;
+    a.chunk_blocks = w_f32 ? CHUNK / BK : a.kblocks;
+    a.chunks = (a.kblocks + a.chunk_blocks - 1) / a.chunk_blocks;
     a.xs = x.scales, a.xs_ld = x.lds;
     a.err = dev.err;
     a.timeout_ns = dev.timeout_ns;
