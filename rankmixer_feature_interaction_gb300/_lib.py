@@ -345,43 +345,57 @@ def rm_debug_alloc_stats() -> tuple[int, int, int]:
 
 
 def rm_fp8_quantize(X: int, dtype: int, rows: int, cols: int, ldx: int, out: rm_fp8_tensor, stream: int) -> None:
-    check(load().rm_fp8_quantize(X, dtype, rows, cols, ldx, out, stream), "rm_fp8_quantize")
+    st = (_lib or load()).rm_fp8_quantize(X, dtype, rows, cols, ldx, out, stream)
+    if st:
+        check(st, "rm_fp8_quantize")
 
 
 def rm_fp8_quantize_weight(W: int, dtype: int, T: int, K: int, N: int, out: rm_fp8_tensor, stream: int) -> None:
-    check(load().rm_fp8_quantize_weight(W, dtype, T, K, N, out, stream), "rm_fp8_quantize_weight")
+    st = (_lib or load()).rm_fp8_quantize_weight(W, dtype, T, K, N, out, stream)
+    if st:
+        check(st, "rm_fp8_quantize_weight")
 
 
 def rm_fp8_dequantize(q: rm_fp8_tensor, rows: int, cols: int, Y: int, dtype: int, ldy: int, stream: int) -> None:
-    check(load().rm_fp8_dequantize(q, rows, cols, Y, dtype, ldy, stream), "rm_fp8_dequantize")
+    st = (_lib or load()).rm_fp8_dequantize(q, rows, cols, Y, dtype, ldy, stream)
+    if st:
+        check(st, "rm_fp8_dequantize")
 
 
 def rm_fp8_matmul(x: rm_fp8_tensor, W: rm_fp8_tensor, bias: int | None, Y: int, dtype: int, B: int, T: int, K: int,
                   N: int, transpose_w: bool, stream: int) -> None:
-    check(load().rm_fp8_matmul(x, W, bias, Y, dtype, B, T, K, N, 1 if transpose_w else 0, stream), "rm_fp8_matmul")
+    st = (_lib or load()).rm_fp8_matmul(x, W, bias, Y, dtype, B, T, K, N, 1 if transpose_w else 0, stream)
+    if st:
+        check(st, "rm_fp8_matmul")
 
 
 def rm_fp8_wgrad(x: rm_fp8_tensor, dY: int, dW: int | None, db: int | None, dtype: int, B: int, T: int, K: int, N: int,
                  stream: int) -> None:
-    check(load().rm_fp8_wgrad(x, dY, dW, db, dtype, B, T, K, N, stream), "rm_fp8_wgrad")
+    st = (_lib or load()).rm_fp8_wgrad(x, dY, dW, db, dtype, B, T, K, N, stream)
+    if st:
+        check(st, "rm_fp8_wgrad")
 
 
 def rm_fp8_pffn_workspace(p: rm_fp8_pffn, B: int, pass_: int) -> int:
     n = ctypes.c_longlong()
-    check(load().rm_fp8_pffn_workspace(p, B, pass_, ctypes.byref(n)), "rm_fp8_pffn_workspace")
+    st = (_lib or load()).rm_fp8_pffn_workspace(p, B, pass_, ctypes.byref(n))
+    if st:
+        check(st, "rm_fp8_pffn_workspace")
     return n.value
 
 
 def rm_fp8_pffn_forward(p: rm_fp8_pffn, X: int, x_dtype: int, V: int, v_dtype: int, keep: rm_fp8_kept | None, B: int,
                         work: int | None, work_bytes: int, stream: int) -> None:
-    check(load().rm_fp8_pffn_forward(p, X, x_dtype, V, v_dtype, keep, B, work, work_bytes, stream),
-          "rm_fp8_pffn_forward")
+    st = (_lib or load()).rm_fp8_pffn_forward(p, X, x_dtype, V, v_dtype, keep, B, work, work_bytes, stream)
+    if st:
+        check(st, "rm_fp8_pffn_forward")
 
 
 def rm_fp8_pffn_backward(p: rm_fp8_pffn, dV: int, dv_dtype: int, kept: rm_fp8_kept, dX: int | None, dx_dtype: int,
                          grads: rm_fp8_grads, B: int, work: int | None, work_bytes: int, stream: int) -> None:
-    check(load().rm_fp8_pffn_backward(p, dV, dv_dtype, kept, dX, dx_dtype, grads, B, work, work_bytes, stream),
-          "rm_fp8_pffn_backward")
+    st = (_lib or load()).rm_fp8_pffn_backward(p, dV, dv_dtype, kept, dX, dx_dtype, grads, B, work, work_bytes, stream)
+    if st:
+        check(st, "rm_fp8_pffn_backward")
 
 
 def rm_fp8_sync_status(stream: int) -> int:

@@ -343,9 +343,14 @@ def head_forward(pooled: torch.Tensor, w: torch.Tensor, b: float, y: torch.Tenso
 
 
 # -- 8-bit operands and checkpoints ---------------------------------------------------
+# These calls are short, so their host side is kept short too: the current stream's handle
+# comes straight from torch's C side, an Fp8Tensor carries its C structure, and its torch
+# tensors are made when they are asked for.
 _F8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 _F8_CODE = {torch.float8_e4m3fn: _lib.RM_E4M3, torch.float8_e5m2: _lib.RM_E5M2}
 _CODE = {torch.bfloat16: _lib.RM_BF16, torch.float32: _lib.RM_F32}
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 class Fp8Tensor:
@@ -353,93 +358,144 @@ class Fp8Tensor:
     row count) and one exponent byte E per 128 values of a row, scales [.., lds] (uint8); for a
     weight [T, K, N] one per 128 x 128 values, scales [T, ceil(K / 128), lds].  A value is
     code * 2^(E - 127).  ld is a multiple of 16, lds of 4; both tensors contiguous."""
-    __slots__ = ("codes", "scales", "cols", "c")
+    __slots__ = ("cols", "c", "lead", "scale_lead", "device", "device_index", "_codes", "_scales", "_arena", "_at")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
-        if codes.dtype not in _F8_CODE or scales.dtype != torch.uint8:
+        cs, ss, fmt = codes.shape, scales.shape, _F8_CODE.get(codes.dtype)
+        if fmt is None or scales.dtype != torch.uint8:
             raise ValueError("codes must be float8_e4m3fn or float8_e5m2, scales uint8")
-        if codes.dim() < 1 or codes.dim() != scales.dim() or codes.device != scales.device:
+        if len(cs) < 1 or len(cs) != len(ss) or codes.get_device() != scales.get_device():
             raise ValueError("codes and scales must have the same rank and device")
-        if not 0 < cols <= codes.shape[-1] or (cols + 127) // 128 > scales.shape[-1]:
-            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not hold {cols} columns")
-        self.codes, self.scales, self.cols = codes, scales, int(cols)
-        self.c = _lib.rm_fp8_tensor(_ptr(codes), _ptr(scales), codes.shape[-1], scales.shape[-1],
-                                    _F8_CODE[codes.dtype])
+        if not 0 < cols <= cs[-1] or (cols + 127) // 128 > ss[-1]:
+            raise ValueError(f"codes {tuple(cs)} and scales {tuple(ss)} do not hold {cols} columns")
+        self.cols, self._codes, self._scales = int(cols), codes, scales
+        self.lead, self.scale_lead, self.device_index = tuple(cs[:-1]), tuple(ss[:-1]), codes.get_device()
+        self.device, self._arena = codes.device, None
+        self.c = _lib.rm_fp8_tensor(_ptr(codes), _ptr(scales), cs[-1], ss[-1], fmt)
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            n, ld = self._at, self.c.ld
+            for d in self.lead:
+                ld *= d
+            fmt = _F8["e5m2" if self.c.format == _lib.RM_E5M2 else "e4m3"]
+            self._codes = self._arena[n:n + ld].view(fmt).view(self.lead + (self.c.ld,))
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            n, size = self.c.scales - self._arena.data_ptr(), self.c.lds
+            for d in self.scale_lead:
+                size *= d
+            self._scales = self._arena[n:n + size].view(self.scale_lead + (self.c.lds,))
+        return self._scales
 
     @property
     def shape(self) -> tuple:
-        return tuple(self.codes.shape[:-1]) + (self.cols,)
+        return self.lead + (self.cols,)
 
     @property
     def nbytes(self) -> int:
-        return self.codes.numel() + self.scales.numel()
+        n, s = self.c.ld, self.c.lds
+        for d in self.lead:
+            n *= d
+        for d in self.scale_lead:
+            s *= d
+        return n + s
 
 
-def _fp8_empty(lead: tuple, cols: int, fmt: str, device, scale_lead: tuple | None = None) -> Fp8Tensor:
-    ld, lds = (cols + 15) // 16 * 16, ((cols + 127) // 128 + 3) // 4 * 4
-    return Fp8Tensor(torch.empty(tuple(lead) + (ld,), dtype=_F8[fmt], device=device),
-                     torch.empty(tuple(lead if scale_lead is None else scale_lead) + (lds,), dtype=torch.uint8,
-                                 device=device), cols)
+def _fp8_new(wanted: list, device: torch.device, index: int) -> list:
+    """8-bit tensors [(lead, cols, format, lead of the scales)] in one allocation, each part 256-byte aligned."""
+    at, places = 0, []
+    for lead, cols, fmt, scale_lead in wanted:
+        ld, lds = (cols + 15) // 16 * 16, (cols + 511) // 512 * 4
+        n, m = ld, lds
+        for d in lead:
+            n *= d
+        for d in scale_lead:
+            m *= d
+        places.append((at, at + (n + 255) // 256 * 256, ld, lds))
+        at = places[-1][1] + (m + 255) // 256 * 256
+    arena = torch.empty(at, dtype=torch.uint8, device=device)
+    base, out = arena.data_ptr(), []
+    for (lead, cols, fmt, scale_lead), (codes, scales, ld, lds) in zip(wanted, places):
+        q = object.__new__(Fp8Tensor)
+        q.cols, q.lead, q.scale_lead, q.device, q.device_index = cols, lead, scale_lead, device, index
+        q._codes = q._scales = None
+        q._arena, q._at = arena, codes
+        q.c = _lib.rm_fp8_tensor(base + codes, base + scales, ld, lds, fmt)
+        out.append(q)
+    return out
 
 
-def _fp8_same_device(*ts) -> None:
-    """The calls run on the current device: every tensor has to live there."""
-    d = torch.cuda.current_device()
-    for t in ts:
-        if t is not None and (t.device.type != "cuda" or t.device.index != d):
-            raise ValueError(f"tensors must be on the current CUDA device (cuda:{d}), got {t.device}")
+def _fp8_device(index: int, *others) -> int:
+    """The current device, on which the calls run: every tensor has to live there."""
+    d = _current_device()
+    if index != d or any(o is not None and o != d for o in others):
+        raise ValueError(f"tensors must be on the current CUDA device (cuda:{d}), got devices {(index, *others)}")
+    return d
 
 
-def _fp8_activation(x: Fp8Tensor, what: str) -> tuple[int, int, int]:
+def _fp8_activation(x: Fp8Tensor, what: str) -> tuple:
     """(B, T, cols) of 8-bit activations, with a scale row for every code row."""
-    if x.codes.dim() != 3 or x.scales.shape[:2] != x.codes.shape[:2]:
-        raise ValueError(f"{what} must be 8-bit activations [B, T, cols] with one row of scales per row, got codes "
-                         f"{tuple(x.codes.shape)}, scales {tuple(x.scales.shape)}")
-    return x.codes.shape[0], x.codes.shape[1], x.cols
+    if len(x.lead) != 2 or x.scale_lead != x.lead:
+        raise ValueError(f"{what} must be 8-bit activations [B, T, cols] with one row of scales per row, got rows "
+                         f"{x.lead}, rows of scales {x.scale_lead}")
+    return x.lead + (x.cols,)
 
 
-def _fp8_weight(w: Fp8Tensor, what: str) -> tuple[int, int, int]:
+def _fp8_weight(w: Fp8Tensor, what: str) -> tuple:
     """(T, K, N) of an 8-bit weight."""
-    if w.codes.dim() != 3 or w.scales.shape[0] != w.codes.shape[0] or \
-            w.scales.shape[1] != (w.codes.shape[1] + 127) // 128:
-        raise ValueError(f"{what} must be an 8-bit weight [T, K, N] with one row of scales per 128 rows, got codes "
-                         f"{tuple(w.codes.shape)}, scales {tuple(w.scales.shape)}")
-    return w.codes.shape[0], w.codes.shape[1], w.cols
+    if len(w.lead) != 2 or w.scale_lead != (w.lead[0], (w.lead[1] + 127) // 128):
+        raise ValueError(f"{what} must be an 8-bit weight [T, K, N] with one row of scales per 128 rows, got rows "
+                         f"{w.lead}, rows of scales {w.scale_lead}")
+    return w.lead + (w.cols,)
 
 
 def fp8_quantize(X: torch.Tensor, fmt: str = "e4m3") -> Fp8Tensor:
     """X [.., C] (bf16 or float32, rows one stride apart) in 8 bits, one scale per 128 values
     of a row: an operand of fp8_matmul, and a checkpoint that fp8_dequantize restores."""
-    _fp8_same_device(X)
-    if X.dtype not in _CODE:
+    d = _fp8_device(X.get_device())
+    dtype, shape = _CODE.get(X.dtype), X.shape
+    if dtype is None:
         raise ValueError(f"X must be bfloat16 or float32, got {X.dtype}")
-    if X.dim() < 1 or (X.stride(-1) != 1 and X.shape[-1] > 1):
+    if len(shape) < 1 or (X.stride(-1) != 1 and shape[-1] > 1):
         raise ValueError("the last dimension of X must be contiguous")
-    rows = X.view(-1, X.shape[-1])            # raises when the rows are not one stride apart
-    out = _fp8_empty(X.shape[:-1], X.shape[-1], fmt, X.device)
-    _lib.rm_fp8_quantize(rows.data_ptr(), _CODE[X.dtype], rows.shape[0], rows.shape[1],
-                         rows.stride(0) if rows.shape[0] > 1 else rows.shape[1], out.c, _stream())
+    C, lead, rows = shape[-1], tuple(shape[:-1]), 1
+    for n in lead:
+        rows *= n
+    ldx = C if X.is_contiguous() else X.view(rows, C).stride(0)       # raises when rows are not one stride apart
+    if rows < 1 or C < 1:
+        _lib.check(_lib.RM_ERR_INVALID_ARG, f"fp8_quantize of an empty tensor {tuple(shape)}")
+    out, = _fp8_new([(lead, C, _F8_CODE[_F8[fmt]], lead)], X.device, d)
+    _lib.rm_fp8_quantize(X.data_ptr(), dtype, rows, C, ldx if rows > 1 else C, out.c, _raw_stream(d))
     return out
 
 
 def fp8_quantize_weight(W: torch.Tensor) -> Fp8Tensor:
     """W [T, K, N] (bf16 or float32) in e4m3, one scale per 128 x 128 values."""
-    _fp8_same_device(W)
+    d = _fp8_device(W.get_device())
     if W.dtype not in _CODE or W.dim() != 3:
         raise ValueError(f"W must be a bfloat16 or float32 [T, K, N], got {W.dtype} {tuple(W.shape)}")
     T, K, N = W.shape
-    out = _fp8_empty((T, K), N, "e4m3", W.device, (T, (K + 127) // 128))
-    _lib.rm_fp8_quantize_weight(_ptr(W), _CODE[W.dtype], T, K, N, out.c, _stream())
+    out, = _fp8_new([((T, K), N, _lib.RM_E4M3, (T, (K + 127) // 128))], W.device, d)
+    _lib.rm_fp8_quantize_weight(_ptr(W), _CODE[W.dtype], T, K, N, out.c, _raw_stream(d))
     return out
 
 
 def fp8_dequantize(q: Fp8Tensor, dtype: str = "bf16") -> torch.Tensor:
     """The values of 8-bit rows [.., C] in bf16 or float32."""
-    _fp8_same_device(q.codes)
-    if q.scales.shape[:-1] != q.codes.shape[:-1]:
+    d = _fp8_device(q.device_index)
+    if q.scale_lead != q.lead:
         raise ValueError("fp8_dequantize takes rows with their own scales (activations)")
-    Y = torch.empty(q.shape, dtype=_DTYPES[dtype][0], device=q.codes.device)
-    _lib.rm_fp8_dequantize(q.c, Y.numel() // q.cols, q.cols, _ptr(Y), _DTYPES[dtype][1], q.cols, _stream())
+    tdt, code = _DTYPES[dtype]
+    Y = torch.empty(q.lead + (q.cols,), dtype=tdt, device=q.device)
+    rows = 1
+    for n in q.lead:
+        rows *= n
+    _lib.rm_fp8_dequantize(q.c, rows, q.cols, Y.data_ptr(), code, q.cols, _raw_stream(d))
     return Y
 
 
@@ -447,32 +503,35 @@ def fp8_matmul(x: Fp8Tensor, w: Fp8Tensor, bias: torch.Tensor | None = None, out
                transpose_w: bool = False) -> torch.Tensor:
     """Y[b, t, :] = x[b, t, :] w[t] (+ bias[t]): x [B, T, K] and w [T, K, N] in 8 bits, bias
     float32 [T, N]; with transpose_w, w is [T, N, K] and Y[b, t, :] = x[b, t, :] w[t]^T."""
-    _fp8_same_device(x.codes, w.codes, bias)
     B, T, K = _fp8_activation(x, "x")
     Tw, Kw, N = _fp8_weight(w, "w")
     if transpose_w:
         Kw, N = N, Kw
     if Tw != T or Kw != K:
         raise ValueError(f"x {x.shape} and w {w.shape} do not fit (transpose_w={transpose_w})")
-    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (T, N)):
-        raise ValueError(f"bias must be float32 [{T}, {N}]")
+    if bias is None:
+        d, b = _fp8_device(x.device_index, w.device_index), None
+    else:
+        d, b = _fp8_device(x.device_index, w.device_index, bias.get_device()), _ptr(bias)
+        if bias.dtype != torch.float32 or bias.shape != (T, N):
+            raise ValueError(f"bias must be float32 [{T}, {N}]")
     tdt, code = _DTYPES[out_dtype]
-    Y = torch.empty((B, T, N), dtype=tdt, device=x.codes.device)
-    _lib.rm_fp8_matmul(x.c, w.c, _ptr(bias), Y.data_ptr(), code, B, T, K, N, transpose_w, _stream())
+    Y = torch.empty((B, T, N), dtype=tdt, device=x.device)
+    _lib.rm_fp8_matmul(x.c, w.c, b, Y.data_ptr(), code, B, T, K, N, transpose_w, _raw_stream(d))
     return Y
 
 
 def fp8_wgrad(x: Fp8Tensor, dY: torch.Tensor, grad_dtype: str = "f32") -> tuple[torch.Tensor, torch.Tensor]:
     """(dW [T, K, N], db [T, N]) of y = x W + b from x [B, T, K] kept in 8 bits and dY [B, T, N] bf16."""
-    _fp8_same_device(x.codes, dY)
+    d = _fp8_device(x.device_index, dY.get_device())
     B, T, K = _fp8_activation(x, "x")
-    if dY.dtype != torch.bfloat16 or dY.dim() != 3 or tuple(dY.shape[:2]) != (B, T):
+    if dY.dtype != torch.bfloat16 or dY.dim() != 3 or dY.shape[:2] != (B, T):
         raise ValueError(f"dY must be bfloat16 [{B}, {T}, N], got {dY.dtype} {tuple(dY.shape)}")
     N = dY.shape[2]
     tdt, code = _DTYPES[grad_dtype]
     dW = torch.empty((T, K, N), dtype=tdt, device=dY.device)
     db = torch.empty((T, N), dtype=tdt, device=dY.device)
-    _lib.rm_fp8_wgrad(x.c, _ptr(dY), dW.data_ptr(), db.data_ptr(), code, B, T, K, N, _stream())
+    _lib.rm_fp8_wgrad(x.c, _ptr(dY), dW.data_ptr(), db.data_ptr(), code, B, T, K, N, _raw_stream(d))
     return dW, db
 
 
@@ -493,40 +552,46 @@ class Fp8PFFN:
         self.b1, self.b2 = b1.to(torch.float32).contiguous(), b2.to(torch.float32).contiguous()
         if tuple(self.b1.shape) != (self.T, self.F) or tuple(self.b2.shape) != (self.T, self.D):
             raise ValueError(f"b1 must be [{self.T}, {self.F}] and b2 [{self.T}, {self.D}]")
-        _fp8_same_device(self.W1.codes, self.W2.codes, self.b1, self.b2)
+        self.device_index = _fp8_device(self.W1.device_index, self.W2.device_index, self.b1.get_device(),
+                                        self.b2.get_device())
         self.c = _lib.rm_fp8_pffn(self.W1.c, self.W2.c, _ptr(self.b1), _ptr(self.b2), self.T, self.D, self.F)
+        self._bytes = {}
 
     def _rows(self, X: torch.Tensor, what: str) -> int:
-        _fp8_same_device(X, self.b1)
-        if X.dtype not in _CODE or X.dim() != 3 or tuple(X.shape[1:]) != (self.T, self.D):
+        _fp8_device(X.get_device(), self.device_index)
+        if X.dtype not in _CODE or X.dim() != 3 or X.shape[1:] != (self.T, self.D):
             raise ValueError(f"{what} must be a bfloat16 or float32 [B, {self.T}, {self.D}], got {X.dtype} "
                              f"{tuple(X.shape)}")
         return X.shape[0]
 
     def _work(self, B: int, pass_: int, device) -> tuple[torch.Tensor, int]:
-        n = _lib.rm_fp8_pffn_workspace(self.c, B, pass_)
+        """This call's workspace (its size is looked up once per batch size)."""
+        n = self._bytes.get((B, pass_))
+        if n is None:
+            n = self._bytes[B, pass_] = _lib.rm_fp8_pffn_workspace(self.c, B, pass_)
         return torch.empty(max(n, 16), dtype=torch.uint8, device=device), n
 
     def forward(self, X: torch.Tensor, out_dtype: str = "bf16") -> torch.Tensor:
         """V [B, T, D] of X [B, T, D]; nothing is kept."""
-        return self._forward(X, out_dtype, None, _lib.RM_FP8_SERVE)
+        B = self._rows(X, "X")
+        work, n = self._work(B, _lib.RM_FP8_SERVE, X.device)
+        return self._forward(X, B, out_dtype, None, work.data_ptr(), n)
 
     def forward_train(self, X: torch.Tensor, out_dtype: str = "bf16") -> tuple[torch.Tensor, dict]:
         """(V, the activations kept for backward: {"x", "u", "a"} in 8 bits)."""
         B = self._rows(X, "X")
-        keep = {"x": _fp8_empty((B, self.T), self.D, "e4m3", X.device),
-                "u": _fp8_empty((B, self.T), self.F, "e4m3", X.device),
-                "a": _fp8_empty((B, self.T), self.F, "e4m3", X.device)}
-        return self._forward(X, out_dtype, keep, _lib.RM_FP8_TRAIN), keep
+        lead = (B, self.T)
+        x, u, a = _fp8_new([(lead, n, _lib.RM_E4M3, lead) for n in (self.D, self.F, self.F)], X.device,
+                           self.device_index)
+        work, n = self._work(B, _lib.RM_FP8_TRAIN, X.device)
+        V = self._forward(X, B, out_dtype, _lib.rm_fp8_kept(x.c, u.c, a.c), work.data_ptr(), n)
+        return V, {"x": x, "u": u, "a": a}
 
-    def _forward(self, X: torch.Tensor, out_dtype: str, keep: dict | None, pass_: int) -> torch.Tensor:
-        B = self._rows(X, "X")
+    def _forward(self, X: torch.Tensor, B: int, out_dtype: str, keep, work: int, n: int) -> torch.Tensor:
         tdt, code = _DTYPES[out_dtype]
-        V = torch.empty(X.shape, dtype=tdt, device=X.device)
-        work, n = self._work(B, pass_, X.device)
-        k = None if keep is None else _lib.rm_fp8_kept(keep["x"].c, keep["u"].c, keep["a"].c)
-        _lib.rm_fp8_pffn_forward(self.c, _ptr(X), _CODE[X.dtype], V.data_ptr(), code, k, B, work.data_ptr(), n,
-                                 _stream())
+        V = torch.empty((B, self.T, self.D), dtype=tdt, device=X.device)
+        _lib.rm_fp8_pffn_forward(self.c, _ptr(X), _CODE[X.dtype], V.data_ptr(), code, keep, B, work, n,
+                                 _raw_stream(self.device_index))
         return V
 
     def backward(self, dV: torch.Tensor, kept: dict, dx_dtype: str = "bf16", grad_dtype: str = "f32",
@@ -537,18 +602,18 @@ class Fp8PFFN:
         for k, cols in (("x", self.D), ("u", self.F), ("a", self.F)):
             if _fp8_activation(kept[k], f"kept[{k!r}]") != (B, self.T, cols):
                 raise ValueError(f"kept[{k!r}] {kept[k].shape} is not of this layer and batch")
-            _fp8_same_device(kept[k].codes)
+            _fp8_device(kept[k].device_index)
         dev, T, D, F = dV.device, self.T, self.D, self.F
-        dX = torch.empty((B, T, D), dtype=_DTYPES[dx_dtype][0], device=dev) if with_dX else None
+        dxt, dxc = _DTYPES[dx_dtype]
+        dX = torch.empty((B, T, D), dtype=dxt, device=dev) if with_dX else None
         tdt, code = _DTYPES[grad_dtype]
         g = {"dW1": torch.empty((T, D, F), dtype=tdt, device=dev), "db1": torch.empty((T, F), dtype=tdt, device=dev),
              "dW2": torch.empty((T, F, D), dtype=tdt, device=dev), "db2": torch.empty((T, D), dtype=tdt, device=dev)}
         work, n = self._work(B, _lib.RM_FP8_BACKWARD, dev)
         _lib.rm_fp8_pffn_backward(self.c, _ptr(dV), _CODE[dV.dtype],
-                                  _lib.rm_fp8_kept(kept["x"].c, kept["u"].c, kept["a"].c), _ptr(dX),
-                                  _DTYPES[dx_dtype][1],
-                                  _lib.rm_fp8_grads(*(g[k].data_ptr() for k in ("dW1", "db1", "dW2", "db2")), code),
-                                  B, work.data_ptr(), n, _stream())
+                                  _lib.rm_fp8_kept(kept["x"].c, kept["u"].c, kept["a"].c), _ptr(dX), dxc,
+                                  _lib.rm_fp8_grads(*(t.data_ptr() for t in g.values()), code), B, work.data_ptr(), n,
+                                  _raw_stream(self.device_index))
         return dX, g
 
 

@@ -55,7 +55,13 @@ struct Fp8Product {
     Fp8View o0, o1;
     float* colpart;
     int B, T, K, N;
+    bool follows = false;       // launched right after another kernel of the same call (which waited for its
+                                // own predecessor before this one could start): W is in memory already
 };
+// Up to this many samples the weights are streamed past all of them at once (launch_fp8_stream).
+constexpr int kFp8StreamMaxB = 64;
+bool fp8_streams(const Fp8Product& p);
+cudaError_t launch_fp8_stream(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s);
 int fp8_colpart_rows(int B);
 cudaError_t launch_fp8_product(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s);
 

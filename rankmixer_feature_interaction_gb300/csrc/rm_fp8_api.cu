@@ -290,11 +290,13 @@ rm_status rm_fp8_pffn_forward(const rm_fp8_pffn* p, const void* X, rm_dtype x_dt
     RM_CHECK_CUDA(launch_fp8_quantize(x_dtype == RM_F32, X, rows, D, D, view(w.kept.x), nullptr, s), "quantize");
     Fp8Product g = product(RM_BF16, w.kept.x, p->W1, false, p->b1, nullptr, B, T, D, F);
     g.epi = FP8_GELU;
+    g.follows = true;
     g.o0 = view(w.kept.a);
     if (keep) g.o1 = view(w.kept.u);
     RM_CHECK_CUDA(launch_fp8_product(g, dev, s), "8-bit layer 1");
-    RM_CHECK_CUDA(launch_fp8_product(product(v_dtype, w.kept.a, p->W2, false, p->b2, V, B, T, F, D), dev, s),
-                  "8-bit layer 2");
+    g = product(v_dtype, w.kept.a, p->W2, false, p->b2, V, B, T, F, D);
+    g.follows = true;
+    RM_CHECK_CUDA(launch_fp8_product(g, dev, s), "8-bit layer 2");
     return RM_OK;
 }
 

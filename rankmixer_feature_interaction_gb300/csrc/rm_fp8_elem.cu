@@ -65,6 +65,8 @@ template <typename IN, bool E5M2, bool VEC, bool COPY>
 __global__ void __launch_bounds__(kThreads)
 quantize_kernel(const IN* __restrict__ X, unsigned long long blocks, int cols, int nb, long long ldx, Fp8View out,
                 __nv_bfloat16* __restrict__ copy) {
+    pdl_wait();
+    pdl_launch_next();
     const int l16 = threadIdx.x & 15;
     const unsigned long long base = (unsigned long long)blockIdx.x * (kThreads / 16 * kUnroll) + (threadIdx.x >> 4);
     float v[kUnroll][8];
@@ -114,6 +116,8 @@ template <typename IN, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 quantize_weight_kernel(const IN* __restrict__ W, int K, int N, Fp8View out) {
     __shared__ uint32_t part[kThreads / 32];
+    pdl_wait();
+    pdl_launch_next();
     const int kb = blockIdx.y, t = blockIdx.z, c0 = blockIdx.x * kFp8Block + 8 * (threadIdx.x & 15);
     float v[8][8];
     uint32_t m = 0;
@@ -148,6 +152,8 @@ quantize_weight_kernel(const IN* __restrict__ W, int K, int N, Fp8View out) {
 template <typename OUT, bool E5M2, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 dequantize_kernel(Fp8View in, unsigned long long chunks, int cols, int nch, OUT* __restrict__ Y, long long ldy) {
+    pdl_wait();
+    pdl_launch_next();
     // one thread per 16 codes; four chunks in flight
     unsigned long long base = (unsigned long long)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
     uint4 w[kUnroll];
@@ -209,6 +215,8 @@ template <typename OUT>
 __global__ void __launch_bounds__(kThreads)
 colsum_kernel(const __nv_bfloat16* __restrict__ Y, OUT* __restrict__ out, int B, int T, int N) {
     __shared__ float part[16][kFp8Block];
+    pdl_wait();
+    pdl_launch_next();
     const int t = blockIdx.y, c0 = blockIdx.x * kFp8Block + 8 * (threadIdx.x & 15), r0 = threadIdx.x >> 4;
     float acc[8] = {};
     if (c0 < N) {
@@ -236,6 +244,8 @@ colsum_kernel(const __nv_bfloat16* __restrict__ Y, OUT* __restrict__ out, int B,
 template <typename OUT>
 __global__ void __launch_bounds__(128)
 sum_parts_kernel(const float* __restrict__ part, OUT* __restrict__ out, int R, int N) {
+    pdl_wait();
+    pdl_launch_next();
     const int t = blockIdx.y, n = 4 * (blockIdx.x * 128 + threadIdx.x);
     if (n >= N) return;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -257,13 +267,8 @@ cudaError_t run_quantize(const void* X, long long rows, int cols, long long ldx,
     const int nb = (cols + kFp8Block - 1) / kFp8Block;
     const unsigned long long blocks = (unsigned long long)rows * nb;
     const unsigned grid = (unsigned)((blocks + kThreads / 16 * kUnroll - 1) / (kThreads / 16 * kUnroll));
-    if (copy)
-        quantize_kernel<IN, E5M2, VEC, true><<<grid, kThreads, 0, s>>>((const IN*)X, blocks, cols, nb, ldx, out,
-                                                                       (__nv_bfloat16*)copy);
-    else
-        quantize_kernel<IN, E5M2, VEC, false><<<grid, kThreads, 0, s>>>((const IN*)X, blocks, cols, nb, ldx, out,
-                                                                        nullptr);
-    return cudaGetLastError();
+    return launch_k(copy ? quantize_kernel<IN, E5M2, VEC, true> : quantize_kernel<IN, E5M2, VEC, false>, dim3(grid),
+                    dim3(kThreads), 0, s, (const IN*)X, blocks, cols, nb, ldx, out, (__nv_bfloat16*)copy);
 }
 
 template <typename IN>
@@ -282,11 +287,9 @@ cudaError_t dequantize_as(const Fp8View& in, long long rows, int cols, void* Y, 
     const int nch = (cols + 15) / 16;
     const unsigned long long chunks = (unsigned long long)rows * nch;
     const unsigned grid = (unsigned)((chunks + kThreads * kUnroll - 1) / (kThreads * kUnroll));
-    if (aligned16p(Y) && (ldy * sizeof(OUT)) % 16 == 0)
-        dequantize_kernel<OUT, E5M2, true><<<grid, kThreads, 0, s>>>(in, chunks, cols, nch, (OUT*)Y, ldy);
-    else
-        dequantize_kernel<OUT, E5M2, false><<<grid, kThreads, 0, s>>>(in, chunks, cols, nch, (OUT*)Y, ldy);
-    return cudaGetLastError();
+    const bool vec = aligned16p(Y) && (ldy * sizeof(OUT)) % 16 == 0;
+    return launch_k(vec ? dequantize_kernel<OUT, E5M2, true> : dequantize_kernel<OUT, E5M2, false>, dim3(grid),
+                    dim3(kThreads), 0, s, in, chunks, cols, nch, (OUT*)Y, ldy);
 }
 
 }  // namespace
@@ -301,18 +304,11 @@ cudaError_t launch_fp8_quantize_weight(bool f32, const void* W, int T, int K, in
                                        cudaStream_t s) {
     const dim3 grid((N + kFp8Block - 1) / kFp8Block, (K + kFp8Block - 1) / kFp8Block, T);
     const bool vec = aligned16p(W) && (size_t)N * (f32 ? 4 : 2) % 16 == 0;
-    if (f32) {
-        if (vec)
-            quantize_weight_kernel<float, true><<<grid, kThreads, 0, s>>>((const float*)W, K, N, out);
-        else
-            quantize_weight_kernel<float, false><<<grid, kThreads, 0, s>>>((const float*)W, K, N, out);
-    } else {
-        if (vec)
-            quantize_weight_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, s>>>((const __nv_bfloat16*)W, K, N, out);
-        else
-            quantize_weight_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, s>>>((const __nv_bfloat16*)W, K, N, out);
-    }
-    return cudaGetLastError();
+    if (f32)
+        return launch_k(vec ? quantize_weight_kernel<float, true> : quantize_weight_kernel<float, false>, grid,
+                        dim3(kThreads), 0, s, (const float*)W, K, N, out);
+    return launch_k(vec ? quantize_weight_kernel<__nv_bfloat16, true> : quantize_weight_kernel<__nv_bfloat16, false>,
+                    grid, dim3(kThreads), 0, s, (const __nv_bfloat16*)W, K, N, out);
 }
 
 cudaError_t launch_fp8_dequantize(const Fp8View& in, long long rows, int cols, void* Y, bool f32, long long ldy,
@@ -327,19 +323,16 @@ cudaError_t launch_fp8_dequantize(const Fp8View& in, long long rows, int cols, v
 cudaError_t launch_fp8_colsum(const void* Y, void* out, bool out_f32, int B, int T, int N, cudaStream_t s) {
     const dim3 grid((N + kFp8Block - 1) / kFp8Block, T);
     if (out_f32)
-        colsum_kernel<float><<<grid, kThreads, 0, s>>>((const __nv_bfloat16*)Y, (float*)out, B, T, N);
-    else
-        colsum_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>((const __nv_bfloat16*)Y, (__nv_bfloat16*)out, B, T, N);
-    return cudaGetLastError();
+        return launch_k(colsum_kernel<float>, grid, dim3(kThreads), 0, s, (const __nv_bfloat16*)Y, (float*)out, B, T, N);
+    return launch_k(colsum_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, (const __nv_bfloat16*)Y, (__nv_bfloat16*)out,
+                    B, T, N);
 }
 
 cudaError_t launch_fp8_sum_parts(const float* part, void* out, bool out_f32, int R, int T, int N, cudaStream_t s) {
     const dim3 grid((N + 511) / 512, T);
     if (out_f32)
-        sum_parts_kernel<float><<<grid, 128, 0, s>>>(part, (float*)out, R, N);
-    else
-        sum_parts_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(part, (__nv_bfloat16*)out, R, N);
-    return cudaGetLastError();
+        return launch_k(sum_parts_kernel<float>, grid, dim3(128), 0, s, part, (float*)out, R, N);
+    return launch_k(sum_parts_kernel<__nv_bfloat16>, grid, dim3(128), 0, s, part, (__nv_bfloat16*)out, R, N);
 }
 
 }  // namespace rm

@@ -319,6 +319,8 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     tc_fence_after();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
     const int kblocks = args.kblocks;
+    pdl_wait();
+    pdl_launch_next();
 
     if (warp < 4) {
         regs_dec<REGS_OTHER>();
@@ -551,13 +553,15 @@ cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap&
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, k, mx, mw, m0, m1, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -574,6 +578,7 @@ int fp8_colpart_rows(int B) { return (B + 2 * f8::BM - 1) / (2 * f8::BM) * 8; }
 
 cudaError_t launch_fp8_product(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s) {
     using namespace f8;
+    if (fp8_streams(p)) return launch_fp8_stream(p, dev, s);
     Args a{};
     a.B = p.B, a.T = p.T, a.K = p.K, a.N = p.N;
     a.m_tiles = (p.B + 2 * BM - 1) / (2 * BM);

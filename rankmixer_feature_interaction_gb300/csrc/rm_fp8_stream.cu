@@ -1,0 +1,396 @@
+// Per-token products of 8-bit operands for few samples: the same product as
+// rm_fp8_gemm.cu with W's columns as the rows of the MMA, so that a token's
+// weights are streamed once and nothing is computed for samples that are not
+// there.
+//   acc[n][b] = sum_k W[t][k][n] x[b][t][k],  128 columns n x NB samples a tile
+// Bound by memory: W is read once (T K N bytes), at one sample 99% of the
+// traffic, so the kernel is a deep pipeline of weight tiles: one persistent CTA
+// per SM, 16 KB of W (128 x 128 codes) and NB rows of x per k-block and stage,
+// 152 x 180 KB in flight.
+//   warp 0       TMA producer of W ([K][N]: MN-major; [N][K]: K-major)
+//   warp 1       MMA issuer (tcgen05.mma kind::mxf8f6f4, M = 128, N = NB, one CTA)
+//   warp 2       scales (as in rm_fp8_gemm.cu: words of four k-blocks' exponents)
+//   warp 3       TMA producer of x
+//   warps 4-7    epilogue: a thread owns one column n of all samples; an 8-bit
+//                output's block of 128 columns is the CTA's 128 threads, whose
+//                largest values meet in a warp maximum and 4 words of shared memory
+// The kernel is launched while its predecessor may still run.  Where that
+// predecessor is one of this library's own launches of the same call, W was in
+// memory before it began, and warp 0 starts on it at once; everything else
+// waits for the predecessor's end.
+// Every mbarrier wait is bounded in time; on expiry the CTA latches an error
+// word and all roles unwind.
+#include <cudaTypedefs.h>
+
+#include "rm_fp8.cuh"
+#include "rm_fp8_tc.cuh"
+
+namespace rm {
+namespace f8s {
+
+constexpr int BM = 128, BK = 128;
+constexpr int W_BYTES = BM * BK;
+constexpr int SF_SLOTS = 4, SF_BYTES = 1024;
+constexpr int EPI_WARPS = 4;
+constexpr int THREADS = 128 + 32 * EPI_WARPS;
+constexpr int TMEM_COLS = 256, SF_COL = 192;
+
+template <int NB>
+struct Cfg {
+    static constexpr int X_BYTES = NB * BK;
+    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
+    static constexpr int FIT = (200 * 1024) / STAGE_BYTES;
+    static constexpr int STAGES = FIT < 12 ? FIT : 12;
+    static constexpr int RED_BYTES = 2 * 2 * EPI_WARPS * NB * 4;
+    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SF_SLOTS * SF_BYTES + RED_BYTES + 512;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+    static_assert(2 * NB <= SF_COL, "two accumulators below the scales");
+};
+
+enum Epi { EPI_BF16, EPI_F32, EPI_GELU, EPI_GELU_KEEP };
+
+struct Args {
+    int B, T, K, N;
+    int n_tiles, kblocks, tiles;
+    const uint8_t* xs;
+    long long xs_ld;
+    const uint8_t* ws;
+    long long ws_ld;
+    int w_rows;
+    uint32_t x_format;
+    bool early;                          // W may be read before the predecessor's end
+    const float* bias;
+    void* y;
+    Fp8View o0, o1;
+    int* err;
+    unsigned long long timeout_ns;
+};
+
+template <int EPI, bool TRANS, int NB>
+__global__ void __launch_bounds__(THREADS, 1)
+fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Args args) {
+    using C = Cfg<NB>;
+    constexpr int STAGES = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t* base_ptr = smem_raw + (base - raw_addr);
+    const uint32_t sW = base, sX = sW + STAGES * W_BYTES, sSF = sX + STAGES * C::X_BYTES;
+    uint32_t* red = reinterpret_cast<uint32_t*>(base_ptr + (sSF - base) + SF_SLOTS * SF_BYTES);
+    const uint32_t bar0 = sSF + SF_SLOTS * SF_BYTES + C::RED_BYTES;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto sfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
+    auto sempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + SF_SLOTS + s); };
+    auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + x); };
+    auto tempty_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 2 + x); };
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + 8 * (2 * STAGES + 2 * SF_SLOTS + 4));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 2);            // W's bytes, x's bytes
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int s = 0; s < SF_SLOTS; ++s) {
+            mbar_init(sfull_bar(s), 1);
+            mbar_init(sempty_bar(s), 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(tfull_bar(x), 1);
+            mbar_init(tempty_bar(x), EPI_WARPS);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 4) {
+        tmem_alloc(smem_u32(tmem_holder), TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
+    const int kblocks = args.kblocks;
+    if (!(args.early && warp == 0)) {
+        pdl_wait();
+        pdl_launch_next();
+    }
+
+    if (warp == 0 || warp == 3) {
+        // ------------------------------ TMA producers -----------------------------
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; ok && i < args.tiles; i += gridDim.x) {
+            const int t = i / args.n_tiles, n0 = (i - t * args.n_tiles) * BM;
+            for (int kb = 0; kb < kblocks; ++kb) {
+                if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    if (warp == 0) {
+                        mbar_arrive_expect_tx(full_bar(stage), W_BYTES);
+                        if (TRANS)
+                            tma_load_3d(&tmW, sW + stage * W_BYTES, full_bar(stage), kb * BK, n0, t);
+                        else
+                            tma_load_3d(&tmW, sW + stage * W_BYTES, full_bar(stage), n0, kb * BK, t);
+                    } else {
+                        mbar_arrive_expect_tx(full_bar(stage), C::X_BYTES);
+                        tma_load_3d(&tmX, sX + stage * C::X_BYTES, full_bar(stage), kb * BK, 0, t);
+                    }
+                }
+                __syncwarp();
+                if (++stage == STAGES) stage = 0, phase ^= 1u;
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------ MMA issuer --------------------------------
+        const uint32_t idesc = idesc_mxf8(BM, NB, !TRANS, false) | (args.x_format << 10);
+        constexpr uint32_t a_step = TRANS ? 32u : 32u * 128u;
+        int stage = 0, slot = 0, acc = 0;
+        uint32_t phase = 0, sphase = 0, acc_phase = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; ok && i < args.tiles; i += gridDim.x) {
+            if (!mbar_wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
+            tc_fence_after();
+            const uint32_t d = tmem_base + (uint32_t)(acc * NB);
+            for (int kb = 0; kb < kblocks; ++kb) {
+                const uint32_t sf = tmem_base + SF_COL + 8u * slot;
+                if ((kb & 3) == 0) {
+                    if (!mbar_wait_bounded(sfull_bar(slot), sphase, abort_flag, args.err, args.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (lane == 0) {
+                        copy_scales<false>(sf, scale_desc(sSF + slot * SF_BYTES));
+                        copy_scales<false>(sf + 4, scale_desc(sSF + slot * SF_BYTES + 512));
+                    }
+                    __syncwarp();
+                }
+                if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, args.err, args.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const bool last = (kb & 3) == 3 || kb + 1 == kblocks;
+                if (lane == 0) {
+                    const uint32_t id = with_scale_id(idesc, (uint32_t)(kb & 3));
+                    const uint32_t a0 = sW + stage * W_BYTES, b0 = sX + stage * C::X_BYTES;
+#pragma unroll
+                    for (int k = 0; k < BK / 32; ++k)
+                        umma_mxf8<false>(d, sw128_operand(a0 + a_step * k, TRANS ? 16u : (uint32_t)W_BYTES),
+                                         sw128_operand(b0 + 32u * k, 16u), id, sf, sf + 4, (kb | k) != 0 ? 1u : 0u);
+                    umma_commit(empty_bar(stage));
+                    if (last) umma_commit(sempty_bar(slot));
+                }
+                __syncwarp();
+                if (++stage == STAGES) stage = 0, phase ^= 1u;
+                if (last && ++slot == SF_SLOTS) slot = 0, sphase ^= 1u;
+            }
+            if (!ok) break;
+            if (lane == 0) umma_commit(tfull_bar(acc));
+            __syncwarp();
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+    } else if (warp == 2) {
+        // ------------------------------ scales ------------------------------------
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const int groups = (kblocks + 3) / 4;
+        for (int i = blockIdx.x; ok && i < args.tiles; i += gridDim.x) {
+            const int t = i / args.n_tiles, nb = i - t * args.n_tiles;
+            for (int g = 0; g < groups; ++g) {
+                uint32_t w[4], c = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int b = 32 * j + lane;
+                    w[j] = 0x7f7f7f7fu;
+                    if (32 * j < NB && b < args.B)
+                        w[j] = __ldg(reinterpret_cast<const uint32_t*>(args.xs + ((size_t)b * args.T + t) *
+                                                                                     (size_t)args.xs_ld) + g);
+                }
+                if (TRANS) {
+                    c = __ldg(reinterpret_cast<const uint32_t*>(
+                                  args.ws + ((size_t)t * args.w_rows + nb) * (size_t)args.ws_ld) + g);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int kb = 4 * g + q < kblocks ? 4 * g + q : kblocks - 1;
+                        c |= (uint32_t)__ldg(args.ws + ((size_t)t * args.w_rows + kb) * (size_t)args.ws_ld + nb) << (8 * q);
+                    }
+                }
+                if (!mbar_wait_bounded(sempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = sSF + slot * SF_BYTES + 16u * lane;
+                st_shared_v4(dst, c, c, c, c);
+                st_shared_v4(dst + 512, w[0], w[1], w[2], w[3]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sfull_bar(slot));
+                if (++slot == SF_SLOTS) slot = 0, phase ^= 1u;
+            }
+        }
+    } else {
+        // ------------------------------ epilogue ----------------------------------
+        const int quad = warp & 3, tid = 32 * quad + lane;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int i = blockIdx.x; i < args.tiles; i += gridDim.x) {
+            const int t = i / args.n_tiles, n0 = (i - t * args.n_tiles) * BM, n = n0 + tid;
+            const float bias = args.bias && n < args.N ? __ldg(args.bias + (size_t)t * args.N + n) : 0.f;
+            if (!mbar_wait_bounded(tfull_bar(acc), acc_phase, abort_flag, args.err, args.timeout_ns)) break;
+            tc_fence_after();
+            uint32_t r[NB];
+            const uint32_t tcol = tmem_base + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * NB);
+            if constexpr (NB == 16) {
+                tmem_ld16_nowait(tcol, r);
+            } else {
+#pragma unroll
+                for (int q = 0; q < NB / 32; ++q)
+                    tmem_ld32_nowait(tcol + 32u * q, reinterpret_cast<uint32_t(&)[32]>(r[32 * q]));
+            }
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(acc));
+            float v[NB];
+#pragma unroll
+            for (int j = 0; j < NB; ++j) v[j] = __uint_as_float(r[j]) + bias;
+            if constexpr (EPI == EPI_BF16 || EPI == EPI_F32) {
+                if (n < args.N) {
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) {
+                        if (j < args.B) {
+                            const size_t at = ((size_t)j * args.T + t) * (size_t)args.N + n;
+                            if constexpr (EPI == EPI_BF16)
+                                reinterpret_cast<__nv_bfloat16*>(args.y)[at] = __float2bfloat16_rn(v[j]);
+                            else
+                                reinterpret_cast<float*>(args.y)[at] = v[j];
+                        }
+                    }
+                }
+            } else {
+                // largest magnitude of each sample's 128 columns: [output][warp][sample], two sets
+                uint32_t* m_a = red + acc * (2 * EPI_WARPS * NB);
+                uint32_t* m_u = m_a + EPI_WARPS * NB;
+                float a[NB];
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    a[j] = gelu_erf(v[j]);
+                    const uint32_t ma = __reduce_max_sync(0xffffffffu, fp8_finite_bits(a[j]));
+                    if (lane == 0) m_a[quad * NB + j] = ma;
+                    if constexpr (EPI == EPI_GELU_KEEP) {
+                        const uint32_t mu = __reduce_max_sync(0xffffffffu, fp8_finite_bits(v[j]));
+                        if (lane == 0) m_u[quad * NB + j] = mu;
+                    }
+                }
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory");
+                auto exponent = [&](const uint32_t* m, int j) {
+                    return fp8_exponent<false>(max(max(m[j], m[NB + j]), max(m[2 * NB + j], m[3 * NB + j])));
+                };
+                if (tid < NB && tid < args.B) {
+                    const size_t row = (size_t)tid * args.T + t;
+                    args.o0.scales[row * (size_t)args.o0.lds + n0 / kFp8Block] = (uint8_t)exponent(m_a, tid);
+                    if constexpr (EPI == EPI_GELU_KEEP)
+                        args.o1.scales[row * (size_t)args.o1.lds + n0 / kFp8Block] = (uint8_t)exponent(m_u, tid);
+                }
+                if (n < args.N) {
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) {
+                        if (j < args.B) {
+                            const size_t row = (size_t)j * args.T + t;
+                            args.o0.codes[row * (size_t)args.o0.ld + n] =
+                                (uint8_t)fp8_pack2<false>(fp8_poison(a[j]) * fp8_inv_scale(exponent(m_a, j)), 0.f);
+                            if constexpr (EPI == EPI_GELU_KEEP)
+                                args.o1.codes[row * (size_t)args.o1.ld + n] =
+                                    (uint8_t)fp8_pack2<false>(fp8_poison(v[j]) * fp8_inv_scale(exponent(m_u, j)), 0.f);
+                        }
+                    }
+                }
+            }
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 4) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, TMEM_COLS);
+    }
+}
+
+template <int EPI, bool TRANS, int NB>
+cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const Args& a, int num_sms, cudaStream_t s) {
+    auto k = fp8_stream_kernel<EPI, TRANS, NB>;
+    cudaError_t e = smem_attr_once((const void*)k, Cfg<NB>::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    return launch_k(k, dim3((unsigned)(a.tiles < num_sms ? a.tiles : num_sms)), dim3(THREADS), Cfg<NB>::SMEM_BYTES, s, mx, mw,
+                    a);
+}
+
+template <int EPI, bool TRANS>
+cudaError_t run_for(const CUtensorMap& mx, const CUtensorMap& mw, const Args& a, int num_sms, cudaStream_t s) {
+    if (a.B <= 16) return run<EPI, TRANS, 16>(mx, mw, a, num_sms, s);
+    if (a.B <= 32) return run<EPI, TRANS, 32>(mx, mw, a, num_sms, s);
+    return run<EPI, TRANS, 64>(mx, mw, a, num_sms, s);
+}
+
+}  // namespace f8s
+
+bool fp8_streams(const Fp8Product& p) {
+    const long long tiles = (long long)p.T * ((p.N + f8s::BM - 1) / f8s::BM);
+    return p.B <= kFp8StreamMaxB && p.epi != FP8_DGELU && tiles < (1ll << 30);
+}
+
+cudaError_t launch_fp8_stream(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s) {
+    using namespace f8s;
+    Args a{};
+    a.B = p.B, a.T = p.T, a.K = p.K, a.N = p.N;
+    a.n_tiles = (p.N + BM - 1) / BM;
+    a.kblocks = (p.K + BK - 1) / BK;
+    a.tiles = p.T * a.n_tiles;
+    a.xs = p.x.scales, a.xs_ld = p.x.lds;
+    a.ws = p.w.scales, a.ws_ld = p.w.lds;
+    const int wr = p.trans ? p.N : p.K, wc = p.trans ? p.K : p.N;
+    a.w_rows = (wr + kFp8Block - 1) / kFp8Block;
+    a.x_format = p.x.e5m2 ? 1u : 0u;
+    a.early = p.follows && pdl_enabled();
+    a.bias = p.bias;
+    a.y = p.y;
+    a.o0 = p.o0, a.o1 = p.o1;
+    a.err = dev.err;
+    a.timeout_ns = dev.timeout_ns;
+    CUtensorMap mx, mw;
+    const auto u8t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const int rows = p.B <= 16 ? 16 : p.B <= 32 ? 32 : 64;
+    if (!fp8_tensor_map(&mx, u8t, p.x.codes, p.K, p.B, p.T, p.T * p.x.ld, p.x.ld, BK, rows) ||
+        !fp8_tensor_map(&mw, u8t, p.w.codes, wc, wr, p.T, p.w.ld, (long long)wr * p.w.ld, 128, 128))
+        return cudaErrorInvalidValue;
+    switch (p.epi) {
+        case FP8_OUT_BF16:
+            return p.trans ? run_for<EPI_BF16, true>(mx, mw, a, dev.num_sms, s)
+                           : run_for<EPI_BF16, false>(mx, mw, a, dev.num_sms, s);
+        case FP8_OUT_F32:
+            return p.trans ? run_for<EPI_F32, true>(mx, mw, a, dev.num_sms, s)
+                           : run_for<EPI_F32, false>(mx, mw, a, dev.num_sms, s);
+        case FP8_GELU:
+            if (p.trans) return cudaErrorNotSupported;
+            return p.o1.codes ? run_for<EPI_GELU_KEEP, false>(mx, mw, a, dev.num_sms, s)
+                              : run_for<EPI_GELU, false>(mx, mw, a, dev.num_sms, s);
+        default: return cudaErrorNotSupported;
+    }
+}
+
+}  // namespace rm
