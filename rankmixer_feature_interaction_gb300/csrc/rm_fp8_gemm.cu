@@ -337,7 +337,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                         ok = false;
                         break;
                     }
-                    if (lane == 0) {
+                    if (elect_one()) {
                         const uint32_t fb = mapa_shared(full_bar(stage), 0);
                         if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2u * STAGE_BYTES);
                         tma_load_3d_pair(&tmX, sA + stage * A_BYTES, fb, kb * BK, xrow, tl.t);
@@ -369,7 +369,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                             break;
                         }
                         tc_fence_after();
-                        if (lane == 0) {
+                        if (elect_one()) {
                             const uint32_t src = sSF + slot * SF_BYTES;
                             copy_scales<true>(sf, scale_desc(src));
                             copy_scales<true>(sf + 4, scale_desc(src + 512));
@@ -383,7 +383,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                     }
                     tc_fence_after();
                     const bool last = (kb & 3) == 3 || kb + 1 == kblocks;
-                    if (lane == 0) {
+                    if (elect_one()) {
                         const uint32_t id = with_scale_id(idesc, (uint32_t)(kb & 3));
                         const uint32_t a0 = sA + stage * A_BYTES, b0 = sB + stage * B_BYTES;
 #pragma unroll
@@ -399,63 +399,68 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                     if (last && ++slot == SF_SLOTS) slot = 0, sphase ^= 1u;
                 }
                 if (!ok) break;
-                if (lane == 0) umma_commit_pair_mc(tfull, (uint16_t)0x3);
+                if (elect_one()) umma_commit_pair_mc(tfull, (uint16_t)0x3);
                 __syncwarp();
             }
         } else if (warp == 2) {
             // ------------------------------ scales ------------------------------------
-            int slot = 0;
-            uint32_t phase = 0;
-            bool ok = true;
+            // one group of four k-blocks ahead: its words are loaded while the slot
+            // of the current one is waited for
             const int groups = (kblocks + 3) / 4;
-            for (long long i = unit; ok && i < args.tiles; i += nunits) {
-                const Tile tl = tile_of(i, args);
-                const uint8_t* xp[4];
-                bool in[4];
+            struct Words {
+                uint32_t x[4], w[2];
+            };
+            auto load = [&](const Tile& tl, int g) {
+                Words r;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int m = tl.m0 + BM * (int)rank + 32 * j + lane;
-                    in[j] = m < args.B;
-                    xp[j] = args.xs + ((size_t)(in[j] ? m : 0) * args.T + tl.t) * (size_t)args.xs_ld;
+                    r.x[j] = 0x7f7f7f7fu;
+                    if (m < args.B)
+                        r.x[j] = __ldg(reinterpret_cast<const uint32_t*>(
+                                           args.xs + ((size_t)m * args.T + tl.t) * (size_t)args.xs_ld) + g);
                 }
-                for (int g = 0; g < groups; ++g) {
-                    uint32_t w[4], c[2];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        w[j] = in[j] ? __ldg(reinterpret_cast<const uint32_t*>(xp[j]) + g) : 0x7f7f7f7fu;
+                for (int h = 0; h < 2; ++h) {
+                    const int nb = tl.n0 / 128 + h;
+                    r.w[h] = 0x7f7f7f7fu;
+                    if (nb * 128 < args.N) {
+                        if (TRANS) {
+                            r.w[h] = __ldg(reinterpret_cast<const uint32_t*>(
+                                               args.ws + ((size_t)tl.t * args.w_rows + nb) * (size_t)args.ws_ld) + g);
+                        } else {
+                            uint32_t v = 0;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int nb = tl.n0 / 128 + h;
-                        c[h] = 0x7f7f7f7fu;
-                        if (nb * 128 < args.N) {
-                            if (TRANS) {
-                                c[h] = __ldg(reinterpret_cast<const uint32_t*>(
-                                                 args.ws + ((size_t)tl.t * args.w_rows + nb) * (size_t)args.ws_ld) + g);
-                            } else {
-                                uint32_t v = 0;
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const int kb = 4 * g + q < kblocks ? 4 * g + q : kblocks - 1;
-                                    v |= (uint32_t)__ldg(args.ws + ((size_t)tl.t * args.w_rows + kb) *
-                                                                       (size_t)args.ws_ld + nb) << (8 * q);
-                                }
-                                c[h] = v;
+                            for (int q = 0; q < 4; ++q) {
+                                const int kb = 4 * g + q < kblocks ? 4 * g + q : kblocks - 1;
+                                v |= (uint32_t)__ldg(args.ws + ((size_t)tl.t * args.w_rows + kb) * (size_t)args.ws_ld +
+                                                     nb) << (8 * q);
                             }
+                            r.w[h] = v;
                         }
                     }
-                    if (!mbar_wait_bounded(sempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t dst = sSF + slot * SF_BYTES + 16u * lane;
-                    st_shared_v4(dst, w[0], w[1], w[2], w[3]);
-                    st_shared_v4(dst + 512, c[0], c[0], c[0], c[0]);
-                    st_shared_v4(dst + 1024, c[1], c[1], c[1], c[1]);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(mapa_shared(sfull_bar(slot), 0));
-                    if (++slot == SF_SLOTS) slot = 0, phase ^= 1u;
                 }
+                return r;
+            };
+            int slot = 0, g = 0;
+            uint32_t phase = 0;
+            long long i = unit;
+            Words now{};
+            if (i < args.tiles) now = load(tile_of(i, args), 0);
+            while (i < args.tiles) {
+                if (++g == groups) g = 0, i += nunits;
+                Words next{};
+                if (i < args.tiles) next = load(tile_of(i, args), g);
+                if (!mbar_wait_bounded(sempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
+                const uint32_t dst = sSF + slot * SF_BYTES + 16u * lane;
+                st_shared_v4(dst, now.x[0], now.x[1], now.x[2], now.x[3]);
+                st_shared_v4(dst + 512, now.w[0], now.w[0], now.w[0], now.w[0]);
+                st_shared_v4(dst + 1024, now.w[1], now.w[1], now.w[1], now.w[1]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(mapa_shared(sfull_bar(slot), 0));
+                if (++slot == SF_SLOTS) slot = 0, phase ^= 1u;
+                now = next;
             }
         }
     } else {

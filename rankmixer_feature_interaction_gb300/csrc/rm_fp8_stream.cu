@@ -132,7 +132,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                     ok = false;
                     break;
                 }
-                if (lane == 0) {
+                if (elect_one()) {
                     if (warp == 0) {
                         mbar_arrive_expect_tx(full_bar(stage), W_BYTES);
                         if (TRANS)
@@ -167,7 +167,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                         break;
                     }
                     tc_fence_after();
-                    if (lane == 0) {
+                    if (elect_one()) {
                         copy_scales<false>(sf, scale_desc(sSF + slot * SF_BYTES));
                         copy_scales<false>(sf + 4, scale_desc(sSF + slot * SF_BYTES + 512));
                     }
@@ -179,7 +179,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 }
                 tc_fence_after();
                 const bool last = (kb & 3) == 3 || kb + 1 == kblocks;
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint32_t id = with_scale_id(idesc, (uint32_t)(kb & 3));
                     const uint32_t a0 = sW + stage * W_BYTES, b0 = sX + stage * C::X_BYTES;
 #pragma unroll
@@ -194,51 +194,59 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 if (last && ++slot == SF_SLOTS) slot = 0, sphase ^= 1u;
             }
             if (!ok) break;
-            if (lane == 0) umma_commit(tfull_bar(acc));
+            if (elect_one()) umma_commit(tfull_bar(acc));
             __syncwarp();
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
     } else if (warp == 2) {
         // ------------------------------ scales ------------------------------------
-        int slot = 0;
-        uint32_t phase = 0;
-        bool ok = true;
+        // one group of four k-blocks ahead, as in rm_fp8_gemm.cu
         const int groups = (kblocks + 3) / 4;
-        for (int i = blockIdx.x; ok && i < args.tiles; i += gridDim.x) {
+        struct Words {
+            uint32_t x[(NB + 31) / 32], w;
+        };
+        auto load = [&](int i, int g) {
             const int t = i / args.n_tiles, nb = i - t * args.n_tiles;
-            for (int g = 0; g < groups; ++g) {
-                uint32_t w[4], c = 0;
+            Words r;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int b = 32 * j + lane;
-                    w[j] = 0x7f7f7f7fu;
-                    if (32 * j < NB && b < args.B)
-                        w[j] = __ldg(reinterpret_cast<const uint32_t*>(args.xs + ((size_t)b * args.T + t) *
-                                                                                     (size_t)args.xs_ld) + g);
-                }
-                if (TRANS) {
-                    c = __ldg(reinterpret_cast<const uint32_t*>(
-                                  args.ws + ((size_t)t * args.w_rows + nb) * (size_t)args.ws_ld) + g);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int kb = 4 * g + q < kblocks ? 4 * g + q : kblocks - 1;
-                        c |= (uint32_t)__ldg(args.ws + ((size_t)t * args.w_rows + kb) * (size_t)args.ws_ld + nb) << (8 * q);
-                    }
-                }
-                if (!mbar_wait_bounded(sempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t dst = sSF + slot * SF_BYTES + 16u * lane;
-                st_shared_v4(dst, c, c, c, c);
-                st_shared_v4(dst + 512, w[0], w[1], w[2], w[3]);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sfull_bar(slot));
-                if (++slot == SF_SLOTS) slot = 0, phase ^= 1u;
+            for (int j = 0; j < (NB + 31) / 32; ++j) {
+                const int b = 32 * j + lane;
+                r.x[j] = 0x7f7f7f7fu;
+                if (b < args.B)
+                    r.x[j] = __ldg(reinterpret_cast<const uint32_t*>(args.xs + ((size_t)b * args.T + t) *
+                                                                                  (size_t)args.xs_ld) + g);
             }
+            if (TRANS) {
+                r.w = __ldg(reinterpret_cast<const uint32_t*>(
+                                args.ws + ((size_t)t * args.w_rows + nb) * (size_t)args.ws_ld) + g);
+            } else {
+                r.w = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int kb = 4 * g + q < kblocks ? 4 * g + q : kblocks - 1;
+                    r.w |= (uint32_t)__ldg(args.ws + ((size_t)t * args.w_rows + kb) * (size_t)args.ws_ld + nb) << (8 * q);
+                }
+            }
+            return r;
+        };
+        int slot = 0, g = 0, i = blockIdx.x;
+        uint32_t phase = 0;
+        Words now{};
+        if (i < args.tiles) now = load(i, 0);
+        while (i < args.tiles) {
+            if (++g == groups) g = 0, i += gridDim.x;
+            Words next{};
+            if (i < args.tiles) next = load(i, g);
+            if (!mbar_wait_bounded(sempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
+            const uint32_t dst = sSF + slot * SF_BYTES + 16u * lane;
+            st_shared_v4(dst, now.w, now.w, now.w, now.w);
+            st_shared_v4(dst + 512, now.x[0], NB > 32 ? now.x[(NB > 32)] : 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sfull_bar(slot));
+            if (++slot == SF_SLOTS) slot = 0, phase ^= 1u;
+            now = next;
         }
     } else {
         // ------------------------------ epilogue ----------------------------------

@@ -78,6 +78,20 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
         asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
+// One lane of a converged warp.  The tensor-core and TMA instructions take their
+// operands from uniform registers: behind this instruction the compiler knows
+// that one lane runs and moves them there once; behind a lane comparison it
+// loops over the lanes that might (78 cycles for each MMA's issue).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Arrive on the pair's barrier (a shared::cluster address) after writes to this
 // CTA's own shared memory that fence_proxy_async_smem has ordered before the
 // tensor core's reads of it.  The fence carries the data; the arrival needs no

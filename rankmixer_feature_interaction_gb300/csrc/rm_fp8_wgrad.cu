@@ -215,7 +215,7 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                     ok = false;
                     break;
                 }
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint32_t fb = mapa_shared(full_bar(stage), 0);
                     if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2u * B_BYTES);
 #pragma unroll
@@ -238,7 +238,7 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                     ok = false;
                     break;
                 }
-                if (lane == 0) {
+                if (elect_one()) {
                     mbar_arrive_expect_tx(rfull_bar(slot), RAW_BYTES);
                     tma_load_3d(&tmX, sRaw + slot * RAW_BYTES, rfull_bar(slot), tl.m0 + BM * (int)rank, kb * BK, tl.t);
                 }
@@ -265,7 +265,7 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                     break;
                 }
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint32_t a0 = sA + stage * A_BYTES, b0 = sB + stage * B_BYTES;
 #pragma unroll
                     for (int k = 0; k < BK / 16; ++k)        // 16 samples: 16 rows of 128 bytes
@@ -276,7 +276,7 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 __syncwarp();
                 if (++stage == STAGES) stage = 0, phase ^= 1u;
                 if (++in_chunk == args.chunk_blocks || kb + 1 == kblocks) {
-                    if (lane == 0) umma_commit_pair_mc(tfull_bar(acc), (uint16_t)0x3);
+                    if (elect_one()) umma_commit_pair_mc(tfull_bar(acc), (uint16_t)0x3);
                     __syncwarp();
                     in_chunk = 0;
                     acc ^= 1;
