@@ -333,7 +333,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                 const Tile tl = tile_of(i, args);
                 const int xrow = tl.m0 + BM * (int)rank, wcol = tl.n0 + BN / 2 * (int)rank;
                 for (int kb = 0; kb < kblocks; ++kb) {
-                    if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                    if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
                         ok = false;
                         break;
                     }
@@ -354,17 +354,18 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             // ------------------------------ MMA issuer --------------------------------
             const uint32_t idesc = idesc_mxf8(2 * BM, BN, false, !TRANS) | (args.x_format << 7);
             constexpr uint32_t b_step = TRANS ? 32u : 32u * 128u;      // 32 values of K further
+            const uint64_t a_desc = sw128_operand(sA, 16u), b_desc = sw128_operand(sB, TRANS ? 16u : (uint32_t)B_BYTES);
             int stage = 0, slot = 0;
             uint32_t phase = 0, sphase = 0, aphase = 0;
             bool ok = true;
             for (long long i = unit; ok && i < args.tiles; i += nunits) {
-                if (!mbar_wait_bounded(tempty, aphase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
+                if (!wait_bounded(tempty, aphase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
                 aphase ^= 1u;
                 tc_fence_after();
                 for (int kb = 0; kb < kblocks; ++kb) {
                     const uint32_t sf = tmem_base + SF_COL + 16u * slot;
                     if ((kb & 3) == 0) {
-                        if (!mbar_wait_bounded(sfull_bar(slot), sphase, abort_flag, args.err, args.timeout_ns)) {
+                        if (!wait_bounded(sfull_bar(slot), sphase, abort_flag, args.err, args.timeout_ns)) {
                             ok = false;
                             break;
                         }
@@ -377,7 +378,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                         }
                         __syncwarp();
                     }
-                    if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, args.err, args.timeout_ns)) {
+                    if (!wait_bounded(full_bar(stage), phase, abort_flag, args.err, args.timeout_ns)) {
                         ok = false;
                         break;
                     }
@@ -385,12 +386,12 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                     const bool last = (kb & 3) == 3 || kb + 1 == kblocks;
                     if (elect_one()) {
                         const uint32_t id = with_scale_id(idesc, (uint32_t)(kb & 3));
-                        const uint32_t a0 = sA + stage * A_BYTES, b0 = sB + stage * B_BYTES;
+                        const uint64_t a = a_desc + (uint32_t)(stage * (A_BYTES >> 4));
+                        const uint64_t b = b_desc + (uint32_t)(stage * (B_BYTES >> 4));
 #pragma unroll
                         for (int k = 0; k < BK / 32; ++k)
-                            umma_mxf8<true>(tmem_base, sw128_operand(a0 + 32u * k, 16u),
-                                            sw128_operand(b0 + b_step * k, TRANS ? 16u : (uint32_t)B_BYTES), id, sf,
-                                            sf + 4, (kb | k) != 0 ? 1u : 0u);
+                            umma_mxf8<true>(tmem_base, a + 2u * k, b + (b_step >> 4) * k, id, sf, sf + 4,
+                                            (kb | k) != 0 ? 1u : 0u);
                         umma_commit_pair_mc(empty_bar(stage), (uint16_t)0x3);
                         if (last) umma_commit_pair_mc(sempty_bar(slot), (uint16_t)0x3);
                     }
@@ -451,7 +452,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                 if (++g == groups) g = 0, i += nunits;
                 Words next{};
                 if (i < args.tiles) next = load(tile_of(i, args), g);
-                if (!mbar_wait_bounded(sempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
+                if (!wait_bounded(sempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
                 const uint32_t dst = sSF + slot * SF_BYTES + 16u * lane;
                 st_shared_v4(dst, now.x[0], now.x[1], now.x[2], now.x[3]);
                 st_shared_v4(dst + 512, now.w[0], now.w[0], now.w[0], now.w[0]);
@@ -485,7 +486,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                                 : make_uint4(0, 0, 0, 0);
                 if (here) u_byte = __ldg(args.us + row * (size_t)args.us_ld + n / kFp8Block);
             }
-            if (!mbar_wait_bounded(tfull, phase, abort_flag, args.err, args.timeout_ns)) break;
+            if (!wait_bounded(tfull, phase, abort_flag, args.err, args.timeout_ns)) break;
             phase ^= 1u;
             tc_fence_after();
             uint32_t r[4][32];

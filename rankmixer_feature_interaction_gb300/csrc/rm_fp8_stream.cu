@@ -128,7 +128,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         for (int i = blockIdx.x; ok && i < args.tiles; i += gridDim.x) {
             const int t = i / args.n_tiles, n0 = (i - t * args.n_tiles) * BM;
             for (int kb = 0; kb < kblocks; ++kb) {
-                if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
                     ok = false;
                     break;
                 }
@@ -152,17 +152,18 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         // ------------------------------ MMA issuer --------------------------------
         const uint32_t idesc = idesc_mxf8(BM, NB, !TRANS, false) | (args.x_format << 10);
         constexpr uint32_t a_step = TRANS ? 32u : 32u * 128u;
+        const uint64_t a_desc = sw128_operand(sW, TRANS ? 16u : (uint32_t)W_BYTES), b_desc = sw128_operand(sX, 16u);
         int stage = 0, slot = 0, acc = 0;
         uint32_t phase = 0, sphase = 0, acc_phase = 0;
         bool ok = true;
         for (int i = blockIdx.x; ok && i < args.tiles; i += gridDim.x) {
-            if (!mbar_wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
+            if (!wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
             tc_fence_after();
             const uint32_t d = tmem_base + (uint32_t)(acc * NB);
             for (int kb = 0; kb < kblocks; ++kb) {
                 const uint32_t sf = tmem_base + SF_COL + 8u * slot;
                 if ((kb & 3) == 0) {
-                    if (!mbar_wait_bounded(sfull_bar(slot), sphase, abort_flag, args.err, args.timeout_ns)) {
+                    if (!wait_bounded(sfull_bar(slot), sphase, abort_flag, args.err, args.timeout_ns)) {
                         ok = false;
                         break;
                     }
@@ -173,7 +174,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                     }
                     __syncwarp();
                 }
-                if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, args.err, args.timeout_ns)) {
+                if (!wait_bounded(full_bar(stage), phase, abort_flag, args.err, args.timeout_ns)) {
                     ok = false;
                     break;
                 }
@@ -181,11 +182,11 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 const bool last = (kb & 3) == 3 || kb + 1 == kblocks;
                 if (elect_one()) {
                     const uint32_t id = with_scale_id(idesc, (uint32_t)(kb & 3));
-                    const uint32_t a0 = sW + stage * W_BYTES, b0 = sX + stage * C::X_BYTES;
+                    const uint64_t a = a_desc + (uint32_t)(stage * (W_BYTES >> 4));
+                    const uint64_t b = b_desc + (uint32_t)(stage * (C::X_BYTES >> 4));
 #pragma unroll
                     for (int k = 0; k < BK / 32; ++k)
-                        umma_mxf8<false>(d, sw128_operand(a0 + a_step * k, TRANS ? 16u : (uint32_t)W_BYTES),
-                                         sw128_operand(b0 + 32u * k, 16u), id, sf, sf + 4, (kb | k) != 0 ? 1u : 0u);
+                        umma_mxf8<false>(d, a + (a_step >> 4) * k, b + 2u * k, id, sf, sf + 4, (kb | k) != 0 ? 1u : 0u);
                     umma_commit(empty_bar(stage));
                     if (last) umma_commit(sempty_bar(slot));
                 }
@@ -238,7 +239,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             if (++g == groups) g = 0, i += gridDim.x;
             Words next{};
             if (i < args.tiles) next = load(i, g);
-            if (!mbar_wait_bounded(sempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
+            if (!wait_bounded(sempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
             const uint32_t dst = sSF + slot * SF_BYTES + 16u * lane;
             st_shared_v4(dst, now.w, now.w, now.w, now.w);
             st_shared_v4(dst + 512, now.x[0], NB > 32 ? now.x[(NB > 32)] : 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
@@ -256,7 +257,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         for (int i = blockIdx.x; i < args.tiles; i += gridDim.x) {
             const int t = i / args.n_tiles, n0 = (i - t * args.n_tiles) * BM, n = n0 + tid;
             const float bias = args.bias && n < args.N ? __ldg(args.bias + (size_t)t * args.N + n) : 0.f;
-            if (!mbar_wait_bounded(tfull_bar(acc), acc_phase, abort_flag, args.err, args.timeout_ns)) break;
+            if (!wait_bounded(tfull_bar(acc), acc_phase, abort_flag, args.err, args.timeout_ns)) break;
             tc_fence_after();
             uint32_t r[NB];
             const uint32_t tcol = tmem_base + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * NB);

@@ -92,6 +92,16 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
+// mbar_wait_bounded that looks at the clock only after some tries: reading the
+// global timer takes longer than most of these waits.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort, int* err,
+                                             uint64_t timeout_ns) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_bounded(bar, parity, abort, err, timeout_ns);
+}
+
 // Arrive on the pair's barrier (a shared::cluster address) after writes to this
 // CTA's own shared memory that fence_proxy_async_smem has ordered before the
 // tensor core's reads of it.  The fence carries the data; the arrival needs no

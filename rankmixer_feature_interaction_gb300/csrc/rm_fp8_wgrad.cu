@@ -37,9 +37,10 @@ constexpr int RAW_BYTES = BK * BM;           // 64 samples x 128 codes
 constexpr int A_BYTES = BK * BM * 2;         // the same in bf16: two boxes of 64 columns x 64 samples
 constexpr int B_BYTES = BK * (BN / 2) * 2;   // dY: two boxes of 64 columns x 64 samples
 constexpr int BOX_BYTES = 64 * BK * 2;
-constexpr int STAGES = 5, RAWS = 4;
+constexpr int STAGES = 4, RAWS = 8;
 constexpr int EPI_WARPS = 8, CONV_WARPS = 8;
-constexpr int CONV_GROUP = 2;                // restoring warps per k-block
+constexpr int CONV_GROUP = 4;                // restoring warps per k-block
+constexpr int GROUPS = CONV_WARPS / CONV_GROUP;
 constexpr int AHEAD = 8;                     // k-blocks whose exponent bytes are loaded together
 // Float32 gradients of more samples are summed in chunks of this many: a chunk's
 // sum leaves the tensor cores' accumulator (which truncates each addition) and
@@ -49,7 +50,7 @@ constexpr int STAGING = 4096;
 constexpr int THREADS = 128 + 32 * (EPI_WARPS + CONV_WARPS);
 constexpr int SMEM_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES) + RAWS * (RAW_BYTES + BK) + EPI_WARPS * STAGING + 256;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-static_assert(RAWS * CONV_GROUP == CONV_WARPS && RAWS < STAGES, "a raw slot per group of restorers");
+static_assert(GROUPS <= RAWS && GROUPS <= STAGES, "a k-block per group of restorers");
 
 struct Args {
     int B, T, K, N;
@@ -211,7 +212,7 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             const Tile tl = tile_of(i, args);
             const int col = tl.n0 + BN / 2 * (int)rank;
             for (int kb = 0; kb < kblocks; ++kb) {
-                if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
                     ok = false;
                     break;
                 }
@@ -234,7 +235,7 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         for (long long i = unit; ok && i < args.tiles; i += nunits) {
             const Tile tl = tile_of(i, args);
             for (int kb = 0; kb < kblocks; ++kb) {
-                if (!mbar_wait_bounded(rempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                if (!wait_bounded(rempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
                     ok = false;
                     break;
                 }
@@ -248,6 +249,7 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         }
     } else if (warp == 1 && rank == 0) {
         // ------------------------------ MMA issuer --------------------------------
+        const uint64_t a_desc = sw128_operand(sA, BOX_BYTES), b_desc = sw128_operand(sB, BOX_BYTES);
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true;
@@ -255,22 +257,22 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             int in_chunk = 0;
             for (int kb = 0; kb < kblocks; ++kb) {
                 if (in_chunk == 0 &&
-                    !mbar_wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                    !wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
                     ok = false;
                     break;
                 }
                 const uint32_t d = tmem_base + (uint32_t)(acc * BN);
-                if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, args.err, args.timeout_ns)) {
+                if (!wait_bounded(full_bar(stage), phase, abort_flag, args.err, args.timeout_ns)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t a0 = sA + stage * A_BYTES, b0 = sB + stage * B_BYTES;
+                    const uint64_t a = a_desc + (uint32_t)(stage * (A_BYTES >> 4));
+                    const uint64_t b = b_desc + (uint32_t)(stage * (B_BYTES >> 4));
 #pragma unroll
                     for (int k = 0; k < BK / 16; ++k)        // 16 samples: 16 rows of 128 bytes
-                        umma_f16_pair(d, sw128_operand(a0 + 2048u * k, BOX_BYTES), sw128_operand(b0 + 2048u * k, BOX_BYTES),
-                                      kIdesc, (in_chunk | k) != 0 ? 1u : 0u);
+                        umma_f16_pair(d, a + 128u * k, b + 128u * k, kIdesc, (in_chunk | k) != 0 ? 1u : 0u);
                     umma_commit_pair_mc(empty_bar(stage), (uint16_t)0x3);
                 }
                 __syncwarp();
@@ -306,7 +308,7 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
 #pragma unroll
                 for (int q = 0; q < AHEAD; ++q) {
                     if (ok && kb0 + q < kblocks) {
-                        ok = mbar_wait_bounded(rempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns);
+                        ok = wait_bounded(rempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns);
                         if (ok) {
                             st_shared_u8(sExp + BK * slot + lane, E[q][0]);
                             st_shared_u8(sExp + BK * slot + 32 + lane, E[q][1]);
@@ -320,34 +322,34 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         }
     } else if (warp >= 12) {
         // ------------------------------ restorers ---------------------------------
-        // Four groups of two warps, each with every fourth k-block (and the raw slot
-        // of that number), so that four k-blocks' latencies overlap.  Lane's 16-byte
-        // chunks: column chunk c of eight of its warp's 32 rows.  The two rows that a
-        // group of eight lanes reads at a time differ by 5 in their low three bits,
-        // which keeps both the reads (chunk c of row r at c ^ (r % 8)) and the writes
-        // (pieces 2 (c % 4), + 1 at ^ (r % 8)) free of bank conflicts.
-        const uint32_t cw = warp - 12, slot = cw >> 1;
+        // Two groups of four warps, each with every other k-block, so that one's
+        // latencies (barriers, shared memory, the fence) pass while the other works.
+        // Lane's 16-byte chunks: column chunk c of four of its warp's 16 rows.  The two
+        // rows that a group of eight lanes reads at a time differ by 5 in their low
+        // three bits, which keeps both the reads (chunk c of row r at c ^ (r % 8)) and
+        // the writes (pieces 2 (c % 4), + 1 at ^ (r % 8)) free of bank conflicts.
+        const uint32_t cw = (uint32_t)(warp - 12) % CONV_GROUP, group = (uint32_t)(warp - 12) / CONV_GROUP;
         const uint32_t c = (lane & 3) | ((lane >> 1) & 4), p = 2u * (c & 3u);
         const uint32_t flip = (lane & 4) ? 5 : 0, rep0 = lane >> 4;
-        const uint32_t src = sRaw + slot * RAW_BYTES, exps = sExp + BK * slot;
+        uint32_t slot = group;
         uint32_t rphase = 0;
         long long done = 0;                          // k-blocks before this tile
-        int stage = (int)slot % STAGES;              // of the group's next k-block
+        int stage = (int)group;                      // of the group's next k-block
         uint32_t phase = 0;
-        long long next = slot;
+        long long next = group;
         bool ok = true;
         for (long long i = unit; ok && i < args.tiles; i += nunits, done += kblocks) {
-            for (; next < done + kblocks; next += RAWS) {
-                if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns) ||
-                    !mbar_wait_bounded(rfull_bar(slot), rphase, abort_flag, args.err, args.timeout_ns)) {
+            for (; next < done + kblocks; next += GROUPS) {
+                if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns) ||
+                    !wait_bounded(rfull_bar(slot), rphase, abort_flag, args.err, args.timeout_ns)) {
                     ok = false;
                     break;
                 }
-                rphase ^= 1u;
+                const uint32_t src = sRaw + slot * RAW_BYTES, exps = sExp + BK * slot;
                 const uint32_t dst = sA + stage * A_BYTES + (c >> 2) * BOX_BYTES;
 #pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) {
-                    const uint32_t x7 = (rep0 | ((j & 1u) << 1)) ^ flip, r = 32u * (cw & 1u) + 8u * (j >> 1) + x7;
+                for (uint32_t j = 0; j < BK / CONV_GROUP / 4; ++j) {
+                    const uint32_t x7 = (rep0 | ((j & 1u) << 1)) ^ flip, r = BK / CONV_GROUP * cw + 8u * (j >> 1) + x7;
                     uint32_t o[8];
                     restore16(ld_shared_u4(src + 128u * r + 16u * (c ^ x7)), ld_shared_u8(exps + r), o);
                     st_shared_v4(dst + 128u * r + 16u * (p ^ x7), o[0], o[1], o[2], o[3]);
@@ -359,8 +361,10 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                     mbar_arrive_pair(mapa_shared(full_bar(stage), 0));
                     mbar_arrive(rempty_bar(slot));
                 }
-                stage += RAWS;
+                stage += GROUPS;
                 if (stage >= STAGES) stage -= STAGES, phase ^= 1u;
+                slot += GROUPS;
+                if (slot >= RAWS) slot -= RAWS, rphase ^= 1u;
             }
         }
     } else if (warp >= 4) {
@@ -375,7 +379,7 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
           const Tile tl = tile_of(i, args);
           for (int chunk = 0; chunk < args.chunks; ++chunk) {
             const int m = tl.m0 + BM * (int)rank + 32 * quad, n = tl.n0 + 128 * half;
-            if (!mbar_wait_bounded(tfull_bar(acc), acc_phase, abort_flag, args.err, args.timeout_ns)) {
+            if (!wait_bounded(tfull_bar(acc), acc_phase, abort_flag, args.err, args.timeout_ns)) {
                 ok = false;
                 break;
             }
