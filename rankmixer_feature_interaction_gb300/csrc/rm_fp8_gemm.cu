@@ -21,8 +21,10 @@
 //                512 bytes per 128 rows to tensor memory (tcgen05.cp)
 //   warps 4-11   epilogue: each thread owns one row's 128 columns, which is one
 //                block of an 8-bit output: its largest value needs no exchange
-// Tensor memory: accumulator in columns 0-255, a ring of four scale slots from
-// column 448 (4 columns for x's 128 rows, 8 for W's 256 columns).
+// Tensor memory (512 columns): two accumulators of 256 columns that share 64,
+// at columns 0 and 192, so that the next tile's product begins as soon as those
+// 64 columns have been read, and a ring of four scale slots from column 448 (4
+// columns for x's 128 rows, 8 for W's 256 columns).
 // Every mbarrier wait is bounded in time; on expiry the CTA latches an error
 // word and all roles unwind.
 #include <cudaTypedefs.h>
@@ -48,6 +50,7 @@ constexpr int SF_BYTES = 512 * 3;        // x: 128 rows, W: 2 x 128 columns
 constexpr int EPI_WARPS = 8;
 constexpr int STAGING = 4096;            // per epilogue warp: 32 rows of 128 bytes
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
+constexpr uint32_t ACC1_COL = 192;       // the second accumulator's first column
 constexpr int SF_COL = 448;
 constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * STAGING + SF_SLOTS * SF_BYTES + 256;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
@@ -117,18 +120,24 @@ __device__ __forceinline__ void staging_free(int lane) {
     __syncwarp();
 }
 
-__device__ __forceinline__ uint32_t row_amax(const float (&v)[128]) {
-    uint32_t m = 0;
+__device__ __forceinline__ float row_amax(const float (&v)[128]) {
+    float m[4] = {};
 #pragma unroll
-    for (int i = 0; i < 128; ++i) m = max(m, fp8_finite_bits(v[i]));
-    return m;
+    for (int i = 0; i < 128; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(v[i]));    // passes over NaN
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
 // The row's 128 values in 8 bits: codes staged and stored, the exponent byte to *scale.
-__device__ __forceinline__ void save_row(const float (&v)[128], const CUtensorMap* map, uint32_t stage, uint8_t* scale,
+__device__ __forceinline__ void save_row(float (&v)[128], const CUtensorMap* map, uint32_t stage, uint8_t* scale,
                                          int n, int m_warp, int t, int lane, bool store, bool row_ok) {
-    const uint32_t E = fp8_exponent<false>(row_amax(v));
-    const float s = fp8_inv_scale(E);
+    float amax = row_amax(v);
+    if (amax == __int_as_float(0x7f800000)) {          // infinities become NaN and do not count
+#pragma unroll
+        for (int i = 0; i < 128; ++i) v[i] = fp8_poison(v[i]);
+        amax = row_amax(v);
+    }
+    const uint32_t E = fp8_exponent<false>(__float_as_uint(amax));
+    const uint64_t s = f2_splat(fp8_inv_scale(E));
     staging_free(lane);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
@@ -136,8 +145,10 @@ __device__ __forceinline__ void save_row(const float (&v)[128], const CUtensorMa
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int i = 16 * c + 4 * j;
-            w[j] = fp8_pack4<false>(fp8_poison(v[i]) * s, fp8_poison(v[i + 1]) * s, fp8_poison(v[i + 2]) * s,
-                                    fp8_poison(v[i + 3]) * s);
+            float q[4];
+            f2_unpack(f2_mul(f2_pack(v[i], v[i + 1]), s), q[0], q[1]);
+            f2_unpack(f2_mul(f2_pack(v[i + 2], v[i + 3]), s), q[2], q[3]);
+            w[j] = fp8_pack4<false>(q[0], q[1], q[2], q[3]);
         }
         stage16(stage, lane, c, w[0], w[1], w[2], w[3]);
     }
@@ -285,8 +296,10 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
     auto sfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
     auto sempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + SF_SLOTS + s); };
-    const uint32_t tfull = bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS), tempty = tfull + 8u;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (tempty + 8u - base));
+    auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + x); };
+    auto tempty_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 2 + x); };
+    const uint32_t shared_bar = bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 4);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (shared_bar + 8u - base));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -304,8 +317,11 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             mbar_init(sfull_bar(s), 2);          // the even CTA's: both CTAs' scale warps
             mbar_init(sempty_bar(s), 1);         // multicast commit
         }
-        mbar_init(tfull, 1);                     // multicast commit
-        mbar_init(tempty, 2 * EPI_WARPS);        // the even CTA's: every epilogue warp of both CTAs
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(tfull_bar(x), 1);              // multicast commit
+            mbar_init(tempty_bar(x), 2 * EPI_WARPS); // the even CTA's: every epilogue warp of both CTAs
+        }
+        mbar_init(shared_bar, EPI_WARPS);        // the even CTA's: the warps that own the shared columns
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -356,12 +372,17 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             constexpr uint32_t b_step = TRANS ? 32u : 32u * 128u;      // 32 values of K further
             const uint64_t a_desc = sw128_operand(sA, 16u), b_desc = sw128_operand(sB, TRANS ? 16u : (uint32_t)B_BYTES);
             int stage = 0, slot = 0;
-            uint32_t phase = 0, sphase = 0, aphase = 0;
+            uint32_t phase = 0, sphase = 0, aphase = 0, cphase = 0;
+            int acc = 0;
             bool ok = true;
             for (long long i = unit; ok && i < args.tiles; i += nunits) {
-                if (!wait_bounded(tempty, aphase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
-                aphase ^= 1u;
+                // this accumulator's last tile is out, and of the other's tile the shared columns
+                if (!wait_bounded(tempty_bar(acc), aphase ^ 1u, abort_flag, args.err, args.timeout_ns) ||
+                    !wait_bounded(shared_bar, cphase ^ 1u, abort_flag, args.err, args.timeout_ns))
+                    break;
+                cphase ^= 1u;
                 tc_fence_after();
+                const uint32_t d = tmem_base + (acc ? ACC1_COL : 0u);
                 for (int kb = 0; kb < kblocks; ++kb) {
                     const uint32_t sf = tmem_base + SF_COL + 16u * slot;
                     if ((kb & 3) == 0) {
@@ -390,7 +411,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                         const uint64_t b = b_desc + (uint32_t)(stage * (B_BYTES >> 4));
 #pragma unroll
                         for (int k = 0; k < BK / 32; ++k)
-                            umma_mxf8<true>(tmem_base, a + 2u * k, b + (b_step >> 4) * k, id, sf, sf + 4,
+                            umma_mxf8<true>(d, a + 2u * k, b + (b_step >> 4) * k, id, sf, sf + 4,
                                             (kb | k) != 0 ? 1u : 0u);
                         umma_commit_pair_mc(empty_bar(stage), (uint16_t)0x3);
                         if (last) umma_commit_pair_mc(sempty_bar(slot), (uint16_t)0x3);
@@ -400,8 +421,10 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                     if (last && ++slot == SF_SLOTS) slot = 0, sphase ^= 1u;
                 }
                 if (!ok) break;
-                if (elect_one()) umma_commit_pair_mc(tfull, (uint16_t)0x3);
+                if (elect_one()) umma_commit_pair_mc(tfull_bar(acc), (uint16_t)0x3);
                 __syncwarp();
+                acc ^= 1;
+                if (acc == 0) aphase ^= 1u;
             }
         } else if (warp == 2) {
             // ------------------------------ scales ------------------------------------
@@ -469,8 +492,9 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
         regs_inc<REGS_EPI>();
         const int quad = warp & 3, half = (warp - 4) >> 2;
         const uint32_t stage = sEpi + (uint32_t)(warp - 4) * STAGING;
-        const uint32_t tempty_leader = mapa_shared(tempty, 0);
+        const uint32_t shared_leader = mapa_shared(shared_bar, 0);
         uint32_t phase = 0;
+        int acc = 0;
         for (long long i = unit; i < args.tiles; i += nunits) {
             const Tile tl = tile_of(i, args);
             const int m_warp = tl.m0 + BM * (int)rank + 32 * quad, n = tl.n0 + 128 * half;
@@ -486,17 +510,39 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                                 : make_uint4(0, 0, 0, 0);
                 if (here) u_byte = __ldg(args.us + row * (size_t)args.us_ld + n / kFp8Block);
             }
-            if (!wait_bounded(tfull, phase, abort_flag, args.err, args.timeout_ns)) break;
-            phase ^= 1u;
+            if (!wait_bounded(tfull_bar(acc), phase, abort_flag, args.err, args.timeout_ns)) break;
             tc_fence_after();
+            // The whole row comes out at once, so the accumulator is free again long
+            // before the epilogue is done; first of all the 64 columns that the other
+            // accumulator shares (the last of accumulator 0, the first of 1).
             uint32_t r[4][32];
-            const uint32_t tcol = tmem_base + ((uint32_t)(32 * quad) << 16) + 128u * half;
+            const uint32_t tcol =
+                tmem_base + ((uint32_t)(32 * quad) << 16) + (acc ? ACC1_COL : 0u) + 128u * half;
+            auto load_half = [&](int h) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32_nowait(tcol + 32u * c, r[c]);
+                for (int c = 0; c < 2; ++c) tmem_ld32_nowait(tcol + 64u * h + 32u * c, r[2 * h + c]);
+            };
+            auto shared_out = [&]() {
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(shared_leader);
+            };
+            if (half == 1) {
+                load_half(1);
+                if (acc == 0) shared_out();
+                load_half(0);
+            } else {
+                load_half(0);
+                if (acc == 1) shared_out();
+                load_half(1);
+            }
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty_leader);
+            if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(acc), 0));
+            acc ^= 1;
+            if (acc == 0) phase ^= 1u;
             float v[128];
 #pragma unroll
             for (int c = 0; c < 128; ++c) v[c] = __uint_as_float(r[c >> 5][c & 31]);

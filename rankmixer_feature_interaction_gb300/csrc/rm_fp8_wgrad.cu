@@ -423,7 +423,7 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+            if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(acc), 0));
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
           }
