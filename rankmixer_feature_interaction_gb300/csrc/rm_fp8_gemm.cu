@@ -44,7 +44,6 @@ constexpr int BK = 128;                  // one scale block
 constexpr int A_BYTES = BM * BK;
 constexpr int B_BYTES = BN / 2 * BK;     // this CTA's half of the columns
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int STAGES = 5;
 constexpr int SF_SLOTS = 4;
 constexpr int SF_BYTES = 512 * 3;        // x: 128 rows, W: 2 x 128 columns
 constexpr int EPI_WARPS = 8;
@@ -52,12 +51,21 @@ constexpr int STAGING = 4096;            // per epilogue warp: 32 rows of 128 by
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr uint32_t ACC1_COL = 192;       // the second accumulator's first column
 constexpr int SF_COL = 448;
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * STAGING + SF_SLOTS * SF_BYTES + 256;
-static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 // registers: 384 threads launched with 168; 128 x 80 + 256 x 208 <= 384 x 168
 constexpr int REGS_OTHER = 80, REGS_EPI = 208;
 
 enum Epi { EPI_BF16, EPI_F32, EPI_GELU, EPI_GELU_KEEP, EPI_DGELU };
+
+// Shared memory: the stages, 4 KB of staging per epilogue warp, the scale slots;
+// for DGELU 4 KB more per epilogue warp for the next tile's kept u, and a stage less.
+template <int EPI>
+struct Cfg {
+    static constexpr int STAGES = EPI == EPI_DGELU ? 4 : 5;
+    static constexpr int U_BYTES = EPI == EPI_DGELU ? EPI_WARPS * STAGING : 0;
+    static constexpr int SMEM_BYTES =
+        1024 + STAGES * STAGE_BYTES + EPI_WARPS * STAGING + U_BYTES + SF_SLOTS * SF_BYTES + 256;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+};
 
 struct Args {
     int B, T, K, N;
@@ -70,14 +78,9 @@ struct Args {
     int w_rows;
     uint32_t x_format;                   // 0 e4m3, 1 e5m2
     const float* bias;                   // [T][N] or null
-    void* y;                             // stored directly where the rows do not suit TMA
-    bool direct;
-    uint8_t* s0;                         // exponent bytes of the 8-bit outputs (GELU: a; DGELU: dU)
-    uint8_t* s1;                         // GELU_KEEP: u
-    long long s0_ld, s1_ld;
-    const uint8_t* u;                    // DGELU: kept u's codes and exponent bytes
-    const uint8_t* us;
-    long long u_ld, us_ld;
+    void* y;                             // [B][T][N]
+    bool vec;                            // y's rows are 16-byte aligned
+    Fp8View o0, o1;                      // GELU: a, u (kept); DGELU: dU, the kept u
     float* colpart;                      // DGELU: sums of dU over 32 rows, [T][m_tiles * 8][N]
     int* err;
     unsigned long long timeout_ns;
@@ -98,25 +101,49 @@ __device__ __forceinline__ Tile tile_of(long long i, const Args& a) {
     return r;
 }
 
-// One row's 128 bytes into this warp's staging (128-byte swizzle: 16-byte piece
-// c of row r at c ^ (r % 8)), four codes or two bf16 per word.
+// One row's 128 bytes into this warp's staging, 16 bytes at a time: piece c of
+// row r at c ^ (r % 8), which keeps rows and pieces free of bank conflicts.
 __device__ __forceinline__ void stage16(uint32_t stage, int lane, int c, uint32_t w0, uint32_t w1, uint32_t w2,
                                         uint32_t w3) {
     st_shared_v4(stage + 128u * lane + 16u * (uint32_t)(c ^ (lane & 7)), w0, w1, w2, w3);
 }
-
-// The staged 32 rows to their place: columns from n, samples from m.
-__device__ __forceinline__ void store_staged(const CUtensorMap* map, uint32_t stage, int n, int m, int t, int lane,
-                                             bool inside) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-        if (inside) tma_store_3d(map, stage, n, m, t);
-        bulk_commit_group();
-    }
+__device__ __forceinline__ uint4 staged16(uint32_t stage, int row, int c) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(stage + 128u * row + 16u * (uint32_t)(c ^ (row & 7))));
+    return v;
 }
-__device__ __forceinline__ void staging_free(int lane) {
-    if (lane == 0) bulk_wait_group_read<0>();
+
+// The staged 32 rows to memory: row r at dst + r pitch, the first `rows` of them,
+// of each the first `bytes` (whole 16-byte pieces when VEC, else elements of ESZ
+// bytes).  Eight lanes write a row's 128 bytes.  Plain stores: the staging is
+// free again after a warp barrier, where a bulk copy's reads would be waited for.
+template <bool VEC, int ESZ>
+__device__ __forceinline__ void store_rows(uint32_t stage, char* dst, size_t pitch, int rows, int bytes, int lane) {
+    __syncwarp();
+    const int c = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        if (r < rows && 16 * c < bytes) {
+            const uint4 v = staged16(stage, r, c);
+            char* p = dst + (size_t)r * pitch + 16 * c;
+            if (VEC) {
+                *reinterpret_cast<uint4*>(p) = v;
+            } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 16 / ESZ; ++e)
+                    if (16 * c + ESZ * e < bytes) {
+                        if (ESZ == 2)
+                            *reinterpret_cast<uint16_t*>(p + 2 * e) = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                        else
+                            *reinterpret_cast<uint32_t*>(p + 4 * e) = w[e];
+                    }
+            }
+        }
+    }
     __syncwarp();
 }
 
@@ -127,9 +154,9 @@ __device__ __forceinline__ float row_amax(const float (&v)[128]) {
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// The row's 128 values in 8 bits: codes staged and stored, the exponent byte to *scale.
-__device__ __forceinline__ void save_row(float (&v)[128], const CUtensorMap* map, uint32_t stage, uint8_t* scale,
-                                         int n, int m_warp, int t, int lane, bool store, bool row_ok) {
+// The row's 128 values in 8 bits to block column n of `out`.
+__device__ __forceinline__ void save_row(float (&v)[128], const Fp8View& out, const Args& a, int t, int m_warp, int n,
+                                         int rows, int lane, uint32_t stage) {
     float amax = row_amax(v);
     if (amax == __int_as_float(0x7f800000)) {          // infinities become NaN and do not count
 #pragma unroll
@@ -138,7 +165,6 @@ __device__ __forceinline__ void save_row(float (&v)[128], const CUtensorMap* map
     }
     const uint32_t E = fp8_exponent<false>(__float_as_uint(amax));
     const uint64_t s = f2_splat(fp8_inv_scale(E));
-    staging_free(lane);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
         uint32_t w[4];
@@ -152,34 +178,33 @@ __device__ __forceinline__ void save_row(float (&v)[128], const CUtensorMap* map
         }
         stage16(stage, lane, c, w[0], w[1], w[2], w[3]);
     }
-    store_staged(map, stage, n, m_warp, t, lane, store);
-    if (row_ok) *scale = (uint8_t)E;
+    const size_t row = (size_t)m_warp * a.T + t;
+    store_rows<true, 1>(stage, reinterpret_cast<char*>(out.codes) + row * (size_t)out.ld + n,
+                        (size_t)a.T * (size_t)out.ld, rows, a.N - n, lane);
+    if (lane < rows) out.scales[(row + (size_t)lane * a.T) * (size_t)out.lds + n / kFp8Block] = (uint8_t)E;
 }
 
-// Sum of v over the 32 lanes for each of 32 columns, column c in lane c.
-__device__ __forceinline__ float column_sums(const float* v, int lane) {
-    float w[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) w[i] = v[i];
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        const bool upper = (lane & o) != 0;
-#pragma unroll
-        for (int i = 0; i < o; ++i) {
-            const float send = upper ? w[i] : w[i + o], keep = upper ? w[i + o] : w[i];
-            w[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-        }
+// 128 bytes of each row of Y from column n on.
+template <typename OUT>
+__device__ __forceinline__ void save_piece(const Args& a, int t, int m_warp, int n, int rows, int lane,
+                                           uint32_t stage) {
+    if (n >= a.N) {
+        __syncwarp();
+        return;
     }
-    return w[0];
+    constexpr int E = sizeof(OUT);
+    char* dst = reinterpret_cast<char*>(a.y) + (((size_t)m_warp * a.T + t) * (size_t)a.N + n) * E;
+    const size_t pitch = (size_t)a.T * (size_t)a.N * E;
+    if (a.vec)
+        store_rows<true, E>(stage, dst, pitch, rows, (a.N - n) * E, lane);
+    else
+        store_rows<false, E>(stage, dst, pitch, rows, (a.N - n) * E, lane);
 }
 
 template <int EPI>
-__device__ __forceinline__ void epilogue(float (&v)[128], const Args& a, const CUtensorMap* m0, const CUtensorMap* m1,
-                                         const uint4 (&u8)[8], uint32_t u_byte, const Tile& tl, int m_warp, int n,
-                                         int lane, uint32_t stage) {
-    const int m = m_warp + lane;
-    const bool row_ok = m < a.B && n < a.N, store = m_warp < a.B && n < a.N;
-    const size_t row = (size_t)m * a.T + tl.t;
+__device__ __forceinline__ void epilogue(float (&v)[128], const Args& a, const Tile& tl, int m_warp, int n, int lane,
+                                         uint32_t stage) {
+    const int rows = n < a.N ? min(32, a.B - m_warp) : 0;        // this warp's rows that exist (may be negative)
     if (EPI != EPI_DGELU && a.bias) {
         const float* b = a.bias + (size_t)tl.t * a.N + n;
         if (n + 128 <= a.N && (a.N & 3) == 0) {
@@ -194,103 +219,97 @@ __device__ __forceinline__ void epilogue(float (&v)[128], const Args& a, const C
                 if (n + i < a.N) v[i] += __ldg(b + i);
         }
     }
-    if constexpr (EPI == EPI_BF16) {
-        if (a.direct) {
-            __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(a.y) + row * (size_t)a.N + n;
+    auto stage_bf16 = [&](const float* p) {
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-                if (row_ok && n + i < a.N) y[i] = __float2bfloat16_rn(v[i]);
-            return;
-        }
+        for (int c = 0; c < 8; ++c)
+            stage16(stage, lane, c, pack_bf16x2(p[8 * c], p[8 * c + 1]), pack_bf16x2(p[8 * c + 2], p[8 * c + 3]),
+                    pack_bf16x2(p[8 * c + 4], p[8 * c + 5]), pack_bf16x2(p[8 * c + 6], p[8 * c + 7]));
+    };
+    auto stage_f32 = [&](const float* p) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            stage16(stage, lane, c, __float_as_uint(p[4 * c]), __float_as_uint(p[4 * c + 1]),
+                    __float_as_uint(p[4 * c + 2]), __float_as_uint(p[4 * c + 3]));
+    };
+    if constexpr (EPI == EPI_BF16) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            staging_free(lane);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const float* p = v + 64 * h + 8 * c;
-                stage16(stage, lane, c, pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]),
-                        pack_bf16x2(p[6], p[7]));
-            }
-            store_staged(m0, stage, n + 64 * h, m_warp, tl.t, lane, store && n + 64 * h < a.N);
+            stage_bf16(v + 64 * h);
+            save_piece<__nv_bfloat16>(a, tl.t, m_warp, n + 64 * h, rows, lane, stage);
         }
     } else if constexpr (EPI == EPI_F32) {
-        if (a.direct) {
-            float* y = reinterpret_cast<float*>(a.y) + row * (size_t)a.N + n;
-#pragma unroll
-            for (int i = 0; i < 128; ++i)
-                if (row_ok && n + i < a.N) y[i] = v[i];
-            return;
-        }
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            staging_free(lane);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const float* p = v + 32 * h + 4 * c;
-                stage16(stage, lane, c, __float_as_uint(p[0]), __float_as_uint(p[1]), __float_as_uint(p[2]),
-                        __float_as_uint(p[3]));
-            }
-            store_staged(m0, stage, n + 32 * h, m_warp, tl.t, lane, store && n + 32 * h < a.N);
+            stage_f32(v + 32 * h);
+            save_piece<float>(a, tl.t, m_warp, n + 32 * h, rows, lane, stage);
         }
     } else if constexpr (EPI == EPI_GELU || EPI == EPI_GELU_KEEP) {
-        const int blk = n / kFp8Block;
-        if constexpr (EPI == EPI_GELU_KEEP)
-            save_row(v, m1, stage, a.s1 + row * (size_t)a.s1_ld + blk, n, m_warp, tl.t, lane, store, row_ok);
+        if constexpr (EPI == EPI_GELU_KEEP) save_row(v, a.o1, a, tl.t, m_warp, n, rows, lane, stage);
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
             const uint64_t g = gelu_erf_x2(f2_pack(v[2 * i], v[2 * i + 1]), 0ull);
             f2_unpack(g, v[2 * i], v[2 * i + 1]);
         }
-        save_row(v, m0, stage, a.s0 + row * (size_t)a.s0_ld + blk, n, m_warp, tl.t, lane, store, row_ok);
+        save_row(v, a.o0, a, tl.t, m_warp, n, rows, lane, stage);
     } else {
-        const float s = fp8_scale(u_byte);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const uint32_t w[4] = {u8[c].x, u8[c].y, u8[c].z, u8[c].w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 f = fp8_unpack2<false>(w[j >> 1] >> (16 * (j & 1)));
-                uint64_t val, grad;
-                gelu_with_grad_x2(f2_pack(f.x, f.y), f2_splat(s), 0ull, val, grad);
-                float g0, g1;
-                f2_unpack(grad, g0, g1);
-                v[16 * c + 2 * j] *= g0;
-                v[16 * c + 2 * j + 1] *= g1;
-            }
-        }
-        // sums over this warp's 32 rows, for the bias gradient
-        float* part = a.colpart + ((size_t)tl.t * a.m_tiles * 8 + m_warp / 32) * a.N;
+        // sums over this warp's 32 rows, for the bias gradient: 32 columns of every row
+        // staged, then lane c adds up column c
+        float* part = a.colpart + ((size_t)tl.t * a.m_tiles * 8 + m_warp / 32) * a.N + n;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            const float cs = column_sums(v + 32 * h, lane);
-            if (n + 32 * h + lane < a.N) part[n + 32 * h + lane] = cs;
+            stage_f32(v + 32 * h);
+            __syncwarp();
+            float sum[2] = {};
+#pragma unroll
+            for (int r = 0; r < 32; ++r) {
+                float x;
+                asm volatile("ld.shared.f32 %0, [%1];"
+                             : "=f"(x)
+                             : "r"(stage + 128u * r + 16u * (uint32_t)((lane >> 2) ^ (r & 7)) + 4u * (lane & 3)));
+                sum[r & 1] += x;
+            }
+            __syncwarp();
+            if (n + 32 * h + lane < a.N) part[32 * h + lane] = sum[0] + sum[1];
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            staging_free(lane);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const float* p = v + 64 * h + 8 * c;
-                stage16(stage, lane, c, pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]),
-                        pack_bf16x2(p[6], p[7]));
-            }
-            store_staged(m1, stage, n + 64 * h, m_warp, tl.t, lane, store && n + 64 * h < a.N);
+            stage_bf16(v + 64 * h);
+            save_piece<__nv_bfloat16>(a, tl.t, m_warp, n + 64 * h, rows, lane, stage);
         }
-        save_row(v, m0, stage, a.s0 + row * (size_t)a.s0_ld + n / kFp8Block, n, m_warp, tl.t, lane, store, row_ok);
+        save_row(v, a.o0, a, tl.t, m_warp, n, rows, lane, stage);
+    }
+}
+
+// v *= Gelu'(u), u the row's 128 codes in shared memory times their scale.
+__device__ __forceinline__ void times_gelu_grad(float (&v)[128], uint32_t codes, float scale, int lane) {
+    const uint64_t s = f2_splat(scale);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const uint4 q = staged16(codes, lane, c);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 f = fp8_unpack2<false>(w[j >> 1] >> (16 * (j & 1)));
+            uint64_t val, grad;
+            gelu_with_grad_x2(f2_pack(f.x, f.y), s, 0ull, val, grad);
+            const int i = 16 * c + 2 * j;
+            f2_unpack(f2_mul(f2_pack(v[i], v[i + 1]), grad), v[i], v[i + 1]);
+        }
     }
 }
 
 template <int EPI, bool TRANS>
 __global__ void __launch_bounds__(THREADS, 1)
 fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                   const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1, const Args args) {
+                   const __grid_constant__ CUtensorMap tmU, const Args args) {
+    constexpr int STAGES = Cfg<EPI>::STAGES;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
     uint8_t* base_ptr = smem_raw + (base - raw_addr);
     const uint32_t sA = base, sB = base + STAGES * A_BYTES;
     const uint32_t sEpi = base + STAGES * STAGE_BYTES;
-    const uint32_t sSF = sEpi + EPI_WARPS * STAGING;
+    const uint32_t sU = sEpi + EPI_WARPS * STAGING, sSF = sU + Cfg<EPI>::U_BYTES;
     const uint32_t bar0 = sSF + SF_SLOTS * SF_BYTES;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
@@ -299,7 +318,8 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + x); };
     auto tempty_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 2 + x); };
     const uint32_t shared_bar = bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 4);
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (shared_bar + 8u - base));
+    auto u_bar = [&](int w) { return shared_bar + 8u + 8u * w; };
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (shared_bar + 8u + 8u * EPI_WARPS - base));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -321,6 +341,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             mbar_init(tfull_bar(x), 1);              // multicast commit
             mbar_init(tempty_bar(x), 2 * EPI_WARPS); // the even CTA's: every epilogue warp of both CTAs
         }
+        for (int w = 0; w < EPI_WARPS; ++w) mbar_init(u_bar(w), 1);
         mbar_init(shared_bar, EPI_WARPS);        // the even CTA's: the warps that own the shared columns
         *abort_flag = 0;
         fence_mbar_init();
@@ -493,23 +514,25 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
         const int quad = warp & 3, half = (warp - 4) >> 2;
         const uint32_t stage = sEpi + (uint32_t)(warp - 4) * STAGING;
         const uint32_t shared_leader = mapa_shared(shared_bar, 0);
-        uint32_t phase = 0;
+        uint32_t phase = 0, uphase = 0, u_next = 127;
         int acc = 0;
+        // DGELU: a tile's kept u is on its way while the tile before is worked on
+        const uint32_t u_codes = sU + (uint32_t)(warp - 4) * STAGING, ub = u_bar(warp - 4);
+        auto fetch_u = [&](long long i) {
+            const Tile tl = tile_of(i, args);
+            const int m = tl.m0 + BM * (int)rank + 32 * quad, n = tl.n0 + 128 * half;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(ub, STAGING);
+                tma_load_3d(&tmU, u_codes, ub, n, m, tl.t);
+            }
+            u_next = 127;
+            if (m + lane < args.B && n < args.N)
+                u_next = __ldg(args.o1.scales + ((size_t)(m + lane) * args.T + tl.t) * (size_t)args.o1.lds + n / kFp8Block);
+        };
+        if (EPI == EPI_DGELU && unit < args.tiles) fetch_u(unit);
         for (long long i = unit; i < args.tiles; i += nunits) {
             const Tile tl = tile_of(i, args);
             const int m_warp = tl.m0 + BM * (int)rank + 32 * quad, n = tl.n0 + 128 * half;
-            uint4 u8[8];
-            uint32_t u_byte = 127;
-            if constexpr (EPI == EPI_DGELU) {        // the kept u, loaded while the product runs
-                const bool here = m_warp + lane < args.B && n < args.N;
-                const size_t row = (size_t)(m_warp + lane) * args.T + tl.t;
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    u8[c] = here && n + 16 * c < args.N
-                                ? __ldg(reinterpret_cast<const uint4*>(args.u + row * (size_t)args.u_ld + n) + c)
-                                : make_uint4(0, 0, 0, 0);
-                if (here) u_byte = __ldg(args.us + row * (size_t)args.us_ld + n / kFp8Block);
-            }
             if (!wait_bounded(tfull_bar(acc), phase, abort_flag, args.err, args.timeout_ns)) break;
             tc_fence_after();
             // The whole row comes out at once, so the accumulator is free again long
@@ -546,9 +569,15 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             float v[128];
 #pragma unroll
             for (int c = 0; c < 128; ++c) v[c] = __uint_as_float(r[c >> 5][c & 31]);
-            epilogue<EPI>(v, args, &tm0, &tm1, u8, u_byte, tl, m_warp, n, lane, stage);
+            if constexpr (EPI == EPI_DGELU) {
+                if (!wait_bounded(ub, uphase, abort_flag, args.err, args.timeout_ns)) break;
+                uphase ^= 1u;
+                times_gelu_grad(v, u_codes, fp8_scale(u_next), lane);
+                __syncwarp();
+                if (i + nunits < args.tiles) fetch_u(i + nunits);
+            }
+            epilogue<EPI>(v, args, tl, m_warp, n, lane, stage);
         }
-        if (lane == 0) bulk_wait_group<0>();         // this warp's tensor stores have landed
     }
 
     tc_fence_before();
@@ -594,16 +623,17 @@ bool fp8_tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, l
 namespace f8 {
 
 template <int EPI, bool TRANS>
-cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& m0, const CUtensorMap& m1,
-                const Args& a, int num_sms, cudaStream_t s) {
+cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& mu, const Args& a, int num_sms,
+                cudaStream_t s) {
     auto k = fp8_product_kernel<EPI, TRANS>;
-    cudaError_t e = smem_attr_once((const void*)k, SMEM_BYTES);
+    constexpr int smem = Cfg<EPI>::SMEM_BYTES;
+    cudaError_t e = smem_attr_once((const void*)k, smem);
     if (e != cudaSuccess) return e;
     const long long pairs = num_sms / 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * (a.tiles < pairs ? a.tiles : pairs)));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -614,14 +644,8 @@ cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap&
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, k, mx, mw, m0, m1, a);
+    e = cudaLaunchKernelEx(&cfg, k, mx, mw, mu, a);
     return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-template <int EPI>
-cudaError_t run_either(bool trans, const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& m0,
-                       const CUtensorMap& m1, const Args& a, int num_sms, cudaStream_t s) {
-    return trans ? run<EPI, true>(mx, mw, m0, m1, a, num_sms, s) : run<EPI, false>(mx, mw, m0, m1, a, num_sms, s);
 }
 
 }  // namespace f8
@@ -646,42 +670,30 @@ cudaError_t launch_fp8_product(const Fp8Product& p, const Fp8Device& dev, cudaSt
     a.y = p.y;
     a.err = dev.err;
     a.timeout_ns = dev.timeout_ns;
-    CUtensorMap mx, mw, m0, m1;
+    a.o0 = p.o0, a.o1 = p.o1;
+    a.colpart = p.colpart;
+    a.vec = p.N % (p.epi == FP8_OUT_F32 ? 4 : 8) == 0;
+    CUtensorMap mx, mw;
     const auto u8t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     if (!fp8_tensor_map(&mx, u8t, p.x.codes, p.K, p.B, p.T, p.T * p.x.ld, p.x.ld, BK, BM) ||
         !fp8_tensor_map(&mw, u8t, p.w.codes, wc, wr, p.T, p.w.ld, (long long)wr * p.w.ld, 128, 128))
         return cudaErrorInvalidValue;
-    m0 = m1 = mx;
-    auto map8 = [&](CUtensorMap* m, const Fp8View& q) {
-        return fp8_tensor_map(m, u8t, q.codes, p.N, p.B, p.T, p.T * q.ld, q.ld, 128, 32);
-    };
-    auto map16 = [&](CUtensorMap* m, void* q) {
-        return fp8_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, p.N, p.B, p.T, 2ll * p.T * p.N, 2ll * p.N, 64, 32);
-    };
+    const int sms = dev.num_sms;
     switch (p.epi) {
         case FP8_OUT_BF16:
-            a.direct = p.N % 8 != 0;
-            if (!a.direct && !map16(&m0, p.y)) return cudaErrorInvalidValue;
-            return run_either<EPI_BF16>(p.trans, mx, mw, m0, m1, a, dev.num_sms, s);
+            return p.trans ? run<EPI_BF16, true>(mx, mw, mx, a, sms, s) : run<EPI_BF16, false>(mx, mw, mx, a, sms, s);
         case FP8_OUT_F32:
-            a.direct = p.N % 4 != 0;
-            if (!a.direct && !fp8_tensor_map(&m0, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.y, p.N, p.B, p.T,
-                                             4ll * p.T * p.N, 4ll * p.N, 32, 32))
-                return cudaErrorInvalidValue;
-            return run_either<EPI_F32>(p.trans, mx, mw, m0, m1, a, dev.num_sms, s);
+            return p.trans ? run<EPI_F32, true>(mx, mw, mx, a, sms, s) : run<EPI_F32, false>(mx, mw, mx, a, sms, s);
         case FP8_GELU:
-            if (p.trans || !map8(&m0, p.o0)) return cudaErrorInvalidValue;
-            a.s0 = p.o0.scales, a.s0_ld = p.o0.lds;
-            if (!p.o1.codes) return run<EPI_GELU, false>(mx, mw, m0, m1, a, dev.num_sms, s);
-            if (!map8(&m1, p.o1)) return cudaErrorInvalidValue;
-            a.s1 = p.o1.scales, a.s1_ld = p.o1.lds;
-            return run<EPI_GELU_KEEP, false>(mx, mw, m0, m1, a, dev.num_sms, s);
-        case FP8_DGELU:
-            if (!p.trans || !map8(&m0, p.o0) || !map16(&m1, p.y)) return cudaErrorInvalidValue;
-            a.s0 = p.o0.scales, a.s0_ld = p.o0.lds;
-            a.u = p.o1.codes, a.u_ld = p.o1.ld, a.us = p.o1.scales, a.us_ld = p.o1.lds;
-            a.colpart = p.colpart;
-            return run<EPI_DGELU, true>(mx, mw, m0, m1, a, dev.num_sms, s);
+            if (p.trans) return cudaErrorNotSupported;
+            return p.o1.codes ? run<EPI_GELU_KEEP, false>(mx, mw, mx, a, sms, s)
+                              : run<EPI_GELU, false>(mx, mw, mx, a, sms, s);
+        case FP8_DGELU: {
+            CUtensorMap mu;
+            if (!p.trans || !fp8_tensor_map(&mu, u8t, p.o1.codes, p.N, p.B, p.T, p.T * p.o1.ld, p.o1.ld, 128, 32))
+                return cudaErrorInvalidValue;
+            return run<EPI_DGELU, true>(mx, mw, mu, a, sms, s);
+        }
     }
     return cudaErrorNotSupported;
 }
