@@ -19,8 +19,11 @@
 //                four k-blocks: lane l takes rows l, l + 32, l + 64, l + 96,
 //                writes 16 bytes to shared memory, and the MMA issuer copies
 //                512 bytes per 128 rows to tensor memory (tcgen05.cp)
-//   warps 4-11   epilogue: each thread owns one row's 128 columns, which is one
-//                block of an 8-bit output: its largest value needs no exchange
+//   warps 4-19   epilogue: each thread owns 64 columns of one row; a block of an
+//                8-bit output is two threads', whose largest values meet in
+//                shared memory.  Four warps per scheduler: with two (128 columns
+//                a thread, no exchange) GELU and its rounding ran at 0.39
+//                instructions per cycle, waiting for themselves
 // Tensor memory (512 columns): two accumulators of 256 columns that share 64,
 // at columns 0 and 192, so that the next tile's product begins as soon as those
 // 64 columns have been read, and a ring of four scale slots from column 448 (4
@@ -46,24 +49,26 @@ constexpr int B_BYTES = BN / 2 * BK;     // this CTA's half of the columns
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int SF_SLOTS = 4;
 constexpr int SF_BYTES = 512 * 3;        // x: 128 rows, W: 2 x 128 columns
-constexpr int EPI_WARPS = 8;
-constexpr int STAGING = 4096;            // per epilogue warp: 32 rows of 128 bytes
+constexpr int EPI_WARPS = 16;
+constexpr int COLS = 64;                 // columns per epilogue warp
+constexpr int STAGING = 2048;            // per epilogue warp: 32 rows of 64 bytes
+constexpr int RED_BYTES = 2 * 2 * EPI_WARPS * 32 * 4;   // rows' largest values: [tile parity][output][warp][row]
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr uint32_t ACC1_COL = 192;       // the second accumulator's first column
 constexpr int SF_COL = 448;
-// registers: 384 threads launched with 168; 128 x 80 + 256 x 208 <= 384 x 168
-constexpr int REGS_OTHER = 80, REGS_EPI = 208;
+// registers: 640 threads launched with 96; 128 x 56 + 512 x 104 <= 640 x 96
+constexpr int REGS_OTHER = 56, REGS_EPI = 104;
 
 enum Epi { EPI_BF16, EPI_F32, EPI_GELU, EPI_GELU_KEEP, EPI_DGELU };
 
-// Shared memory: the stages, 4 KB of staging per epilogue warp, the scale slots;
-// for DGELU 4 KB more per epilogue warp for the next tile's kept u, and a stage less.
+// Shared memory: the stages, 2 KB of staging per epilogue warp, the scale slots;
+// for DGELU 2 KB more per epilogue warp for the next tile's kept u, and a stage less.
 template <int EPI>
 struct Cfg {
     static constexpr int STAGES = EPI == EPI_DGELU ? 4 : 5;
     static constexpr int U_BYTES = EPI == EPI_DGELU ? EPI_WARPS * STAGING : 0;
     static constexpr int SMEM_BYTES =
-        1024 + STAGES * STAGE_BYTES + EPI_WARPS * STAGING + U_BYTES + SF_SLOTS * SF_BYTES + 256;
+        1024 + STAGES * STAGE_BYTES + EPI_WARPS * STAGING + U_BYTES + SF_SLOTS * SF_BYTES + RED_BYTES + 512;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 
@@ -101,31 +106,30 @@ __device__ __forceinline__ Tile tile_of(long long i, const Args& a) {
     return r;
 }
 
-// One row's 128 bytes into this warp's staging, 16 bytes at a time: piece c of
-// row r at c ^ (r % 8), which keeps rows and pieces free of bank conflicts.
-__device__ __forceinline__ void stage16(uint32_t stage, int lane, int c, uint32_t w0, uint32_t w1, uint32_t w2,
-                                        uint32_t w3) {
-    st_shared_v4(stage + 128u * lane + 16u * (uint32_t)(c ^ (lane & 7)), w0, w1, w2, w3);
+// One row's 64 bytes into this warp's staging, 16 bytes at a time: piece c of row
+// r at c ^ (r / 2 % 4), which keeps rows and pieces free of bank conflicts.
+__device__ __forceinline__ uint32_t staged_at(uint32_t stage, int row, int c) {
+    return stage + 64u * row + 16u * (uint32_t)(c ^ ((row >> 1) & 3));
 }
 __device__ __forceinline__ uint4 staged16(uint32_t stage, int row, int c) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(stage + 128u * row + 16u * (uint32_t)(c ^ (row & 7))));
+                 : "r"(staged_at(stage, row, c)));
     return v;
 }
 
 // The staged 32 rows to memory: row r at dst + r pitch, the first `rows` of them,
 // of each the first `bytes` (whole 16-byte pieces when VEC, else elements of ESZ
-// bytes).  Eight lanes write a row's 128 bytes.  Plain stores: the staging is
-// free again after a warp barrier, where a bulk copy's reads would be waited for.
+// bytes).  Four lanes write a row's 64 bytes.  Plain stores: the staging is free
+// again after a warp barrier, where a bulk copy's reads would be waited for.
 template <bool VEC, int ESZ>
 __device__ __forceinline__ void store_rows(uint32_t stage, char* dst, size_t pitch, int rows, int bytes, int lane) {
     __syncwarp();
-    const int c = lane & 7;
+    const int c = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3);
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
         if (r < rows && 16 * c < bytes) {
             const uint4 v = staged16(stage, r, c);
             char* p = dst + (size_t)r * pitch + 16 * c;
@@ -147,26 +151,48 @@ __device__ __forceinline__ void store_rows(uint32_t stage, char* dst, size_t pit
     __syncwarp();
 }
 
-__device__ __forceinline__ float row_amax(const float (&v)[128]) {
+// Where the two warps of a block meet: this warp's and the partner's rows of the
+// exchange (written once per tile and output, and read before the partner can
+// write them again two tiles later) and a barrier of two arrivals, bounded as all.
+struct Partner {
+    volatile float* mine;
+    const volatile float* theirs;
+    uint32_t bar, phase;
+    volatile int* abort;
+};
+
+// Largest magnitude of the row's block, this thread's half and its partner's;
+// passes over NaN.  False when the wait ran out.
+__device__ __forceinline__ float half_amax(const float (&v)[COLS]) {
     float m[4] = {};
 #pragma unroll
-    for (int i = 0; i < 128; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(v[i]));    // passes over NaN
+    for (int i = 0; i < COLS; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(v[i]));
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
-
-// The row's 128 values in 8 bits to block column n of `out`.
-__device__ __forceinline__ void save_row(float (&v)[128], const Fp8View& out, const Args& a, int t, int m_warp, int n,
-                                         int rows, int lane, uint32_t stage) {
-    float amax = row_amax(v);
-    if (amax == __int_as_float(0x7f800000)) {          // infinities become NaN and do not count
+__device__ __forceinline__ bool block_amax(float (&v)[COLS], Partner& p, int which, const Args& a, int lane, float& amax) {
+    float m = half_amax(v);
+    if (m == __int_as_float(0x7f800000)) {             // infinities become NaN and do not count
 #pragma unroll
-        for (int i = 0; i < 128; ++i) v[i] = fp8_poison(v[i]);
-        amax = row_amax(v);
+        for (int i = 0; i < COLS; ++i) v[i] = fp8_poison(v[i]);
+        m = half_amax(v);
     }
+    p.mine[which * EPI_WARPS * 32 + lane] = m;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(p.bar);
+    if (!wait_bounded(p.bar, p.phase, p.abort, a.err, a.timeout_ns)) return false;
+    p.phase ^= 1u;
+    amax = fmaxf(m, p.theirs[which * EPI_WARPS * 32 + lane]);
+    return true;
+}
+
+// The row's 64 values in 8 bits to columns n on of `out`; the warp with a block's
+// first half also writes its exponent bytes.
+__device__ __forceinline__ void save_row(const float (&v)[COLS], float amax, const Fp8View& out, const Args& a, int t,
+                                         int m_warp, int n, int rows, int lane, uint32_t stage) {
     const uint32_t E = fp8_exponent<false>(__float_as_uint(amax));
     const uint64_t s = f2_splat(fp8_inv_scale(E));
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < COLS / 16; ++c) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -176,23 +202,30 @@ __device__ __forceinline__ void save_row(float (&v)[128], const Fp8View& out, co
             f2_unpack(f2_mul(f2_pack(v[i + 2], v[i + 3]), s), q[2], q[3]);
             w[j] = fp8_pack4<false>(q[0], q[1], q[2], q[3]);
         }
-        stage16(stage, lane, c, w[0], w[1], w[2], w[3]);
+        st_shared_v4(staged_at(stage, lane, c), w[0], w[1], w[2], w[3]);
     }
     const size_t row = (size_t)m_warp * a.T + t;
     store_rows<true, 1>(stage, reinterpret_cast<char*>(out.codes) + row * (size_t)out.ld + n,
                         (size_t)a.T * (size_t)out.ld, rows, a.N - n, lane);
-    if (lane < rows) out.scales[(row + (size_t)lane * a.T) * (size_t)out.lds + n / kFp8Block] = (uint8_t)E;
+    if (n % kFp8Block == 0 && lane < rows)
+        out.scales[(row + (size_t)lane * a.T) * (size_t)out.lds + n / kFp8Block] = (uint8_t)E;
 }
 
-// 128 bytes of each row of Y from column n on.
+// 64 bytes of each row of Y from column n on.
 template <typename OUT>
-__device__ __forceinline__ void save_piece(const Args& a, int t, int m_warp, int n, int rows, int lane,
+__device__ __forceinline__ void save_piece(const float* v, const Args& a, int t, int m_warp, int n, int rows, int lane,
                                            uint32_t stage) {
-    if (n >= a.N) {
-        __syncwarp();
-        return;
-    }
     constexpr int E = sizeof(OUT);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if constexpr (E == 2)
+            st_shared_v4(staged_at(stage, lane, c), pack_bf16x2(v[8 * c], v[8 * c + 1]),
+                         pack_bf16x2(v[8 * c + 2], v[8 * c + 3]), pack_bf16x2(v[8 * c + 4], v[8 * c + 5]),
+                         pack_bf16x2(v[8 * c + 6], v[8 * c + 7]));
+        else
+            st_shared_v4(staged_at(stage, lane, c), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                         __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+    }
     char* dst = reinterpret_cast<char*>(a.y) + (((size_t)m_warp * a.T + t) * (size_t)a.N + n) * E;
     const size_t pitch = (size_t)a.T * (size_t)a.N * E;
     if (a.vec)
@@ -202,89 +235,85 @@ __device__ __forceinline__ void save_piece(const Args& a, int t, int m_warp, int
 }
 
 template <int EPI>
-__device__ __forceinline__ void epilogue(float (&v)[128], const Args& a, const Tile& tl, int m_warp, int n, int lane,
-                                         uint32_t stage) {
+__device__ __forceinline__ bool epilogue(float (&v)[COLS], const Args& a, const Tile& tl, int m_warp, int n, int lane,
+                                         uint32_t stage, Partner& partner) {
     const int rows = n < a.N ? min(32, a.B - m_warp) : 0;        // this warp's rows that exist (may be negative)
     if (EPI != EPI_DGELU && a.bias) {
         const float* b = a.bias + (size_t)tl.t * a.N + n;
-        if (n + 128 <= a.N && (a.N & 3) == 0) {
+        if (n + COLS <= a.N && (a.N & 3) == 0) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < COLS / 4; ++i) {
                 const float4 q = __ldg(reinterpret_cast<const float4*>(b) + i);
                 v[4 * i] += q.x, v[4 * i + 1] += q.y, v[4 * i + 2] += q.z, v[4 * i + 3] += q.w;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
+            for (int i = 0; i < COLS; ++i)
                 if (n + i < a.N) v[i] += __ldg(b + i);
         }
     }
-    auto stage_bf16 = [&](const float* p) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            stage16(stage, lane, c, pack_bf16x2(p[8 * c], p[8 * c + 1]), pack_bf16x2(p[8 * c + 2], p[8 * c + 3]),
-                    pack_bf16x2(p[8 * c + 4], p[8 * c + 5]), pack_bf16x2(p[8 * c + 6], p[8 * c + 7]));
-    };
-    auto stage_f32 = [&](const float* p) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            stage16(stage, lane, c, __float_as_uint(p[4 * c]), __float_as_uint(p[4 * c + 1]),
-                    __float_as_uint(p[4 * c + 2]), __float_as_uint(p[4 * c + 3]));
-    };
     if constexpr (EPI == EPI_BF16) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            stage_bf16(v + 64 * h);
-            save_piece<__nv_bfloat16>(a, tl.t, m_warp, n + 64 * h, rows, lane, stage);
-        }
+        for (int h = 0; h < 2; ++h)
+            save_piece<__nv_bfloat16>(v + 32 * h, a, tl.t, m_warp, n + 32 * h, rows, lane, stage);
     } else if constexpr (EPI == EPI_F32) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            stage_f32(v + 32 * h);
-            save_piece<float>(a, tl.t, m_warp, n + 32 * h, rows, lane, stage);
-        }
+        for (int h = 0; h < 4; ++h) save_piece<float>(v + 16 * h, a, tl.t, m_warp, n + 16 * h, rows, lane, stage);
     } else if constexpr (EPI == EPI_GELU || EPI == EPI_GELU_KEEP) {
-        if constexpr (EPI == EPI_GELU_KEEP) save_row(v, a.o1, a, tl.t, m_warp, n, rows, lane, stage);
+        if constexpr (EPI == EPI_GELU_KEEP) {
+            float m;
+            if (!block_amax(v, partner, 1, a, lane, m)) return false;
+            save_row(v, m, a.o1, a, tl.t, m_warp, n, rows, lane, stage);
+        }
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
+        for (int i = 0; i < COLS / 2; ++i) {
             const uint64_t g = gelu_erf_x2(f2_pack(v[2 * i], v[2 * i + 1]), 0ull);
             f2_unpack(g, v[2 * i], v[2 * i + 1]);
         }
-        save_row(v, a.o0, a, tl.t, m_warp, n, rows, lane, stage);
+        float m;
+        if (!block_amax(v, partner, 0, a, lane, m)) return false;
+        save_row(v, m, a.o0, a, tl.t, m_warp, n, rows, lane, stage);
     } else {
-        // sums over this warp's 32 rows, for the bias gradient: 32 columns of every row
-        // staged, then lane c adds up column c
+        // sums over this warp's 32 rows, for the bias gradient: 16 columns of every row
+        // staged, then lane c (and c + 16) adds up column c of 16 rows
         float* part = a.colpart + ((size_t)tl.t * a.m_tiles * 8 + m_warp / 32) * a.N + n;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            stage_f32(v + 32 * h);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                st_shared_v4(staged_at(stage, lane, c), __float_as_uint(v[16 * h + 4 * c]),
+                             __float_as_uint(v[16 * h + 4 * c + 1]), __float_as_uint(v[16 * h + 4 * c + 2]),
+                             __float_as_uint(v[16 * h + 4 * c + 3]));
             __syncwarp();
             float sum[2] = {};
 #pragma unroll
-            for (int r = 0; r < 32; ++r) {
+            for (int r = 0; r < 16; ++r) {
                 float x;
                 asm volatile("ld.shared.f32 %0, [%1];"
                              : "=f"(x)
-                             : "r"(stage + 128u * r + 16u * (uint32_t)((lane >> 2) ^ (r & 7)) + 4u * (lane & 3)));
+                             : "r"(staged_at(stage, 2 * r + (lane >> 4), (lane >> 2) & 3) + 4u * (lane & 3)));
                 sum[r & 1] += x;
             }
             __syncwarp();
-            if (n + 32 * h + lane < a.N) part[32 * h + lane] = sum[0] + sum[1];
+            float cs = sum[0] + sum[1];
+            cs += __shfl_xor_sync(0xffffffffu, cs, 16);
+            if (lane < 16 && n + 16 * h + lane < a.N) part[16 * h + lane] = cs;
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            stage_bf16(v + 64 * h);
-            save_piece<__nv_bfloat16>(a, tl.t, m_warp, n + 64 * h, rows, lane, stage);
-        }
-        save_row(v, a.o0, a, tl.t, m_warp, n, rows, lane, stage);
+        for (int h = 0; h < 2; ++h)
+            save_piece<__nv_bfloat16>(v + 32 * h, a, tl.t, m_warp, n + 32 * h, rows, lane, stage);
+        float m;
+        if (!block_amax(v, partner, 0, a, lane, m)) return false;
+        save_row(v, m, a.o0, a, tl.t, m_warp, n, rows, lane, stage);
     }
+    return true;
 }
 
-// v *= Gelu'(u), u the row's 128 codes in shared memory times their scale.
-__device__ __forceinline__ void times_gelu_grad(float (&v)[128], uint32_t codes, float scale, int lane) {
+// v *= Gelu'(u), u the row's 64 codes in shared memory times their scale.
+__device__ __forceinline__ void times_gelu_grad(float (&v)[COLS], uint32_t codes, float scale, int lane) {
     const uint64_t s = f2_splat(scale);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < COLS / 16; ++c) {
         const uint4 q = staged16(codes, lane, c);
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -310,7 +339,8 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     const uint32_t sA = base, sB = base + STAGES * A_BYTES;
     const uint32_t sEpi = base + STAGES * STAGE_BYTES;
     const uint32_t sU = sEpi + EPI_WARPS * STAGING, sSF = sU + Cfg<EPI>::U_BYTES;
-    const uint32_t bar0 = sSF + SF_SLOTS * SF_BYTES;
+    float* red = reinterpret_cast<float*>(base_ptr + (sSF - base) + SF_SLOTS * SF_BYTES);
+    const uint32_t bar0 = sSF + SF_SLOTS * SF_BYTES + RED_BYTES;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
     auto sfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
@@ -319,7 +349,8 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     auto tempty_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 2 + x); };
     const uint32_t shared_bar = bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 4);
     auto u_bar = [&](int w) { return shared_bar + 8u + 8u * w; };
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (shared_bar + 8u + 8u * EPI_WARPS - base));
+    auto pair_bar = [&](int w) { return shared_bar + 8u + 8u * (EPI_WARPS + w); };
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (pair_bar(EPI_WARPS / 2) - base));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -342,7 +373,8 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             mbar_init(tempty_bar(x), 2 * EPI_WARPS); // the even CTA's: every epilogue warp of both CTAs
         }
         for (int w = 0; w < EPI_WARPS; ++w) mbar_init(u_bar(w), 1);
-        mbar_init(shared_bar, EPI_WARPS);        // the even CTA's: the warps that own the shared columns
+        for (int w = 0; w < EPI_WARPS / 2; ++w) mbar_init(pair_bar(w), 2);
+        mbar_init(shared_bar, 2 * EPI_WARPS / 4);    // the even CTA's: the warps that own the shared columns
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -511,16 +543,17 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     } else {
         // ------------------------------ epilogue --------------------------------------
         regs_inc<REGS_EPI>();
-        const int quad = warp & 3, half = (warp - 4) >> 2;
+        const int quad = warp & 3, part = (warp - 4) >> 2;       // 32 rows, 64 columns
         const uint32_t stage = sEpi + (uint32_t)(warp - 4) * STAGING;
         const uint32_t shared_leader = mapa_shared(shared_bar, 0);
+        Partner partner{nullptr, nullptr, pair_bar(4 * (part >> 1) + quad), 0, abort_flag};
         uint32_t phase = 0, uphase = 0, u_next = 127;
         int acc = 0;
         // DGELU: a tile's kept u is on its way while the tile before is worked on
         const uint32_t u_codes = sU + (uint32_t)(warp - 4) * STAGING, ub = u_bar(warp - 4);
         auto fetch_u = [&](long long i) {
             const Tile tl = tile_of(i, args);
-            const int m = tl.m0 + BM * (int)rank + 32 * quad, n = tl.n0 + 128 * half;
+            const int m = tl.m0 + BM * (int)rank + 32 * quad, n = tl.n0 + COLS * part;
             if (lane == 0) {
                 mbar_arrive_expect_tx(ub, STAGING);
                 tma_load_3d(&tmU, u_codes, ub, n, m, tl.t);
@@ -532,43 +565,27 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
         if (EPI == EPI_DGELU && unit < args.tiles) fetch_u(unit);
         for (long long i = unit; i < args.tiles; i += nunits) {
             const Tile tl = tile_of(i, args);
-            const int m_warp = tl.m0 + BM * (int)rank + 32 * quad, n = tl.n0 + 128 * half;
+            const int m_warp = tl.m0 + BM * (int)rank + 32 * quad, n = tl.n0 + COLS * part;
             if (!wait_bounded(tfull_bar(acc), phase, abort_flag, args.err, args.timeout_ns)) break;
             tc_fence_after();
-            // The whole row comes out at once, so the accumulator is free again long
-            // before the epilogue is done; first of all the 64 columns that the other
-            // accumulator shares (the last of accumulator 0, the first of 1).
-            uint32_t r[4][32];
+            // A thread's columns come out at once, so the accumulator is free again long
+            // before the epilogue is done; the 64 columns that the other accumulator
+            // shares are the last of accumulator 0 and the first of 1.
+            uint32_t r[2][32];
             const uint32_t tcol =
-                tmem_base + ((uint32_t)(32 * quad) << 16) + (acc ? ACC1_COL : 0u) + 128u * half;
-            auto load_half = [&](int h) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) tmem_ld32_nowait(tcol + 64u * h + 32u * c, r[2 * h + c]);
-            };
-            auto shared_out = [&]() {
-                tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(shared_leader);
-            };
-            if (half == 1) {
-                load_half(1);
-                if (acc == 0) shared_out();
-                load_half(0);
-            } else {
-                load_half(0);
-                if (acc == 1) shared_out();
-                load_half(1);
-            }
+                tmem_base + ((uint32_t)(32 * quad) << 16) + (acc ? ACC1_COL : 0u) + (uint32_t)(COLS * part);
+            tmem_ld32_nowait(tcol, r[0]);
+            tmem_ld32_nowait(tcol + 32u, r[1]);
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(acc), 0));
-            acc ^= 1;
-            if (acc == 0) phase ^= 1u;
-            float v[128];
+            if (lane == 0) {
+                if (part == (acc ? 0 : 3)) mbar_arrive_pair(shared_leader);
+                mbar_arrive_pair(mapa_shared(tempty_bar(acc), 0));
+            }
+            float v[COLS];
 #pragma unroll
-            for (int c = 0; c < 128; ++c) v[c] = __uint_as_float(r[c >> 5][c & 31]);
+            for (int c = 0; c < COLS; ++c) v[c] = __uint_as_float(r[c >> 5][c & 31]);
             if constexpr (EPI == EPI_DGELU) {
                 if (!wait_bounded(ub, uphase, abort_flag, args.err, args.timeout_ns)) break;
                 uphase ^= 1u;
@@ -576,7 +593,11 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                 __syncwarp();
                 if (i + nunits < args.tiles) fetch_u(i + nunits);
             }
-            epilogue<EPI>(v, args, tl, m_warp, n, lane, stage);
+            partner.mine = red + (acc * 2 * EPI_WARPS + (warp - 4)) * 32;
+            partner.theirs = partner.mine + ((part & 1) ? -128 : 128);
+            if (!epilogue<EPI>(v, args, tl, m_warp, n, lane, stage, partner)) break;
+            acc ^= 1;
+            if (acc == 0) phase ^= 1u;
         }
     }
 
@@ -616,7 +637,9 @@ bool fp8_tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, l
     cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1u};
     cuuint32_t estr[3] = {1, 1, 1};
     return f8::g_encode(m, type, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        box_inner == 64 && type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                                                 : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -690,7 +713,7 @@ cudaError_t launch_fp8_product(const Fp8Product& p, const Fp8Device& dev, cudaSt
                               : run<EPI_GELU, false>(mx, mw, mx, a, sms, s);
         case FP8_DGELU: {
             CUtensorMap mu;
-            if (!p.trans || !fp8_tensor_map(&mu, u8t, p.o1.codes, p.N, p.B, p.T, p.T * p.o1.ld, p.o1.ld, 128, 32))
+            if (!p.trans || !fp8_tensor_map(&mu, u8t, p.o1.codes, p.N, p.B, p.T, p.T * p.o1.ld, p.o1.ld, COLS, 32))
                 return cudaErrorInvalidValue;
             return run<EPI_DGELU, true>(mx, mw, mu, a, sms, s);
         }

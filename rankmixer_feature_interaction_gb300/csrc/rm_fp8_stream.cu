@@ -84,7 +84,8 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     auto sempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + SF_SLOTS + s); };
     auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + x); };
     auto tempty_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 2 + x); };
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + 8 * (2 * STAGES + 2 * SF_SLOTS + 4));
+    const uint32_t meet_bar = bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 4);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (meet_bar + 8u - base));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -103,6 +104,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             mbar_init(tfull_bar(x), 1);
             mbar_init(tempty_bar(x), EPI_WARPS);
         }
+        mbar_init(meet_bar, EPI_WARPS);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -253,7 +255,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         // ------------------------------ epilogue ----------------------------------
         const int quad = warp & 3, tid = 32 * quad + lane;
         int acc = 0;
-        uint32_t acc_phase = 0;
+        uint32_t acc_phase = 0, meet = 0;
         for (int i = blockIdx.x; i < args.tiles; i += gridDim.x) {
             const int t = i / args.n_tiles, n0 = (i - t * args.n_tiles) * BM, n = n0 + tid;
             const float bias = args.bias && n < args.N ? __ldg(args.bias + (size_t)t * args.N + n) : 0.f;
@@ -303,7 +305,10 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                         if (lane == 0) m_u[quad * NB + j] = mu;
                     }
                 }
-                asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(meet_bar);
+                if (!wait_bounded(meet_bar, meet, abort_flag, args.err, args.timeout_ns)) break;
+                meet ^= 1u;
                 auto exponent = [&](const uint32_t* m, int j) {
                     return fp8_exponent<false>(max(max(m[j], m[NB + j]), max(m[2 * NB + j], m[3 * NB + j])));
                 };

@@ -8,8 +8,8 @@
 namespace rm {
 
 // 3-D tensor map {inner, rows, groups} with boxes of box_inner x box_rows
-// elements (128 bytes wide) and the 128-byte swizzle; what lies outside reads
-// as zero and is not written.
+// elements (128 bytes wide with the 128-byte swizzle, or 64 bytes of codes with
+// the 64-byte one); what lies outside reads as zero and is not written.
 bool fp8_tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, long long inner, long long rows,
                     long long groups, long long row_bytes, long long group_bytes, int box_inner, int box_rows);
 
