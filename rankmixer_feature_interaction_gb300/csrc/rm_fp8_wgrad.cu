@@ -96,33 +96,34 @@ __device__ __forceinline__ uint32_t spread2(uint32_t w, uint32_t selector) {
 }
 
 // 16 codes to 16 bf16 of code * 2^(E - 127): exact where bf16 is normal, else
-// rounded once.
-__device__ __forceinline__ void restore16(const uint4& q, uint32_t E, uint32_t (&o)[8]) {
+// rounded once.  restore16 is for blocks up to 57344 (E <= 134: 2^120 2^(E - 127)
+// is a bf16) without NaN codes; restore16_any takes the rest.
+__device__ __forceinline__ bool plain16(const uint4& q, uint32_t E) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        o[2 * i] = spread2(w[i], 0x9180u);
-        o[2 * i + 1] = spread2(w[i], 0xb3a2u);
-    }
-    if (E <= 134u) {                                   // 2^120 2^(E - 127) is a bf16
-        const uint32_t h = (E + 120u) << 7, s = h | (h << 16);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], s);
-    } else {                                           // blocks above 57344: in two steps, the first exact
-        const uint32_t h = E == 255u ? 0x7fc0u : E << 7, s = h | (h << 16);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(mul_bf16x2(o[i], 0x7b807b80u), s);
-    }
     uint32_t nan = 0;                                  // codes of magnitude 0x7f
 #pragma unroll
-    for (int i = 0; i < 4; ++i) nan |= ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-    if (nan) {
+    for (int i = 0; i < 4; ++i) nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
+    return E <= 134u && (nan & 0x80808080u) == 0u;
+}
+__device__ __forceinline__ void restore16(const uint4& q, uint32_t E, uint32_t (&o)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const uint32_t h = (E + 120u) << 7, s = h | (h << 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t m = ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-            o[2 * i] |= (m & 0x80u ? 0x7fffu : 0u) | (m & 0x8000u ? 0x7fff0000u : 0u);
-            o[2 * i + 1] |= (m & 0x800000u ? 0x7fffu : 0u) | (m & 0x80000000u ? 0x7fff0000u : 0u);
-        }
+    for (int i = 0; i < 4; ++i) {
+        o[2 * i] = mul_bf16x2(spread2(w[i], 0x9180u), s);
+        o[2 * i + 1] = mul_bf16x2(spread2(w[i], 0xb3a2u), s);
+    }
+}
+__device__ __noinline__ void restore16_any(const uint4& q, uint32_t E, uint32_t (&o)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const uint32_t h = E == 255u ? 0x7fc0u : E == 0u ? 0x0040u : E << 7, s = h | (h << 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {                      // in two steps, the first exact
+        o[2 * i] = mul_bf16x2(mul_bf16x2(spread2(w[i], 0x9180u), 0x7b807b80u), s);
+        o[2 * i + 1] = mul_bf16x2(mul_bf16x2(spread2(w[i], 0xb3a2u), 0x7b807b80u), s);
+        const uint32_t m = ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+        o[2 * i] |= (m & 0x80u ? 0x7fffu : 0u) | (m & 0x8000u ? 0x7fff0000u : 0u);
+        o[2 * i + 1] |= (m & 0x800000u ? 0x7fffu : 0u) | (m & 0x80000000u ? 0x7fff0000u : 0u);
     }
 }
 
@@ -347,13 +348,39 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 }
                 const uint32_t src = sRaw + slot * RAW_BYTES, exps = sExp + BK * slot;
                 const uint32_t dst = sA + stage * A_BYTES + (c >> 2) * BOX_BYTES;
+                // all chunks are loaded first and restored without a branch between them
+                constexpr int CH = BK / CONV_GROUP / 4;
+                uint4 q[CH];
+                uint32_t E[CH];
+                bool plain = true;
 #pragma unroll
-                for (uint32_t j = 0; j < BK / CONV_GROUP / 4; ++j) {
+                for (int j = 0; j < CH; ++j) {
                     const uint32_t x7 = (rep0 | ((j & 1u) << 1)) ^ flip, r = BK / CONV_GROUP * cw + 8u * (j >> 1) + x7;
-                    uint32_t o[8];
-                    restore16(ld_shared_u4(src + 128u * r + 16u * (c ^ x7)), ld_shared_u8(exps + r), o);
+                    q[j] = ld_shared_u4(src + 128u * r + 16u * (c ^ x7));
+                    E[j] = ld_shared_u8(exps + r);
+                }
+#pragma unroll
+                for (int j = 0; j < CH; ++j) plain = plain && plain16(q[j], E[j]);
+                auto put = [&](int j, const uint32_t (&o)[8]) {
+                    const uint32_t x7 = (rep0 | ((j & 1u) << 1)) ^ flip, r = BK / CONV_GROUP * cw + 8u * (j >> 1) + x7;
                     st_shared_v4(dst + 128u * r + 16u * (p ^ x7), o[0], o[1], o[2], o[3]);
                     st_shared_v4(dst + 128u * r + 16u * ((p + 1u) ^ x7), o[4], o[5], o[6], o[7]);
+                };
+                if (plain) {
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) {
+                        uint32_t o[8];
+                        restore16(q[j], E[j], o);
+                        put(j, o);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int j = 0; j < CH; ++j) {
+                        uint32_t o[8];
+                        const uint32_t x7 = (rep0 | ((j & 1u) << 1)) ^ flip, r = BK / CONV_GROUP * cw + 8u * (j >> 1) + x7;
+                        restore16_any(ld_shared_u4(src + 128u * r + 16u * (c ^ x7)), ld_shared_u8(exps + r), o);
+                        put(j, o);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
