@@ -527,9 +527,9 @@ RM_API rm_status rm_fp8_matmul(const rm_fp8_tensor *x, const rm_fp8_tensor *W, c
 /* Gradients of a per-token linear layer from its input kept in 8 bits:
  *   dW[t][k][n] = sum_b x[b][t][k] dY[b][t][n],  db[t][n] = sum_b dY[b][t][n].
  * x: [B][T][K], e4m3; dY: device bf16 [B][T][N], contiguous, N a multiple of 8
- * (RM_ERR_UNSUPPORTED otherwise); dW [T][K][N] and db [T][N] (either may be
- * NULL): device, of dtype, overwritten.  Sums in float32, in an order that
- * depends on the sizes alone. */
+ * (RM_ERR_UNSUPPORTED otherwise); dW [T][K][N] and db [T][N] (nullable):
+ * device, of dtype, overwritten.  Sums in float32, in an order that depends on
+ * the sizes alone. */
 RM_API rm_status rm_fp8_wgrad(const rm_fp8_tensor *x, const void *dY, void *dW, void *db, rm_dtype dtype, int B, int T,
                               int K, int N, void *stream);
 

@@ -28,10 +28,6 @@ cudaError_t launch_fp8_quantize_weight(bool f32, const void* W, int T, int K, in
 cudaError_t launch_fp8_dequantize(const Fp8View& in, long long rows, int cols, void* Y, bool f32, long long ldy,
                                   cudaStream_t s);
 
-// out[t][n] = sum over b of Y[b][t][n] (bf16, [B][T][N], N a multiple of 8), of
-// float or bf16, in a fixed order.
-cudaError_t launch_fp8_colsum(const void* Y, void* out, bool out_f32, int B, int T, int N, cudaStream_t s);
-
 // What the tensor-core kernels need of the current device: its SM count, the
 // error word that bounded waits latch and their bound.
 struct Fp8Device {
@@ -43,8 +39,7 @@ struct Fp8Device {
 // acc[b][t][n] = sum_k x[b][t][k] W[t][k][n] (trans: W[t][n][k]), then
 //   FP8_OUT_*:  y = acc + bias (bias nullable)
 //   FP8_GELU:   u = acc + bias; o0 = Q(Gelu(u)) and, where o1.codes is not null, o1 = Q(u)
-//   FP8_DGELU:  dU = acc Gelu'(u) with u read from o1; o0 = Q(dU), y = dU in bf16, and its
-//               sums over 32 rows in colpart [T][fp8_colpart_rows(B)][N]
+//   FP8_DGELU:  dU = acc Gelu'(u) with u read from o1; o0 = Q(dU), y = dU in bf16
 enum Fp8Epilogue { FP8_OUT_BF16, FP8_OUT_F32, FP8_GELU, FP8_DGELU };
 struct Fp8Product {
     Fp8Epilogue epi;
@@ -53,7 +48,6 @@ struct Fp8Product {
     const float* bias;
     void* y;
     Fp8View o0, o1;
-    float* colpart;
     int B, T, K, N;
     bool follows = false;       // launched right after another kernel of the same call (which waited for its
                                 // own predecessor before this one could start): W is in memory already
@@ -62,14 +56,11 @@ struct Fp8Product {
 constexpr int kFp8StreamMaxB = 64;
 bool fp8_streams(const Fp8Product& p);
 cudaError_t launch_fp8_stream(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s);
-int fp8_colpart_rows(int B);
 cudaError_t launch_fp8_product(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s);
 
-// out[t][n] = sum over r < R of part[t][r][n], of float or bf16, in a fixed order.
-cudaError_t launch_fp8_sum_parts(const float* part, void* out, bool out_f32, int R, int T, int N, cudaStream_t s);
-
-// dW[t][k][n] = sum_b x[b][t][k] dY[b][t][n], dY bf16 [B][T][N].
-cudaError_t launch_fp8_wgrad(const Fp8View& x, const void* dY, void* dW, bool w_f32, int B, int T, int K, int N,
+// dW[t][k][n] = sum_b x[b][t][k] dY[b][t][n] and, where db is not null, db[t][n] =
+// sum_b dY[b][t][n], both float or both bf16; dY bf16 [B][T][N].
+cudaError_t launch_fp8_wgrad(const Fp8View& x, const void* dY, void* dW, void* db, bool f32, int B, int T, int K, int N,
                              const Fp8Device& dev, cudaStream_t s);
 
 }  // namespace rm

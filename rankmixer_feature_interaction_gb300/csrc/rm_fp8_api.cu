@@ -151,7 +151,6 @@ ForwardWork forward_work(const rm_fp8_pffn* p, int B, const rm_fp8_kept* keep, b
 struct BackwardWork {
     rm_fp8_tensor dv, du;
     void *dv16, *du16;
-    float* colpart;
     long long bytes;
 };
 BackwardWork backward_work(const rm_fp8_pffn* p, int B, void* base) {
@@ -162,7 +161,6 @@ BackwardWork backward_work(const rm_fp8_pffn* p, int B, void* base) {
     w.du = c.tensor(rows, p->F);
     w.dv16 = c.take(rows * p->D * 2);
     w.du16 = c.take(rows * p->F * 2);
-    w.colpart = (float*)c.take((long long)p->T * fp8_colpart_rows(B) * p->F * 4);
     w.bytes = c.used;
     return w;
 }
@@ -242,19 +240,17 @@ rm_status rm_fp8_matmul(const rm_fp8_tensor* x, const rm_fp8_tensor* W, const fl
 
 rm_status rm_fp8_wgrad(const rm_fp8_tensor* x, const void* dY, void* dW, void* db, rm_dtype dtype, int B, int T, int K,
                        int N, void* stream) {
-    if (!dY) return fail(RM_ERR_INVALID_ARG, "dY is NULL");
-    if (!dW && !db) return fail(RM_ERR_INVALID_ARG, "no output requested");
+    if (!dY || !dW) return fail(RM_ERR_INVALID_ARG, "dY / dW is NULL");
     if (!known(dtype)) return fail(RM_ERR_INVALID_ARG, "unknown dtype");
     RM_CHECK(check_sizes(B, T, K, N));
     if (N % 8 != 0) return fail(RM_ERR_UNSUPPORTED, "N (%d) must be a multiple of 8", N);
     RM_CHECK(check_tensor(x, K, "x", true));
-    if (!aligned(dY, 16) || (dW && !aligned(dW, 16)) || (db && !aligned(db, 16)))
+    if (!aligned(dY, 16) || !aligned(dW, 16) || (db && !aligned(db, 16)))
         return fail(RM_ERR_INVALID_ARG, "dY, dW and db must be 16-byte aligned");
     const cudaStream_t s = as_stream(stream);
     Fp8Device dev;
     RM_CHECK(device_info(&dev));
-    if (dW) RM_CHECK_CUDA(launch_fp8_wgrad(view(*x), dY, dW, dtype == RM_F32, B, T, K, N, dev, s), "weight gradient");
-    if (db) RM_CHECK_CUDA(launch_fp8_colsum(dY, db, dtype == RM_F32, B, T, N, s), "bias gradient");
+    RM_CHECK_CUDA(launch_fp8_wgrad(view(*x), dY, dW, db, dtype == RM_F32, B, T, K, N, dev, s), "weight gradient");
     return RM_OK;
 }
 
@@ -328,14 +324,11 @@ rm_status rm_fp8_pffn_backward(const rm_fp8_pffn* p, const void* dV, rm_dtype dv
     g.epi = FP8_DGELU;
     g.o0 = view(w.du);
     g.o1 = view(kept->u);
-    g.colpart = w.colpart;
     RM_CHECK_CUDA(launch_fp8_product(g, dev, s), "dU");
     if (dX)
         RM_CHECK_CUDA(launch_fp8_product(product(dx_dtype, w.du, p->W1, true, nullptr, dX, B, T, F, D), dev, s), "dX");
-    RM_CHECK_CUDA(launch_fp8_wgrad(view(kept->a), dv16, grads->dW2, g32, B, T, F, D, dev, s), "dW2");
-    RM_CHECK_CUDA(launch_fp8_colsum(dv16, grads->db2, g32, B, T, D, s), "db2");
-    RM_CHECK_CUDA(launch_fp8_wgrad(view(kept->x), w.du16, grads->dW1, g32, B, T, D, F, dev, s), "dW1");
-    RM_CHECK_CUDA(launch_fp8_sum_parts(w.colpart, grads->db1, g32, fp8_colpart_rows(B), T, F, s), "db1");
+    RM_CHECK_CUDA(launch_fp8_wgrad(view(kept->a), dv16, grads->dW2, grads->db2, g32, B, T, F, D, dev, s), "dW2");
+    RM_CHECK_CUDA(launch_fp8_wgrad(view(kept->x), w.du16, grads->dW1, grads->db1, g32, B, T, D, F, dev, s), "dW1");
     return RM_OK;
 }
 

@@ -1,5 +1,5 @@
-// Elementwise and reduction kernels of the 8-bit operators: saving rows and
-// weights in 8 bits, restoring rows, and column sums.
+// Elementwise kernels of the 8-bit operators: saving rows and weights in 8 bits,
+// and restoring rows.
 //
 // Saving reads every value once and writes one byte for it; 16 lanes own one
 // block of 128 values (8 each: one or two 16-byte loads), agree on its largest
@@ -210,55 +210,6 @@ dequantize_kernel(Fp8View in, unsigned long long chunks, int cols, int nch, OUT*
     }
 }
 
-// One CTA per (token, 128 columns): 16 lanes of 8 columns x 16 rows of samples.
-template <typename OUT>
-__global__ void __launch_bounds__(kThreads)
-colsum_kernel(const __nv_bfloat16* __restrict__ Y, OUT* __restrict__ out, int B, int T, int N) {
-    __shared__ float part[16][kFp8Block];
-    pdl_wait();
-    pdl_launch_next();
-    const int t = blockIdx.y, c0 = blockIdx.x * kFp8Block + 8 * (threadIdx.x & 15), r0 = threadIdx.x >> 4;
-    float acc[8] = {};
-    if (c0 < N) {
-#pragma unroll 4
-        for (int b = r0; b < B; b += 16) {
-            float v[8];
-            load8<__nv_bfloat16, true>(Y + ((size_t)b * T + t) * N + c0, 8, v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] += v[j];
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) part[r0][8 * (threadIdx.x & 15) + j] = acc[j];
-    __syncthreads();
-    const int n = blockIdx.x * kFp8Block + threadIdx.x;
-    if (threadIdx.x < kFp8Block && n < N) {
-        float s = 0.f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s += part[r][threadIdx.x];
-        out[(size_t)t * N + n] = from_f32<OUT>(s);
-    }
-}
-
-// One thread per 4 columns (N is a multiple of 4), rows in order.
-template <typename OUT>
-__global__ void __launch_bounds__(128)
-sum_parts_kernel(const float* __restrict__ part, OUT* __restrict__ out, int R, int N) {
-    pdl_wait();
-    pdl_launch_next();
-    const int t = blockIdx.y, n = 4 * (blockIdx.x * 128 + threadIdx.x);
-    if (n >= N) return;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* p = part + (size_t)t * R * N + n;
-#pragma unroll 8
-    for (int r = 0; r < R; ++r) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p + (size_t)r * N));
-        a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-    }
-    OUT* o = out + (size_t)t * N + n;
-    o[0] = from_f32<OUT>(a.x), o[1] = from_f32<OUT>(a.y), o[2] = from_f32<OUT>(a.z), o[3] = from_f32<OUT>(a.w);
-}
-
 bool aligned16p(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 template <typename IN, bool E5M2, bool VEC>
@@ -318,21 +269,6 @@ cudaError_t launch_fp8_dequantize(const Fp8View& in, long long rows, int cols, v
                        : dequantize_as<float, false>(in, rows, cols, Y, ldy, s);
     return in.e5m2 ? dequantize_as<__nv_bfloat16, true>(in, rows, cols, Y, ldy, s)
                    : dequantize_as<__nv_bfloat16, false>(in, rows, cols, Y, ldy, s);
-}
-
-cudaError_t launch_fp8_colsum(const void* Y, void* out, bool out_f32, int B, int T, int N, cudaStream_t s) {
-    const dim3 grid((N + kFp8Block - 1) / kFp8Block, T);
-    if (out_f32)
-        return launch_k(colsum_kernel<float>, grid, dim3(kThreads), 0, s, (const __nv_bfloat16*)Y, (float*)out, B, T, N);
-    return launch_k(colsum_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, (const __nv_bfloat16*)Y, (__nv_bfloat16*)out,
-                    B, T, N);
-}
-
-cudaError_t launch_fp8_sum_parts(const float* part, void* out, bool out_f32, int R, int T, int N, cudaStream_t s) {
-    const dim3 grid((N + 511) / 512, T);
-    if (out_f32)
-        return launch_k(sum_parts_kernel<float>, grid, dim3(128), 0, s, part, (float*)out, R, N);
-    return launch_k(sum_parts_kernel<__nv_bfloat16>, grid, dim3(128), 0, s, part, (__nv_bfloat16*)out, R, N);
 }
 
 }  // namespace rm

@@ -86,7 +86,6 @@ struct Args {
     void* y;                             // [B][T][N]
     bool vec;                            // y's rows are 16-byte aligned
     Fp8View o0, o1;                      // GELU: a, u (kept); DGELU: dU, the kept u
-    float* colpart;                      // DGELU: sums of dU over 32 rows, [T][m_tiles * 8][N]
     int* err;
     unsigned long long timeout_ns;
 };
@@ -104,51 +103,6 @@ __device__ __forceinline__ Tile tile_of(long long i, const Args& a) {
     r.m0 = (rem - nb * a.m_tiles) * 2 * BM;
     r.n0 = nb * BN;
     return r;
-}
-
-// One row's 64 bytes into this warp's staging, 16 bytes at a time: piece c of row
-// r at c ^ (r / 2 % 4), which keeps rows and pieces free of bank conflicts.
-__device__ __forceinline__ uint32_t staged_at(uint32_t stage, int row, int c) {
-    return stage + 64u * row + 16u * (uint32_t)(c ^ ((row >> 1) & 3));
-}
-__device__ __forceinline__ uint4 staged16(uint32_t stage, int row, int c) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(staged_at(stage, row, c)));
-    return v;
-}
-
-// The staged 32 rows to memory: row r at dst + r pitch, the first `rows` of them,
-// of each the first `bytes` (whole 16-byte pieces when VEC, else elements of ESZ
-// bytes).  Four lanes write a row's 64 bytes.  Plain stores: the staging is free
-// again after a warp barrier, where a bulk copy's reads would be waited for.
-template <bool VEC, int ESZ>
-__device__ __forceinline__ void store_rows(uint32_t stage, char* dst, size_t pitch, int rows, int bytes, int lane) {
-    __syncwarp();
-    const int c = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 2);
-        if (r < rows && 16 * c < bytes) {
-            const uint4 v = staged16(stage, r, c);
-            char* p = dst + (size_t)r * pitch + 16 * c;
-            if (VEC) {
-                *reinterpret_cast<uint4*>(p) = v;
-            } else {
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 16 / ESZ; ++e)
-                    if (16 * c + ESZ * e < bytes) {
-                        if (ESZ == 2)
-                            *reinterpret_cast<uint16_t*>(p + 2 * e) = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-                        else
-                            *reinterpret_cast<uint32_t*>(p + 4 * e) = w[e];
-                    }
-            }
-        }
-    }
-    __syncwarp();
 }
 
 // Where the two warps of a block meet: this warp's and the partner's rows of the
@@ -274,31 +228,6 @@ __device__ __forceinline__ bool epilogue(float (&v)[COLS], const Args& a, const 
         if (!block_amax(v, partner, 0, a, lane, m)) return false;
         save_row(v, m, a.o0, a, tl.t, m_warp, n, rows, lane, stage);
     } else {
-        // sums over this warp's 32 rows, for the bias gradient: 16 columns of every row
-        // staged, then lane c (and c + 16) adds up column c of 16 rows
-        float* part = a.colpart + ((size_t)tl.t * a.m_tiles * 8 + m_warp / 32) * a.N + n;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                st_shared_v4(staged_at(stage, lane, c), __float_as_uint(v[16 * h + 4 * c]),
-                             __float_as_uint(v[16 * h + 4 * c + 1]), __float_as_uint(v[16 * h + 4 * c + 2]),
-                             __float_as_uint(v[16 * h + 4 * c + 3]));
-            __syncwarp();
-            float sum[2] = {};
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                float x;
-                asm volatile("ld.shared.f32 %0, [%1];"
-                             : "=f"(x)
-                             : "r"(staged_at(stage, 2 * r + (lane >> 4), (lane >> 2) & 3) + 4u * (lane & 3)));
-                sum[r & 1] += x;
-            }
-            __syncwarp();
-            float cs = sum[0] + sum[1];
-            cs += __shfl_xor_sync(0xffffffffu, cs, 16);
-            if (lane < 16 && n + 16 * h + lane < a.N) part[16 * h + lane] = cs;
-        }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             save_piece<__nv_bfloat16>(v + 32 * h, a, tl.t, m_warp, n + 32 * h, rows, lane, stage);
@@ -673,8 +602,6 @@ cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap&
 
 }  // namespace f8
 
-int fp8_colpart_rows(int B) { return (B + 2 * f8::BM - 1) / (2 * f8::BM) * 8; }
-
 cudaError_t launch_fp8_product(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s) {
     using namespace f8;
     if (fp8_streams(p)) return launch_fp8_stream(p, dev, s);
@@ -694,7 +621,6 @@ cudaError_t launch_fp8_product(const Fp8Product& p, const Fp8Device& dev, cudaSt
     a.err = dev.err;
     a.timeout_ns = dev.timeout_ns;
     a.o0 = p.o0, a.o1 = p.o1;
-    a.colpart = p.colpart;
     a.vec = p.N % (p.epi == FP8_OUT_F32 ? 4 : 8) == 0;
     CUtensorMap mx, mw;
     const auto u8t = CU_TENSOR_MAP_DATA_TYPE_UINT8;

@@ -119,4 +119,49 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// One row's 64 bytes into this warp's staging, 16 bytes at a time: piece c of row
+// r at c ^ (r / 2 % 4), which keeps rows and pieces free of bank conflicts.
+__device__ __forceinline__ uint32_t staged_at(uint32_t stage, int row, int c) {
+    return stage + 64u * row + 16u * (uint32_t)(c ^ ((row >> 1) & 3));
+}
+__device__ __forceinline__ uint4 staged16(uint32_t stage, int row, int c) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(staged_at(stage, row, c)));
+    return v;
+}
+
+// The staged 32 rows to memory: row r at dst + r pitch, the first `rows` of them,
+// of each the first `bytes` (whole 16-byte pieces when VEC, else elements of ESZ
+// bytes).  Four lanes write a row's 64 bytes.  Plain stores: the staging is free
+// again after a warp barrier, where a bulk copy's reads would be waited for.
+template <bool VEC, int ESZ>
+__device__ __forceinline__ void store_rows(uint32_t stage, char* dst, size_t pitch, int rows, int bytes, int lane) {
+    __syncwarp();
+    const int c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        if (r < rows && 16 * c < bytes) {
+            const uint4 v = staged16(stage, r, c);
+            char* p = dst + (size_t)r * pitch + 16 * c;
+            if (VEC) {
+                *reinterpret_cast<uint4*>(p) = v;
+            } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 16 / ESZ; ++e)
+                    if (16 * c + ESZ * e < bytes) {
+                        if (ESZ == 2)
+                            *reinterpret_cast<uint16_t*>(p + 2 * e) = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                        else
+                            *reinterpret_cast<uint32_t*>(p + 4 * e) = w[e];
+                    }
+            }
+        }
+    }
+    __syncwarp();
+}
+
 }  // namespace rm

@@ -14,6 +14,9 @@
 //   warp 1        MMA issuer (the even CTA's): kind::f16 on bf16, M = N = 256
 //   warp 2        TMA producer of x's codes (64 samples x 128 bytes)
 //   warps 4-11    epilogue
+//   warps 20-21   db, the column sums of dY, in the tiles of the first 256 k: from
+//                 dY's operand tile in shared memory once the MMA is done with it,
+//                 so dY is not read again
 //   warp 3        x's exponent bytes into shared memory, eight k-blocks' loads
 //                 at a time so that their latency is paid once in eight
 //   warps 12-19   restore codes to bf16: MN-major operand rows are samples, so
@@ -47,7 +50,9 @@ constexpr int AHEAD = 8;                     // k-blocks whose exponent bytes ar
 // is added to dW in memory with rounding to nearest.
 constexpr int CHUNK = 2048;
 constexpr int STAGING = 4096;
-constexpr int THREADS = 128 + 32 * (EPI_WARPS + CONV_WARPS);
+constexpr int SUM_WARPS = 2;                 // one per box of 64 columns of dY
+constexpr int SUM_WARP0 = 4 + EPI_WARPS + CONV_WARPS;
+constexpr int THREADS = 32 * (SUM_WARP0 + SUM_WARPS);
 constexpr int SMEM_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES) + RAWS * (RAW_BYTES + BK) + EPI_WARPS * STAGING + 256;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 static_assert(GROUPS <= RAWS && GROUPS <= STAGES, "a k-block per group of restorers");
@@ -59,6 +64,7 @@ struct Args {
     long long tiles;
     const uint8_t* xs;
     long long xs_ld;
+    void* db;                            // [T][N] or null
     int* err;
     unsigned long long timeout_ns;
 };
@@ -166,7 +172,9 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     auto rempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + RAWS + s); };
     auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * RAWS + x); };
     auto tempty_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * RAWS + 2 + x); };
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + 8 * (2 * STAGES + 2 * RAWS + 4));
+    auto summed_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 2 * RAWS + 4 + s); };
+    uint32_t* tmem_holder =
+        reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + 8 * (3 * STAGES + 2 * RAWS + 4));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -179,6 +187,7 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_bar(s), 1 + 2 * CONV_GROUP);   // the even CTA's: dY's bytes of both CTAs, both CTAs' restorers
             mbar_init(empty_bar(s), 1);                   // multicast commit
+            mbar_init(summed_bar(s), SUM_WARPS);          // the same, and dY has been summed
         }
         for (int s = 0; s < RAWS; ++s) {
             mbar_init(rfull_bar(s), 2);                   // x's bytes, its exponents
@@ -213,7 +222,8 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             const Tile tl = tile_of(i, args);
             const int col = tl.n0 + BN / 2 * (int)rank;
             for (int kb = 0; kb < kblocks; ++kb) {
-                if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                if (!wait_bounded(args.db ? summed_bar(stage) : empty_bar(stage), phase ^ 1u, abort_flag, args.err,
+                                  args.timeout_ns)) {
                     ok = false;
                     break;
                 }
@@ -318,6 +328,60 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                             if (++slot == RAWS) slot = 0, phase ^= 1u;
                         }
                     }
+                }
+            }
+        }
+    } else if (warp >= SUM_WARP0) {
+        // ------------------------------ bias gradient -----------------------------
+        // Lane: 8 columns (16 bytes) of this warp's box, every fourth row.  Every
+        // k-block passes through here to the dY producer; those of the first 256 k
+        // are summed.
+        const int box = warp - SUM_WARP0, c = lane & 7, r0 = lane >> 3;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (long long i = unit; args.db && ok && i < args.tiles; i += nunits) {
+            const Tile tl = tile_of(i, args);
+            float sum[8] = {};
+            for (int kb = 0; kb < kblocks; ++kb) {
+                if (!wait_bounded(empty_bar(stage), phase, abort_flag, args.err, args.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                if (tl.m0 == 0) {
+                    const uint32_t src = sB + stage * B_BYTES + box * BOX_BYTES;
+#pragma unroll 8
+                    for (int r = r0; r < BK; r += 4) {
+                        const uint4 q = ld_shared_u4(src + 128u * r + 16u * (uint32_t)(c ^ (r & 7)));
+                        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            sum[2 * j] += __uint_as_float(w[j] << 16);
+                            sum[2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(summed_bar(stage));
+                if (++stage == STAGES) stage = 0, phase ^= 1u;
+            }
+            if (tl.m0 != 0) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 8);
+                sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
+            }
+            const int n = tl.n0 + BN / 2 * (int)rank + 64 * box + 8 * c;
+            if (ok && r0 == 0 && n < args.N) {       // N is a multiple of 8
+                const size_t at = (size_t)tl.t * args.N + n;
+                if (F32) {
+                    float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(args.db) + at);
+                    o[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+                    o[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+                } else {
+                    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(args.db) + at) =
+                        make_uint4(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]),
+                                   pack_bf16x2(sum[4], sum[5]), pack_bf16x2(sum[6], sum[7]));
                 }
             }
         }
@@ -494,7 +558,7 @@ cudaError_t run(const CUtensorMap& mx, const CUtensorMap& my, const CUtensorMap&
 
 }  // namespace f8w
 
-cudaError_t launch_fp8_wgrad(const Fp8View& x, const void* dY, void* dW, bool w_f32, int B, int T, int K, int N,
+cudaError_t launch_fp8_wgrad(const Fp8View& x, const void* dY, void* dW, void* db, bool f32, int B, int T, int K, int N,
                              const Fp8Device& dev, cudaStream_t s) {
     using namespace f8w;
     Args a{};
@@ -503,18 +567,19 @@ cudaError_t launch_fp8_wgrad(const Fp8View& x, const void* dY, void* dW, bool w_
     a.n_tiles = (N + BN - 1) / BN;
     a.kblocks = (B + BK - 1) / BK;
     a.tiles = (long long)T * a.m_tiles * a.n_tiles;
-    a.chunk_blocks = w_f32 ? CHUNK / BK : a.kblocks;
+    a.chunk_blocks = f32 ? CHUNK / BK : a.kblocks;
     a.chunks = (a.kblocks + a.chunk_blocks - 1) / a.chunk_blocks;
     a.xs = x.scales, a.xs_ld = x.lds;
+    a.db = db;
     a.err = dev.err;
     a.timeout_ns = dev.timeout_ns;
     CUtensorMap mx, my, mw;
     if (!fp8_tensor_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, x.codes, K, B, T, T * x.ld, x.ld, BM, BK) ||
         !fp8_tensor_map(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, N, B, T, 2ll * T * N, 2ll * N, 64, BK) ||
-        !fp8_tensor_map(&mw, w_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dW, N, K, T,
-                        (w_f32 ? 4ll : 2ll) * N, (w_f32 ? 4ll : 2ll) * K * N, w_f32 ? 32 : 64, 32))
+        !fp8_tensor_map(&mw, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dW, N, K, T,
+                        (f32 ? 4ll : 2ll) * N, (f32 ? 4ll : 2ll) * K * N, f32 ? 32 : 64, 32))
         return cudaErrorInvalidValue;
-    return w_f32 ? run<true>(mx, my, mw, a, dev.num_sms, s) : run<false>(mx, my, mw, a, dev.num_sms, s);
+    return f32 ? run<true>(mx, my, mw, a, dev.num_sms, s) : run<false>(mx, my, mw, a, dev.num_sms, s);
 }
 
 }  // namespace rm
