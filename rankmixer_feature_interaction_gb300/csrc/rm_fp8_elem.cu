@@ -1,10 +1,14 @@
 // Elementwise kernels of the 8-bit operators: saving rows and weights in 8 bits,
 // and restoring rows.
 //
-// Saving reads every value once and writes one byte for it; 16 lanes own one
-// block of 128 values (8 each: one or two 16-byte loads), agree on its largest
-// magnitude with four shuffles and write 8 bytes of codes each.  Four blocks
-// per half warp are loaded before the first is used.
+// Saving reads every value once and writes one byte for it; 16 lanes own one block
+// of 128 values, 8 each (16-byte loads), agree on its largest magnitude with four
+// shuffles and write 8 bytes of codes each.  64 bytes per thread are loaded before
+// the first is used and stay as they came (bf16 pairs) until then: few registers,
+// so many warps, are what hides the loads' latency.  Rows that are not 16-byte aligned are read
+// an element at a time, neighbouring lanes neighbouring elements, and their
+// codes pass through shared memory to the same 8-byte stores; restoring such
+// rows mirrors that.
 #include "rm_common.cuh"
 #include "rm_fp8.cuh"
 
@@ -12,7 +16,7 @@ namespace rm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 4;                  // 16-byte pieces in flight per thread
 
 template <typename IN, bool VEC>
 __device__ __forceinline__ void load8(const IN* __restrict__ p, int n, float (&v)[8]) {
@@ -35,78 +39,150 @@ __device__ __forceinline__ void load8(const IN* __restrict__ p, int n, float (&v
     }
 }
 
-// Largest of 16 lanes, for all of them.
-__device__ __forceinline__ uint32_t max16(uint32_t m) {
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    return m;
-}
-
-// One block of a row: 8 values per lane of a half warp (n of them inside the row).
-template <bool E5M2>
-__device__ __forceinline__ void save_block(const float (&v)[8], int n, int l16, uint8_t* codes, uint8_t* scale,
-                                           int room) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, fp8_finite_bits(v[i]));
-    const uint32_t E = fp8_exponent<E5M2>(max16(m));
-    const float s = fp8_inv_scale(E);
-    float q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = fp8_poison(v[i]) * s;
-    if (room >= 8) {        // code rows are padded to 16 bytes, so a lane's 8 bytes fit or are not there at all
-        const uint2 w = make_uint2(fp8_pack4<E5M2>(q[0], q[1], q[2], q[3]), fp8_pack4<E5M2>(q[4], q[5], q[6], q[7]));
-        *reinterpret_cast<uint2*>(codes) = w;
+// Row and piece (of n per row) of a running number, and of the one `step` further
+// (step = dq n + dr).
+__device__ __forceinline__ void split_id(unsigned long long id, unsigned long long count, int n, unsigned long long& row,
+                                         int& j) {
+    if (count <= 0xffffffffull) {
+        const uint32_t r = (uint32_t)id / (uint32_t)n;
+        row = r;
+        j = (int)((uint32_t)id - r * (uint32_t)n);
+    } else {
+        row = id / (unsigned)n;
+        j = (int)(id - row * (unsigned)n);
     }
-    if (l16 == 0 && n > 0) *scale = (uint8_t)E;
+}
+__device__ __forceinline__ void next_id(unsigned long long& row, int& j, int dq, int dr, int n) {
+    row += dq;
+    j += dr;
+    if (j >= n) j -= n, ++row;
 }
 
+// Eight values of a row as they lie in memory, zeros past its end.
+template <typename IN>
+struct Raw8 {
+    uint32_t w[sizeof(IN) * 2];
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(IN) == 2)
+            return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+        else
+            return __uint_as_float(w[i]);
+    }
+    __device__ __forceinline__ void set(int i, IN x) {
+        if constexpr (sizeof(IN) == 2)
+            w[i >> 1] = i & 1 ? (w[i >> 1] & 0xffffu) | ((uint32_t)__bfloat16_as_ushort(x) << 16)
+                              : (w[i >> 1] & 0xffff0000u) | __bfloat16_as_ushort(x);
+        else
+            w[i] = __float_as_uint(x);
+    }
+    __device__ __forceinline__ void load(const IN* __restrict__ p, int n) {
+        if (n >= 8) {
+#pragma unroll
+            for (int k = 0; k < (int)sizeof(IN) / 2; ++k) {
+                const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p) + k);
+                w[4 * k] = q.x, w[4 * k + 1] = q.y, w[4 * k + 2] = q.z, w[4 * k + 3] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(IN) * 2; ++i) w[i] = 0;
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (i < n) set(i, p[i]);
+        }
+    }
+    // every 16th value from p on, 8 of them
+    __device__ __forceinline__ void gather(const IN* __restrict__ p, int n) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(IN) * 2; ++i) w[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (16 * i < n) set(i, p[16 * i]);
+    }
+    // float bits of the largest magnitude; infinities and NaN count as they are
+    __device__ __forceinline__ uint32_t amax_bits() const {
+        uint32_t m = 0;
+        if constexpr (sizeof(IN) == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+            return max(m << 16, m & 0xffff0000u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+            return m;
+        }
+    }
+};
+
+// kUnroll blocks per 16 lanes (half of that for float32).
 template <typename IN, bool E5M2, bool VEC, bool COPY>
 __global__ void __launch_bounds__(kThreads)
-quantize_kernel(const IN* __restrict__ X, unsigned long long blocks, int cols, int nb, long long ldx, Fp8View out,
-                __nv_bfloat16* __restrict__ copy) {
+quantize_kernel(const IN* __restrict__ X, unsigned long long blocks, int cols, int nb, int dq, int dr, long long ldx,
+                Fp8View out, __nv_bfloat16* __restrict__ copy) {
+    constexpr int UNROLL = sizeof(IN) == 2 ? kUnroll : kUnroll / 2, PER = kThreads / 16;
+    __shared__ uint2 bytes[VEC ? 1 : kThreads];      // a thread's 8 codes: a block's 128 are contiguous
     pdl_wait();
     pdl_launch_next();
     const int l16 = threadIdx.x & 15;
-    const unsigned long long base = (unsigned long long)blockIdx.x * (kThreads / 16 * kUnroll) + (threadIdx.x >> 4);
-    float v[kUnroll][8];
-    unsigned long long row[kUnroll];
-    int col[kUnroll], left[kUnroll];
+    const unsigned long long base = (unsigned long long)blockIdx.x * (PER * UNROLL) + (threadIdx.x >> 4);
+    Raw8<IN> v[UNROLL];
+    unsigned long long row0 = 0;
+    int j0 = 0;
+    if (base < blocks) split_id(base, blocks, nb, row0, j0);
+    {
+        unsigned long long row = row0;
+        int j = j0;
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-        const unsigned long long id = base + (unsigned long long)i * (kThreads / 16);
-        unsigned long long r = 0;
-        int j = 0;
-        left[i] = 0;
-        if (id < blocks) {
-            if (blocks <= 0xffffffffull) {
-                r = (uint32_t)id / (uint32_t)nb;
-                j = (int)((uint32_t)id - (uint32_t)r * (uint32_t)nb);
-            } else {
-                r = id / (unsigned)nb;
-                j = (int)(id - r * (unsigned)nb);
-            }
-            left[i] = cols - (j * kFp8Block + 8 * l16);
+        for (int i = 0; i < UNROLL; ++i) {
+            const int n = base + (unsigned long long)i * PER < blocks ? cols - j * kFp8Block : 0;
+            const IN* p = X + row * (unsigned long long)ldx + j * kFp8Block;
+            if (VEC)
+                v[i].load(p + 8 * l16, n - 8 * l16);
+            else
+                v[i].gather(p + l16, n - l16);
+            next_id(row, j, dq, dr, nb);
         }
-        row[i] = r;
-        col[i] = j * kFp8Block + 8 * l16;
-        load8<IN, VEC>(X + r * (unsigned long long)ldx + col[i], left[i], v[i]);
     }
+    unsigned long long row = row0;
+    int j = j0;
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-        const bool here = base + (unsigned long long)i * (kThreads / 16) < blocks;
-        const int room = here ? (cols + 15) / 16 * 16 - col[i] : 0;
-        save_block<E5M2>(v[i], here ? cols - (col[i] - 8 * l16) : 0, l16,
-                         out.codes + row[i] * (unsigned long long)out.ld + col[i],
-                         out.scales + row[i] * (unsigned long long)out.lds + col[i] / kFp8Block, room);
-        if (COPY && left[i] >= 8) {
-            uint4 w;
-            w.x = pack_bf16x2(v[i][0], v[i][1]);
-            w.y = pack_bf16x2(v[i][2], v[i][3]);
-            w.z = pack_bf16x2(v[i][4], v[i][5]);
-            w.w = pack_bf16x2(v[i][6], v[i][7]);
-            *reinterpret_cast<uint4*>(copy + row[i] * (unsigned long long)cols + col[i]) = w;
+    for (int i = 0; i < UNROLL; ++i) {
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = v[i].get(k);
+        uint32_t m = v[i].amax_bits();
+        if (m >= 0x7f800000u) {                      // infinities become NaN, and neither counts
+            m = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                m = max(m, fp8_finite_bits(f[k]));
+                f[k] = fp8_poison(f[k]);
+            }
         }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const uint32_t E = fp8_exponent<E5M2>(m);
+        const float s = fp8_inv_scale(E);
+        uint2 w = make_uint2(fp8_pack4<E5M2>(f[0] * s, f[1] * s, f[2] * s, f[3] * s),
+                             fp8_pack4<E5M2>(f[4] * s, f[5] * s, f[6] * s, f[7] * s));
+        if (!VEC) {                                  // lane's codes are every 16th: to their places
+            uint8_t* mine = reinterpret_cast<uint8_t*>(bytes) + (threadIdx.x & ~15) * 8 + l16;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mine[16 * k] = (uint8_t)((k < 4 ? w.x : w.y) >> (8 * (k & 3)));
+            __syncwarp();
+            w = bytes[threadIdx.x];
+            __syncwarp();
+        }
+        const int col = j * kFp8Block + 8 * l16;
+        // code rows are padded to 16 bytes, so a lane's 8 fit when they begin before that
+        if (base + (unsigned long long)i * PER < blocks && col < (cols + 15) / 16 * 16) {
+            *reinterpret_cast<uint2*>(out.codes + row * (unsigned long long)out.ld + col) = w;
+            if (l16 == 0) out.scales[row * (unsigned long long)out.lds + j] = (uint8_t)E;
+            if (COPY)                                // cols is a multiple of 16
+                *reinterpret_cast<uint4*>(copy + row * (unsigned long long)cols + col) =
+                    make_uint4(pack_bf16x2(v[i].get(0), v[i].get(1)), pack_bf16x2(v[i].get(2), v[i].get(3)),
+                               pack_bf16x2(v[i].get(4), v[i].get(5)), pack_bf16x2(v[i].get(6), v[i].get(7)));
+        }
+        next_id(row, j, dq, dr, nb);
     }
 }
 
@@ -151,61 +227,78 @@ quantize_weight_kernel(const IN* __restrict__ W, int K, int N, Fp8View out) {
 
 template <typename OUT, bool E5M2, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-dequantize_kernel(Fp8View in, unsigned long long chunks, int cols, int nch, OUT* __restrict__ Y, long long ldy) {
+dequantize_kernel(Fp8View in, unsigned long long chunks, int cols, int nch, int dq, int dr, OUT* __restrict__ Y,
+                  long long ldy) {
+    // one thread per 16 codes; four chunks in flight
+    __shared__ OUT stage[VEC ? 1 : kThreads * 17];   // a thread's 16 values, one apart from the next thread's
     pdl_wait();
     pdl_launch_next();
-    // one thread per 16 codes; four chunks in flight
-    unsigned long long base = (unsigned long long)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+    const unsigned long long base = (unsigned long long)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
     uint4 w[kUnroll];
     float sc[kUnroll];
     unsigned long long row[kUnroll];
     int col[kUnroll];
+    unsigned long long r = 0;
+    int c = 0;
+    if (base < chunks) split_id(base, chunks, nch, r, c);
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-        const unsigned long long id = base + (unsigned long long)i * kThreads;
-        row[i] = 0;
+        row[i] = r;
         col[i] = cols;
-        if (id < chunks) {
-            unsigned long long r;
-            if (chunks <= 0xffffffffull)
-                r = (uint32_t)id / (uint32_t)nch;
-            else
-                r = id / (unsigned)nch;
-            row[i] = r;
-            col[i] = (int)(id - r * (unsigned)nch) * 16;
-            w[i] = *reinterpret_cast<const uint4*>(in.codes + r * (unsigned long long)in.ld + col[i]);
+        w[i] = make_uint4(0, 0, 0, 0);
+        sc[i] = 0.f;
+        if (base + (unsigned long long)i * kThreads < chunks) {
+            col[i] = 16 * c;
+            w[i] = __ldcs(reinterpret_cast<const uint4*>(in.codes + r * (unsigned long long)in.ld + col[i]));
             sc[i] = fp8_scale(in.scales[r * (unsigned long long)in.lds + col[i] / kFp8Block]);
         }
+        next_id(r, c, dq, dr, nch);
     }
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
         const int n = cols - col[i];
-        if (n <= 0) continue;
         const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
         float v[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 f = fp8_unpack2<E5M2>(u[j >> 1] >> (16 * (j & 1)));
-            v[2 * j] = f.x * sc[i];
-            v[2 * j + 1] = f.y * sc[i];
+        for (int k = 0; k < 8; ++k) {
+            const float2 f = fp8_unpack2<E5M2>(u[k >> 1] >> (16 * (k & 1)));
+            v[2 * k] = f.x * sc[i];
+            v[2 * k + 1] = f.y * sc[i];
         }
         OUT* y = Y + row[i] * (unsigned long long)ldy + col[i];
-        if (VEC && n >= 16) {
-            if constexpr (sizeof(OUT) == 2) {
+        if (VEC) {
+            if (n >= 16) {
+                if constexpr (sizeof(OUT) == 2) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    reinterpret_cast<uint4*>(y)[j] =
-                        make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                   pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+                    for (int k = 0; k < 2; ++k)
+                        reinterpret_cast<uint4*>(y)[k] =
+                            make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                                       pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        reinterpret_cast<float4*>(y)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                }
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    reinterpret_cast<float4*>(y)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                for (int k = 0; k < 16; ++k)
+                    if (k < n) y[k] = from_f32<OUT>(v[k]);
             }
-        } else {
+        } else {                       // the warp's 512 values, 32 neighbours at a time
+            const int lane = threadIdx.x & 31;
+            OUT* mine = stage + threadIdx.x * 17;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (j < n) y[j] = from_f32<OUT>(v[j]);
+            for (int k = 0; k < 16; ++k) mine[k] = from_f32<OUT>(v[k]);
+            __syncwarp();
+            const OUT* warp = stage + (threadIdx.x & ~31) * 17;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const int owner = 2 * k + (lane >> 4), e = lane & 15;
+                const unsigned long long at = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(y), owner);
+                const int m = __shfl_sync(0xffffffffu, n, owner);
+                if (e < m) reinterpret_cast<OUT*>(at)[e] = warp[owner * 17 + e];
+            }
+            __syncwarp();
         }
     }
 }
@@ -215,11 +308,13 @@ bool aligned16p(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) =
 template <typename IN, bool E5M2, bool VEC>
 cudaError_t run_quantize(const void* X, long long rows, int cols, long long ldx, const Fp8View& out, void* copy,
                          cudaStream_t s) {
-    const int nb = (cols + kFp8Block - 1) / kFp8Block;
+    const int nb = (cols + kFp8Block - 1) / kFp8Block, half = kThreads / 16,
+              per = half * (sizeof(IN) == 2 ? kUnroll : kUnroll / 2);
     const unsigned long long blocks = (unsigned long long)rows * nb;
-    const unsigned grid = (unsigned)((blocks + kThreads / 16 * kUnroll - 1) / (kThreads / 16 * kUnroll));
+    const unsigned grid = (unsigned)((blocks + per - 1) / per);
     return launch_k(copy ? quantize_kernel<IN, E5M2, VEC, true> : quantize_kernel<IN, E5M2, VEC, false>, dim3(grid),
-                    dim3(kThreads), 0, s, (const IN*)X, blocks, cols, nb, ldx, out, (__nv_bfloat16*)copy);
+                    dim3(kThreads), 0, s, (const IN*)X, blocks, cols, nb, half / nb, half % nb, ldx, out,
+                    (__nv_bfloat16*)copy);
 }
 
 template <typename IN>
@@ -240,7 +335,7 @@ cudaError_t dequantize_as(const Fp8View& in, long long rows, int cols, void* Y, 
     const unsigned grid = (unsigned)((chunks + kThreads * kUnroll - 1) / (kThreads * kUnroll));
     const bool vec = aligned16p(Y) && (ldy * sizeof(OUT)) % 16 == 0;
     return launch_k(vec ? dequantize_kernel<OUT, E5M2, true> : dequantize_kernel<OUT, E5M2, false>, dim3(grid),
-                    dim3(kThreads), 0, s, in, chunks, cols, nch, (OUT*)Y, ldy);
+                    dim3(kThreads), 0, s, in, chunks, cols, nch, kThreads / nch, kThreads % nch, (OUT*)Y, ldy);
 }
 
 }  // namespace
