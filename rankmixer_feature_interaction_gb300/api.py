@@ -4,6 +4,9 @@ arithmetic of the method happens here; every step runs in the CUDA kernels.
 """
 from __future__ import annotations
 
+import functools
+import math
+
 import torch
 
 from . import _lib
@@ -346,6 +349,7 @@ def head_forward(pooled: torch.Tensor, w: torch.Tensor, b: float, y: torch.Tenso
 # These calls are short, so their host side is kept short too: the current stream's handle
 # comes straight from torch's C side, an Fp8Tensor carries its C structure, and its torch
 # tensors are made when they are asked for.
+_FORMATS = {"e4m3": _lib.RM_E4M3, "e5m2": _lib.RM_E5M2}
 _F8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 _F8_CODE = {torch.float8_e4m3fn: _lib.RM_E4M3, torch.float8_e5m2: _lib.RM_E5M2}
 _CODE = {torch.bfloat16: _lib.RM_BF16, torch.float32: _lib.RM_F32}
@@ -376,9 +380,7 @@ class Fp8Tensor:
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
-            n, ld = self._at, self.c.ld
-            for d in self.lead:
-                ld *= d
+            n, ld = self._at, self.c.ld * math.prod(self.lead)
             fmt = _F8["e5m2" if self.c.format == _lib.RM_E5M2 else "e4m3"]
             self._codes = self._arena[n:n + ld].view(fmt).view(self.lead + (self.c.ld,))
         return self._codes
@@ -386,9 +388,7 @@ class Fp8Tensor:
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is None:
-            n, size = self.c.scales - self._arena.data_ptr(), self.c.lds
-            for d in self.scale_lead:
-                size *= d
+            n, size = self.c.scales - self._arena.data_ptr(), self.c.lds * math.prod(self.scale_lead)
             self._scales = self._arena[n:n + size].view(self.scale_lead + (self.c.lds,))
         return self._scales
 
@@ -398,27 +398,26 @@ class Fp8Tensor:
 
     @property
     def nbytes(self) -> int:
-        n, s = self.c.ld, self.c.lds
-        for d in self.lead:
-            n *= d
-        for d in self.scale_lead:
-            s *= d
-        return n + s
+        return self.c.ld * math.prod(self.lead) + self.c.lds * math.prod(self.scale_lead)
 
 
-def _fp8_new(wanted: list, device: torch.device, index: int) -> list:
-    """8-bit tensors [(lead, cols, format, lead of the scales)] in one allocation, each part 256-byte aligned."""
+@functools.lru_cache(maxsize=256)
+def _fp8_layout(wanted: tuple) -> tuple:
+    """Where the parts of 8-bit tensors (lead, cols, format, lead of the scales) lie in one
+    allocation: (its bytes, [(codes, scales, ld, lds)]), each part 256-byte aligned."""
     at, places = 0, []
     for lead, cols, fmt, scale_lead in wanted:
         ld, lds = (cols + 15) // 16 * 16, (cols + 511) // 512 * 4
-        n, m = ld, lds
-        for d in lead:
-            n *= d
-        for d in scale_lead:
-            m *= d
-        places.append((at, at + (n + 255) // 256 * 256, ld, lds))
-        at = places[-1][1] + (m + 255) // 256 * 256
-    arena = torch.empty(at, dtype=torch.uint8, device=device)
+        scales = at + (math.prod(lead) * ld + 255) // 256 * 256
+        places.append((at, scales, ld, lds))
+        at = scales + (math.prod(scale_lead) * lds + 255) // 256 * 256
+    return at, places
+
+
+def _fp8_new(wanted: tuple, device: torch.device, index: int) -> list:
+    """Uninitialised 8-bit tensors (lead, cols, format, lead of the scales) in one allocation."""
+    size, places = _fp8_layout(wanted)
+    arena = torch.empty(size, dtype=torch.uint8, device=device)
     base, out = arena.data_ptr(), []
     for (lead, cols, fmt, scale_lead), (codes, scales, ld, lds) in zip(wanted, places):
         q = object.__new__(Fp8Tensor)
@@ -433,7 +432,7 @@ def _fp8_new(wanted: list, device: torch.device, index: int) -> list:
 def _fp8_device(index: int, *others) -> int:
     """The current device, on which the calls run: every tensor has to live there."""
     d = _current_device()
-    if index != d or any(o is not None and o != d for o in others):
+    if index != d or (others and others != (d,) * len(others)):
         raise ValueError(f"tensors must be on the current CUDA device (cuda:{d}), got devices {(index, *others)}")
     return d
 
@@ -461,16 +460,17 @@ def fp8_quantize(X: torch.Tensor, fmt: str = "e4m3") -> Fp8Tensor:
     dtype, shape = _CODE.get(X.dtype), X.shape
     if dtype is None:
         raise ValueError(f"X must be bfloat16 or float32, got {X.dtype}")
-    if len(shape) < 1 or (X.stride(-1) != 1 and shape[-1] > 1):
-        raise ValueError("the last dimension of X must be contiguous")
-    C, lead, rows = shape[-1], tuple(shape[:-1]), 1
-    for n in lead:
-        rows *= n
-    ldx = C if X.is_contiguous() else X.view(rows, C).stride(0)       # raises when rows are not one stride apart
+    *lead, C = shape
+    lead, rows = tuple(lead), math.prod(lead)
     if rows < 1 or C < 1:
-        _lib.check(_lib.RM_ERR_INVALID_ARG, f"fp8_quantize of an empty tensor {tuple(shape)}")
-    out, = _fp8_new([(lead, C, _F8_CODE[_F8[fmt]], lead)], X.device, d)
-    _lib.rm_fp8_quantize(X.data_ptr(), dtype, rows, C, ldx if rows > 1 else C, out.c, _raw_stream(d))
+        raise _lib.RankMixerError(_lib.RM_ERR_INVALID_ARG, "fp8_quantize", f"empty tensor {tuple(shape)}")
+    ldx = C
+    if not X.is_contiguous():
+        if X.stride(-1) != 1 and C > 1:
+            raise ValueError("the last dimension of X must be contiguous")
+        ldx = X.view(rows, C).stride(0) if rows > 1 else C            # raises when rows are not one stride apart
+    out, = _fp8_new(((lead, C, _FORMATS[fmt], lead),), X.device, d)
+    _lib.rm_fp8_quantize(X.data_ptr(), dtype, rows, C, ldx, out.c, _raw_stream(d))
     return out
 
 
@@ -480,7 +480,7 @@ def fp8_quantize_weight(W: torch.Tensor) -> Fp8Tensor:
     if W.dtype not in _CODE or W.dim() != 3:
         raise ValueError(f"W must be a bfloat16 or float32 [T, K, N], got {W.dtype} {tuple(W.shape)}")
     T, K, N = W.shape
-    out, = _fp8_new([((T, K), N, _lib.RM_E4M3, (T, (K + 127) // 128))], W.device, d)
+    out, = _fp8_new((((T, K), N, _lib.RM_E4M3, (T, (K + 127) // 128)),), W.device, d)
     _lib.rm_fp8_quantize_weight(_ptr(W), _CODE[W.dtype], T, K, N, out.c, _raw_stream(d))
     return out
 
@@ -492,10 +492,7 @@ def fp8_dequantize(q: Fp8Tensor, dtype: str = "bf16") -> torch.Tensor:
         raise ValueError("fp8_dequantize takes rows with their own scales (activations)")
     tdt, code = _DTYPES[dtype]
     Y = torch.empty(q.lead + (q.cols,), dtype=tdt, device=q.device)
-    rows = 1
-    for n in q.lead:
-        rows *= n
-    _lib.rm_fp8_dequantize(q.c, rows, q.cols, Y.data_ptr(), code, q.cols, _raw_stream(d))
+    _lib.rm_fp8_dequantize(q.c, math.prod(q.lead), q.cols, Y.data_ptr(), code, q.cols, _raw_stream(d))
     return Y
 
 
@@ -581,7 +578,7 @@ class Fp8PFFN:
         """(V, the activations kept for backward: {"x", "u", "a"} in 8 bits)."""
         B = self._rows(X, "X")
         lead = (B, self.T)
-        x, u, a = _fp8_new([(lead, n, _lib.RM_E4M3, lead) for n in (self.D, self.F, self.F)], X.device,
+        x, u, a = _fp8_new(tuple((lead, n, _lib.RM_E4M3, lead) for n in (self.D, self.F, self.F)), X.device,
                            self.device_index)
         work, n = self._work(B, _lib.RM_FP8_TRAIN, X.device)
         V = self._forward(X, B, out_dtype, _lib.rm_fp8_kept(x.c, u.c, a.c), work.data_ptr(), n)
