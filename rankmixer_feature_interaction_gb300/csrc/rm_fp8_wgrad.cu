@@ -14,7 +14,7 @@
 //   warp 1        MMA issuer (the even CTA's): kind::f16 on bf16, M = N = 256
 //   warp 2        TMA producer of x's codes (64 samples x 128 bytes)
 //   warps 4-11    epilogue
-//   warps 20-21   db, the column sums of dY, in the tiles of the first 256 k: from
+//   warps 20-23   db, the column sums of dY, in the tiles of the first 256 k: from
 //                 dY's operand tile in shared memory once the MMA is done with it,
 //                 so dY is not read again
 //   warp 3        x's exponent bytes into shared memory, eight k-blocks' loads
@@ -42,7 +42,7 @@ constexpr int B_BYTES = BK * (BN / 2) * 2;   // dY: two boxes of 64 columns x 64
 constexpr int BOX_BYTES = 64 * BK * 2;
 constexpr int STAGES = 4, RAWS = 8;
 constexpr int EPI_WARPS = 8, CONV_WARPS = 8;
-constexpr int CONV_GROUP = 4;                // restoring warps per k-block
+constexpr int CONV_GROUP = 2;                // restoring warps per k-block
 constexpr int GROUPS = CONV_WARPS / CONV_GROUP;
 constexpr int AHEAD = 8;                     // k-blocks whose exponent bytes are loaded together
 // Float32 gradients of more samples are summed in chunks of this many: a chunk's
@@ -50,7 +50,7 @@ constexpr int AHEAD = 8;                     // k-blocks whose exponent bytes ar
 // is added to dW in memory with rounding to nearest.
 constexpr int CHUNK = 2048;
 constexpr int STAGING = 4096;
-constexpr int SUM_WARPS = 2;                 // one per box of 64 columns of dY
+constexpr int SUM_WARPS = 4;                 // 32 columns of dY each
 constexpr int SUM_WARP0 = 4 + EPI_WARPS + CONV_WARPS;
 constexpr int THREADS = 32 * (SUM_WARP0 + SUM_WARPS);
 constexpr int SMEM_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES) + RAWS * (RAW_BYTES + BK) + EPI_WARPS * STAGING + 256;
@@ -333,10 +333,11 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         }
     } else if (warp >= SUM_WARP0) {
         // ------------------------------ bias gradient -----------------------------
-        // Lane: 8 columns (16 bytes) of this warp's box, every fourth row.  Every
-        // k-block passes through here to the dY producer; those of the first 256 k
-        // are summed.
-        const int box = warp - SUM_WARP0, c = lane & 7, r0 = lane >> 3;
+        // Lane: 8 columns (16 bytes) of every eighth row.  Every k-block passes through
+        // here to the dY producer; those of the first 256 k are summed.  Eight lanes
+        // read four chunks of rows r and r + 4, whose swizzles have no bank in common.
+        const int box = (warp - SUM_WARP0) >> 1, c = (lane & 3) + 4 * ((warp - SUM_WARP0) & 1);
+        const int r0 = (lane >> 3) + (lane & 4);
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -350,8 +351,8 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 }
                 if (tl.m0 == 0) {
                     const uint32_t src = sB + stage * B_BYTES + box * BOX_BYTES;
-#pragma unroll 8
-                    for (int r = r0; r < BK; r += 4) {
+#pragma unroll
+                    for (int r = r0; r < BK; r += 8) {
                         const uint4 q = ld_shared_u4(src + 128u * r + 16u * (uint32_t)(c ^ (r & 7)));
                         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -368,11 +369,12 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             if (tl.m0 != 0) continue;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
+                sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 4);
                 sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 8);
                 sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
             }
             const int n = tl.n0 + BN / 2 * (int)rank + 64 * box + 8 * c;
-            if (ok && r0 == 0 && n < args.N) {       // N is a multiple of 8
+            if (ok && lane < 4 && n < args.N) {       // N is a multiple of 8
                 const size_t at = (size_t)tl.t * args.N + n;
                 if (F32) {
                     float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(args.db) + at);
@@ -387,9 +389,9 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         }
     } else if (warp >= 12) {
         // ------------------------------ restorers ---------------------------------
-        // Two groups of four warps, each with every other k-block, so that one's
-        // latencies (barriers, shared memory, the fence) pass while the other works.
-        // Lane's 16-byte chunks: column chunk c of four of its warp's 16 rows.  The two
+        // Four groups of two warps, each with every fourth k-block, so that one's
+        // latencies (barriers, shared memory, the fence) pass while others work.
+        // Lane's 16-byte chunks: column chunk c of eight of its warp's 32 rows.  The two
         // rows that a group of eight lanes reads at a time differ by 5 in their low
         // three bits, which keeps both the reads (chunk c of row r at c ^ (r % 8)) and
         // the writes (pieces 2 (c % 4), + 1 at ^ (r % 8)) free of bank conflicts.
