@@ -11,9 +11,11 @@
 //   warp 1       MMA issuer (tcgen05.mma kind::mxf8f6f4, M = 128, N = NB, one CTA)
 //   warp 2       scales (as in rm_fp8_gemm.cu: words of four k-blocks' exponents)
 //   warp 3       TMA producer of x
-//   warps 4-7    epilogue: a thread owns one column n of all samples; an 8-bit
-//                output's block of 128 columns is the CTA's 128 threads, whose
-//                largest values meet in a warp maximum and 4 words of shared memory
+//   warps 4-7 (and 8-11 for 64 samples)  epilogue: a thread owns one column n of
+//                16 or 32 samples; an 8-bit output's block of 128 columns is four
+//                warps' threads, whose largest values meet in a warp maximum and
+//                four words of shared memory; one thread per sample then makes the
+//                scale that the others read
 // The kernel is launched while its predecessor may still run.  Where that
 // predecessor is one of this library's own launches of the same call, W was in
 // memory before it began, and warp 0 starts on it at once; everything else
@@ -31,8 +33,6 @@ namespace f8s {
 constexpr int BM = 128, BK = 128;
 constexpr int W_BYTES = BM * BK;
 constexpr int SF_SLOTS = 4, SF_BYTES = 1024;
-constexpr int EPI_WARPS = 4;
-constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr int TMEM_COLS = 256, SF_COL = 192;
 
 template <int NB>
@@ -41,7 +41,10 @@ struct Cfg {
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
     static constexpr int FIT = (200 * 1024) / STAGE_BYTES;
     static constexpr int STAGES = FIT < 12 ? FIT : 12;
-    static constexpr int RED_BYTES = 2 * 2 * EPI_WARPS * NB * 4;
+    static constexpr int EPI_WARPS = NB == 64 ? 8 : 4;
+    static constexpr int THREADS = 128 + 32 * EPI_WARPS;
+    static constexpr int SAMPLES = NB / (EPI_WARPS / 4);            // per epilogue thread
+    static constexpr int RED_BYTES = 2 * (4 + 1) * NB * 4;          // [output][warp of the block, then the scale][sample]
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SF_SLOTS * SF_BYTES + RED_BYTES + 512;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
     static_assert(2 * NB <= SF_COL, "two accumulators below the scales");
@@ -67,10 +70,10 @@ struct Args {
 };
 
 template <int EPI, bool TRANS, int NB>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Cfg<NB>::THREADS, 1)
 fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Args args) {
     using C = Cfg<NB>;
-    constexpr int STAGES = C::STAGES;
+    constexpr int STAGES = C::STAGES, EPI_WARPS = C::EPI_WARPS;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -85,7 +88,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + x); };
     auto tempty_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 2 + x); };
     const uint32_t meet_bar = bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 4);
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (meet_bar + 8u - base));
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (meet_bar + 16u - base));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -104,7 +107,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             mbar_init(tfull_bar(x), 1);
             mbar_init(tempty_bar(x), EPI_WARPS);
         }
-        mbar_init(meet_bar, EPI_WARPS);
+        for (int g = 0; g < 2; ++g) mbar_init(meet_bar + 8u * g, 4);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -253,36 +256,47 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         }
     } else {
         // ------------------------------ epilogue ----------------------------------
-        const int quad = warp & 3, tid = 32 * quad + lane;
+        constexpr int NS = C::SAMPLES;
+        const int quad = warp & 3, tid = 32 * quad + lane, group = (warp - 4) >> 2, j0 = NS * group;
+        const uint32_t meet_group = meet_bar + 8u * group;
         int acc = 0;
         uint32_t acc_phase = 0, meet = 0;
+        // the four warps of a block wait for one another
+        auto all_here = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(meet_group);
+            const bool ok = wait_bounded(meet_group, meet, abort_flag, args.err, args.timeout_ns);
+            meet ^= 1u;
+            return ok;
+        };
         for (int i = blockIdx.x; i < args.tiles; i += gridDim.x) {
             const int t = i / args.n_tiles, n0 = (i - t * args.n_tiles) * BM, n = n0 + tid;
             const float bias = args.bias && n < args.N ? __ldg(args.bias + (size_t)t * args.N + n) : 0.f;
             if (!wait_bounded(tfull_bar(acc), acc_phase, abort_flag, args.err, args.timeout_ns)) break;
             tc_fence_after();
-            uint32_t r[NB];
-            const uint32_t tcol = tmem_base + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * NB);
-            if constexpr (NB == 16) {
+            uint32_t r[NS];
+            const uint32_t tcol = tmem_base + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * NB + j0);
+            if constexpr (NS == 16)
                 tmem_ld16_nowait(tcol, r);
-            } else {
-#pragma unroll
-                for (int q = 0; q < NB / 32; ++q)
-                    tmem_ld32_nowait(tcol + 32u * q, reinterpret_cast<uint32_t(&)[32]>(r[32 * q]));
-            }
+            else
+                tmem_ld32_nowait(tcol, r);
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(tempty_bar(acc));
-            float v[NB];
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+            const int count = args.B - j0;               // samples of this thread that exist: the first `count` (may be <= 0)
+            const size_t row0 = (size_t)j0 * args.T + t;
+            float v[NS];
 #pragma unroll
-            for (int j = 0; j < NB; ++j) v[j] = __uint_as_float(r[j]) + bias;
+            for (int j = 0; j < NS; ++j) v[j] = __uint_as_float(r[j]) + bias;
             if constexpr (EPI == EPI_BF16 || EPI == EPI_F32) {
                 if (n < args.N) {
 #pragma unroll
-                    for (int j = 0; j < NB; ++j) {
-                        if (j < args.B) {
-                            const size_t at = ((size_t)j * args.T + t) * (size_t)args.N + n;
+                    for (int j = 0; j < NS; ++j) {
+                        if (j < count) {
+                            const size_t at = (row0 + (size_t)j * args.T) * (size_t)args.N + n;
                             if constexpr (EPI == EPI_BF16)
                                 reinterpret_cast<__nv_bfloat16*>(args.y)[at] = __float2bfloat16_rn(v[j]);
                             else
@@ -291,49 +305,47 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                     }
                 }
             } else {
-                // largest magnitude of each sample's 128 columns: [output][warp][sample], two sets
-                uint32_t* m_a = red + acc * (2 * EPI_WARPS * NB);
-                uint32_t* m_u = m_a + EPI_WARPS * NB;
-                float a[NB];
+                // one 8-bit output: the largest magnitudes of each sample's 128 columns meet,
+                // thread j makes sample j's scale, all round by it
+                auto save = [&](const Fp8View& out, float (&x)[NS], uint32_t* m) {
+                    uint32_t* scale = m + 4 * NB;
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    a[j] = gelu_erf(v[j]);
-                    const uint32_t ma = __reduce_max_sync(0xffffffffu, fp8_finite_bits(a[j]));
-                    if (lane == 0) m_a[quad * NB + j] = ma;
-                    if constexpr (EPI == EPI_GELU_KEEP) {
-                        const uint32_t mu = __reduce_max_sync(0xffffffffu, fp8_finite_bits(v[j]));
-                        if (lane == 0) m_u[quad * NB + j] = mu;
+                    for (int j = 0; j < NS; ++j) {
+                        const uint32_t a = __reduce_max_sync(0xffffffffu, fp8_finite_bits(x[j]));
+                        if (lane == 0) m[quad * NB + j0 + j] = a;
                     }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(meet_bar);
-                if (!wait_bounded(meet_bar, meet, abort_flag, args.err, args.timeout_ns)) break;
-                meet ^= 1u;
-                auto exponent = [&](const uint32_t* m, int j) {
-                    return fp8_exponent<false>(max(max(m[j], m[NB + j]), max(m[2 * NB + j], m[3 * NB + j])));
-                };
-                if (tid < NB && tid < args.B) {
-                    const size_t row = (size_t)tid * args.T + t;
-                    args.o0.scales[row * (size_t)args.o0.lds + n0 / kFp8Block] = (uint8_t)exponent(m_a, tid);
-                    if constexpr (EPI == EPI_GELU_KEEP)
-                        args.o1.scales[row * (size_t)args.o1.lds + n0 / kFp8Block] = (uint8_t)exponent(m_u, tid);
-                }
-                if (n < args.N) {
+                    if (!all_here()) return false;
+                    if (tid < NS) {
+                        const uint32_t* q = m + j0 + tid;
+                        const uint32_t E = fp8_exponent<false>(max(max(q[0], q[NB]), max(q[2 * NB], q[3 * NB])));
+                        scale[j0 + tid] = __float_as_uint(fp8_inv_scale(E));
+                        if (tid < count)
+                            out.scales[(row0 + (size_t)tid * args.T) * (size_t)out.lds + n0 / kFp8Block] = (uint8_t)E;
+                    }
+                    if (!all_here()) return false;
+                    if (n < args.N) {
+                        uint8_t* code = out.codes + row0 * (size_t)out.ld + n;
+                        const size_t step = (size_t)args.T * (size_t)out.ld;
 #pragma unroll
-                    for (int j = 0; j < NB; ++j) {
-                        if (j < args.B) {
-                            const size_t row = (size_t)j * args.T + t;
-                            args.o0.codes[row * (size_t)args.o0.ld + n] =
-                                (uint8_t)fp8_pack2<false>(fp8_poison(a[j]) * fp8_inv_scale(exponent(m_a, j)), 0.f);
-                            if constexpr (EPI == EPI_GELU_KEEP)
-                                args.o1.codes[row * (size_t)args.o1.ld + n] =
-                                    (uint8_t)fp8_pack2<false>(fp8_poison(v[j]) * fp8_inv_scale(exponent(m_u, j)), 0.f);
+                        for (int j = 0; j < NS; j += 4) {
+                            const uint4 sc = *reinterpret_cast<const uint4*>(scale + j0 + j);
+                            const uint32_t c = fp8_pack4<false>(fp8_poison(x[j]) * __uint_as_float(sc.x),
+                                                                fp8_poison(x[j + 1]) * __uint_as_float(sc.y),
+                                                                fp8_poison(x[j + 2]) * __uint_as_float(sc.z),
+                                                                fp8_poison(x[j + 3]) * __uint_as_float(sc.w));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (j + e < count) code[(size_t)(j + e) * step] = (uint8_t)(c >> (8 * e));
                         }
                     }
-                }
+                    return true;
+                };
+                if constexpr (EPI == EPI_GELU_KEEP)
+                    if (!save(args.o1, v, red + 5 * NB)) break;
+#pragma unroll
+                for (int j = 0; j < NS; ++j) v[j] = gelu_erf(v[j]);
+                if (!save(args.o0, v, red)) break;
             }
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1u;
         }
     }
 
@@ -350,7 +362,7 @@ cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const Args& a, int
     auto k = fp8_stream_kernel<EPI, TRANS, NB>;
     cudaError_t e = smem_attr_once((const void*)k, Cfg<NB>::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    return launch_k(k, dim3((unsigned)(a.tiles < num_sms ? a.tiles : num_sms)), dim3(THREADS), Cfg<NB>::SMEM_BYTES, s, mx, mw,
+    return launch_k(k, dim3((unsigned)(a.tiles < num_sms ? a.tiles : num_sms)), dim3(Cfg<NB>::THREADS), Cfg<NB>::SMEM_BYTES, s, mx, mw,
                     a);
 }
 
