@@ -365,36 +365,35 @@ class Fp8Tensor:
     __slots__ = ("cols", "c", "lead", "scale_lead", "device", "device_index", "_codes", "_scales", "_arena", "_at")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
-        cs, ss, fmt = codes.shape, scales.shape, _F8_CODE.get(codes.dtype)
-        if fmt is None or scales.dtype != torch.uint8:
+        cs, ss, fmt, d = codes.shape, scales.shape, _F8_CODE.get(codes.dtype), codes.get_device()
+        if fmt is None or scales.dtype is not torch.uint8:
             raise ValueError("codes must be float8_e4m3fn or float8_e5m2, scales uint8")
-        if len(cs) < 1 or len(cs) != len(ss) or codes.get_device() != scales.get_device():
+        if len(cs) < 1 or len(cs) != len(ss) or d != scales.get_device():
             raise ValueError("codes and scales must have the same rank and device")
-        if not 0 < cols <= cs[-1] or (cols + 127) // 128 > ss[-1]:
+        if not 0 < cols <= cs[-1] or cols > 128 * ss[-1]:
             raise ValueError(f"codes {tuple(cs)} and scales {tuple(ss)} do not hold {cols} columns")
-        self.cols, self._codes, self._scales = int(cols), codes, scales
-        self.lead, self.scale_lead, self.device_index = tuple(cs[:-1]), tuple(ss[:-1]), codes.get_device()
-        self.device, self._arena = codes.device, None
         self.c = _lib.rm_fp8_tensor(_ptr(codes), _ptr(scales), cs[-1], ss[-1], fmt)
+        self.cols, self._codes, self._scales, self._arena = cols, codes, scales, None
+        self.lead, self.scale_lead, self.device, self.device_index = cs[:-1], ss[:-1], codes.device, d
 
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
             n, ld = self._at, self.c.ld * math.prod(self.lead)
             fmt = _F8["e5m2" if self.c.format == _lib.RM_E5M2 else "e4m3"]
-            self._codes = self._arena[n:n + ld].view(fmt).view(self.lead + (self.c.ld,))
+            self._codes = self._arena[n:n + ld].view(fmt).view(*self.lead, self.c.ld)
         return self._codes
 
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is None:
             n, size = self.c.scales - self._arena.data_ptr(), self.c.lds * math.prod(self.scale_lead)
-            self._scales = self._arena[n:n + size].view(self.scale_lead + (self.c.lds,))
+            self._scales = self._arena[n:n + size].view(*self.scale_lead, self.c.lds)
         return self._scales
 
     @property
     def shape(self) -> tuple:
-        return self.lead + (self.cols,)
+        return (*self.lead, self.cols)
 
     @property
     def nbytes(self) -> int:
@@ -439,18 +438,20 @@ def _fp8_device(index: int, *others) -> int:
 
 def _fp8_activation(x: Fp8Tensor, what: str) -> tuple:
     """(B, T, cols) of 8-bit activations, with a scale row for every code row."""
-    if len(x.lead) != 2 or x.scale_lead != x.lead:
+    lead = x.lead
+    if len(lead) != 2 or x.scale_lead != lead:
         raise ValueError(f"{what} must be 8-bit activations [B, T, cols] with one row of scales per row, got rows "
-                         f"{x.lead}, rows of scales {x.scale_lead}")
-    return x.lead + (x.cols,)
+                         f"{tuple(lead)}, rows of scales {tuple(x.scale_lead)}")
+    return (*lead, x.cols)
 
 
 def _fp8_weight(w: Fp8Tensor, what: str) -> tuple:
     """(T, K, N) of an 8-bit weight."""
-    if len(w.lead) != 2 or w.scale_lead != (w.lead[0], (w.lead[1] + 127) // 128):
+    lead = w.lead
+    if len(lead) != 2 or w.scale_lead != (lead[0], (lead[1] + 127) // 128):
         raise ValueError(f"{what} must be an 8-bit weight [T, K, N] with one row of scales per 128 rows, got rows "
-                         f"{w.lead}, rows of scales {w.scale_lead}")
-    return w.lead + (w.cols,)
+                         f"{tuple(lead)}, rows of scales {tuple(w.scale_lead)}")
+    return (*lead, w.cols)
 
 
 def fp8_quantize(X: torch.Tensor, fmt: str = "e4m3") -> Fp8Tensor:
@@ -491,7 +492,7 @@ def fp8_dequantize(q: Fp8Tensor, dtype: str = "bf16") -> torch.Tensor:
     if q.scale_lead != q.lead:
         raise ValueError("fp8_dequantize takes rows with their own scales (activations)")
     tdt, code = _DTYPES[dtype]
-    Y = torch.empty(q.lead + (q.cols,), dtype=tdt, device=q.device)
+    Y = torch.empty((*q.lead, q.cols), dtype=tdt, device=q.device)
     _lib.rm_fp8_dequantize(q.c, math.prod(q.lead), q.cols, Y.data_ptr(), code, q.cols, _raw_stream(d))
     return Y
 

@@ -134,30 +134,36 @@ __device__ __forceinline__ uint4 staged16(uint32_t stage, int row, int c) {
 
 // The staged 32 rows to memory: row r at dst + r pitch, the first `rows` of them,
 // of each the first `bytes` (whole 16-byte pieces when VEC, else elements of ESZ
-// bytes).  Four lanes write a row's 64 bytes.  Plain stores: the staging is free
-// again after a warp barrier, where a bulk copy's reads would be waited for.
+// bytes, neighbouring lanes neighbouring elements).  Plain stores: the staging is
+// free again after a warp barrier, where a bulk copy's reads would be waited for.
 template <bool VEC, int ESZ>
 __device__ __forceinline__ void store_rows(uint32_t stage, char* dst, size_t pitch, int rows, int bytes, int lane) {
     __syncwarp();
-    const int c = lane & 3;
+    if (VEC) {
+        const int c = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 2);
-        if (r < rows && 16 * c < bytes) {
-            const uint4 v = staged16(stage, r, c);
-            char* p = dst + (size_t)r * pitch + 16 * c;
-            if (VEC) {
-                *reinterpret_cast<uint4*>(p) = v;
-            } else {
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 16 / ESZ; ++e)
-                    if (16 * c + ESZ * e < bytes) {
-                        if (ESZ == 2)
-                            *reinterpret_cast<uint16_t*>(p + 2 * e) = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-                        else
-                            *reinterpret_cast<uint32_t*>(p + 4 * e) = w[e];
-                    }
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
+            if (r < rows && 16 * c < bytes)
+                *reinterpret_cast<uint4*>(dst + (size_t)r * pitch + 16 * c) = staged16(stage, r, c);
+        }
+    } else {
+        constexpr int PER = 64 / ESZ;              // elements of a row's 64 bytes
+        const int at = ESZ * (lane % PER);
+#pragma unroll 4
+        for (int r = lane / PER; r < rows; r += 32 / PER) {
+            const uint32_t src = staged_at(stage, r, at >> 4) + (at & 15);
+            if (at < bytes) {
+                char* p = dst + (size_t)r * pitch + at;
+                if (ESZ == 2) {
+                    uint16_t v;
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(src));
+                    *reinterpret_cast<uint16_t*>(p) = v;
+                } else {
+                    uint32_t v;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(src));
+                    *reinterpret_cast<uint32_t*>(p) = v;
+                }
             }
         }
     }
