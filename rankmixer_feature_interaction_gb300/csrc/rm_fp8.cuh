@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "rm_common.cuh"
 #include "rm_fp8.h"
 
 namespace rm {
@@ -65,6 +66,35 @@ __device__ __forceinline__ uint32_t fp8_finite_bits(float x) {
 // Infinities become NaN (the code for both).
 __device__ __forceinline__ float fp8_poison(float x) {
     return (__float_as_uint(x) & 0x7fffffffu) < 0x7f800000u ? x : __uint_as_float(0x7fc00000u);
+}
+
+// Gelu(u) = u Phi(u) and Gelu'(u) = Phi(u) + u phi(u) by Abramowitz & Stegun
+// 7.1.26 (|error of erf| <= 1.5e-7), as gelu_erf in rm_common.cuh, written for
+// the epilogues that hold a whole row in registers: one value at a time, every
+// constant an immediate of its instruction.  (The packed two-value form needs
+// each constant in a register pair; with 64 values held there is no room for
+// them, and moving them in costs more than the packing saves: 25 against 19
+// instructions per value of a rounded and kept GELU.)
+// The upper tail Q(|u|) = 1 - Phi(|u|) = t (h1 + t (h2 + ... )) exp(-u^2 / 2),
+// t = 1 / (1 + (p / sqrt 2) |u|), h_i = a_i / 2.
+__device__ __forceinline__ float gelu_tail(float u, float& e) {
+    const float t = rcp_approx(fmaf(fabsf(u), 0.23164189f, 1.0f));
+    float q = fmaf(t, 0.5307027145f, -0.7265760135f);
+    q = fmaf(t, q, 0.7107068705f);
+    q = fmaf(t, q, -0.142248368f);
+    q = fmaf(t, q, 0.127414796f);
+    e = ex2_approx(u * u * -0.72134752f);          // log2(e) / 2
+    return q * t * e;
+}
+__device__ __forceinline__ float fp8_gelu(float u) {
+    float e;
+    const float Q = gelu_tail(u, e);
+    return fmaf(-fabsf(u), Q, fmaxf(u, 0.f));
+}
+__device__ __forceinline__ float fp8_gelu_grad(float u) {
+    float e;
+    const float Q = gelu_tail(u, e);
+    return fmaf(u * 0.39894228f, e, 0.5f + copysignf(0.5f - Q, u));   // phi(u) = e / sqrt(2 pi)
 }
 
 }  // namespace rm

@@ -36,7 +36,6 @@
 
 #include "rm_fp8.cuh"
 #include "rm_fp8_tc.cuh"
-#include "rm_train_math.cuh"
 
 namespace rm {
 namespace f8 {
@@ -144,17 +143,14 @@ __device__ __forceinline__ bool block_amax(float (&v)[COLS], Partner& p, int whi
 __device__ __forceinline__ void save_row(const float (&v)[COLS], float amax, const Fp8View& out, const Args& a, int t,
                                          int m_warp, int n, int rows, int lane, uint32_t stage) {
     const uint32_t E = fp8_exponent<false>(__float_as_uint(amax));
-    const uint64_t s = f2_splat(fp8_inv_scale(E));
+    const float s = fp8_inv_scale(E);
 #pragma unroll
     for (int c = 0; c < COLS / 16; ++c) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int i = 16 * c + 4 * j;
-            float q[4];
-            f2_unpack(f2_mul(f2_pack(v[i], v[i + 1]), s), q[0], q[1]);
-            f2_unpack(f2_mul(f2_pack(v[i + 2], v[i + 3]), s), q[2], q[3]);
-            w[j] = fp8_pack4<false>(q[0], q[1], q[2], q[3]);
+            w[j] = fp8_pack4<false>(v[i] * s, v[i + 1] * s, v[i + 2] * s, v[i + 3] * s);
         }
         st_shared_v4(staged_at(stage, lane, c), w[0], w[1], w[2], w[3]);
     }
@@ -192,19 +188,16 @@ template <int EPI>
 __device__ __forceinline__ bool epilogue(float (&v)[COLS], const Args& a, const Tile& tl, int m_warp, int n, int lane,
                                          uint32_t stage, Partner& partner) {
     const int rows = n < a.N ? min(32, a.B - m_warp) : 0;        // this warp's rows that exist (may be negative)
-    if (EPI != EPI_DGELU && a.bias) {
-        const float* b = a.bias + (size_t)tl.t * a.N + n;
-        if (n + COLS <= a.N && (a.N & 3) == 0) {
+    if (EPI != EPI_DGELU && a.bias) {                  // brought to the staging before the tile was waited for
 #pragma unroll
-            for (int i = 0; i < COLS / 4; ++i) {
-                const float4 q = __ldg(reinterpret_cast<const float4*>(b) + i);
-                v[4 * i] += q.x, v[4 * i + 1] += q.y, v[4 * i + 2] += q.z, v[4 * i + 3] += q.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < COLS; ++i)
-                if (n + i < a.N) v[i] += __ldg(b + i);
+        for (int i = 0; i < COLS / 4; ++i) {
+            float4 q;
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
+                         : "r"(stage + 16u * i));
+            v[4 * i] += q.x, v[4 * i + 1] += q.y, v[4 * i + 2] += q.z, v[4 * i + 3] += q.w;
         }
+        __syncwarp();
     }
     if constexpr (EPI == EPI_BF16) {
 #pragma unroll
@@ -220,10 +213,7 @@ __device__ __forceinline__ bool epilogue(float (&v)[COLS], const Args& a, const 
             save_row(v, m, a.o1, a, tl.t, m_warp, n, rows, lane, stage);
         }
 #pragma unroll
-        for (int i = 0; i < COLS / 2; ++i) {
-            const uint64_t g = gelu_erf_x2(f2_pack(v[2 * i], v[2 * i + 1]), 0ull);
-            f2_unpack(g, v[2 * i], v[2 * i + 1]);
-        }
+        for (int i = 0; i < COLS; ++i) v[i] = fp8_gelu(v[i]);
         float m;
         if (!block_amax(v, partner, 0, a, lane, m)) return false;
         save_row(v, m, a.o0, a, tl.t, m_warp, n, rows, lane, stage);
@@ -240,7 +230,6 @@ __device__ __forceinline__ bool epilogue(float (&v)[COLS], const Args& a, const 
 
 // v *= Gelu'(u), u the row's 64 codes in shared memory times their scale.
 __device__ __forceinline__ void times_gelu_grad(float (&v)[COLS], uint32_t codes, float scale, int lane) {
-    const uint64_t s = f2_splat(scale);
 #pragma unroll
     for (int c = 0; c < COLS / 16; ++c) {
         const uint4 q = staged16(codes, lane, c);
@@ -248,10 +237,9 @@ __device__ __forceinline__ void times_gelu_grad(float (&v)[COLS], uint32_t codes
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float2 f = fp8_unpack2<false>(w[j >> 1] >> (16 * (j & 1)));
-            uint64_t val, grad;
-            gelu_with_grad_x2(f2_pack(f.x, f.y), s, 0ull, val, grad);
             const int i = 16 * c + 2 * j;
-            f2_unpack(f2_mul(f2_pack(v[i], v[i + 1]), grad), v[i], v[i + 1]);
+            v[i] *= fp8_gelu_grad(f.x * scale);
+            v[i + 1] *= fp8_gelu_grad(f.y * scale);
         }
     }
 }
@@ -495,6 +483,15 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
         for (long long i = unit; i < args.tiles; i += nunits) {
             const Tile tl = tile_of(i, args);
             const int m_warp = tl.m0 + BM * (int)rank + 32 * quad, n = tl.n0 + COLS * part;
+            if (EPI != EPI_DGELU && args.bias) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c = n + 32 * h + lane;
+                    const float b = c < args.N ? __ldg(args.bias + (size_t)tl.t * args.N + c) : 0.f;
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage + 128u * h + 4u * lane), "f"(b) : "memory");
+                }
+                __syncwarp();
+            }
             if (!wait_bounded(tfull_bar(acc), phase, abort_flag, args.err, args.timeout_ns)) break;
             tc_fence_after();
             // A thread's columns come out at once, so the accumulator is free again long

@@ -343,7 +343,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 if constexpr (EPI == EPI_GELU_KEEP)
                     if (!save(args.o1, v, red + 5 * NB)) break;
 #pragma unroll
-                for (int j = 0; j < NS; ++j) v[j] = gelu_erf(v[j]);
+                for (int j = 0; j < NS; ++j) v[j] = fp8_gelu(v[j]);
                 if (!save(args.o0, v, red)) break;
             }
         }
