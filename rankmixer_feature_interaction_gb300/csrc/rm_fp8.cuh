@@ -68,33 +68,43 @@ __device__ __forceinline__ float fp8_poison(float x) {
     return (__float_as_uint(x) & 0x7fffffffu) < 0x7f800000u ? x : __uint_as_float(0x7fc00000u);
 }
 
-// Gelu(u) = u Phi(u) and Gelu'(u) = Phi(u) + u phi(u) by Abramowitz & Stegun
-// 7.1.26 (|error of erf| <= 1.5e-7), as gelu_erf in rm_common.cuh, written for
-// the epilogues that hold a whole row in registers: one value at a time, every
-// constant an immediate of its instruction.  (The packed two-value form needs
-// each constant in a register pair; with 64 values held there is no room for
-// them, and moving them in costs more than the packing saves: 25 against 19
-// instructions per value of a rounded and kept GELU.)
-// The upper tail Q(|u|) = 1 - Phi(|u|) = t (h1 + t (h2 + ... )) exp(-u^2 / 2),
-// t = 1 / (1 + (p / sqrt 2) |u|), h_i = a_i / 2.
-__device__ __forceinline__ float gelu_tail(float u, float& e) {
-    const float t = rcp_approx(fmaf(fabsf(u), 0.23164189f, 1.0f));
-    float q = fmaf(t, 0.5307027145f, -0.7265760135f);
+// Largest of three (one instruction).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Gelu(u) = u Phi(u) for the epilogues that hold a row in registers, written as
+// relu(u) - |u| Q(|u|) with the upper tail Q = 1 - Phi.  Q is positive and its
+// logarithm nearly a parabola, so one exponential of a polynomial gives it,
+// Q(x) = 2^P(x): P of degree 6 fitted to log2 Q over [0, 6] for the smallest
+// largest error in Q (a linear program, weights Q ln 2), 1.1e-7; above 6, where
+// Q < 1e-9, x is held at 6.  In float32 the result is within 1.9e-7 |u|.  Ten
+// instructions, every constant an immediate of its own (the rational form needs
+// a reciprocal and an exponential; the packed two-value form needs constants in
+// register pairs, for which 64 held values leave no room).
+__device__ __forceinline__ float fp8_gelu(float u) {
+    const float x = fminf(fabsf(u), 6.0f);
+    float p = fmaf(x, 1.91779014e-05f, -6.58627096e-04f);
+    p = fmaf(x, p, 7.75446597e-03f);
+    p = fmaf(x, p, -5.29654577e-02f);
+    p = fmaf(x, p, -4.59060221e-01f);
+    p = fmaf(x, p, -1.15112206f);
+    p = fmaf(x, p, -9.99999693e-01f);
+    return fmaf(-fabsf(u), ex2_approx(p), fmaxf(u, 0.f));
+}
+
+// Gelu'(u) = Phi(u) + u phi(u), by Abramowitz & Stegun 7.1.26 (|error of erf| <=
+// 1.5e-7) as in rm_common.cuh, with phi(u) = exp(-u^2 / 2) / sqrt(2 pi).
+__device__ __forceinline__ float fp8_gelu_grad(float u) {
+    const float t = rcp_approx(fmaf(fabsf(u), 0.23164189f, 1.0f));   // p / sqrt 2
+    float q = fmaf(t, 0.5307027145f, -0.7265760135f);                // a_i / 2
     q = fmaf(t, q, 0.7107068705f);
     q = fmaf(t, q, -0.142248368f);
     q = fmaf(t, q, 0.127414796f);
-    e = ex2_approx(u * u * -0.72134752f);          // log2(e) / 2
-    return q * t * e;
-}
-__device__ __forceinline__ float fp8_gelu(float u) {
-    float e;
-    const float Q = gelu_tail(u, e);
-    return fmaf(-fabsf(u), Q, fmaxf(u, 0.f));
-}
-__device__ __forceinline__ float fp8_gelu_grad(float u) {
-    float e;
-    const float Q = gelu_tail(u, e);
-    return fmaf(u * 0.39894228f, e, 0.5f + copysignf(0.5f - Q, u));   // phi(u) = e / sqrt(2 pi)
+    const float e = ex2_approx(u * u * -0.72134752f);                // log2(e) / 2
+    return fmaf(u * 0.39894228f, e, 0.5f + copysignf(0.5f - q * t * e, u));
 }
 
 }  // namespace rm

@@ -61,13 +61,16 @@ constexpr int REGS_OTHER = 56, REGS_EPI = 104;
 enum Epi { EPI_BF16, EPI_F32, EPI_GELU, EPI_GELU_KEEP, EPI_DGELU };
 
 // Shared memory: the stages, 2 KB of staging per epilogue warp, the scale slots;
-// for DGELU 2 KB more per epilogue warp for the next tile's kept u, and a stage less.
+// for DGELU 2 KB more per epilogue warp for the next tile's kept u and the table of
+// Gelu', and a stage less.
+constexpr int TAB_LO = 127 - 33, TAB_ROWS = 38, TAB_BYTES = TAB_ROWS * 128 * 4;
 template <int EPI>
 struct Cfg {
     static constexpr int STAGES = EPI == EPI_DGELU ? 4 : 5;
     static constexpr int U_BYTES = EPI == EPI_DGELU ? EPI_WARPS * STAGING : 0;
+    static constexpr int TAB = EPI == EPI_DGELU ? TAB_BYTES : 0;
     static constexpr int SMEM_BYTES =
-        1024 + STAGES * STAGE_BYTES + EPI_WARPS * STAGING + U_BYTES + SF_SLOTS * SF_BYTES + RED_BYTES + 512;
+        1024 + STAGES * STAGE_BYTES + EPI_WARPS * STAGING + U_BYTES + SF_SLOTS * SF_BYTES + RED_BYTES + TAB + 512;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 
@@ -117,10 +120,10 @@ struct Partner {
 // Largest magnitude of the row's block, this thread's half and its partner's;
 // passes over NaN.  False when the wait ran out.
 __device__ __forceinline__ float half_amax(const float (&v)[COLS]) {
-    float m[4] = {};
+    float m[2] = {};
 #pragma unroll
-    for (int i = 0; i < COLS; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(v[i]));
-    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    for (int i = 0; i < COLS; i += 2) m[i >> 1 & 1] = max3(m[i >> 1 & 1], fabsf(v[i]), fabsf(v[i + 1]));
+    return fmaxf(m[0], m[1]);
 }
 __device__ __forceinline__ bool block_amax(float (&v)[COLS], Partner& p, int which, const Args& a, int lane, float& amax) {
     float m = half_amax(v);
@@ -143,14 +146,17 @@ __device__ __forceinline__ bool block_amax(float (&v)[COLS], Partner& p, int whi
 __device__ __forceinline__ void save_row(const float (&v)[COLS], float amax, const Fp8View& out, const Args& a, int t,
                                          int m_warp, int n, int rows, int lane, uint32_t stage) {
     const uint32_t E = fp8_exponent<false>(__float_as_uint(amax));
-    const float s = fp8_inv_scale(E);
+    const uint64_t s = f2_splat(fp8_inv_scale(E));
 #pragma unroll
     for (int c = 0; c < COLS / 16; ++c) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int i = 16 * c + 4 * j;
-            w[j] = fp8_pack4<false>(v[i] * s, v[i + 1] * s, v[i + 2] * s, v[i + 3] * s);
+            float q[4];
+            f2_unpack(f2_mul(f2_pack(v[i], v[i + 1]), s), q[0], q[1]);
+            f2_unpack(f2_mul(f2_pack(v[i + 2], v[i + 3]), s), q[2], q[3]);
+            w[j] = fp8_pack4<false>(q[0], q[1], q[2], q[3]);
         }
         st_shared_v4(staged_at(stage, lane, c), w[0], w[1], w[2], w[3]);
     }
@@ -195,7 +201,8 @@ __device__ __forceinline__ bool epilogue(float (&v)[COLS], const Args& a, const 
             asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                          : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
                          : "r"(stage + 16u * i));
-            v[4 * i] += q.x, v[4 * i + 1] += q.y, v[4 * i + 2] += q.z, v[4 * i + 3] += q.w;
+            f2_unpack(f2_add(f2_pack(v[4 * i], v[4 * i + 1]), f2_pack(q.x, q.y)), v[4 * i], v[4 * i + 1]);
+            f2_unpack(f2_add(f2_pack(v[4 * i + 2], v[4 * i + 3]), f2_pack(q.z, q.w)), v[4 * i + 2], v[4 * i + 3]);
         }
         __syncwarp();
     }
@@ -228,18 +235,46 @@ __device__ __forceinline__ bool epilogue(float (&v)[COLS], const Args& a, const 
     return true;
 }
 
-// v *= Gelu'(u), u the row's 64 codes in shared memory times their scale.
-__device__ __forceinline__ void times_gelu_grad(float (&v)[COLS], uint32_t codes, float scale, int lane) {
+// Gelu'(u) of a kept u depends on 8 bits and an exponent, so a table in shared
+// memory holds it: Gelu'(u) - 1/2, an odd function, for the 128 magnitudes under
+// every exponent byte from TAB_LO on, built once by each CTA.  Below TAB_LO |u| is
+// so small that the lowest row is right to 4e-8; blocks above the last row (|u|
+// up to 7168) are computed.  Seven instructions a value where the formula takes 18.
+__device__ __forceinline__ void build_table(float* tab, int i, int n) {
+    for (; i < TAB_ROWS * 128; i += n)
+        tab[i] = fp8_gelu_grad(fp8_unpack2<false>((uint32_t)i & 127u).x * fp8_scale(TAB_LO + (i >> 7))) - 0.5f;
+}
+
+// v *= Gelu'(u), u the row's 64 codes in shared memory under exponent byte E.
+__device__ __forceinline__ void times_gelu_grad(float (&v)[COLS], uint32_t codes, uint32_t E, uint32_t tab, int lane) {
+    if (E < TAB_LO + TAB_ROWS) {
+        const uint32_t row = tab + 512u * (max(E, (uint32_t)TAB_LO) - TAB_LO);
 #pragma unroll
-    for (int c = 0; c < COLS / 16; ++c) {
-        const uint4 q = staged16(codes, lane, c);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        for (int c = 0; c < COLS / 16; ++c) {
+            const uint4 q = staged16(codes, lane, c);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 f = fp8_unpack2<false>(w[j >> 1] >> (16 * (j & 1)));
-            const int i = 16 * c + 2 * j;
-            v[i] *= fp8_gelu_grad(f.x * scale);
-            v[i + 1] *= fp8_gelu_grad(f.y * scale);
+            for (int j = 0; j < 16; ++j) {
+                const uint32_t x = w[j >> 2];
+                const int k = 8 * (j & 3);
+                uint32_t h;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(h) : "r"(row + ((k ? x >> (k - 2) : x << 2) & 0x1fcu)));
+                const float g = __uint_as_float(h ^ (x << (24 - k) & 0x80000000u));
+                v[16 * c + j] = fmaf(v[16 * c + j], g, 0.5f * v[16 * c + j]);
+            }
+        }
+    } else {
+        const float scale = fp8_scale(E);
+#pragma unroll
+        for (int c = 0; c < COLS / 16; ++c) {
+            const uint4 q = staged16(codes, lane, c);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 f = fp8_unpack2<false>(w[j >> 1] >> (16 * (j & 1)));
+                v[16 * c + 2 * j] *= fp8_gelu_grad(f.x * scale);
+                v[16 * c + 2 * j + 1] *= fp8_gelu_grad(f.y * scale);
+            }
         }
     }
 }
@@ -257,7 +292,8 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     const uint32_t sEpi = base + STAGES * STAGE_BYTES;
     const uint32_t sU = sEpi + EPI_WARPS * STAGING, sSF = sU + Cfg<EPI>::U_BYTES;
     float* red = reinterpret_cast<float*>(base_ptr + (sSF - base) + SF_SLOTS * SF_BYTES);
-    const uint32_t bar0 = sSF + SF_SLOTS * SF_BYTES + RED_BYTES;
+    float* tab = red + RED_BYTES / 4;
+    const uint32_t bar0 = sSF + SF_SLOTS * SF_BYTES + RED_BYTES + Cfg<EPI>::TAB;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
     auto sfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
@@ -299,6 +335,8 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
         tmem_alloc_pair(smem_u32(tmem_holder), 512);
         tmem_relinquish_pair();
     }
+    if constexpr (EPI == EPI_DGELU)
+        if (warp >= 4) build_table(tab, threadIdx.x - 128, 32 * EPI_WARPS);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -479,7 +517,9 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             if (m + lane < args.B && n < args.N)
                 u_next = __ldg(args.o1.scales + ((size_t)(m + lane) * args.T + tl.t) * (size_t)args.o1.lds + n / kFp8Block);
         };
-        if (EPI == EPI_DGELU && unit < args.tiles) fetch_u(unit);
+        if constexpr (EPI == EPI_DGELU) {
+            if (unit < args.tiles) fetch_u(unit);
+        }
         for (long long i = unit; i < args.tiles; i += nunits) {
             const Tile tl = tile_of(i, args);
             const int m_warp = tl.m0 + BM * (int)rank + 32 * quad, n = tl.n0 + COLS * part;
@@ -515,7 +555,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             if constexpr (EPI == EPI_DGELU) {
                 if (!wait_bounded(ub, uphase, abort_flag, args.err, args.timeout_ns)) break;
                 uphase ^= 1u;
-                times_gelu_grad(v, u_codes, fp8_scale(u_next), lane);
+                times_gelu_grad(v, u_codes, u_next, smem_u32(tab), lane);
                 __syncwarp();
                 if (i + nunits < args.tiles) fetch_u(i + nunits);
             }
