@@ -296,7 +296,8 @@ def code_step(v, scales, cols):
 
 
 FFN_SIZES = [(1, 1, 16, 16), (3, 2, 128, 256), (8, 4, 256, 1024), (40, 3, 208, 416), (100, 2, 384, 640), (129, 1, 256, 272),
-             (250, 2, 512, 1536), (300, 3, 144, 400), (1, 32, 256, 512)]
+             (250, 2, 512, 1536), (300, 3, 144, 400), (1, 32, 256, 512), (16, 1, 128, 400), (17, 3, 272, 128),
+             (32, 2, 640, 144), (33, 1, 16, 256), (64, 2, 400, 528), (65, 2, 128, 128), (257, 1, 528, 272)]
 # the hidden GELU is within 5e-7 |u| of the exact one (Abramowitz & Stegun 7.1.26: 1.5e-7 in erf; a reciprocal and a
 # power of two of 2^-22 each; float32 steps), its derivative within 1e-6 (1 + |u|)
 GELU_ERR, GRAD_ERR = 5e-7, 1e-6
@@ -369,6 +370,55 @@ def _scales(x):
     n = x.shape[-1]
     v = torch.nn.functional.pad(x, (0, -n % 128)).reshape(x.shape[:-1] + (-1, 128)).abs().amax(-1)
     return (ref.exponent(v, "e4m3") + 127).to(torch.uint8)
+
+
+@pytest.mark.parametrize("B", [6, 40, 300])
+def test_pffn_with_hidden_values_of_any_size(B):
+    """Hidden pre-activations from 1e-12 to 1e9 (rows of any exponent, far above and below where GELU bends), rows of
+    zeros and a row with a NaN: kept values, outputs and gradients follow the formulas, and the NaN stays in its row."""
+    T, D, F = 2, 128, 384
+    m = ffn(T, D, F, 70)
+    m.b1.zero_()
+    size = torch.logspace(-12, 9, B).reshape(B, 1, 1)
+    X = (rows((B, T, D), 73, 0.0) * size).to(DEV)
+    X[2] = 0
+    X[1, 1, 5] = float("nan")
+    V, kept = m.forward_train(X, "f32")
+    dV = rows((B, T, D), 74, 0.5).to(torch.bfloat16).to(DEV)
+    dX, _ = m.backward(dV, kept, "f32")
+    bad = torch.zeros((B, T, 1), dtype=torch.bool, device=DEV)
+    bad[1, 1] = True
+    assert torch.equal(V.isnan(), bad.expand(B, T, D)) and torch.equal(dX.isnan(), bad.expand(B, T, D))
+    fine = ~bad[..., 0]
+    xv, uv, av = (ref.value(kept[k]) for k in "xua")
+    w1, w2 = ref.weight_value(m.W1), ref.weight_value(m.W2)
+    zero = torch.zeros((), dtype=torch.float64, device=DEV)
+    xv = torch.where(bad, zero, xv)
+    u, us = ref.matmul(xv, w1), ref.matmul(xv.abs(), w1.abs())
+    uerr = ref.sum_bound(D, us)
+    within(uv[fine], u[fine], (uerr + code_step(u.abs() + uerr, kept["u"].scales, F))[fine], "kept u")
+    a, aerr = ref.gelu(u), 1.13 * uerr + GELU_ERR * u.abs() + 1e-30
+    within(av[fine], a[fine], (aerr + code_step(a.abs() + aerr, kept["a"].scales, F))[fine], "kept a")
+    av, uv = torch.where(bad, zero, av), torch.where(bad, zero, uv)
+    want, vs = ref.matmul(av, w2), ref.matmul(av.abs(), w2.abs())
+    within(V[fine], (want + m.b2.double())[fine], ref.sum_bound(F + 1, vs + m.b2.double().abs())[fine], "V")
+    dv8 = ref.rounded(dV.double())
+    da, das = ref.matmul(dv8, w2.transpose(1, 2)), ref.matmul(dv8.abs(), w2.abs().transpose(1, 2))
+    # beyond |u| = 10 the derivative is 0 or 1 to 1e-21: its formula in float64 would be inf * 0 far out
+    slope = ref.gelu_grad(uv.clamp(-30, 30))
+    du, duerr = da * slope, ref.sum_bound(D, das) * 1.13 + GRAD_ERR * (1 + uv.abs().clamp(max=30)) * da.abs()
+    step = duerr + 2 * code_step(du.abs() + duerr, _scales(du), F)
+    dxw = w1.transpose(1, 2)
+    tol = ref.matmul(step, dxw.abs()) + ref.sum_bound(F, ref.matmul(du.abs() + step, dxw.abs()))
+    within(dX[fine], ref.matmul(du, dxw)[fine], tol[fine], "dX")
+    ok()
+
+
+def test_the_example_learns():
+    from examples.pffn_8bit import train
+    r = train(B=300, T=4, D=128, k=2, steps=60)
+    assert r["last"] < 0.5 * r["first"], r
+    assert r["kept_bytes"] < 0.52 * r["bytes_in_16_bits"]
 
 
 def test_pffn_gradients_against_differences():
