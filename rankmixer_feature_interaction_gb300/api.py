@@ -362,7 +362,7 @@ class Fp8Tensor:
     row count) and one exponent byte E per 128 values of a row, scales [.., lds] (uint8); for a
     weight [T, K, N] one per 128 x 128 values, scales [T, ceil(K / 128), lds].  A value is
     code * 2^(E - 127).  ld is a multiple of 16, lds of 4; both tensors contiguous."""
-    __slots__ = ("cols", "c", "lead", "scale_lead", "device", "device_index", "_codes", "_scales", "_arena", "_at")
+    __slots__ = ("cols", "c", "cs", "ss", "device", "device_index", "_codes", "_scales", "_arena")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
         cs, ss, fmt, d = codes.shape, scales.shape, _F8_CODE.get(codes.dtype), codes.get_device()
@@ -372,44 +372,47 @@ class Fp8Tensor:
             raise ValueError("codes and scales must have the same rank and device")
         if not 0 < cols <= cs[-1] or cols > 128 * ss[-1]:
             raise ValueError(f"codes {tuple(cs)} and scales {tuple(ss)} do not hold {cols} columns")
-        self.c = _lib.rm_fp8_tensor(_ptr(codes), _ptr(scales), cs[-1], ss[-1], fmt)
-        self.cols, self._codes, self._scales, self._arena = cols, codes, scales, None
-        self.lead, self.scale_lead, self.device, self.device_index = cs[:-1], ss[:-1], codes.device, d
+        if not (codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError("tensors passed to librankmixer must be contiguous")
+        self.c = _lib.rm_fp8_tensor(codes.data_ptr(), scales.data_ptr(), cs[-1], ss[-1], fmt)
+        self.cols, self.cs, self.ss, self.device, self.device_index = cols, cs, ss, codes.device, d
+        self._codes, self._scales, self._arena = codes, scales, None
 
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
-            n, ld = self._at, self.c.ld * math.prod(self.lead)
+            at = self.c.codes - self._arena.data_ptr()
             fmt = _F8["e5m2" if self.c.format == _lib.RM_E5M2 else "e4m3"]
-            self._codes = self._arena[n:n + ld].view(fmt).view(*self.lead, self.c.ld)
+            self._codes = self._arena[at:at + math.prod(self.cs)].view(fmt).view(self.cs)
         return self._codes
 
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is None:
-            n, size = self.c.scales - self._arena.data_ptr(), self.c.lds * math.prod(self.scale_lead)
-            self._scales = self._arena[n:n + size].view(*self.scale_lead, self.c.lds)
+            at = self.c.scales - self._arena.data_ptr()
+            self._scales = self._arena[at:at + math.prod(self.ss)].view(self.ss)
         return self._scales
 
     @property
     def shape(self) -> tuple:
-        return (*self.lead, self.cols)
+        return (*self.cs[:-1], self.cols)
 
     @property
     def nbytes(self) -> int:
-        return self.c.ld * math.prod(self.lead) + self.c.lds * math.prod(self.scale_lead)
+        return math.prod(self.cs) + math.prod(self.ss)
 
 
 @functools.lru_cache(maxsize=256)
 def _fp8_layout(wanted: tuple) -> tuple:
     """Where the parts of 8-bit tensors (lead, cols, format, lead of the scales) lie in one
-    allocation: (its bytes, [(codes, scales, ld, lds)]), each part 256-byte aligned."""
+    allocation: (its bytes, [(codes, scales, shape of codes, shape of scales)]), each part
+    256-byte aligned."""
     at, places = 0, []
     for lead, cols, fmt, scale_lead in wanted:
-        ld, lds = (cols + 15) // 16 * 16, (cols + 511) // 512 * 4
-        scales = at + (math.prod(lead) * ld + 255) // 256 * 256
-        places.append((at, scales, ld, lds))
-        at = scales + (math.prod(scale_lead) * lds + 255) // 256 * 256
+        cs, ss = (*lead, (cols + 15) // 16 * 16), (*scale_lead, (cols + 511) // 512 * 4)
+        scales = at + (math.prod(cs) + 255) // 256 * 256
+        places.append((at, scales, cs, ss))
+        at = scales + (math.prod(ss) + 255) // 256 * 256
     return at, places
 
 
@@ -418,40 +421,39 @@ def _fp8_new(wanted: tuple, device: torch.device, index: int) -> list:
     size, places = _fp8_layout(wanted)
     arena = torch.empty(size, dtype=torch.uint8, device=device)
     base, out = arena.data_ptr(), []
-    for (lead, cols, fmt, scale_lead), (codes, scales, ld, lds) in zip(wanted, places):
+    for (_, cols, fmt, _), (codes, scales, cs, ss) in zip(wanted, places):
         q = object.__new__(Fp8Tensor)
-        q.cols, q.lead, q.scale_lead, q.device, q.device_index = cols, lead, scale_lead, device, index
-        q._codes = q._scales = None
-        q._arena, q._at = arena, codes
-        q.c = _lib.rm_fp8_tensor(base + codes, base + scales, ld, lds, fmt)
+        q.c = _lib.rm_fp8_tensor(base + codes, base + scales, cs[-1], ss[-1], fmt)
+        q.cols, q.cs, q.ss, q.device, q.device_index = cols, cs, ss, device, index
+        q._codes, q._scales, q._arena = None, None, arena
         out.append(q)
     return out
 
 
-def _fp8_device(index: int, *others) -> int:
+def _fp8_device(*indices) -> int:
     """The current device, on which the calls run: every tensor has to live there."""
     d = _current_device()
-    if index != d or (others and others != (d,) * len(others)):
-        raise ValueError(f"tensors must be on the current CUDA device (cuda:{d}), got devices {(index, *others)}")
+    if indices != (d,) * len(indices):
+        raise ValueError(f"tensors must be on the current CUDA device (cuda:{d}), got devices {indices}")
     return d
 
 
 def _fp8_activation(x: Fp8Tensor, what: str) -> tuple:
     """(B, T, cols) of 8-bit activations, with a scale row for every code row."""
-    lead = x.lead
-    if len(lead) != 2 or x.scale_lead != lead:
-        raise ValueError(f"{what} must be 8-bit activations [B, T, cols] with one row of scales per row, got rows "
-                         f"{tuple(lead)}, rows of scales {tuple(x.scale_lead)}")
-    return (*lead, x.cols)
+    cs, ss = x.cs, x.ss
+    if len(cs) != 3 or ss[0] != cs[0] or ss[1] != cs[1]:
+        raise ValueError(f"{what} must be 8-bit activations [B, T, cols] with one row of scales per row, got codes "
+                         f"{tuple(cs)}, scales {tuple(ss)}")
+    return cs[0], cs[1], x.cols
 
 
 def _fp8_weight(w: Fp8Tensor, what: str) -> tuple:
     """(T, K, N) of an 8-bit weight."""
-    lead = w.lead
-    if len(lead) != 2 or w.scale_lead != (lead[0], (lead[1] + 127) // 128):
-        raise ValueError(f"{what} must be an 8-bit weight [T, K, N] with one row of scales per 128 rows, got rows "
-                         f"{tuple(lead)}, rows of scales {tuple(w.scale_lead)}")
-    return (*lead, w.cols)
+    cs, ss = w.cs, w.ss
+    if len(cs) != 3 or ss[0] != cs[0] or ss[1] != (cs[1] + 127) // 128:
+        raise ValueError(f"{what} must be an 8-bit weight [T, K, N] with one row of scales per 128 rows, got codes "
+                         f"{tuple(cs)}, scales {tuple(ss)}")
+    return cs[0], cs[1], w.cols
 
 
 def fp8_quantize(X: torch.Tensor, fmt: str = "e4m3") -> Fp8Tensor:
@@ -489,11 +491,12 @@ def fp8_quantize_weight(W: torch.Tensor) -> Fp8Tensor:
 def fp8_dequantize(q: Fp8Tensor, dtype: str = "bf16") -> torch.Tensor:
     """The values of 8-bit rows [.., C] in bf16 or float32."""
     d = _fp8_device(q.device_index)
-    if q.scale_lead != q.lead:
+    lead, cols = q.cs[:-1], q.cols
+    if q.ss[:-1] != lead:
         raise ValueError("fp8_dequantize takes rows with their own scales (activations)")
     tdt, code = _DTYPES[dtype]
-    Y = torch.empty((*q.lead, q.cols), dtype=tdt, device=q.device)
-    _lib.rm_fp8_dequantize(q.c, math.prod(q.lead), q.cols, Y.data_ptr(), code, q.cols, _raw_stream(d))
+    Y = torch.empty((*lead, cols), dtype=tdt, device=q.device)
+    _lib.rm_fp8_dequantize(q.c, math.prod(lead), cols, Y.data_ptr(), code, cols, _raw_stream(d))
     return Y
 
 
@@ -527,8 +530,8 @@ def fp8_wgrad(x: Fp8Tensor, dY: torch.Tensor, grad_dtype: str = "f32") -> tuple[
         raise ValueError(f"dY must be bfloat16 [{B}, {T}, N], got {dY.dtype} {tuple(dY.shape)}")
     N = dY.shape[2]
     tdt, code = _DTYPES[grad_dtype]
-    dW = torch.empty((T, K, N), dtype=tdt, device=dY.device)
-    db = torch.empty((T, N), dtype=tdt, device=dY.device)
+    dW = torch.empty((T, K, N), dtype=tdt, device=x.device)
+    db = torch.empty((T, N), dtype=tdt, device=x.device)
     _lib.rm_fp8_wgrad(x.c, _ptr(dY), dW.data_ptr(), db.data_ptr(), code, B, T, K, N, _raw_stream(d))
     return dW, db
 
