@@ -1,11 +1,12 @@
 // Elementwise kernels of the 8-bit operators: saving rows and weights in 8 bits,
 // and restoring rows.
 //
-// Saving reads every value once and writes one byte for it; 16 lanes own one block
-// of 128 values, 8 each (16-byte loads), agree on its largest magnitude with four
-// shuffles and write 8 bytes of codes each.  64 bytes per thread are loaded before
-// the first is used and stay as they came (bf16 pairs) until then: few registers,
-// so many warps, are what hides the loads' latency.  Rows that are not 16-byte aligned are read
+// Saving reads every value once and writes one byte for it; 8 lanes own one block
+// of 128 values, two runs of 8 each (a load instruction's 8 lanes read 128 bytes
+// in a row), agree on its largest magnitude with three shuffles and write twice 8
+// bytes of codes.  64 bytes per thread are loaded before the first is used and stay
+// as they came (bf16 pairs) until then: few registers, so many warps, are what
+// hides the loads' latency, and few instructions per value what lets them.  Rows that are not 16-byte aligned are read
 // an element at a time, neighbouring lanes neighbouring elements, and their
 // codes pass through shared memory to the same 8-byte stores; restoring such
 // rows mirrors that.
@@ -90,13 +91,13 @@ struct Raw8 {
                 if (i < n) set(i, p[i]);
         }
     }
-    // every 16th value from p on, 8 of them
+    // every eighth value from p on, 8 of them
     __device__ __forceinline__ void gather(const IN* __restrict__ p, int n) {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(IN) * 2; ++i) w[i] = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (16 * i < n) set(i, p[16 * i]);
+            if (8 * i < n) set(i, p[8 * i]);
     }
     // float bits of the largest magnitude; infinities and NaN count as they are
     __device__ __forceinline__ uint32_t amax_bits() const {
@@ -113,18 +114,21 @@ struct Raw8 {
     }
 };
 
-// kUnroll blocks per 16 lanes (half of that for float32).
+// Blocks per 8 lanes: 64 bytes of values per thread.
+template <typename IN>
+constexpr int kBlocks = sizeof(IN) == 2 ? 2 : 1;
+
 template <typename IN, bool E5M2, bool VEC, bool COPY>
 __global__ void __launch_bounds__(kThreads)
 quantize_kernel(const IN* __restrict__ X, unsigned long long blocks, int cols, int nb, int dq, int dr, long long ldx,
                 Fp8View out, __nv_bfloat16* __restrict__ copy) {
-    constexpr int UNROLL = sizeof(IN) == 2 ? kUnroll : kUnroll / 2, PER = kThreads / 16;
-    __shared__ uint2 bytes[VEC ? 1 : kThreads];      // a thread's 8 codes: a block's 128 are contiguous
+    constexpr int UNROLL = kBlocks<IN>, PER = kThreads / 8;
+    __shared__ uint2 bytes[VEC ? 1 : 2 * kThreads];  // a block's 128 codes are contiguous
     pdl_wait();
     pdl_launch_next();
-    const int l16 = threadIdx.x & 15;
-    const unsigned long long base = (unsigned long long)blockIdx.x * (PER * UNROLL) + (threadIdx.x >> 4);
-    Raw8<IN> v[UNROLL];
+    const int l8 = threadIdx.x & 7;
+    const unsigned long long base = (unsigned long long)blockIdx.x * (PER * UNROLL) + (threadIdx.x >> 3);
+    Raw8<IN> v[UNROLL][2];
     unsigned long long row0 = 0;
     int j0 = 0;
     if (base < blocks) split_id(base, blocks, nb, row0, j0);
@@ -135,10 +139,13 @@ quantize_kernel(const IN* __restrict__ X, unsigned long long blocks, int cols, i
         for (int i = 0; i < UNROLL; ++i) {
             const int n = base + (unsigned long long)i * PER < blocks ? cols - j * kFp8Block : 0;
             const IN* p = X + row * (unsigned long long)ldx + j * kFp8Block;
-            if (VEC)
-                v[i].load(p + 8 * l16, n - 8 * l16);
-            else
-                v[i].gather(p + l16, n - l16);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (VEC)
+                    v[i][h].load(p + 8 * l8 + 64 * h, n - 8 * l8 - 64 * h);
+                else
+                    v[i][h].gather(p + l8 + 64 * h, n - l8 - 64 * h);
+            }
             next_id(row, j, dq, dr, nb);
         }
     }
@@ -146,41 +153,58 @@ quantize_kernel(const IN* __restrict__ X, unsigned long long blocks, int cols, i
     int j = j0;
 #pragma unroll
     for (int i = 0; i < UNROLL; ++i) {
-        float f[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = v[i].get(k);
-        uint32_t m = v[i].amax_bits();
-        if (m >= 0x7f800000u) {                      // infinities become NaN, and neither counts
+        uint32_t m = max(v[i][0].amax_bits(), v[i][1].amax_bits());
+        const bool odd = m >= 0x7f800000u;           // infinities or NaN among them: neither counts
+        if (odd) {
             m = 0;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                m = max(m, fp8_finite_bits(f[k]));
-                f[k] = fp8_poison(f[k]);
-            }
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) m = max(m, fp8_finite_bits(v[i][h].get(k)));
         }
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const uint32_t E = fp8_exponent<E5M2>(m);
-        const float s = fp8_inv_scale(E);
-        uint2 w = make_uint2(fp8_pack4<E5M2>(f[0] * s, f[1] * s, f[2] * s, f[3] * s),
-                             fp8_pack4<E5M2>(f[4] * s, f[5] * s, f[6] * s, f[7] * s));
-        if (!VEC) {                                  // lane's codes are every 16th: to their places
-            uint8_t* mine = reinterpret_cast<uint8_t*>(bytes) + (threadIdx.x & ~15) * 8 + l16;
+        const uint64_t s = f2_splat(fp8_inv_scale(E));
+        uint2 w[2];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) mine[16 * k] = (uint8_t)((k < 4 ? w.x : w.y) >> (8 * (k & 3)));
+        for (int h = 0; h < 2; ++h) {
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 8; k += 2)
+                f2_unpack(f2_mul(f2_pack(v[i][h].get(k), v[i][h].get(k + 1)), s), f[k], f[k + 1]);
+            if (odd) {                               // infinities become NaN
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] = fp8_poison(v[i][h].get(k)) * fp8_inv_scale(E);
+            }
+            w[h] = make_uint2(fp8_pack4<E5M2>(f[0], f[1], f[2], f[3]), fp8_pack4<E5M2>(f[4], f[5], f[6], f[7]));
+        }
+        if (!VEC) {                                  // lane's codes are every eighth: to their places
+            uint2* block = bytes + (threadIdx.x & ~7) * 2;
+            uint8_t* mine = reinterpret_cast<uint8_t*>(block) + l8;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mine[64 * h + 8 * k] = (uint8_t)((k < 4 ? w[h].x : w[h].y) >> (8 * (k & 3)));
             __syncwarp();
-            w = bytes[threadIdx.x];
+            w[0] = block[l8];
+            w[1] = block[8 + l8];
             __syncwarp();
         }
-        const int col = j * kFp8Block + 8 * l16;
-        // code rows are padded to 16 bytes, so a lane's 8 fit when they begin before that
-        if (base + (unsigned long long)i * PER < blocks && col < (cols + 15) / 16 * 16) {
-            *reinterpret_cast<uint2*>(out.codes + row * (unsigned long long)out.ld + col) = w;
-            if (l16 == 0) out.scales[row * (unsigned long long)out.lds + j] = (uint8_t)E;
-            if (COPY)                                // cols is a multiple of 16
-                *reinterpret_cast<uint4*>(copy + row * (unsigned long long)cols + col) =
-                    make_uint4(pack_bf16x2(v[i].get(0), v[i].get(1)), pack_bf16x2(v[i].get(2), v[i].get(3)),
-                               pack_bf16x2(v[i].get(4), v[i].get(5)), pack_bf16x2(v[i].get(6), v[i].get(7)));
+        if (base + (unsigned long long)i * PER < blocks) {
+            if (l8 == 0) out.scales[row * (unsigned long long)out.lds + j] = (uint8_t)E;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int col = j * kFp8Block + 8 * l8 + 64 * h;
+                // code rows are padded to 16 bytes, so a lane's 8 fit when they begin before that
+                if (col < (cols + 15) / 16 * 16) {
+                    *reinterpret_cast<uint2*>(out.codes + row * (unsigned long long)out.ld + col) = w[h];
+                    if (COPY)                        // cols is a multiple of 16
+                        *reinterpret_cast<uint4*>(copy + row * (unsigned long long)cols + col) =
+                            make_uint4(pack_bf16x2(v[i][h].get(0), v[i][h].get(1)), pack_bf16x2(v[i][h].get(2), v[i][h].get(3)),
+                                       pack_bf16x2(v[i][h].get(4), v[i][h].get(5)), pack_bf16x2(v[i][h].get(6), v[i][h].get(7)));
+                }
+            }
         }
         next_id(row, j, dq, dr, nb);
     }
@@ -308,12 +332,12 @@ bool aligned16p(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) =
 template <typename IN, bool E5M2, bool VEC>
 cudaError_t run_quantize(const void* X, long long rows, int cols, long long ldx, const Fp8View& out, void* copy,
                          cudaStream_t s) {
-    const int nb = (cols + kFp8Block - 1) / kFp8Block, half = kThreads / 16,
-              per = half * (sizeof(IN) == 2 ? kUnroll : kUnroll / 2);
+    const int nb = (cols + kFp8Block - 1) / kFp8Block, step = kThreads / 8,
+              per = step * kBlocks<IN>;
     const unsigned long long blocks = (unsigned long long)rows * nb;
     const unsigned grid = (unsigned)((blocks + per - 1) / per);
     return launch_k(copy ? quantize_kernel<IN, E5M2, VEC, true> : quantize_kernel<IN, E5M2, VEC, false>, dim3(grid),
-                    dim3(kThreads), 0, s, (const IN*)X, blocks, cols, nb, half / nb, half % nb, ldx, out,
+                    dim3(kThreads), 0, s, (const IN*)X, blocks, cols, nb, step / nb, step % nb, ldx, out,
                     (__nv_bfloat16*)copy);
 }
 
