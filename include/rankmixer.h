@@ -483,9 +483,12 @@ RM_API rm_status rm_debug_mix_residual(const void *X, int from_z, float *Y, int 
  * cols (codes) and past the last block (scales) are never interpreted.
  *
  * These calls need no context: they run on the current device, which must own
- * the buffers, on `stream`, allocate nothing, keep nothing between calls and
- * may be captured into a CUDA graph.  Calls on different streams are
- * independent when their buffers (and workspaces) are.  Device-side errors (a
+ * the buffers, on `stream`, allocate nothing and keep nothing between calls.
+ * They may be captured into a CUDA graph once any of them has run on that
+ * device outside capture (which looks up the device's error word).  Calls on
+ * different streams are independent when their buffers (and workspaces) are.
+ * Lengths that are summed over (K; B for the weight gradients) are at most
+ * 2^27, B T is below 2^31 (RM_ERR_UNSUPPORTED, RM_ERR_INVALID_ARG otherwise).  Device-side errors (a
  * bounded wait that ran out) are latched per device and reported by
  * rm_fp8_sync_status. */
 typedef enum rm_fp8_format {

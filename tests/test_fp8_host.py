@@ -111,6 +111,11 @@ def test_matmul_and_wgrad_refusals(lib, mem):
     assert lib.rm_fp8_wgrad(q, p + 2, p, p, 0, 3, 2, 200, 200, None) == BAD
     assert lib.rm_fp8_wgrad(q, p, p, p, 0, 3, 2, 200, 204, None) == NO
     assert lib.rm_fp8_wgrad(t8(p, 200, _lib.RM_E5M2), p, p, p, 0, 3, 2, 200, 200, None) == NO
+    # lengths summed over
+    big = (1 << 27) + 16
+    assert lib.rm_fp8_matmul(t8(p, big), t8(p, 200), None, p, 0, 1, 1, big, 200, 0, None) == NO
+    assert lib.rm_fp8_wgrad(q, p, p, p, 0, big, 1, 200, 200, None) == NO
+    assert "2^27" in _lib.rm_last_error()
 
 
 def test_pffn_refusals(lib, mem):
