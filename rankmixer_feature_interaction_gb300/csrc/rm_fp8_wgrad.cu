@@ -14,9 +14,9 @@
 //   warp 1        MMA issuer (the even CTA's): kind::f16 on bf16, M = N = 256
 //   warp 2        TMA producer of x's codes (64 samples x 128 bytes)
 //   warps 4-11    epilogue
-//   warps 20-23   db, the column sums of dY, in the tiles of the first 256 k: from
-//                 dY's operand tile in shared memory once the MMA is done with it,
-//                 so dY is not read again
+//   warps 20-23   db, the column sums of dY, in one tile of each column of tiles:
+//                 from dY's operand tile in shared memory once the MMA is done with
+//                 it, so dY is not read again
 //   warp 3        x's exponent bytes into shared memory, eight k-blocks' loads
 //                 at a time so that their latency is paid once in eight
 //   warps 12-19   restore codes to bf16: MN-major operand rows are samples, so
@@ -25,6 +25,14 @@
 //                 exponent and mantissa, are the code times 2^-120 (also for
 //                 subnormal codes), so one packed product by 2^120 times the
 //                 scale restores it: 4 instructions for two codes
+// db's sums cost a hop on the operand ring, so only the k-blocks that are summed
+// take it (all of them did at first: 844 us against 816 at the size below, in f32).
+//
+// Measured, T = 32, K = 1536, N = 6144, dW and db: B = 2048 816 us in f32 (1516
+// TFLOP/s) and 773 us in bf16, B = 1024 476 and 421 us; B = 8, where a tile is one
+// k-block and the time is dW's, 207 us (5.8 TB/s) and 109 us (5.5 TB/s).  Bound at
+// large B by the tensor cores under the power limit and the restorers beside them
+// (shared memory), at small B by dW's stores.
 // Every mbarrier wait is bounded in time; on expiry the CTA latches an error
 // word and all roles unwind.
 #include <cudaTypedefs.h>
@@ -53,7 +61,7 @@ constexpr int STAGING = 4096;
 constexpr int SUM_WARPS = 4;                 // 32 columns of dY each
 constexpr int SUM_WARP0 = 4 + EPI_WARPS + CONV_WARPS;
 constexpr int THREADS = 32 * (SUM_WARP0 + SUM_WARPS);
-constexpr int SMEM_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES) + RAWS * (RAW_BYTES + BK) + EPI_WARPS * STAGING + 256;
+constexpr int SMEM_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES) + RAWS * (RAW_BYTES + BK) + EPI_WARPS * STAGING + 320;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 static_assert(GROUPS <= RAWS && GROUPS <= STAGES, "a k-block per group of restorers");
 
@@ -71,6 +79,7 @@ struct Args {
 
 struct Tile {
     int t, m0, n0;
+    bool sums;                           // adds up dY's columns: one tile of each column of tiles
 };
 __device__ __forceinline__ Tile tile_of(long long i, const Args& a) {
     const int per = a.m_tiles * a.n_tiles;
@@ -79,6 +88,9 @@ __device__ __forceinline__ Tile tile_of(long long i, const Args& a) {
     const int rem = (int)(i - (long long)r.t * per), nb = rem / a.m_tiles;
     r.m0 = (rem - nb * a.m_tiles) * 2 * BM;
     r.n0 = nb * BN;
+    // not always the first: tiles go round the CTA pairs, and the pairs' number may share
+    // a factor with m_tiles, which would leave all the sums to a few of them
+    r.sums = rem - nb * a.m_tiles == (int)((unsigned)(r.t + nb) % (unsigned)a.m_tiles);
     return r;
 }
 
@@ -173,8 +185,9 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * RAWS + x); };
     auto tempty_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * RAWS + 2 + x); };
     auto summed_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 2 * RAWS + 4 + s); };
+    auto sready_bar = [&](int s) { return bar0 + 8u * (3 * STAGES + 2 * RAWS + 4 + s); };
     uint32_t* tmem_holder =
-        reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + 8 * (3 * STAGES + 2 * RAWS + 4));
+        reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + 8 * (4 * STAGES + 2 * RAWS + 4));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -187,7 +200,8 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_bar(s), 1 + 2 * CONV_GROUP);   // the even CTA's: dY's bytes of both CTAs, both CTAs' restorers
             mbar_init(empty_bar(s), 1);                   // multicast commit
-            mbar_init(summed_bar(s), SUM_WARPS);          // the same, and dY has been summed
+            mbar_init(sready_bar(s), 1);                  // the same, for k-blocks of tiles that are summed
+            mbar_init(summed_bar(s), SUM_WARPS);          // ... and these have been summed
         }
         for (int s = 0; s < RAWS; ++s) {
             mbar_init(rfull_bar(s), 2);                   // x's bytes, its exponents
@@ -217,16 +231,22 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         // ------------------------------ dY producer -------------------------------
         int stage = 0;
         uint32_t phase = 0;
+        uint32_t held = 0, sphase = 0;         // per stage: holds a k-block to be summed; its barrier's phase
         bool ok = true;
         for (long long i = unit; ok && i < args.tiles; i += nunits) {
             const Tile tl = tile_of(i, args);
             const int col = tl.n0 + BN / 2 * (int)rank;
             for (int kb = 0; kb < kblocks; ++kb) {
-                if (!wait_bounded(args.db ? summed_bar(stage) : empty_bar(stage), phase ^ 1u, abort_flag, args.err,
+                const uint32_t bit = 1u << stage;
+                const bool summed = (held & bit) != 0;
+                if (!wait_bounded(summed ? summed_bar(stage) : empty_bar(stage),
+                                  summed ? (uint32_t)((sphase & bit) != 0) : phase ^ 1u, abort_flag, args.err,
                                   args.timeout_ns)) {
                     ok = false;
                     break;
                 }
+                if (summed) sphase ^= bit;
+                held = args.db && tl.sums ? held | bit : held & ~bit;
                 if (elect_one()) {
                     const uint32_t fb = mapa_shared(full_bar(stage), 0);
                     if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2u * B_BYTES);
@@ -265,6 +285,7 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true;
         for (long long i = unit; ok && i < args.tiles; i += nunits) {
+            const bool sums = args.db && tile_of(i, args).sums;
             int in_chunk = 0;
             for (int kb = 0; kb < kblocks; ++kb) {
                 if (in_chunk == 0 &&
@@ -285,6 +306,7 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                     for (int k = 0; k < BK / 16; ++k)        // 16 samples: 16 rows of 128 bytes
                         umma_f16_pair(d, a + 128u * k, b + 128u * k, kIdesc, (in_chunk | k) != 0 ? 1u : 0u);
                     umma_commit_pair_mc(empty_bar(stage), (uint16_t)0x3);
+                    if (sums) umma_commit_pair_mc(sready_bar(stage), (uint16_t)0x3);
                 }
                 __syncwarp();
                 if (++stage == STAGES) stage = 0, phase ^= 1u;
@@ -299,74 +321,86 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         }
     } else if (warp == 3) {
         // ------------------------------ exponents ---------------------------------
-        int slot = 0;
+        // AHEAD k-blocks at a time, across the ends of tiles: with one k-block per tile
+        // (few samples) each tile would otherwise wait for a load of its own.
+        int slot = 0, kb = 0, k0 = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (long long i = unit; ok && i < args.tiles; i += nunits) {
-            const Tile tl = tile_of(i, args);
-            const int k0 = tl.m0 + BM * (int)rank;
-            const uint8_t* sp = args.xs + (size_t)tl.t * (size_t)args.xs_ld + k0 / kFp8Block;
-            const size_t step = (size_t)args.T * (size_t)args.xs_ld;
-            for (int kb0 = 0; ok && kb0 < kblocks; kb0 += AHEAD) {
-                uint32_t E[AHEAD][2];
+        const uint8_t* sp = args.xs;
+        const size_t step = (size_t)args.T * (size_t)args.xs_ld;
+        for (long long i = unit; ok && i < args.tiles;) {
+            uint32_t E[AHEAD][2];
+            int n = 0;
 #pragma unroll
-                for (int q = 0; q < AHEAD; ++q)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int b = (kb0 + q) * BK + 32 * j + lane;
-                        E[q][j] = b < args.B && k0 < args.K ? __ldg(sp + (size_t)b * step) : 127u;
+            for (int q = 0; q < AHEAD; ++q) {
+                if (i < args.tiles) {
+                    if (kb == 0) {
+                        const Tile tl = tile_of(i, args);
+                        k0 = tl.m0 + BM * (int)rank;
+                        sp = args.xs + (size_t)tl.t * (size_t)args.xs_ld + k0 / kFp8Block;
                     }
 #pragma unroll
-                for (int q = 0; q < AHEAD; ++q) {
-                    if (ok && kb0 + q < kblocks) {
-                        ok = wait_bounded(rempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns);
-                        if (ok) {
-                            st_shared_u8(sExp + BK * slot + lane, E[q][0]);
-                            st_shared_u8(sExp + BK * slot + 32 + lane, E[q][1]);
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(rfull_bar(slot));
-                            if (++slot == RAWS) slot = 0, phase ^= 1u;
-                        }
+                    for (int j = 0; j < 2; ++j) {
+                        const int b = kb * BK + 32 * j + lane;
+                        E[q][j] = b < args.B && k0 < args.K ? __ldg(sp + (size_t)b * step) : 127u;
+                    }
+                    if (++kb == kblocks) kb = 0, i += nunits;
+                    n = q + 1;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < AHEAD; ++q) {
+                if (ok && q < n) {
+                    ok = wait_bounded(rempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns);
+                    if (ok) {
+                        st_shared_u8(sExp + BK * slot + lane, E[q][0]);
+                        st_shared_u8(sExp + BK * slot + 32 + lane, E[q][1]);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(rfull_bar(slot));
+                        if (++slot == RAWS) slot = 0, phase ^= 1u;
                     }
                 }
             }
         }
     } else if (warp >= SUM_WARP0) {
         // ------------------------------ bias gradient -----------------------------
-        // Lane: 8 columns (16 bytes) of every eighth row.  Every k-block passes through
-        // here to the dY producer; those of the first 256 k are summed.  Eight lanes
-        // read four chunks of rows r and r + 4, whose swizzles have no bank in common.
+        // Lane: 8 columns (16 bytes) of every eighth row.  Eight lanes read four chunks of
+        // rows r and r + 4, whose swizzles have no bank in common.  Only the k-blocks of
+        // tiles that are summed pass through here on their way back to the dY producer,
+        // by barriers of their own, whose phases count those k-blocks alone.
         const int box = (warp - SUM_WARP0) >> 1, c = (lane & 3) + 4 * ((warp - SUM_WARP0) & 1);
         const int r0 = (lane >> 3) + (lane & 4);
         int stage = 0;
-        uint32_t phase = 0;
+        uint32_t phase = 0;                            // per stage
         bool ok = true;
         for (long long i = unit; args.db && ok && i < args.tiles; i += nunits) {
             const Tile tl = tile_of(i, args);
+            if (!tl.sums) {
+                stage = (stage + kblocks) % STAGES;
+                continue;
+            }
             float sum[8] = {};
             for (int kb = 0; kb < kblocks; ++kb) {
-                if (!wait_bounded(empty_bar(stage), phase, abort_flag, args.err, args.timeout_ns)) {
+                if (!wait_bounded(sready_bar(stage), (phase >> stage) & 1u, abort_flag, args.err, args.timeout_ns)) {
                     ok = false;
                     break;
                 }
-                if (tl.m0 == 0) {
-                    const uint32_t src = sB + stage * B_BYTES + box * BOX_BYTES;
+                phase ^= 1u << stage;
+                const uint32_t src = sB + stage * B_BYTES + box * BOX_BYTES;
 #pragma unroll
-                    for (int r = r0; r < BK; r += 8) {
-                        const uint4 q = ld_shared_u4(src + 128u * r + 16u * (uint32_t)(c ^ (r & 7)));
-                        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                for (int r = r0; r < BK; r += 8) {
+                    const uint4 q = ld_shared_u4(src + 128u * r + 16u * (uint32_t)(c ^ (r & 7)));
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            sum[2 * j] += __uint_as_float(w[j] << 16);
-                            sum[2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
-                        }
+                    for (int j = 0; j < 4; ++j) {
+                        sum[2 * j] += __uint_as_float(w[j] << 16);
+                        sum[2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
                     }
-                    __syncwarp();
                 }
+                __syncwarp();
                 if (lane == 0) mbar_arrive(summed_bar(stage));
-                if (++stage == STAGES) stage = 0, phase ^= 1u;
+                if (++stage == STAGES) stage = 0;
             }
-            if (tl.m0 != 0) continue;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 4);
@@ -400,65 +434,59 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         const uint32_t flip = (lane & 4) ? 5 : 0, rep0 = lane >> 4;
         uint32_t slot = group;
         uint32_t rphase = 0;
-        long long done = 0;                          // k-blocks before this tile
         int stage = (int)group;                      // of the group's next k-block
         uint32_t phase = 0;
-        long long next = group;
-        bool ok = true;
-        for (long long i = unit; ok && i < args.tiles; i += nunits, done += kblocks) {
-            for (; next < done + kblocks; next += GROUPS) {
-                if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns) ||
-                    !wait_bounded(rfull_bar(slot), rphase, abort_flag, args.err, args.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t src = sRaw + slot * RAW_BYTES, exps = sExp + BK * slot;
-                const uint32_t dst = sA + stage * A_BYTES + (c >> 2) * BOX_BYTES;
-                // all chunks are loaded first and restored without a branch between them
-                constexpr int CH = BK / CONV_GROUP / 4;
-                uint4 q[CH];
-                uint32_t E[CH];
-                bool plain = true;
+        long long left = ((args.tiles - 1 - unit) / nunits + 1) * kblocks - group;   // unit < tiles: the grid's size
+        for (; left > 0; left -= GROUPS) {
+            if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns) ||
+                !wait_bounded(rfull_bar(slot), rphase, abort_flag, args.err, args.timeout_ns))
+                break;
+            const uint32_t src = sRaw + slot * RAW_BYTES, exps = sExp + BK * slot;
+            const uint32_t dst = sA + stage * A_BYTES + (c >> 2) * BOX_BYTES;
+            // all chunks are loaded first and restored without a branch between them
+            constexpr int CH = BK / CONV_GROUP / 4;
+            uint4 q[CH];
+            uint32_t E[CH];
+            bool plain = true;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                const uint32_t x7 = (rep0 | ((j & 1u) << 1)) ^ flip, r = BK / CONV_GROUP * cw + 8u * (j >> 1) + x7;
+                q[j] = ld_shared_u4(src + 128u * r + 16u * (c ^ x7));
+                E[j] = ld_shared_u8(exps + r);
+            }
+#pragma unroll
+            for (int j = 0; j < CH; ++j) plain = plain && plain16(q[j], E[j]);
+            auto put = [&](int j, const uint32_t (&o)[8]) {
+                const uint32_t x7 = (rep0 | ((j & 1u) << 1)) ^ flip, r = BK / CONV_GROUP * cw + 8u * (j >> 1) + x7;
+                st_shared_v4(dst + 128u * r + 16u * (p ^ x7), o[0], o[1], o[2], o[3]);
+                st_shared_v4(dst + 128u * r + 16u * ((p + 1u) ^ x7), o[4], o[5], o[6], o[7]);
+            };
+            if (plain) {
 #pragma unroll
                 for (int j = 0; j < CH; ++j) {
-                    const uint32_t x7 = (rep0 | ((j & 1u) << 1)) ^ flip, r = BK / CONV_GROUP * cw + 8u * (j >> 1) + x7;
-                    q[j] = ld_shared_u4(src + 128u * r + 16u * (c ^ x7));
-                    E[j] = ld_shared_u8(exps + r);
+                    uint32_t o[8];
+                    restore16(q[j], E[j], o);
+                    put(j, o);
                 }
-#pragma unroll
-                for (int j = 0; j < CH; ++j) plain = plain && plain16(q[j], E[j]);
-                auto put = [&](int j, const uint32_t (&o)[8]) {
-                    const uint32_t x7 = (rep0 | ((j & 1u) << 1)) ^ flip, r = BK / CONV_GROUP * cw + 8u * (j >> 1) + x7;
-                    st_shared_v4(dst + 128u * r + 16u * (p ^ x7), o[0], o[1], o[2], o[3]);
-                    st_shared_v4(dst + 128u * r + 16u * ((p + 1u) ^ x7), o[4], o[5], o[6], o[7]);
-                };
-                if (plain) {
-#pragma unroll
-                    for (int j = 0; j < CH; ++j) {
-                        uint32_t o[8];
-                        restore16(q[j], E[j], o);
-                        put(j, o);
-                    }
-                } else {
+            } else {
 #pragma unroll 1
-                    for (int j = 0; j < CH; ++j) {
-                        uint32_t o[8];
-                        const uint32_t x7 = (rep0 | ((j & 1u) << 1)) ^ flip, r = BK / CONV_GROUP * cw + 8u * (j >> 1) + x7;
-                        restore16_any(ld_shared_u4(src + 128u * r + 16u * (c ^ x7)), ld_shared_u8(exps + r), o);
-                        put(j, o);
-                    }
+                for (int j = 0; j < CH; ++j) {
+                    uint32_t o[8];
+                    const uint32_t x7 = (rep0 | ((j & 1u) << 1)) ^ flip, r = BK / CONV_GROUP * cw + 8u * (j >> 1) + x7;
+                    restore16_any(ld_shared_u4(src + 128u * r + 16u * (c ^ x7)), ld_shared_u8(exps + r), o);
+                    put(j, o);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive_pair(mapa_shared(full_bar(stage), 0));
-                    mbar_arrive(rempty_bar(slot));
-                }
-                stage += GROUPS;
-                if (stage >= STAGES) stage -= STAGES, phase ^= 1u;
-                slot += GROUPS;
-                if (slot >= RAWS) slot -= RAWS, rphase ^= 1u;
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive_pair(mapa_shared(full_bar(stage), 0));
+                mbar_arrive(rempty_bar(slot));
+            }
+            stage += GROUPS;
+            if (stage >= STAGES) stage -= STAGES, phase ^= 1u;
+            slot += GROUPS;
+            if (slot >= RAWS) slot -= RAWS, rphase ^= 1u;
         }
     } else if (warp >= 4) {
         // ------------------------------ epilogue ----------------------------------
@@ -480,27 +508,32 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             const uint32_t tcol = tmem_base + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * BN) + 128u * half;
 #pragma unroll
             for (int h = 0; h < 128 / PIECE; ++h) {
-                uint32_t r[PIECE];
+#pragma unroll 1                              // unrolled, both halves' registers are live and spill
+                for (int q = 0; q < PIECE / 32; ++q) {
+                    uint32_t r[32];
+                    tmem_ld32_nowait(tcol + PIECE * h + 32 * q, r);
+                    tmem_wait_ld();
+                    if (q == 0) {
+                        if (lane == 0) {
+                            if (F32 && chunk > 0)
+                                bulk_wait_group<0>();        // the chunk before is in memory
+                            else
+                                bulk_wait_group_read<0>();
+                        }
+                        __syncwarp();
+                    }
+                    constexpr int PER = F32 ? 4 : 8;         // columns in 16 bytes
 #pragma unroll
-                for (int q = 0; q < PIECE / 32; ++q)
-                    tmem_ld32_nowait(tcol + PIECE * h + 32 * q, reinterpret_cast<uint32_t(&)[32]>(r[32 * q]));
-                tmem_wait_ld();
-                if (lane == 0) {
-                    if (F32 && chunk > 0)
-                        bulk_wait_group<0>();        // the chunk before is in memory
-                    else
-                        bulk_wait_group_read<0>();
-                }
-                __syncwarp();
+                    for (int p = 0; p < 32 / PER; ++p) {
+                        uint32_t w[4];
 #pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        w[q] = F32 ? r[4 * p + q]
-                                   : pack_bf16x2(__uint_as_float(r[(8 * p + 2 * q) % PIECE]),
-                                                 __uint_as_float(r[(8 * p + 2 * q + 1) % PIECE]));
-                    st_shared_v4(stage + 128u * lane + 16u * (uint32_t)(p ^ (lane & 7)), w[0], w[1], w[2], w[3]);
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = F32 ? r[4 * p + j]
+                                       : pack_bf16x2(__uint_as_float(r[(8 * p + 2 * j) % 32]),
+                                                     __uint_as_float(r[(8 * p + 2 * j + 1) % 32]));
+                        const uint32_t c = (uint32_t)(p + q * (32 / PER));
+                        st_shared_v4(stage + 128u * lane + 16u * (c ^ (lane & 7)), w[0], w[1], w[2], w[3]);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
