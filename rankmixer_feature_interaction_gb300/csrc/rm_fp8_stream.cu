@@ -24,6 +24,8 @@
 // word and all roles unwind.
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "rm_fp8.cuh"
 #include "rm_fp8_tc.cuh"
 
@@ -34,6 +36,23 @@ constexpr int BM = 128, BK = 128;
 constexpr int W_BYTES = BM * BK;
 constexpr int SF_SLOTS = 4, SF_BYTES = 1024;
 constexpr int TMEM_COLS = 256, SF_COL = 192;
+// Where the tiles are fewer than half of the SMs, 2 or 4 CTAs share each tile's K.
+constexpr int MAX_SPLIT = 4;
+
+// Four words to another CTA's shared memory, counted there by its barrier.
+__device__ __forceinline__ void st_async_v4(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+                 "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
+                 : "memory");
+}
+// A phase already seen to be complete, looked at once more so that what other CTAs
+// of the cluster stored for it is seen too.
+__device__ __forceinline__ void mbar_acquire_cluster(uint32_t bar, uint32_t parity) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar), "r"(parity)
+        : "memory");
+}
 
 template <int NB>
 struct Cfg {
@@ -44,9 +63,11 @@ struct Cfg {
     static constexpr int EPI_WARPS = NB == 64 ? 8 : 4;
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     static constexpr int SAMPLES = NB / (EPI_WARPS / 4);            // per epilogue thread
+    static constexpr int PART_BYTES = BM * NB * 4;                  // one CTA's partial sums of a split tile
     static constexpr int RED_BYTES = 2 * (4 + 1) * NB * 4;          // [output][warp of the block, then the scale][sample]
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SF_SLOTS * SF_BYTES + RED_BYTES + 512;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+    static_assert((MAX_SPLIT - 1) * PART_BYTES <= STAGES * STAGE_BYTES / 2, "half of the ring remains when K is split");
     static_assert(2 * NB <= SF_COL, "two accumulators below the scales");
 };
 
@@ -55,6 +76,8 @@ enum Epi { EPI_BF16, EPI_F32, EPI_GELU, EPI_GELU_KEEP };
 struct Args {
     int B, T, K, N;
     int n_tiles, kblocks, tiles;
+    int split, groups;                   // CTAs (a cluster) that share a tile's K; groups of four k-blocks for each
+    int stages;                          // of the ring; what a split's partial sums take is not part of it
     const uint8_t* xs;
     long long xs_ld;
     const uint8_t* ws;
@@ -78,7 +101,9 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
     uint8_t* base_ptr = smem_raw + (base - raw_addr);
-    const uint32_t sW = base, sX = sW + STAGES * W_BYTES, sSF = sX + STAGES * C::X_BYTES;
+    const int stages = args.stages;
+    const uint32_t sW = base, sX = sW + stages * W_BYTES, sSF = base + STAGES * C::STAGE_BYTES;
+    const uint32_t sPart = sX + stages * C::X_BYTES;        // [rank - 1][sample / 4][column][sample % 4] float
     uint32_t* red = reinterpret_cast<uint32_t*>(base_ptr + (sSF - base) + SF_SLOTS * SF_BYTES);
     const uint32_t bar0 = sSF + SF_SLOTS * SF_BYTES + C::RED_BYTES;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -88,7 +113,8 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + x); };
     auto tempty_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 2 + x); };
     const uint32_t meet_bar = bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 4);
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (meet_bar + 16u - base));
+    const uint32_t part_bar = meet_bar + 16u;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (part_bar + 8u - base));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -108,8 +134,11 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             mbar_init(tempty_bar(x), EPI_WARPS);
         }
         for (int g = 0; g < 2; ++g) mbar_init(meet_bar + 8u * g, 4);
+        mbar_init(part_bar, 1);                   // the other CTAs' partial sums
         *abort_flag = 0;
         fence_mbar_init();
+        if (args.split > 1 && cluster_ctarank() == 0)
+            mbar_arrive_expect_tx(part_bar, (uint32_t)(args.split - 1) * C::PART_BYTES);
     }
     if (warp == 4) {
         tmem_alloc(smem_u32(tmem_holder), TMEM_COLS);
@@ -117,9 +146,14 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     }
     tc_fence_before();
     __syncthreads();
+    if (args.split > 1) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
-    const int kblocks = args.kblocks;
+    // this CTA's tiles, and its k-blocks of each
+    const int rank = args.split > 1 ? (int)cluster_ctarank() : 0;
+    const int unit = (int)blockIdx.x / args.split, units = (int)gridDim.x / args.split;
+    const int kb0 = 4 * args.groups * rank;
+    const int kb1 = min(kb0 + 4 * args.groups, args.kblocks);
     if (!(args.early && warp == 0)) {
         pdl_wait();
         pdl_launch_next();
@@ -130,9 +164,9 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int i = blockIdx.x; ok && i < args.tiles; i += gridDim.x) {
+        for (int i = unit; ok && i < args.tiles; i += units) {
             const int t = i / args.n_tiles, n0 = (i - t * args.n_tiles) * BM;
-            for (int kb = 0; kb < kblocks; ++kb) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
                     ok = false;
                     break;
@@ -150,7 +184,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                     }
                 }
                 __syncwarp();
-                if (++stage == STAGES) stage = 0, phase ^= 1u;
+                if (++stage == stages) stage = 0, phase ^= 1u;
             }
         }
     } else if (warp == 1) {
@@ -161,11 +195,11 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         int stage = 0, slot = 0, acc = 0;
         uint32_t phase = 0, sphase = 0, acc_phase = 0;
         bool ok = true;
-        for (int i = blockIdx.x; ok && i < args.tiles; i += gridDim.x) {
+        for (int i = unit; ok && i < args.tiles; i += units) {
             if (!wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
             tc_fence_after();
             const uint32_t d = tmem_base + (uint32_t)(acc * NB);
-            for (int kb = 0; kb < kblocks; ++kb) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 const uint32_t sf = tmem_base + SF_COL + 8u * slot;
                 if ((kb & 3) == 0) {
                     if (!wait_bounded(sfull_bar(slot), sphase, abort_flag, args.err, args.timeout_ns)) {
@@ -184,19 +218,19 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                     break;
                 }
                 tc_fence_after();
-                const bool last = (kb & 3) == 3 || kb + 1 == kblocks;
+                const bool last = (kb & 3) == 3 || kb + 1 == kb1;
                 if (elect_one()) {
                     const uint32_t id = with_scale_id(idesc, (uint32_t)(kb & 3));
                     const uint64_t a = a_desc + (uint32_t)(stage * (W_BYTES >> 4));
                     const uint64_t b = b_desc + (uint32_t)(stage * (C::X_BYTES >> 4));
 #pragma unroll
                     for (int k = 0; k < BK / 32; ++k)
-                        umma_mxf8<false>(d, a + (a_step >> 4) * k, b + 2u * k, id, sf, sf + 4, (kb | k) != 0 ? 1u : 0u);
+                        umma_mxf8<false>(d, a + (a_step >> 4) * k, b + 2u * k, id, sf, sf + 4, kb != kb0 || k != 0 ? 1u : 0u);
                     umma_commit(empty_bar(stage));
                     if (last) umma_commit(sempty_bar(slot));
                 }
                 __syncwarp();
-                if (++stage == STAGES) stage = 0, phase ^= 1u;
+                if (++stage == stages) stage = 0, phase ^= 1u;
                 if (last && ++slot == SF_SLOTS) slot = 0, sphase ^= 1u;
             }
             if (!ok) break;
@@ -208,7 +242,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     } else if (warp == 2) {
         // ------------------------------ scales ------------------------------------
         // one group of four k-blocks ahead, as in rm_fp8_gemm.cu
-        const int groups = (kblocks + 3) / 4;
+        const int g0 = kb0 / 4, g1 = (kb1 + 3) / 4;
         struct Words {
             uint32_t x[(NB + 31) / 32], w;
         };
@@ -230,18 +264,18 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 r.w = 0;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int kb = 4 * g + q < kblocks ? 4 * g + q : kblocks - 1;
+                    const int kb = 4 * g + q < args.kblocks ? 4 * g + q : args.kblocks - 1;
                     r.w |= (uint32_t)__ldg(args.ws + ((size_t)t * args.w_rows + kb) * (size_t)args.ws_ld + nb) << (8 * q);
                 }
             }
             return r;
         };
-        int slot = 0, g = 0, i = blockIdx.x;
+        int slot = 0, g = g0, i = unit;
         uint32_t phase = 0;
         Words now{};
-        if (i < args.tiles) now = load(i, 0);
+        if (i < args.tiles) now = load(i, g0);
         while (i < args.tiles) {
-            if (++g == groups) g = 0, i += gridDim.x;
+            if (++g == g1) g = g0, i += units;
             Words next{};
             if (i < args.tiles) next = load(i, g);
             if (!wait_bounded(sempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
@@ -269,7 +303,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             meet ^= 1u;
             return ok;
         };
-        for (int i = blockIdx.x; i < args.tiles; i += gridDim.x) {
+        for (int i = unit; i < args.tiles; i += units) {
             const int t = i / args.n_tiles, n0 = (i - t * args.n_tiles) * BM, n = n0 + tid;
             const float bias = args.bias && n < args.N ? __ldg(args.bias + (size_t)t * args.N + n) : 0.f;
             if (!wait_bounded(tfull_bar(acc), acc_phase, abort_flag, args.err, args.timeout_ns)) break;
@@ -288,19 +322,45 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             if (acc == 0) acc_phase ^= 1u;
             const int count = args.B - j0;               // samples of this thread that exist: the first `count` (may be <= 0)
             const size_t row0 = (size_t)j0 * args.T + t;
+            if (rank != 0) {                             // the first CTA adds up and finishes
+                const uint32_t dst = mapa_shared(sPart + (uint32_t)(rank - 1) * C::PART_BYTES, 0);
+                const uint32_t bar = mapa_shared(part_bar, 0);
+#pragma unroll
+                for (int j = 0; j < NS; j += 4)
+                    st_async_v4(dst + 16u * (uint32_t)((j0 + j) / 4 * BM + tid), r[j], r[j + 1], r[j + 2], r[j + 3], bar);
+                continue;
+            }
             float v[NS];
 #pragma unroll
-            for (int j = 0; j < NS; ++j) v[j] = __uint_as_float(r[j]) + bias;
-            if constexpr (EPI == EPI_BF16 || EPI == EPI_F32) {
-                if (n < args.N) {
+            for (int j = 0; j < NS; ++j) v[j] = __uint_as_float(r[j]);
+            if (args.split > 1) {
+                if (!wait_bounded(part_bar, 0, abort_flag, args.err, args.timeout_ns)) break;
+                mbar_acquire_cluster(part_bar, 0);
+                for (int p = 0; p + 1 < args.split; ++p)
 #pragma unroll
-                    for (int j = 0; j < NS; ++j) {
+                    for (int j = 0; j < NS; j += 4) {
+                        const uint4 q = ld_shared_u4(sPart + (uint32_t)p * C::PART_BYTES +
+                                                     16u * (uint32_t)((j0 + j) / 4 * BM + tid));
+                        v[j] += __uint_as_float(q.x);
+                        v[j + 1] += __uint_as_float(q.y);
+                        v[j + 2] += __uint_as_float(q.z);
+                        v[j + 3] += __uint_as_float(q.w);
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < NS; ++j) v[j] += bias;
+            if constexpr (EPI == EPI_BF16 || EPI == EPI_F32) {
+                using Out = typename std::conditional<EPI == EPI_BF16, __nv_bfloat16, float>::type;
+                if (n < args.N) {
+                    Out* y = reinterpret_cast<Out*>(args.y) + row0 * (size_t)args.N + n;
+                    const size_t step = (size_t)args.T * (size_t)args.N;
+#pragma unroll
+                    for (int j = 0; j < NS; ++j, y += step) {
                         if (j < count) {
-                            const size_t at = (row0 + (size_t)j * args.T) * (size_t)args.N + n;
                             if constexpr (EPI == EPI_BF16)
-                                reinterpret_cast<__nv_bfloat16*>(args.y)[at] = __float2bfloat16_rn(v[j]);
+                                *y = __float2bfloat16_rn(v[j]);
                             else
-                                reinterpret_cast<float*>(args.y)[at] = v[j];
+                                *y = v[j];
                         }
                     }
                 }
@@ -334,8 +394,8 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                                                                 fp8_poison(x[j + 2]) * __uint_as_float(sc.z),
                                                                 fp8_poison(x[j + 3]) * __uint_as_float(sc.w));
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (j + e < count) code[(size_t)(j + e) * step] = (uint8_t)(c >> (8 * e));
+                            for (int e = 0; e < 4; ++e, code += step)
+                                if (j + e < count) *code = (uint8_t)(c >> (8 * e));
                         }
                     }
                     return true;
@@ -351,6 +411,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
 
     tc_fence_before();
     __syncthreads();
+    if (args.split > 1) cluster_sync_all();      // no CTA leaves while another may still write to its memory
     if (warp == 4) {
         tc_fence_after();
         tmem_dealloc(tmem_base, TMEM_COLS);
@@ -358,12 +419,32 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
 }
 
 template <int EPI, bool TRANS, int NB>
-cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const Args& a, int num_sms, cudaStream_t s) {
+cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, Args a, int num_sms, cudaStream_t s) {
     auto k = fp8_stream_kernel<EPI, TRANS, NB>;
     cudaError_t e = smem_attr_once((const void*)k, Cfg<NB>::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    return launch_k(k, dim3((unsigned)(a.tiles < num_sms ? a.tiles : num_sms)), dim3(Cfg<NB>::THREADS), Cfg<NB>::SMEM_BYTES, s, mx, mw,
-                    a);
+    const dim3 block(Cfg<NB>::THREADS);
+    if (a.split == 1) {
+        a.stages = Cfg<NB>::STAGES;
+        const int ctas = a.tiles < num_sms ? a.tiles : num_sms;
+        return launch_k(k, dim3((unsigned)ctas), block, Cfg<NB>::SMEM_BYTES, s, mx, mw, a);
+    }
+    a.stages = (Cfg<NB>::STAGES * Cfg<NB>::STAGE_BYTES - (a.split - 1) * Cfg<NB>::PART_BYTES) / Cfg<NB>::STAGE_BYTES;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.tiles * a.split));
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = Cfg<NB>::SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)a.split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k, mx, mw, a);
 }
 
 template <int EPI, bool TRANS>
@@ -387,6 +468,12 @@ cudaError_t launch_fp8_stream(const Fp8Product& p, const Fp8Device& dev, cudaStr
     a.n_tiles = (p.N + BM - 1) / BM;
     a.kblocks = (p.K + BK - 1) / BK;
     a.tiles = p.T * a.n_tiles;
+    const int groups = (a.kblocks + 3) / 4;
+    a.split = 1, a.groups = groups;
+    for (int c = 2; c <= MAX_SPLIT && (long long)c * a.tiles <= dev.num_sms && c <= groups; c *= 2) {
+        const int each = (groups + c - 1) / c;
+        if ((c - 1) * each < groups) a.split = c, a.groups = each;     // no CTA is left without k-blocks
+    }
     a.xs = p.x.scales, a.xs_ld = p.x.lds;
     a.ws = p.w.scales, a.ws_ld = p.w.lds;
     const int wr = p.trans ? p.N : p.K, wc = p.trans ? p.K : p.N;

@@ -92,6 +92,12 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
 // mbar_wait_bounded that looks at the clock only after some tries: reading the
 // global timer takes longer than most of these waits.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort, int* err,

@@ -372,6 +372,28 @@ def _scales(x):
     return (ref.exponent(v, "e4m3") + 127).to(torch.uint8)
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("B,T,K,N", [(1, 8, 2048, 512), (9, 1, 640, 128), (16, 3, 1500, 200), (30, 1, 8192, 100), (48, 2, 4097, 257),
+                                     (64, 5, 2500, 384), (64, 38, 2048, 128), (2, 39, 2048, 128), (2, 77, 1024, 128)])
+def test_matmul_of_few_samples_and_tiles(B, T, K, N, trans, out):
+    """Tiles whose K several thread blocks share: whole and ragged shares, and the counts of tiles around which the rule turns."""
+    test_matmul(B, T, K, N, trans, out)
+
+
+def test_matmul_of_shared_k_is_repeatable():
+    x, w = act((40, 8, 2048), 50), weight(8, 2048, 512, 51)
+    y = fp8_matmul(x, w, None, "f32")
+    for _ in range(20):
+        assert torch.equal(fp8_matmul(x, w, None, "f32"), y)
+    ok()
+
+
+@pytest.mark.parametrize("B,T,D,F", [(1, 8, 512, 2048), (12, 4, 1040, 256), (33, 2, 2048, 400), (64, 8, 512, 2048)])
+def test_pffn_of_few_samples_and_tiles(B, T, D, F):
+    test_pffn_forward_and_backward_stage_by_stage(B, T, D, F)
+
+
 @pytest.mark.parametrize("B", [6, 40, 300])
 def test_pffn_with_hidden_values_of_any_size(B):
     """Hidden pre-activations from 1e-12 to 1e9 (rows of any exponent, far above and below where GELU bends), rows of
