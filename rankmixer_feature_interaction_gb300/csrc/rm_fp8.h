@@ -52,7 +52,9 @@ struct Fp8Product {
     bool follows = false;       // launched right after another kernel of the same call (which waited for its
                                 // own predecessor before this one could start): W is in memory already
 };
-// Up to this many samples the weights are streamed past all of them at once (launch_fp8_stream).
+// Up to this many samples the weights are streamed past all of them at once (launch_fp8_stream), without
+// the tiles' 256 rows: at 64 samples T = 32, K = 1536, N = 6144 takes 68 us against 76, T = 8, K = 512,
+// N = 2048 10.9 against 13.0; at 65, where the tiles take 76 too, their rows hold twice as many samples.
 constexpr int kFp8StreamMaxB = 64;
 bool fp8_streams(const Fp8Product& p);
 cudaError_t launch_fp8_stream(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s);

@@ -11,11 +11,19 @@
 //   warp 1       MMA issuer (tcgen05.mma kind::mxf8f6f4, M = 128, N = NB, one CTA)
 //   warp 2       scales (as in rm_fp8_gemm.cu: words of four k-blocks' exponents)
 //   warp 3       TMA producer of x
-//   warps 4-7 (and 8-11 for 64 samples)  epilogue: a thread owns one column n of
-//                16 or 32 samples; an 8-bit output's block of 128 columns is four
+//   warps 4-7 (and 8-11 for more than 16 samples)  epilogue: a thread owns one
+//                column n of 16 or 32 samples; an 8-bit output's block of 128 columns is four
 //                warps' threads, whose largest values meet in a warp maximum and
 //                four words of shared memory; one thread per sample then makes the
 //                scale that the others read
+// A CTA walks all of its tile's K by itself, so where the tiles are few, most SMs
+// would idle: then 2 or 4 CTAs (a cluster) each take a part of K.  The first one's
+// epilogue adds the others' sums, which they store straight from registers into
+// what its ring leaves free of its shared memory; always in the same order.
+// Measured (within a graph): T = 32, K = 1536, N = 6144, bf16 out, one sample 48.3
+// us = 6.3 TB/s of W, 64 samples 54 us; K = 6144, N = 1536 (384 tiles, 2.5 rounds of
+// the SMs) 53.5 and 55.6 us.  Few tiles are bound by latency: T = 8, K = 512, N =
+// 2048 3.1 us, K = 2048, N = 512 (32 tiles) 4.8 us, 7.1 without sharing K.
 // The kernel is launched while its predecessor may still run.  Where that
 // predecessor is one of this library's own launches of the same call, W was in
 // memory before it began, and warp 0 starts on it at once; everything else
@@ -60,7 +68,9 @@ struct Cfg {
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
     static constexpr int FIT = (200 * 1024) / STAGE_BYTES;
     static constexpr int STAGES = FIT < 12 ? FIT : 12;
-    static constexpr int EPI_WARPS = NB == 64 ? 8 : 4;
+    // FFN of T = 8, D = 512, F = 2048: 32 samples 12.4 us with 4 warps, 11.7 with 8;
+    // 64 samples 14.25 with 8 or 16, but T = 32, D = 1536, F = 6144 113 with 8, 116 with 16
+    static constexpr int EPI_WARPS = NB == 16 ? 4 : 8;
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     static constexpr int SAMPLES = NB / (EPI_WARPS / 4);            // per epilogue thread
     static constexpr int PART_BYTES = BM * NB * 4;                  // one CTA's partial sums of a split tile
@@ -113,7 +123,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + x); };
     auto tempty_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 2 + x); };
     const uint32_t meet_bar = bar0 + 8u * (2 * STAGES + 2 * SF_SLOTS + 4);
-    const uint32_t part_bar = meet_bar + 16u;
+    const uint32_t part_bar = meet_bar + 8u * (EPI_WARPS / 4);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (part_bar + 8u - base));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -133,7 +143,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             mbar_init(tfull_bar(x), 1);
             mbar_init(tempty_bar(x), EPI_WARPS);
         }
-        for (int g = 0; g < 2; ++g) mbar_init(meet_bar + 8u * g, 4);
+        for (int g = 0; g < EPI_WARPS / 4; ++g) mbar_init(meet_bar + 8u * g, 4);
         mbar_init(part_bar, 1);                   // the other CTAs' partial sums
         *abort_flag = 0;
         fence_mbar_init();
@@ -449,6 +459,7 @@ cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, Args a, int num_sm
 
 template <int EPI, bool TRANS>
 cudaError_t run_for(const CUtensorMap& mx, const CUtensorMap& mw, const Args& a, int num_sms, cudaStream_t s) {
+    // the MMA's N; T = 8, K = 512, N = 2048, one sample: 3.2 us with 16, 3.6 with 32, 4.2 with 64
     if (a.B <= 16) return run<EPI, TRANS, 16>(mx, mw, a, num_sms, s);
     if (a.B <= 32) return run<EPI, TRANS, 32>(mx, mw, a, num_sms, s);
     return run<EPI, TRANS, 64>(mx, mw, a, num_sms, s);
