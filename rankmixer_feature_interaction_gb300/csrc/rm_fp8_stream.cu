@@ -44,8 +44,11 @@ constexpr int BM = 128, BK = 128;
 constexpr int W_BYTES = BM * BK;
 constexpr int SF_SLOTS = 4, SF_BYTES = 1024;
 constexpr int TMEM_COLS = 256, SF_COL = 192;
-// Where the tiles are fewer than half of the SMs, 2 or 4 CTAs share each tile's K.
-constexpr int MAX_SPLIT = 4;
+// Where the tiles are at most half of the SMs, 2 or 4 CTAs share each tile's K; only 2
+// for more than 32 samples, whose sums (32 KB from each CTA into one) take longer than
+// the shorter K saves: T = 8, K = 2048, N = 512, 64 samples 6.9 us with 4, 6.5 with 2,
+// 7.6 with 1; 16 samples 4.6 with 4, 7.1 with 1.
+constexpr int MAX_SPLIT = 4, MAX_SPLIT_64 = 2;
 
 // Four words to another CTA's shared memory, counted there by its barrier.
 __device__ __forceinline__ void st_async_v4(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t bar) {
@@ -77,7 +80,7 @@ struct Cfg {
     static constexpr int RED_BYTES = 2 * (4 + 1) * NB * 4;          // [output][warp of the block, then the scale][sample]
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SF_SLOTS * SF_BYTES + RED_BYTES + 512;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-    static_assert((MAX_SPLIT - 1) * PART_BYTES <= STAGES * STAGE_BYTES / 2, "half of the ring remains when K is split");
+    static_assert(((NB > 32 ? MAX_SPLIT_64 : MAX_SPLIT) - 1) * PART_BYTES <= STAGES * STAGE_BYTES / 2, "half of the ring remains when K is split");
     static_assert(2 * NB <= SF_COL, "two accumulators below the scales");
 };
 
@@ -481,7 +484,8 @@ cudaError_t launch_fp8_stream(const Fp8Product& p, const Fp8Device& dev, cudaStr
     a.tiles = p.T * a.n_tiles;
     const int groups = (a.kblocks + 3) / 4;
     a.split = 1, a.groups = groups;
-    for (int c = 2; c <= MAX_SPLIT && (long long)c * a.tiles <= dev.num_sms && c <= groups; c *= 2) {
+    const int most = p.B > 32 ? MAX_SPLIT_64 : MAX_SPLIT;
+    for (int c = 2; c <= most && (long long)c * a.tiles <= dev.num_sms && c <= groups; c *= 2) {
         const int each = (groups + c - 1) / c;
         if ((c - 1) * each < groups) a.split = c, a.groups = each;     // no CTA is left without k-blocks
     }
