@@ -52,10 +52,11 @@ struct Fp8Product {
     bool follows = false;       // launched right after another kernel of the same call (which waited for its
                                 // own predecessor before this one could start): W is in memory already
 };
-// Up to this many samples the weights are streamed past all of them at once (launch_fp8_stream), without
-// the tiles' 256 rows: at 64 samples T = 32, K = 1536, N = 6144 takes 68 us against 76, T = 8, K = 512,
-// N = 2048 10.9 against 13.0; at 65, where the tiles take 76 too, their rows hold twice as many samples.
-constexpr int kFp8StreamMaxB = 64;
+// Up to this many samples the weights are streamed past all of them at once (launch_fp8_stream) instead of
+// in tiles of 256 samples: at 64 samples T = 32, K = 1536, N = 6144 takes 54 us against 64, at 128 61 against
+// 66.5; T = 8, K = 512, N = 2048 takes 3.5 and 4.1 us against 6.4 and 7.0.  (Only a training step's first
+// layer loses, at 72 samples of T = 32, D = 1536, F = 6144: 137 us against 133 for both layers.)
+constexpr int kFp8StreamMaxB = 128;
 bool fp8_streams(const Fp8Product& p);
 cudaError_t launch_fp8_stream(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s);
 cudaError_t launch_fp8_product(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s);

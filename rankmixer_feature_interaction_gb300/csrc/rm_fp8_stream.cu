@@ -11,8 +11,8 @@
 //   warp 1       MMA issuer (tcgen05.mma kind::mxf8f6f4, M = 128, N = NB, one CTA)
 //   warp 2       scales (as in rm_fp8_gemm.cu: words of four k-blocks' exponents)
 //   warp 3       TMA producer of x
-//   warps 4-7 (and 8-11 for more than 16 samples)  epilogue: a thread owns one
-//                column n of 16 or 32 samples; an 8-bit output's block of 128 columns is four
+//   warps 4-7 (to 11 for more than 16 samples, to 19 for more than 64)  epilogue: a
+//                thread owns one column n of 16 or 32 samples; an 8-bit output's block of 128 columns is four
 //                warps' threads, whose largest values meet in a warp maximum and
 //                four words of shared memory; one thread per sample then makes the
 //                scale that the others read
@@ -21,7 +21,7 @@
 // epilogue adds the others' sums, which they store straight from registers into
 // what its ring leaves free of its shared memory; always in the same order.
 // Measured (within a graph): T = 32, K = 1536, N = 6144, bf16 out, one sample 48.3
-// us = 6.3 TB/s of W, 64 samples 54 us; K = 6144, N = 1536 (384 tiles, 2.5 rounds of
+// us = 6.3 TB/s of W, 64 samples 54 us, 128 samples 61 us; K = 6144, N = 1536 (384 tiles, 2.5 rounds of
 // the SMs) 53.5 and 55.6 us.  Few tiles are bound by latency: T = 8, K = 512, N =
 // 2048 3.1 us, K = 2048, N = 512 (32 tiles) 4.8 us, 7.1 without sharing K.
 // The kernel is launched while its predecessor may still run.  Where that
@@ -43,7 +43,6 @@ namespace f8s {
 constexpr int BM = 128, BK = 128;
 constexpr int W_BYTES = BM * BK;
 constexpr int SF_SLOTS = 4, SF_BYTES = 1024;
-constexpr int TMEM_COLS = 256, SF_COL = 192;
 // Where the tiles are at most half of the SMs, 2 or 4 CTAs share each tile's K; only 2
 // for more than 32 samples, whose sums (32 KB from each CTA into one) take longer than
 // the shorter K saves: T = 8, K = 2048, N = 512, 64 samples 6.9 us with 4, 6.5 with 2,
@@ -73,7 +72,8 @@ struct Cfg {
     static constexpr int STAGES = FIT < 12 ? FIT : 12;
     // FFN of T = 8, D = 512, F = 2048: 32 samples 12.4 us with 4 warps, 11.7 with 8;
     // 64 samples 14.25 with 8 or 16, but T = 32, D = 1536, F = 6144 113 with 8, 116 with 16
-    static constexpr int EPI_WARPS = NB == 16 ? 4 : 8;
+    static constexpr int EPI_WARPS = NB == 16 ? 4 : NB == 128 ? 16 : 8;
+    static constexpr int TMEM_COLS = NB == 128 ? 512 : 256, SF_COL = NB == 128 ? 256 : 192;
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     static constexpr int SAMPLES = NB / (EPI_WARPS / 4);            // per epilogue thread
     static constexpr int PART_BYTES = BM * NB * 4;                  // one CTA's partial sums of a split tile
@@ -154,7 +154,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             mbar_arrive_expect_tx(part_bar, (uint32_t)(args.split - 1) * C::PART_BYTES);
     }
     if (warp == 4) {
-        tmem_alloc(smem_u32(tmem_holder), TMEM_COLS);
+        tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -213,7 +213,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             tc_fence_after();
             const uint32_t d = tmem_base + (uint32_t)(acc * NB);
             for (int kb = kb0; kb < kb1; ++kb) {
-                const uint32_t sf = tmem_base + SF_COL + 8u * slot;
+                const uint32_t sf = tmem_base + C::SF_COL + 8u * slot;
                 if ((kb & 3) == 0) {
                     if (!wait_bounded(sfull_bar(slot), sphase, abort_flag, args.err, args.timeout_ns)) {
                         ok = false;
@@ -294,7 +294,8 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             if (!wait_bounded(sempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
             const uint32_t dst = sSF + slot * SF_BYTES + 16u * lane;
             st_shared_v4(dst, now.w, now.w, now.w, now.w);
-            st_shared_v4(dst + 512, now.x[0], NB > 32 ? now.x[(NB > 32)] : 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+            st_shared_v4(dst + 512, now.x[0], NB > 32 ? now.x[(NB > 32)] : 0x7f7f7f7fu, NB > 64 ? now.x[2 * (NB > 64)] : 0x7f7f7f7fu,
+                         NB > 64 ? now.x[3 * (NB > 64)] : 0x7f7f7f7fu);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(sfull_bar(slot));
@@ -427,7 +428,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     if (args.split > 1) cluster_sync_all();      // no CTA leaves while another may still write to its memory
     if (warp == 4) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, TMEM_COLS);
+        tmem_dealloc(tmem_base, C::TMEM_COLS);
     }
 }
 
@@ -465,7 +466,8 @@ cudaError_t run_for(const CUtensorMap& mx, const CUtensorMap& mw, const Args& a,
     // the MMA's N; T = 8, K = 512, N = 2048, one sample: 3.2 us with 16, 3.6 with 32, 4.2 with 64
     if (a.B <= 16) return run<EPI, TRANS, 16>(mx, mw, a, num_sms, s);
     if (a.B <= 32) return run<EPI, TRANS, 32>(mx, mw, a, num_sms, s);
-    return run<EPI, TRANS, 64>(mx, mw, a, num_sms, s);
+    if (a.B <= 64) return run<EPI, TRANS, 64>(mx, mw, a, num_sms, s);
+    return run<EPI, TRANS, 128>(mx, mw, a, num_sms, s);
 }
 
 }  // namespace f8s
@@ -502,7 +504,7 @@ cudaError_t launch_fp8_stream(const Fp8Product& p, const Fp8Device& dev, cudaStr
     a.timeout_ns = dev.timeout_ns;
     CUtensorMap mx, mw;
     const auto u8t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    const int rows = p.B <= 16 ? 16 : p.B <= 32 ? 32 : 64;
+    const int rows = p.B <= 16 ? 16 : p.B <= 32 ? 32 : p.B <= 64 ? 64 : 128;
     if (!fp8_tensor_map(&mx, u8t, p.x.codes, p.K, p.B, p.T, p.T * p.x.ld, p.x.ld, BK, rows) ||
         !fp8_tensor_map(&mw, u8t, p.w.codes, wc, wr, p.T, p.w.ld, (long long)wr * p.w.ld, 128, 128))
         return cudaErrorInvalidValue;
