@@ -641,7 +641,7 @@ cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap&
 
 cudaError_t launch_fp8_product(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s) {
     using namespace f8;
-    if (fp8_streams(p)) return launch_fp8_stream(p, dev, s);
+    if (fp8_streams(p, dev)) return launch_fp8_stream(p, dev, s);
     Args a{};
     a.B = p.B, a.T = p.T, a.K = p.K, a.N = p.N;
     a.m_tiles = (p.B + 2 * BM - 1) / (2 * BM);

@@ -12,18 +12,21 @@
 //   warp 2       scales (as in rm_fp8_gemm.cu: words of four k-blocks' exponents)
 //   warp 3       TMA producer of x
 //   warps 4-7 (to 11 for more than 16 samples, to 19 for more than 64)  epilogue: a
-//                thread owns one column n of 16 or 32 samples; an 8-bit output's block of 128 columns is four
-//                warps' threads, whose largest values meet in a warp maximum and
-//                four words of shared memory; one thread per sample then makes the
-//                scale that the others read
+//                thread owns one column n of 16 or 32 samples; an 8-bit output's
+//                block of 128 columns is four warps' threads, whose largest values
+//                meet in a warp maximum and four words of shared memory; one thread
+//                per sample then makes the scale that the others read
 // A CTA walks all of its tile's K by itself, so where the tiles are few, most SMs
 // would idle: then 2 or 4 CTAs (a cluster) each take a part of K.  The first one's
 // epilogue adds the others' sums, which they store straight from registers into
 // what its ring leaves free of its shared memory; always in the same order.
+// More than 128 samples come here, as several tiles of samples, only where all tiles
+// fit on the SMs at once.
 // Measured (within a graph): T = 32, K = 1536, N = 6144, bf16 out, one sample 48.3
-// us = 6.3 TB/s of W, 64 samples 54 us, 128 samples 61 us; K = 6144, N = 1536 (384 tiles, 2.5 rounds of
-// the SMs) 53.5 and 55.6 us.  Few tiles are bound by latency: T = 8, K = 512, N =
-// 2048 3.1 us, K = 2048, N = 512 (32 tiles) 4.8 us, 7.1 without sharing K.
+// us = 6.3 TB/s of W, 64 samples 54 us, 128 samples 61 us; K = 6144, N = 1536 (384
+// tiles, 2.5 rounds of the SMs) 53.5, 55.6 and 59.5 us.  Few tiles are bound by
+// latency: T = 8, K = 512, N = 2048 3.1 us, K = 2048, N = 512 (32 tiles) 4.8 us, 7.1
+// without sharing K.
 // The kernel is launched while its predecessor may still run.  Where that
 // predecessor is one of this library's own launches of the same call, W was in
 // memory before it began, and warp 0 starts on it at once; everything else
@@ -41,6 +44,7 @@ namespace rm {
 namespace f8s {
 
 constexpr int BM = 128, BK = 128;
+constexpr int SAMPLES_MAX = 128;             // of a tile
 constexpr int W_BYTES = BM * BK;
 constexpr int SF_SLOTS = 4, SF_BYTES = 1024;
 // Where the tiles are at most half of the SMs, 2 or 4 CTAs share each tile's K; only 2
@@ -88,7 +92,7 @@ enum Epi { EPI_BF16, EPI_F32, EPI_GELU, EPI_GELU_KEEP };
 
 struct Args {
     int B, T, K, N;
-    int n_tiles, kblocks, tiles;
+    int n_tiles, m_tiles, kblocks, tiles;
     int split, groups;                   // CTAs (a cluster) that share a tile's K; groups of four k-blocks for each
     int stages;                          // of the ring; what a split's partial sums take is not part of it
     const uint8_t* xs;
@@ -104,6 +108,22 @@ struct Args {
     int* err;
     unsigned long long timeout_ns;
 };
+
+struct Tile {
+    int t, n0, b0;
+};
+// Sample tiles fastest: those that share a weight tile run side by side.
+__device__ __forceinline__ Tile tile_of(int i, const Args& a) {
+    Tile r{0, 0, 0};
+    if (a.m_tiles > 1) {
+        const int q = i / a.m_tiles;
+        r.b0 = (i - q * a.m_tiles) * SAMPLES_MAX;
+        i = q;
+    }
+    r.t = i / a.n_tiles;
+    r.n0 = (i - r.t * a.n_tiles) * BM;
+    return r;
+}
 
 template <int EPI, bool TRANS, int NB>
 __global__ void __launch_bounds__(Cfg<NB>::THREADS, 1)
@@ -178,7 +198,8 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         uint32_t phase = 0;
         bool ok = true;
         for (int i = unit; ok && i < args.tiles; i += units) {
-            const int t = i / args.n_tiles, n0 = (i - t * args.n_tiles) * BM;
+            const Tile tl = tile_of(i, args);
+            const int t = tl.t, n0 = tl.n0;
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
                     ok = false;
@@ -193,7 +214,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                             tma_load_3d(&tmW, sW + stage * W_BYTES, full_bar(stage), n0, kb * BK, t);
                     } else {
                         mbar_arrive_expect_tx(full_bar(stage), C::X_BYTES);
-                        tma_load_3d(&tmX, sX + stage * C::X_BYTES, full_bar(stage), kb * BK, 0, t);
+                        tma_load_3d(&tmX, sX + stage * C::X_BYTES, full_bar(stage), kb * BK, tl.b0, t);
                     }
                 }
                 __syncwarp();
@@ -260,11 +281,12 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             uint32_t x[(NB + 31) / 32], w;
         };
         auto load = [&](int i, int g) {
-            const int t = i / args.n_tiles, nb = i - t * args.n_tiles;
+            const Tile tl = tile_of(i, args);
+            const int t = tl.t, nb = tl.n0 / BM;
             Words r;
 #pragma unroll
             for (int j = 0; j < (NB + 31) / 32; ++j) {
-                const int b = 32 * j + lane;
+                const int b = tl.b0 + 32 * j + lane;
                 r.x[j] = 0x7f7f7f7fu;
                 if (b < args.B)
                     r.x[j] = __ldg(reinterpret_cast<const uint32_t*>(args.xs + ((size_t)b * args.T + t) *
@@ -318,7 +340,8 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             return ok;
         };
         for (int i = unit; i < args.tiles; i += units) {
-            const int t = i / args.n_tiles, n0 = (i - t * args.n_tiles) * BM, n = n0 + tid;
+            const Tile tl = tile_of(i, args);
+            const int t = tl.t, n0 = tl.n0, n = n0 + tid;
             const float bias = args.bias && n < args.N ? __ldg(args.bias + (size_t)t * args.N + n) : 0.f;
             if (!wait_bounded(tfull_bar(acc), acc_phase, abort_flag, args.err, args.timeout_ns)) break;
             tc_fence_after();
@@ -334,8 +357,8 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             if (lane == 0) mbar_arrive(tempty_bar(acc));
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
-            const int count = args.B - j0;               // samples of this thread that exist: the first `count` (may be <= 0)
-            const size_t row0 = (size_t)j0 * args.T + t;
+            const int count = args.B - tl.b0 - j0;               // samples of this thread that exist: the first `count` (may be <= 0)
+            const size_t row0 = (size_t)(tl.b0 + j0) * args.T + t;
             if (rank != 0) {                             // the first CTA adds up and finishes
                 const uint32_t dst = mapa_shared(sPart + (uint32_t)(rank - 1) * C::PART_BYTES, 0);
                 const uint32_t bar = mapa_shared(part_bar, 0);
@@ -472,9 +495,15 @@ cudaError_t run_for(const CUtensorMap& mx, const CUtensorMap& mw, const Args& a,
 
 }  // namespace f8s
 
-bool fp8_streams(const Fp8Product& p) {
-    const long long tiles = (long long)p.T * ((p.N + f8s::BM - 1) / f8s::BM);
-    return p.B <= kFp8StreamMaxB && p.epi != FP8_DGELU && tiles < (1ll << 30);
+static long long stream_tiles(const Fp8Product& p) {
+    const long long m = (p.B + f8s::SAMPLES_MAX - 1) / f8s::SAMPLES_MAX;
+    return m * p.T * ((p.N + f8s::BM - 1) / f8s::BM);
+}
+
+bool fp8_streams(const Fp8Product& p, const Fp8Device& dev) {
+    const long long tiles = stream_tiles(p);
+    if (p.epi == FP8_DGELU || tiles >= (1ll << 30)) return false;
+    return p.B <= kFp8StreamMaxB || tiles <= dev.num_sms;
 }
 
 cudaError_t launch_fp8_stream(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s) {
@@ -483,7 +512,8 @@ cudaError_t launch_fp8_stream(const Fp8Product& p, const Fp8Device& dev, cudaStr
     a.B = p.B, a.T = p.T, a.K = p.K, a.N = p.N;
     a.n_tiles = (p.N + BM - 1) / BM;
     a.kblocks = (p.K + BK - 1) / BK;
-    a.tiles = p.T * a.n_tiles;
+    a.m_tiles = (p.B + SAMPLES_MAX - 1) / SAMPLES_MAX;
+    a.tiles = (int)stream_tiles(p);
     const int groups = (a.kblocks + 3) / 4;
     a.split = 1, a.groups = groups;
     const int most = p.B > 32 ? MAX_SPLIT_64 : MAX_SPLIT;

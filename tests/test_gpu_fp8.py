@@ -436,6 +436,36 @@ def test_pffn_with_hidden_values_of_any_size(B):
     ok()
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("B,T,K,N", [(130, 64, 200, 257), (257, 40, 1000, 130), (333, 20, 272, 520), (513, 31, 128, 264),
+                                     (1000, 76, 96, 16)])
+def test_matmul_of_many_tiles(B, T, K, N, trans, out):
+    """More samples than are streamed past the weights, in more tiles than thread blocks fit on the device at once."""
+    test_matmul(B, T, K, N, trans, out)
+
+
+def test_matmul_of_many_tiles_applies_every_exponent_and_keeps_nan():
+    B, T, K, N = 2500, 2, 520, 400
+    g = gen(52)
+    one = torch.ones(1).to(torch.float8_e4m3fn).view(torch.uint8).item()
+    E = torch.randint(125, 130, (B, T, 8), generator=g, dtype=torch.uint8)
+    Ew = torch.randint(125, 130, (T, 5, 4), generator=g, dtype=torch.uint8)
+    x = Fp8Tensor(torch.full((B, T, 528), one, dtype=torch.uint8).view(torch.float8_e4m3fn).to(DEV), E.to(DEV), K)
+    w = Fp8Tensor(torch.full((T, K, N), one, dtype=torch.uint8).view(torch.float8_e4m3fn).to(DEV), Ew.to(DEV), N)
+    assert torch.equal(fp8_matmul(x, w, None, "f32").double(), ref.matmul(ref.value(x), ref.weight_value(w)))
+    test_matmul_keeps_nan_in_its_row_and_reads_no_padding(5000)
+
+
+@pytest.mark.parametrize("B,T,D,F", [(300, 64, 128, 256), (257, 80, 80, 272), (513, 32, 160, 144)])
+def test_pffn_of_many_tiles(B, T, D, F):
+    test_pffn_forward_and_backward_stage_by_stage(B, T, D, F)
+
+
+def test_pffn_of_many_tiles_with_hidden_values_of_any_size():
+    test_pffn_with_hidden_values_of_any_size(9800)
+
+
 def test_the_example_learns():
     from examples.pffn_8bit import train
     r = train(B=300, T=4, D=128, k=2, steps=60)
