@@ -39,7 +39,9 @@ struct Fp8Device {
 // acc[b][t][n] = sum_k x[b][t][k] W[t][k][n] (trans: W[t][n][k]), then
 //   FP8_OUT_*:  y = acc + bias (bias nullable)
 //   FP8_GELU:   u = acc + bias; o0 = Q(Gelu(u)) and, where o1.codes is not null, o1 = Q(u)
-//   FP8_DGELU:  dU = acc Gelu'(u) with u read from o1; o0 = Q(dU), y = dU in bf16
+//   FP8_DGELU:  dU = acc Gelu'(u) with u read from o1; o0 = Q(dU), y = dU in bf16 (the operand
+//               of dW1: at most 2^-8 of each value, as large as a bf16 gradient's own rounding, where
+//               Q(dU) would be off by up to 2^-4 and float32 halve that product's rate)
 enum Fp8Epilogue { FP8_OUT_BF16, FP8_OUT_F32, FP8_GELU, FP8_DGELU };
 struct Fp8Product {
     Fp8Epilogue epi;

@@ -6,10 +6,12 @@
 // in a row), agree on its largest magnitude with three shuffles and write twice 8
 // bytes of codes.  64 bytes per thread are loaded before the first is used and stay
 // as they came (bf16 pairs) until then: few registers, so many warps, are what
-// hides the loads' latency, and few instructions per value what lets them.  Rows that are not 16-byte aligned are read
-// an element at a time, neighbouring lanes neighbouring elements, and their
-// codes pass through shared memory to the same 8-byte stores; restoring such
-// rows mirrors that.
+// hides the loads' latency, and few instructions per value what lets them.  Rows
+// that are not 16-byte aligned are read an element at a time, neighbouring lanes
+// neighbouring elements, and their codes pass through shared memory to the same
+// 8-byte stores; restoring such rows mirrors that.
+// Measured, 65,536 rows of 6144 in bf16 (805 MB; 406 MB in 8 bits): saving 185 us,
+// restoring 185 us, 6.5 TB/s each: bound by memory.
 #include "rm_common.cuh"
 #include "rm_fp8.cuh"
 

@@ -84,7 +84,8 @@ struct Cfg {
     static constexpr int RED_BYTES = 2 * (4 + 1) * NB * 4;          // [output][warp of the block, then the scale][sample]
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SF_SLOTS * SF_BYTES + RED_BYTES + 512;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-    static_assert(((NB > 32 ? MAX_SPLIT_64 : MAX_SPLIT) - 1) * PART_BYTES <= STAGES * STAGE_BYTES / 2, "half of the ring remains when K is split");
+    static_assert(((NB > 32 ? MAX_SPLIT_64 : MAX_SPLIT) - 1) * PART_BYTES <= STAGES * STAGE_BYTES / 2,
+                  "half of the ring remains when K is split");
     static_assert(2 * NB <= SF_COL, "two accumulators below the scales");
 };
 
@@ -316,7 +317,8 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             if (!wait_bounded(sempty_bar(slot), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
             const uint32_t dst = sSF + slot * SF_BYTES + 16u * lane;
             st_shared_v4(dst, now.w, now.w, now.w, now.w);
-            st_shared_v4(dst + 512, now.x[0], NB > 32 ? now.x[(NB > 32)] : 0x7f7f7f7fu, NB > 64 ? now.x[2 * (NB > 64)] : 0x7f7f7f7fu,
+            st_shared_v4(dst + 512, now.x[0], NB > 32 ? now.x[(NB > 32)] : 0x7f7f7f7fu,
+                         NB > 64 ? now.x[2 * (NB > 64)] : 0x7f7f7f7fu,
                          NB > 64 ? now.x[3 * (NB > 64)] : 0x7f7f7f7fu);
             fence_proxy_async_smem();
             __syncwarp();
