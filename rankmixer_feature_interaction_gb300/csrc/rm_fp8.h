@@ -62,6 +62,10 @@ struct Fp8Product {
 // tiles) 8.9 us against 10.1, T = 2, K = 256, N = 512, 1000 samples (64 tiles) 3.6 against 5.7; past one tile
 // per SM it loses: T = 8, K = 2048, N = 512, 768 samples (192 tiles) 14.8 us against 11.0.
 constexpr int kFp8StreamMaxB = 128;
+// dU (FP8_DGELU) reads the kept u a byte at a time there and has no table of Gelu', so only up to 32 samples:
+// the backward pass of T = 8, D = 512, F = 2048 takes 28.2 us at 1 sample and 30.3 at 32, against 33.2 and 33.9;
+// T = 32, D = 1536, F = 6144 342 against 354 at 32, but 386 against 367 at 64.
+constexpr int kFp8StreamMaxBdU = 32;
 bool fp8_streams(const Fp8Product& p, const Fp8Device& dev);
 cudaError_t launch_fp8_stream(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s);
 cudaError_t launch_fp8_product(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s);

@@ -329,11 +329,15 @@ rm_status rm_fp8_pffn_backward(const rm_fp8_pffn* p, const void* dV, rm_dtype dv
     RM_CHECK_CUDA(launch_fp8_quantize(f32, dV, rows, D, D, view(w.dv), f32 ? w.dv16 : nullptr, s), "quantize dV");
     Fp8Product g = product(RM_BF16, w.dv, p->W2, true, nullptr, w.du16, B, T, D, F);
     g.epi = FP8_DGELU;
+    g.follows = true;
     g.o0 = view(w.du);
     g.o1 = view(kept->u);
     RM_CHECK_CUDA(launch_fp8_product(g, dev, s), "dU");
-    if (dX)
-        RM_CHECK_CUDA(launch_fp8_product(product(dx_dtype, w.du, p->W1, true, nullptr, dX, B, T, F, D), dev, s), "dX");
+    if (dX) {
+        g = product(dx_dtype, w.du, p->W1, true, nullptr, dX, B, T, F, D);
+        g.follows = true;
+        RM_CHECK_CUDA(launch_fp8_product(g, dev, s), "dX");
+    }
     RM_CHECK_CUDA(launch_fp8_wgrad(view(kept->a), dv16, grads->dW2, grads->db2, g32, B, T, F, D, dev, s), "dW2");
     RM_CHECK_CUDA(launch_fp8_wgrad(view(kept->x), w.du16, grads->dW1, grads->db1, g32, B, T, D, F, dev, s), "dW1");
     return RM_OK;

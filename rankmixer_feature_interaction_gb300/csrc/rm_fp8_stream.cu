@@ -89,7 +89,7 @@ struct Cfg {
     static_assert(2 * NB <= SF_COL, "two accumulators below the scales");
 };
 
-enum Epi { EPI_BF16, EPI_F32, EPI_GELU, EPI_GELU_KEEP };
+enum Epi { EPI_BF16, EPI_F32, EPI_GELU, EPI_GELU_KEEP, EPI_DGELU };
 
 struct Args {
     int B, T, K, N;
@@ -345,6 +345,21 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             const Tile tl = tile_of(i, args);
             const int t = tl.t, n0 = tl.n0, n = n0 + tid;
             const float bias = args.bias && n < args.N ? __ldg(args.bias + (size_t)t * args.N + n) : 0.f;
+            const int count = args.B - tl.b0 - j0;       // samples of this thread that exist: the first `count` (may be <= 0)
+            const size_t row0 = (size_t)(tl.b0 + j0) * args.T + t;
+            uint32_t u[EPI == EPI_DGELU ? NS / 2 : 1];   // DGELU: two samples' kept u a word, code and exponent byte each
+            if constexpr (EPI == EPI_DGELU) {
+                const uint8_t* code = args.o1.codes + row0 * (size_t)args.o1.ld + n;
+                const uint8_t* scale = args.o1.scales + row0 * (size_t)args.o1.lds + n0 / kFp8Block;
+#pragma unroll
+                for (int j = 0; j < NS; ++j) {
+                    uint32_t w = 127u << 8;
+                    if (rank == 0 && j < count && n < args.N) w = __ldg(code) | (uint32_t)__ldg(scale) << 8;
+                    u[j / 2] = j % 2 ? u[j / 2] | w << 16 : w;
+                    code += (size_t)args.T * (size_t)args.o1.ld;
+                    scale += (size_t)args.T * (size_t)args.o1.lds;
+                }
+            }
             if (!wait_bounded(tfull_bar(acc), acc_phase, abort_flag, args.err, args.timeout_ns)) break;
             tc_fence_after();
             uint32_t r[NS];
@@ -359,8 +374,6 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             if (lane == 0) mbar_arrive(tempty_bar(acc));
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
-            const int count = args.B - tl.b0 - j0;               // samples of this thread that exist: the first `count` (may be <= 0)
-            const size_t row0 = (size_t)(tl.b0 + j0) * args.T + t;
             if (rank != 0) {                             // the first CTA adds up and finishes
                 const uint32_t dst = mapa_shared(sPart + (uint32_t)(rank - 1) * C::PART_BYTES, 0);
                 const uint32_t bar = mapa_shared(part_bar, 0);
@@ -386,24 +399,33 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                         v[j + 3] += __uint_as_float(q.w);
                     }
             }
+            if constexpr (EPI == EPI_DGELU) {
 #pragma unroll
-            for (int j = 0; j < NS; ++j) v[j] += bias;
-            if constexpr (EPI == EPI_BF16 || EPI == EPI_F32) {
-                using Out = typename std::conditional<EPI == EPI_BF16, __nv_bfloat16, float>::type;
+                for (int j = 0; j < NS; ++j) {
+                    const uint32_t w = u[j / 2] >> (16 * (j % 2));
+                    v[j] *= fp8_gelu_grad(fp8_unpack2<false>(w & 0xffu).x * fp8_scale(w >> 8 & 0xffu));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NS; ++j) v[j] += bias;
+            }
+            if constexpr (EPI == EPI_BF16 || EPI == EPI_F32 || EPI == EPI_DGELU) {
+                using Out = typename std::conditional<EPI == EPI_F32, float, __nv_bfloat16>::type;
                 if (n < args.N) {
                     Out* y = reinterpret_cast<Out*>(args.y) + row0 * (size_t)args.N + n;
                     const size_t step = (size_t)args.T * (size_t)args.N;
 #pragma unroll
                     for (int j = 0; j < NS; ++j, y += step) {
                         if (j < count) {
-                            if constexpr (EPI == EPI_BF16)
-                                *y = __float2bfloat16_rn(v[j]);
-                            else
+                            if constexpr (EPI == EPI_F32)
                                 *y = v[j];
+                            else
+                                *y = __float2bfloat16_rn(v[j]);
                         }
                     }
                 }
-            } else {
+            }
+            if constexpr (EPI == EPI_GELU || EPI == EPI_GELU_KEEP || EPI == EPI_DGELU) {
                 // one 8-bit output: the largest magnitudes of each sample's 128 columns meet,
                 // thread j makes sample j's scale, all round by it
                 auto save = [&](const Fp8View& out, float (&x)[NS], uint32_t* m) {
@@ -441,8 +463,10 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 };
                 if constexpr (EPI == EPI_GELU_KEEP)
                     if (!save(args.o1, v, red + 5 * NB)) break;
+                if constexpr (EPI != EPI_DGELU) {
 #pragma unroll
-                for (int j = 0; j < NS; ++j) v[j] = fp8_gelu(v[j]);
+                    for (int j = 0; j < NS; ++j) v[j] = fp8_gelu(v[j]);
+                }
                 if (!save(args.o0, v, red)) break;
             }
         }
@@ -490,9 +514,11 @@ template <int EPI, bool TRANS>
 cudaError_t run_for(const CUtensorMap& mx, const CUtensorMap& mw, const Args& a, int num_sms, cudaStream_t s) {
     // the MMA's N; T = 8, K = 512, N = 2048, one sample: 3.2 us with 16, 3.6 with 32, 4.2 with 64
     if (a.B <= 16) return run<EPI, TRANS, 16>(mx, mw, a, num_sms, s);
-    if (a.B <= 32) return run<EPI, TRANS, 32>(mx, mw, a, num_sms, s);
-    if (a.B <= 64) return run<EPI, TRANS, 64>(mx, mw, a, num_sms, s);
-    return run<EPI, TRANS, 128>(mx, mw, a, num_sms, s);
+    if (EPI == EPI_DGELU || a.B <= 32) return run<EPI, TRANS, 32>(mx, mw, a, num_sms, s);
+    if constexpr (EPI != EPI_DGELU) {
+        if (a.B <= 64) return run<EPI, TRANS, 64>(mx, mw, a, num_sms, s);
+        return run<EPI, TRANS, 128>(mx, mw, a, num_sms, s);
+    }
 }
 
 }  // namespace f8s
@@ -504,7 +530,8 @@ static long long stream_tiles(const Fp8Product& p) {
 
 bool fp8_streams(const Fp8Product& p, const Fp8Device& dev) {
     const long long tiles = stream_tiles(p);
-    if (p.epi == FP8_DGELU || tiles >= (1ll << 30)) return false;
+    if (tiles >= (1ll << 30)) return false;
+    if (p.epi == FP8_DGELU) return p.B <= kFp8StreamMaxBdU;
     return p.B <= kFp8StreamMaxB || tiles <= dev.num_sms;
 }
 
@@ -551,6 +578,9 @@ cudaError_t launch_fp8_stream(const Fp8Product& p, const Fp8Device& dev, cudaStr
             if (p.trans) return cudaErrorNotSupported;
             return p.o1.codes ? run_for<EPI_GELU_KEEP, false>(mx, mw, a, dev.num_sms, s)
                               : run_for<EPI_GELU, false>(mx, mw, a, dev.num_sms, s);
+        case FP8_DGELU:
+            if (!p.trans) return cudaErrorNotSupported;
+            return run_for<EPI_DGELU, true>(mx, mw, a, dev.num_sms, s);
         default: return cudaErrorNotSupported;
     }
 }
