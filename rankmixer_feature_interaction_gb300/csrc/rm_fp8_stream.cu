@@ -444,20 +444,21 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                             out.scales[(row0 + (size_t)tid * args.T) * (size_t)out.lds + n0 / kFp8Block] = (uint8_t)E;
                     }
                     if (!all_here()) return false;
-                    if (n < args.N) {
-                        uint8_t* code = out.codes + row0 * (size_t)out.ld + n;
-                        const size_t step = (size_t)args.T * (size_t)out.ld;
+                    // four samples of four neighbouring columns change places among four lanes, so that
+                    // a lane stores four columns of one sample (N is a multiple of 16 here)
+                    uint8_t* code = out.codes + (row0 + (size_t)(lane & 3) * args.T) * (size_t)out.ld + (n & ~3);
+                    const size_t step = 4 * (size_t)args.T * (size_t)out.ld;
+                    const uint32_t pick1 = (lane & 1) ? 0x3715u : 0x6240u, pick2 = (lane & 2) ? 0x3276u : 0x5410u;
 #pragma unroll
-                        for (int j = 0; j < NS; j += 4) {
-                            const uint4 sc = *reinterpret_cast<const uint4*>(scale + j0 + j);
-                            const uint32_t c = fp8_pack4<false>(fp8_poison(x[j]) * __uint_as_float(sc.x),
-                                                                fp8_poison(x[j + 1]) * __uint_as_float(sc.y),
-                                                                fp8_poison(x[j + 2]) * __uint_as_float(sc.z),
-                                                                fp8_poison(x[j + 3]) * __uint_as_float(sc.w));
-#pragma unroll
-                            for (int e = 0; e < 4; ++e, code += step)
-                                if (j + e < count) *code = (uint8_t)(c >> (8 * e));
-                        }
+                    for (int j = 0; j < NS; j += 4, code += step) {
+                        const uint4 sc = *reinterpret_cast<const uint4*>(scale + j0 + j);
+                        uint32_t c = fp8_pack4<false>(fp8_poison(x[j]) * __uint_as_float(sc.x),
+                                                      fp8_poison(x[j + 1]) * __uint_as_float(sc.y),
+                                                      fp8_poison(x[j + 2]) * __uint_as_float(sc.z),
+                                                      fp8_poison(x[j + 3]) * __uint_as_float(sc.w));
+                        c = __byte_perm(c, __shfl_xor_sync(0xffffffffu, c, 1), pick1);
+                        c = __byte_perm(c, __shfl_xor_sync(0xffffffffu, c, 2), pick2);
+                        if (n < args.N && j + (lane & 3) < count) *reinterpret_cast<uint32_t*>(code) = c;
                     }
                     return true;
                 };
