@@ -56,8 +56,8 @@ struct Fp8Product {
 };
 // Up to this many samples the weights are streamed past all of them at once (launch_fp8_stream) instead of
 // in tiles of 256 samples: at 64 samples T = 32, K = 1536, N = 6144 takes 54 us against 64, at 128 61 against
-// 66.5; T = 8, K = 512, N = 2048 takes 3.5 and 4.1 us against 6.4 and 7.0.  (Only a training step's first
-// layer loses, at 72 samples of T = 32, D = 1536, F = 6144: 137 us against 133 for both layers.)
+// 66.5; T = 8, K = 512, N = 2048 takes 3.5 and 4.1 us against 6.4 and 7.0.  (Closest for the
+// training forward, at 72 samples of T = 32, D = 1536, F = 6144: 132 us against 133.)
 // More samples go there too where that makes no more tiles than SMs: T = 8, K = 2048, N = 512, 250 samples (64
 // tiles) 8.9 us against 10.1, T = 2, K = 256, N = 512, 1000 samples (64 tiles) 3.6 against 5.7; past one tile
 // per SM it loses: T = 8, K = 2048, N = 512, 768 samples (192 tiles) 14.8 us against 11.0.
