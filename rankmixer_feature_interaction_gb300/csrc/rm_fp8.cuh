@@ -78,21 +78,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // Gelu(u) = u Phi(u) for the epilogues that hold a row in registers, written as
 // relu(u) - |u| Q(|u|) with the upper tail Q = 1 - Phi.  Q is positive and its
 // logarithm nearly a parabola, so one exponential of a polynomial gives it,
-// Q(x) = 2^P(x): P of degree 6 fitted to log2 Q over [0, 6] for the smallest
-// largest error in Q (a linear program, weights Q ln 2), 1.1e-7; above 6, where
-// Q < 1e-9, x is held at 6.  In float32 the result is within 1.9e-7 |u|.  Ten
-// instructions, every constant an immediate of its own (the rational form needs
-// a reciprocal and an exponential; the packed two-value form needs constants in
-// register pairs, for which 64 held values leave no room).
+// Q(x) = 2^P(x): P of degree 7 fitted to log2 Q over [0, 12.9] (where Q is the
+// smallest normal float) by a linear program, for the smallest largest error in Q,
+// 2.4e-7, under the condition that Q is within 1.5% of itself everywhere: a block
+// of 8-bit outputs is scaled by its own largest value, so where all of its u are far
+// below zero the tail's relative error is what is kept (half a step is 6%).
+// P falls for all x (its leading coefficient is negative) and the exponential
+// flushes below 2^-126, so Gelu goes to zero without a bound on x.  In float32 the
+// result is within 3.5e-7 |u|.  Ten instructions, every constant an immediate of
+// its own (the rational form needs a reciprocal and an exponential; the packed
+// two-value form needs constants in register pairs, for which 64 held values leave
+// no room).
 __device__ __forceinline__ float fp8_gelu(float u) {
-    const float x = fminf(fabsf(u), 6.0f);
-    float p = fmaf(x, 1.91779014e-05f, -6.58627096e-04f);
-    p = fmaf(x, p, 7.75446597e-03f);
-    p = fmaf(x, p, -5.29654577e-02f);
-    p = fmaf(x, p, -4.59060221e-01f);
-    p = fmaf(x, p, -1.15112206f);
-    p = fmaf(x, p, -9.99999693e-01f);
-    return fmaf(-fabsf(u), ex2_approx(p), fmaxf(u, 0.f));
+    const float x = fabsf(u);
+    float p = fmaf(x, -9.30538079e-07f, 4.20015094e-05f);
+    p = fmaf(x, p, -7.80347327e-04f);
+    p = fmaf(x, p, 8.01421981e-03f);
+    p = fmaf(x, p, -5.32146059e-02f);
+    p = fmaf(x, p, -4.58957642e-01f);
+    p = fmaf(x, p, -1.15113652f);
+    p = fmaf(x, p, -9.99999404e-01f);
+    return fmaf(-x, ex2_approx(p), fmaxf(u, 0.f));
 }
 
 // Gelu'(u) = Phi(u) + u phi(u), by Abramowitz & Stegun 7.1.26 (|error of erf| <=
