@@ -487,10 +487,14 @@ RM_API rm_status rm_debug_mix_residual(const void *X, int from_z, float *Y, int 
  * They may be captured into a CUDA graph once any of them has run on that
  * device outside capture (which looks up the device's error word).  Calls on
  * different streams are independent when their buffers (and workspaces) are.
- * Lengths that are summed over (K; B for the weight gradients) are at most
- * 2^27, B T is below 2^31 (RM_ERR_UNSUPPORTED, RM_ERR_INVALID_ARG otherwise).  Device-side errors (a
- * bounded wait that ran out) are latched per device and reported by
- * rm_fp8_sync_status. */
+ * Sums are float32; the tensor cores truncate as they add, so that a long sum
+ * of terms of one sign comes out small.  The lengths summed over are held to
+ * where that loss is below 2^-9: K (D and F of the FFN) is at most 2^19, B of
+ * weight gradients in bf16 at most 2^17.  Weight gradients in float32 join sums
+ * of 2048 samples with rounding to nearest; their B is at most 2^27
+ * (RM_ERR_UNSUPPORTED otherwise).  B T is below 2^31 (RM_ERR_INVALID_ARG
+ * otherwise).  Device-side errors (a bounded wait that ran out) are latched per
+ * device and reported by rm_fp8_sync_status. */
 typedef enum rm_fp8_format {
     RM_E4M3 = 0,
     RM_E5M2 = 1
@@ -531,8 +535,8 @@ RM_API rm_status rm_fp8_matmul(const rm_fp8_tensor *x, const rm_fp8_tensor *W, c
  *   dW[t][k][n] = sum_b x[b][t][k] dY[b][t][n],  db[t][n] = sum_b dY[b][t][n].
  * x: [B][T][K], e4m3; dY: device bf16 [B][T][N], contiguous, N a multiple of 8
  * (RM_ERR_UNSUPPORTED otherwise); dW [T][K][N] and db [T][N] (nullable):
- * device, of dtype, overwritten.  Sums in float32, in an order that depends on
- * the sizes alone. */
+ * device, of dtype, overwritten.  Sums in float32 (bf16 gradients: B at most
+ * 2^17), in an order that depends on the sizes alone. */
 RM_API rm_status rm_fp8_wgrad(const rm_fp8_tensor *x, const void *dY, void *dW, void *db, rm_dtype dtype, int B, int T,
                               int K, int N, void *stream);
 

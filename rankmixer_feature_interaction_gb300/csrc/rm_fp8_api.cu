@@ -39,10 +39,17 @@ Fp8View view(const rm_fp8_tensor& t) {
     return Fp8View{(uint8_t*)t.codes, t.scales, t.ld, t.lds, t.format == RM_E5M2};
 }
 
-// rows are limited so that row and block numbers of every kernel fit 32-bit grids,
-// summed lengths so that one tile's sum stays well inside the bound of the waits
+// rows are limited so that row and block numbers of every kernel fit 32-bit grids
 constexpr long long kMaxRows = 1ll << 31;
-constexpr int kMaxSum = 1 << 27;
+// Summed lengths.  The tensor cores' accumulator truncates as it adds, about a unit
+// in the last place an instruction (32 products, or 16 of the weight gradient), so
+// sums that stay in it are held to lengths at which terms of one sign lose less than
+// 2^-9, below bf16's own rounding: K of the products, and B of bf16 gradients (2^21
+// samples lost 1.2%, 2^17 0.05%).  Float32 gradients join sums of 2048 samples with
+// rounding to nearest; their B only keeps a tile's time well inside the waits' bound.
+constexpr int kMaxK = 1 << 19;
+constexpr int kMaxBatchBf16 = 1 << 17;
+constexpr int kMaxBatch = 1 << 27;
 
 constexpr unsigned long long kWaitTimeoutNs = 2000000000ull;    // bound of every device-side wait
 
@@ -93,13 +100,20 @@ rm_status check_sizes(int B, int T, int K, int N) {
     return RM_OK;
 }
 
+rm_status check_batch(int B, rm_dtype grads) {
+    if (B > kMaxBatch) return fail(RM_ERR_UNSUPPORTED, "B (%d) is at most 2^27", B);
+    if (grads == RM_BF16 && B > kMaxBatchBf16)
+        return fail(RM_ERR_UNSUPPORTED, "B (%d) is at most 2^17 for bf16 gradients (float32 ones take more)", B);
+    return RM_OK;
+}
+
 rm_status check_ffn(const rm_fp8_pffn* p) {
     if (!p) return fail(RM_ERR_INVALID_ARG, "p is NULL");
     RM_CHECK(check_sizes(1, p->T, p->D, p->F));
     if (p->D % 16 != 0 || p->F % 16 != 0)
         return fail(RM_ERR_UNSUPPORTED, "D (%d) and F (%d) must be multiples of 16", p->D, p->F);
-    if (p->D > kMaxSum || p->F > kMaxSum)
-        return fail(RM_ERR_UNSUPPORTED, "D (%d) and F (%d) are at most 2^27", p->D, p->F);
+    if (p->D > kMaxK || p->F > kMaxK)
+        return fail(RM_ERR_UNSUPPORTED, "D (%d) and F (%d) are at most 2^19", p->D, p->F);
     RM_CHECK(check_tensor(&p->W1, p->F, "W1", true));
     RM_CHECK(check_tensor(&p->W2, p->D, "W2", true));
     if (!p->b1 || !p->b2) return fail(RM_ERR_INVALID_ARG, "b1 / b2 is NULL");
@@ -231,7 +245,7 @@ rm_status rm_fp8_matmul(const rm_fp8_tensor* x, const rm_fp8_tensor* W, const fl
     if (!Y) return fail(RM_ERR_INVALID_ARG, "Y is NULL");
     if (!known(dtype)) return fail(RM_ERR_INVALID_ARG, "unknown dtype");
     RM_CHECK(check_sizes(B, T, K, N));
-    if (K > kMaxSum) return fail(RM_ERR_UNSUPPORTED, "K (%d) is at most 2^27", K);
+    if (K > kMaxK) return fail(RM_ERR_UNSUPPORTED, "K (%d) is at most 2^19", K);
     RM_CHECK(check_tensor(x, K, "x", false));
     RM_CHECK(check_tensor(W, transpose_w ? K : N, "W", true));
     if (!aligned(Y, 16) || (bias && !aligned(bias, 16)))
@@ -249,7 +263,7 @@ rm_status rm_fp8_wgrad(const rm_fp8_tensor* x, const void* dY, void* dW, void* d
     if (!known(dtype)) return fail(RM_ERR_INVALID_ARG, "unknown dtype");
     RM_CHECK(check_sizes(B, T, K, N));
     if (N % 8 != 0) return fail(RM_ERR_UNSUPPORTED, "N (%d) must be a multiple of 8", N);
-    if (B > kMaxSum) return fail(RM_ERR_UNSUPPORTED, "B (%d) is at most 2^27", B);
+    RM_CHECK(check_batch(B, dtype));
     RM_CHECK(check_tensor(x, K, "x", true));
     if (!aligned(dY, 16) || !aligned(dW, 16) || (db && !aligned(db, 16)))
         return fail(RM_ERR_INVALID_ARG, "dY, dW and db must be 16-byte aligned");
@@ -315,7 +329,7 @@ rm_status rm_fp8_pffn_backward(const rm_fp8_pffn* p, const void* dV, rm_dtype dv
                           (const void*)grads->db2})
         if (!aligned(q, 16)) return fail(RM_ERR_INVALID_ARG, "dV, dX and the gradients must be 16-byte aligned");
     RM_CHECK(check_sizes(B, p->T, p->D, p->F));
-    if (B > kMaxSum) return fail(RM_ERR_UNSUPPORTED, "B (%d) is at most 2^27", B);
+    RM_CHECK(check_batch(B, grads->dtype));
     RM_CHECK(check_kept(kept, p));
     const BackwardWork w = backward_work(p, B, work);
     RM_CHECK(check_work(work, work_bytes, w.bytes));

@@ -1,0 +1,49 @@
+"""Refusals of the 8-bit operators at the ends of their ranges, on the host before anything is launched (no GPU
+needed)."""
+import ctypes
+import os
+
+import pytest
+
+from rankmixer_feature_interaction_gb300 import _lib
+from rankmixer_feature_interaction_gb300 import build as rm_build
+
+BAD, NO = _lib.RM_ERR_INVALID_ARG, _lib.RM_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        rm_build.build()
+    return _lib.load()
+
+
+@pytest.fixture(scope="module")
+def mem():
+    buf = ctypes.create_string_buffer(1 << 16)
+    yield (ctypes.addressof(buf) + 255) // 256 * 256
+    del buf
+
+
+def t8(p, cols, fmt=_lib.RM_E4M3):
+    return _lib.rm_fp8_tensor(codes=p, scales=p + 4096, ld=(cols + 15) // 16 * 16,
+                              lds=((cols + 127) // 128 + 3) // 4 * 4, format=fmt)
+
+
+def test_sums_longer_than_the_accumulator_holds_are_refused(lib, mem):
+    p, n = mem, ctypes.c_longlong()
+    k = (1 << 19) + 16
+    assert lib.rm_fp8_matmul(t8(p, k), t8(p, 32), None, p, 0, 1, 1, k, 32, 0, None) == NO
+    assert "2^19" in _lib.rm_last_error()
+    assert lib.rm_fp8_matmul(t8(p, k), t8(p, k), None, p, 0, 1, 1, k, 32, 1, None) == NO
+    for D, F in ((k, 32), (32, k)):
+        f = _lib.rm_fp8_pffn(t8(p, F), t8(p, D), p, p, 1, D, F)
+        assert lib.rm_fp8_pffn_workspace(f, 1, _lib.RM_FP8_SERVE, ctypes.byref(n)) == NO
+    b = (1 << 17) + 1
+    assert lib.rm_fp8_wgrad(t8(p, 32), p, p, p, _lib.RM_BF16, b, 1, 32, 32, None) == NO
+    assert "2^17" in _lib.rm_last_error()
+    f = _lib.rm_fp8_pffn(t8(p, 32), t8(p, 32), p, p, 1, 32, 32)
+    assert lib.rm_fp8_pffn_workspace(f, b, _lib.RM_FP8_BACKWARD, ctypes.byref(n)) == _lib.RM_OK
+    kept = _lib.rm_fp8_kept(t8(p, 32), t8(p, 32), t8(p, 32))
+    assert lib.rm_fp8_pffn_backward(f, p, 0, kept, p, 0, _lib.rm_fp8_grads(p, p, p, p, _lib.RM_BF16), b, p, n.value,
+                                    None) == NO

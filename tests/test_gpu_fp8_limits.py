@@ -8,7 +8,8 @@ import pytest
 import torch
 
 from rankmixer_feature_interaction_gb300 import _lib
-from rankmixer_feature_interaction_gb300.api import Fp8PFFN, Fp8Tensor, fp8_quantize_weight, fp8_sync_status
+from rankmixer_feature_interaction_gb300.api import (Fp8PFFN, Fp8Tensor, fp8_matmul, fp8_quantize, fp8_quantize_weight,
+                                                     fp8_sync_status, fp8_wgrad)
 from tests import fp8_reference as ref
 
 pytestmark = pytest.mark.gpu
@@ -64,4 +65,35 @@ def test_hidden_values_of_blocks_far_below_zero(B):
     low, high = ref.exponent((top - off).clamp(min=0), "e4m3"), ref.exponent(top + off, "e4m3")
     assert ((e >= low) & (e <= high) | (top <= off) & (e == 0)).all()
     assert torch.equal(m.forward(X, "f32"), V)
+    ok()
+
+
+# ---- long sums ----------------------------------------------------------------------------------------
+
+def positive(shape, seed):
+    """Values of one sign that share no grid."""
+    return torch.exp(torch.randn(shape, generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV))
+
+
+@pytest.mark.parametrize("B", [1, 40])
+def test_products_of_the_longest_sums(B):
+    """Terms of one sign, K = 2^19: K / 32 instructions, each truncates what it adds and what it has, a unit in the last
+    place (2^-23) of a running sum that is half the final one on average: K / 32 * 2^-23 = 2^-9."""
+    K, N = 1 << 19, 16
+    x, w = fp8_quantize(positive((B, 1, K), 83)), fp8_quantize_weight(positive((1, K, N), 84))
+    want = ref.matmul(ref.value(x), ref.weight_value(w))
+    within(fp8_matmul(x, w, None, "f32"), want, 2.0 ** -9 * want, "K = 2^19")
+    ok()
+
+
+def test_bf16_gradients_of_the_most_samples():
+    """The same for B = 2^17 samples, 16 an instruction: B / 16 * 2^-23 = 2^-10, and half a step of bf16."""
+    B, K, N = 1 << 17, 32, 24
+    x, dy = fp8_quantize(positive((B, 1, K), 85)), positive((B, 1, N), 86).to(torch.bfloat16)
+    dw, db = fp8_wgrad(x, dy, "bf16")
+    want = ref.outer(ref.value(x), dy.double())
+    within(dw, want, (2.0 ** -10 + ref.HALF_BF16) * want, "dW")
+    assert abs(((dw.double() - want) / want).mean().item()) <= 2.0 ** -10
+    want = dy.double().sum(0)
+    within(db, want, (2.0 ** -10 + ref.HALF_BF16) * want, "db")
     ok()
