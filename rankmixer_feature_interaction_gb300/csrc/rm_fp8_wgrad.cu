@@ -373,7 +373,10 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 stage = (stage + kblocks) % STAGES;
                 continue;
             }
-            float sum[8] = {};
+            // float32 sums are joined from sums of a chunk, as dW's are: in one running sum a
+            // value that is constant over the samples would be rounded the same way each time
+            float total[8] = {}, sum[8] = {};
+            int in_chunk = 0;
             for (int kb = 0; kb < kblocks; ++kb) {
                 if (!wait_bounded(sready_bar(stage), (phase >> stage) & 1u, abort_flag, args.err, args.timeout_ns)) {
                     ok = false;
@@ -394,9 +397,15 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(summed_bar(stage));
                 if (++stage == STAGES) stage = 0;
+                if (++in_chunk == args.chunk_blocks) {
+                    in_chunk = 0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) total[j] += sum[j], sum[j] = 0.f;
+                }
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
+                sum[j] += total[j];
                 sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 4);
                 sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 8);
                 sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);

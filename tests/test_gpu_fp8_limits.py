@@ -97,3 +97,18 @@ def test_bf16_gradients_of_the_most_samples():
     want = dy.double().sum(0)
     within(db, want, (2.0 ** -10 + ref.HALF_BF16) * want, "db")
     ok()
+
+
+def test_float32_gradients_of_millions_of_samples():
+    """Float32 gradients are joined from sums of 2048 samples.  dW: within a chunk 128 instructions lose a unit in the
+    last place each (2^-23) of a running sum of half the chunk's, 2^-17; 2049 chunks are added with rounding to nearest,
+    half a unit (2^-24) of half the sum on average, 2^-14.  db, of one value that all samples share and that float32
+    does not add exactly past 2^24 of its units: 256 additions in a chunk, which are exact, and the same 2049."""
+    B, K, N = (1 << 22) + 65, 16, 8
+    x = fp8_quantize(positive((B, 1, K), 87))
+    dy = torch.full((B, 1, N), 129 / 128, dtype=torch.bfloat16, device=DEV)
+    dw, db = fp8_wgrad(x, dy)
+    want = ref.outer(ref.value(x), dy.double())
+    within(db, dy.double().sum(0), 2.0 ** -14 * dy.double().sum(0), "db")
+    within(dw, want, (2.0 ** -17 + 2.0 ** -14) * want, "dW")
+    ok()
