@@ -112,3 +112,97 @@ def test_float32_gradients_of_millions_of_samples():
     within(db, dy.double().sum(0), 2.0 ** -14 * dy.double().sum(0), "db")
     within(dw, want, (2.0 ** -17 + 2.0 ** -14) * want, "dW")
     ok()
+
+
+# ---- weight gradients that are joined from chunks -----------------------------------------------------
+
+def wgrad_into(x, dy, dtype, with_db=True, fill=float("nan")):
+    """The C entry, into buffers that hold `fill`: (dW, db)."""
+    (B, T, K), N = x.shape, dy.shape[-1]
+    tdt, code = (torch.float32, _lib.RM_F32) if dtype == "f32" else (torch.bfloat16, _lib.RM_BF16)
+    dw, db = (torch.full(s, fill, dtype=tdt, device=DEV) for s in ((T, K, N), (T, N)))
+    _lib.rm_fp8_wgrad(x.c, dy.data_ptr(), dw.data_ptr(), db.data_ptr() if with_db else None, code, B, T, K, N,
+                      torch.cuda.current_stream().cuda_stream)
+    return dw, db
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,K,N", [(2049, 2, 272, 520), (4161, 3, 130, 264), (9000, 1, 1001, 40), (4096, 40, 500, 776),
+                                     (6145, 80, 128, 136)])
+def test_wgrad_of_several_chunks(B, T, K, N, dtype):
+    """Elementwise as for one chunk (float32 additions of B exact products), the buffers full of NaN and then of ones
+    before the call: the first chunk overwrites, the others add once."""
+    x = fp8_quantize(torch.randn((B, T, K), generator=torch.Generator(device=DEV).manual_seed(88), device=DEV))
+    dy = torch.randn((B, T, N), generator=torch.Generator(device=DEV).manual_seed(89), device=DEV).to(torch.bfloat16)
+    xv, yv = ref.value(x), dy.double()
+    dw, db = wgrad_into(x, dy, dtype)
+    again = wgrad_into(x, dy, dtype, fill=1.0)
+    assert torch.equal(again[0], dw) and torch.equal(again[1], db)
+    for got, want, size, what in ((dw, ref.outer(xv, yv), ref.outer(xv.abs(), yv.abs()), "dW"),
+                                  (db, yv.sum(0), yv.abs().sum(0), "db")):
+        tol = ref.sum_bound(B, size)
+        if dtype == "bf16":
+            tol = tol + ref.HALF_BF16 * (want.abs() + tol)
+        within(got, want, tol, f"{what} {dtype}")
+    if dtype == "f32":
+        # a lost or doubled chunk is off by about 1 / sqrt(chunks) in norm; the sums lose at most 2^-17 (a chunk of terms
+        # of one sign) of the magnitudes' sum, in norm at most sqrt(B) times the gradient of independent samples
+        off = ((dw.double() - ref.outer(xv, yv)).norm() / ref.outer(xv, yv).norm()).item()
+        assert off <= 2.0 ** -17 * math.sqrt(B), off
+    ok()
+
+
+@pytest.mark.parametrize("B", [3, 700, 5000])
+def test_wgrad_without_the_bias_gradient(B):
+    T, K, N = 3, 400, 776
+    x = fp8_quantize(torch.randn((B, T, K), generator=gen(90)).to(DEV))
+    dy = torch.randn((B, T, N), generator=gen(91)).to(torch.bfloat16).to(DEV)
+    for dtype in ("f32", "bf16"):
+        dw, db = wgrad_into(x, dy, dtype, with_db=False)
+        assert torch.equal(dw, wgrad_into(x, dy, dtype)[0]) and db.isnan().all()
+    ok()
+
+
+# ---- forms of the arguments -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt,trans", [("e5m2", False), ("e4m3", True)])
+@pytest.mark.parametrize("B,T,K,N", [(1, 3, 200, 72), (20, 1, 2048, 130), (100, 2, 257, 129), (333, 20, 272, 520)])
+def test_either_format_in_either_direction(B, T, K, N, fmt, trans):
+    x = fp8_quantize(torch.randn((B, T, K), generator=gen(92)).to(DEV), fmt)
+    w = fp8_quantize_weight(torch.randn((T, N, K) if trans else (T, K, N), generator=gen(93)).to(DEV))
+    wv = ref.weight_value(w)
+    xv, wv = ref.value(x), wv.transpose(1, 2) if trans else wv
+    within(fp8_matmul(x, w, None, "f32", trans), ref.matmul(xv, wv), ref.sum_bound(K, ref.matmul(xv.abs(), wv.abs())),
+           f"{fmt} trans={trans}")
+    ok()
+
+
+@pytest.mark.parametrize("C,extra", [(200, 48), (1003, 16), (128, 400)])
+def test_rows_longer_than_their_columns(C, extra):
+    """Code, scale and value rows with room behind them, which stays as it is; products and gradients read past it."""
+    B, T, N = 140, 2, 136
+    ld, lds = (C + 15) // 16 * 16 + extra, (C + 511) // 512 * 4 + 8
+    v = torch.randn((B, T, C), generator=gen(94)).to(DEV)
+    codes = torch.full((B, T, ld), 0x7f, dtype=torch.uint8, device=DEV)
+    scales = torch.full((B, T, lds), 255, dtype=torch.uint8, device=DEV)
+    q = Fp8Tensor(codes.view(torch.float8_e4m3fn), scales, C)
+    s = torch.cuda.current_stream().cuda_stream
+    _lib.rm_fp8_quantize(v.data_ptr(), _lib.RM_F32, B * T, C, C, q.c, s)
+    plain = fp8_quantize(v)
+    nb = (C + 127) // 128
+    assert torch.equal(codes[..., :C], plain.codes.view(torch.uint8)[..., :C])
+    assert torch.equal(scales[..., :nb], plain.scales[..., :nb])
+    assert (codes[..., (C + 15) // 16 * 16:] == 0x7f).all() and (scales[..., nb:] == 255).all()
+    for dt, code in ((torch.float32, _lib.RM_F32), (torch.bfloat16, _lib.RM_BF16)):
+        for ldy in (C, C + 1, C + 24):
+            y = torch.full((B * T, ldy), 7.0, dtype=dt, device=DEV)
+            _lib.rm_fp8_dequantize(q.c, B * T, C, y.data_ptr(), code, ldy, s)
+            assert torch.equal(y[:, :C].double().reshape(B, T, C), ref.value(plain)) and (y[:, C:] == 7).all()
+    w = fp8_quantize_weight(torch.randn((T, C, N), generator=gen(95)).to(DEV))
+    for b in (7, B):
+        part = Fp8Tensor(q.codes[:b], q.scales[:b], C)
+        whole = Fp8Tensor(plain.codes[:b], plain.scales[:b], C)
+        assert torch.equal(fp8_matmul(part, w, None, "f32"), fp8_matmul(whole, w, None, "f32"))
+        dy = torch.randn((b, T, N), generator=gen(96)).to(torch.bfloat16).to(DEV)
+        assert all(torch.equal(a, c) for a, c in zip(fp8_wgrad(part, dy), fp8_wgrad(whole, dy)))
+    ok()
