@@ -19,8 +19,8 @@ struct Fp8View {
     bool e5m2;
 };
 
-// X [rows][ldx] (float, or bf16) -> out.  copy (nullable): the rows in bf16,
-// [rows][cols] contiguous, cols a multiple of 8.
+// X [rows][ldx] (float, or bf16) -> out.  copy (nullable; of 16-byte aligned float
+// rows to e4m3 only): the rows in bf16, [rows][cols] contiguous, cols a multiple of 16.
 cudaError_t launch_fp8_quantize(bool f32, const void* X, long long rows, int cols, long long ldx, const Fp8View& out,
                                 void* copy, cudaStream_t s);
 cudaError_t launch_fp8_quantize_weight(bool f32, const void* W, int T, int K, int N, const Fp8View& out,

@@ -12,6 +12,8 @@
 // 8-byte stores; restoring such rows mirrors that.
 // Measured, 65,536 rows of 6144 in bf16 (805 MB; 406 MB in 8 bits): saving 185 us,
 // restoring 185 us, 6.5 TB/s each: bound by memory.
+#include <type_traits>
+
 #include "rm_common.cuh"
 #include "rm_fp8.cuh"
 
@@ -126,6 +128,7 @@ template <typename IN, bool E5M2, bool VEC, bool COPY>
 __global__ void __launch_bounds__(kThreads)
 quantize_kernel(const IN* __restrict__ X, unsigned long long blocks, int cols, int nb, int dq, int dr, long long ldx,
                 Fp8View out, __nv_bfloat16* __restrict__ copy) {
+    static_assert(VEC || !COPY, "the copy takes eight neighbouring values of a lane");
     constexpr int UNROLL = kBlocks<IN>, PER = kThreads / 8;
     __shared__ uint2 bytes[VEC ? 1 : 2 * kThreads];  // a block's 128 codes are contiguous
     pdl_wait();
@@ -340,8 +343,13 @@ cudaError_t run_quantize(const void* X, long long rows, int cols, long long ldx,
               per = step * kBlocks<IN>;
     const unsigned long long blocks = (unsigned long long)rows * nb;
     const unsigned grid = (unsigned)((blocks + per - 1) / per);
-    return launch_k(copy ? quantize_kernel<IN, E5M2, VEC, true> : quantize_kernel<IN, E5M2, VEC, false>, dim3(grid),
-                    dim3(kThreads), 0, s, (const IN*)X, blocks, cols, nb, step / nb, step % nb, ldx, out,
+    auto k = quantize_kernel<IN, E5M2, VEC, false>;
+    if constexpr (std::is_same<IN, float>::value && VEC && !E5M2) {
+        if (copy) k = quantize_kernel<IN, E5M2, VEC, true>;
+    } else if (copy) {
+        return cudaErrorNotSupported;
+    }
+    return launch_k(k, dim3(grid), dim3(kThreads), 0, s, (const IN*)X, blocks, cols, nb, step / nb, step % nb, ldx, out,
                     (__nv_bfloat16*)copy);
 }
 
