@@ -344,19 +344,32 @@ def rm_debug_alloc_stats() -> tuple[int, int, int]:
     return v[0].value, v[1].value, v[2].value
 
 
+def too_long(where: str, *sizes: int) -> None:
+    """Refuse sizes of 2^31 or more (or below 0): the C interface takes 32 bits, and ctypes would pass the low ones."""
+    for n in sizes:
+        if n >> 31:
+            raise RankMixerError(RM_ERR_INVALID_ARG, where, f"size {n} does not fit 32 bits")
+
+
 def rm_fp8_quantize(X: int, dtype: int, rows: int, cols: int, ldx: int, out: rm_fp8_tensor, stream: int) -> None:
+    if cols >> 31:
+        too_long("rm_fp8_quantize", cols)
     st = (_lib or load()).rm_fp8_quantize(X, dtype, rows, cols, ldx, out, stream)
     if st:
         check(st, "rm_fp8_quantize")
 
 
 def rm_fp8_quantize_weight(W: int, dtype: int, T: int, K: int, N: int, out: rm_fp8_tensor, stream: int) -> None:
+    if (T | K | N) >> 31:
+        too_long("rm_fp8_quantize_weight", T, K, N)
     st = (_lib or load()).rm_fp8_quantize_weight(W, dtype, T, K, N, out, stream)
     if st:
         check(st, "rm_fp8_quantize_weight")
 
 
 def rm_fp8_dequantize(q: rm_fp8_tensor, rows: int, cols: int, Y: int, dtype: int, ldy: int, stream: int) -> None:
+    if cols >> 31:
+        too_long("rm_fp8_dequantize", cols)
     st = (_lib or load()).rm_fp8_dequantize(q, rows, cols, Y, dtype, ldy, stream)
     if st:
         check(st, "rm_fp8_dequantize")
@@ -364,6 +377,8 @@ def rm_fp8_dequantize(q: rm_fp8_tensor, rows: int, cols: int, Y: int, dtype: int
 
 def rm_fp8_matmul(x: rm_fp8_tensor, W: rm_fp8_tensor, bias: int | None, Y: int, dtype: int, B: int, T: int, K: int,
                   N: int, transpose_w: bool, stream: int) -> None:
+    if (B | T | K | N) >> 31:
+        too_long("rm_fp8_matmul", B, T, K, N)
     st = (_lib or load()).rm_fp8_matmul(x, W, bias, Y, dtype, B, T, K, N, 1 if transpose_w else 0, stream)
     if st:
         check(st, "rm_fp8_matmul")
@@ -371,12 +386,16 @@ def rm_fp8_matmul(x: rm_fp8_tensor, W: rm_fp8_tensor, bias: int | None, Y: int, 
 
 def rm_fp8_wgrad(x: rm_fp8_tensor, dY: int, dW: int | None, db: int | None, dtype: int, B: int, T: int, K: int, N: int,
                  stream: int) -> None:
+    if (B | T | K | N) >> 31:
+        too_long("rm_fp8_wgrad", B, T, K, N)
     st = (_lib or load()).rm_fp8_wgrad(x, dY, dW, db, dtype, B, T, K, N, stream)
     if st:
         check(st, "rm_fp8_wgrad")
 
 
 def rm_fp8_pffn_workspace(p: rm_fp8_pffn, B: int, pass_: int) -> int:
+    if B >> 31:
+        too_long("rm_fp8_pffn_workspace", B)
     n = ctypes.c_longlong()
     st = (_lib or load()).rm_fp8_pffn_workspace(p, B, pass_, ctypes.byref(n))
     if st:
@@ -386,6 +405,8 @@ def rm_fp8_pffn_workspace(p: rm_fp8_pffn, B: int, pass_: int) -> int:
 
 def rm_fp8_pffn_forward(p: rm_fp8_pffn, X: int, x_dtype: int, V: int, v_dtype: int, keep: rm_fp8_kept | None, B: int,
                         work: int | None, work_bytes: int, stream: int) -> None:
+    if B >> 31:
+        too_long("rm_fp8_pffn_forward", B)
     st = (_lib or load()).rm_fp8_pffn_forward(p, X, x_dtype, V, v_dtype, keep, B, work, work_bytes, stream)
     if st:
         check(st, "rm_fp8_pffn_forward")
@@ -393,6 +414,8 @@ def rm_fp8_pffn_forward(p: rm_fp8_pffn, X: int, x_dtype: int, V: int, v_dtype: i
 
 def rm_fp8_pffn_backward(p: rm_fp8_pffn, dV: int, dv_dtype: int, kept: rm_fp8_kept, dX: int | None, dx_dtype: int,
                          grads: rm_fp8_grads, B: int, work: int | None, work_bytes: int, stream: int) -> None:
+    if B >> 31:
+        too_long("rm_fp8_pffn_backward", B)
     st = (_lib or load()).rm_fp8_pffn_backward(p, dV, dv_dtype, kept, dX, dx_dtype, grads, B, work, work_bytes, stream)
     if st:
         check(st, "rm_fp8_pffn_backward")

@@ -550,6 +550,7 @@ class Fp8PFFN:
         self.T, self.D, self.F = _fp8_weight(self.W1, "W1")
         if _fp8_weight(self.W2, "W2") != (self.T, self.F, self.D):
             raise ValueError(f"W1 {self.W1.shape} and W2 {self.W2.shape} do not fit")
+        _lib.too_long("Fp8PFFN", self.T, self.D, self.F)
         self.b1, self.b2 = b1.to(torch.float32).contiguous(), b2.to(torch.float32).contiguous()
         if tuple(self.b1.shape) != (self.T, self.F) or tuple(self.b2.shape) != (self.T, self.D):
             raise ValueError(f"b1 must be [{self.T}, {self.F}] and b2 [{self.T}, {self.D}]")

@@ -4,9 +4,11 @@ import ctypes
 import os
 
 import pytest
+import torch
 
 from rankmixer_feature_interaction_gb300 import _lib
 from rankmixer_feature_interaction_gb300 import build as rm_build
+from rankmixer_feature_interaction_gb300.api import Fp8PFFN, Fp8Tensor
 
 BAD, NO = _lib.RM_ERR_INVALID_ARG, _lib.RM_ERR_UNSUPPORTED
 
@@ -47,3 +49,34 @@ def test_sums_longer_than_the_accumulator_holds_are_refused(lib, mem):
     kept = _lib.rm_fp8_kept(t8(p, 32), t8(p, 32), t8(p, 32))
     assert lib.rm_fp8_pffn_backward(f, p, 0, kept, p, 0, _lib.rm_fp8_grads(p, p, p, p, _lib.RM_BF16), b, p, n.value,
                                     None) == NO
+
+
+def test_binding_refuses_sizes_that_do_not_fit_the_interface(lib, mem):
+    """The C interface takes 32-bit sizes: 2^32 + 128 columns must not arrive there as 128."""
+    p, n, q = mem, (1 << 32) + 128, t8(mem, 128)
+    wide = t8(p, n)
+    f = _lib.rm_fp8_pffn(t8(p, 32), t8(p, 32), p, p, 1, 32, 32)
+    kept = _lib.rm_fp8_kept(t8(p, 32), t8(p, 32), t8(p, 32))
+    calls = [lambda: _lib.rm_fp8_quantize(p, _lib.RM_F32, 1, n, n, wide, 0),
+             lambda: _lib.rm_fp8_dequantize(wide, 1, n, p, _lib.RM_F32, n, 0),
+             lambda: _lib.rm_fp8_quantize_weight(p, _lib.RM_F32, 1, n, 16, q, 0),
+             lambda: _lib.rm_fp8_quantize_weight(p, _lib.RM_F32, 1, 16, n, wide, 0),
+             lambda: _lib.rm_fp8_quantize_weight(p, _lib.RM_F32, (1 << 32) + 1, 16, 16, q, 0),
+             lambda: _lib.rm_fp8_matmul(q, q, None, p, _lib.RM_F32, n, 1, 128, 128, False, 0),
+             lambda: _lib.rm_fp8_matmul(q, wide, None, p, _lib.RM_F32, 1, 1, 128, n, False, 0),
+             lambda: _lib.rm_fp8_matmul(wide, q, None, p, _lib.RM_F32, 1, 1, n, 128, False, 0),
+             lambda: _lib.rm_fp8_wgrad(q, p, p, p, _lib.RM_F32, n, 1, 128, 128, 0),
+             lambda: _lib.rm_fp8_pffn_workspace(f, n, _lib.RM_FP8_SERVE),
+             lambda: _lib.rm_fp8_pffn_forward(f, p, 0, p, 0, None, n, p, 1 << 50, 0),
+             lambda: _lib.rm_fp8_pffn_backward(f, p, 0, kept, p, 0, _lib.rm_fp8_grads(p, p, p, p, 0), n, p, 1 << 50, 0)]
+    for i, call in enumerate(calls):
+        with pytest.raises(_lib.RankMixerError) as e:
+            call()
+        assert e.value.status == BAD, i
+    n, meta = (1 << 32) + 16, {"device": "meta"}
+    w1 = Fp8Tensor(torch.empty((1, 16, n), dtype=torch.float8_e4m3fn, **meta),
+                   torch.empty((1, 1, (n + 511) // 512 * 4), dtype=torch.uint8, **meta), n)
+    w2 = Fp8Tensor(torch.empty((1, n, 16), dtype=torch.float8_e4m3fn, **meta),
+                   torch.empty((1, (n + 127) // 128, 4), dtype=torch.uint8, **meta), 16)
+    with pytest.raises(_lib.RankMixerError, match="32 bits"):
+        Fp8PFFN(w1, torch.empty((1, n), **meta), w2, torch.empty((1, 16), **meta))
