@@ -492,9 +492,10 @@ RM_API rm_status rm_debug_mix_residual(const void *X, int from_z, float *Y, int 
  * where that loss is below 2^-9: K (D and F of the FFN) is at most 2^19, B of
  * weight gradients in bf16 at most 2^17.  Weight gradients in float32 join sums
  * of 2048 samples with rounding to nearest; their B is at most 2^27
- * (RM_ERR_UNSUPPORTED otherwise).  B T is below 2^31 (RM_ERR_INVALID_ARG
- * otherwise).  Device-side errors (a bounded wait that ran out) are latched per
- * device and reported by rm_fp8_sync_status. */
+ * (RM_ERR_UNSUPPORTED otherwise).  B T is below 2^31, other sizes are at most
+ * 2^31 - 512 (RM_ERR_INVALID_ARG otherwise).  Device-side errors (a bounded
+ * wait that ran out) are latched per device and reported by
+ * rm_fp8_sync_status. */
 typedef enum rm_fp8_format {
     RM_E4M3 = 0,
     RM_E5M2 = 1

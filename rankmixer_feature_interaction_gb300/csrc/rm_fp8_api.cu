@@ -41,6 +41,8 @@ Fp8View view(const rm_fp8_tensor& t) {
 
 // rows are limited so that row and block numbers of every kernel fit 32-bit grids
 constexpr long long kMaxRows = 1ll << 31;
+// ... and every other size so that rounding it up to whole tiles does not overflow
+constexpr int kMaxSize = 0x7fffffff - 511;
 // Summed lengths.  The tensor cores' accumulator truncates as it adds, about a unit
 // in the last place an instruction (32 products, or 16 of the weight gradient), so
 // sums that stay in it are held to lengths at which terms of one sign lose less than
@@ -95,8 +97,15 @@ rm_status check_tensor(const rm_fp8_tensor* t, int cols, const char* name, bool 
 
 rm_status check_sizes(int B, int T, int K, int N) {
     if (B < 1 || T < 1 || K < 1 || N < 1) return fail(RM_ERR_INVALID_ARG, "sizes must be positive");
+    if (B > kMaxSize || K > kMaxSize || N > kMaxSize) return fail(RM_ERR_INVALID_ARG, "sizes are at most 2^31 - 512");
     if (T > 65535) return fail(RM_ERR_INVALID_ARG, "T (%d) is at most 65535", T);
     if ((long long)B * T >= kMaxRows) return fail(RM_ERR_INVALID_ARG, "B T (%d x %d) must be below 2^31", B, T);
+    return RM_OK;
+}
+
+rm_status check_rows(long long rows, int cols) {
+    if (rows < 1 || rows >= kMaxRows || cols < 1 || cols > kMaxSize)
+        return fail(RM_ERR_INVALID_ARG, "rows must be in [1, 2^31), cols in [1, 2^31 - 512]");
     return RM_OK;
 }
 
@@ -205,7 +214,7 @@ rm_status rm_fp8_quantize(const void* X, rm_dtype dtype, long long rows, int col
                           const rm_fp8_tensor* out, void* stream) {
     if (!X) return fail(RM_ERR_INVALID_ARG, "X is NULL");
     if (!known(dtype)) return fail(RM_ERR_INVALID_ARG, "unknown dtype");
-    if (rows < 1 || rows >= kMaxRows || cols < 1) return fail(RM_ERR_INVALID_ARG, "rows must be in [1, 2^31), cols positive");
+    RM_CHECK(check_rows(rows, cols));
     if (ldx < cols) return fail(RM_ERR_INVALID_ARG, "ldx (%lld) is below cols (%d)", ldx, cols);
     if (!aligned(X, dtype == RM_F32 ? 4 : 2)) return fail(RM_ERR_INVALID_ARG, "X must be aligned to its elements");
     RM_CHECK(check_tensor(out, cols, "out", false));
@@ -231,7 +240,7 @@ rm_status rm_fp8_dequantize(const rm_fp8_tensor* in, long long rows, int cols, v
                             void* stream) {
     if (!Y) return fail(RM_ERR_INVALID_ARG, "Y is NULL");
     if (!known(dtype)) return fail(RM_ERR_INVALID_ARG, "unknown dtype");
-    if (rows < 1 || rows >= kMaxRows || cols < 1) return fail(RM_ERR_INVALID_ARG, "rows must be in [1, 2^31), cols positive");
+    RM_CHECK(check_rows(rows, cols));
     if (ldy < cols) return fail(RM_ERR_INVALID_ARG, "ldy (%lld) is below cols (%d)", ldy, cols);
     if (!aligned(Y, dtype == RM_F32 ? 4 : 2)) return fail(RM_ERR_INVALID_ARG, "Y must be aligned to its elements");
     RM_CHECK(check_tensor(in, cols, "in", false));

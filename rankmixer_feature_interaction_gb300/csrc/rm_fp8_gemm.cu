@@ -189,10 +189,11 @@ __device__ __forceinline__ void save_piece(const float* v, const Args& a, int t,
     }
     char* dst = reinterpret_cast<char*>(a.y) + (((size_t)m_warp * a.T + t) * (size_t)a.N + n) * E;
     const size_t pitch = (size_t)a.T * (size_t)a.N * E;
+    const int bytes = min(a.N - n, 64) * E;            // the row's rest may be more bytes than fit 32 bits
     if (a.vec)
-        store_rows<true, E>(stage, dst, pitch, rows, (a.N - n) * E, lane);
+        store_rows<true, E>(stage, dst, pitch, rows, bytes, lane);
     else
-        store_rows<false, E>(stage, dst, pitch, rows, (a.N - n) * E, lane);
+        store_rows<false, E>(stage, dst, pitch, rows, bytes, lane);
 }
 
 template <int EPI>

@@ -80,3 +80,21 @@ def test_binding_refuses_sizes_that_do_not_fit_the_interface(lib, mem):
                    torch.empty((1, (n + 127) // 128, 4), dtype=torch.uint8, **meta), 16)
     with pytest.raises(_lib.RankMixerError, match="32 bits"):
         Fp8PFFN(w1, torch.empty((1, n), **meta), w2, torch.empty((1, 16), **meta))
+
+
+@pytest.mark.parametrize("n", [(1 << 31) - 1, (1 << 31) - 128, (1 << 31) - 255])
+def test_sizes_are_refused_before_they_overflow_when_rounded_up(lib, mem, n):
+    """2^31 - 1 columns round up to -2^31 in 32 bits: the row of scales would pass as long enough at any length."""
+    p, q = mem, t8(mem, 128)
+    short = _lib.rm_fp8_tensor(p, p + 4096, (n + 15) // 16 * 16, 4, _lib.RM_E4M3)
+    wide = t8(p, n)
+    for t in (short, wide):
+        assert lib.rm_fp8_quantize(p, _lib.RM_F32, 1, n, n, t, None) == BAD
+        assert lib.rm_fp8_dequantize(t, 1, n, p, _lib.RM_F32, n, None) == BAD
+        assert lib.rm_fp8_quantize_weight(p, _lib.RM_F32, 1, 16, n, t, None) == BAD
+        assert lib.rm_fp8_matmul(q, t, None, p, _lib.RM_F32, 1, 1, 128, n, 0, None) == BAD
+        assert lib.rm_fp8_matmul(t, q, None, p, _lib.RM_F32, 1, 1, n, 128, 0, None) in (BAD, NO)
+        assert lib.rm_fp8_wgrad(t, p, p, p, _lib.RM_F32, 1, 1, n, 128, None) == BAD
+    assert lib.rm_fp8_matmul(q, q, None, p, _lib.RM_F32, n, 1, 128, 128, 0, None) == BAD
+    assert lib.rm_fp8_matmul(q, q, None, p, _lib.RM_F32, 1, 1, 128, n, 1, None) == BAD
+    assert lib.rm_fp8_wgrad(q, p, p, p, _lib.RM_F32, 1, 1, 128, n // 8 * 8, None) == BAD
