@@ -591,10 +591,17 @@ RM_API rm_status rm_fp8_pffn_backward(const rm_fp8_pffn *p, const void *dV, rm_d
                                       void *dX, rm_dtype dx_dtype, const rm_fp8_grads *grads, int B, void *work,
                                       long long work_bytes, void *stream);
 
-/* Synchronise `stream`, then report and clear the current device's error word
- * of the calls above: RM_OK, RM_ERR_TIMEOUT or RM_ERR_DEVICE (RM_ERR_CUDA if
- * the synchronisation itself failed). */
+/* Synchronise `stream`, then report the device errors of the calls above:
+ * RM_OK, RM_ERR_TIMEOUT or RM_ERR_DEVICE (RM_ERR_CUDA if the synchronisation
+ * itself failed).  The calls of all of a device's streams share one error word,
+ * so an error of any of them is reported, once to every stream that is asked
+ * about: not RM_OK means that a call on this device has failed since this
+ * stream's last report (or ever, in its first).  Thread-safe. */
 RM_API rm_status rm_fp8_sync_status(void *stream);
+
+/* Test hook: rm_debug_wait_timeout for the calls above, on the current device;
+ * rm_fp8_sync_status reports the wait that ran out. */
+RM_API rm_status rm_debug_fp8_wait_timeout(int timeout_us, void *stream);
 
 /* Synchronise `stream`, then report and clear the context's device error
  * word: RM_OK, RM_ERR_TIMEOUT or RM_ERR_DEVICE (or RM_ERR_CUDA if the

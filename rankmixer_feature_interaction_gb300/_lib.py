@@ -57,7 +57,8 @@ EXPORTED = ["rm_create", "rm_destroy", "rm_block_forward", "rm_stack_forward", "
             "rm_set_unimixing", "rm_unimixing_weights", "rm_unimixing", "rm_debug_mix_residual",
             "rm_debug_fail_alloc", "rm_debug_alloc_stats", "rm_stack_forward_host_async", "rm_host_wait",
             "rm_fp8_quantize", "rm_fp8_quantize_weight", "rm_fp8_dequantize", "rm_fp8_matmul", "rm_fp8_wgrad",
-            "rm_fp8_pffn_workspace", "rm_fp8_pffn_forward", "rm_fp8_pffn_backward", "rm_fp8_sync_status"]
+            "rm_fp8_pffn_workspace", "rm_fp8_pffn_forward", "rm_fp8_pffn_backward", "rm_fp8_sync_status",
+            "rm_debug_fp8_wait_timeout"]
 
 
 class rm_config(ctypes.Structure):
@@ -176,6 +177,7 @@ def load() -> ctypes.CDLL:
         "rm_fp8_pffn_forward": (st, [ffn8, vp, i, vp, i, kept8, i, vp, ll, vp]),
         "rm_fp8_pffn_backward": (st, [ffn8, vp, i, kept8, vp, i, ctypes.POINTER(rm_fp8_grads), i, vp, ll, vp]),
         "rm_fp8_sync_status": (st, [vp]),
+        "rm_debug_fp8_wait_timeout": (st, [i, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -424,6 +426,10 @@ def rm_fp8_pffn_backward(p: rm_fp8_pffn, dV: int, dv_dtype: int, kept: rm_fp8_ke
 def rm_fp8_sync_status(stream: int) -> int:
     """Returns the raw status (RM_OK, RM_ERR_TIMEOUT, ...) without raising."""
     return load().rm_fp8_sync_status(stream)
+
+
+def rm_debug_fp8_wait_timeout(timeout_us: int, stream: int) -> None:
+    check(load().rm_debug_fp8_wait_timeout(timeout_us, stream), "rm_debug_fp8_wait_timeout")
 
 
 def rm_debug_gelu_grad(u: int, out: int, n: int, stream: int) -> None:

@@ -620,5 +620,6 @@ class Fp8PFFN:
 
 
 def fp8_sync_status() -> int:
-    """Synchronise the current stream and report the 8-bit operators' device status (RM_OK, RM_ERR_TIMEOUT, ...)."""
+    """Synchronise the current stream and report the 8-bit operators' device status (RM_OK, RM_ERR_TIMEOUT, ...).
+    Every stream is told once of an error, whichever stream's call it came from."""
     return _lib.rm_fp8_sync_status(_stream())

@@ -1,6 +1,8 @@
 // C entry points of the 8-bit operators (include/rankmixer.h, "8-bit operands
 // and checkpoints"): argument checks, workspace layout, launches.
 #include <mutex>
+#include <new>
+#include <unordered_map>
 
 #include "../../include/rankmixer.h"
 #include "rm_fp8.h"
@@ -55,16 +57,31 @@ constexpr int kMaxBatch = 1 << 27;
 
 constexpr unsigned long long kWaitTimeoutNs = 2000000000ull;    // bound of every device-side wait
 
-// The error word of the tensor-core kernels, one per device that loads the library.
-__device__ int g_fp8_error;
+// The error word of the tensor-core kernels, one per device that loads the library;
+// what rm_fp8_sync_status took from it, and a flag that nothing sets (the test hook's).
+__device__ int g_fp8_error, g_fp8_taken, g_fp8_unset;
+
+// Read and cleared at once: an error latched meanwhile is in this word or the next one.
+__global__ void take_error_kernel() { g_fp8_taken = atomicExch(&g_fp8_error, 0); }
+
+// The word does not tell whose call ran out, so every stream that asks is told of every
+// error once: how many there were, the latest, and how many each stream (by its
+// identifier, which is not reused) has been told of.
+struct Reported {
+    std::mutex mu;
+    unsigned long long count = 0;
+    int last = 0;
+    std::unordered_map<unsigned long long, unsigned long long> seen;
+};
+constexpr int kMaxDevices = 64;
 
 // SM count and error word of the current device, looked up once per device.
 rm_status device_info(Fp8Device* out) {
     static std::mutex mu;
-    static Fp8Device known_devices[64];
+    static Fp8Device known_devices[kMaxDevices];
     int d = 0;
     RM_CHECK_CUDA(cudaGetDevice(&d), "cudaGetDevice");
-    if (d < 0 || d >= 64) return fail(RM_ERR_UNSUPPORTED, "device %d", d);
+    if (d < 0 || d >= kMaxDevices) return fail(RM_ERR_UNSUPPORTED, "device %d", d);
     std::lock_guard<std::mutex> lk(mu);
     Fp8Device& k = known_devices[d];
     if (!k.err) {
@@ -367,15 +384,41 @@ rm_status rm_fp8_pffn_backward(const rm_fp8_pffn* p, const void* dV, rm_dtype dv
 }
 
 rm_status rm_fp8_sync_status(void* stream) {
-    cudaError_t e = cudaStreamSynchronize(as_stream(stream));
+    const cudaStream_t s = as_stream(stream);
+    cudaError_t e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "rm_fp8_sync_status");
     Fp8Device dev;
     RM_CHECK(device_info(&dev));
-    int v = 0;
-    const int zero = 0;
-    RM_CHECK_CUDA(cudaMemcpy(&v, dev.err, sizeof v, cudaMemcpyDeviceToHost), "error word");
-    if (v == 0) return RM_OK;
-    RM_CHECK_CUDA(cudaMemcpy(dev.err, &zero, sizeof zero, cudaMemcpyHostToDevice), "error word");
-    return v == kDevErrTimeout ? fail(RM_ERR_TIMEOUT, "a device-side wait of an 8-bit operator ran out")
-                               : fail(RM_ERR_DEVICE, "device error %d in an 8-bit operator", v);
+    int d = 0, v = 0;
+    unsigned long long id = 0;
+    RM_CHECK_CUDA(cudaGetDevice(&d), "cudaGetDevice");
+    RM_CHECK_CUDA(cudaStreamGetId(s, &id), "cudaStreamGetId");
+    static Reported reported[kMaxDevices];
+    Reported& r = reported[d];
+    std::lock_guard<std::mutex> lk(r.mu);
+    take_error_kernel<<<1, 1, 0, s>>>();
+    RM_CHECK_CUDA(cudaGetLastError(), "error word");
+    RM_CHECK_CUDA(cudaMemcpyFromSymbolAsync(&v, g_fp8_taken, sizeof v, 0, cudaMemcpyDeviceToHost, s), "error word");
+    RM_CHECK_CUDA(cudaStreamSynchronize(s), "error word");
+    if (v != 0) ++r.count, r.last = v;
+    try {
+        unsigned long long& seen = r.seen[id];
+        if (seen == r.count) return RM_OK;
+        seen = r.count;
+    } catch (const std::bad_alloc&) {
+        return fail(RM_ERR_OOM, "rm_fp8_sync_status");
+    }
+    return r.last == kDevErrTimeout ? fail(RM_ERR_TIMEOUT, "a device-side wait of an 8-bit operator ran out")
+                                    : fail(RM_ERR_DEVICE, "device error %d in an 8-bit operator", r.last);
+}
+
+rm_status rm_debug_fp8_wait_timeout(int timeout_us, void* stream) {
+    if (timeout_us < 1 || timeout_us > 10000000) return fail(RM_ERR_INVALID_ARG, "timeout_us out of range");
+    Fp8Device dev;
+    RM_CHECK(device_info(&dev));
+    void* flag = nullptr;
+    RM_CHECK_CUDA(cudaGetSymbolAddress(&flag, g_fp8_unset), "flag");
+    RM_CHECK_CUDA(launch_debug_wait((const int*)flag, dev.err, (unsigned long long)timeout_us * 1000ull, as_stream(stream)),
+                  "debug wait");
+    return RM_OK;
 }

@@ -3,6 +3,10 @@ between streams, and forms of the arguments that the products of ordinary layers
 from __future__ import annotations
 
 import math
+import os
+import subprocess
+import sys
+import textwrap
 
 import pytest
 import torch
@@ -14,6 +18,7 @@ from tests import fp8_reference as ref
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def gen(seed):
@@ -206,3 +211,44 @@ def test_rows_longer_than_their_columns(C, extra):
         dy = torch.randn((b, T, N), generator=gen(96)).to(torch.bfloat16).to(DEV)
         assert all(torch.equal(a, c) for a, c in zip(fp8_wgrad(part, dy), fp8_wgrad(whole, dy)))
     ok()
+
+
+# ---- what the streams of a device share -----------------------------------------------------------------
+
+def in_child(body):
+    """Run `body` in a process of its own: its errors and first calls are not this process's."""
+    code = "import torch\nfrom rankmixer_feature_interaction_gb300 import _lib, api\n" + textwrap.dedent(body)
+    env = {**os.environ, "PYTHONPATH": ROOT}
+    r = subprocess.run([sys.executable, "-c", code], env=env, cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_a_wait_that_ran_out_is_reported_to_every_stream():
+    """A wait with a short limit runs out on one stream.  Whichever stream is asked first, the other one's report is
+    not lost; each is told once, and later calls are right."""
+    in_child("""
+        g = torch.Generator(device="cuda").manual_seed(1)
+        x = api.fp8_quantize(torch.randn((200, 2, 256), generator=g, device="cuda"))
+        w = api.fp8_quantize_weight(torch.randn((2, 256, 512), generator=g, device="cuda"))
+        want = api.fp8_matmul(x, w)
+        assert api.fp8_sync_status() == _lib.RM_OK
+        a, b = torch.cuda.Stream(), torch.cuda.Stream()
+        for n in range(2):
+            _lib.rm_debug_fp8_wait_timeout(2000, b.cuda_stream)
+            torch.cuda.synchronize()
+            for s in (a, b, torch.cuda.current_stream()):
+                with torch.cuda.stream(s):
+                    first, then, y = api.fp8_sync_status(), api.fp8_sync_status(), api.fp8_matmul(x, w)
+                    last = api.fp8_sync_status()
+                assert (first, then, last) == (_lib.RM_ERR_TIMEOUT, _lib.RM_OK, _lib.RM_OK), (n, first, then, last)
+                assert torch.equal(y, want)
+        new = torch.cuda.Stream(priority=-1)           # never asked before: told of what happened before, once
+        with torch.cuda.stream(new):
+            assert api.fp8_sync_status() == _lib.RM_ERR_TIMEOUT and api.fp8_sync_status() == _lib.RM_OK
+    """)
+
+
+def test_the_wait_hook_refuses_other_limits():
+    for us in (0, -1, 10000001):
+        with pytest.raises(_lib.RankMixerError):
+            _lib.rm_debug_fp8_wait_timeout(us, 0)
