@@ -484,8 +484,7 @@ RM_API rm_status rm_debug_mix_residual(const void *X, int from_z, float *Y, int 
  *
  * These calls need no context: they run on the current device, which must own
  * the buffers, on `stream`, allocate nothing and keep nothing between calls.
- * They may be captured into a CUDA graph once any of them has run on that
- * device outside capture (which looks up the device's error word).  Calls on
+ * They may be captured into a CUDA graph, also at their first call.  Calls on
  * different streams are independent when their buffers (and workspaces) are.
  * Sums are float32; the tensor cores truncate as they add, so that a long sum
  * of terms of one sign comes out small.  The lengths summed over are held to

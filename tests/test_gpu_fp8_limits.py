@@ -252,3 +252,25 @@ def test_the_wait_hook_refuses_other_limits():
     for us in (0, -1, 10000001):
         with pytest.raises(_lib.RankMixerError):
             _lib.rm_debug_fp8_wait_timeout(us, 0)
+
+
+@pytest.mark.parametrize("first", ["pass", "api.fp8_quantize(X)", "api.fp8_quantize_weight(W)", "api.fp8_dequantize(x)"])
+def test_first_calls_may_be_captured(first):
+    """Products and gradients captured at their first call, after another 8-bit call or none."""
+    in_child(f"""
+        X, W = torch.ones((40, 2, 256), device="cuda"), torch.ones((2, 256, 256), device="cuda")
+        dY = torch.ones((40, 2, 256), device="cuda").to(torch.bfloat16)
+        def ones(shape, blocks):
+            return api.Fp8Tensor(torch.ones(shape, device="cuda").to(torch.float8_e4m3fn),
+                                 torch.full(blocks, 127, dtype=torch.uint8, device="cuda"), shape[-1])
+        x, w = ones((40, 2, 256), (40, 2, 4)), ones((2, 256, 256), (2, 2, 4))
+        {first}
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y, (dw, db) = api.fp8_matmul(x, w), api.fp8_wgrad(x, dY)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (y == 256).all() and (dw == 40).all() and (db == 40).all()
+        assert api.fp8_sync_status() == _lib.RM_OK
+    """)
