@@ -353,8 +353,10 @@ _FORMATS = {"e4m3": _lib.RM_E4M3, "e5m2": _lib.RM_E5M2}
 _F8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 _F8_CODE = {torch.float8_e4m3fn: _lib.RM_E4M3, torch.float8_e5m2: _lib.RM_E5M2}
 _CODE = {torch.bfloat16: _lib.RM_BF16, torch.float32: _lib.RM_F32}
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+
+
+def _raw_stream(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)      # not there on a torch without CUDA
 
 
 class Fp8Tensor:
@@ -432,7 +434,9 @@ def _fp8_new(wanted: tuple, device: torch.device, index: int) -> list:
 
 def _fp8_device(*indices) -> int:
     """The current device, on which the calls run: every tensor has to live there."""
-    d = _current_device()
+    if indices[0] < 0:
+        raise ValueError(f"tensors must be on the current CUDA device, got devices {indices}")
+    d = torch._C._cuda_getDevice()
     if indices != (d,) * len(indices):
         raise ValueError(f"tensors must be on the current CUDA device (cuda:{d}), got devices {indices}")
     return d

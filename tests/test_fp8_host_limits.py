@@ -2,6 +2,8 @@
 needed)."""
 import ctypes
 import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -98,3 +100,18 @@ def test_sizes_are_refused_before_they_overflow_when_rounded_up(lib, mem, n):
     assert lib.rm_fp8_matmul(q, q, None, p, _lib.RM_F32, n, 1, 128, 128, 0, None) == BAD
     assert lib.rm_fp8_matmul(q, q, None, p, _lib.RM_F32, 1, 1, 128, n, 1, None) == BAD
     assert lib.rm_fp8_wgrad(q, p, p, p, _lib.RM_F32, 1, 1, 128, n // 8 * 8, None) == BAD
+
+
+def test_the_package_imports_on_a_torch_without_cuda():
+    """A torch built without CUDA has none of torch._C's stream and device functions."""
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "from rankmixer_feature_interaction_gb300 import api\n"
+            "try:\n    api.fp8_quantize(torch.zeros(2, 3))\n"
+            "except ValueError as e:\n    assert 'CUDA' in str(e), e\n"
+            "else:\n    raise SystemExit('not refused')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, env={**os.environ, "PYTHONPATH": root},
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
