@@ -47,10 +47,12 @@ constexpr int BM = 128, BK = 128;
 constexpr int SAMPLES_MAX = 128;             // of a tile
 constexpr int W_BYTES = BM * BK;
 constexpr int SF_SLOTS = 4, SF_BYTES = 1024;
-// Where the tiles are at most half of the SMs, 2 or 4 CTAs share each tile's K; only 2
-// for more than 32 samples, whose sums (32 KB from each CTA into one) take longer than
-// the shorter K saves: T = 8, K = 2048, N = 512, 64 samples 6.9 us with 4, 6.5 with 2,
-// 7.6 with 1; 16 samples 4.6 with 4, 7.1 with 1.
+// Where as many clusters are resident at once as there are tiles, 2 or 4 CTAs share each
+// tile's K.  Of clusters of four 36 are resident (not 38, a quarter of the SMs): K = 2048,
+// 8 samples 4.7 us for 36 tiles, 8.0 for 37 with a second round of them, 5.2 with clusters
+// of two.  Only 2 for more than 32 samples, whose sums (32 KB from each CTA into one) take
+// longer than the shorter K saves: T = 8, K = 2048, N = 512, 64 samples 6.9 us with 4, 6.5
+// with 2, 7.6 with 1; 16 samples 4.6 with 4, 7.1 with 1.
 constexpr int MAX_SPLIT = 4, MAX_SPLIT_64 = 2;
 
 // Four words to another CTA's shared memory, counted there by its barrier.
@@ -488,6 +490,14 @@ cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, Args a, int num_sm
     cudaError_t e = smem_attr_once((const void*)k, Cfg<NB>::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     const dim3 block(Cfg<NB>::THREADS);
+    const int groups = (a.kblocks + 3) / 4;
+    a.split = 1, a.groups = groups;
+    for (int c = 2; c <= (a.B > 32 ? MAX_SPLIT_64 : MAX_SPLIT) && (long long)c * a.tiles <= num_sms && c <= groups; c *= 2) {
+        const int each = (groups + c - 1) / c;
+        if ((c - 1) * each < groups &&                         // no CTA is left without k-blocks
+            a.tiles <= cluster_occupancy_once((const void*)k, Cfg<NB>::THREADS, Cfg<NB>::SMEM_BYTES, c, num_sms))
+            a.split = c, a.groups = each;
+    }
     if (a.split == 1) {
         a.stages = Cfg<NB>::STAGES;
         const int ctas = a.tiles < num_sms ? a.tiles : num_sms;
@@ -544,13 +554,6 @@ cudaError_t launch_fp8_stream(const Fp8Product& p, const Fp8Device& dev, cudaStr
     a.kblocks = (p.K + BK - 1) / BK;
     a.m_tiles = (p.B + SAMPLES_MAX - 1) / SAMPLES_MAX;
     a.tiles = (int)stream_tiles(p);
-    const int groups = (a.kblocks + 3) / 4;
-    a.split = 1, a.groups = groups;
-    const int most = p.B > 32 ? MAX_SPLIT_64 : MAX_SPLIT;
-    for (int c = 2; c <= most && (long long)c * a.tiles <= dev.num_sms && c <= groups; c *= 2) {
-        const int each = (groups + c - 1) / c;
-        if ((c - 1) * each < groups) a.split = c, a.groups = each;     // no CTA is left without k-blocks
-    }
     a.xs = p.x.scales, a.xs_ld = p.x.lds;
     a.ws = p.w.scales, a.ws_ld = p.w.lds;
     const int wr = p.trans ? p.N : p.K, wc = p.trans ? p.K : p.N;

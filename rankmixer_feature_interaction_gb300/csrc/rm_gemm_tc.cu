@@ -32,6 +32,7 @@
 #include <cstdlib>
 #include <map>
 #include <mutex>
+#include <tuple>
 #include <string>
 #include <utility>
 
@@ -55,22 +56,22 @@ cudaError_t smem_attr_once(const void* func, int bytes) {
     return e;
 }
 
-int pair_occupancy_once(const void* func, int threads, int smem, int num_sms) {
+int cluster_occupancy_once(const void* func, int threads, int smem, int size, int num_sms) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return num_sms / 2;
+    if (cudaGetDevice(&dev) != cudaSuccess) return num_sms / size;
     static std::mutex mu;
-    static std::map<std::pair<const void*, int>, int> cache;
+    static std::map<std::tuple<const void*, int, int>, int> cache;
     std::lock_guard<std::mutex> lk(mu);
-    auto key = std::make_pair(func, dev);
+    auto key = std::make_tuple(func, dev, size);
     auto it = cache.find(key);
     if (it != cache.end()) return it->second;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * (num_sms / 2)), 1, 1);
+    cfg.gridDim = dim3((unsigned)(size * (num_sms / size)), 1, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = (size_t)smem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.x = (unsigned)size;
     attr.val.clusterDim.y = 1;
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
@@ -78,10 +79,14 @@ int pair_occupancy_once(const void* func, int threads, int smem, int num_sms) {
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, func, &cfg) != cudaSuccess || n <= 0) {
         cudaGetLastError();
-        n = num_sms / 2;
+        n = num_sms / size;
     }
     cache[key] = n;
     return n;
+}
+
+int pair_occupancy_once(const void* func, int threads, int smem, int num_sms) {
+    return cluster_occupancy_once(func, threads, smem, 2, num_sms);
 }
 
 namespace tc {

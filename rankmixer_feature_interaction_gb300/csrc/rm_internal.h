@@ -43,9 +43,10 @@ void set_last_error(const char* fmt, ...);
 // set it once per (kernel, device), so that a process driving several GPUs
 // gets it on each.
 cudaError_t smem_attr_once(const void* func, int bytes);
-// Resident clusters of two CTAs of `func` on the current device at `smem`
-// bytes per CTA and `threads` per CTA, cached per (kernel, device); falls back
-// to half the SM count if the query fails.
+// Resident clusters of `size` CTAs of `func` on the current device at `smem`
+// bytes per CTA and `threads` per CTA, cached per (kernel, device, size); falls
+// back to the SM count / size if the query fails.  pair_occupancy_once: size 2.
+int cluster_occupancy_once(const void* func, int threads, int smem, int size, int num_sms);
 int pair_occupancy_once(const void* func, int threads, int smem, int num_sms);
 
 inline size_t act_size(Act a) { return a == Act::F32 ? 4 : 2; }

@@ -274,3 +274,41 @@ def test_first_calls_may_be_captured(first):
         assert (y == 256).all() and (dw == 40).all() and (db == 40).all()
         assert api.fp8_sync_status() == _lib.RM_OK
     """)
+
+
+# ---- how few tiles share their sums ---------------------------------------------------------------------
+
+def graph_us(call, n=50, reps=7):
+    """Device time of one call among others, in a graph (the best of some replays)."""
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(n):
+            call()
+    best = math.inf
+    for _ in range(reps):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3 / n)
+    return best
+
+
+@pytest.mark.parametrize("B,K", [(8, 2048), (8, 4096), (40, 2048)])
+def test_fewer_tiles_do_not_take_longer_than_more(B, K):
+    """One tile a token.  K is shared by clusters of thread blocks only where all of them are resident at once: with a
+    second round of clusters 38 tiles took 1.5 times as long as 39 by clusters of two."""
+    us = {}
+    for T in (30, 34, 36, 37, 38, 39, 44, 72, 76, 77):
+        x = fp8_quantize(torch.randn((B, T, K), generator=torch.Generator(device=DEV).manual_seed(97), device=DEV))
+        w = fp8_quantize_weight(torch.randn((T, K, 128), generator=torch.Generator(device=DEV).manual_seed(98), device=DEV))
+        us[T] = graph_us(lambda: fp8_matmul(x, w))
+    print(" ".join(f"{t}: {v:.2f}" for t, v in us.items()))
+    for few in us:
+        for more in us:
+            if few < more:
+                assert us[few] <= 1.25 * us[more], (few, more, us)
+    ok()
