@@ -108,6 +108,20 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
     return mbar_wait_bounded(bar, parity, abort, err, timeout_ns);
 }
 
+// For a CTA that gives up because a wait ran out, after all of its warps have come
+// out of their loops: loads that it issued into its ring, MMAs and their commits may
+// still be under way, and must not reach its shared or tensor memory once these
+// belong to another CTA.  No barrier tells of all of them at this point; they take
+// microseconds, so they are given a millisecond.
+__device__ __forceinline__ void settle_when_aborted(uint32_t abort_saddr) {
+    int abort;
+    asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(abort) : "r"(abort_saddr) : "memory");
+    if (abort) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000u) __nanosleep(1000);
+    }
+}
+
 // Arrive on the pair's barrier (a shared::cluster address) after writes to this
 // CTA's own shared memory that fence_proxy_async_smem has ordered before the
 // tensor core's reads of it.  The fence carries the data; the arrival needs no
