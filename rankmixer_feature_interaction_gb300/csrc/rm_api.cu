@@ -58,6 +58,15 @@ void rm::set_last_error(const char* fmt, ...) {
     g_last_error = buf;
 }
 
+bool rm::nvtx_on() {
+    static int env = -1;
+    if (env < 0) {
+        const char* v = getenv("RM_NVTX");
+        env = (v && v[0] == '1') ? 1 : 0;
+    }
+    return env == 1;
+}
+
 cudaError_t rm::debug_bounds_fail(const char* what) {
     t_bounds_what = what;
     return cudaErrorInvalidValue;
@@ -376,15 +385,6 @@ const char* const kKindNames[RM_K_COUNT] = {
     "rm:mix_ln1", "rm:gemm1", "rm:gemm2", "rm:ln2_out", "rm:pool", "rm:rowstats", "rm:moe_route", "rm:moe_gemm1",
     "rm:moe_gemm2", "rm:misc", "rm:moe_combine", "rm:bwd_recompute", "rm:bwd_dgrad", "rm:bwd_wgrad",
     "rm:bwd_rows", "rm:tokenize", "rm:head", "rm:unimix", "rm:pffn"};
-
-bool nvtx_on() {
-    static int env = -1;
-    if (env < 0) {
-        const char* v = getenv("RM_NVTX");
-        env = (v && v[0] == '1') ? 1 : 0;
-    }
-    return env == 1;
-}
 
 struct ProfScope {
     rm_ctx* c;

@@ -1,5 +1,7 @@
 // C entry points of the 8-bit operators (include/rankmixer.h, "8-bit operands
 // and checkpoints"): argument checks, workspace layout, launches.
+#include <nvtx3/nvToolsExt.h>
+
 #include <mutex>
 #include <new>
 #include <unordered_map>
@@ -25,6 +27,21 @@ rm_status cuda_fail(cudaError_t e, const char* what) {
     do {                                                   \
         cudaError_t _e = (expr);                           \
         if (_e != cudaSuccess) return cuda_fail(_e, what); \
+    } while (0)
+// A launch, in an NVTX range of its kind's name where these are on (RM_NVTX).
+struct Range {
+    const bool on = nvtx_on();
+    explicit Range(const char* name) {
+        if (on) nvtxRangePushA(name);
+    }
+    ~Range() {
+        if (on) nvtxRangePop();
+    }
+};
+#define RM_LAUNCH(kind, what, ...)                               \
+    do {                                                         \
+        const Range _r("rm:fp8_" #kind);                         \
+        RM_CHECK_CUDA(launch_fp8_##kind(__VA_ARGS__), what);     \
     } while (0)
 #define RM_CHECK(expr)                        \
     do {                                      \
@@ -235,8 +252,7 @@ rm_status rm_fp8_quantize(const void* X, rm_dtype dtype, long long rows, int col
     if (ldx < cols) return fail(RM_ERR_INVALID_ARG, "ldx (%lld) is below cols (%d)", ldx, cols);
     if (!aligned(X, dtype == RM_F32 ? 4 : 2)) return fail(RM_ERR_INVALID_ARG, "X must be aligned to its elements");
     RM_CHECK(check_tensor(out, cols, "out", false));
-    RM_CHECK_CUDA(launch_fp8_quantize(dtype == RM_F32, X, rows, cols, ldx, view(*out), nullptr, as_stream(stream)),
-                  "quantize");
+    RM_LAUNCH(quantize, "quantize", dtype == RM_F32, X, rows, cols, ldx, view(*out), nullptr, as_stream(stream));
     return RM_OK;
 }
 
@@ -248,8 +264,7 @@ rm_status rm_fp8_quantize_weight(const void* W, rm_dtype dtype, int T, int K, in
     if ((K + kFp8Block - 1) / kFp8Block > 65535) return fail(RM_ERR_INVALID_ARG, "K (%d) is too large", K);
     if (!aligned(W, dtype == RM_F32 ? 4 : 2)) return fail(RM_ERR_INVALID_ARG, "W must be aligned to its elements");
     RM_CHECK(check_tensor(out, N, "out", true));
-    RM_CHECK_CUDA(launch_fp8_quantize_weight(dtype == RM_F32, W, T, K, N, view(*out), as_stream(stream)),
-                  "quantize weight");
+    RM_LAUNCH(quantize_weight, "quantize weight", dtype == RM_F32, W, T, K, N, view(*out), as_stream(stream));
     return RM_OK;
 }
 
@@ -261,8 +276,7 @@ rm_status rm_fp8_dequantize(const rm_fp8_tensor* in, long long rows, int cols, v
     if (ldy < cols) return fail(RM_ERR_INVALID_ARG, "ldy (%lld) is below cols (%d)", ldy, cols);
     if (!aligned(Y, dtype == RM_F32 ? 4 : 2)) return fail(RM_ERR_INVALID_ARG, "Y must be aligned to its elements");
     RM_CHECK(check_tensor(in, cols, "in", false));
-    RM_CHECK_CUDA(launch_fp8_dequantize(view(*in), rows, cols, Y, dtype == RM_F32, ldy, as_stream(stream)),
-                  "dequantize");
+    RM_LAUNCH(dequantize, "dequantize", view(*in), rows, cols, Y, dtype == RM_F32, ldy, as_stream(stream));
     return RM_OK;
 }
 
@@ -278,8 +292,7 @@ rm_status rm_fp8_matmul(const rm_fp8_tensor* x, const rm_fp8_tensor* W, const fl
         return fail(RM_ERR_INVALID_ARG, "Y and bias must be 16-byte aligned");
     Fp8Device dev;
     RM_CHECK(device_info(&dev));
-    RM_CHECK_CUDA(launch_fp8_product(product(dtype, *x, *W, transpose_w != 0, bias, Y, B, T, K, N), dev, as_stream(stream)),
-                  "8-bit product");
+    RM_LAUNCH(product, "8-bit product", product(dtype, *x, *W, transpose_w != 0, bias, Y, B, T, K, N), dev, as_stream(stream));
     return RM_OK;
 }
 
@@ -296,7 +309,7 @@ rm_status rm_fp8_wgrad(const rm_fp8_tensor* x, const void* dY, void* dW, void* d
     const cudaStream_t s = as_stream(stream);
     Fp8Device dev;
     RM_CHECK(device_info(&dev));
-    RM_CHECK_CUDA(launch_fp8_wgrad(view(*x), dY, dW, db, dtype == RM_F32, B, T, K, N, dev, s), "weight gradient");
+    RM_LAUNCH(wgrad, "weight gradient", view(*x), dY, dW, db, dtype == RM_F32, B, T, K, N, dev, s);
     return RM_OK;
 }
 
@@ -329,16 +342,16 @@ rm_status rm_fp8_pffn_forward(const rm_fp8_pffn* p, const void* X, rm_dtype x_dt
     const cudaStream_t s = as_stream(stream);
     Fp8Device dev;
     RM_CHECK(device_info(&dev));
-    RM_CHECK_CUDA(launch_fp8_quantize(x_dtype == RM_F32, X, rows, D, D, view(w.kept.x), nullptr, s), "quantize");
+    RM_LAUNCH(quantize, "quantize", x_dtype == RM_F32, X, rows, D, D, view(w.kept.x), nullptr, s);
     Fp8Product g = product(RM_BF16, w.kept.x, p->W1, false, p->b1, nullptr, B, T, D, F);
     g.epi = FP8_GELU;
     g.follows = true;
     g.o0 = view(w.kept.a);
     if (keep) g.o1 = view(w.kept.u);
-    RM_CHECK_CUDA(launch_fp8_product(g, dev, s), "8-bit layer 1");
+    RM_LAUNCH(product, "8-bit layer 1", g, dev, s);
     g = product(v_dtype, w.kept.a, p->W2, false, p->b2, V, B, T, F, D);
     g.follows = true;
-    RM_CHECK_CUDA(launch_fp8_product(g, dev, s), "8-bit layer 2");
+    RM_LAUNCH(product, "8-bit layer 2", g, dev, s);
     return RM_OK;
 }
 
@@ -366,20 +379,20 @@ rm_status rm_fp8_pffn_backward(const rm_fp8_pffn* p, const void* dV, rm_dtype dv
     Fp8Device dev;
     RM_CHECK(device_info(&dev));
     const void* dv16 = f32 ? w.dv16 : dV;
-    RM_CHECK_CUDA(launch_fp8_quantize(f32, dV, rows, D, D, view(w.dv), f32 ? w.dv16 : nullptr, s), "quantize dV");
+    RM_LAUNCH(quantize, "quantize dV", f32, dV, rows, D, D, view(w.dv), f32 ? w.dv16 : nullptr, s);
     Fp8Product g = product(RM_BF16, w.dv, p->W2, true, nullptr, w.du16, B, T, D, F);
     g.epi = FP8_DGELU;
     g.follows = true;
     g.o0 = view(w.du);
     g.o1 = view(kept->u);
-    RM_CHECK_CUDA(launch_fp8_product(g, dev, s), "dU");
+    RM_LAUNCH(product, "dU", g, dev, s);
     if (dX) {
         g = product(dx_dtype, w.du, p->W1, true, nullptr, dX, B, T, F, D);
         g.follows = true;
-        RM_CHECK_CUDA(launch_fp8_product(g, dev, s), "dX");
+        RM_LAUNCH(product, "dX", g, dev, s);
     }
-    RM_CHECK_CUDA(launch_fp8_wgrad(view(kept->a), dv16, grads->dW2, grads->db2, g32, B, T, F, D, dev, s), "dW2");
-    RM_CHECK_CUDA(launch_fp8_wgrad(view(kept->x), w.du16, grads->dW1, grads->db1, g32, B, T, D, F, dev, s), "dW1");
+    RM_LAUNCH(wgrad, "dW2", view(kept->a), dv16, grads->dW2, grads->db2, g32, B, T, F, D, dev, s);
+    RM_LAUNCH(wgrad, "dW1", view(kept->x), w.du16, grads->dW1, grads->db1, g32, B, T, D, F, dev, s);
     return RM_OK;
 }
 

@@ -36,6 +36,9 @@ cudaError_t debug_bounds_fail(const char* what);
         if (::rm::kDebugBounds && !(cond)) return ::rm::debug_bounds_fail(#cond); \
     } while (0)
 
+// Whether launches are wrapped in NVTX ranges (RM_NVTX=1 in the environment).
+bool nvtx_on();
+
 // Set what rm_last_error() returns on this host thread (printf-style).
 void set_last_error(const char* fmt, ...);
 
