@@ -72,14 +72,18 @@ cudaError_t rm::debug_bounds_fail(const char* what) {
     return cudaErrorInvalidValue;
 }
 
+const char* rm::take_debug_bounds() {
+    const char* what = t_bounds_what;
+    t_bounds_what = nullptr;
+    return what;
+}
+
 namespace {
 
 rm_status cuda_fail(cudaError_t e, const char* what) {
-    if (e == cudaErrorInvalidValue && t_bounds_what) {
-        const char* cond = t_bounds_what;
-        t_bounds_what = nullptr;
-        return fail(RM_ERR_INVALID_ARG, "%s: bounds check failed: %s", what, cond);
-    }
+    if (e == cudaErrorInvalidValue)
+        if (const char* cond = take_debug_bounds())
+            return fail(RM_ERR_INVALID_ARG, "%s: bounds check failed: %s", what, cond);
     if (e == cudaErrorMemoryAllocation)
         return fail(RM_ERR_OOM, "%s: %s", what,
                     alloc_failure_was_injected() ? "injected failure (device allocation)" : cudaGetErrorString(e));

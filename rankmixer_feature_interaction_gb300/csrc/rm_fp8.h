@@ -19,6 +19,13 @@ struct Fp8View {
     bool e5m2;
 };
 
+// For the launchers' checks in the debug build: rows that hold `cols` codes and their exponent bytes.
+inline bool fp8_on(const void* p, unsigned n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1u)) == 0; }
+inline bool fp8_holds(const Fp8View& v, int cols) {
+    return fp8_on(v.codes, 16) && fp8_on(v.scales, 4) && v.ld >= cols && v.ld % 16 == 0 &&
+           v.lds >= (cols + kFp8Block - 1) / kFp8Block && v.lds % 4 == 0;
+}
+
 // X [rows][ldx] (float, or bf16) -> out.  copy (nullable; of 16-byte aligned float
 // rows to e4m3 only): the rows in bf16, [rows][cols] contiguous, cols a multiple of 16.
 cudaError_t launch_fp8_quantize(bool f32, const void* X, long long rows, int cols, long long ldx, const Fp8View& out,

@@ -20,6 +20,9 @@ rm_status fail(rm_status st, const char* fmt, A... a) {
     return st;
 }
 rm_status cuda_fail(cudaError_t e, const char* what) {
+    if (e == cudaErrorInvalidValue)
+        if (const char* cond = take_debug_bounds())
+            return fail(RM_ERR_INVALID_ARG, "%s: bounds check failed: %s", what, cond);
     if (e == cudaErrorNotSupported) return fail(RM_ERR_UNSUPPORTED, "%s: shape not supported by this kernel", what);
     return fail(e == cudaErrorMemoryAllocation ? RM_ERR_OOM : RM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }

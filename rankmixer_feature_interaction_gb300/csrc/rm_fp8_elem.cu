@@ -378,12 +378,15 @@ cudaError_t dequantize_as(const Fp8View& in, long long rows, int cols, void* Y, 
 
 cudaError_t launch_fp8_quantize(bool f32, const void* X, long long rows, int cols, long long ldx, const Fp8View& out,
                                 void* copy, cudaStream_t s) {
+    RM_HOST_BOUNDS(rows >= 1 && cols >= 1 && ldx >= cols && fp8_on(X, f32 ? 4 : 2) && fp8_holds(out, cols));
+    RM_HOST_BOUNDS(!copy || (cols % 16 == 0 && fp8_on(copy, 16)));
     return f32 ? quantize_as<float>(X, rows, cols, ldx, out, copy, s)
                : quantize_as<__nv_bfloat16>(X, rows, cols, ldx, out, copy, s);
 }
 
 cudaError_t launch_fp8_quantize_weight(bool f32, const void* W, int T, int K, int N, const Fp8View& out,
                                        cudaStream_t s) {
+    RM_HOST_BOUNDS(T >= 1 && K >= 1 && N >= 1 && fp8_on(W, f32 ? 4 : 2) && fp8_holds(out, N) && !out.e5m2);
     const dim3 grid((N + kFp8Block - 1) / kFp8Block, (K + kFp8Block - 1) / kFp8Block, T);
     const bool vec = aligned16p(W) && (size_t)N * (f32 ? 4 : 2) % 16 == 0;
     if (f32)
@@ -395,6 +398,7 @@ cudaError_t launch_fp8_quantize_weight(bool f32, const void* W, int T, int K, in
 
 cudaError_t launch_fp8_dequantize(const Fp8View& in, long long rows, int cols, void* Y, bool f32, long long ldy,
                                   cudaStream_t s) {
+    RM_HOST_BOUNDS(rows >= 1 && cols >= 1 && ldy >= cols && fp8_on(Y, f32 ? 4 : 2) && fp8_holds(in, cols));
     if (f32)
         return in.e5m2 ? dequantize_as<float, true>(in, rows, cols, Y, ldy, s)
                        : dequantize_as<float, false>(in, rows, cols, Y, ldy, s);

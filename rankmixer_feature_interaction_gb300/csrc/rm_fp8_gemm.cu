@@ -648,6 +648,11 @@ cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap&
 
 cudaError_t launch_fp8_product(const Fp8Product& p, const Fp8Device& dev, cudaStream_t s) {
     using namespace f8;
+    RM_HOST_BOUNDS(p.B >= 1 && p.T >= 1 && p.K >= 1 && p.N >= 1 && fp8_holds(p.x, p.K) && !p.w.e5m2);
+    RM_HOST_BOUNDS(fp8_holds(p.w, p.trans ? p.K : p.N) && (!p.bias || fp8_on(p.bias, 16)));
+    RM_HOST_BOUNDS(p.epi == FP8_GELU || fp8_on(p.y, 16));
+    RM_HOST_BOUNDS(p.epi == FP8_OUT_BF16 || p.epi == FP8_OUT_F32 || (p.N % 16 == 0 && fp8_holds(p.o0, p.N)));
+    RM_HOST_BOUNDS(p.epi == FP8_DGELU || p.o1.codes ? fp8_holds(p.o1, p.N) && !p.o1.e5m2 : true);
     if (fp8_streams(p, dev)) return launch_fp8_stream(p, dev, s);
     Args a{};
     a.B = p.B, a.T = p.T, a.K = p.K, a.N = p.N;

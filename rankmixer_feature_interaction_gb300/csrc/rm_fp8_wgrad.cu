@@ -600,6 +600,8 @@ cudaError_t run(const CUtensorMap& mx, const CUtensorMap& my, const CUtensorMap&
 cudaError_t launch_fp8_wgrad(const Fp8View& x, const void* dY, void* dW, void* db, bool f32, int B, int T, int K, int N,
                              const Fp8Device& dev, cudaStream_t s) {
     using namespace f8w;
+    RM_HOST_BOUNDS(B >= 1 && T >= 1 && K >= 1 && N >= 1 && N % 8 == 0 && fp8_holds(x, K) && !x.e5m2);
+    RM_HOST_BOUNDS(fp8_on(dY, 16) && fp8_on(dW, 16) && (!db || fp8_on(db, 16)));
     Args a{};
     a.B = B, a.T = T, a.K = K, a.N = N;
     a.m_tiles = (K + 2 * BM - 1) / (2 * BM);

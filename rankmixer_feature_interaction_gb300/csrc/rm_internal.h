@@ -31,6 +31,7 @@ constexpr bool kDebugBounds = false;
 // Host-side launcher check of the debug build: a failed condition returns
 // cudaErrorInvalidValue from the launcher with the condition's text recorded.
 cudaError_t debug_bounds_fail(const char* what);
+const char* take_debug_bounds();    // that text, once (nullptr: none failed since)
 #define RM_HOST_BOUNDS(cond)                                                   \
     do {                                                                       \
         if (::rm::kDebugBounds && !(cond)) return ::rm::debug_bounds_fail(#cond); \
