@@ -575,7 +575,6 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
 
     tc_fence_before();
     __syncthreads();
-    settle_when_aborted(pair_bar(EPI_WARPS / 2) + 4u);
     cluster_sync_all();    // no CTA leaves while its peer may still touch its memory
     if (warp == 3) {
         tc_fence_after();

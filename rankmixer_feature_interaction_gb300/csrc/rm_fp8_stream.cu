@@ -477,7 +477,6 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
 
     tc_fence_before();
     __syncthreads();
-    settle_when_aborted(part_bar + 8u + 4u);
     if (args.split > 1) cluster_sync_all();      // no CTA leaves while another may still write to its memory
     if (warp == 4) {
         tc_fence_after();

@@ -100,26 +100,24 @@ __device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
 
 // mbar_wait_bounded that looks at the clock only after some tries: reading the
 // global timer takes longer than most of these waits.
+// A warp that gives up stays for another millisecond: loads into the CTA's ring, MMAs
+// and their commits may still be under way, and must not reach shared or tensor memory
+// once these belong to another CTA.  They take microseconds, nothing is issued for long
+// after one of the roles has stopped, and the CTA ends only when all of its warps have.
+// (At the end of the kernel the same wait cost a register and 3% of the FFN's forward.)
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort, int* err,
                                              uint64_t timeout_ns) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
         if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait_bounded(bar, parity, abort, err, timeout_ns);
-}
-
-// For a CTA that gives up because a wait ran out, after all of its warps have come
-// out of their loops: loads that it issued into its ring, MMAs and their commits may
-// still be under way, and must not reach its shared or tensor memory once these
-// belong to another CTA.  No barrier tells of all of them at this point; they take
-// microseconds, so they are given a millisecond.
-__device__ __forceinline__ void settle_when_aborted(uint32_t abort_saddr) {
-    int abort;
-    asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(abort) : "r"(abort_saddr) : "memory");
-    if (abort) {
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 1000000u) __nanosleep(1000);
-    }
+    if (mbar_wait_bounded(bar, parity, abort, err, timeout_ns)) return true;
+    uint32_t t0, t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t0));
+    do {
+        __nanosleep(1000);
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    } while (t - t0 < 1000000u);
+    return false;
 }
 
 // Arrive on the pair's barrier (a shared::cluster address) after writes to this

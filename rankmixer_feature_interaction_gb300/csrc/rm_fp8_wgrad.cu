@@ -562,7 +562,6 @@ fp8_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
 
     tc_fence_before();
     __syncthreads();
-    settle_when_aborted(bar0 + 8u * (4 * STAGES + 2 * RAWS + 4) + 4u);
     cluster_sync_all();    // no CTA leaves while its peer may still touch its memory
     if (warp == 3) {
         tc_fence_after();
