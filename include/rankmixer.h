@@ -479,7 +479,10 @@ RM_API rm_status rm_debug_mix_residual(const void *X, int from_z, float *Y, int 
  *     t K + k of codes as above, and the byte of the block (i, j) of token t's
  *     matrix at scales + (t ceil(K / 128) + i) lds + j.  One copy serves the
  *     forward product and, through transpose_w, the data gradient.
- * codes must be 16-byte, scales 4-byte aligned.  Rows are padded: bytes past
+ * codes must be 16-byte, scales 4-byte aligned, and so (to 16 bytes) the other
+ * buffers of the products, the gradients and the FFN; what is saved and
+ * restored (X, W and Y of rm_fp8_quantize, rm_fp8_quantize_weight and
+ * rm_fp8_dequantize) only to its own elements.  Rows are padded: bytes past
  * cols (codes) and past the last block (scales) are never interpreted.
  *
  * These calls need no context: they run on the current device, which must own
@@ -584,8 +587,9 @@ RM_API rm_status rm_fp8_pffn_forward(const rm_fp8_pffn *p, const void *X, rm_dty
  *   dU = (Q(dV) W2^T) Gelu'(u),  dX = Q(dU) W1^T,
  *   dW2 = a^T dV, db2 = sum dV,  dW1 = x^T dU, db1 = sum dU   (sums over b).
  * dV: device [B][T][D] of dv_dtype; dX (nullable): device [B][T][D] of
- * dx_dtype.  The weight gradients take dV and dU rounded to bf16.  kept is
- * read only: a second backward from it gives the same values. */
+ * dx_dtype.  All four gradients of weights and biases take dV and dU rounded to
+ * bf16, a float32 dV too.  kept is read only: a second backward from it gives
+ * the same values. */
 RM_API rm_status rm_fp8_pffn_backward(const rm_fp8_pffn *p, const void *dV, rm_dtype dv_dtype, const rm_fp8_kept *kept,
                                       void *dX, rm_dtype dx_dtype, const rm_fp8_grads *grads, int B, void *work,
                                       long long work_bytes, void *stream);

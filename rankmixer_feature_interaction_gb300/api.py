@@ -603,7 +603,8 @@ class Fp8PFFN:
     def backward(self, dV: torch.Tensor, kept: dict, dx_dtype: str = "bf16", grad_dtype: str = "f32",
                  with_dX: bool = True) -> tuple[torch.Tensor | None, dict]:
         """(dX [B, T, D], {"dW1", "db1", "dW2", "db2"}) for the gradient dV at V, from what
-        forward_train kept."""
+        forward_train kept.  The gradients of weights and biases are summed in float32 from dV
+        and dU rounded to bf16 (a float32 dV too); grad_dtype "bf16": B at most 2^17."""
         B = self._rows(dV, "dV")
         for k, cols in (("x", self.D), ("u", self.F), ("a", self.F)):
             if _fp8_activation(kept[k], f"kept[{k!r}]") != (B, self.T, cols):

@@ -25,7 +25,7 @@
 // Measured (within a graph): T = 32, K = 1536, N = 6144, bf16 out, one sample 48.3
 // us = 6.3 TB/s of W, 64 samples 54 us, 128 samples 61 us; K = 6144, N = 1536 (384
 // tiles, 2.5 rounds of the SMs) 53.5, 55.6 and 59.5 us.  Few tiles are bound by
-// latency: T = 8, K = 512, N = 2048 3.1 us, K = 2048, N = 512 (32 tiles) 4.8 us, 7.1
+// latency: T = 8, K = 512, N = 2048 3.2 us, K = 2048, N = 512 (32 tiles) 4.6 us, 7.1
 // without sharing K.
 // The kernel is launched while its predecessor may still run.  Where that
 // predecessor is one of this library's own launches of the same call, W was in

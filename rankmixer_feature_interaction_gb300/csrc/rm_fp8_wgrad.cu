@@ -28,8 +28,8 @@
 // db's sums cost a hop on the operand ring, so only the k-blocks that are summed
 // take it (all of them did at first: 844 us against 816 at the size below, in f32).
 //
-// Measured, T = 32, K = 1536, N = 6144, dW and db: B = 2048 816 us in f32 (1516
-// TFLOP/s) and 773 us in bf16, B = 1024 476 and 421 us; B = 8, where a tile is one
+// Measured, T = 32, K = 1536, N = 6144, dW and db: B = 2048 812 us in f32 (1523
+// TFLOP/s) and 783 us in bf16, B = 1024 472 and 422 us; B = 8, where a tile is one
 // k-block and the time is dW's, 207 us (5.8 TB/s) and 109 us (5.5 TB/s).  Bound at
 // large B by the tensor cores under the power limit and the restorers beside them
 // (shared memory), at small B by dW's stores.
