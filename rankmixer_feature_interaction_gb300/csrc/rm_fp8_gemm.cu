@@ -29,8 +29,8 @@
 // 64 columns have been read, and a ring of four scale slots from column 448 (4
 // columns for x's 128 rows, 8 for W's 256 columns).
 // Measured, T = 32, bf16 out: 4096 samples, 6144 to 1536 717 us (3.45 PFLOP/s), 1536
-// to 6144 836 us (2.96, 12 k-blocks a tile); 1024 samples 205 and 230 us (between
-// boxes up to 736 and 957 us at 4096).  Bound by the tensor cores, which the power limit
+// to 6144 836 us (2.96, 12 k-blocks a tile); 1024 samples 205 and 230 us (on other
+// GPUs up to 736 and 957 us at 4096).  Bound by the tensor cores, which the power limit
 // slows at the large sizes, and where a tile has few k-blocks by what lies between two
 // tiles (the shared columns); with an 8-bit
 // output and Gelu or its derivative, by the epilogue's instructions beside them (50
