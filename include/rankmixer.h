@@ -606,6 +606,156 @@ RM_API rm_status rm_fp8_sync_status(void *stream);
  * rm_fp8_sync_status reports the wait that ran out. */
 RM_API rm_status rm_debug_fp8_wait_timeout(int timeout_us, void *stream);
 
+/* ---- 4-bit operands ------------------------------------------------------
+ *
+ * Microscaled 4-bit floating point: codes of four bits (e2m1: 0, 1/2, 1, 3/2,
+ * 2, 3, 4, 6 and their negatives), two a byte, the value of even index in the
+ * low four bits, and one exponent byte E per block of 32 consecutive values
+ * along K, the axis that the products sum over; a value is code * 2^(E - 127).
+ * The calls that make such tensors choose for every block the smallest E (at
+ * least 1; 127 for a block of zeros) for which its largest magnitude is at most
+ * 6 2^(E - 127), so that no value saturates, and round value / 2^(E - 127) to
+ * the nearest code, ties to the even one.  A block with an infinity or a NaN
+ * has E = 255 and is NaN as a whole (the codes have neither).  Restoring is
+ * exact in float32 (and in bf16, except below 2^-133).
+ *   Activations: rows of `cols` values; row r has its codes at codes + r ld (ld
+ *     a multiple of 16, at least 16 ceil(cols / 32)) and the byte of its block j
+ *     at scales + r lds + j (lds a multiple of 16, at least ceil(cols / 32)).
+ *     Codes between cols and the end of the last block are zero (the calls
+ *     below write them so); what lies behind is not interpreted.
+ *   Weights: matrices [G][K][N] (y = x W) are kept as rows (g, n) along K: row
+ *     g N + n of codes as above, and exponent bytes in the order in which the
+ *     tensor cores take them: those of rows 128 i .. + 127 of matrix g and
+ *     values 128 j .. + 127 of K are the 512 bytes at
+ *     scales + 512 ((g ceil(N / 128) + i) lds + j), row r's block c (of four)
+ *     at 16 (r % 32) + 4 (r / 32) + c of them; lds = 2 ceil(K / 256).  Bytes of
+ *     rows and blocks that do not exist are 127.
+ * codes and scales must be 16-byte aligned, and so the other buffers of the
+ * products and FFNs; X, W and Y of rm_fp4_quantize, rm_fp4_quantize_weight and
+ * rm_fp4_dequantize, and the rows of the calls "Rows by expert", only to their
+ * own elements (16-byte aligned rows run faster).
+ *
+ * What is said of the 8-bit calls above about devices, streams, graphs, memory
+ * and the limits of sizes and K holds for these too; their device-side errors
+ * are reported by rm_fp8_sync_status. */
+typedef struct rm_fp4_tensor {
+    void *codes;             /* device */
+    unsigned char *scales;   /* device */
+    long long ld;            /* bytes between rows of codes */
+    long long lds;           /* activations: bytes between rows of scales; weights: see above */
+} rm_fp4_tensor;
+
+/* Rows to 4 bits: X device [rows][ldx] of dtype, cols values of each row. */
+RM_API rm_status rm_fp4_quantize(const void *X, rm_dtype dtype, long long rows, int cols, long long ldx,
+                                 const rm_fp4_tensor *out, void *stream);
+
+/* G weights W device [G][K][N] (contiguous) to 4 bits, blocks along K; G at most 65535. */
+RM_API rm_status rm_fp4_quantize_weight(const void *W, rm_dtype dtype, int G, int K, int N, const rm_fp4_tensor *out,
+                                        void *stream);
+
+/* Rows kept in 4 bits (activations) back: Y device [rows][ldy] of dtype. */
+RM_API rm_status rm_fp4_dequantize(const rm_fp4_tensor *in, long long rows, int cols, void *Y, rm_dtype dtype,
+                                   long long ldy, void *stream);
+
+/* Per-token product of 4-bit operands,
+ *   Y[b][t][n] = sum_k x[b][t][k] W[t][k][n] + bias[t][n].
+ * x: activations [B][T][K]; W: T weights; bias (nullable): device float32
+ * [T][N]; Y: device [B][T][N] of dtype, contiguous.  Products exact, sums in
+ * float32, one rounding to dtype. */
+RM_API rm_status rm_fp4_matmul(const rm_fp4_tensor *x, const rm_fp4_tensor *W, const float *bias, void *Y,
+                               rm_dtype dtype, int B, int T, int K, int N, void *stream);
+
+/* A per-token FFN ("RankMixer" section 3.3.2 Eq. 6-9) with 4-bit weights: W1 T
+ * matrices [D][F], W2 T matrices [F][D], b1 [T][F] and b2 [T][D] float32.  D and
+ * F multiples of 32 (RM_ERR_UNSUPPORTED otherwise). */
+typedef struct rm_fp4_pffn {
+    rm_fp4_tensor W1, W2;
+    const float *b1, *b2;
+    int T, D, F;
+} rm_fp4_pffn;
+
+/* Serving: with Q the 4-bit rounding above,
+ *   V = Q(Gelu(Q(X) W1 + b1)) W2 + b2.
+ * X: device [B][T][D] of x_dtype; V: device [B][T][D] of v_dtype.  work: device,
+ * 16-byte aligned, at least the bytes that rm_fp4_pffn_workspace gives for B. */
+RM_API rm_status rm_fp4_pffn_workspace(const rm_fp4_pffn *p, int B, long long *bytes);
+RM_API rm_status rm_fp4_pffn_forward(const rm_fp4_pffn *p, const void *X, rm_dtype x_dtype, void *V, rm_dtype v_dtype,
+                                     int B, void *work, long long work_bytes, void *stream);
+
+/* ---- Rows by expert ------------------------------------------------------
+ *
+ * Expert e of token t is open for sample b where its gate G[b][t][e] (ReLU
+ * routing, "RankMixer" section 3.4 Eq. 10) is above zero; a gate of NaN is
+ * closed.  The open (t, e, b), in ascending order of t, then e, then b, are the
+ * sorted rows; a row's slot is its place among them.
+ *   offsets  int [T E + 1]: the first slot of group t E + e; the last entry is
+ *            the number of sorted rows
+ *   source   int [B T E]: the row b T + t that a slot comes from (entries behind
+ *            the last slot are left as they were)
+ *   slot     int [B][T][E]: the slot of (b, t, e), -1 where closed
+ *   tiles    int [4 (1 + T E ceil(B / 256))], 16-byte aligned: pieces of at most
+ *            256 rows of one group, for the experts' products
+ * all on the device and the caller's; B T E is below 2^31, T E at most 65535.
+ * The calls below take such a sort, read only, and sorted rows [n][D] of a
+ * caller who has room for n of them: slots from n on are treated as closed, and
+ * rows behind the last slot are left as they were.  n = 0 is allowed.  Results
+ * do not depend on the order in which anything runs. */
+typedef struct rm_expert_rows {
+    int *offsets, *source, *slot, *tiles;
+    int B, T, E;
+} rm_expert_rows;
+
+/* Sort G device float32 [B][T][E].  work: device, 16-byte aligned. */
+RM_API rm_status rm_expert_sort_workspace(int B, int T, int E, long long *bytes);
+RM_API rm_status rm_expert_sort(const float *G, const rm_expert_rows *rows, void *work, long long work_bytes,
+                                void *stream);
+
+/* Xs[slot] = X[b][t]: X device [B][T][D], Xs device [n][D], both of dtype; or the
+ * rows rounded to 4 bits as rm_fp4_quantize does, in the same pass. */
+RM_API rm_status rm_expert_gather(const void *X, rm_dtype dtype, const rm_expert_rows *rows, void *Xs, long long n, int D,
+                                  void *stream);
+RM_API rm_status rm_fp4_expert_gather(const void *X, rm_dtype dtype, const rm_expert_rows *rows, const rm_fp4_tensor *out,
+                                      long long n, int D, void *stream);
+
+/* V[b][t] = sum over the open e of G[b][t][e] Y[slot of (b, t, e)], in float32 and
+ * ascending e; zero where no expert is open.  Y: device [n][D] of y_dtype, V:
+ * device [B][T][D] of v_dtype (float32, or bf16 where Y is).  G NULL: without
+ * gates, which is the gradient of rm_expert_gather (Y: the gradient at Xs). */
+RM_API rm_status rm_expert_combine(const void *Y, rm_dtype y_dtype, const rm_expert_rows *rows, const float *G, void *V,
+                                   rm_dtype v_dtype, long long n, int D, void *stream);
+
+/* Gradients of rm_expert_combine for the gradient dV at V:
+ *   dY[slot] = G[b][t][e] dV[b][t],  dG[b][t][e] = Y[slot] . dV[b][t]
+ * (0 where closed).  dV [B][T][D], Y and dY [n][D]: device, all of dtype; G and
+ * dG: device float32 [B][T][E]. */
+RM_API rm_status rm_expert_combine_backward(const void *dV, const void *Y, rm_dtype dtype, const rm_expert_rows *rows,
+                                            const float *G, void *dY, float *dG, long long n, int D, void *stream);
+
+/* The experts' products of sorted rows in 4 bits: for the rows r of group g,
+ *   Y[r][n] = sum_k x[r][k] W[g][k][n] + bias[g][n].
+ * x: activations [n][K]; W: T E weights; bias (nullable): device float32
+ * [T E][N]; Y: device [n][N] of dtype. */
+RM_API rm_status rm_fp4_expert_matmul(const rm_fp4_tensor *x, const rm_fp4_tensor *W, const rm_expert_rows *rows,
+                                      const float *bias, void *Y, rm_dtype dtype, long long n, int K, int N,
+                                      void *stream);
+
+/* A Sparse-MoE per-token FFN ("RankMixer" section 3.4 Eq. 10) with 4-bit
+ * experts: W1 T E matrices [D][F], W2 T E matrices [F][D], b1 [T E][F] and
+ * b2 [T E][D] float32; D and F multiples of 32. */
+typedef struct rm_fp4_moe {
+    rm_fp4_tensor W1, W2;
+    const float *b1, *b2;
+    int T, E, D, F;
+} rm_fp4_moe;
+
+/* Serving: V[b][t] = sum over the open e of G[b][t][e] FFN_{t,e}(X[b][t]), each
+ * expert as in rm_fp4_pffn_forward; an expert's output is rounded to bf16 before
+ * its gate is applied.  X: device [B][T][D] of x_dtype; G: device float32
+ * [B][T][E]; V: device [B][T][D] of v_dtype. */
+RM_API rm_status rm_fp4_moe_workspace(const rm_fp4_moe *p, int B, long long *bytes);
+RM_API rm_status rm_fp4_moe_forward(const rm_fp4_moe *p, const void *X, rm_dtype x_dtype, const float *G, void *V,
+                                    rm_dtype v_dtype, int B, void *work, long long work_bytes, void *stream);
+
 /* Synchronise `stream`, then report and clear the context's device error
  * word: RM_OK, RM_ERR_TIMEOUT or RM_ERR_DEVICE (or RM_ERR_CUDA if the
  * synchronisation itself failed). */

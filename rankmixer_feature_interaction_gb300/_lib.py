@@ -58,7 +58,10 @@ EXPORTED = ["rm_create", "rm_destroy", "rm_block_forward", "rm_stack_forward", "
             "rm_debug_fail_alloc", "rm_debug_alloc_stats", "rm_stack_forward_host_async", "rm_host_wait",
             "rm_fp8_quantize", "rm_fp8_quantize_weight", "rm_fp8_dequantize", "rm_fp8_matmul", "rm_fp8_wgrad",
             "rm_fp8_pffn_workspace", "rm_fp8_pffn_forward", "rm_fp8_pffn_backward", "rm_fp8_sync_status",
-            "rm_debug_fp8_wait_timeout"]
+            "rm_debug_fp8_wait_timeout", "rm_fp4_quantize", "rm_fp4_quantize_weight", "rm_fp4_dequantize",
+            "rm_fp4_matmul", "rm_fp4_pffn_workspace", "rm_fp4_pffn_forward", "rm_expert_sort_workspace",
+            "rm_expert_sort", "rm_expert_gather", "rm_fp4_expert_gather", "rm_expert_combine",
+            "rm_expert_combine_backward", "rm_fp4_expert_matmul", "rm_fp4_moe_workspace", "rm_fp4_moe_forward"]
 
 
 class rm_config(ctypes.Structure):
@@ -110,6 +113,26 @@ class rm_fp8_grads(ctypes.Structure):
                 ("db2", ctypes.c_void_p), ("dtype", ctypes.c_int)]
 
 
+class rm_fp4_tensor(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("ld", ctypes.c_longlong),
+                ("lds", ctypes.c_longlong)]
+
+
+class rm_fp4_pffn(ctypes.Structure):
+    _fields_ = [("W1", rm_fp4_tensor), ("W2", rm_fp4_tensor), ("b1", ctypes.c_void_p), ("b2", ctypes.c_void_p),
+                ("T", ctypes.c_int), ("D", ctypes.c_int), ("F", ctypes.c_int)]
+
+
+class rm_expert_rows(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("source", ctypes.c_void_p), ("slot", ctypes.c_void_p),
+                ("tiles", ctypes.c_void_p), ("B", ctypes.c_int), ("T", ctypes.c_int), ("E", ctypes.c_int)]
+
+
+class rm_fp4_moe(ctypes.Structure):
+    _fields_ = [("W1", rm_fp4_tensor), ("W2", rm_fp4_tensor), ("b1", ctypes.c_void_p), ("b2", ctypes.c_void_p),
+                ("T", ctypes.c_int), ("E", ctypes.c_int), ("D", ctypes.c_int), ("F", ctypes.c_int)]
+
+
 class RankMixerError(RuntimeError):
     def __init__(self, status: int, where: str, msg: str):
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}: {msg}")
@@ -131,6 +154,7 @@ def load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     vp, i, st = ctypes.c_void_p, ctypes.c_int, ctypes.c_int
     ll, t8 = ctypes.c_longlong, ctypes.POINTER(rm_fp8_tensor)
+    t4, ffn4, moe4, exp = (ctypes.POINTER(c) for c in (rm_fp4_tensor, rm_fp4_pffn, rm_fp4_moe, rm_expert_rows))
     ffn8, kept8 = ctypes.POINTER(rm_fp8_pffn), ctypes.POINTER(rm_fp8_kept)
     sig = {
         "rm_create": (st, [ctypes.POINTER(rm_config), ctypes.POINTER(rm_layer_params), i, ctypes.POINTER(vp)]),
@@ -178,6 +202,21 @@ def load() -> ctypes.CDLL:
         "rm_fp8_pffn_backward": (st, [ffn8, vp, i, kept8, vp, i, ctypes.POINTER(rm_fp8_grads), i, vp, ll, vp]),
         "rm_fp8_sync_status": (st, [vp]),
         "rm_debug_fp8_wait_timeout": (st, [i, vp]),
+        "rm_fp4_quantize": (st, [vp, i, ll, i, ll, t4, vp]),
+        "rm_fp4_quantize_weight": (st, [vp, i, i, i, i, t4, vp]),
+        "rm_fp4_dequantize": (st, [t4, ll, i, vp, i, ll, vp]),
+        "rm_fp4_matmul": (st, [t4, t4, vp, vp, i, i, i, i, i, vp]),
+        "rm_fp4_pffn_workspace": (st, [ffn4, i, ctypes.POINTER(ll)]),
+        "rm_fp4_pffn_forward": (st, [ffn4, vp, i, vp, i, i, vp, ll, vp]),
+        "rm_expert_sort_workspace": (st, [i, i, i, ctypes.POINTER(ll)]),
+        "rm_expert_sort": (st, [vp, exp, vp, ll, vp]),
+        "rm_expert_gather": (st, [vp, i, exp, vp, ll, i, vp]),
+        "rm_fp4_expert_gather": (st, [vp, i, exp, t4, ll, i, vp]),
+        "rm_expert_combine": (st, [vp, i, exp, vp, vp, i, ll, i, vp]),
+        "rm_expert_combine_backward": (st, [vp, vp, i, exp, vp, vp, vp, ll, i, vp]),
+        "rm_fp4_expert_matmul": (st, [t4, t4, exp, vp, vp, i, ll, i, i, vp]),
+        "rm_fp4_moe_workspace": (st, [moe4, i, ctypes.POINTER(ll)]),
+        "rm_fp4_moe_forward": (st, [moe4, vp, i, vp, vp, i, i, vp, ll, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -430,6 +469,127 @@ def rm_fp8_sync_status(stream: int) -> int:
 
 def rm_debug_fp8_wait_timeout(timeout_us: int, stream: int) -> None:
     check(load().rm_debug_fp8_wait_timeout(timeout_us, stream), "rm_debug_fp8_wait_timeout")
+
+
+def rm_fp4_quantize(X: int, dtype: int, rows: int, cols: int, ldx: int, out: rm_fp4_tensor, stream: int) -> None:
+    if cols >> 31:
+        too_long("rm_fp4_quantize", cols)
+    st = (_lib or load()).rm_fp4_quantize(X, dtype, rows, cols, ldx, out, stream)
+    if st:
+        check(st, "rm_fp4_quantize")
+
+
+def rm_fp4_quantize_weight(W: int, dtype: int, G: int, K: int, N: int, out: rm_fp4_tensor, stream: int) -> None:
+    if (G | K | N) >> 31:
+        too_long("rm_fp4_quantize_weight", G, K, N)
+    st = (_lib or load()).rm_fp4_quantize_weight(W, dtype, G, K, N, out, stream)
+    if st:
+        check(st, "rm_fp4_quantize_weight")
+
+
+def rm_fp4_dequantize(q: rm_fp4_tensor, rows: int, cols: int, Y: int, dtype: int, ldy: int, stream: int) -> None:
+    if cols >> 31:
+        too_long("rm_fp4_dequantize", cols)
+    st = (_lib or load()).rm_fp4_dequantize(q, rows, cols, Y, dtype, ldy, stream)
+    if st:
+        check(st, "rm_fp4_dequantize")
+
+
+def rm_fp4_matmul(x: rm_fp4_tensor, W: rm_fp4_tensor, bias: int | None, Y: int, dtype: int, B: int, T: int, K: int,
+                  N: int, stream: int) -> None:
+    if (B | T | K | N) >> 31:
+        too_long("rm_fp4_matmul", B, T, K, N)
+    st = (_lib or load()).rm_fp4_matmul(x, W, bias, Y, dtype, B, T, K, N, stream)
+    if st:
+        check(st, "rm_fp4_matmul")
+
+
+def rm_fp4_pffn_workspace(p: rm_fp4_pffn, B: int) -> int:
+    if B >> 31:
+        too_long("rm_fp4_pffn_workspace", B)
+    n = ctypes.c_longlong()
+    check((_lib or load()).rm_fp4_pffn_workspace(p, B, ctypes.byref(n)), "rm_fp4_pffn_workspace")
+    return n.value
+
+
+def rm_fp4_pffn_forward(p: rm_fp4_pffn, X: int, x_dtype: int, V: int, v_dtype: int, B: int, work: int | None,
+                        work_bytes: int, stream: int) -> None:
+    st = (_lib or load()).rm_fp4_pffn_forward(p, X, x_dtype, V, v_dtype, B, work, work_bytes, stream)
+    if st:
+        check(st, "rm_fp4_pffn_forward")
+
+
+def rm_expert_sort_workspace(B: int, T: int, E: int) -> int:
+    if (B | T | E) >> 31:
+        too_long("rm_expert_sort_workspace", B, T, E)
+    n = ctypes.c_longlong()
+    check((_lib or load()).rm_expert_sort_workspace(B, T, E, ctypes.byref(n)), "rm_expert_sort_workspace")
+    return n.value
+
+
+def rm_expert_sort(G: int, rows: rm_expert_rows, work: int | None, work_bytes: int, stream: int) -> None:
+    st = (_lib or load()).rm_expert_sort(G, rows, work, work_bytes, stream)
+    if st:
+        check(st, "rm_expert_sort")
+
+
+def rm_expert_gather(X: int, dtype: int, rows: rm_expert_rows, Xs: int | None, n: int, D: int, stream: int) -> None:
+    if D >> 31:
+        too_long("rm_expert_gather", D)
+    st = (_lib or load()).rm_expert_gather(X, dtype, rows, Xs, n, D, stream)
+    if st:
+        check(st, "rm_expert_gather")
+
+
+def rm_fp4_expert_gather(X: int, dtype: int, rows: rm_expert_rows, out: rm_fp4_tensor, n: int, D: int,
+                         stream: int) -> None:
+    if D >> 31:
+        too_long("rm_fp4_expert_gather", D)
+    st = (_lib or load()).rm_fp4_expert_gather(X, dtype, rows, out, n, D, stream)
+    if st:
+        check(st, "rm_fp4_expert_gather")
+
+
+def rm_expert_combine(Y: int | None, y_dtype: int, rows: rm_expert_rows, G: int | None, V: int, v_dtype: int, n: int,
+                      D: int, stream: int) -> None:
+    if D >> 31:
+        too_long("rm_expert_combine", D)
+    st = (_lib or load()).rm_expert_combine(Y, y_dtype, rows, G, V, v_dtype, n, D, stream)
+    if st:
+        check(st, "rm_expert_combine")
+
+
+def rm_expert_combine_backward(dV: int, Y: int | None, dtype: int, rows: rm_expert_rows, G: int, dY: int | None,
+                               dG: int, n: int, D: int, stream: int) -> None:
+    if D >> 31:
+        too_long("rm_expert_combine_backward", D)
+    st = (_lib or load()).rm_expert_combine_backward(dV, Y, dtype, rows, G, dY, dG, n, D, stream)
+    if st:
+        check(st, "rm_expert_combine_backward")
+
+
+def rm_fp4_expert_matmul(x: rm_fp4_tensor, W: rm_fp4_tensor, rows: rm_expert_rows, bias: int | None, Y: int | None,
+                         dtype: int, n: int, K: int, N: int, stream: int) -> None:
+    if (K | N) >> 31:
+        too_long("rm_fp4_expert_matmul", K, N)
+    st = (_lib or load()).rm_fp4_expert_matmul(x, W, rows, bias, Y, dtype, n, K, N, stream)
+    if st:
+        check(st, "rm_fp4_expert_matmul")
+
+
+def rm_fp4_moe_workspace(p: rm_fp4_moe, B: int) -> int:
+    if B >> 31:
+        too_long("rm_fp4_moe_workspace", B)
+    n = ctypes.c_longlong()
+    check((_lib or load()).rm_fp4_moe_workspace(p, B, ctypes.byref(n)), "rm_fp4_moe_workspace")
+    return n.value
+
+
+def rm_fp4_moe_forward(p: rm_fp4_moe, X: int, x_dtype: int, G: int, V: int, v_dtype: int, B: int, work: int | None,
+                       work_bytes: int, stream: int) -> None:
+    st = (_lib or load()).rm_fp4_moe_forward(p, X, x_dtype, G, V, v_dtype, B, work, work_bytes, stream)
+    if st:
+        check(st, "rm_fp4_moe_forward")
 
 
 def rm_debug_gelu_grad(u: int, out: int, n: int, stream: int) -> None:

@@ -628,3 +628,396 @@ def fp8_sync_status() -> int:
     """Synchronise the current stream and report the 8-bit operators' device status (RM_OK, RM_ERR_TIMEOUT, ...).
     Every stream is told once of an error, whichever stream's call it came from."""
     return _lib.rm_fp8_sync_status(_stream())
+
+
+# -- 4-bit operands -------------------------------------------------------------------
+class Fp4Tensor:
+    """Values in microscaled 4-bit floating point: codes (uint8, two a byte: e2m1, the value of even
+    index in the low four bits) and one exponent byte E per 32 consecutive values, scales (uint8); a
+    value is code * 2^(E - 127).
+    Activations (weight False): codes [.., ld], scales [.., lds], `cols` values a row; ld and lds are
+    multiples of 16, codes past `cols` up to the end of the last 32 are zero.
+    Weights [.., K, N] (weight True) are kept along K, cols = K: codes [.., N, ld] and scales
+    [.., ceil(N / 128), 2 ceil(K / 256), 512], in the tensor cores' order: of rows 128 i .. + 127 and
+    values 128 j .. + 127, row r's block c at [.., i, j, 16 (r % 32) + 4 (r / 32) + c]; 127 where there
+    is no row or block."""
+    __slots__ = ("cols", "weight", "c", "cs", "ss", "device", "device_index", "_codes", "_scales", "_arena")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, weight: bool = False):
+        cs, ss, d, nb = codes.shape, scales.shape, codes.get_device(), (cols + 31) // 32
+        if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
+            raise ValueError("codes and scales must be uint8")
+        if d != scales.get_device():
+            raise ValueError("codes and scales must be on the same device")
+        if weight:
+            fits = len(cs) >= 2 and tuple(ss) == (*cs[:-2], (cs[-2] + 127) // 128, 2 * ((cols + 255) // 256), 512)
+        else:
+            fits = len(cs) >= 1 and ss[:-1] == cs[:-1] and ss[-1] >= nb
+        if not fits or cols < 1 or 16 * nb > cs[-1]:
+            raise ValueError(f"codes {tuple(cs)} and scales {tuple(ss)} do not hold {cols} columns")
+        if not (codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError("tensors passed to librankmixer must be contiguous")
+        self.c = _lib.rm_fp4_tensor(codes.data_ptr(), scales.data_ptr(), cs[-1], ss[-2] if weight else ss[-1])
+        self.cols, self.weight, self.cs, self.ss, self.device, self.device_index = cols, weight, cs, ss, codes.device, d
+        self._codes, self._scales, self._arena = codes, scales, None
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            at = self.c.codes - self._arena.data_ptr()
+            self._codes = self._arena[at:at + math.prod(self.cs)].view(self.cs)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            at = self.c.scales - self._arena.data_ptr()
+            self._scales = self._arena[at:at + math.prod(self.ss)].view(self.ss)
+        return self._scales
+
+    @property
+    def shape(self) -> tuple:
+        """Of the values: [.., cols], of a weight [.., K, N]."""
+        return (*self.cs[:-2], self.cols, self.cs[-2]) if self.weight else (*self.cs[:-1], self.cols)
+
+    @property
+    def nbytes(self) -> int:
+        return math.prod(self.cs) + math.prod(self.ss)
+
+
+def _fp4_new(lead: tuple, cols: int, weight: bool, device: torch.device, index: int) -> Fp4Tensor:
+    """An uninitialised 4-bit tensor of rows [*lead, cols], in one allocation."""
+    nb = (cols + 31) // 32
+    q = object.__new__(Fp4Tensor)
+    q.cs = (*lead, 16 * nb)
+    q.ss = (*lead[:-1], (lead[-1] + 127) // 128, 2 * ((cols + 255) // 256), 512) if weight else (*lead, (nb + 15) // 16 * 16)
+    at = (math.prod(q.cs) + 255) // 256 * 256
+    q._arena = torch.empty(at + math.prod(q.ss), dtype=torch.uint8, device=device)
+    base = q._arena.data_ptr()
+    q.c = _lib.rm_fp4_tensor(base, base + at, 16 * nb, q.ss[-2] if weight else q.ss[-1])
+    q.cols, q.weight, q.device, q.device_index, q._codes, q._scales = cols, weight, device, index, None, None
+    return q
+
+
+def _fp4_activation(x: Fp4Tensor, dims: int, what: str) -> tuple:
+    if x.weight or len(x.cs) != dims:
+        raise ValueError(f"{what} must be 4-bit activations of {dims} dimensions, got {x.shape} (weight={x.weight})")
+    return x.shape
+
+
+def _fp4_weight(w: Fp4Tensor, dims: int, what: str) -> tuple:
+    if not w.weight or len(w.cs) != dims:
+        raise ValueError(f"{what} must be a 4-bit weight of {dims} dimensions, got {w.shape} (weight={w.weight})")
+    return w.shape
+
+
+def _bias(bias: torch.Tensor | None, shape: tuple) -> int | None:
+    if bias is None:
+        return None
+    if bias.dtype != torch.float32 or bias.shape != shape:
+        raise ValueError(f"bias must be float32 {list(shape)}")
+    return _ptr(bias)
+
+
+def fp4_quantize(X: torch.Tensor) -> Fp4Tensor:
+    """X [.., C] (bf16 or float32, rows one stride apart) in 4 bits, one scale per 32 values of a
+    row: an operand of fp4_matmul, and a copy that fp4_dequantize reads back."""
+    d = _fp8_device(X.get_device())
+    dtype, shape = _CODE.get(X.dtype), X.shape
+    if dtype is None:
+        raise ValueError(f"X must be bfloat16 or float32, got {X.dtype}")
+    if len(shape) < 1:
+        raise ValueError("X must have at least one dimension")
+    lead, C = tuple(shape[:-1]), shape[-1]
+    rows = math.prod(lead)
+    if rows < 1 or C < 1:
+        raise _lib.RankMixerError(_lib.RM_ERR_INVALID_ARG, "fp4_quantize", f"empty tensor {tuple(shape)}")
+    ldx = C
+    if not X.is_contiguous():
+        if X.stride(-1) != 1 and C > 1:
+            raise ValueError("the last dimension of X must be contiguous")
+        ldx = X.view(rows, C).stride(0) if rows > 1 else C            # raises when rows are not one stride apart
+    out = _fp4_new(lead, C, False, X.device, d)
+    _lib.rm_fp4_quantize(X.data_ptr(), dtype, rows, C, ldx, out.c, _raw_stream(d))
+    return out
+
+
+def fp4_quantize_weight(W: torch.Tensor) -> Fp4Tensor:
+    """W [.., K, N] (bf16 or float32) in 4 bits, one scale per 32 values along K."""
+    d = _fp8_device(W.get_device())
+    if W.dtype not in _CODE or W.dim() < 2:
+        raise ValueError(f"W must be a bfloat16 or float32 [.., K, N], got {W.dtype} {tuple(W.shape)}")
+    *lead, K, N = W.shape
+    G = math.prod(lead)
+    if G < 1 or K < 1 or N < 1:
+        raise _lib.RankMixerError(_lib.RM_ERR_INVALID_ARG, "fp4_quantize_weight", f"empty tensor {tuple(W.shape)}")
+    out = _fp4_new((*lead, N), K, True, W.device, d)
+    _lib.rm_fp4_quantize_weight(_ptr(W), _CODE[W.dtype], G, K, N, out.c, _raw_stream(d))
+    return out
+
+
+def fp4_dequantize(q: Fp4Tensor, dtype: str = "bf16") -> torch.Tensor:
+    """The values of 4-bit rows [.., C] (activations) in bf16 or float32."""
+    d = _fp8_device(q.device_index)
+    if q.weight:
+        raise ValueError("fp4_dequantize takes activations")
+    tdt, code = _DTYPES[dtype]
+    Y = torch.empty(q.shape, dtype=tdt, device=q.device)
+    _lib.rm_fp4_dequantize(q.c, math.prod(q.cs[:-1]), q.cols, Y.data_ptr(), code, q.cols, _raw_stream(d))
+    return Y
+
+
+def fp4_matmul(x: Fp4Tensor, w: Fp4Tensor, bias: torch.Tensor | None = None, out_dtype: str = "bf16") -> torch.Tensor:
+    """Y[b, t, :] = x[b, t, :] w[t] (+ bias[t]): x [B, T, K] and w [T, K, N] in 4 bits, bias float32 [T, N]."""
+    B, T, K = _fp4_activation(x, 3, "x")
+    Tw, Kw, N = _fp4_weight(w, 3, "w")
+    if Tw != T or Kw != K:
+        raise ValueError(f"x {x.shape} and w {w.shape} do not fit")
+    d = _fp8_device(x.device_index, w.device_index, *(() if bias is None else (bias.get_device(),)))
+    tdt, code = _DTYPES[out_dtype]
+    b = _bias(bias, (T, N))
+    Y = torch.empty((B, T, N), dtype=tdt, device=x.device)
+    _lib.rm_fp4_matmul(x.c, w.c, b, Y.data_ptr(), code, B, T, K, N, _raw_stream(d))
+    return Y
+
+
+class _Fp4FFN:
+    """What Fp4PFFN and Fp4MoE share: 4-bit weights [*lead, D, F] and [*lead, F, D], float32 biases."""
+
+    def __init__(self, W1, b1: torch.Tensor, W2, b2: torch.Tensor, dims: int):
+        self.W1 = W1 if isinstance(W1, Fp4Tensor) else fp4_quantize_weight(W1)
+        self.W2 = W2 if isinstance(W2, Fp4Tensor) else fp4_quantize_weight(W2)
+        *lead, D, F = _fp4_weight(self.W1, dims, "W1")
+        if _fp4_weight(self.W2, dims, "W2") != (*lead, F, D):
+            raise ValueError(f"W1 {self.W1.shape} and W2 {self.W2.shape} do not fit")
+        _lib.too_long(type(self).__name__, *lead, D, F)
+        self.lead, self.D, self.F = tuple(lead), D, F
+        self.b1, self.b2 = b1.to(torch.float32).contiguous(), b2.to(torch.float32).contiguous()
+        if tuple(self.b1.shape) != (*lead, F) or tuple(self.b2.shape) != (*lead, D):
+            raise ValueError(f"b1 must be {[*lead, F]} and b2 {[*lead, D]}")
+        self.device_index = _fp8_device(self.W1.device_index, self.W2.device_index, self.b1.get_device(),
+                                        self.b2.get_device())
+        self._bytes = {}
+
+    def _rows(self, X: torch.Tensor) -> int:
+        _fp8_device(X.get_device(), self.device_index)
+        if X.dtype not in _CODE or X.dim() != 3 or X.shape[1:] != (self.lead[0], self.D):
+            raise ValueError(f"X must be a bfloat16 or float32 [B, {self.lead[0]}, {self.D}], got {X.dtype} "
+                             f"{tuple(X.shape)}")
+        return X.shape[0]
+
+    def _work(self, B: int, device, ask) -> tuple[torch.Tensor, int]:
+        """This call's workspace (its size is looked up once per batch size)."""
+        n = self._bytes.get(B)
+        if n is None:
+            n = self._bytes[B] = ask(self.c, B)
+        return torch.empty(n, dtype=torch.uint8, device=device), n
+
+
+class Fp4PFFN(_Fp4FFN):
+    """The per-token FFN on 4-bit operands, for serving: V = Gelu(X W1 + b1) W2 + b2 for every token,
+    with X and the hidden activation rounded to 4 bits before their products.
+
+    W1 [T, D, F] and W2 [T, F, D]: bf16 or float32 tensors (quantised here, once) or Fp4Tensor;
+    b1 [T, F], b2 [T, D]; D and F multiples of 32."""
+
+    def __init__(self, W1, b1: torch.Tensor, W2, b2: torch.Tensor):
+        super().__init__(W1, b1, W2, b2, 3)
+        self.T, = self.lead
+        self.c = _lib.rm_fp4_pffn(self.W1.c, self.W2.c, _ptr(self.b1), _ptr(self.b2), self.T, self.D, self.F)
+
+    def forward(self, X: torch.Tensor, out_dtype: str = "bf16") -> torch.Tensor:
+        """V [B, T, D] of X [B, T, D]."""
+        B = self._rows(X)
+        tdt, code = _DTYPES[out_dtype]
+        work, n = self._work(B, X.device, _lib.rm_fp4_pffn_workspace)
+        V = torch.empty(X.shape, dtype=tdt, device=X.device)
+        _lib.rm_fp4_pffn_forward(self.c, _ptr(X), _CODE[X.dtype], V.data_ptr(), code, B, work.data_ptr(), n,
+                                 _raw_stream(self.device_index))
+        return V
+
+
+# -- rows by expert -------------------------------------------------------------------
+class ExpertRows:
+    """The rows of a batch sorted by expert (expert_sort): offsets [T E + 1] (first slot of group
+    t E + e; the last entry is the number of sorted rows), slot [B, T, E] (-1 where the expert is
+    closed) and source [B T E] (the row b T + t that a slot comes from; the first offsets[-1] count),
+    int32 tensors on the device."""
+    __slots__ = ("B", "T", "E", "c", "device", "device_index", "_arena", "_at")
+
+    def __init__(self, B: int, T: int, E: int, device: torch.device, index: int):
+        self.B, self.T, self.E, self.device, self.device_index = B, T, E, device, index
+        self._at, size = _expert_layout(B, T, E)
+        self._arena = torch.empty(size, dtype=torch.int32, device=device)
+        base = self._arena.data_ptr()
+        self.c = _lib.rm_expert_rows(*(base + 4 * at for at in self._at), B, T, E)
+
+    @property
+    def offsets(self) -> torch.Tensor:
+        return self._arena[self._at[0]:self._at[0] + self.T * self.E + 1]
+
+    @property
+    def source(self) -> torch.Tensor:
+        return self._arena[self._at[1]:self._at[1] + self.B * self.T * self.E]
+
+    @property
+    def slot(self) -> torch.Tensor:
+        return self._arena[self._at[2]:self._at[2] + self.B * self.T * self.E].view(self.B, self.T, self.E)
+
+    def count(self) -> int:
+        """The number of sorted rows (waits for the sort)."""
+        return int(self.offsets[-1])
+
+
+@functools.lru_cache(maxsize=256)
+def _expert_layout(B: int, T: int, E: int) -> tuple:
+    """Where offsets, source, slot and tiles lie in one allocation of int32, and its length."""
+    at, places = 0, []
+    for n in (T * E + 1, B * T * E, B * T * E, 4 * (1 + T * E * ((B + 255) // 256))):
+        places.append(at)
+        at += (n + 63) // 64 * 64
+    return tuple(places), at
+
+
+@functools.lru_cache(maxsize=256)
+def _expert_sort_bytes(B: int, T: int, E: int) -> int:
+    return _lib.rm_expert_sort_workspace(B, T, E)
+
+
+def expert_sort(G: torch.Tensor) -> ExpertRows:
+    """The open (t, e, b) of the gates G [B, T, E] (float32; open: above zero), sorted in that order."""
+    d = _fp8_device(G.get_device())
+    if G.dtype != torch.float32 or G.dim() != 3:
+        raise ValueError(f"G must be a float32 [B, T, E], got {G.dtype} {tuple(G.shape)}")
+    B, T, E = G.shape
+    n = _expert_sort_bytes(B, T, E)
+    rows = ExpertRows(B, T, E, G.device, d)
+    work = torch.empty(n, dtype=torch.uint8, device=G.device)
+    _lib.rm_expert_sort(_ptr(G), rows.c, work.data_ptr(), n, _raw_stream(d))
+    return rows
+
+
+def _batch_rows(X: torch.Tensor, rows: ExpertRows, what: str) -> int:
+    if X.dtype not in _CODE or X.dim() != 3 or X.shape[0] != rows.B or X.shape[1] != rows.T:
+        raise ValueError(f"{what} must be a bfloat16 or float32 [{rows.B}, {rows.T}, D], got {X.dtype} {tuple(X.shape)}")
+    return X.shape[2]
+
+
+def _gates(G: torch.Tensor, rows: ExpertRows) -> int:
+    if G.dtype != torch.float32 or G.shape != (rows.B, rows.T, rows.E):
+        raise ValueError(f"G must be float32 [{rows.B}, {rows.T}, {rows.E}], got {G.dtype} {tuple(G.shape)}")
+    return _ptr(G)
+
+
+def _room(rows: ExpertRows, n: int | None) -> int:
+    if n is not None and n < 0:
+        raise ValueError(f"n must not be negative, got {n}")
+    return rows.B * rows.T * rows.E if n is None else n
+
+
+def expert_gather(X: torch.Tensor, rows: ExpertRows, n: int | None = None) -> torch.Tensor:
+    """Xs [n, D]: the rows of X [B, T, D] (bf16 or float32), each copied to its slots.  n: room for
+    that many rows (default: for all that there can be); slots from n on are left out, rows behind
+    the last slot uninitialised."""
+    d = _fp8_device(X.get_device(), rows.device_index)
+    D, n = _batch_rows(X, rows, "X"), _room(rows, n)
+    Xs = torch.empty((n, D), dtype=X.dtype, device=X.device)
+    _lib.rm_expert_gather(_ptr(X), _CODE[X.dtype], rows.c, Xs.data_ptr(), n, D, _raw_stream(d))
+    return Xs
+
+
+def fp4_expert_gather(X: torch.Tensor, rows: ExpertRows, n: int | None = None) -> Fp4Tensor:
+    """expert_gather and fp4_quantize in one pass: [n, D] in 4 bits."""
+    d = _fp8_device(X.get_device(), rows.device_index)
+    D, n = _batch_rows(X, rows, "X"), _room(rows, n)
+    out = _fp4_new((n,), D, False, X.device, d)
+    _lib.rm_fp4_expert_gather(_ptr(X), _CODE[X.dtype], rows.c, out.c, n, D, _raw_stream(d))
+    return out
+
+
+def _sorted_rows(Y: torch.Tensor, what: str) -> tuple:
+    if Y.dtype not in _CODE or Y.dim() != 2:
+        raise ValueError(f"{what} must be a bfloat16 or float32 [n, D], got {Y.dtype} {tuple(Y.shape)}")
+    return Y.shape
+
+
+def expert_gather_backward(dXs: torch.Tensor, rows: ExpertRows) -> torch.Tensor:
+    """dX [B, T, D] for the gradient dXs [n, D] at expert_gather's rows: their sum over a row's slots."""
+    return _combine(dXs, rows, None, "dXs", None)
+
+
+def expert_combine(Y: torch.Tensor, rows: ExpertRows, G: torch.Tensor, out_dtype: str | None = None) -> torch.Tensor:
+    """V [B, T, D]: V[b, t] = sum over the open experts e of G[b, t, e] Y[slot of (b, t, e)] (float32
+    sums, ascending e; zero where none is open).  Y [n, D]; V in Y's type, or float32 (out_dtype "f32")."""
+    return _combine(Y, rows, G, "Y", out_dtype)
+
+
+def _combine(Y: torch.Tensor, rows: ExpertRows, G: torch.Tensor | None, what: str, out_dtype: str | None) -> torch.Tensor:
+    n, D = _sorted_rows(Y, what)
+    d = _fp8_device(Y.get_device(), rows.device_index, *(() if G is None else (G.get_device(),)))
+    tdt, code = _DTYPES[out_dtype] if out_dtype is not None else (Y.dtype, _CODE[Y.dtype])
+    g = None if G is None else _gates(G, rows)
+    V = torch.empty((rows.B, rows.T, D), dtype=tdt, device=Y.device)
+    _lib.rm_expert_combine(_ptr(Y), _CODE[Y.dtype], rows.c, g, V.data_ptr(), code, n, D, _raw_stream(d))
+    return V
+
+
+def expert_combine_backward(dV: torch.Tensor, Y: torch.Tensor, rows: ExpertRows,
+                            G: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """(dY [n, D], dG [B, T, E] float32) of expert_combine(Y, rows, G) for the gradient dV [B, T, D]
+    (of Y's type) at V; dG is zero where an expert is closed, rows of dY behind the last slot
+    uninitialised."""
+    d = _fp8_device(dV.get_device(), Y.get_device(), rows.device_index, G.get_device())
+    n, D = _sorted_rows(Y, "Y")
+    if _batch_rows(dV, rows, "dV") != D or dV.dtype != Y.dtype:
+        raise ValueError(f"dV {dV.dtype} {tuple(dV.shape)} and Y {Y.dtype} {tuple(Y.shape)} do not fit")
+    g = _gates(G, rows)
+    dY = torch.empty((n, D), dtype=Y.dtype, device=Y.device)
+    dG = torch.empty((rows.B, rows.T, rows.E), dtype=torch.float32, device=Y.device)
+    _lib.rm_expert_combine_backward(_ptr(dV), _ptr(Y), _CODE[Y.dtype], rows.c, g, dY.data_ptr(), dG.data_ptr(), n, D,
+                                    _raw_stream(d))
+    return dY, dG
+
+
+def fp4_expert_matmul(x: Fp4Tensor, w: Fp4Tensor, rows: ExpertRows, bias: torch.Tensor | None = None,
+                      out_dtype: str = "bf16") -> torch.Tensor:
+    """Y [n, N] of the sorted rows x [n, K] in 4 bits: those of group (t, e) times w[t, e] [K, N]
+    (+ bias[t, e], float32 [T, E, N]); rows behind the last slot uninitialised."""
+    n, K = _fp4_activation(x, 2, "x")
+    T, E, Kw, N = _fp4_weight(w, 4, "w")
+    if (T, E) != (rows.T, rows.E) or Kw != K:
+        raise ValueError(f"x {x.shape}, w {w.shape} and rows of T = {rows.T}, E = {rows.E} do not fit")
+    d = _fp8_device(x.device_index, w.device_index, rows.device_index,
+                    *(() if bias is None else (bias.get_device(),)))
+    tdt, code = _DTYPES[out_dtype]
+    b = _bias(bias, (T, E, N))
+    Y = torch.empty((n, N), dtype=tdt, device=x.device)
+    _lib.rm_fp4_expert_matmul(x.c, w.c, rows.c, b, Y.data_ptr(), code, n, K, N, _raw_stream(d))
+    return Y
+
+
+class Fp4MoE(_Fp4FFN):
+    """The Sparse-MoE per-token FFN with 4-bit experts, for serving: V[b, t] = sum over the experts
+    with a gate above zero of G[b, t, e] FFN_{t,e}(X[b, t]), each on 4-bit operands as in Fp4PFFN;
+    an expert's output is rounded to bf16 before its gate is applied.
+
+    W1 [T, E, D, F] and W2 [T, E, F, D]: bf16 or float32 tensors (quantised here, once) or
+    Fp4Tensor; b1 [T, E, F], b2 [T, E, D]; D and F multiples of 32."""
+
+    def __init__(self, W1, b1: torch.Tensor, W2, b2: torch.Tensor):
+        super().__init__(W1, b1, W2, b2, 4)
+        self.T, self.E = self.lead
+        self.c = _lib.rm_fp4_moe(self.W1.c, self.W2.c, _ptr(self.b1), _ptr(self.b2), self.T, self.E, self.D, self.F)
+
+    def forward(self, X: torch.Tensor, G: torch.Tensor, out_dtype: str = "bf16") -> torch.Tensor:
+        """V [B, T, D] of X [B, T, D] and the gates G [B, T, E] (float32)."""
+        B = self._rows(X)
+        _fp8_device(G.get_device())
+        if G.dtype != torch.float32 or G.shape != (B, self.T, self.E):
+            raise ValueError(f"G must be float32 [{B}, {self.T}, {self.E}], got {G.dtype} {tuple(G.shape)}")
+        tdt, code = _DTYPES[out_dtype]
+        work, n = self._work(B, X.device, _lib.rm_fp4_moe_workspace)
+        V = torch.empty(X.shape, dtype=tdt, device=X.device)
+        _lib.rm_fp4_moe_forward(self.c, _ptr(X), _CODE[X.dtype], _ptr(G), V.data_ptr(), code, B, work.data_ptr(), n,
+                                _raw_stream(self.device_index))
+        return V

@@ -1,0 +1,501 @@
+// Rows by expert: the open (t, e, b) of a batch's gates in that order, a batch's
+// rows copied there and back, and the gradients of both.
+//
+// Sorting.  Seen as a matrix [B][T E] the gates are sorted by column, so a row's slot
+// is the number of open gates in the columns before its own plus those above it.  A
+// CTA owns eight neighbouring columns (32 bytes of every row, a whole sector), each
+// of its 32 warps a run of rows, four at a time; ranks within a warp come from
+// ballots.  First launch: every warp's counts.  Second: the columns before (their
+// totals are summed anew by every CTA, T E numbers), the warps before, the slots.
+// Up to kSmallSort gates of few rows one CTA does both, without the first launch.  No
+// atomics, so the order is always the same.
+//
+// Rows.  One warp per (b, t): the row is read once and written to (or summed from)
+// the slots of its open experts, in ascending order of e.  Bound by memory.
+#include <initializer_list>
+
+#include "rm_fp4.cuh"
+
+namespace rm {
+namespace {
+
+constexpr int kCols = 8, kSortWarps = 32, kSortThreads = 32 * kSortWarps;
+constexpr int kSmallSort = 16384, kSmallRows = 64;
+bool sorts_at_once(int B, long long TE) { return B <= kSmallRows && B * TE <= kSmallSort; }
+
+__device__ __forceinline__ int col_count(uint32_t ballot, int col) { return __popc(ballot & (0x01010101u << col)); }
+
+// The rows of one warp of kSortWarps.
+__device__ __forceinline__ void warp_rows(int B, int warp, int& b0, int& b1) {
+    const int per = (B + 4 * kSortWarps - 1) / (4 * kSortWarps) * 4;
+    b0 = min((long long)B, (long long)warp * per);
+    b1 = min((long long)B, (long long)b0 + per);
+}
+
+// counts[warp][g]: open gates of column g among the warp's rows; totals[g].
+__global__ void __launch_bounds__(kSortThreads)
+sort_count_kernel(const float* __restrict__ G, int B, int TE, int* __restrict__ counts, int* __restrict__ totals) {
+    constexpr int UNROLL = 8;
+    __shared__ int part[kSortWarps][kCols];
+    pdl_wait();
+    pdl_launch_next();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = lane & 7, g = blockIdx.x * kCols + col;
+    int b0, b1, n = 0;
+    warp_rows(B, warp, b0, b1);
+    for (int b = b0; b < b1; b += 4 * UNROLL) {
+        float x[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int r = b + 4 * u + (lane >> 3);
+            x[u] = r < b1 && g < TE ? __ldg(G + (size_t)r * TE + g) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) n += col_count(__ballot_sync(0xffffffffu, x[u] > 0.f), col);
+    }
+    if (lane < kCols) {
+        part[warp][lane] = n;
+        if (g < TE) counts[(size_t)warp * TE + g] = n;
+    }
+    __syncthreads();
+    if (threadIdx.x < kCols && g < TE) {
+        int t = 0;
+        for (int w = 0; w < kSortWarps; ++w) t += part[w][threadIdx.x];
+        totals[g] = t;
+    }
+}
+
+// Sum over the CTA's threads, and the sum of the threads before this one.
+__device__ __forceinline__ int block_scan(int v, int* shared, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) shared[warp] = x;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+    for (int w = 0; w < warps; ++w) {
+        if (w < warp) before += shared[w];
+        total += shared[w];
+    }
+    return before + x - v;
+}
+
+// offsets and tiles from the totals, by one CTA; total(g) gives a column's count.
+template <typename F>
+__device__ __forceinline__ void write_groups(F total, const ExpertRows& r, int TE, int* shared) {
+    int rows = 0, tiles = 0;
+    for (int g0 = 0; g0 < TE; g0 += blockDim.x) {
+        const int g = g0 + threadIdx.x, n = g < TE ? total(g) : 0;
+        int all, all_tiles;
+        const int at = rows + block_scan(n, shared, all);
+        const int tile = tiles + block_scan((n + kExpertTile - 1) / kExpertTile, shared, all_tiles);
+        if (g < TE) {
+            r.offsets[g] = at;
+            for (int i = 0; i * kExpertTile < n; ++i)
+                r.tiles[1 + tile + i] = make_int4(g, at + i * kExpertTile, min(kExpertTile, n - i * kExpertTile), 0);
+        }
+        rows += all, tiles += all_tiles;
+    }
+    if (threadIdx.x == 0) {
+        r.offsets[TE] = rows;
+        r.tiles[0] = make_int4(tiles, rows, 0, 0);
+    }
+}
+
+// A gate's place among the open ones.
+__device__ __forceinline__ void place(const ExpertRows& r, size_t at, bool open, int slot, int source) {
+    r.slot[at] = open ? slot : -1;
+    if (open) r.source[slot] = source;
+}
+
+__global__ void __launch_bounds__(kSortThreads)
+sort_place_kernel(const float* __restrict__ G, int TE, const int* __restrict__ counts, const int* __restrict__ totals,
+                  ExpertRows r) {
+    constexpr int UNROLL = 8;
+    __shared__ int shared[kSortWarps], base[kCols];
+    pdl_wait();
+    pdl_launch_next();
+    if (blockIdx.x == gridDim.x - 1) {                 // the last CTA has no columns
+        write_groups([&](int g) { return totals[g]; }, r, TE, shared);
+        return;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = lane & 7, g0 = blockIdx.x * kCols, g = g0 + col;
+    int before = 0;
+    for (int i = threadIdx.x; i < g0; i += kSortThreads) before += totals[i];
+    int all;
+    block_scan(before, shared, all);
+    if (threadIdx.x < kCols) {
+        int x = all;
+        for (int i = g0; i < g0 + (int)threadIdx.x && i < TE; ++i) x += totals[i];
+        base[threadIdx.x] = x;
+    }
+    int mine = 0;
+    // the warps before this one: lanes 8 j + col take warps j, j + 4, ..
+    for (int w = lane >> 3; w < warp; w += 4)
+        if (g < TE) mine += counts[(size_t)w * TE + g];
+    mine += __shfl_xor_sync(0xffffffffu, mine, 8);
+    mine += __shfl_xor_sync(0xffffffffu, mine, 16);
+    __syncthreads();
+    mine += base[col];
+    int b0, b1;
+    warp_rows(r.B, warp, b0, b1);
+    const uint32_t below = (0x01010101u << col) & ((1u << lane) - 1u);
+    for (int b = b0; b < b1; b += 4 * UNROLL) {
+        float x[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int row = b + 4 * u + (lane >> 3);
+            x[u] = row < b1 && g < TE ? __ldg(G + (size_t)row * TE + g) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int row = b + 4 * u + (lane >> 3);
+            const uint32_t m = __ballot_sync(0xffffffffu, x[u] > 0.f);
+            if (row < b1 && g < TE)
+                place(r, (size_t)row * TE + g, x[u] > 0.f, mine + __popc(m & below), row * r.T + g / r.E);
+            mine += col_count(m, col);
+        }
+    }
+}
+
+// Few gates: one CTA, a thread per column.
+__global__ void __launch_bounds__(kSortThreads)
+sort_small_kernel(const float* __restrict__ G, int TE, ExpertRows r, int* __restrict__ totals) {
+    __shared__ int shared[kSortWarps];
+    pdl_wait();
+    pdl_launch_next();
+    int rows = 0;
+    for (int g0 = 0; g0 < TE; g0 += kSortThreads) {
+        const int g = g0 + threadIdx.x;
+        int n = 0, all;
+        if (g < TE) {
+#pragma unroll 8
+            for (int b = 0; b < r.B; ++b) n += __ldg(G + (size_t)b * TE + g) > 0.f;
+            totals[g] = n;
+        }
+        int at = rows + block_scan(n, shared, all);
+        rows += all;
+        if (g < TE)
+#pragma unroll 8
+            for (int b = 0; b < r.B; ++b) {
+                const bool open = __ldg(G + (size_t)b * TE + g) > 0.f;
+                place(r, (size_t)b * TE + g, open, at, b * r.T + g / r.E);
+                at += open;
+            }
+    }
+    __syncthreads();
+    write_groups([&](int g) { return totals[g]; }, r, TE, shared);
+}
+
+// ---- rows ----------------------------------------------------------------------
+constexpr int kRowWarps = 4;
+
+// A lane's piece of a row: 16 bytes, or one element where rows are not 16-byte aligned.
+template <typename T, bool VEC>
+struct Piece {
+    static constexpr int N = VEC ? 16 / (int)sizeof(T) : 1;
+    uint32_t w[VEC ? 4 : 1];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (VEC) {
+            const uint4 q = *reinterpret_cast<const uint4*>(p);
+            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        } else if constexpr (sizeof(T) == 4) {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+            w[0] = *reinterpret_cast<const uint16_t*>(p);
+        }
+    }
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (VEC)
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<uint32_t*>(p) = w[0];
+        else
+            *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+    __device__ __forceinline__ void set(const float (&v)[N]) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = __float_as_uint(v[i]);
+        } else if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        } else {
+            w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+        }
+    }
+};
+// Pieces of a row that a lane holds at once.
+template <bool VEC>
+constexpr int kHeld = VEC ? 3 : 8;
+
+// Open experts e0 .. e0 + 31 of row bt, as a mask; slot: lane e's.
+__device__ __forceinline__ uint32_t open_experts(const int* __restrict__ slots, size_t bt, int E, int e0, long long n,
+                                                 int lane, int& slot) {
+    slot = e0 + lane < E ? __ldg(slots + bt * E + e0 + lane) : -1;
+    return __ballot_sync(0xffffffffu, slot >= 0 && slot < n);
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(32 * kRowWarps)
+gather_kernel(const T* __restrict__ X, ExpertRows r, T* __restrict__ Xs, long long n, int D) {
+    using P = Piece<T, VEC>;
+    constexpr int H = kHeld<VEC>;
+    pdl_wait();
+    pdl_launch_next();
+    const int lane = threadIdx.x & 31;
+    const size_t bt = (size_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    if (bt >= (size_t)r.B * r.T) return;
+    const int pieces = D / P::N;
+    for (int p0 = lane; p0 - lane < pieces; p0 += 32 * H) {
+        P x[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i)
+            if (p0 + 32 * i < pieces) x[i].load(X + bt * D + (size_t)(p0 + 32 * i) * P::N);
+        for (int e0 = 0; e0 < r.E; e0 += 32) {
+            int slot;
+            for (uint32_t m = open_experts(r.slot, bt, r.E, e0, n, lane, slot); m; m &= m - 1) {
+                T* dst = Xs + (size_t)__shfl_sync(0xffffffffu, slot, __ffs(m) - 1) * D;
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+                    if (p0 + 32 * i < pieces) x[i].store(dst + (size_t)(p0 + 32 * i) * P::N);
+            }
+        }
+    }
+}
+
+// The same with the rows in 4 bits: a lane rounds eight values, four lanes a block.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(32 * kRowWarps)
+gather_fp4_kernel(const T* __restrict__ X, ExpertRows r, Fp4View out, long long n, int D, int nb) {
+    constexpr int H = 3;
+    pdl_wait();
+    pdl_launch_next();
+    const int lane = threadIdx.x & 31;
+    const size_t bt = (size_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    if (bt >= (size_t)r.B * r.T) return;
+    for (int p0 = lane; p0 - lane < 4 * nb; p0 += 32 * H) {
+        uint32_t code[H], E[H];
+        float v[H][8];
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const int p = p0 + 32 * i;
+            fp4_load8<T, VEC>(X + bt * D + 8 * (size_t)p, D - 8 * p, v[i]);     // past the row's end: zeros
+        }
+#pragma unroll
+        for (int i = 0; i < H; ++i) code[i] = fp4_round8(v[i], E[i]);
+        for (int e0 = 0; e0 < r.E; e0 += 32) {
+            int slot;
+            for (uint32_t m = open_experts(r.slot, bt, r.E, e0, n, lane, slot); m; m &= m - 1) {
+                const size_t row = (size_t)__shfl_sync(0xffffffffu, slot, __ffs(m) - 1);
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const int p = p0 + 32 * i;
+                    if (p < 4 * nb) {
+                        *reinterpret_cast<uint32_t*>(out.codes + row * out.ld + 4 * p) = code[i];
+                        if ((p & 3) == 0) out.scales[row * out.lds + (p >> 2)] = (uint8_t)E[i];
+                    }
+                }
+            }
+        }
+    }
+}
+
+// TO: the type of V; sums in float32, ascending e.
+template <typename T, typename TO, bool VEC>
+__global__ void __launch_bounds__(32 * kRowWarps)
+combine_kernel(const T* __restrict__ Y, ExpertRows r, const float* __restrict__ G, TO* __restrict__ V, long long n, int D) {
+    using P = Piece<T, VEC>;
+    constexpr int H = kHeld<VEC>, N = P::N;
+    pdl_wait();
+    pdl_launch_next();
+    const int lane = threadIdx.x & 31;
+    const size_t bt = (size_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    if (bt >= (size_t)r.B * r.T) return;
+    const int pieces = D / N;
+    for (int p0 = lane; p0 - lane < pieces; p0 += 32 * H) {
+        float v[H][N] = {};
+        for (int e0 = 0; e0 < r.E; e0 += 32) {
+            int slot;
+            const uint32_t open = open_experts(r.slot, bt, r.E, e0, n, lane, slot);
+            const float gate = G && e0 + lane < r.E ? __ldg(G + bt * r.E + e0 + lane) : 1.f;
+            for (uint32_t m = open; m; m &= m - 1) {
+                const int e = __ffs(m) - 1;
+                const T* src = Y + (size_t)__shfl_sync(0xffffffffu, slot, e) * D;
+                const float g = __shfl_sync(0xffffffffu, gate, e);
+                P y[H];
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+                    if (p0 + 32 * i < pieces) y[i].load(src + (size_t)(p0 + 32 * i) * N);
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+                    if (p0 + 32 * i < pieces) {
+#pragma unroll
+                        for (int k = 0; k < N; ++k) v[i][k] = fmaf(g, y[i].get(k), v[i][k]);
+                    }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < H; ++i)
+            if (p0 + 32 * i < pieces) {
+                TO* dst = V + bt * D + (size_t)(p0 + 32 * i) * N;
+                if constexpr (sizeof(T) == sizeof(TO)) {
+                    Piece<TO, VEC> o;
+                    o.set(v[i]);
+                    o.store(dst);
+                } else if constexpr (VEC) {                 // bf16 rows to float
+                    reinterpret_cast<float4*>(dst)[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+                    reinterpret_cast<float4*>(dst)[1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
+                } else {
+                    *dst = v[i][0];
+                }
+            }
+    }
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(32 * kRowWarps)
+combine_backward_kernel(const T* __restrict__ dV, const T* __restrict__ Y, ExpertRows r, const float* __restrict__ G,
+                        T* __restrict__ dY, float* __restrict__ dG, long long n, int D) {
+    using P = Piece<T, VEC>;
+    constexpr int H = kHeld<VEC>, N = P::N;
+    pdl_wait();
+    pdl_launch_next();
+    const int lane = threadIdx.x & 31;
+    const size_t bt = (size_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    if (bt >= (size_t)r.B * r.T) return;
+    const int pieces = D / N;
+    for (int e0 = 0; e0 < r.E; e0 += 32) {
+        int slot;
+        const uint32_t open = open_experts(r.slot, bt, r.E, e0, n, lane, slot);
+        const float gate = e0 + lane < r.E ? __ldg(G + bt * r.E + e0 + lane) : 0.f;
+        float mine = 0.f;                                   // lane e's dG
+        for (uint32_t m = open; m; m &= m - 1) {
+            const int e = __ffs(m) - 1;
+            const size_t row = (size_t)__shfl_sync(0xffffffffu, slot, e) * D;
+            const float g = __shfl_sync(0xffffffffu, gate, e);
+            float dot = 0.f;
+            for (int p0 = lane; p0 < pieces; p0 += 32 * H) {
+                P y[H], d[H];
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+                    if (p0 + 32 * i < pieces) {
+                        d[i].load(dV + bt * D + (size_t)(p0 + 32 * i) * N);
+                        y[i].load(Y + row + (size_t)(p0 + 32 * i) * N);
+                    }
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+                    if (p0 + 32 * i < pieces) {
+                        float o[N];
+#pragma unroll
+                        for (int k = 0; k < N; ++k) {
+                            dot = fmaf(y[i].get(k), d[i].get(k), dot);
+                            o[k] = g * d[i].get(k);
+                        }
+                        P q;
+                        q.set(o);
+                        q.store(dY + row + (size_t)(p0 + 32 * i) * N);
+                    }
+            }
+            dot = warp_sum(dot);
+            if (lane == e) mine = dot;
+        }
+        if (e0 + lane < r.E) dG[bt * r.E + e0 + lane] = mine;
+    }
+}
+
+bool aligned_rows(std::initializer_list<const void*> ps, int D, int esz) {
+    for (const void* p : ps)
+        if (!fp8_on(p, 16)) return false;
+    return D * (long long)esz % 16 == 0;
+}
+dim3 row_grid(const ExpertRows& r) { return dim3((unsigned)(((long long)r.B * r.T + kRowWarps - 1) / kRowWarps)); }
+const dim3 kRowBlock(32 * kRowWarps);
+
+template <typename T>
+cudaError_t gather(const T* X, const ExpertRows& r, T* Xs, long long n, int D, cudaStream_t s) {
+    auto k = aligned_rows({X, Xs}, D, sizeof(T)) ? gather_kernel<T, true> : gather_kernel<T, false>;
+    return launch_k(k, row_grid(r), kRowBlock, 0, s, X, r, Xs, n, D);
+}
+template <typename T>
+cudaError_t gather_fp4(const T* X, const ExpertRows& r, const Fp4View& out, long long n, int D, cudaStream_t s) {
+    auto k = aligned_rows({X}, D, sizeof(T)) ? gather_fp4_kernel<T, true> : gather_fp4_kernel<T, false>;
+    return launch_k(k, row_grid(r), kRowBlock, 0, s, X, r, out, n, D, (int)fp4_blocks(D));
+}
+template <typename T, typename TO>
+cudaError_t combine(const T* Y, const ExpertRows& r, const float* G, TO* V, long long n, int D, cudaStream_t s) {
+    auto k = aligned_rows({Y, V}, D, sizeof(T)) ? combine_kernel<T, TO, true> : combine_kernel<T, TO, false>;
+    return launch_k(k, row_grid(r), kRowBlock, 0, s, Y, r, G, V, n, D);
+}
+template <typename T>
+cudaError_t combine_backward(const T* dV, const T* Y, const ExpertRows& r, const float* G, T* dY, float* dG, long long n,
+                             int D, cudaStream_t s) {
+    auto k = aligned_rows({dV, Y, dY}, D, sizeof(T)) ? combine_backward_kernel<T, true> : combine_backward_kernel<T, false>;
+    return launch_k(k, row_grid(r), kRowBlock, 0, s, dV, Y, r, G, dY, dG, n, D);
+}
+bool rows_ok(const ExpertRows& r, long long n, int D) {
+    return r.B >= 1 && r.T >= 1 && r.E >= 1 && (long long)r.B * r.T * r.E < (1ll << 31) && r.slot && n >= 0 && D >= 1;
+}
+
+}  // namespace
+
+long long expert_sort_work(int B, int T, int E) {
+    const long long TE = (long long)T * E;
+    return sorts_at_once(B, TE) ? TE : (kSortWarps + 1) * TE;
+}
+
+cudaError_t launch_expert_sort(const float* G, const ExpertRows& r, int* work, cudaStream_t s) {
+    RM_HOST_BOUNDS(G && rows_ok(r, 0, 1) && r.offsets && r.source && fp8_on(r.tiles, 16) && work);
+    const int TE = r.T * r.E;
+    if (sorts_at_once(r.B, TE))
+        return launch_k(sort_small_kernel, dim3(1), dim3(kSortThreads), 0, s, G, TE, r, work);
+    int *totals = work, *counts = work + TE;
+    const unsigned ctas = (unsigned)((TE + kCols - 1) / kCols);
+    const cudaError_t e = launch_k(sort_count_kernel, dim3(ctas), dim3(kSortThreads), 0, s, G, r.B, TE, counts, totals);
+    if (e != cudaSuccess) return e;
+    return launch_k(sort_place_kernel, dim3(ctas + 1), dim3(kSortThreads), 0, s, G, TE, (const int*)counts,
+                    (const int*)totals, r);
+}
+
+cudaError_t launch_expert_gather(const void* X, bool f32, const ExpertRows& r, void* Xs, long long n, int D,
+                                 cudaStream_t s) {
+    RM_HOST_BOUNDS(X && Xs && rows_ok(r, n, D));
+    return f32 ? gather(static_cast<const float*>(X), r, static_cast<float*>(Xs), n, D, s)
+               : gather(static_cast<const __nv_bfloat16*>(X), r, static_cast<__nv_bfloat16*>(Xs), n, D, s);
+}
+
+cudaError_t launch_expert_gather_fp4(const void* X, bool f32, const ExpertRows& r, const Fp4View& out, long long n, int D,
+                                     cudaStream_t s) {
+    RM_HOST_BOUNDS(X && rows_ok(r, n, D) && fp4_holds(out, D));
+    return f32 ? gather_fp4(static_cast<const float*>(X), r, out, n, D, s)
+               : gather_fp4(static_cast<const __nv_bfloat16*>(X), r, out, n, D, s);
+}
+
+cudaError_t launch_expert_combine(const void* Y, bool y_f32, const ExpertRows& r, const float* G, void* V, bool v_f32,
+                                  long long n, int D, cudaStream_t s) {
+    RM_HOST_BOUNDS((Y || n == 0) && V && rows_ok(r, n, D));
+    if (y_f32 && !v_f32) return cudaErrorNotSupported;
+    if (y_f32) return combine(static_cast<const float*>(Y), r, G, static_cast<float*>(V), n, D, s);
+    if (v_f32) return combine(static_cast<const __nv_bfloat16*>(Y), r, G, static_cast<float*>(V), n, D, s);
+    return combine(static_cast<const __nv_bfloat16*>(Y), r, G, static_cast<__nv_bfloat16*>(V), n, D, s);
+}
+
+cudaError_t launch_expert_combine_backward(const void* dV, const void* Y, bool f32, const ExpertRows& r, const float* G,
+                                           void* dY, float* dG, long long n, int D, cudaStream_t s) {
+    RM_HOST_BOUNDS(dV && (n == 0 || (Y && dY)) && dG && G && rows_ok(r, n, D));
+    using H = __nv_bfloat16;
+    return f32 ? combine_backward(static_cast<const float*>(dV), static_cast<const float*>(Y), r, G, static_cast<float*>(dY),
+                                  dG, n, D, s)
+               : combine_backward(static_cast<const H*>(dV), static_cast<const H*>(Y), r, G, static_cast<H*>(dY), dG, n, D, s);
+}
+
+}  // namespace rm

@@ -1,0 +1,97 @@
+// Device helpers of the 4-bit operators: the block exponent, codes and their
+// values (the format of include/rankmixer.h, "4-bit operands").
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "rm_common.cuh"
+#include "rm_fp4.h"
+
+namespace rm {
+
+// Exponent byte of a block whose largest magnitude has the float bits amax: the
+// smallest E with amax <= 6 2^(E - 127), at least 1; 127 for zeros; 255 (the block
+// is NaN) where a value is not finite.  6 = 1.5 2^2, so with amax = 1.m 2^(x - 127)
+// that is E = x - 2, one more when 1.m > 1.5.
+__device__ __forceinline__ uint32_t fp4_exponent(uint32_t amax) {
+    if (amax >= 0x7f800000u) return 255u;
+    const int e = (int)(amax >> 23) - 2 + ((amax & 0x7fffffu) > 0x400000u ? 1 : 0);
+    return amax == 0u ? 127u : (uint32_t)(e < 1 ? 1 : e);
+}
+// 2^(127 - E) for E in [1, 253]; 0 for 255.
+__device__ __forceinline__ float fp4_inv_scale(uint32_t E) { return E == 255u ? 0.f : __uint_as_float((254u - E) << 23); }
+
+// Eight floats (already scaled) to eight codes, the first in the lowest bits: to the
+// nearest, ties to the even code.
+__device__ __forceinline__ uint32_t fp4_pack8(const float (&v)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+// The eight numbers that eight codes stand for (exact).
+__device__ __forceinline__ void fp4_unpack8(uint32_t codes, float (&v)[8]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(codes));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ uint32_t fp4_abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Eight values of a row from p on as float, the first n of them (the rest zero).  VEC:
+// p is 16-byte aligned where n is 8 or more.
+template <typename IN, bool VEC>
+__device__ __forceinline__ void fp4_load8(const IN* __restrict__ p, int n, float (&v)[8]) {
+    if (VEC && n >= 8) {
+        if constexpr (sizeof(IN) == 2) {
+            const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(u[i] << 16);
+                v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            }
+        } else {
+            const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
+    }
+}
+
+// Eight values of one of a block's four lanes (neighbours) to their codes; E: the block's exponent byte.
+__device__ __forceinline__ uint32_t fp4_round8(float (&v)[8], uint32_t& E) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, fp4_abs_bits(v[i]));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    E = fp4_exponent(m);
+    const float s = fp4_inv_scale(E);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= s;
+    return fp4_pack8(v);
+}
+
+}  // namespace rm

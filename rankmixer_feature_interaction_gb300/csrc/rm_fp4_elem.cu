@@ -1,0 +1,277 @@
+// Elementwise kernels of the 4-bit operators: rows and weights to 4 bits, rows back.
+//
+// Rows: four neighbouring lanes own a block of 32 values, eight each (16 bytes of
+// bf16), agree on its largest magnitude with two shuffles and write four bytes of
+// codes each, so a warp reads 512 bytes in a row and writes 128.  Rows that are not
+// 16-byte aligned are read (or written) an element at a time, neighbouring lanes
+// neighbouring elements, and change their order in a kilobyte of shared memory per
+// warp.  Bound by memory: 2.53 bytes a value from bf16.
+#include "rm_fp4.cuh"
+
+namespace rm {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+// Row and piece of a running number (pieces of a row: n).
+__device__ __forceinline__ void split(unsigned long long id, bool small, unsigned n, unsigned long long& row, int& j) {
+    if (small) {
+        const uint32_t r = (uint32_t)id / n;
+        row = r, j = (int)((uint32_t)id - r * n);
+    } else {
+        row = id / n, j = (int)(id - row * n);
+    }
+}
+
+// Aligned rows: `lanes` = 4 per block.
+template <typename IN>
+__global__ void __launch_bounds__(kThreads)
+quantize_kernel(const IN* __restrict__ X, unsigned long long pieces, int cols, int nb, long long ldx, Fp4View out) {
+    constexpr int UNROLL = sizeof(IN) == 2 ? 4 : 2;
+    pdl_wait();
+    pdl_launch_next();
+    const unsigned long long base = (unsigned long long)blockIdx.x * (kThreads * UNROLL) + threadIdx.x;
+    const bool small = pieces <= 0xffffffffull;
+    float v[UNROLL][8];
+    unsigned long long row[UNROLL];
+    int j[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        const unsigned long long id = base + (unsigned long long)u * kThreads;
+        split(id < pieces ? id : pieces - 1, small, 4u * nb, row[u], j[u]);
+        fp4_load8<IN, true>(X + row[u] * ldx + 8 * j[u], cols - 8 * j[u], v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        uint32_t E;
+        const uint32_t c = fp4_round8(v[u], E);
+        if (base + (unsigned long long)u * kThreads < pieces) {
+            *reinterpret_cast<uint32_t*>(out.codes + row[u] * out.ld + 4 * j[u]) = c;
+            if ((j[u] & 3) == 0) out.scales[row[u] * out.lds + (j[u] >> 2)] = (uint8_t)E;
+        }
+    }
+}
+
+// Other rows: a warp takes 256 values of a row.
+template <typename IN>
+__global__ void __launch_bounds__(kThreads)
+quantize_odd_kernel(const IN* __restrict__ X, unsigned long long chunks, int cols, int nb, int per_row, long long ldx,
+                    Fp4View out) {
+    __shared__ float turn[kWarps][256];
+    pdl_wait();
+    pdl_launch_next();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned long long id = (unsigned long long)blockIdx.x * kWarps + warp;
+    if (id >= chunks) return;
+    unsigned long long row;
+    int c;
+    split(id, chunks <= 0xffffffffull, per_row, row, c);
+    const IN* p = X + row * ldx + 256 * (long long)c;
+    const int n = cols - 256 * c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int k = 32 * i + lane;
+        turn[warp][k] = k < n ? to_f32(p[k]) : 0.f;
+    }
+    __syncwarp();
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = turn[warp][8 * lane + i];
+    uint32_t E;
+    const uint32_t w = fp4_round8(v, E);
+    const int b = 8 * c + (lane >> 2);
+    if (b < nb) {
+        *reinterpret_cast<uint32_t*>(out.codes + row * out.ld + 16 * b + 4 * (lane & 3)) = w;
+        if ((lane & 3) == 0) out.scales[row * out.lds + b] = (uint8_t)E;
+    }
+}
+
+template <typename OUT>
+__device__ __forceinline__ void value8(uint32_t codes, uint32_t E, float (&v)[8]) {
+    fp4_unpack8(codes, v);
+    // 2^(E - 127); 0 stands for 2^-127, 255 for NaN
+    const float s = E == 0u ? __uint_as_float(0x00400000u) : E == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(E << 23);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= s;
+}
+
+template <typename OUT>
+__global__ void __launch_bounds__(kThreads)
+dequantize_kernel(Fp4View in, unsigned long long pieces, int cols, int nb, OUT* __restrict__ Y, long long ldy) {
+    constexpr int UNROLL = 4;
+    pdl_wait();
+    pdl_launch_next();
+    const unsigned long long base = (unsigned long long)blockIdx.x * (kThreads * UNROLL) + threadIdx.x;
+    const bool small = pieces <= 0xffffffffull;
+    uint32_t c[UNROLL], E[UNROLL];
+    unsigned long long row[UNROLL];
+    int j[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        const unsigned long long id = base + (unsigned long long)u * kThreads;
+        split(id < pieces ? id : pieces - 1, small, 4u * nb, row[u], j[u]);
+        c[u] = *reinterpret_cast<const uint32_t*>(in.codes + row[u] * in.ld + 4 * j[u]);
+        E[u] = in.scales[row[u] * in.lds + (j[u] >> 2)];
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        if (base + (unsigned long long)u * kThreads >= pieces) return;
+        float v[8];
+        value8<OUT>(c[u], E[u], v);
+        OUT* y = Y + row[u] * ldy + 8 * j[u];
+        const int n = cols - 8 * j[u];
+        if (n >= 8) {
+            if constexpr (sizeof(OUT) == 2) {
+                __stcs(reinterpret_cast<uint4*>(y), make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+            } else {
+                __stcs(reinterpret_cast<float4*>(y), make_float4(v[0], v[1], v[2], v[3]));
+                __stcs(reinterpret_cast<float4*>(y) + 1, make_float4(v[4], v[5], v[6], v[7]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (i < n) y[i] = from_f32<OUT>(v[i]);
+        }
+    }
+}
+
+template <typename OUT>
+__global__ void __launch_bounds__(kThreads)
+dequantize_odd_kernel(Fp4View in, unsigned long long chunks, int cols, int nb, int per_row, OUT* __restrict__ Y,
+                      long long ldy) {
+    __shared__ float turn[kWarps][256];
+    pdl_wait();
+    pdl_launch_next();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned long long id = (unsigned long long)blockIdx.x * kWarps + warp;
+    if (id >= chunks) return;
+    unsigned long long row;
+    int c;
+    split(id, chunks <= 0xffffffffull, per_row, row, c);
+    const int b = 8 * c + (lane >> 2);
+    float v[8] = {};
+    if (b < nb)
+        value8<OUT>(*reinterpret_cast<const uint32_t*>(in.codes + row * in.ld + 16 * b + 4 * (lane & 3)),
+                    in.scales[row * in.lds + b], v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn[warp][8 * lane + i] = v[i];
+    __syncwarp();
+    OUT* y = Y + row * ldy + 256 * (long long)c;
+    const int n = cols - 256 * c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int k = 32 * i + lane;
+        if (k < n) y[k] = from_f32<OUT>(turn[warp][k]);
+    }
+}
+
+// Weights [G][K][N] to rows along K: a thread owns 128 values of K of one column (a
+// warp reads 32 neighbouring columns at a time), writes 64 bytes of codes and the
+// word of four exponent bytes where the products read it.  Columns past N and blocks
+// past K get exponent bytes of 127.
+constexpr int kWeightThreads = 128;
+template <typename IN>
+__global__ void __launch_bounds__(kWeightThreads)
+quantize_weight_kernel(const IN* __restrict__ W, int K, int N, int nb, Fp4View out) {
+    pdl_wait();
+    pdl_launch_next();
+    const int tile = blockIdx.x, g = blockIdx.z, r = threadIdx.x, n = tile * kFp4TileRows + r;
+    const long long tiles = (N + kFp4TileRows - 1) / kFp4TileRows;
+    for (int q = blockIdx.y; q < out.lds; q += gridDim.y) {
+        uint32_t word = 0;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+            const int b = 4 * q + c, k0 = kFp4Block * b;
+            uint32_t E = 127;
+            if (n < N && b < nb) {
+                float v[4][8];
+                const IN* p = W + ((size_t)g * K + k0) * N + n;
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float x = k0 + i < K ? to_f32(p[(size_t)i * N]) : 0.f;
+                    v[i >> 3][i & 7] = x;
+                    m = max(m, fp4_abs_bits(x));
+                }
+                E = fp4_exponent(m);
+                const float s = fp4_inv_scale(E);
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[i][k] *= s;
+                    w[i] = fp4_pack8(v[i]);
+                }
+                *reinterpret_cast<uint4*>(out.codes + ((size_t)g * N + n) * out.ld + 16 * (size_t)b) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            word |= E << (8 * c);
+        }
+        *reinterpret_cast<uint32_t*>(out.scales + (((size_t)g * tiles + tile) * out.lds + q) * 512 + 16 * (r & 31) +
+                                     4 * (r >> 5)) = word;
+    }
+}
+
+bool rows_aligned(const void* p, long long ld, int esz) { return fp8_on(p, 16) && ld * esz % 16 == 0; }
+
+template <typename IN>
+cudaError_t quantize(const IN* X, long long rows, int cols, long long ldx, const Fp4View& out, cudaStream_t s) {
+    const int nb = (int)fp4_blocks(cols);
+    if (rows_aligned(X, ldx, sizeof(IN))) {
+        constexpr int PER = kThreads * (sizeof(IN) == 2 ? 4 : 2);
+        const unsigned long long pieces = 4ull * rows * nb, grid = (pieces + PER - 1) / PER;
+        if (grid > 0x7fffffffull) return cudaErrorNotSupported;
+        return launch_k(quantize_kernel<IN>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, pieces, cols, nb, ldx, out);
+    }
+    const int per_row = (cols + 255) / 256;
+    const unsigned long long chunks = (unsigned long long)rows * per_row, grid = (chunks + kWarps - 1) / kWarps;
+    if (grid > 0x7fffffffull) return cudaErrorNotSupported;
+    return launch_k(quantize_odd_kernel<IN>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, chunks, cols, nb, per_row, ldx,
+                    out);
+}
+
+template <typename OUT>
+cudaError_t dequantize(const Fp4View& in, long long rows, int cols, OUT* Y, long long ldy, cudaStream_t s) {
+    const int nb = (int)fp4_blocks(cols);
+    if (rows_aligned(Y, ldy, sizeof(OUT))) {
+        const unsigned long long pieces = 4ull * rows * nb, grid = (pieces + 4 * kThreads - 1) / (4 * kThreads);
+        if (grid > 0x7fffffffull) return cudaErrorNotSupported;
+        return launch_k(dequantize_kernel<OUT>, dim3((unsigned)grid), dim3(kThreads), 0, s, in, pieces, cols, nb, Y, ldy);
+    }
+    const int per_row = (cols + 255) / 256;
+    const unsigned long long chunks = (unsigned long long)rows * per_row, grid = (chunks + kWarps - 1) / kWarps;
+    if (grid > 0x7fffffffull) return cudaErrorNotSupported;
+    return launch_k(dequantize_odd_kernel<OUT>, dim3((unsigned)grid), dim3(kThreads), 0, s, in, chunks, cols, nb, per_row,
+                    Y, ldy);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_quantize(bool f32, const void* X, long long rows, int cols, long long ldx, const Fp4View& out,
+                                cudaStream_t s) {
+    RM_HOST_BOUNDS(X && rows >= 1 && cols >= 1 && ldx >= cols && fp4_holds(out, cols));
+    return f32 ? quantize(static_cast<const float*>(X), rows, cols, ldx, out, s)
+               : quantize(static_cast<const __nv_bfloat16*>(X), rows, cols, ldx, out, s);
+}
+
+cudaError_t launch_fp4_dequantize(const Fp4View& in, long long rows, int cols, void* Y, bool f32, long long ldy,
+                                  cudaStream_t s) {
+    RM_HOST_BOUNDS(Y && rows >= 1 && cols >= 1 && ldy >= cols && fp4_holds(in, cols));
+    return f32 ? dequantize(in, rows, cols, static_cast<float*>(Y), ldy, s)
+               : dequantize(in, rows, cols, static_cast<__nv_bfloat16*>(Y), ldy, s);
+}
+
+cudaError_t launch_fp4_quantize_weight(bool f32, const void* W, int G, int K, int N, const Fp4View& out, cudaStream_t s) {
+    RM_HOST_BOUNDS(W && G >= 1 && G <= 65535 && K >= 1 && N >= 1 && out.lds == fp4_weight_quads(K) &&
+                   fp8_on(out.codes, 16) && fp8_on(out.scales, 16) && out.ld % 16 == 0 && out.ld >= 16 * fp4_blocks(K));
+    const int nb = (int)fp4_blocks(K);
+    const dim3 grid((unsigned)((N + kFp4TileRows - 1) / kFp4TileRows), (unsigned)(out.lds < 65535 ? out.lds : 65535),
+                    (unsigned)G);
+    return f32 ? launch_k(quantize_weight_kernel<float>, grid, dim3(kWeightThreads), 0, s, static_cast<const float*>(W), K, N,
+                          nb, out)
+               : launch_k(quantize_weight_kernel<__nv_bfloat16>, grid, dim3(kWeightThreads), 0, s,
+                          static_cast<const __nv_bfloat16*>(W), K, N, nb, out);
+}
+
+}  // namespace rm

@@ -42,6 +42,8 @@ struct Fp8Device {
     int* err;
     unsigned long long timeout_ns;
 };
+// Of the current device, looked up once per device; RM_OK (0) or the call's status.
+int fp8_device(Fp8Device* out);
 
 // acc[b][t][n] = sum_k x[b][t][k] W[t][k][n] (trans: W[t][n][k]), then
 //   FP8_OUT_*:  y = acc + bias (bias nullable)

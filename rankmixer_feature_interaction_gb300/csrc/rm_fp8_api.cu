@@ -247,6 +247,10 @@ Fp8Product product(rm_dtype dtype, const rm_fp8_tensor& x, const rm_fp8_tensor& 
 
 }  // namespace
 
+namespace rm {
+int fp8_device(Fp8Device* out) { return device_info(out); }
+}  // namespace rm
+
 rm_status rm_fp8_quantize(const void* X, rm_dtype dtype, long long rows, int cols, long long ldx,
                           const rm_fp8_tensor* out, void* stream) {
     if (!X) return fail(RM_ERR_INVALID_ARG, "X is NULL");
@@ -424,8 +428,8 @@ rm_status rm_fp8_sync_status(void* stream) {
     } catch (const std::bad_alloc&) {
         return fail(RM_ERR_OOM, "rm_fp8_sync_status");
     }
-    return r.last == kDevErrTimeout ? fail(RM_ERR_TIMEOUT, "a device-side wait of an 8-bit operator ran out")
-                                    : fail(RM_ERR_DEVICE, "device error %d in an 8-bit operator", r.last);
+    return r.last == kDevErrTimeout ? fail(RM_ERR_TIMEOUT, "a device-side wait of an 8-bit or 4-bit operator ran out")
+                                    : fail(RM_ERR_DEVICE, "device error %d in an 8-bit or 4-bit operator", r.last);
 }
 
 rm_status rm_debug_fp8_wait_timeout(int timeout_us, void* stream) {
