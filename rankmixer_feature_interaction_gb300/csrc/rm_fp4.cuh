@@ -57,6 +57,13 @@ __device__ __forceinline__ void fp4_unpack8(uint32_t codes, float (&v)[8]) {
 }
 __device__ __forceinline__ uint32_t fp4_abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
+// Largest of three; NaN where one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Eight values of a row from p on as float, the first n of them (the rest zero).  VEC:
 // p is 16-byte aligned where n is 8 or more.
 template <typename IN, bool VEC>

@@ -1,82 +1,468 @@
-// Products of 4-bit operands, in the simplest form: a thread per column, the rows of a
-// tile one after another, codes and scales read where they lie.
-#include "rm_fp4.cuh"
-#include "rm_fp8.cuh"
+// Products of 4-bit operands on the 5th-generation tensor cores:
+//   Y[row][n] = sum_k x[row][k] W[g][n][k]    for the rows of every group g,
+// groups being the tokens of a sample-major batch, or the experts of sorted rows.
+// One power-of-two scale per 32 values of K of either operand, which the
+// block-scaled MMA (tcgen05.mma kind::mxf4, 64 values of K a step) multiplies in on
+// the way into the float32 accumulator; both operands K-major, as that kind has it.
+//
+// Kernel: one persistent pair of CTAs (two SMs) per 256 x 256 tile of one group;
+// each CTA holds 128 rows of x and 128 rows (columns of Y) of W per k-block of 256
+// values, 32 KB of codes a stage and 3 KB of exponent bytes.
+//   warp 0       TMA producer: codes of x and W, W's exponent bytes (already in the
+//                tensor cores' order, those of all 256 columns in both CTAs)
+//   warp 1       MMA issuer (the even CTA's): six copies of exponent bytes to tensor
+//                memory and four MMAs a k-block
+//   warp 2       x's exponent bytes (rows may start anywhere, so they lie row by
+//                row): 16 bytes a row are two k-blocks', turned in registers
+//   warps 4-19   epilogue: each thread owns 64 columns of one row, so that a block of
+//                32 of a 4-bit output is one thread's
+// Tensor memory (512 columns): two accumulators of 256 columns that share 64, at
+// columns 0 and 192, so that the next tile's product begins as soon as those 64
+// columns have been read, and two slots of exponent bytes from column 448 (8 columns
+// for x, 16 for W).  Copies and MMAs of one thread run in order, so the slots need no
+// barriers of their own.
+// Every mbarrier wait is bounded in time; on expiry the CTA latches an error
+// word and all roles unwind.
+#include <cudaTypedefs.h>
+
+#include "rm_fp4_tc.cuh"
 
 namespace rm {
-namespace {
+namespace f4 {
 
-constexpr int kThreads = 128;
+constexpr int BM = 128;                  // rows per CTA
+constexpr int BN = 256;                  // columns per tile
+constexpr int A_BYTES = BM * 128, B_BYTES = BN / 2 * 128, SFB_BYTES = 2 * SF_BYTES;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int TX_BYTES = STAGE_BYTES + SFB_BYTES;       // what TMA brings to a CTA's stage
+constexpr int STAGES = 5;
+constexpr int EPI_WARPS = 16;
+constexpr int COLS = 64;                 // columns per epilogue warp
+constexpr int STAGING = 2048;            // per epilogue warp: 32 rows of 64 bytes
+constexpr int THREADS = 128 + 32 * EPI_WARPS;
+constexpr uint32_t ACC1_COL = 192;       // the second accumulator's first column
+constexpr uint32_t SF_COL = 448, SF_COLS = 24;
+// registers: 640 threads launched with 96; 128 x 64 + 512 x 104 = 640 x 96
+constexpr int REGS_OTHER = 64, REGS_EPI = 104;
+constexpr int SMEM_BYTES = 1024 + STAGES * (STAGE_BYTES + SF_BYTES + SFB_BYTES) + EPI_WARPS * STAGING + 256;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 
-__device__ __forceinline__ float scale_of(uint32_t E) { return fp8_scale(E); }
+struct Args {
+    int B, G, K, N;                      // rows of a group (per token), groups
+    int m_tiles, n_tiles, kblocks, nb;
+    long long units;                     // tiles; experts: columns of tiles (times the table's length)
+    const int4* table;                   // experts: the tiles of rows (null: per token)
+    long long n;                         // experts: rows that exist
+    long long step;                      // between rows of a group
+    const uint8_t* xs;
+    long long xs_ld;
+    const float* bias;                   // [G][N] or null
+    void* y;
+    bool vec;                            // y's rows are 16-byte aligned
+    Fp4View o;
+    int* err;
+    unsigned long long timeout_ns;
+};
 
-template <int EPI>
-__global__ void __launch_bounds__(kThreads)
-product_kernel(Fp4Product p, long long n_rows) {
+struct Tile {
+    RowTile r;
+    int n0;
+};
+// Per token, tiles of rows fastest: neighbouring pairs share W's columns, and a
+// token's x (which every tile of columns reads again) stays in L2.  Experts: columns
+// fastest, so that a tile of rows is read from memory once.
+template <bool EXPERTS>
+__device__ __forceinline__ Tile tile_of(long long i, const Args& a) {
+    Tile t;
+    if (EXPERTS) {
+        const long long l = i / a.n_tiles;
+        t.n0 = (int)(i - l * a.n_tiles) * BN;
+        const int4 e = __ldg(a.table + 1 + l);
+        t.r = RowTile{e.x, e.y, 0, (int)min((long long)e.z, max(a.n - e.y, 0ll)), e.y};
+    } else {
+        const int per = a.m_tiles * a.n_tiles, g = (int)(i / per), rem = (int)(i - (long long)g * per), nt = rem / a.m_tiles;
+        const int m0 = (rem - nt * a.m_tiles) * 2 * BM;
+        t.n0 = nt * BN;
+        t.r = RowTile{g, m0, g, a.B - m0, (long long)m0 * a.G + g};
+    }
+    return t;
+}
+
+// 64 bytes of each row of Y from column n on.
+template <typename OUT>
+__device__ __forceinline__ void save_piece(const float* v, const Args& a, long long row, int n, int rows, int lane,
+                                           uint32_t stage) {
+    constexpr int E = sizeof(OUT);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if constexpr (E == 2)
+            st_shared_v4(staged_at(stage, lane, c), pack_bf16x2(v[8 * c], v[8 * c + 1]),
+                         pack_bf16x2(v[8 * c + 2], v[8 * c + 3]), pack_bf16x2(v[8 * c + 4], v[8 * c + 5]),
+                         pack_bf16x2(v[8 * c + 6], v[8 * c + 7]));
+        else
+            st_shared_v4(staged_at(stage, lane, c), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                         __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+    }
+    char* dst = reinterpret_cast<char*>(a.y) + (row * (long long)a.N + n) * E;
+    const size_t pitch = (size_t)a.step * (size_t)a.N * E;
+    const int bytes = min(a.N - n, 64) * E;            // the row's rest may be more bytes than fit 32 bits
+    if (a.vec)
+        store_rows<true, E>(stage, dst, pitch, rows, bytes, lane);
+    else
+        store_rows<false, E>(stage, dst, pitch, rows, bytes, lane);
+}
+
+// 32 columns of this thread's row in 4 bits.
+__device__ __forceinline__ void save_block(const float* v, const Fp4View& o, long long row, int n) {
+    float m[2] = {};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) m[i >> 1 & 1] = max3_nan(m[i >> 1 & 1], fabsf(v[i]), fabsf(v[i + 1]));
+    const uint32_t E = fp4_exponent(fp4_abs_bits(max3_nan(m[0], m[0], m[1])));
+    const uint64_t s = f2_splat(fp4_inv_scale(E));
+    uint32_t w[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) f2_unpack(f2_mul(f2_pack(v[8 * c + i], v[8 * c + i + 1]), s), q[i], q[i + 1]);
+        w[c] = fp4_pack8(q);
+    }
+    *reinterpret_cast<uint4*>(o.codes + row * o.ld + n / 2) = make_uint4(w[0], w[1], w[2], w[3]);
+    o.scales[row * o.lds + n / kFp4Block] = (uint8_t)E;
+}
+
+template <int EPI, bool EXPERTS>
+__global__ void __launch_bounds__(THREADS, 1)
+fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                   const __grid_constant__ CUtensorMap tmS, const Args args) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t* base_ptr = smem_raw + (base - raw_addr);
+    const uint32_t sA = base, sB = base + STAGES * A_BYTES;
+    const uint32_t sSFA = base + STAGES * STAGE_BYTES, sSFB = sSFA + STAGES * SF_BYTES;
+    const uint32_t sEpi = sSFB + STAGES * SFB_BYTES;
+    const uint32_t bar0 = sEpi + EPI_WARPS * STAGING;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + x); };
+    auto tempty_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 + x); };
+    const uint32_t shared_bar = bar0 + 8u * (2 * STAGES + 4);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (shared_bar + 8u - base));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const long long unit = blockIdx.x >> 1, nunits = gridDim.x >> 1;
+
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmS);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 3);           // the even CTA's: its producer, expecting both CTAs' bytes, and both scale warps
+            mbar_init(empty_bar(s), 1);          // multicast commit
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(tfull_bar(x), 1);              // multicast commit
+            mbar_init(tempty_bar(x), 2 * EPI_WARPS); // the even CTA's: every epilogue warp of both CTAs
+        }
+        mbar_init(shared_bar, 2 * EPI_WARPS / 4);    // the even CTA's: the warps that own the shared columns
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 3) {
+        tmem_alloc_pair(smem_u32(tmem_holder), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
+    const int kblocks = args.kblocks;
     pdl_wait();
     pdl_launch_next();
-    const int n = blockIdx.x * kThreads + threadIdx.x, nb = (p.K + kFp4Block - 1) / kFp4Block;
-    const bool live = n < p.N;
-    const long long tiles_n = (p.N + kFp4TileRows - 1) / kFp4TileRows;
-    long long units = p.tiles ? p.tiles[0].x : (long long)p.B * p.G;
-    for (long long u = blockIdx.y; u < units; u += gridDim.y) {
-        int g, rows = 1;
-        long long row0;
-        if (p.tiles) {
-            const int4 t = p.tiles[1 + u];
-            g = t.x, row0 = t.y, rows = t.z;
-        } else {
-            g = (int)(u % p.G), row0 = u;
-        }
-        for (int i = 0; i < rows && row0 + i < n_rows; ++i) {
-            const long long row = row0 + i;
-            float acc = 0.f;
-            if (live)
-                for (int b = 0; b < nb; ++b) {
-                    const uint4 xc = *reinterpret_cast<const uint4*>(p.x.codes + row * p.x.ld + 16 * b);
-                    const uint4 wc = *reinterpret_cast<const uint4*>(p.w.codes + ((long long)g * p.N + n) * p.w.ld + 16 * b);
-                    const uint32_t* xw = &xc.x;
-                    const uint32_t* ww = &wc.x;
-                    const uint8_t ws = p.w.scales[(((long long)g * tiles_n + n / 128) * p.w.lds + b / 4) * 512 + 16 * (n % 32) +
-                                                  4 * (n % 128 / 32) + b % 4];
-                    const float s = scale_of(p.x.scales[row * p.x.lds + b]) * scale_of(ws);
-                    float sum = 0.f;
-                    for (int q = 0; q < 4; ++q) {
-                        float a[8], w[8];
-                        fp4_unpack8(xw[q], a);
-                        fp4_unpack8(ww[q], w);
-                        for (int k = 0; k < 8; ++k) sum = fmaf(a[k], w[k], sum);
+    const long long tiles = EXPERTS ? (long long)__ldg(&args.table[0].x) * args.n_tiles : args.units;
+
+    if (warp < 4) {
+        regs_dec<REGS_OTHER>();
+        if (warp == 0) {
+            // ------------------------------ TMA producer ------------------------------
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            Tile next{};
+            if (unit < tiles) next = tile_of<EXPERTS>(unit, args);
+            for (long long i = unit; ok && i < tiles; i += nunits) {
+                const Tile tl = next;
+                if (i + nunits < tiles) next = tile_of<EXPERTS>(i + nunits, args);
+                const int xrow = tl.r.row + BM * (int)rank, wrow = tl.n0 + BN / 2 * (int)rank;
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                        ok = false;
+                        break;
                     }
-                    acc = fmaf(s, sum, acc);
+                    if (elect_one()) {
+                        const uint32_t fb = mapa_shared(full_bar(stage), 0);
+                        if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2u * TX_BYTES);
+                        tma_load_3d_pair(&tmX, sA + stage * A_BYTES, fb, kb * 128, xrow, tl.r.plane);
+                        tma_load_3d_pair(&tmW, sB + stage * B_BYTES, fb, kb * 128, wrow, tl.r.g);
+                        tma_load_3d_pair(&tmS, sSFB + stage * SFB_BYTES, fb, kb * (SF_BYTES / 4), tl.n0 / 128, tl.r.g);
+                    }
+                    __syncwarp();
+                    if (++stage == STAGES) stage = 0, phase ^= 1u;
                 }
-            if (p.bias && live) acc += p.bias[(long long)g * p.N + n];
-            if (EPI == FP4_GELU) {
-                const float a = live ? fp8_gelu(acc) : 0.f;
-                const uint32_t E = fp4_exponent(__reduce_max_sync(0xffffffffu, fp4_abs_bits(a)));
-                float v[8];
-                for (int k = 0; k < 8; ++k) v[k] = __shfl_sync(0xffffffffu, a, (threadIdx.x & 24) + k) * fp4_inv_scale(E);
-                const uint32_t c = fp4_pack8(v);
-                if (live && (threadIdx.x & 7) == 0) *reinterpret_cast<uint32_t*>(p.o.codes + row * p.o.ld + n / 2) = c;
-                if (live && (threadIdx.x & 31) == 0) p.o.scales[row * p.o.lds + n / 32] = (uint8_t)E;
-            } else if (live) {
-                if (EPI == FP4_OUT_F32)
-                    static_cast<float*>(p.y)[row * p.N + n] = acc;
-                else
-                    static_cast<__nv_bfloat16*>(p.y)[row * p.N + n] = __float2bfloat16_rn(acc);
+            }
+        } else if (warp == 1 && rank == 0) {
+            // ------------------------------ MMA issuer --------------------------------
+            const uint32_t idesc = idesc_mxf4(2 * BM, BN);
+            const uint64_t a_desc = sw128_operand(sA, 16u), b_desc = sw128_operand(sB, 16u);
+            const uint64_t sfa_desc = scale_desc(sSFA), sfb_desc = scale_desc(sSFB);
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, aphase = 0, cphase = 0, slot = 0;
+            bool ok = true;
+            for (long long i = unit; ok && i < tiles; i += nunits) {
+                // this accumulator's last tile is out, and of the other's tile the shared columns
+                if (!wait_bounded(tempty_bar(acc), aphase ^ 1u, abort_flag, args.err, args.timeout_ns) ||
+                    !wait_bounded(shared_bar, cphase ^ 1u, abort_flag, args.err, args.timeout_ns))
+                    break;
+                cphase ^= 1u;
+                tc_fence_after();
+                const uint32_t d = tmem_base + (acc ? ACC1_COL : 0u);
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!wait_bounded(full_bar(stage), phase, abort_flag, args.err, args.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t sf = tmem_base + SF_COL + SF_COLS * slot;
+                        const uint64_t sa = sfa_desc + (uint32_t)(stage * (SF_BYTES >> 4));
+                        const uint64_t sb = sfb_desc + (uint32_t)(stage * (SFB_BYTES >> 4));
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            copy_scales<true>(sf + 4u * q, sa + (uint32_t)(q * (QUAD_BYTES >> 4)));
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                copy_scales<true>(sf + 8u + 8u * q + 4u * h, sb + (uint32_t)((2 * h + q) * (QUAD_BYTES >> 4)));
+                        }
+                        const uint64_t a = a_desc + (uint32_t)(stage * (A_BYTES >> 4));
+                        const uint64_t b = b_desc + (uint32_t)(stage * (B_BYTES >> 4));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            umma_mxf4<true>(d, a + 2u * k, b + 2u * k, with_scale_id(idesc, 2u * (k & 1)), sf + 4u * (k >> 1),
+                                            sf + 8u + 8u * (k >> 1), (kb | k) != 0 ? 1u : 0u);
+                        umma_commit_pair_mc(empty_bar(stage), (uint16_t)0x3);
+                    }
+                    __syncwarp();
+                    slot ^= 1u;
+                    if (++stage == STAGES) stage = 0, phase ^= 1u;
+                }
+                if (!ok) break;
+                if (elect_one()) umma_commit_pair_mc(tfull_bar(acc), (uint16_t)0x3);
+                __syncwarp();
+                acc ^= 1;
+                if (acc == 0) aphase ^= 1u;
+            }
+        } else if (warp == 2) {
+            // ------------------------------ scales of x -------------------------------
+            // two k-blocks ahead: their words are loaded while these are written
+            const int groups = (kblocks + 1) / 2;
+            auto load = [&](const Tile& tl, int g) {
+                RowScales r;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int m = BM * (int)rank + 32 * j + lane;
+                    r.w[j] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    if (m < tl.r.rows) r.w[j] = load_scales(args.xs + (tl.r.at + m * args.step) * args.xs_ld, g, args.nb);
+                }
+                return r;
+            };
+            int stage = 0, g = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            long long i = unit;
+            Tile tl{};
+            RowScales now{};
+            if (i < tiles) tl = tile_of<EXPERTS>(i, args), now = load(tl, 0);
+            while (ok && i < tiles) {
+                const int kb = 2 * g;
+                if (++g == groups) {
+                    g = 0, i += nunits;
+                    if (i < tiles) tl = tile_of<EXPERTS>(i, args);
+                }
+                RowScales next{};
+                if (i < tiles) next = load(tl, g);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (kb + h >= kblocks) break;
+                    if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    now.store(sSFA + stage * SF_BYTES, h, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_pair(mapa_shared(full_bar(stage), 0));
+                    if (++stage == STAGES) stage = 0, phase ^= 1u;
+                }
+                now = next;
             }
         }
+    } else {
+        // ------------------------------ epilogue --------------------------------------
+        regs_inc<REGS_EPI>();
+        const int quad = warp & 3, part = (warp - 4) >> 2;       // 32 rows, 64 columns
+        const uint32_t stage = sEpi + (uint32_t)(warp - 4) * STAGING;
+        const uint32_t shared_leader = mapa_shared(shared_bar, 0);
+        uint32_t phase = 0;
+        int acc = 0;
+        for (long long i = unit; i < tiles; i += nunits) {
+            const Tile tl = tile_of<EXPERTS>(i, args);
+            const int m_warp = BM * (int)rank + 32 * quad, n = tl.n0 + COLS * part;
+            const int rows = n < args.N ? min(32, tl.r.rows - m_warp) : 0;    // this warp's rows that exist (may be negative)
+            const long long row = tl.r.at + m_warp * args.step;
+            if (args.bias) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c = n + 32 * h + lane;
+                    const float b = c < args.N ? __ldg(args.bias + (size_t)tl.r.g * args.N + c) : 0.f;
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage + 128u * h + 4u * lane), "f"(b) : "memory");
+                }
+                __syncwarp();
+            }
+            if (!wait_bounded(tfull_bar(acc), phase, abort_flag, args.err, args.timeout_ns)) break;
+            tc_fence_after();
+            // A thread's columns come out at once, so the accumulator is free again long
+            // before the epilogue is done; the 64 columns that the other accumulator
+            // shares are the last of accumulator 0 and the first of 1.
+            uint32_t r[2][32];
+            const uint32_t tcol =
+                tmem_base + ((uint32_t)(32 * quad) << 16) + (acc ? ACC1_COL : 0u) + (uint32_t)(COLS * part);
+            tmem_ld32_nowait(tcol, r[0]);
+            tmem_ld32_nowait(tcol + 32u, r[1]);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (part == (acc ? 0 : 3)) mbar_arrive_pair(shared_leader);
+                mbar_arrive_pair(mapa_shared(tempty_bar(acc), 0));
+            }
+            acc ^= 1;
+            if (acc == 0) phase ^= 1u;
+            float v[COLS];
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) v[c] = __uint_as_float(r[c >> 5][c & 31]);
+            if (args.bias) {                             // brought to the staging before the tile was waited for
+#pragma unroll
+                for (int c = 0; c < COLS / 4; ++c) {
+                    float4 q;
+                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
+                                 : "r"(stage + 16u * c));
+                    f2_unpack(f2_add(f2_pack(v[4 * c], v[4 * c + 1]), f2_pack(q.x, q.y)), v[4 * c], v[4 * c + 1]);
+                    f2_unpack(f2_add(f2_pack(v[4 * c + 2], v[4 * c + 3]), f2_pack(q.z, q.w)), v[4 * c + 2], v[4 * c + 3]);
+                }
+                __syncwarp();
+            }
+            if constexpr (EPI == FP4_OUT_BF16) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) save_piece<__nv_bfloat16>(v + 32 * h, args, row, n + 32 * h, rows, lane, stage);
+            } else if constexpr (EPI == FP4_OUT_F32) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) save_piece<float>(v + 16 * h, args, row, n + 16 * h, rows, lane, stage);
+            } else if (lane < rows) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (n + 32 * h >= args.N) break;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) v[32 * h + c] = fp8_gelu(v[32 * h + c]);
+                    save_block(v + 32 * h, args.o, row + lane * args.step, n + 32 * h);
+                }
+            }
+            __syncwarp();
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();    // no CTA leaves while its peer may still touch its memory
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
     }
 }
 
-}  // namespace
+template <int EPI, bool EXPERTS>
+cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& ms, const Args& a, int num_sms,
+                cudaStream_t s) {
+    auto k = fp4_product_kernel<EPI, EXPERTS>;
+    cudaError_t e = smem_attr_once((const void*)k, SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    const long long pairs = num_sms / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * (!EXPERTS && a.units < pairs ? a.units : pairs)));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k, mx, mw, ms, a);
+}
+template <int EPI>
+cudaError_t run_for(bool experts, const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& ms, const Args& a,
+                    int num_sms, cudaStream_t s) {
+    return experts ? run<EPI, true>(mx, mw, ms, a, num_sms, s) : run<EPI, false>(mx, mw, ms, a, num_sms, s);
+}
+
+}  // namespace f4
 
 cudaError_t launch_fp4_product(const Fp4Product& p, const Fp8Device& dev, cudaStream_t s) {
-    const long long rows = p.tiles ? p.n : (long long)p.B * p.G;
-    const dim3 grid((unsigned)((p.N + kThreads - 1) / kThreads), (unsigned)(rows < 4096 ? (rows ? rows : 1) : 4096));
+    using namespace f4;
+    RM_HOST_BOUNDS(p.B >= 1 && p.G >= 1 && p.K >= 1 && p.N >= 1 && p.n >= 1 && fp4_holds(p.x, p.K));
+    RM_HOST_BOUNDS(fp8_on(p.w.codes, 16) && fp8_on(p.w.scales, 16) && p.w.lds == fp4_weight_quads(p.K) &&
+                   p.w.ld % 16 == 0 && p.w.ld >= 16 * fp4_blocks(p.K) && (!p.bias || fp8_on(p.bias, 16)));
+    RM_HOST_BOUNDS(p.epi == FP4_GELU ? p.N % 32 == 0 && fp4_holds(p.o, p.N) : fp8_on(p.y, 16));
+    if (p.B <= kFp4StreamMaxB) return launch_fp4_stream(p, dev, s);
+    Args a{};
+    a.B = p.B, a.G = p.G, a.K = p.K, a.N = p.N;
+    a.m_tiles = (p.B + 2 * BM - 1) / (2 * BM);
+    a.n_tiles = (p.N + BN - 1) / BN;
+    a.kblocks = (p.K + BK - 1) / BK;
+    a.nb = (int)fp4_blocks(p.K);
+    a.table = p.tiles;
+    a.units = (long long)p.G * a.m_tiles * a.n_tiles;
+    a.n = p.n;
+    a.step = p.tiles ? 1 : p.G;
+    a.xs = p.x.scales, a.xs_ld = p.x.lds;
+    a.bias = p.bias;
+    a.y = p.y;
+    a.vec = p.N % (p.epi == FP4_OUT_F32 ? 4 : 8) == 0;
+    a.o = p.o;
+    a.err = dev.err;
+    a.timeout_ns = dev.timeout_ns;
+    const auto u8t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const long long wide = 16ll * a.nb, tiles = (p.N + kFp4TileRows - 1) / kFp4TileRows;
+    CUtensorMap mx, mw, ms;
+    const bool ok =
+        (p.tiles ? fp8_tensor_map(&mx, u8t, p.x.codes, wide, p.n, 1, p.x.ld, p.x.ld, 128, BM)
+                 : fp8_tensor_map(&mx, u8t, p.x.codes, wide, p.B, p.G, p.G * p.x.ld, p.x.ld, 128, BM)) &&
+        fp8_tensor_map(&mw, u8t, p.w.codes, wide, p.N, p.G, p.w.ld, p.N * p.w.ld, 128, BN / 2) &&
+        fp8_tensor_map(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT32, p.w.scales, p.w.lds * (QUAD_BYTES / 4), tiles, p.G,
+                       p.w.lds * QUAD_BYTES, tiles * p.w.lds * QUAD_BYTES, SF_BYTES / 4, 2, true);
+    if (!ok) return cudaErrorInvalidValue;
     switch (p.epi) {
-        case FP4_OUT_BF16: return launch_k(product_kernel<FP4_OUT_BF16>, grid, dim3(kThreads), 0, s, p, rows);
-        case FP4_OUT_F32: return launch_k(product_kernel<FP4_OUT_F32>, grid, dim3(kThreads), 0, s, p, rows);
-        case FP4_GELU: return launch_k(product_kernel<FP4_GELU>, grid, dim3(kThreads), 0, s, p, rows);
+        case FP4_OUT_BF16: return run_for<FP4_OUT_BF16>(p.tiles != nullptr, mx, mw, ms, a, dev.num_sms, s);
+        case FP4_OUT_F32: return run_for<FP4_OUT_F32>(p.tiles != nullptr, mx, mw, ms, a, dev.num_sms, s);
+        case FP4_GELU: return run_for<FP4_GELU>(p.tiles != nullptr, mx, mw, ms, a, dev.num_sms, s);
     }
     return cudaErrorNotSupported;
 }

@@ -604,15 +604,17 @@ bool get_encoder() {
 }  // namespace f8
 
 bool fp8_tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, long long inner, long long rows,
-                    long long groups, long long row_bytes, long long group_bytes, int box_inner, int box_rows) {
+                    long long groups, long long row_bytes, long long group_bytes, int box_inner, int box_rows,
+                    bool plain) {
     if (!f8::get_encoder()) return false;
     cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)groups};
     cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)group_bytes};
     cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1u};
     cuuint32_t estr[3] = {1, 1, 1};
     return f8::g_encode(m, type, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        box_inner == 64 && type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                                                 : CU_TENSOR_MAP_SWIZZLE_128B,
+                        plain ? CU_TENSOR_MAP_SWIZZLE_NONE
+                        : box_inner == 64 && type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                                                   : CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -9,9 +9,11 @@ namespace rm {
 
 // 3-D tensor map {inner, rows, groups} with boxes of box_inner x box_rows
 // elements (128 bytes wide with the 128-byte swizzle, or 64 bytes of codes with
-// the 64-byte one); what lies outside reads as zero and is not written.
+// the 64-byte one; plain: of any width, as they lie); what lies outside reads as
+// zero and is not written.
 bool fp8_tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, long long inner, long long rows,
-                    long long groups, long long row_bytes, long long group_bytes, int box_inner, int box_rows);
+                    long long groups, long long row_bytes, long long group_bytes, int box_inner, int box_rows,
+                    bool plain = false);
 
 // Operand tile of 128-byte rows written by TMA with the 128-byte swizzle
 // (layout type 2, descriptor version 1), base 1024-byte aligned.  K-major: a row
