@@ -12,8 +12,7 @@
 //                tensor cores' order, those of all 256 columns in both CTAs)
 //   warp 1       MMA issuer (the even CTA's): six copies of exponent bytes to tensor
 //                memory and four MMAs a k-block
-//   warp 2       x's exponent bytes (rows may start anywhere, so they lie row by
-//                row): 16 bytes a row are two k-blocks', turned in registers
+//   warp 2       x's exponent bytes (RowScales)
 //   warps 4-19   epilogue: each thread owns 64 columns of one row, so that a block of
 //                32 of a 4-bit output is one thread's
 // Tensor memory (512 columns): two accumulators of 256 columns that share 64, at
@@ -44,7 +43,8 @@ constexpr uint32_t ACC1_COL = 192;       // the second accumulator's first colum
 constexpr uint32_t SF_COL = 448, SF_COLS = 24;
 // registers: 640 threads launched with 96; 128 x 64 + 512 x 104 = 640 x 96
 constexpr int REGS_OTHER = 64, REGS_EPI = 104;
-constexpr int SMEM_BYTES = 1024 + STAGES * (STAGE_BYTES + SF_BYTES + SFB_BYTES) + EPI_WARPS * STAGING + 256;
+using Scales = RowScales<BM, 8>;
+constexpr int SMEM_BYTES = 1024 + STAGES * (STAGE_BYTES + SF_BYTES + SFB_BYTES) + EPI_WARPS * STAGING + Scales::BYTES + 256;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 
 struct Args {
@@ -142,7 +142,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     const uint32_t sA = base, sB = base + STAGES * A_BYTES;
     const uint32_t sSFA = base + STAGES * STAGE_BYTES, sSFB = sSFA + STAGES * SF_BYTES;
     const uint32_t sEpi = sSFB + STAGES * SFB_BYTES;
-    const uint32_t bar0 = sEpi + EPI_WARPS * STAGING;
+    const uint32_t sRing = sEpi + EPI_WARPS * STAGING, bar0 = sRing + Scales::BYTES;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
     auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + x); };
@@ -267,48 +267,45 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             }
         } else if (warp == 2) {
             // ------------------------------ scales of x -------------------------------
-            // two k-blocks ahead: their words are loaded while these are written
             const int groups = (kblocks + 1) / 2;
-            auto load = [&](const Tile& tl, int g) {
-                RowScales r;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int m = BM * (int)rank + 32 * j + lane;
-                    r.w[j] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
-                    if (m < tl.r.rows) r.w[j] = load_scales(args.xs + (tl.r.at + m * args.step) * args.xs_ld, g, args.nb);
-                }
-                return r;
-            };
-            int stage = 0, g = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            long long i = unit;
+            Scales sc(sRing);
+            long long i = unit;                          // of the next step to fetch
+            int g = 0;
             Tile tl{};
-            RowScales now{};
-            if (i < tiles) tl = tile_of<EXPERTS>(i, args), now = load(tl, 0);
-            while (ok && i < tiles) {
-                const int kb = 2 * g;
+            if (i < tiles) tl = tile_of<EXPERTS>(i, args);
+            auto fetch = [&]() {
+                if (i >= tiles) return sc.done();
+                const int m0 = BM * (int)rank;
+                sc.fetch(args.xs + (tl.r.at + m0 * args.step) * args.xs_ld, args.step * args.xs_ld, tl.r.rows - m0, g, lane);
                 if (++g == groups) {
                     g = 0, i += nunits;
                     if (i < tiles) tl = tile_of<EXPERTS>(i, args);
                 }
-                RowScales next{};
-                if (i < tiles) next = load(tl, g);
+            };
+#pragma unroll 1
+            for (int d = 0; d < Scales::STEPS; ++d) fetch();
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (long long j = unit; ok && j < tiles; j += nunits)
+                for (int kb = 0; ok && kb < kblocks; kb += 2) {
+                    sc.take(kb / 2, args.nb, lane);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (kb + h >= kblocks) break;
-                    if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
-                        ok = false;
-                        break;
+                    for (int h = 0; h < 2; ++h) {
+                        if (kb + h >= kblocks) break;
+                        if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        sc.store(sSFA + stage * SF_BYTES, h, lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_pair(mapa_shared(full_bar(stage), 0));
+                        if (++stage == STAGES) stage = 0, phase ^= 1u;
                     }
-                    now.store(sSFA + stage * SF_BYTES, h, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_pair(mapa_shared(full_bar(stage), 0));
-                    if (++stage == STAGES) stage = 0, phase ^= 1u;
+                    fetch();
                 }
-                now = next;
-            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else {
         // ------------------------------ epilogue --------------------------------------

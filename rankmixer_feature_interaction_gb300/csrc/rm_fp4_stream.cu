@@ -7,7 +7,7 @@
 // stage 16 KB of W's codes, 1 KB of its exponent bytes and NB rows of x.
 //   warp 0       TMA producer of W: codes, and exponent bytes as they lie
 //   warp 1       MMA issuer (tcgen05.mma kind::mxf4, M = 128, N = NB, one CTA)
-//   warp 2       x's exponent bytes (as in rm_fp4_gemm.cu)
+//   warp 2       x's exponent bytes (RowScales)
 //   warp 3       TMA producer of x's codes
 //   warps 4-7 (to 11 for more than 16 rows, to 19 for more than 64)  epilogue: a
 //                thread owns one column n of 16 or 32 rows; a block of 32 columns of a
@@ -34,13 +34,14 @@ template <int NB>
 struct Cfg {
     static constexpr int X_BYTES = NB * 128;
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + 2 * SF_BYTES;
-    static constexpr int FIT = (220 * 1024) / STAGE_BYTES;
+    using Scales = RowScales<NB, 8>;
+    static constexpr int FIT = (225 * 1024 - Scales::BYTES) / STAGE_BYTES;
     static constexpr int STAGES = FIT < 12 ? FIT : 12;
     static constexpr int EPI_WARPS = NB == 16 ? 4 : NB == 128 ? 16 : 8;
     static constexpr int TMEM_COLS = NB == 128 ? 512 : 256, SF_COL = 2 * NB;
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     static constexpr int ROWS = NB / (EPI_WARPS / 4);               // per epilogue thread
-    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 512;
+    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + Scales::BYTES + 512;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
     static_assert(SF_COL + 32 <= TMEM_COLS, "two accumulators and two slots of exponent bytes");
 };
@@ -102,7 +103,7 @@ fp4_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
     uint8_t* base_ptr = smem_raw + (base - raw_addr);
     const uint32_t sW = base, sX = sW + STAGES * W_BYTES, sSFW = sX + STAGES * C::X_BYTES, sSFX = sSFW + STAGES * SF_BYTES;
-    const uint32_t bar0 = sSFX + STAGES * SF_BYTES;
+    const uint32_t sRing = sSFX + STAGES * SF_BYTES, bar0 = sRing + C::Scales::BYTES;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
     auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + x); };
@@ -218,47 +219,43 @@ fp4_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     } else if (warp == 2) {
         // ------------------------------ scales of x -------------------------------
         const int groups = (kblocks + 1) / 2;
-        auto load = [&](const Tile& tl, int g) {
-            RowScales r;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                r.w[j] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
-                const int m = 32 * j + lane;
-                if (32 * j < NB && m < tl.r.rows)
-                    r.w[j] = load_scales(args.xs + (tl.r.at + m * args.step) * args.xs_ld, g, args.nb);
-            }
-            return r;
-        };
-        int stage = 0, g = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        long long i = blockIdx.x;
+        typename C::Scales sc(sRing);
+        long long i = blockIdx.x;                        // of the next step to fetch
+        int g = 0;
         Tile tl{};
-        RowScales now{};
-        if (i < tiles) tl = tile_of<EXPERTS>(i, args), now = load(tl, 0);
-        while (ok && i < tiles) {
-            const int kb = 2 * g;
+        if (i < tiles) tl = tile_of<EXPERTS>(i, args);
+        auto fetch = [&]() {
+            if (i >= tiles) return sc.done();
+            sc.fetch(args.xs + tl.r.at * args.xs_ld, args.step * args.xs_ld, tl.r.rows, g, lane);
             if (++g == groups) {
                 g = 0, i += units;
                 if (i < tiles) tl = tile_of<EXPERTS>(i, args);
             }
-            RowScales next{};
-            if (i < tiles) next = load(tl, g);
+        };
+#pragma unroll 1
+        for (int d = 0; d < C::Scales::STEPS; ++d) fetch();
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (long long j = blockIdx.x; ok && j < tiles; j += units)
+            for (int kb = 0; ok && kb < kblocks; kb += 2) {
+                sc.take(kb / 2, args.nb, lane);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (kb + h >= kblocks) break;
-                if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
-                    ok = false;
-                    break;
+                for (int h = 0; h < 2; ++h) {
+                    if (kb + h >= kblocks) break;
+                    if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    sc.store(sSFX + stage * SF_BYTES, h, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full_bar(stage));
+                    if (++stage == STAGES) stage = 0, phase ^= 1u;
                 }
-                now.store(sSFX + stage * SF_BYTES, h, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full_bar(stage));
-                if (++stage == STAGES) stage = 0, phase ^= 1u;
+                fetch();
             }
-            now = next;
-        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         // ------------------------------ epilogue ----------------------------------
         constexpr int NS = C::ROWS;
