@@ -12,7 +12,7 @@
 //                tensor cores' order, those of all 256 columns in both CTAs)
 //   warp 1       MMA issuer (the even CTA's): six copies of exponent bytes to tensor
 //                memory and four MMAs a k-block
-//   warp 2       x's exponent bytes (RowScales)
+//   warps 2, 3   x's exponent bytes (RowScales), every other step of two k-blocks
 //   warps 4-19   epilogue: each thread owns 64 columns of one row, so that a block of
 //                32 of a 4-bit output is one thread's
 // Tensor memory (512 columns): two accumulators of 256 columns that share 64, at
@@ -38,13 +38,16 @@ constexpr int STAGES = 5;
 constexpr int EPI_WARPS = 16;
 constexpr int COLS = 64;                 // columns per epilogue warp
 constexpr int STAGING = 2048;            // per epilogue warp: 32 rows of 64 bytes
+constexpr int BIAS_BYTES = COLS * 4;     // per epilogue warp
+constexpr int SF_OUT_BYTES = 4 * 2 * 256;  // exponent bytes of a 4-bit output: four quarters, two buffers
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr uint32_t ACC1_COL = 192;       // the second accumulator's first column
 constexpr uint32_t SF_COL = 448, SF_COLS = 24;
 // registers: 640 threads launched with 96; 128 x 64 + 512 x 104 = 640 x 96
 constexpr int REGS_OTHER = 64, REGS_EPI = 104;
-using Scales = RowScales<BM, 8>;
-constexpr int SMEM_BYTES = 1024 + STAGES * (STAGE_BYTES + SF_BYTES + SFB_BYTES) + EPI_WARPS * STAGING + Scales::BYTES + 256;
+using Scales = RowScales<BM, 3>;        // of each of the two warps
+constexpr int SMEM_BYTES = 1024 + STAGES * (STAGE_BYTES + SF_BYTES + SFB_BYTES) + EPI_WARPS * (STAGING + BIAS_BYTES) +
+                           2 * Scales::BYTES + SF_OUT_BYTES + 256;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 
 struct Args {
@@ -88,11 +91,20 @@ __device__ __forceinline__ Tile tile_of(long long i, const Args& a) {
     return t;
 }
 
-// 64 bytes of each row of Y from column n on.
-template <typename OUT>
-__device__ __forceinline__ void save_piece(const float* v, const Args& a, long long row, int n, int rows, int lane,
-                                           uint32_t stage) {
+// The staging is free again: what was written from it before has been read.
+__device__ __forceinline__ void staging_free(int lane) {
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+}
+
+// 64 bytes of each row of Y from column n on, through the staging: 32 existing rows by
+// TMA (which clips what lies outside Y), the last rows of an expert, whose neighbours
+// are another's, and unaligned ones by plain stores.  y: the warp's first row in tmY.
+template <typename OUT, bool EXPERTS>
+__device__ __forceinline__ void save_piece(const float* v, const Args& a, const CUtensorMap* tmY, int y, int plane,
+                                           long long row, int n, int rows, int lane, uint32_t stage) {
     constexpr int E = sizeof(OUT);
+    staging_free(lane);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         if constexpr (E == 2)
@@ -103,6 +115,16 @@ __device__ __forceinline__ void save_piece(const float* v, const Args& a, long l
             st_shared_v4(staged_at(stage, lane, c), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
                          __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
     }
+    if (n >= a.N) return;
+    if (a.vec && (!EXPERTS || rows >= 32)) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(tmY, stage, n * E, y, plane);
+            bulk_commit_group();
+        }
+        return;
+    }
     char* dst = reinterpret_cast<char*>(a.y) + (row * (long long)a.N + n) * E;
     const size_t pitch = (size_t)a.step * (size_t)a.N * E;
     const int bytes = min(a.N - n, 64) * E;            // the row's rest may be more bytes than fit 32 bits
@@ -112,14 +134,13 @@ __device__ __forceinline__ void save_piece(const float* v, const Args& a, long l
         store_rows<false, E>(stage, dst, pitch, rows, bytes, lane);
 }
 
-// 32 columns of this thread's row in 4 bits.
-__device__ __forceinline__ void save_block(const float* v, const Fp4View& o, long long row, int n) {
+// 32 columns of this thread's row in 4 bits: 16 bytes of codes; E: the exponent byte.
+__device__ __forceinline__ void round_block(const float* v, uint32_t (&w)[4], uint32_t& E) {
     float m[2] = {};
 #pragma unroll
     for (int i = 0; i < 32; i += 2) m[i >> 1 & 1] = max3_nan(m[i >> 1 & 1], fabsf(v[i]), fabsf(v[i + 1]));
-    const uint32_t E = fp4_exponent(fp4_abs_bits(max3_nan(m[0], m[0], m[1])));
+    E = fp4_exponent(fp4_abs_bits(max3_nan(m[0], m[0], m[1])));
     const uint64_t s = f2_splat(fp4_inv_scale(E));
-    uint32_t w[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         float q[8];
@@ -127,14 +148,54 @@ __device__ __forceinline__ void save_block(const float* v, const Fp4View& o, lon
         for (int i = 0; i < 8; i += 2) f2_unpack(f2_mul(f2_pack(v[8 * c + i], v[8 * c + i + 1]), s), q[i], q[i + 1]);
         w[c] = fp4_pack8(q);
     }
-    *reinterpret_cast<uint4*>(o.codes + row * o.ld + n / 2) = make_uint4(w[0], w[1], w[2], w[3]);
-    o.scales[row * o.lds + n / kFp4Block] = (uint8_t)E;
+}
+
+// A 4-bit output leaves by four warps together, those of the same 32 rows: 128 bytes of
+// codes a row (256 columns) and 8 exponent bytes.  A thread that stored its own 16
+// bytes and its byte made every store 32 requests of part of a sector: the FFN at B =
+// 2048 took 684 us with that.  The staging of the four warps is two buffers of 32
+// rows, used in turn: the codes as TMA takes them with the 128-byte swizzle, and the
+// exponent bytes, a row's eight together.
+constexpr int CODE_BYTES = 32 * 128;
+static_assert(2 * CODE_BYTES <= 4 * STAGING, "two buffers of codes in the staging");
+
+// 32 rows of a tile's 256 columns out of the buffers, by one warp.
+template <bool EXPERTS>
+__device__ __forceinline__ void save_four(const Args& a, const CUtensorMap* tmY, const Tile& tl, int m_warp, long long row,
+                                          uint32_t codes, uint32_t bytes, int lane) {
+    const int rows = min(32, tl.r.rows - m_warp);                            // may be negative
+    const int left = (a.N - tl.n0) / kFp4Block;                              // blocks of the rows from n0 on
+    if (rows <= 0) return;
+    if (!EXPERTS || rows == 32) {
+        if (lane == 0) {
+            tma_store_3d(tmY, codes, tl.n0 / 2, tl.r.row + m_warp, tl.r.plane);
+            bulk_commit_group();
+        }
+    } else {                                                                 // an expert's last rows
+        for (int r = lane >> 3; r < rows; r += 4) {
+            const int c = lane & 7;
+            if (c < left) {
+                const uint4 q = ld_shared_u4(codes + 128u * r + 16u * (uint32_t)(c ^ (r & 7)));
+                *reinterpret_cast<uint4*>(a.o.codes + (row + r) * a.o.ld + tl.n0 / 2 + 16 * c) = q;
+            }
+        }
+    }
+    if (lane < rows) {
+        uint32_t w[2];
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(bytes + 8u * lane));
+        uint8_t* p = a.o.scales + (row + lane * a.step) * a.o.lds + tl.n0 / kFp4Block;
+        if (left >= 8) {                                                     // lds is a multiple of 16, n0 of 256
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        } else {
+            for (int b = 0; b < left; ++b) p[b] = (uint8_t)(w[b >> 2] >> (8 * (b & 3)));
+        }
+    }
 }
 
 template <int EPI, bool EXPERTS>
 __global__ void __launch_bounds__(THREADS, 1)
 fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                   const __grid_constant__ CUtensorMap tmS, const Args args) {
+                   const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmY, const Args args) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -142,13 +203,14 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     const uint32_t sA = base, sB = base + STAGES * A_BYTES;
     const uint32_t sSFA = base + STAGES * STAGE_BYTES, sSFB = sSFA + STAGES * SF_BYTES;
     const uint32_t sEpi = sSFB + STAGES * SFB_BYTES;
-    const uint32_t sRing = sEpi + EPI_WARPS * STAGING, bar0 = sRing + Scales::BYTES;
+    const uint32_t sBias = sEpi + EPI_WARPS * STAGING, sRing = sBias + EPI_WARPS * BIAS_BYTES, sOut = sRing + 2 * Scales::BYTES, bar0 = sOut + SF_OUT_BYTES;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
     auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + x); };
     auto tempty_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 + x); };
     const uint32_t shared_bar = bar0 + 8u * (2 * STAGES + 4);
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (shared_bar + 8u - base));
+    auto meet_bar = [&](int q) { return shared_bar + 8u + 8u * q; };
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (meet_bar(4) - base));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -167,6 +229,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             mbar_init(tfull_bar(x), 1);              // multicast commit
             mbar_init(tempty_bar(x), 2 * EPI_WARPS); // the even CTA's: every epilogue warp of both CTAs
         }
+        for (int q = 0; q < 4; ++q) mbar_init(meet_bar(q), 4);
         mbar_init(shared_bar, 2 * EPI_WARPS / 4);    // the even CTA's: the warps that own the shared columns
         *abort_flag = 0;
         fence_mbar_init();
@@ -265,30 +328,42 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                 acc ^= 1;
                 if (acc == 0) aphase ^= 1u;
             }
-        } else if (warp == 2) {
+        } else if (warp >= 2) {
             // ------------------------------ scales of x -------------------------------
             const int groups = (kblocks + 1) / 2;
-            Scales sc(sRing);
+            Scales sc(sRing + (warp - 2) * Scales::BYTES);
             long long i = unit;                          // of the next step to fetch
             int g = 0;
             Tile tl{};
-            if (i < tiles) tl = tile_of<EXPERTS>(i, args);
-            auto fetch = [&]() {
-                if (i >= tiles) return sc.done();
-                const int m0 = BM * (int)rank;
-                sc.fetch(args.xs + (tl.r.at + m0 * args.step) * args.xs_ld, args.step * args.xs_ld, tl.r.rows - m0, g, lane);
+            auto skip = [&]() {
                 if (++g == groups) {
                     g = 0, i += nunits;
                     if (i < tiles) tl = tile_of<EXPERTS>(i, args);
                 }
             };
+            auto fetch = [&]() {
+                if (i >= tiles) return sc.done();
+                const int m0 = BM * (int)rank;
+                sc.fetch(args.xs + (tl.r.at + m0 * args.step) * args.xs_ld, args.step * args.xs_ld, tl.r.rows - m0, g, lane);
+                skip();
+                if (i < tiles) skip();
+            };
+            if (i < tiles) {
+                tl = tile_of<EXPERTS>(i, args);
+                if (warp == 3) skip();
+            }
 #pragma unroll 1
             for (int d = 0; d < Scales::STEPS; ++d) fetch();
             int stage = 0;
             uint32_t phase = 0;
-            bool ok = true;
+            bool ok = true, mine = warp == 2;
             for (long long j = unit; ok && j < tiles; j += nunits)
-                for (int kb = 0; ok && kb < kblocks; kb += 2) {
+                for (int kb = 0; ok && kb < kblocks; kb += 2, mine = !mine) {
+                    if (!mine) {
+                        stage += min(2, kblocks - kb);
+                        if (stage >= STAGES) stage -= STAGES, phase ^= 1u;
+                        continue;
+                    }
                     sc.take(kb / 2, args.nb, lane);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -311,9 +386,11 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
         // ------------------------------ epilogue --------------------------------------
         regs_inc<REGS_EPI>();
         const int quad = warp & 3, part = (warp - 4) >> 2;       // 32 rows, 64 columns
-        const uint32_t stage = sEpi + (uint32_t)(warp - 4) * STAGING;
+        const uint32_t stage = sEpi + (uint32_t)(warp - 4) * STAGING, bias = sBias + (uint32_t)(warp - 4) * BIAS_BYTES;
         const uint32_t shared_leader = mapa_shared(shared_bar, 0);
-        uint32_t phase = 0;
+        // (GELU) the four warps' buffers: codes, exponent bytes
+        const uint32_t out = sEpi + (uint32_t)quad * (4 * STAGING), sf_out = sOut + (uint32_t)quad * 512u;
+        uint32_t phase = 0, turn = 0, meet = 0;
         int acc = 0;
         for (long long i = unit; i < tiles; i += nunits) {
             const Tile tl = tile_of<EXPERTS>(i, args);
@@ -325,7 +402,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                 for (int h = 0; h < 2; ++h) {
                     const int c = n + 32 * h + lane;
                     const float b = c < args.N ? __ldg(args.bias + (size_t)tl.r.g * args.N + c) : 0.f;
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage + 128u * h + 4u * lane), "f"(b) : "memory");
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(bias + 128u * h + 4u * lane), "f"(b) : "memory");
                 }
                 __syncwarp();
             }
@@ -351,13 +428,13 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             float v[COLS];
 #pragma unroll
             for (int c = 0; c < COLS; ++c) v[c] = __uint_as_float(r[c >> 5][c & 31]);
-            if (args.bias) {                             // brought to the staging before the tile was waited for
+            if (args.bias) {                             // brought there before the tile was waited for
 #pragma unroll
                 for (int c = 0; c < COLS / 4; ++c) {
                     float4 q;
                     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                                  : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
-                                 : "r"(stage + 16u * c));
+                                 : "r"(bias + 16u * c));
                     f2_unpack(f2_add(f2_pack(v[4 * c], v[4 * c + 1]), f2_pack(q.x, q.y)), v[4 * c], v[4 * c + 1]);
                     f2_unpack(f2_add(f2_pack(v[4 * c + 2], v[4 * c + 3]), f2_pack(q.z, q.w)), v[4 * c + 2], v[4 * c + 3]);
                 }
@@ -365,21 +442,41 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             }
             if constexpr (EPI == FP4_OUT_BF16) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) save_piece<__nv_bfloat16>(v + 32 * h, args, row, n + 32 * h, rows, lane, stage);
+                for (int h = 0; h < 2; ++h)
+                    if (rows > 0)
+                        save_piece<__nv_bfloat16, EXPERTS>(v + 32 * h, args, &tmY, tl.r.row + m_warp, tl.r.plane, row,
+                                                           n + 32 * h, rows, lane, stage);
             } else if constexpr (EPI == FP4_OUT_F32) {
 #pragma unroll
-                for (int h = 0; h < 4; ++h) save_piece<float>(v + 16 * h, args, row, n + 16 * h, rows, lane, stage);
-            } else if (lane < rows) {
+                for (int h = 0; h < 4; ++h)
+                    if (rows > 0)
+                        save_piece<float, EXPERTS>(v + 16 * h, args, &tmY, tl.r.row + m_warp, tl.r.plane, row, n + 16 * h,
+                                                   rows, lane, stage);
+            } else {
+                const uint32_t codes = out + turn * CODE_BYTES, bytes = sf_out + turn * 256u;
+                uint32_t E[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (n + 32 * h >= args.N) break;
+                    uint32_t w[4];
 #pragma unroll
                     for (int c = 0; c < 32; ++c) v[32 * h + c] = fp8_gelu(v[32 * h + c]);
-                    save_block(v + 32 * h, args.o, row + lane * args.step, n + 32 * h);
+                    round_block(v + 32 * h, w, E[h]);
+                    st_shared_v4(codes + 128u * lane + 16u * (uint32_t)((2 * part + h) ^ (lane & 7)), w[0], w[1], w[2], w[3]);
                 }
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(bytes + 8u * lane + 2u * part), "h"((uint16_t)(E[0] | E[1] << 8))
+                             : "memory");
+                fence_proxy_async_smem();
+                if (part == 0 && lane == 0) bulk_wait_group_read<0>();       // the other buffer is free for the next tile
+                __syncwarp();
+                if (lane == 0) mbar_arrive(meet_bar(quad));
+                if (!wait_bounded(meet_bar(quad), meet, abort_flag, args.err, args.timeout_ns)) break;
+                meet ^= 1u;
+                if (part == 0) save_four<EXPERTS>(args, &tmY, tl, m_warp, row, codes, bytes, lane);
+                turn ^= 1u;
             }
             __syncwarp();
         }
+        if (lane == 0) bulk_wait_group<0>();
     }
 
     tc_fence_before();
@@ -392,7 +489,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
 }
 
 template <int EPI, bool EXPERTS>
-cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& ms, const Args& a, int num_sms,
+cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& ms, const CUtensorMap& my, const Args& a, int num_sms,
                 cudaStream_t s) {
     auto k = fp4_product_kernel<EPI, EXPERTS>;
     cudaError_t e = smem_attr_once((const void*)k, SMEM_BYTES);
@@ -412,12 +509,12 @@ cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap&
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k, mx, mw, ms, a);
+    return cudaLaunchKernelEx(&cfg, k, mx, mw, ms, my, a);
 }
 template <int EPI>
-cudaError_t run_for(bool experts, const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& ms, const Args& a,
-                    int num_sms, cudaStream_t s) {
-    return experts ? run<EPI, true>(mx, mw, ms, a, num_sms, s) : run<EPI, false>(mx, mw, ms, a, num_sms, s);
+cudaError_t run_for(bool experts, const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& ms, const CUtensorMap& my,
+                    const Args& a, int num_sms, cudaStream_t s) {
+    return experts ? run<EPI, true>(mx, mw, ms, my, a, num_sms, s) : run<EPI, false>(mx, mw, ms, my, a, num_sms, s);
 }
 
 }  // namespace f4
@@ -455,11 +552,20 @@ cudaError_t launch_fp4_product(const Fp4Product& p, const Fp8Device& dev, cudaSt
         fp8_tensor_map(&mw, u8t, p.w.codes, wide, p.N, p.G, p.w.ld, p.N * p.w.ld, 128, BN / 2) &&
         fp8_tensor_map(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT32, p.w.scales, p.w.lds * (QUAD_BYTES / 4), tiles, p.G,
                        p.w.lds * QUAD_BYTES, tiles * p.w.lds * QUAD_BYTES, SF_BYTES / 4, 2, true);
+    // what leaves by TMA, in bytes: 64 of 32 rows of Y, or 128 of 32 rows of codes
+    CUtensorMap my = mx;
+    const bool gelu = p.epi == FP4_GELU;
+    const long long bytes = gelu ? p.N / 2 : p.N * (p.epi == FP4_OUT_F32 ? 4ll : 2ll), pitch = gelu ? p.o.ld : bytes;
+    const void* dst = gelu ? p.o.codes : p.y;
+    if (ok && (gelu || a.vec) &&
+        !(p.tiles ? fp8_tensor_map(&my, u8t, dst, bytes, p.n, 1, pitch, pitch, gelu ? 128 : 64, 32)
+                  : fp8_tensor_map(&my, u8t, dst, bytes, p.B, p.G, p.G * pitch, pitch, gelu ? 128 : 64, 32)))
+        return cudaErrorInvalidValue;
     if (!ok) return cudaErrorInvalidValue;
     switch (p.epi) {
-        case FP4_OUT_BF16: return run_for<FP4_OUT_BF16>(p.tiles != nullptr, mx, mw, ms, a, dev.num_sms, s);
-        case FP4_OUT_F32: return run_for<FP4_OUT_F32>(p.tiles != nullptr, mx, mw, ms, a, dev.num_sms, s);
-        case FP4_GELU: return run_for<FP4_GELU>(p.tiles != nullptr, mx, mw, ms, a, dev.num_sms, s);
+        case FP4_OUT_BF16: return run_for<FP4_OUT_BF16>(p.tiles != nullptr, mx, mw, ms, my, a, dev.num_sms, s);
+        case FP4_OUT_F32: return run_for<FP4_OUT_F32>(p.tiles != nullptr, mx, mw, ms, my, a, dev.num_sms, s);
+        case FP4_GELU: return run_for<FP4_GELU>(p.tiles != nullptr, mx, mw, ms, my, a, dev.num_sms, s);
     }
     return cudaErrorNotSupported;
 }
