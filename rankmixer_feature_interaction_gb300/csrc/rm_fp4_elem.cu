@@ -1,11 +1,12 @@
 // Elementwise kernels of the 4-bit operators: rows and weights to 4 bits, rows back.
 //
-// Rows: four neighbouring lanes own a block of 32 values, eight each (16 bytes of
-// bf16), agree on its largest magnitude with two shuffles and write four bytes of
-// codes each, so a warp reads 512 bytes in a row and writes 128.  Rows that are not
-// 16-byte aligned are read (or written) an element at a time, neighbouring lanes
-// neighbouring elements, and change their order in a kilobyte of shared memory per
-// warp.  Bound by memory: 2.53 bytes a value from bf16.
+// Rows: two neighbouring lanes own a block of 32 values, 16 each (32 bytes of bf16),
+// agree on its largest magnitude with one shuffle and write eight bytes of codes each,
+// so a warp reads a kilobyte of bf16 in a row and writes 256 bytes.  What a thread has
+// loaded stays as it came until it is rounded: few registers, so many loads under way.
+// Rows that are not 16-byte aligned are read (or written) an element at a time,
+// neighbouring lanes neighbouring elements, and change their order in shared memory.
+// Bound by memory: 2.53 bytes a value from bf16.
 #include "rm_fp4.cuh"
 
 namespace rm {
@@ -23,32 +24,100 @@ __device__ __forceinline__ void split(unsigned long long id, bool small, unsigne
     }
 }
 
-// Aligned rows: `lanes` = 4 per block.
+// Row and piece of the running number that is `step` (dq rows and dr pieces) further.
+__device__ __forceinline__ void advance(unsigned long long& row, int& j, int dq, int dr, int n) {
+    row += dq, j += dr;
+    if (j >= n) j -= n, ++row;
+}
+
+// Sixteen values of a row as they lie in memory, zeros past its end.
+template <typename IN>
+struct Raw16 {
+    static constexpr int WORDS = 4 * sizeof(IN);
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const IN* __restrict__ p, int n) {
+        if (n >= 16) {
+#pragma unroll
+            for (int i = 0; i < WORDS / 4; ++i) {
+                const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+                w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                if constexpr (sizeof(IN) == 4) {
+                    w[i] = i < n ? __float_as_uint(p[i]) : 0u;
+                } else {
+                    w[i] = 2 * i < n ? __bfloat16_as_ushort(p[2 * i]) : 0u;
+                    if (2 * i + 1 < n) w[i] |= (uint32_t)__bfloat16_as_ushort(p[2 * i + 1]) << 16;
+                }
+            }
+        }
+    }
+    // float bits of the largest magnitude; infinities and NaN count as they are
+    __device__ __forceinline__ uint32_t amax_bits() const {
+        uint32_t m = 0;
+        if constexpr (sizeof(IN) == 2) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+            return max(m << 16, m & 0xffff0000u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) m = max(m, w[i] & 0x7fffffffu);
+            return m;
+        }
+    }
+    __device__ __forceinline__ uint32_t codes(int half, uint64_t scale) const {
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint64_t pair;
+            if constexpr (sizeof(IN) == 2) {
+                const uint32_t x = w[4 * half + i];
+                pair = f2_pack(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+            } else {
+                pair = f2_pack(__uint_as_float(w[8 * half + 2 * i]), __uint_as_float(w[8 * half + 2 * i + 1]));
+            }
+            f2_unpack(f2_mul(pair, scale), q[2 * i], q[2 * i + 1]);
+        }
+        return fp4_pack8(q);
+    }
+};
+
+template <typename IN>
+constexpr int kInFlight = sizeof(IN) == 2 ? 4 : 2;      // pieces of 16 values per thread
+
 template <typename IN>
 __global__ void __launch_bounds__(kThreads)
-quantize_kernel(const IN* __restrict__ X, unsigned long long pieces, int cols, int nb, long long ldx, Fp4View out) {
-    constexpr int UNROLL = sizeof(IN) == 2 ? 4 : 2;
+quantize_kernel(const IN* __restrict__ X, unsigned long long pieces, int cols, int nb, int dq, int dr, long long ldx,
+                Fp4View out) {
+    constexpr int UNROLL = kInFlight<IN>;
     pdl_wait();
     pdl_launch_next();
     const unsigned long long base = (unsigned long long)blockIdx.x * (kThreads * UNROLL) + threadIdx.x;
-    const bool small = pieces <= 0xffffffffull;
-    float v[UNROLL][8];
-    unsigned long long row[UNROLL];
-    int j[UNROLL];
+    unsigned long long row;
+    int j;
+    split(base, pieces <= 0xffffffffull, 2u * nb, row, j);
+    Raw16<IN> v[UNROLL];
+    unsigned long long at = row;
+    int k = j;
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-        const unsigned long long id = base + (unsigned long long)u * kThreads;
-        split(id < pieces ? id : pieces - 1, small, 4u * nb, row[u], j[u]);
-        fp4_load8<IN, true>(X + row[u] * ldx + 8 * j[u], cols - 8 * j[u], v[u]);
+        const bool there = base + (unsigned long long)u * kThreads < pieces;
+        v[u].load(X + at * ldx + 16 * k, there ? cols - 16 * k : 0);
+        advance(at, k, dq, dr, 2 * nb);
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-        uint32_t E;
-        const uint32_t c = fp4_round8(v[u], E);
+        uint32_t m = v[u].amax_bits();
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        const uint32_t E = fp4_exponent(m);
+        const uint64_t s = f2_splat(fp4_inv_scale(E));
         if (base + (unsigned long long)u * kThreads < pieces) {
-            *reinterpret_cast<uint32_t*>(out.codes + row[u] * out.ld + 4 * j[u]) = c;
-            if ((j[u] & 3) == 0) out.scales[row[u] * out.lds + (j[u] >> 2)] = (uint8_t)E;
+            *reinterpret_cast<uint2*>(out.codes + row * out.ld + 8 * j) = make_uint2(v[u].codes(0, s), v[u].codes(1, s));
+            if ((j & 1) == 0) out.scales[row * out.lds + (j >> 1)] = (uint8_t)E;
         }
+        advance(row, j, dq, dr, 2 * nb);
     }
 }
 
@@ -219,10 +288,11 @@ template <typename IN>
 cudaError_t quantize(const IN* X, long long rows, int cols, long long ldx, const Fp4View& out, cudaStream_t s) {
     const int nb = (int)fp4_blocks(cols);
     if (rows_aligned(X, ldx, sizeof(IN))) {
-        constexpr int PER = kThreads * (sizeof(IN) == 2 ? 4 : 2);
-        const unsigned long long pieces = 4ull * rows * nb, grid = (pieces + PER - 1) / PER;
+        constexpr int PER = kThreads * kInFlight<IN>;
+        const unsigned long long pieces = 2ull * rows * nb, grid = (pieces + PER - 1) / PER;
         if (grid > 0x7fffffffull) return cudaErrorNotSupported;
-        return launch_k(quantize_kernel<IN>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, pieces, cols, nb, ldx, out);
+        return launch_k(quantize_kernel<IN>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, pieces, cols, nb,
+                        kThreads / (2 * nb), kThreads % (2 * nb), ldx, out);
     }
     const int per_row = (cols + 255) / 256;
     const unsigned long long chunks = (unsigned long long)rows * per_row, grid = (chunks + kWarps - 1) / kWarps;
