@@ -134,6 +134,22 @@ __device__ __forceinline__ void save_piece(const float* v, const Args& a, const 
         store_rows<false, E>(stage, dst, pitch, rows, bytes, lane);
 }
 
+// fp8_gelu of two values, the polynomial in -|u| so that one constant sign serves both
+// it and the last step: 7 instead of 10 instructions a value.
+__device__ __forceinline__ void gelu2(float& a, float& b) {
+    const uint64_t u = f2_pack(a, b), x = u | 0x8000000080000000ull;
+    uint64_t p = f2_fma(x, f2_splat(9.30538079e-07f), f2_splat(4.20015094e-05f));
+    p = f2_fma(x, p, f2_splat(7.80347327e-04f));
+    p = f2_fma(x, p, f2_splat(8.01421981e-03f));
+    p = f2_fma(x, p, f2_splat(5.32146059e-02f));
+    p = f2_fma(x, p, f2_splat(-4.58957642e-01f));
+    p = f2_fma(x, p, f2_splat(1.15113652f));
+    p = f2_fma(x, p, f2_splat(-9.99999404e-01f));
+    float p0, p1;
+    f2_unpack(p, p0, p1);
+    f2_unpack(f2_fma(x, f2_pack(ex2_approx(p0), ex2_approx(p1)), f2_pack(fmaxf(a, 0.f), fmaxf(b, 0.f))), a, b);
+}
+
 // 32 columns of this thread's row in 4 bits: 16 bytes of codes; E: the exponent byte.
 __device__ __forceinline__ void round_block(const float* v, uint32_t (&w)[4], uint32_t& E) {
     float m[2] = {};
@@ -459,7 +475,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                 for (int h = 0; h < 2; ++h) {
                     uint32_t w[4];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) v[32 * h + c] = fp8_gelu(v[32 * h + c]);
+                    for (int c = 0; c < 32; c += 2) gelu2(v[32 * h + c], v[32 * h + c + 1]);
                     round_block(v + 32 * h, w, E[h]);
                     st_shared_v4(codes + 128u * lane + 16u * (uint32_t)((2 * part + h) ^ (lane & 7)), w[0], w[1], w[2], w[3]);
                 }
