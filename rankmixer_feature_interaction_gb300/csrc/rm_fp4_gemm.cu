@@ -53,7 +53,7 @@ static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 struct Args {
     int B, G, K, N;                      // rows of a group (per token), groups
     int m_tiles, n_tiles, kblocks, nb;
-    long long units;                     // tiles; experts: columns of tiles (times the table's length)
+    uint32_t units;                      // tiles (per token; experts: the table's length times n_tiles)
     const int4* table;                   // experts: the tiles of rows (null: per token)
     long long n;                         // experts: rows that exist
     long long step;                      // between rows of a group
@@ -67,28 +67,39 @@ struct Args {
     unsigned long long timeout_ns;
 };
 
+// Rows m0 .. of group g (per token: samples; experts: sorted rows), columns n0 ..
 struct Tile {
-    RowTile r;
-    int n0;
+    int g, m0, rows, n0;
 };
 // Per token, tiles of rows fastest: neighbouring pairs share W's columns, and a
 // token's x (which every tile of columns reads again) stays in L2.  Experts: columns
 // fastest, so that a tile of rows is read from memory once.
 template <bool EXPERTS>
-__device__ __forceinline__ Tile tile_of(long long i, const Args& a) {
+__device__ __forceinline__ Tile tile_of(uint32_t i, const Args& a) {
     Tile t;
     if (EXPERTS) {
-        const long long l = i / a.n_tiles;
+        const uint32_t l = i / (uint32_t)a.n_tiles;
         t.n0 = (int)(i - l * a.n_tiles) * BN;
         const int4 e = __ldg(a.table + 1 + l);
-        t.r = RowTile{e.x, e.y, 0, (int)min((long long)e.z, max(a.n - e.y, 0ll)), e.y};
+        t.g = e.x, t.m0 = e.y;
+        t.rows = (int)min((long long)e.z, a.n - e.y);
     } else {
-        const int per = a.m_tiles * a.n_tiles, g = (int)(i / per), rem = (int)(i - (long long)g * per), nt = rem / a.m_tiles;
-        const int m0 = (rem - nt * a.m_tiles) * 2 * BM;
-        t.n0 = nt * BN;
-        t.r = RowTile{g, m0, g, a.B - m0, (long long)m0 * a.G + g};
+        const uint32_t column = i / (uint32_t)a.m_tiles;
+        t.g = (int)(column / (uint32_t)a.n_tiles);
+        t.m0 = (int)(i - column * a.m_tiles) * 2 * BM;
+        t.n0 = (int)(column - t.g * a.n_tiles) * BN;
+        t.rows = a.B - t.m0;
     }
     return t;
+}
+// The row of x and of the output that the tile's row i is, and its plane of their tensor maps.
+template <bool EXPERTS>
+__device__ __forceinline__ long long row_of(const Tile& t, int i, const Args& a) {
+    return EXPERTS ? (long long)t.m0 + i : (long long)(t.m0 + i) * a.G + t.g;
+}
+template <bool EXPERTS>
+__device__ __forceinline__ int plane_of(const Tile& t) {
+    return EXPERTS ? 0 : t.g;
 }
 
 // The staging is free again: what was written from it before has been read.
@@ -179,12 +190,12 @@ static_assert(2 * CODE_BYTES <= 4 * STAGING, "two buffers of codes in the stagin
 template <bool EXPERTS>
 __device__ __forceinline__ void save_four(const Args& a, const CUtensorMap* tmY, const Tile& tl, int m_warp, long long row,
                                           uint32_t codes, uint32_t bytes, int lane) {
-    const int rows = min(32, tl.r.rows - m_warp);                            // may be negative
+    const int rows = min(32, tl.rows - m_warp);                            // may be negative
     const int left = (a.N - tl.n0) / kFp4Block;                              // blocks of the rows from n0 on
     if (rows <= 0) return;
     if (!EXPERTS || rows == 32) {
         if (lane == 0) {
-            tma_store_3d(tmY, codes, tl.n0 / 2, tl.r.row + m_warp, tl.r.plane);
+            tma_store_3d(tmY, codes, tl.n0 / 2, tl.m0 + m_warp, plane_of<EXPERTS>(tl));
             bulk_commit_group();
         }
     } else {                                                                 // an expert's last rows
@@ -231,7 +242,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const long long unit = blockIdx.x >> 1, nunits = gridDim.x >> 1;
+    const uint32_t unit = blockIdx.x >> 1, nunits = gridDim.x >> 1;
 
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmX);
@@ -262,7 +273,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     const int kblocks = args.kblocks;
     pdl_wait();
     pdl_launch_next();
-    const long long tiles = EXPERTS ? (long long)__ldg(&args.table[0].x) * args.n_tiles : args.units;
+    const uint32_t tiles = EXPERTS ? (uint32_t)__ldg(&args.table[0].x) * (uint32_t)args.n_tiles : args.units;
 
     if (warp < 4) {
         regs_dec<REGS_OTHER>();
@@ -273,10 +284,10 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             bool ok = true;
             Tile next{};
             if (unit < tiles) next = tile_of<EXPERTS>(unit, args);
-            for (long long i = unit; ok && i < tiles; i += nunits) {
+            for (uint32_t i = unit; ok && i < tiles; i += nunits) {
                 const Tile tl = next;
                 if (i + nunits < tiles) next = tile_of<EXPERTS>(i + nunits, args);
-                const int xrow = tl.r.row + BM * (int)rank, wrow = tl.n0 + BN / 2 * (int)rank;
+                const int xrow = tl.m0 + BM * (int)rank, wrow = tl.n0 + BN / 2 * (int)rank;
                 for (int kb = 0; kb < kblocks; ++kb) {
                     if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
                         ok = false;
@@ -285,9 +296,9 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                     if (elect_one()) {
                         const uint32_t fb = mapa_shared(full_bar(stage), 0);
                         if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2u * TX_BYTES);
-                        tma_load_3d_pair(&tmX, sA + stage * A_BYTES, fb, kb * 128, xrow, tl.r.plane);
-                        tma_load_3d_pair(&tmW, sB + stage * B_BYTES, fb, kb * 128, wrow, tl.r.g);
-                        tma_load_3d_pair(&tmS, sSFB + stage * SFB_BYTES, fb, kb * (SF_BYTES / 4), tl.n0 / 128, tl.r.g);
+                        tma_load_3d_pair(&tmX, sA + stage * A_BYTES, fb, kb * 128, xrow, plane_of<EXPERTS>(tl));
+                        tma_load_3d_pair(&tmW, sB + stage * B_BYTES, fb, kb * 128, wrow, tl.g);
+                        tma_load_3d_pair(&tmS, sSFB + stage * SFB_BYTES, fb, kb * (SF_BYTES / 4), tl.n0 / 128, tl.g);
                     }
                     __syncwarp();
                     if (++stage == STAGES) stage = 0, phase ^= 1u;
@@ -301,7 +312,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             int stage = 0, acc = 0;
             uint32_t phase = 0, aphase = 0, cphase = 0, slot = 0;
             bool ok = true;
-            for (long long i = unit; ok && i < tiles; i += nunits) {
+            for (uint32_t i = unit; ok && i < tiles; i += nunits) {
                 // this accumulator's last tile is out, and of the other's tile the shared columns
                 if (!wait_bounded(tempty_bar(acc), aphase ^ 1u, abort_flag, args.err, args.timeout_ns) ||
                     !wait_bounded(shared_bar, cphase ^ 1u, abort_flag, args.err, args.timeout_ns))
@@ -348,7 +359,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             // ------------------------------ scales of x -------------------------------
             const int groups = (kblocks + 1) / 2;
             Scales sc(sRing + (warp - 2) * Scales::BYTES);
-            long long i = unit;                          // of the next step to fetch
+            uint32_t i = unit;                           // of the next step to fetch
             int g = 0;
             Tile tl{};
             auto skip = [&]() {
@@ -360,7 +371,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             auto fetch = [&]() {
                 if (i >= tiles) return sc.done();
                 const int m0 = BM * (int)rank;
-                sc.fetch(args.xs + (tl.r.at + m0 * args.step) * args.xs_ld, args.step * args.xs_ld, tl.r.rows - m0, g, lane);
+                sc.fetch(args.xs + row_of<EXPERTS>(tl, m0, args) * args.xs_ld, args.step * args.xs_ld, tl.rows - m0, g, lane);
                 skip();
                 if (i < tiles) skip();
             };
@@ -373,7 +384,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true, mine = warp == 2;
-            for (long long j = unit; ok && j < tiles; j += nunits)
+            for (uint32_t j = unit; ok && j < tiles; j += nunits)
                 for (int kb = 0; ok && kb < kblocks; kb += 2, mine = !mine) {
                     if (!mine) {
                         stage += min(2, kblocks - kb);
@@ -408,18 +419,30 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
         const uint32_t out = sEpi + (uint32_t)quad * (4 * STAGING), sf_out = sOut + (uint32_t)quad * 512u;
         uint32_t phase = 0, turn = 0, meet = 0;
         int acc = 0;
-        for (long long i = unit; i < tiles; i += nunits) {
-            const Tile tl = tile_of<EXPERTS>(i, args);
-            const int m_warp = BM * (int)rank + 32 * quad, n = tl.n0 + COLS * part;
-            const int rows = n < args.N ? min(32, tl.r.rows - m_warp) : 0;    // this warp's rows that exist (may be negative)
-            const long long row = tl.r.at + m_warp * args.step;
+        // the next tile and its bias come while this one is worked on
+        Tile next{};
+        float b[2] = {};
+        auto look_ahead = [&](uint32_t i) {
+            if (i >= tiles) return;
+            next = tile_of<EXPERTS>(i, args);
             if (args.bias) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int c = n + 32 * h + lane;
-                    const float b = c < args.N ? __ldg(args.bias + (size_t)tl.r.g * args.N + c) : 0.f;
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(bias + 128u * h + 4u * lane), "f"(b) : "memory");
+                    const int c = next.n0 + COLS * part + 32 * h + lane;
+                    b[h] = c < args.N ? __ldg(args.bias + (size_t)next.g * args.N + c) : 0.f;
                 }
+            }
+        };
+        look_ahead(unit);
+        for (uint32_t i = unit; i < tiles; i += nunits) {
+            const Tile tl = next;
+            const int m_warp = BM * (int)rank + 32 * quad, n = tl.n0 + COLS * part;
+            const int rows = n < args.N ? min(32, tl.rows - m_warp) : 0;      // this warp's rows that exist (may be negative)
+            const long long row = row_of<EXPERTS>(tl, m_warp, args);
+            if (args.bias) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(bias + 128u * h + 4u * lane), "f"(b[h]) : "memory");
                 __syncwarp();
             }
             if (!wait_bounded(tfull_bar(acc), phase, abort_flag, args.err, args.timeout_ns)) break;
@@ -441,6 +464,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             }
             acc ^= 1;
             if (acc == 0) phase ^= 1u;
+            look_ahead(i + nunits);
             float v[COLS];
 #pragma unroll
             for (int c = 0; c < COLS; ++c) v[c] = __uint_as_float(r[c >> 5][c & 31]);
@@ -460,13 +484,13 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     if (rows > 0)
-                        save_piece<__nv_bfloat16, EXPERTS>(v + 32 * h, args, &tmY, tl.r.row + m_warp, tl.r.plane, row,
+                        save_piece<__nv_bfloat16, EXPERTS>(v + 32 * h, args, &tmY, tl.m0 + m_warp, plane_of<EXPERTS>(tl), row,
                                                            n + 32 * h, rows, lane, stage);
             } else if constexpr (EPI == FP4_OUT_F32) {
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
                     if (rows > 0)
-                        save_piece<float, EXPERTS>(v + 16 * h, args, &tmY, tl.r.row + m_warp, tl.r.plane, row, n + 16 * h,
+                        save_piece<float, EXPERTS>(v + 16 * h, args, &tmY, tl.m0 + m_warp, plane_of<EXPERTS>(tl), row, n + 16 * h,
                                                    rows, lane, stage);
             } else {
                 const uint32_t codes = out + turn * CODE_BYTES, bytes = sf_out + turn * 256u;
@@ -549,7 +573,9 @@ cudaError_t launch_fp4_product(const Fp4Product& p, const Fp8Device& dev, cudaSt
     a.kblocks = (p.K + BK - 1) / BK;
     a.nb = (int)fp4_blocks(p.K);
     a.table = p.tiles;
-    a.units = (long long)p.G * a.m_tiles * a.n_tiles;
+    const long long units = (long long)p.G * a.m_tiles * a.n_tiles;
+    if (units >= 1ll << 31) return cudaErrorNotSupported;        // more tiles than a device's memory holds outputs for
+    a.units = (uint32_t)units;
     a.n = p.n;
     a.step = p.tiles ? 1 : p.G;
     a.xs = p.x.scales, a.xs_ld = p.x.lds;
