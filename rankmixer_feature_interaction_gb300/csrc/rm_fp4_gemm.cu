@@ -13,11 +13,14 @@
 //   warp 1       MMA issuer (the even CTA's): six copies of exponent bytes to tensor
 //                memory and four MMAs a k-block
 //   warps 2, 3   x's exponent bytes (RowScales), every other step of two k-blocks
-//   warps 4-19   epilogue: each thread owns 64 columns of one row, so that a block of
-//                32 of a 4-bit output is one thread's
+//   warps 4-19   epilogue, two groups of eight warps for every other tile, so that one
+//                group's waits and reads lie beside the other's arithmetic (all sixteen
+//                on one tile: layer 1 at B = 2048 290 us).  A warp owns 32 rows and 128
+//                columns, a thread 64 of one row at a time, so that a block of 32 of a
+//                4-bit output is one thread's
 // Tensor memory (512 columns): two accumulators of 256 columns that share 64, at
 // columns 0 and 192, so that the next tile's product begins as soon as those 64
-// columns have been read, and two slots of exponent bytes from column 448 (8 columns
+// columns have been read (first), and two slots of exponent bytes from column 448 (8 columns
 // for x, 16 for W).  Copies and MMAs of one thread run in order, so the slots need no
 // barriers of their own.
 // Every mbarrier wait is bounded in time; on expiry the CTA latches an error
@@ -35,11 +38,10 @@ constexpr int A_BYTES = BM * 128, B_BYTES = BN / 2 * 128, SFB_BYTES = 2 * SF_BYT
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int TX_BYTES = STAGE_BYTES + SFB_BYTES;       // what TMA brings to a CTA's stage
 constexpr int STAGES = 5;
-constexpr int EPI_WARPS = 16;
-constexpr int COLS = 64;                 // columns per epilogue warp
+constexpr int EPI_WARPS = 16, GROUP_WARPS = 8;
+constexpr int COLS = 64;                 // columns of a thread at a time, half of a warp's
 constexpr int STAGING = 2048;            // per epilogue warp: 32 rows of 64 bytes
 constexpr int BIAS_BYTES = COLS * 4;     // per epilogue warp
-constexpr int SF_OUT_BYTES = 4 * 2 * 256;  // exponent bytes of a 4-bit output: four quarters, two buffers
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr uint32_t ACC1_COL = 192;       // the second accumulator's first column
 constexpr uint32_t SF_COL = 448, SF_COLS = 24;
@@ -47,7 +49,7 @@ constexpr uint32_t SF_COL = 448, SF_COLS = 24;
 constexpr int REGS_OTHER = 64, REGS_EPI = 104;
 using Scales = RowScales<BM, 3>;        // of each of the two warps
 constexpr int SMEM_BYTES = 1024 + STAGES * (STAGE_BYTES + SF_BYTES + SFB_BYTES) + EPI_WARPS * (STAGING + BIAS_BYTES) +
-                           2 * Scales::BYTES + SF_OUT_BYTES + 256;
+                           2 * Scales::BYTES + 256;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 
 struct Args {
@@ -177,44 +179,30 @@ __device__ __forceinline__ void round_block(const float* v, uint32_t (&w)[4], ui
     }
 }
 
-// A 4-bit output leaves by four warps together, those of the same 32 rows: 128 bytes of
-// codes a row (256 columns) and 8 exponent bytes.  A thread that stored its own 16
-// bytes and its byte made every store 32 requests of part of a sector: the FFN at B =
-// 2048 took 684 us with that.  The staging of the four warps is two buffers of 32
-// rows, used in turn: the codes as TMA takes them with the 128-byte swizzle, and the
-// exponent bytes, a row's eight together.
-constexpr int CODE_BYTES = 32 * 128;
-static_assert(2 * CODE_BYTES <= 4 * STAGING, "two buffers of codes in the staging");
-
-// 32 rows of a tile's 256 columns out of the buffers, by one warp.
+// 128 columns of a warp's rows in 4 bits out of the staging, and their exponent bytes
+// (of this lane's row).  A thread that stored its own 16 bytes and its byte made every
+// store 32 requests of part of a sector: the FFN at B = 2048 took 684 us with that
+// where it takes 510 with rows of 128 bytes by TMA.
 template <bool EXPERTS>
-__device__ __forceinline__ void save_four(const Args& a, const CUtensorMap* tmY, const Tile& tl, int m_warp, long long row,
-                                          uint32_t codes, uint32_t bytes, int lane) {
-    const int rows = min(32, tl.rows - m_warp);                            // may be negative
-    const int left = (a.N - tl.n0) / kFp4Block;                              // blocks of the rows from n0 on
-    if (rows <= 0) return;
+__device__ __forceinline__ void save_codes(const Args& a, const CUtensorMap* tmY, const Tile& tl, int m_warp, long long row,
+                                           int n, int rows, uint32_t E, int lane, uint32_t stage) {
     if (!EXPERTS || rows == 32) {
+        fence_proxy_async_smem();
+        __syncwarp();
         if (lane == 0) {
-            tma_store_3d(tmY, codes, tl.n0 / 2, tl.m0 + m_warp, plane_of<EXPERTS>(tl));
+            tma_store_3d(tmY, stage, n / 2, tl.m0 + m_warp, plane_of<EXPERTS>(tl));
             bulk_commit_group();
         }
-    } else {                                                                 // an expert's last rows
-        for (int r = lane >> 3; r < rows; r += 4) {
-            const int c = lane & 7;
-            if (c < left) {
-                const uint4 q = ld_shared_u4(codes + 128u * r + 16u * (uint32_t)(c ^ (r & 7)));
-                *reinterpret_cast<uint4*>(a.o.codes + (row + r) * a.o.ld + tl.n0 / 2 + 16 * c) = q;
-            }
-        }
+    } else {                                             // an expert's last rows: the next ones are another's
+        store_rows<true, 1>(stage, reinterpret_cast<char*>(a.o.codes) + row * a.o.ld + n / 2, (size_t)a.o.ld, rows,
+                            (a.N - n) / 2, lane);
     }
     if (lane < rows) {
-        uint32_t w[2];
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(bytes + 8u * lane));
-        uint8_t* p = a.o.scales + (row + lane * a.step) * a.o.lds + tl.n0 / kFp4Block;
-        if (left >= 8) {                                                     // lds is a multiple of 16, n0 of 256
-            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        uint8_t* p = a.o.scales + (row + lane * a.step) * a.o.lds + n / kFp4Block;
+        if (n + 128 <= a.N) {                            // lds is a multiple of 16, n of 128
+            *reinterpret_cast<uint32_t*>(p) = E;
         } else {
-            for (int b = 0; b < left; ++b) p[b] = (uint8_t)(w[b >> 2] >> (8 * (b & 3)));
+            for (int b = 0; n + kFp4Block * b < a.N; ++b) p[b] = (uint8_t)(E >> (8 * b));
         }
     }
 }
@@ -230,14 +218,13 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     const uint32_t sA = base, sB = base + STAGES * A_BYTES;
     const uint32_t sSFA = base + STAGES * STAGE_BYTES, sSFB = sSFA + STAGES * SF_BYTES;
     const uint32_t sEpi = sSFB + STAGES * SFB_BYTES;
-    const uint32_t sBias = sEpi + EPI_WARPS * STAGING, sRing = sBias + EPI_WARPS * BIAS_BYTES, sOut = sRing + 2 * Scales::BYTES, bar0 = sOut + SF_OUT_BYTES;
+    const uint32_t sBias = sEpi + EPI_WARPS * STAGING, sRing = sBias + EPI_WARPS * BIAS_BYTES, bar0 = sRing + 2 * Scales::BYTES;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
     auto tfull_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + x); };
     auto tempty_bar = [&](int x) { return bar0 + 8u * (2 * STAGES + 2 + x); };
     const uint32_t shared_bar = bar0 + 8u * (2 * STAGES + 4);
-    auto meet_bar = [&](int q) { return shared_bar + 8u + 8u * q; };
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (meet_bar(4) - base));
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + (shared_bar + 8u - base));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -254,10 +241,9 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(tfull_bar(x), 1);              // multicast commit
-            mbar_init(tempty_bar(x), 2 * EPI_WARPS); // the even CTA's: every epilogue warp of both CTAs
+            mbar_init(tempty_bar(x), 2 * GROUP_WARPS);   // the even CTA's: the group's warps of both CTAs
         }
-        for (int q = 0; q < 4; ++q) mbar_init(meet_bar(q), 4);
-        mbar_init(shared_bar, 2 * EPI_WARPS / 4);    // the even CTA's: the warps that own the shared columns
+        mbar_init(shared_bar, 2 * GROUP_WARPS / 2);  // the even CTA's: the warps that own the shared columns
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -412,109 +398,105 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     } else {
         // ------------------------------ epilogue --------------------------------------
         regs_inc<REGS_EPI>();
-        const int quad = warp & 3, part = (warp - 4) >> 2;       // 32 rows, 64 columns
+        // the group's accumulator; 32 rows, 128 columns
+        const int acc = (warp - 4) / GROUP_WARPS, quad = warp & 3, part = ((warp - 4) >> 2) & 1;
         const uint32_t stage = sEpi + (uint32_t)(warp - 4) * STAGING, bias = sBias + (uint32_t)(warp - 4) * BIAS_BYTES;
-        const uint32_t shared_leader = mapa_shared(shared_bar, 0);
-        // (GELU) the four warps' buffers: codes, exponent bytes
-        const uint32_t out = sEpi + (uint32_t)quad * (4 * STAGING), sf_out = sOut + (uint32_t)quad * 512u;
-        uint32_t phase = 0, turn = 0, meet = 0;
-        int acc = 0;
-        // the next tile and its bias come while this one is worked on
+        // The 64 columns that the other accumulator shares are the last of accumulator 0
+        // and the first of 1: their owners read them first.
+        const bool owner = part != acc;
+        const int first = acc == 0 && part == 1 ? 1 : 0;             // the half of the warp's columns that comes first
+        uint32_t phase = 0;
+        // the group's next tile and its bias come while this one is worked on
         Tile next{};
-        float b[2] = {};
+        float b[4] = {};
         auto look_ahead = [&](uint32_t i) {
             if (i >= tiles) return;
             next = tile_of<EXPERTS>(i, args);
             if (args.bias) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int c = next.n0 + COLS * part + 32 * h + lane;
+                for (int h = 0; h < 4; ++h) {
+                    const int c = next.n0 + 2 * COLS * part + 32 * h + lane;
                     b[h] = c < args.N ? __ldg(args.bias + (size_t)next.g * args.N + c) : 0.f;
                 }
             }
         };
-        look_ahead(unit);
-        for (uint32_t i = unit; i < tiles; i += nunits) {
+        look_ahead(unit + acc * nunits);
+        for (uint32_t i = unit + acc * nunits; i < tiles; i += 2 * nunits) {
             const Tile tl = next;
-            const int m_warp = BM * (int)rank + 32 * quad, n = tl.n0 + COLS * part;
-            const int rows = n < args.N ? min(32, tl.rows - m_warp) : 0;      // this warp's rows that exist (may be negative)
+            const int m_warp = BM * (int)rank + 32 * quad, n_warp = tl.n0 + 2 * COLS * part;
+            const int rows = n_warp < args.N ? min(32, tl.rows - m_warp) : 0;     // this warp's rows that exist (may be negative)
             const long long row = row_of<EXPERTS>(tl, m_warp, args);
-            if (args.bias) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(bias + 128u * h + 4u * lane), "f"(b[h]) : "memory");
-                __syncwarp();
-            }
             if (!wait_bounded(tfull_bar(acc), phase, abort_flag, args.err, args.timeout_ns)) break;
+            phase ^= 1u;
             tc_fence_after();
-            // A thread's columns come out at once, so the accumulator is free again long
-            // before the epilogue is done; the 64 columns that the other accumulator
-            // shares are the last of accumulator 0 and the first of 1.
-            uint32_t r[2][32];
-            const uint32_t tcol =
-                tmem_base + ((uint32_t)(32 * quad) << 16) + (acc ? ACC1_COL : 0u) + (uint32_t)(COLS * part);
-            tmem_ld32_nowait(tcol, r[0]);
-            tmem_ld32_nowait(tcol + 32u, r[1]);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (part == (acc ? 0 : 3)) mbar_arrive_pair(shared_leader);
-                mbar_arrive_pair(mapa_shared(tempty_bar(acc), 0));
-            }
-            acc ^= 1;
-            if (acc == 0) phase ^= 1u;
-            look_ahead(i + nunits);
-            float v[COLS];
+            uint32_t E = 0;                                  // (4-bit output) exponent bytes of the row's four blocks
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) {
+                const int half = k ^ first, n = n_warp + COLS * half;
+                float v[COLS];
+                {
+                    uint32_t r[2][32];
+                    const uint32_t tcol = tmem_base + ((uint32_t)(32 * quad) << 16) + (acc ? ACC1_COL : 0u) +
+                                          (uint32_t)(2 * COLS * part + COLS * half);
+                    tmem_ld32_nowait(tcol, r[0]);
+                    tmem_ld32_nowait(tcol + 32u, r[1]);
+                    if (args.bias) {
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) v[c] = __uint_as_float(r[c >> 5][c & 31]);
-            if (args.bias) {                             // brought there before the tile was waited for
+                        for (int h = 0; h < 2; ++h)
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(bias + 128u * h + 4u * lane),
+                                         "f"(half ? b[2 + h] : b[h])
+                                         : "memory");
+                    }
+                    tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < COLS / 4; ++c) {
-                    float4 q;
-                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
-                                 : "r"(bias + 16u * c));
-                    f2_unpack(f2_add(f2_pack(v[4 * c], v[4 * c + 1]), f2_pack(q.x, q.y)), v[4 * c], v[4 * c + 1]);
-                    f2_unpack(f2_add(f2_pack(v[4 * c + 2], v[4 * c + 3]), f2_pack(q.z, q.w)), v[4 * c + 2], v[4 * c + 3]);
+                    for (int c = 0; c < COLS; ++c) v[c] = __uint_as_float(r[c >> 5][c & 31]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (k == 0 && owner) mbar_arrive_pair(mapa_shared(shared_bar, 0));
+                    if (k == 1) mbar_arrive_pair(mapa_shared(tempty_bar(acc), 0));
+                }
+                if (k == 1) look_ahead(i + 2 * nunits);
+                if (rows > 0) {
+                    if (args.bias) {
+#pragma unroll
+                        for (int c = 0; c < COLS / 4; ++c) {
+                            float4 q;
+                            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                         : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
+                                         : "r"(bias + 16u * c));
+                            f2_unpack(f2_add(f2_pack(v[4 * c], v[4 * c + 1]), f2_pack(q.x, q.y)), v[4 * c], v[4 * c + 1]);
+                            f2_unpack(f2_add(f2_pack(v[4 * c + 2], v[4 * c + 3]), f2_pack(q.z, q.w)), v[4 * c + 2],
+                                      v[4 * c + 3]);
+                        }
+                    }
+                    if constexpr (EPI == FP4_OUT_BF16) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            save_piece<__nv_bfloat16, EXPERTS>(v + 32 * h, args, &tmY, tl.m0 + m_warp, plane_of<EXPERTS>(tl),
+                                                               row, n + 32 * h, rows, lane, stage);
+                    } else if constexpr (EPI == FP4_OUT_F32) {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h)
+                            save_piece<float, EXPERTS>(v + 16 * h, args, &tmY, tl.m0 + m_warp, plane_of<EXPERTS>(tl), row,
+                                                       n + 16 * h, rows, lane, stage);
+                    } else {
+                        if (k == 0) staging_free(lane);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t w[4], e;
+#pragma unroll
+                            for (int c = 0; c < 32; c += 2) gelu2(v[32 * h + c], v[32 * h + c + 1]);
+                            round_block(v + 32 * h, w, e);
+                            st_shared_v4(staged_at(stage, lane, 2 * half + h), w[0], w[1], w[2], w[3]);
+                            E |= e << (16 * half + 8 * h);
+                        }
+                        if (k == 1) save_codes<EXPERTS>(args, &tmY, tl, m_warp, row, n_warp, rows, E, lane, stage);
+                    }
                 }
                 __syncwarp();
             }
-            if constexpr (EPI == FP4_OUT_BF16) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (rows > 0)
-                        save_piece<__nv_bfloat16, EXPERTS>(v + 32 * h, args, &tmY, tl.m0 + m_warp, plane_of<EXPERTS>(tl), row,
-                                                           n + 32 * h, rows, lane, stage);
-            } else if constexpr (EPI == FP4_OUT_F32) {
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-                    if (rows > 0)
-                        save_piece<float, EXPERTS>(v + 16 * h, args, &tmY, tl.m0 + m_warp, plane_of<EXPERTS>(tl), row, n + 16 * h,
-                                                   rows, lane, stage);
-            } else {
-                const uint32_t codes = out + turn * CODE_BYTES, bytes = sf_out + turn * 256u;
-                uint32_t E[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) gelu2(v[32 * h + c], v[32 * h + c + 1]);
-                    round_block(v + 32 * h, w, E[h]);
-                    st_shared_v4(codes + 128u * lane + 16u * (uint32_t)((2 * part + h) ^ (lane & 7)), w[0], w[1], w[2], w[3]);
-                }
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(bytes + 8u * lane + 2u * part), "h"((uint16_t)(E[0] | E[1] << 8))
-                             : "memory");
-                fence_proxy_async_smem();
-                if (part == 0 && lane == 0) bulk_wait_group_read<0>();       // the other buffer is free for the next tile
-                __syncwarp();
-                if (lane == 0) mbar_arrive(meet_bar(quad));
-                if (!wait_bounded(meet_bar(quad), meet, abort_flag, args.err, args.timeout_ns)) break;
-                meet ^= 1u;
-                if (part == 0) save_four<EXPERTS>(args, &tmY, tl, m_warp, row, codes, bytes, lane);
-                turn ^= 1u;
-            }
-            __syncwarp();
         }
         if (lane == 0) bulk_wait_group<0>();
     }
@@ -600,8 +582,8 @@ cudaError_t launch_fp4_product(const Fp4Product& p, const Fp8Device& dev, cudaSt
     const long long bytes = gelu ? p.N / 2 : p.N * (p.epi == FP4_OUT_F32 ? 4ll : 2ll), pitch = gelu ? p.o.ld : bytes;
     const void* dst = gelu ? p.o.codes : p.y;
     if (ok && (gelu || a.vec) &&
-        !(p.tiles ? fp8_tensor_map(&my, u8t, dst, bytes, p.n, 1, pitch, pitch, gelu ? 128 : 64, 32)
-                  : fp8_tensor_map(&my, u8t, dst, bytes, p.B, p.G, p.G * pitch, pitch, gelu ? 128 : 64, 32)))
+        !(p.tiles ? fp8_tensor_map(&my, u8t, dst, bytes, p.n, 1, pitch, pitch, 64, 32)
+                  : fp8_tensor_map(&my, u8t, dst, bytes, p.B, p.G, p.G * pitch, pitch, 64, 32)))
         return cudaErrorInvalidValue;
     if (!ok) return cudaErrorInvalidValue;
     switch (p.epi) {
