@@ -685,16 +685,23 @@ class Fp4Tensor:
         return math.prod(self.cs) + math.prod(self.ss)
 
 
+@functools.lru_cache(maxsize=256)
+def _fp4_layout(lead: tuple, cols: int, weight: bool) -> tuple:
+    """(shape of codes, shape of scales, where the scales begin, bytes) of 4-bit rows [*lead, cols] in one allocation."""
+    nb = (cols + 31) // 32
+    cs = (*lead, 16 * nb)
+    ss = (*lead[:-1], (lead[-1] + 127) // 128, 2 * ((cols + 255) // 256), 512) if weight else (*lead, (nb + 15) // 16 * 16)
+    at = (math.prod(cs) + 255) // 256 * 256
+    return cs, ss, at, at + math.prod(ss), ss[-2] if weight else ss[-1]
+
+
 def _fp4_new(lead: tuple, cols: int, weight: bool, device: torch.device, index: int) -> Fp4Tensor:
     """An uninitialised 4-bit tensor of rows [*lead, cols], in one allocation."""
-    nb = (cols + 31) // 32
     q = object.__new__(Fp4Tensor)
-    q.cs = (*lead, 16 * nb)
-    q.ss = (*lead[:-1], (lead[-1] + 127) // 128, 2 * ((cols + 255) // 256), 512) if weight else (*lead, (nb + 15) // 16 * 16)
-    at = (math.prod(q.cs) + 255) // 256 * 256
-    q._arena = torch.empty(at + math.prod(q.ss), dtype=torch.uint8, device=device)
+    q.cs, q.ss, at, size, lds = _fp4_layout(lead, cols, weight)
+    q._arena = torch.empty(size, dtype=torch.uint8, device=device)
     base = q._arena.data_ptr()
-    q.c = _lib.rm_fp4_tensor(base, base + at, 16 * nb, q.ss[-2] if weight else q.ss[-1])
+    q.c = _lib.rm_fp4_tensor(base, base + at, q.cs[-1], lds)
     q.cols, q.weight, q.device, q.device_index, q._codes, q._scales = cols, weight, device, index, None, None
     return q
 
@@ -714,6 +721,7 @@ def _fp4_weight(w: Fp4Tensor, dims: int, what: str) -> tuple:
 def _bias(bias: torch.Tensor | None, shape: tuple) -> int | None:
     if bias is None:
         return None
+    _fp8_device(bias.get_device())
     if bias.dtype != torch.float32 or bias.shape != shape:
         raise ValueError(f"bias must be float32 {list(shape)}")
     return _ptr(bias)
@@ -726,13 +734,13 @@ def fp4_quantize(X: torch.Tensor) -> Fp4Tensor:
     dtype, shape = _CODE.get(X.dtype), X.shape
     if dtype is None:
         raise ValueError(f"X must be bfloat16 or float32, got {X.dtype}")
-    if len(shape) < 1:
+    if not shape:
         raise ValueError("X must have at least one dimension")
-    lead, C = tuple(shape[:-1]), shape[-1]
-    rows = math.prod(lead)
-    if rows < 1 or C < 1:
+    *lead, C = shape
+    lead, n = tuple(lead), X.numel()
+    if n < 1:
         raise _lib.RankMixerError(_lib.RM_ERR_INVALID_ARG, "fp4_quantize", f"empty tensor {tuple(shape)}")
-    ldx = C
+    rows, ldx = n // C, C
     if not X.is_contiguous():
         if X.stride(-1) != 1 and C > 1:
             raise ValueError("the last dimension of X must be contiguous")
@@ -773,7 +781,7 @@ def fp4_matmul(x: Fp4Tensor, w: Fp4Tensor, bias: torch.Tensor | None = None, out
     Tw, Kw, N = _fp4_weight(w, 3, "w")
     if Tw != T or Kw != K:
         raise ValueError(f"x {x.shape} and w {w.shape} do not fit")
-    d = _fp8_device(x.device_index, w.device_index, *(() if bias is None else (bias.get_device(),)))
+    d = _fp8_device(x.device_index, w.device_index)
     tdt, code = _DTYPES[out_dtype]
     b = _bias(bias, (T, N))
     Y = torch.empty((B, T, N), dtype=tdt, device=x.device)
@@ -847,10 +855,10 @@ class ExpertRows:
 
     def __init__(self, B: int, T: int, E: int, device: torch.device, index: int):
         self.B, self.T, self.E, self.device, self.device_index = B, T, E, device, index
-        self._at, size = _expert_layout(B, T, E)
+        self._at, size, _ = _expert_layout(B, T, E)
         self._arena = torch.empty(size, dtype=torch.int32, device=device)
-        base = self._arena.data_ptr()
-        self.c = _lib.rm_expert_rows(*(base + 4 * at for at in self._at), B, T, E)
+        base, (o, s, t, i, _) = self._arena.data_ptr(), self._at
+        self.c = _lib.rm_expert_rows(base + 4 * o, base + 4 * s, base + 4 * t, base + 4 * i, B, T, E)
 
     @property
     def offsets(self) -> torch.Tensor:
@@ -871,17 +879,13 @@ class ExpertRows:
 
 @functools.lru_cache(maxsize=256)
 def _expert_layout(B: int, T: int, E: int) -> tuple:
-    """Where offsets, source, slot and tiles lie in one allocation of int32, and its length."""
-    at, places = 0, []
-    for n in (T * E + 1, B * T * E, B * T * E, 4 * (1 + T * E * ((B + 255) // 256))):
+    """Where offsets, source, slot, tiles and the sort's workspace lie in one allocation of int32, its
+    length, and the bytes of the workspace."""
+    at, places, work = 0, [], _lib.rm_expert_sort_workspace(B, T, E)
+    for n in (T * E + 1, B * T * E, B * T * E, 4 * (1 + T * E * ((B + 255) // 256)), work // 4):
         places.append(at)
         at += (n + 63) // 64 * 64
-    return tuple(places), at
-
-
-@functools.lru_cache(maxsize=256)
-def _expert_sort_bytes(B: int, T: int, E: int) -> int:
-    return _lib.rm_expert_sort_workspace(B, T, E)
+    return tuple(places), at, work
 
 
 def expert_sort(G: torch.Tensor) -> ExpertRows:
@@ -890,17 +894,17 @@ def expert_sort(G: torch.Tensor) -> ExpertRows:
     if G.dtype != torch.float32 or G.dim() != 3:
         raise ValueError(f"G must be a float32 [B, T, E], got {G.dtype} {tuple(G.shape)}")
     B, T, E = G.shape
-    n = _expert_sort_bytes(B, T, E)
     rows = ExpertRows(B, T, E, G.device, d)
-    work = torch.empty(n, dtype=torch.uint8, device=G.device)
-    _lib.rm_expert_sort(_ptr(G), rows.c, work.data_ptr(), n, _raw_stream(d))
+    at, _, work = _expert_layout(B, T, E)
+    _lib.rm_expert_sort(_ptr(G), rows.c, rows._arena.data_ptr() + 4 * at[4], work, _raw_stream(d))
     return rows
 
 
 def _batch_rows(X: torch.Tensor, rows: ExpertRows, what: str) -> int:
-    if X.dtype not in _CODE or X.dim() != 3 or X.shape[0] != rows.B or X.shape[1] != rows.T:
-        raise ValueError(f"{what} must be a bfloat16 or float32 [{rows.B}, {rows.T}, D], got {X.dtype} {tuple(X.shape)}")
-    return X.shape[2]
+    shape = X.shape
+    if X.dtype not in _CODE or len(shape) != 3 or shape[0] != rows.B or shape[1] != rows.T:
+        raise ValueError(f"{what} must be a bfloat16 or float32 [{rows.B}, {rows.T}, D], got {X.dtype} {tuple(shape)}")
+    return shape[2]
 
 
 def _gates(G: torch.Tensor, rows: ExpertRows) -> int:
@@ -954,9 +958,12 @@ def expert_combine(Y: torch.Tensor, rows: ExpertRows, G: torch.Tensor, out_dtype
 
 def _combine(Y: torch.Tensor, rows: ExpertRows, G: torch.Tensor | None, what: str, out_dtype: str | None) -> torch.Tensor:
     n, D = _sorted_rows(Y, what)
-    d = _fp8_device(Y.get_device(), rows.device_index, *(() if G is None else (G.get_device(),)))
+    d = _fp8_device(Y.get_device(), rows.device_index)
     tdt, code = _DTYPES[out_dtype] if out_dtype is not None else (Y.dtype, _CODE[Y.dtype])
-    g = None if G is None else _gates(G, rows)
+    g = None
+    if G is not None:
+        _fp8_device(G.get_device())
+        g = _gates(G, rows)
     V = torch.empty((rows.B, rows.T, D), dtype=tdt, device=Y.device)
     _lib.rm_expert_combine(_ptr(Y), _CODE[Y.dtype], rows.c, g, V.data_ptr(), code, n, D, _raw_stream(d))
     return V
@@ -987,8 +994,7 @@ def fp4_expert_matmul(x: Fp4Tensor, w: Fp4Tensor, rows: ExpertRows, bias: torch.
     T, E, Kw, N = _fp4_weight(w, 4, "w")
     if (T, E) != (rows.T, rows.E) or Kw != K:
         raise ValueError(f"x {x.shape}, w {w.shape} and rows of T = {rows.T}, E = {rows.E} do not fit")
-    d = _fp8_device(x.device_index, w.device_index, rows.device_index,
-                    *(() if bias is None else (bias.get_device(),)))
+    d = _fp8_device(x.device_index, w.device_index, rows.device_index)
     tdt, code = _DTYPES[out_dtype]
     b = _bias(bias, (T, E, N))
     Y = torch.empty((n, N), dtype=tdt, device=x.device)

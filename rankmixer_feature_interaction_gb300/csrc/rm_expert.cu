@@ -163,33 +163,43 @@ sort_place_kernel(const float* __restrict__ G, int TE, const int* __restrict__ c
     }
 }
 
-// Few gates: one CTA, a thread per column.
+// Few gates: one CTA, a thread per column, its open gates a mask of 64 bits.  A group
+// of so few rows is one tile: rows and tiles are counted in one sum.
 __global__ void __launch_bounds__(kSortThreads)
-sort_small_kernel(const float* __restrict__ G, int TE, ExpertRows r, int* __restrict__ totals) {
+sort_small_kernel(const float* __restrict__ G, int TE, ExpertRows r) {
+    static_assert(kSmallRows <= 64 && kSmallSort < 32768, "a mask, and two sums of 16 bits");
     __shared__ int shared[kSortWarps];
     pdl_wait();
     pdl_launch_next();
-    int rows = 0;
+    int sum = 0;                                       // rows, and 2^16 tiles
     for (int g0 = 0; g0 < TE; g0 += kSortThreads) {
         const int g = g0 + threadIdx.x;
-        int n = 0, all;
+        unsigned long long open = 0;
         if (g < TE) {
 #pragma unroll 8
-            for (int b = 0; b < r.B; ++b) n += __ldg(G + (size_t)b * TE + g) > 0.f;
-            totals[g] = n;
+            for (int b = 0; b < r.B; ++b) open |= (unsigned long long)(__ldg(G + (size_t)b * TE + g) > 0.f) << b;
         }
-        int at = rows + block_scan(n, shared, all);
-        rows += all;
-        if (g < TE)
+        const int n = __popcll(open);
+        int all;
+        const int at = sum + block_scan(n | (n > 0 ? 1 << 16 : 0), shared, all);
+        sum += all;
+        if (g < TE) {
+            int slot = at & 0xffff;
+            const int source = g / r.E;
+            r.offsets[g] = slot;
+            if (n > 0) r.tiles[1 + (at >> 16)] = make_int4(g, slot, n, 0);
 #pragma unroll 8
             for (int b = 0; b < r.B; ++b) {
-                const bool open = __ldg(G + (size_t)b * TE + g) > 0.f;
-                place(r, (size_t)b * TE + g, open, at, b * r.T + g / r.E);
-                at += open;
+                const bool is = open >> b & 1;
+                place(r, (size_t)b * TE + g, is, slot, b * r.T + source);
+                slot += is;
             }
+        }
     }
-    __syncthreads();
-    write_groups([&](int g) { return totals[g]; }, r, TE, shared);
+    if (threadIdx.x == 0) {
+        r.offsets[TE] = sum & 0xffff;
+        r.tiles[0] = make_int4(sum >> 16, sum & 0xffff, 0, 0);
+    }
 }
 
 // ---- rows ----------------------------------------------------------------------
@@ -234,9 +244,24 @@ struct Piece {
         }
     }
 };
-// Pieces of a row that a lane holds at once.
+// A warp takes a run of a row: kHeld pieces a lane, held at once.
 template <bool VEC>
 constexpr int kHeld = VEC ? 3 : 8;
+
+struct Run {
+    size_t bt;          // the row
+    int p;              // this lane's first piece
+    bool there;
+};
+template <int HELD>
+__device__ __forceinline__ Run run_of(const ExpertRows& r, int runs) {
+    const unsigned long long id = (unsigned long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    Run u;
+    u.bt = id / (unsigned)runs;
+    u.p = (int)(id - u.bt * runs) * 32 * HELD + (threadIdx.x & 31);
+    u.there = u.bt < (size_t)r.B * r.T;
+    return u;
+}
 
 // Open experts e0 .. e0 + 31 of row bt, as a mask; slot: lane e's.
 __device__ __forceinline__ uint32_t open_experts(const int* __restrict__ slots, size_t bt, int E, int e0, long long n,
@@ -247,200 +272,263 @@ __device__ __forceinline__ uint32_t open_experts(const int* __restrict__ slots, 
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(32 * kRowWarps)
-gather_kernel(const T* __restrict__ X, ExpertRows r, T* __restrict__ Xs, long long n, int D) {
+gather_kernel(const T* __restrict__ X, ExpertRows r, T* __restrict__ Xs, long long n, int D, int runs) {
     using P = Piece<T, VEC>;
     constexpr int H = kHeld<VEC>;
     pdl_wait();
     pdl_launch_next();
-    const int lane = threadIdx.x & 31;
-    const size_t bt = (size_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-    if (bt >= (size_t)r.B * r.T) return;
-    const int pieces = D / P::N;
-    for (int p0 = lane; p0 - lane < pieces; p0 += 32 * H) {
-        P x[H];
+    const int lane = threadIdx.x & 31, pieces = D / P::N;
+    const Run u = run_of<H>(r, runs);
+    if (!u.there) return;
+    P x[H];
 #pragma unroll
-        for (int i = 0; i < H; ++i)
-            if (p0 + 32 * i < pieces) x[i].load(X + bt * D + (size_t)(p0 + 32 * i) * P::N);
-        for (int e0 = 0; e0 < r.E; e0 += 32) {
-            int slot;
-            for (uint32_t m = open_experts(r.slot, bt, r.E, e0, n, lane, slot); m; m &= m - 1) {
-                T* dst = Xs + (size_t)__shfl_sync(0xffffffffu, slot, __ffs(m) - 1) * D;
+    for (int i = 0; i < H; ++i)
+        if (u.p + 32 * i < pieces) x[i].load(X + u.bt * D + (size_t)(u.p + 32 * i) * P::N);
+    for (int e0 = 0; e0 < r.E; e0 += 32) {
+        int slot;
+        for (uint32_t m = open_experts(r.slot, u.bt, r.E, e0, n, lane, slot); m; m &= m - 1) {
+            T* dst = Xs + (size_t)__shfl_sync(0xffffffffu, slot, __ffs(m) - 1) * D;
 #pragma unroll
-                for (int i = 0; i < H; ++i)
-                    if (p0 + 32 * i < pieces) x[i].store(dst + (size_t)(p0 + 32 * i) * P::N);
-            }
+            for (int i = 0; i < H; ++i)
+                if (u.p + 32 * i < pieces) x[i].store(dst + (size_t)(u.p + 32 * i) * P::N);
         }
     }
 }
 
-// The same with the rows in 4 bits: a lane rounds eight values, four lanes a block.
+// The same with the rows in 4 bits: a lane rounds 16 values, two lanes a block.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(32 * kRowWarps)
-gather_fp4_kernel(const T* __restrict__ X, ExpertRows r, Fp4View out, long long n, int D, int nb) {
-    constexpr int H = 3;
+gather_fp4_kernel(const T* __restrict__ X, ExpertRows r, Fp4View out, long long n, int D, int nb, int runs) {
     pdl_wait();
     pdl_launch_next();
     const int lane = threadIdx.x & 31;
-    const size_t bt = (size_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-    if (bt >= (size_t)r.B * r.T) return;
-    for (int p0 = lane; p0 - lane < 4 * nb; p0 += 32 * H) {
-        uint32_t code[H], E[H];
-        float v[H][8];
-#pragma unroll
-        for (int i = 0; i < H; ++i) {
-            const int p = p0 + 32 * i;
-            fp4_load8<T, VEC>(X + bt * D + 8 * (size_t)p, D - 8 * p, v[i]);     // past the row's end: zeros
-        }
-#pragma unroll
-        for (int i = 0; i < H; ++i) code[i] = fp4_round8(v[i], E[i]);
-        for (int e0 = 0; e0 < r.E; e0 += 32) {
-            int slot;
-            for (uint32_t m = open_experts(r.slot, bt, r.E, e0, n, lane, slot); m; m &= m - 1) {
-                const size_t row = (size_t)__shfl_sync(0xffffffffu, slot, __ffs(m) - 1);
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    const int p = p0 + 32 * i;
-                    if (p < 4 * nb) {
-                        *reinterpret_cast<uint32_t*>(out.codes + row * out.ld + 4 * p) = code[i];
-                        if ((p & 3) == 0) out.scales[row * out.lds + (p >> 2)] = (uint8_t)E[i];
-                    }
-                }
+    const Run u = run_of<1>(r, runs);
+    if (!u.there) return;
+    Fp4Raw16<T> v;
+    v.template load<VEC>(X + u.bt * D + 16 * (size_t)u.p, D - 16 * u.p);         // past the row's end: zeros
+    int slot;
+    uint32_t m = open_experts(r.slot, u.bt, r.E, 0, n, lane, slot);
+    uint32_t E;
+    const uint2 code = v.round(E);
+    for (int e0 = 0;;) {
+        for (; m; m &= m - 1) {
+            const size_t row = (size_t)__shfl_sync(0xffffffffu, slot, __ffs(m) - 1);
+            if (u.p < 2 * nb) {
+                *reinterpret_cast<uint2*>(out.codes + row * out.ld + 8 * u.p) = code;
+                if ((u.p & 1) == 0) out.scales[row * out.lds + (u.p >> 1)] = (uint8_t)E;
             }
         }
+        if ((e0 += 32) >= r.E) break;
+        m = open_experts(r.slot, u.bt, r.E, e0, n, lane, slot);
     }
 }
 
-// TO: the type of V; sums in float32, ascending e.
+// TO: the type of V; sums in float32, ascending e, two experts' rows loaded at a time.
 template <typename T, typename TO, bool VEC>
 __global__ void __launch_bounds__(32 * kRowWarps)
-combine_kernel(const T* __restrict__ Y, ExpertRows r, const float* __restrict__ G, TO* __restrict__ V, long long n, int D) {
+combine_kernel(const T* __restrict__ Y, ExpertRows r, const float* __restrict__ G, TO* __restrict__ V, long long n, int D,
+               int runs) {
     using P = Piece<T, VEC>;
     constexpr int H = kHeld<VEC>, N = P::N;
     pdl_wait();
     pdl_launch_next();
-    const int lane = threadIdx.x & 31;
-    const size_t bt = (size_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-    if (bt >= (size_t)r.B * r.T) return;
-    const int pieces = D / N;
-    for (int p0 = lane; p0 - lane < pieces; p0 += 32 * H) {
-        float v[H][N] = {};
-        for (int e0 = 0; e0 < r.E; e0 += 32) {
-            int slot;
-            const uint32_t open = open_experts(r.slot, bt, r.E, e0, n, lane, slot);
-            const float gate = G && e0 + lane < r.E ? __ldg(G + bt * r.E + e0 + lane) : 1.f;
-            for (uint32_t m = open; m; m &= m - 1) {
-                const int e = __ffs(m) - 1;
-                const T* src = Y + (size_t)__shfl_sync(0xffffffffu, slot, e) * D;
-                const float g = __shfl_sync(0xffffffffu, gate, e);
-                P y[H];
+    const int lane = threadIdx.x & 31, pieces = D / N;
+    const Run u = run_of<H>(r, runs);
+    if (!u.there) return;
+    float v[H][N] = {};
+    for (int e0 = 0; e0 < r.E; e0 += 32) {
+        const float gate = G && e0 + lane < r.E ? __ldg(G + u.bt * r.E + e0 + lane) : 1.f;
+        int slot;
+        uint32_t m = open_experts(r.slot, u.bt, r.E, e0, n, lane, slot);
+        while (m) {
+            const int e = __ffs(m) - 1;
+            m &= m - 1;
+            const bool two = m != 0;
+            const int f = two ? __ffs(m) - 1 : e;
+            m &= m - 1;
+            const T* src = Y + (size_t)__shfl_sync(0xffffffffu, slot, e) * D;
+            const T* src2 = Y + (size_t)__shfl_sync(0xffffffffu, slot, f) * D;
+            const float g = __shfl_sync(0xffffffffu, gate, e), g2 = __shfl_sync(0xffffffffu, gate, f);
+            P y[H], z[H];
 #pragma unroll
-                for (int i = 0; i < H; ++i)
-                    if (p0 + 32 * i < pieces) y[i].load(src + (size_t)(p0 + 32 * i) * N);
+            for (int i = 0; i < H; ++i)
+                if (u.p + 32 * i < pieces) {
+                    y[i].load(src + (size_t)(u.p + 32 * i) * N);
+                    if (two) z[i].load(src2 + (size_t)(u.p + 32 * i) * N);
+                }
 #pragma unroll
-                for (int i = 0; i < H; ++i)
-                    if (p0 + 32 * i < pieces) {
+            for (int i = 0; i < H; ++i)
+                if (u.p + 32 * i < pieces) {
 #pragma unroll
-                        for (int k = 0; k < N; ++k) v[i][k] = fmaf(g, y[i].get(k), v[i][k]);
+                    for (int k = 0; k < N; ++k) {
+                        v[i][k] = fmaf(g, y[i].get(k), v[i][k]);
+                        if (two) v[i][k] = fmaf(g2, z[i].get(k), v[i][k]);
                     }
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+        if (u.p + 32 * i < pieces) {
+            TO* dst = V + u.bt * D + (size_t)(u.p + 32 * i) * N;
+            if constexpr (sizeof(T) == sizeof(TO)) {
+                Piece<TO, VEC> o;
+                o.set(v[i]);
+                o.store(dst);
+            } else if constexpr (VEC) {                 // bf16 rows to float
+                reinterpret_cast<float4*>(dst)[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+                reinterpret_cast<float4*>(dst)[1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
+            } else {
+                *dst = v[i][0];
             }
         }
-#pragma unroll
-        for (int i = 0; i < H; ++i)
-            if (p0 + 32 * i < pieces) {
-                TO* dst = V + bt * D + (size_t)(p0 + 32 * i) * N;
-                if constexpr (sizeof(T) == sizeof(TO)) {
-                    Piece<TO, VEC> o;
-                    o.set(v[i]);
-                    o.store(dst);
-                } else if constexpr (VEC) {                 // bf16 rows to float
-                    reinterpret_cast<float4*>(dst)[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-                    reinterpret_cast<float4*>(dst)[1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
-                } else {
-                    *dst = v[i][0];
-                }
-            }
-    }
 }
 
-template <typename T, bool VEC>
+// WARPS warps a row (where rows are few, all of the CTA's), two experts at a time.
+template <typename T, bool VEC, int WARPS>
 __global__ void __launch_bounds__(32 * kRowWarps)
 combine_backward_kernel(const T* __restrict__ dV, const T* __restrict__ Y, ExpertRows r, const float* __restrict__ G,
                         T* __restrict__ dY, float* __restrict__ dG, long long n, int D) {
     using P = Piece<T, VEC>;
-    constexpr int H = kHeld<VEC>, N = P::N;
+    constexpr int H = WARPS == 1 || !VEC ? kHeld<VEC> : 2, N = P::N, STEP = 32 * WARPS;
+    __shared__ float sums[2][kRowWarps];
     pdl_wait();
     pdl_launch_next();
-    const int lane = threadIdx.x & 31;
-    const size_t bt = (size_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pieces = D / N;
+    const size_t bt = (size_t)blockIdx.x * (kRowWarps / WARPS) + (WARPS == 1 ? warp : 0);
     if (bt >= (size_t)r.B * r.T) return;
-    const int pieces = D / N;
+    const int first = WARPS == 1 ? lane : (int)threadIdx.x;
     for (int e0 = 0; e0 < r.E; e0 += 32) {
-        int slot;
-        const uint32_t open = open_experts(r.slot, bt, r.E, e0, n, lane, slot);
         const float gate = e0 + lane < r.E ? __ldg(G + bt * r.E + e0 + lane) : 0.f;
+        int slot;
+        uint32_t m = open_experts(r.slot, bt, r.E, e0, n, lane, slot);
         float mine = 0.f;                                   // lane e's dG
-        for (uint32_t m = open; m; m &= m - 1) {
+        while (m) {
             const int e = __ffs(m) - 1;
-            const size_t row = (size_t)__shfl_sync(0xffffffffu, slot, e) * D;
-            const float g = __shfl_sync(0xffffffffu, gate, e);
-            float dot = 0.f;
-            for (int p0 = lane; p0 < pieces; p0 += 32 * H) {
-                P y[H], d[H];
+            m &= m - 1;
+            const bool two = m != 0;
+            const int f = two ? __ffs(m) - 1 : e;
+            m &= m - 1;
+            const size_t row = (size_t)__shfl_sync(0xffffffffu, slot, e) * D, row2 = (size_t)__shfl_sync(0xffffffffu, slot, f) * D;
+            const float g = __shfl_sync(0xffffffffu, gate, e), g2 = __shfl_sync(0xffffffffu, gate, f);
+            float dot = 0.f, dot2 = 0.f;
+            for (int p0 = first; p0 < pieces; p0 += STEP * H) {
+                P y[H], z[H], d[H];
 #pragma unroll
                 for (int i = 0; i < H; ++i)
-                    if (p0 + 32 * i < pieces) {
-                        d[i].load(dV + bt * D + (size_t)(p0 + 32 * i) * N);
-                        y[i].load(Y + row + (size_t)(p0 + 32 * i) * N);
+                    if (p0 + STEP * i < pieces) {
+                        const size_t at = (size_t)(p0 + STEP * i) * N;
+                        d[i].load(dV + bt * D + at);
+                        y[i].load(Y + row + at);
+                        if (two) z[i].load(Y + row2 + at);
                     }
 #pragma unroll
                 for (int i = 0; i < H; ++i)
-                    if (p0 + 32 * i < pieces) {
+                    if (p0 + STEP * i < pieces) {
+                        const size_t at = (size_t)(p0 + STEP * i) * N;
                         float o[N];
+                        P q;
 #pragma unroll
                         for (int k = 0; k < N; ++k) {
                             dot = fmaf(y[i].get(k), d[i].get(k), dot);
                             o[k] = g * d[i].get(k);
                         }
-                        P q;
                         q.set(o);
-                        q.store(dY + row + (size_t)(p0 + 32 * i) * N);
+                        q.store(dY + row + at);
+                        if (two) {
+#pragma unroll
+                            for (int k = 0; k < N; ++k) {
+                                dot2 = fmaf(z[i].get(k), d[i].get(k), dot2);
+                                o[k] = g2 * d[i].get(k);
+                            }
+                            q.set(o);
+                            q.store(dY + row2 + at);
+                        }
                     }
             }
             dot = warp_sum(dot);
+            dot2 = warp_sum(dot2);
+            if constexpr (WARPS > 1) {                      // the same mask in every warp of the CTA
+                __syncthreads();
+                if (lane == 0) sums[0][warp] = dot, sums[1][warp] = dot2;
+                __syncthreads();
+                dot = dot2 = 0.f;
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) dot += sums[0][w], dot2 += sums[1][w];
+            }
             if (lane == e) mine = dot;
+            if (two && lane == f) mine = dot2;
         }
-        if (e0 + lane < r.E) dG[bt * r.E + e0 + lane] = mine;
+        if (e0 + lane < r.E && (WARPS == 1 || warp == 0)) dG[bt * r.E + e0 + lane] = mine;
     }
 }
+
+// Up to this many rows the gates' gradient takes four warps a row.
+constexpr int kFewRows = 4096;
 
 bool aligned_rows(std::initializer_list<const void*> ps, int D, int esz) {
     for (const void* p : ps)
         if (!fp8_on(p, 16)) return false;
     return D * (long long)esz % 16 == 0;
 }
-dim3 row_grid(const ExpertRows& r) { return dim3((unsigned)(((long long)r.B * r.T + kRowWarps - 1) / kRowWarps)); }
 const dim3 kRowBlock(32 * kRowWarps);
+// CTAs for `runs` warps a row.
+bool row_grid(const ExpertRows& r, long long runs, dim3* grid) {
+    const long long ctas = ((long long)r.B * r.T * runs + kRowWarps - 1) / kRowWarps;
+    *grid = dim3((unsigned)ctas);
+    return ctas <= 0x7fffffffll;
+}
+template <bool VEC>
+int runs_of(int D, int esz) {
+    const int per = 32 * kHeld<VEC> * (VEC ? 16 / esz : 1);
+    return (int)(((long long)D + per - 1) / per);
+}
 
+template <typename T, bool VEC>
+cudaError_t gather_v(const T* X, const ExpertRows& r, T* Xs, long long n, int D, cudaStream_t s) {
+    const int runs = runs_of<VEC>(D, sizeof(T));
+    dim3 grid;
+    if (!row_grid(r, runs, &grid)) return cudaErrorNotSupported;
+    return launch_k(gather_kernel<T, VEC>, grid, kRowBlock, 0, s, X, r, Xs, n, D, runs);
+}
 template <typename T>
 cudaError_t gather(const T* X, const ExpertRows& r, T* Xs, long long n, int D, cudaStream_t s) {
-    auto k = aligned_rows({X, Xs}, D, sizeof(T)) ? gather_kernel<T, true> : gather_kernel<T, false>;
-    return launch_k(k, row_grid(r), kRowBlock, 0, s, X, r, Xs, n, D);
+    return aligned_rows({X, Xs}, D, sizeof(T)) ? gather_v<T, true>(X, r, Xs, n, D, s) : gather_v<T, false>(X, r, Xs, n, D, s);
 }
 template <typename T>
 cudaError_t gather_fp4(const T* X, const ExpertRows& r, const Fp4View& out, long long n, int D, cudaStream_t s) {
     auto k = aligned_rows({X}, D, sizeof(T)) ? gather_fp4_kernel<T, true> : gather_fp4_kernel<T, false>;
-    return launch_k(k, row_grid(r), kRowBlock, 0, s, X, r, out, n, D, (int)fp4_blocks(D));
+    const int nb = (int)fp4_blocks(D), runs = (2 * nb + 31) / 32;
+    dim3 grid;
+    if (!row_grid(r, runs, &grid)) return cudaErrorNotSupported;
+    return launch_k(k, grid, kRowBlock, 0, s, X, r, out, n, D, nb, runs);
+}
+template <typename T, typename TO, bool VEC>
+cudaError_t combine_v(const T* Y, const ExpertRows& r, const float* G, TO* V, long long n, int D, cudaStream_t s) {
+    const int runs = runs_of<VEC>(D, sizeof(T));
+    dim3 grid;
+    if (!row_grid(r, runs, &grid)) return cudaErrorNotSupported;
+    return launch_k(combine_kernel<T, TO, VEC>, grid, kRowBlock, 0, s, Y, r, G, V, n, D, runs);
 }
 template <typename T, typename TO>
 cudaError_t combine(const T* Y, const ExpertRows& r, const float* G, TO* V, long long n, int D, cudaStream_t s) {
-    auto k = aligned_rows({Y, V}, D, sizeof(T)) ? combine_kernel<T, TO, true> : combine_kernel<T, TO, false>;
-    return launch_k(k, row_grid(r), kRowBlock, 0, s, Y, r, G, V, n, D);
+    return aligned_rows({Y, V}, D, sizeof(T)) ? combine_v<T, TO, true>(Y, r, G, V, n, D, s)
+                                              : combine_v<T, TO, false>(Y, r, G, V, n, D, s);
+}
+template <typename T, bool VEC>
+cudaError_t combine_backward_v(const T* dV, const T* Y, const ExpertRows& r, const float* G, T* dY, float* dG, long long n,
+                               int D, cudaStream_t s) {
+    const bool few = (long long)r.B * r.T <= kFewRows;
+    dim3 grid;
+    if (!row_grid(r, few ? kRowWarps : 1, &grid)) return cudaErrorNotSupported;
+    auto k = few ? combine_backward_kernel<T, VEC, kRowWarps> : combine_backward_kernel<T, VEC, 1>;
+    return launch_k(k, grid, kRowBlock, 0, s, dV, Y, r, G, dY, dG, n, D);
 }
 template <typename T>
 cudaError_t combine_backward(const T* dV, const T* Y, const ExpertRows& r, const float* G, T* dY, float* dG, long long n,
                              int D, cudaStream_t s) {
-    auto k = aligned_rows({dV, Y, dY}, D, sizeof(T)) ? combine_backward_kernel<T, true> : combine_backward_kernel<T, false>;
-    return launch_k(k, row_grid(r), kRowBlock, 0, s, dV, Y, r, G, dY, dG, n, D);
+    return aligned_rows({dV, Y, dY}, D, sizeof(T)) ? combine_backward_v<T, true>(dV, Y, r, G, dY, dG, n, D, s)
+                                                   : combine_backward_v<T, false>(dV, Y, r, G, dY, dG, n, D, s);
 }
 bool rows_ok(const ExpertRows& r, long long n, int D) {
     return r.B >= 1 && r.T >= 1 && r.E >= 1 && (long long)r.B * r.T * r.E < (1ll << 31) && r.slot && n >= 0 && D >= 1;
@@ -450,14 +538,14 @@ bool rows_ok(const ExpertRows& r, long long n, int D) {
 
 long long expert_sort_work(int B, int T, int E) {
     const long long TE = (long long)T * E;
-    return sorts_at_once(B, TE) ? TE : (kSortWarps + 1) * TE;
+    return sorts_at_once(B, TE) ? 0 : (kSortWarps + 1) * TE;
 }
 
 cudaError_t launch_expert_sort(const float* G, const ExpertRows& r, int* work, cudaStream_t s) {
-    RM_HOST_BOUNDS(G && rows_ok(r, 0, 1) && r.offsets && r.source && fp8_on(r.tiles, 16) && work);
+    RM_HOST_BOUNDS(G && rows_ok(r, 0, 1) && r.offsets && r.source && fp8_on(r.tiles, 16));
     const int TE = r.T * r.E;
     if (sorts_at_once(r.B, TE))
-        return launch_k(sort_small_kernel, dim3(1), dim3(kSortThreads), 0, s, G, TE, r, work);
+        return launch_k(sort_small_kernel, dim3(1), dim3(kSortThreads), 0, s, G, TE, r);
     int *totals = work, *counts = work + TE;
     const unsigned ctas = (unsigned)((TE + kCols - 1) / kCols);
     const cudaError_t e = launch_k(sort_count_kernel, dim3(ctas), dim3(kSortThreads), 0, s, G, r.B, TE, counts, totals);

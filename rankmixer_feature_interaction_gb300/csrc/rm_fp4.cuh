@@ -64,28 +64,69 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     return r;
 }
 
-// Eight values of a row from p on as float, the first n of them (the rest zero).  VEC:
-// p is 16-byte aligned where n is 8 or more.
-template <typename IN, bool VEC>
-__device__ __forceinline__ void fp4_load8(const IN* __restrict__ p, int n, float (&v)[8]) {
-    if (VEC && n >= 8) {
-        if constexpr (sizeof(IN) == 2) {
-            const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// Sixteen values of a row as they lie in memory, zeros past its end.
+template <typename IN>
+struct Fp4Raw16 {
+    static constexpr int WORDS = 4 * sizeof(IN);
+    uint32_t w[WORDS];
+    // VEC: p is 16-byte aligned where n is 16 or more
+    template <bool VEC>
+    __device__ __forceinline__ void load(const IN* __restrict__ p, int n) {
+        if (VEC && n >= 16) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(u[i] << 16);
-                v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            for (int i = 0; i < WORDS / 4; ++i) {
+                const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+                w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
             }
         } else {
-            const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        }
-    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
+            for (int i = 0; i < WORDS; ++i) {
+                if constexpr (sizeof(IN) == 4) {
+                    w[i] = i < n ? __float_as_uint(p[i]) : 0u;
+                } else {
+                    w[i] = 2 * i < n ? __bfloat16_as_ushort(p[2 * i]) : 0u;
+                    if (2 * i + 1 < n) w[i] |= (uint32_t)__bfloat16_as_ushort(p[2 * i + 1]) << 16;
+                }
+            }
+        }
     }
-}
+    // float bits of the largest magnitude; infinities and NaN count as they are
+    __device__ __forceinline__ uint32_t amax_bits() const {
+        uint32_t m = 0;
+        if constexpr (sizeof(IN) == 2) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+            return max(m << 16, m & 0xffff0000u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) m = max(m, w[i] & 0x7fffffffu);
+            return m;
+        }
+    }
+    __device__ __forceinline__ uint32_t codes(int half, uint64_t scale) const {
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint64_t pair;
+            if constexpr (sizeof(IN) == 2) {
+                const uint32_t x = w[4 * half + i];
+                pair = f2_pack(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+            } else {
+                pair = f2_pack(__uint_as_float(w[8 * half + 2 * i]), __uint_as_float(w[8 * half + 2 * i + 1]));
+            }
+            f2_unpack(f2_mul(pair, scale), q[2 * i], q[2 * i + 1]);
+        }
+        return fp4_pack8(q);
+    }
+    // Codes, by the scale of the block that this lane and its neighbour (lane ^ 1) hold.
+    __device__ __forceinline__ uint2 round(uint32_t& E) const {
+        uint32_t m = amax_bits();
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        E = fp4_exponent(m);
+        const uint64_t s = f2_splat(fp4_inv_scale(E));
+        return make_uint2(codes(0, s), codes(1, s));
+    }
+};
 
 // Eight values of one of a block's four lanes (neighbours) to their codes; E: the block's exponent byte.
 __device__ __forceinline__ uint32_t fp4_round8(float (&v)[8], uint32_t& E) {

@@ -30,60 +30,6 @@ __device__ __forceinline__ void advance(unsigned long long& row, int& j, int dq,
     if (j >= n) j -= n, ++row;
 }
 
-// Sixteen values of a row as they lie in memory, zeros past its end.
-template <typename IN>
-struct Raw16 {
-    static constexpr int WORDS = 4 * sizeof(IN);
-    uint32_t w[WORDS];
-    __device__ __forceinline__ void load(const IN* __restrict__ p, int n) {
-        if (n >= 16) {
-#pragma unroll
-            for (int i = 0; i < WORDS / 4; ++i) {
-                const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-                w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < WORDS; ++i) {
-                if constexpr (sizeof(IN) == 4) {
-                    w[i] = i < n ? __float_as_uint(p[i]) : 0u;
-                } else {
-                    w[i] = 2 * i < n ? __bfloat16_as_ushort(p[2 * i]) : 0u;
-                    if (2 * i + 1 < n) w[i] |= (uint32_t)__bfloat16_as_ushort(p[2 * i + 1]) << 16;
-                }
-            }
-        }
-    }
-    // float bits of the largest magnitude; infinities and NaN count as they are
-    __device__ __forceinline__ uint32_t amax_bits() const {
-        uint32_t m = 0;
-        if constexpr (sizeof(IN) == 2) {
-#pragma unroll
-            for (int i = 0; i < WORDS; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-            return max(m << 16, m & 0xffff0000u);
-        } else {
-#pragma unroll
-            for (int i = 0; i < WORDS; ++i) m = max(m, w[i] & 0x7fffffffu);
-            return m;
-        }
-    }
-    __device__ __forceinline__ uint32_t codes(int half, uint64_t scale) const {
-        float q[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint64_t pair;
-            if constexpr (sizeof(IN) == 2) {
-                const uint32_t x = w[4 * half + i];
-                pair = f2_pack(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-            } else {
-                pair = f2_pack(__uint_as_float(w[8 * half + 2 * i]), __uint_as_float(w[8 * half + 2 * i + 1]));
-            }
-            f2_unpack(f2_mul(pair, scale), q[2 * i], q[2 * i + 1]);
-        }
-        return fp4_pack8(q);
-    }
-};
-
 template <typename IN>
 constexpr int kInFlight = sizeof(IN) == 2 ? 4 : 2;      // pieces of 16 values per thread
 
@@ -98,23 +44,21 @@ quantize_kernel(const IN* __restrict__ X, unsigned long long pieces, int cols, i
     unsigned long long row;
     int j;
     split(base, pieces <= 0xffffffffull, 2u * nb, row, j);
-    Raw16<IN> v[UNROLL];
+    Fp4Raw16<IN> v[UNROLL];
     unsigned long long at = row;
     int k = j;
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
         const bool there = base + (unsigned long long)u * kThreads < pieces;
-        v[u].load(X + at * ldx + 16 * k, there ? cols - 16 * k : 0);
+        v[u].template load<true>(X + at * ldx + 16 * k, there ? cols - 16 * k : 0);
         advance(at, k, dq, dr, 2 * nb);
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-        uint32_t m = v[u].amax_bits();
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        const uint32_t E = fp4_exponent(m);
-        const uint64_t s = f2_splat(fp4_inv_scale(E));
+        uint32_t E;
+        const uint2 c = v[u].round(E);
         if (base + (unsigned long long)u * kThreads < pieces) {
-            *reinterpret_cast<uint2*>(out.codes + row * out.ld + 8 * j) = make_uint2(v[u].codes(0, s), v[u].codes(1, s));
+            *reinterpret_cast<uint2*>(out.codes + row * out.ld + 8 * j) = c;
             if ((j & 1) == 0) out.scales[row * out.lds + (j >> 1)] = (uint8_t)E;
         }
         advance(row, j, dq, dr, 2 * nb);

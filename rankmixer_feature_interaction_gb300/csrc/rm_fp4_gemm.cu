@@ -547,7 +547,7 @@ cudaError_t launch_fp4_product(const Fp4Product& p, const Fp8Device& dev, cudaSt
     RM_HOST_BOUNDS(fp8_on(p.w.codes, 16) && fp8_on(p.w.scales, 16) && p.w.lds == fp4_weight_quads(p.K) &&
                    p.w.ld % 16 == 0 && p.w.ld >= 16 * fp4_blocks(p.K) && (!p.bias || fp8_on(p.bias, 16)));
     RM_HOST_BOUNDS(p.epi == FP4_GELU ? p.N % 32 == 0 && fp4_holds(p.o, p.N) : fp8_on(p.y, 16));
-    if (p.B <= kFp4StreamMaxB) return launch_fp4_stream(p, dev, s);
+    if (fp4_streams(p, dev)) return launch_fp4_stream(p, dev, s);
     Args a{};
     a.B = p.B, a.G = p.G, a.K = p.K, a.N = p.N;
     a.m_tiles = (p.B + 2 * BM - 1) / (2 * BM);

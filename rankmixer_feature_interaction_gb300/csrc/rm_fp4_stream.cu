@@ -48,8 +48,8 @@ struct Cfg {
 
 struct Args {
     int B, G, K, N;
-    int n_tiles, kblocks, nb;
-    long long tiles;                     // per token
+    int n_tiles, m_tiles, kblocks, nb;
+    uint32_t tiles;                      // per token
     const int4* table;                   // experts: as in rm_fp4_gemm.cu
     long long n, step;
     const uint8_t* xs;
@@ -65,21 +65,33 @@ struct Args {
 };
 
 struct Tile {
-    RowTile r;
-    int n0;
+    int g, m0, rows, n0;
 };
+// Tiles of rows fastest (per token): those that share a weight tile run side by side.
 template <bool EXPERTS>
-__device__ __forceinline__ Tile tile_of(long long i, const Args& a) {
-    const long long l = i / a.n_tiles;
+__device__ __forceinline__ Tile tile_of(uint32_t i, const Args& a) {
     Tile t;
+    t.m0 = 0;
+    if (!EXPERTS && a.m_tiles > 1) {
+        const uint32_t q = i / (uint32_t)a.m_tiles;
+        t.m0 = (int)(i - q * a.m_tiles) * kFp4StreamMaxB;
+        i = q;
+    }
+    const uint32_t l = i / (uint32_t)a.n_tiles;
     t.n0 = (int)(i - l * a.n_tiles) * BM;
     if (EXPERTS) {
         const int4 e = __ldg(a.table + 1 + l);
-        t.r = RowTile{e.x, e.y, 0, (int)min((long long)e.z, max(a.n - e.y, 0ll)), e.y};
+        t.g = e.x, t.m0 = e.y;
+        t.rows = (int)min((long long)e.z, a.n - e.y);
     } else {
-        t.r = RowTile{(int)l, 0, (int)l, a.B, l};
+        t.g = (int)l;
+        t.rows = a.B - t.m0;
     }
     return t;
+}
+template <bool EXPERTS>
+__device__ __forceinline__ long long row_of(const Tile& t, int i, const Args& a) {
+    return EXPERTS ? (long long)t.m0 + i : (long long)(t.m0 + i) * a.G + t.g;
 }
 
 // Eight rows' codes of one column each in a lane to eight columns' of one row: lane
@@ -135,12 +147,12 @@ fp4_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     tc_fence_after();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
     const int kblocks = args.kblocks;
-    const long long units = gridDim.x;
+    const uint32_t units = gridDim.x;
     if (!(args.early && warp == 0)) {
         pdl_wait();
         pdl_launch_next();
     }
-    const long long tiles = EXPERTS ? (long long)__ldg(&args.table[0].x) * args.n_tiles : args.tiles;
+    const uint32_t tiles = EXPERTS ? (uint32_t)__ldg(&args.table[0].x) * (uint32_t)args.n_tiles : args.tiles;
 
     if (warp == 0 || warp == 3) {
         // ------------------------------ TMA producers -----------------------------
@@ -149,10 +161,10 @@ fp4_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         bool ok = true;
         Tile next{};
         if (blockIdx.x < tiles) next = tile_of<EXPERTS>(blockIdx.x, args);
-        for (long long i = blockIdx.x; ok && i < tiles; i += units) {
+        for (uint32_t i = blockIdx.x; ok && i < tiles; i += units) {
             const Tile tl = next;
             if (i + units < tiles) next = tile_of<EXPERTS>(i + units, args);
-            const uint8_t* sf = args.ws + (((long long)tl.r.g * args.n_tiles + tl.n0 / BM) * args.quads) * QUAD_BYTES;
+            const uint8_t* sf = args.ws + (((long long)tl.g * args.n_tiles + tl.n0 / BM) * args.quads) * QUAD_BYTES;
             for (int kb = 0; kb < kblocks; ++kb) {
                 if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
                     ok = false;
@@ -161,11 +173,11 @@ fp4_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 if (elect_one()) {
                     if (warp == 0) {
                         mbar_arrive_expect_tx(full_bar(stage), W_BYTES + SF_BYTES);
-                        tma_load_3d(&tmW, sW + stage * W_BYTES, full_bar(stage), kb * 128, tl.n0, tl.r.g);
+                        tma_load_3d(&tmW, sW + stage * W_BYTES, full_bar(stage), kb * 128, tl.n0, tl.g);
                         bulk_copy_g2s(sSFW + stage * SF_BYTES, sf + (size_t)kb * SF_BYTES, SF_BYTES, full_bar(stage));
                     } else {
                         mbar_arrive_expect_tx(full_bar(stage), C::X_BYTES);
-                        tma_load_3d(&tmX, sX + stage * C::X_BYTES, full_bar(stage), kb * 128, tl.r.row, tl.r.plane);
+                        tma_load_3d(&tmX, sX + stage * C::X_BYTES, full_bar(stage), kb * 128, tl.m0, EXPERTS ? 0 : tl.g);
                     }
                 }
                 __syncwarp();
@@ -180,7 +192,7 @@ fp4_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0, slot = 0;
         bool ok = true;
-        for (long long i = blockIdx.x; ok && i < tiles; i += units) {
+        for (uint32_t i = blockIdx.x; ok && i < tiles; i += units) {
             if (!wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_flag, args.err, args.timeout_ns)) break;
             tc_fence_after();
             const uint32_t d = tmem_base + (uint32_t)(acc * NB);
@@ -220,13 +232,13 @@ fp4_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         // ------------------------------ scales of x -------------------------------
         const int groups = (kblocks + 1) / 2;
         typename C::Scales sc(sRing);
-        long long i = blockIdx.x;                        // of the next step to fetch
+        uint32_t i = blockIdx.x;                         // of the next step to fetch
         int g = 0;
         Tile tl{};
         if (i < tiles) tl = tile_of<EXPERTS>(i, args);
         auto fetch = [&]() {
             if (i >= tiles) return sc.done();
-            sc.fetch(args.xs + tl.r.at * args.xs_ld, args.step * args.xs_ld, tl.r.rows, g, lane);
+            sc.fetch(args.xs + row_of<EXPERTS>(tl, 0, args) * args.xs_ld, args.step * args.xs_ld, tl.rows, g, lane);
             if (++g == groups) {
                 g = 0, i += units;
                 if (i < tiles) tl = tile_of<EXPERTS>(i, args);
@@ -237,7 +249,7 @@ fp4_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (long long j = blockIdx.x; ok && j < tiles; j += units)
+        for (uint32_t j = blockIdx.x; ok && j < tiles; j += units)
             for (int kb = 0; ok && kb < kblocks; kb += 2) {
                 sc.take(kb / 2, args.nb, lane);
 #pragma unroll
@@ -262,12 +274,12 @@ fp4_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         const int quad = warp & 3, j0 = NS * ((warp - 4) >> 2);
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (long long i = blockIdx.x; i < tiles; i += units) {
+        for (uint32_t i = blockIdx.x; i < tiles; i += units) {
             const Tile tl = tile_of<EXPERTS>(i, args);
             const int n = tl.n0 + 32 * quad + lane;
-            const float bias = args.bias && n < args.N ? __ldg(args.bias + (size_t)tl.r.g * args.N + n) : 0.f;
-            const int count = tl.r.rows - j0;            // rows of this thread that exist: the first `count` (may be <= 0)
-            const long long row0 = tl.r.at + j0 * args.step;
+            const float bias = args.bias && n < args.N ? __ldg(args.bias + (size_t)tl.g * args.N + n) : 0.f;
+            const int count = tl.rows - j0;            // rows of this thread that exist: the first `count` (may be <= 0)
+            const long long row0 = row_of<EXPERTS>(tl, j0, args);
             if (!wait_bounded(tfull_bar(acc), acc_phase, abort_flag, args.err, args.timeout_ns)) break;
             tc_fence_after();
             uint32_t r[NS];
@@ -331,8 +343,8 @@ cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const Args& a, int
     auto k = fp4_stream_kernel<EPI, NB, EXPERTS>;
     const cudaError_t e = smem_attr_once((const void*)k, Cfg<NB>::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    const long long ctas = EXPERTS || a.tiles > num_sms ? num_sms : a.tiles;
-    return launch_k(k, dim3((unsigned)ctas), dim3(Cfg<NB>::THREADS), Cfg<NB>::SMEM_BYTES, s, mx, mw, a);
+    const uint32_t ctas = EXPERTS || a.tiles > (uint32_t)num_sms ? (uint32_t)num_sms : a.tiles;
+    return launch_k(k, dim3(ctas), dim3(Cfg<NB>::THREADS), Cfg<NB>::SMEM_BYTES, s, mx, mw, a);
 }
 
 template <int EPI, bool EXPERTS>
@@ -345,6 +357,12 @@ cudaError_t run_for(const CUtensorMap& mx, const CUtensorMap& mw, const Args& a,
 
 }  // namespace f4s
 
+bool fp4_streams(const Fp4Product& p, const Fp8Device& dev) {
+    if (p.B <= kFp4StreamMaxB) return true;
+    const long long m = (p.B + kFp4StreamMaxB - 1) / kFp4StreamMaxB, n = (p.N + f4s::BM - 1) / f4s::BM;
+    return !p.tiles && m * n * p.G <= dev.num_sms;
+}
+
 cudaError_t launch_fp4_stream(const Fp4Product& p, const Fp8Device& dev, cudaStream_t s) {
     using namespace f4s;
     Args a{};
@@ -352,7 +370,10 @@ cudaError_t launch_fp4_stream(const Fp4Product& p, const Fp8Device& dev, cudaStr
     a.n_tiles = (p.N + BM - 1) / BM;
     a.kblocks = (p.K + BK - 1) / BK;
     a.nb = (int)fp4_blocks(p.K);
-    a.tiles = (long long)p.G * a.n_tiles;
+    a.m_tiles = p.tiles ? 1 : (p.B + kFp4StreamMaxB - 1) / kFp4StreamMaxB;
+    const long long tiles = (long long)p.G * a.n_tiles * a.m_tiles;
+    if (tiles >= 1ll << 31) return cudaErrorNotSupported;        // more tiles than a device's memory holds weights for
+    a.tiles = (uint32_t)tiles;
     a.table = p.tiles;
     a.n = p.n;
     a.step = p.tiles ? 1 : p.G;

@@ -117,18 +117,13 @@ struct RowScales {
     }
 };
 
-// A tile of rows of one group: row i lies at (row + i step) of x and of the output,
-// its codes at coordinates (row, plane) of x's tensor map.
-struct RowTile {
-    int g, row, plane, rows;
-    long long at;
-};
-
 }  // namespace f4
 
 // Groups of up to this many rows: the weights are streamed past all of them at once
-// (launch_fp4_stream) instead of in tiles of 256 rows.
+// (launch_fp4_stream) instead of in tiles of 256 rows.  So are those of more samples
+// where that makes no more tiles than SMs (per token).
 constexpr int kFp4StreamMaxB = 128;
+bool fp4_streams(const Fp4Product& p, const Fp8Device& dev);
 cudaError_t launch_fp4_stream(const Fp4Product& p, const Fp8Device& dev, cudaStream_t s);
 
 }  // namespace rm
