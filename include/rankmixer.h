@@ -617,7 +617,8 @@ RM_API rm_status rm_debug_fp8_wait_timeout(int timeout_us, void *stream);
  * 6 2^(E - 127), so that no value saturates, and round value / 2^(E - 127) to
  * the nearest code, ties to the even one.  A block with an infinity or a NaN
  * has E = 255 and is NaN as a whole (the codes have neither).  Restoring is
- * exact in float32 (and in bf16, except below 2^-133).
+ * exact in float32 (and in bf16, except below 2^-133); magnitudes above
+ * 7/8 2^128 round to 2^128, which is an infinity there.
  *   Activations: rows of `cols` values; row r has its codes at codes + r ld (ld
  *     a multiple of 16, at least 16 ceil(cols / 32)) and the byte of its block j
  *     at scales + r lds + j (lds a multiple of 16, at least ceil(cols / 32)).

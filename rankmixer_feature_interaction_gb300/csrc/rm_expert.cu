@@ -561,7 +561,7 @@ cudaError_t launch_expert_gather(const void* X, bool f32, const ExpertRows& r, v
                : gather(static_cast<const __nv_bfloat16*>(X), r, static_cast<__nv_bfloat16*>(Xs), n, D, s);
 }
 
-cudaError_t launch_expert_gather_fp4(const void* X, bool f32, const ExpertRows& r, const Fp4View& out, long long n, int D,
+cudaError_t launch_fp4_expert_gather(const void* X, bool f32, const ExpertRows& r, const Fp4View& out, long long n, int D,
                                      cudaStream_t s) {
     RM_HOST_BOUNDS(X && rows_ok(r, n, D) && fp4_holds(out, D));
     return f32 ? gather_fp4(static_cast<const float*>(X), r, out, n, D, s)

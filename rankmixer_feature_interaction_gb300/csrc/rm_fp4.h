@@ -54,7 +54,7 @@ cudaError_t launch_expert_sort(const float* G, const ExpertRows& r, int* work, c
 // Xs[slot] = X[b][t] for every open slot below n; or the same row in 4 bits.
 cudaError_t launch_expert_gather(const void* X, bool f32, const ExpertRows& r, void* Xs, long long n, int D,
                                  cudaStream_t s);
-cudaError_t launch_expert_gather_fp4(const void* X, bool f32, const ExpertRows& r, const Fp4View& out, long long n, int D,
+cudaError_t launch_fp4_expert_gather(const void* X, bool f32, const ExpertRows& r, const Fp4View& out, long long n, int D,
                                      cudaStream_t s);
 // V[b][t] = sum over the open e of G[b][t][e] Y[slot] (G null: of Y[slot]).
 cudaError_t launch_expert_combine(const void* Y, bool y_f32, const ExpertRows& r, const float* G, void* V, bool v_f32,

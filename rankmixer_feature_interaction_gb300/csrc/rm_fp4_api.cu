@@ -327,7 +327,7 @@ rm_status rm_fp4_expert_gather(const void* X, rm_dtype dtype, const rm_expert_ro
     if (!aligned(X, size_of(dtype))) return fail(RM_ERR_INVALID_ARG, "X must be aligned to its elements");
     if (n == 0) return RM_OK;
     RM_CHECK(check_tensor(out, D, "out", false));
-    RM_LAUNCH(expert_gather_fp4, "gather", X, dtype == RM_F32, sorted(*rows), view(*out), n, D, as_stream(stream));
+    RM_LAUNCH(fp4_expert_gather, "gather", X, dtype == RM_F32, sorted(*rows), view(*out), n, D, as_stream(stream));
     return RM_OK;
 }
 
@@ -399,7 +399,7 @@ rm_status rm_fp4_moe_forward(const rm_fp4_moe* p, const void* X, rm_dtype x_dtyp
     Fp8Device dev;
     RM_CHECK(fp8_device(&dev));
     RM_LAUNCH(expert_sort, "sort by expert", G, w.rows, w.sort, s);
-    RM_LAUNCH(expert_gather_fp4, "gather", X, x_dtype == RM_F32, w.rows, w.x, w.n, D, s);
+    RM_LAUNCH(fp4_expert_gather, "gather", X, x_dtype == RM_F32, w.rows, w.x, w.n, D, s);
     Fp4Product g = product(RM_BF16, w.x, view(p->W1), p->b1, nullptr, B, groups, D, F);
     g.epi = FP4_GELU;
     g.o = w.a;

@@ -24,7 +24,7 @@ def gates(B, T, E, share, seed):
 
 
 SORTS = [(1, 1, 1), (1, 3, 5), (8, 32, 8), (64, 32, 8), (65, 32, 8), (64, 3, 90), (63, 1, 1), (130, 1, 1), (129, 5, 7),
-         (500, 2, 33), (1000, 3, 4), (4100, 1, 9), (257, 16, 40), (2, 700, 12), (3000, 4, 2)]
+         (500, 2, 33), (1000, 3, 4), (4100, 1, 9), (257, 16, 40), (2, 700, 12), (3000, 4, 2), (4, 400, 10)]
 
 
 @pytest.mark.parametrize("B,T,E", SORTS)
