@@ -6,7 +6,8 @@
 // loaded stays as it came until it is rounded: few registers, so many loads under way.
 // Rows that are not 16-byte aligned are read (or written) an element at a time,
 // neighbouring lanes neighbouring elements, and change their order in shared memory.
-// Bound by memory: 2.53 bytes a value from bf16.
+// Measured, 65,536 rows of 6144 in bf16: to 4 bits 147 us (6.9 TB/s; 326 with eight values
+// a lane, unpacked at once), back 154 us (6.6 TB/s): bound by memory, 2.53 bytes a value.
 #include "rm_fp4.cuh"
 
 namespace rm {

@@ -23,6 +23,13 @@
 // columns have been read (first), and two slots of exponent bytes from column 448 (8 columns
 // for x, 16 for W).  Copies and MMAs of one thread run in order, so the slots need no
 // barriers of their own.
+// Measured, T = 32, 4096 samples, bf16 out: 6144 to 1536 340 us (7.3 PFLOP/s), 1536 to
+// 6144 466 us (5.3; float32 out 620, 3.2 GB written); T = 4, 12288 to 6144 315 us (7.9).
+// Bound by what the SMs take in from L2: a k-block of a CTA is 35 KB in 512 cycles of the
+// tensor core, 68 bytes a cycle, and comes in about 630; with few k-blocks a tile also
+// by the outputs' way through shared memory, which the tensor core's operands share
+// (1536 to 6144 without an epilogue: 366 us), and with Gelu by its instructions beside
+// them (2048 samples: 260 us, 195 without).
 // Every mbarrier wait is bounded in time; on expiry the CTA latches an error
 // word and all roles unwind.
 #include <cudaTypedefs.h>
@@ -39,9 +46,9 @@ constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int TX_BYTES = STAGE_BYTES + SFB_BYTES;       // what TMA brings to a CTA's stage
 constexpr int STAGES = 5;
 constexpr int EPI_WARPS = 16, GROUP_WARPS = 8;
-constexpr int COLS = 64;                 // columns of a thread at a time, half of a warp's
+constexpr int WARP_COLS = 128, CHUNK = 32;      // columns of a warp, and of a thread at a time
 constexpr int STAGING = 2048;            // per epilogue warp: 32 rows of 64 bytes
-constexpr int BIAS_BYTES = COLS * 4;     // per epilogue warp
+constexpr int BIAS_BYTES = 2 * CHUNK * 4;       // per epilogue warp
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr uint32_t ACC1_COL = 192;       // the second accumulator's first column
 constexpr uint32_t SF_COL = 448, SF_COLS = 24;
@@ -415,7 +422,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             if (args.bias) {
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    const int c = next.n0 + 2 * COLS * part + 32 * h + lane;
+                    const int c = next.n0 + WARP_COLS * part + 32 * h + lane;
                     b[h] = c < args.N ? __ldg(args.bias + (size_t)next.g * args.N + c) : 0.f;
                 }
             }
@@ -423,80 +430,90 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
         look_ahead(unit + acc * nunits);
         for (uint32_t i = unit + acc * nunits; i < tiles; i += 2 * nunits) {
             const Tile tl = next;
-            const int m_warp = BM * (int)rank + 32 * quad, n_warp = tl.n0 + 2 * COLS * part;
+            const int m_warp = BM * (int)rank + 32 * quad, n_warp = tl.n0 + WARP_COLS * part;
             const int rows = n_warp < args.N ? min(32, tl.rows - m_warp) : 0;     // this warp's rows that exist (may be negative)
             const long long row = row_of<EXPERTS>(tl, m_warp, args);
             if (!wait_bounded(tfull_bar(acc), phase, abort_flag, args.err, args.timeout_ns)) break;
             phase ^= 1u;
             tc_fence_after();
             uint32_t E = 0;                                  // (4-bit output) exponent bytes of the row's four blocks
-#pragma unroll 1
-            for (int k = 0; k < 2; ++k) {
-                const int half = k ^ first, n = n_warp + COLS * half;
-                float v[COLS];
-                {
-                    uint32_t r[2][32];
-                    const uint32_t tcol = tmem_base + ((uint32_t)(32 * quad) << 16) + (acc ? ACC1_COL : 0u) +
-                                          (uint32_t)(2 * COLS * part + COLS * half);
-                    tmem_ld32_nowait(tcol, r[0]);
-                    tmem_ld32_nowait(tcol + 32u, r[1]);
-                    if (args.bias) {
+            const uint32_t tcol =
+                tmem_base + ((uint32_t)(32 * quad) << 16) + (acc ? ACC1_COL : 0u) + (uint32_t)(WARP_COLS * part);
+            // 64 floats of the bias, for the two chunks to come
+            auto put_bias = [&](int half) {
+                if (!args.bias) return;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(bias + 128u * h + 4u * lane),
-                                         "f"(half ? b[2 + h] : b[h])
-                                         : "memory");
+                for (int h = 0; h < 2; ++h)
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(bias + 128u * h + 4u * lane), "f"(half ? b[2 + h] : b[h])
+                                 : "memory");
+            };
+            // 32 columns, the warp's chunk c
+            auto finish = [&](const uint32_t (&r)[CHUNK], int c) {
+                const int n = n_warp + CHUNK * c;
+                float v[CHUNK];
+#pragma unroll
+                for (int k = 0; k < CHUNK; ++k) v[k] = __uint_as_float(r[k]);
+                if (args.bias) {
+#pragma unroll
+                    for (int k = 0; k < CHUNK / 4; ++k) {
+                        float4 q;
+                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
+                                     : "r"(bias + 128u * (c & 1) + 16u * k));
+                        f2_unpack(f2_add(f2_pack(v[4 * k], v[4 * k + 1]), f2_pack(q.x, q.y)), v[4 * k], v[4 * k + 1]);
+                        f2_unpack(f2_add(f2_pack(v[4 * k + 2], v[4 * k + 3]), f2_pack(q.z, q.w)), v[4 * k + 2], v[4 * k + 3]);
                     }
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < COLS; ++c) v[c] = __uint_as_float(r[c >> 5][c & 31]);
                 }
-                tc_fence_before();
+                if constexpr (EPI == FP4_OUT_BF16) {
+                    save_piece<__nv_bfloat16, EXPERTS>(v, args, &tmY, tl.m0 + m_warp, plane_of<EXPERTS>(tl), row, n, rows,
+                                                       lane, stage);
+                } else if constexpr (EPI == FP4_OUT_F32) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        save_piece<float, EXPERTS>(v + 16 * h, args, &tmY, tl.m0 + m_warp, plane_of<EXPERTS>(tl), row,
+                                                   n + 16 * h, rows, lane, stage);
+                } else {
+                    uint32_t w[4], e;
+#pragma unroll
+                    for (int k = 0; k < CHUNK; k += 2) gelu2(v[k], v[k + 1]);
+                    round_block(v, w, e);
+                    st_shared_v4(staged_at(stage, lane, c), w[0], w[1], w[2], w[3]);
+                    E |= e << (8 * c);
+                }
+            };
+            // Two chunks at once, so that the shared columns are free early; the other two
+            // come, one by one, while a chunk is worked on: layer 1 at B = 2048 260 us, 270
+            // with 64 columns read, worked on and read again.
+            uint32_t r0[CHUNK], r1[CHUNK];
+            const int c0 = 2 * first, c2 = 2 - c0;
+            tmem_ld32_nowait(tcol + CHUNK * c0, r0);
+            tmem_ld32_nowait(tcol + CHUNK * (c0 + 1), r1);
+            put_bias(first);
+            if (EPI == FP4_GELU) staging_free(lane);
+            tmem_wait_ld32(r0);
+            tmem_wait_ld32(r1);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && owner) mbar_arrive_pair(mapa_shared(shared_bar, 0));
+            if (rows > 0) {                              // (as a loop: 356 us instead of 260, registers in memory)
+                finish(r0, c0);
+                tmem_ld32_nowait(tcol + CHUNK * c2, r0);
+                finish(r1, c0 + 1);
                 __syncwarp();
-                if (lane == 0) {
-                    if (k == 0 && owner) mbar_arrive_pair(mapa_shared(shared_bar, 0));
-                    if (k == 1) mbar_arrive_pair(mapa_shared(tempty_bar(acc), 0));
-                }
-                if (k == 1) look_ahead(i + 2 * nunits);
-                if (rows > 0) {
-                    if (args.bias) {
-#pragma unroll
-                        for (int c = 0; c < COLS / 4; ++c) {
-                            float4 q;
-                            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                         : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
-                                         : "r"(bias + 16u * c));
-                            f2_unpack(f2_add(f2_pack(v[4 * c], v[4 * c + 1]), f2_pack(q.x, q.y)), v[4 * c], v[4 * c + 1]);
-                            f2_unpack(f2_add(f2_pack(v[4 * c + 2], v[4 * c + 3]), f2_pack(q.z, q.w)), v[4 * c + 2],
-                                      v[4 * c + 3]);
-                        }
-                    }
-                    if constexpr (EPI == FP4_OUT_BF16) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            save_piece<__nv_bfloat16, EXPERTS>(v + 32 * h, args, &tmY, tl.m0 + m_warp, plane_of<EXPERTS>(tl),
-                                                               row, n + 32 * h, rows, lane, stage);
-                    } else if constexpr (EPI == FP4_OUT_F32) {
-#pragma unroll
-                        for (int h = 0; h < 4; ++h)
-                            save_piece<float, EXPERTS>(v + 16 * h, args, &tmY, tl.m0 + m_warp, plane_of<EXPERTS>(tl), row,
-                                                       n + 16 * h, rows, lane, stage);
-                    } else {
-                        if (k == 0) staging_free(lane);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t w[4], e;
-#pragma unroll
-                            for (int c = 0; c < 32; c += 2) gelu2(v[32 * h + c], v[32 * h + c + 1]);
-                            round_block(v + 32 * h, w, e);
-                            st_shared_v4(staged_at(stage, lane, 2 * half + h), w[0], w[1], w[2], w[3]);
-                            E |= e << (16 * half + 8 * h);
-                        }
-                        if (k == 1) save_codes<EXPERTS>(args, &tmY, tl, m_warp, row, n_warp, rows, E, lane, stage);
-                    }
-                }
+                put_bias(first ^ 1);
                 __syncwarp();
+                tmem_wait_ld32(r0);
+                tmem_ld32_nowait(tcol + CHUNK * (c2 + 1), r1);
+                finish(r0, c2);
+                tmem_wait_ld32(r1);
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(acc), 0));
+            if (rows > 0) finish(r1, c2 + 1);
+            look_ahead(i + 2 * nunits);
+            if (EPI == FP4_GELU && rows > 0) save_codes<EXPERTS>(args, &tmY, tl, m_warp, row, n_warp, rows, E, lane, stage);
+            __syncwarp();
         }
         if (lane == 0) bulk_wait_group<0>();
     }

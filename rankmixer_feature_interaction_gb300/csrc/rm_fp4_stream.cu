@@ -17,6 +17,13 @@
 // is one of this library's own launches of the same call, W was in memory before it
 // began, and warp 0 starts on it at once (per token; the experts' tiles are known only
 // after the sort); everything else waits for the predecessor's end.
+// Measured (in a graph, bf16 out): T = 32, K = 1536, N = 6144 27.7 us at 1 sample (160 MB:
+// 5.8 TB/s), 31.9 at 64, 35.0 at 128; K = 6144, N = 1536 (384 tiles, 2.5 rounds of the SMs)
+// 29.1, 30.1, 32.5; the experts of T = 32, E = 8, K = 1536, N = 2048 at 8 samples 54 us for
+// 384 MB of open weights, 7.1 TB/s.  The rest at one sample is the last, partly filled
+// round (11 where 10.1 would do) and the start.  Dividing that round's tiles into quarters
+// of 32 columns made it slower (29 to 39 us): a k-block's chain of loads, exponent bytes
+// and MMAs takes as long for a quarter.
 // Every mbarrier wait is bounded in time; on expiry the CTA latches an error
 // word and all roles unwind.
 #include <cudaTypedefs.h>
@@ -284,11 +291,13 @@ fp4_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             tc_fence_after();
             uint32_t r[NS];
             const uint32_t tcol = tmem_base + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * NB + j0);
-            if constexpr (NS == 16)
+            if constexpr (NS == 16) {
                 tmem_ld16_nowait(tcol, r);
-            else
+                tmem_wait_ld16(r);
+            } else {
                 tmem_ld32_nowait(tcol, r);
-            tmem_wait_ld();
+                tmem_wait_ld32(r);
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(tempty_bar(acc));
@@ -360,7 +369,7 @@ cudaError_t run_for(const CUtensorMap& mx, const CUtensorMap& mw, const Args& a,
 bool fp4_streams(const Fp4Product& p, const Fp8Device& dev) {
     if (p.B <= kFp4StreamMaxB) return true;
     const long long m = (p.B + kFp4StreamMaxB - 1) / kFp4StreamMaxB, n = (p.N + f4s::BM - 1) / f4s::BM;
-    return !p.tiles && m * n * p.G <= dev.num_sms;
+    return !p.tiles && m * n * p.G <= (p.epi == FP4_GELU ? 1 : 2) * dev.num_sms;
 }
 
 cudaError_t launch_fp4_stream(const Fp4Product& p, const Fp8Device& dev, cudaStream_t s) {

@@ -120,8 +120,16 @@ struct RowScales {
 }  // namespace f4
 
 // Groups of up to this many rows: the weights are streamed past all of them at once
-// (launch_fp4_stream) instead of in tiles of 256 rows.  So are those of more samples
-// where that makes no more tiles than SMs (per token).
+// (launch_fp4_stream) instead of in tiles of 256 rows by pairs.  In a graph, streamed and
+// by pairs: T = 32, K = 1536, N = 6144 27.7 and 39.2 us at 1 sample, 35.0 and 37.4 at 128
+// (of 130 samples, two tiles, 48.9 and 37.4); T = 8, K = 512, N = 2048 2.6 and 5.9, 3.5 and
+// 6.3; the experts of T = 32, E = 8, D = 1536, F = 2048 131 and 161 us at 8 samples, 180
+// and 190 at 128.  (The FFN T = 32, D = 1536, F = 6144 81.1 and 81.4 at 96, but 90.5 and
+// 83.1 at 128: Gelu of 128 rows.)
+// More samples are streamed too, per token, where that makes no more tiles than two rounds
+// of the SMs (one with Gelu): T = 8, K = 512, N = 2048, 256 samples (256 tiles) 4.9 and 6.3
+// us, K = 2048, N = 512, 512 samples (128 tiles) 5.3 and 7.2; 512 samples of the first (512
+// tiles) 7.8 and 7.3; with Gelu the FFN's 256 tiles took 18.4 us where pairs take 15.0.
 constexpr int kFp4StreamMaxB = 128;
 bool fp4_streams(const Fp4Product& p, const Fp8Device& dev);
 cudaError_t launch_fp4_stream(const Fp4Product& p, const Fp8Device& dev, cudaStream_t s);

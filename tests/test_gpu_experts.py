@@ -24,7 +24,8 @@ def gates(B, T, E, share, seed):
 
 
 SORTS = [(1, 1, 1), (1, 3, 5), (8, 32, 8), (64, 32, 8), (65, 32, 8), (64, 3, 90), (63, 1, 1), (130, 1, 1), (129, 5, 7),
-         (500, 2, 33), (1000, 3, 4), (4100, 1, 9), (257, 16, 40), (2, 700, 12), (3000, 4, 2), (4, 400, 10)]
+         (500, 2, 33), (1000, 3, 4), (4100, 1, 9), (257, 16, 40), (2, 700, 12), (3000, 4, 2), (4, 400, 10), (70000, 1, 3),
+         (20001, 2, 12), (2049, 1, 64)]
 
 
 @pytest.mark.parametrize("B,T,E", SORTS)
