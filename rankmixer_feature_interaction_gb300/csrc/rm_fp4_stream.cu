@@ -15,8 +15,9 @@
 //                maximum and turns eight rows' codes in three exchanges
 // The kernel is launched while its predecessor may still run.  Where that predecessor
 // is one of this library's own launches of the same call, W was in memory before it
-// began, and warp 0 starts on it at once (per token; the experts' tiles are known only
-// after the sort); everything else waits for the predecessor's end.
+// began, and the experts' tiles too (the sort is the launch before it or an earlier one,
+// and it waited for that one's end before this kernel could start): warp 0 starts on W at
+// once, everything else waits for the predecessor's end.
 // Measured (in a graph, bf16 out): T = 32, K = 1536, N = 6144 27.7 us at 1 sample (160 MB:
 // 5.8 TB/s), 31.9 at 64, 35.0 at 128; K = 6144, N = 1536 (384 tiles, 2.5 rounds of the SMs)
 // 29.1, 30.1, 32.5; the experts of T = 32, E = 8, K = 1536, N = 2048 at 8 samples 54 us for
@@ -388,7 +389,7 @@ cudaError_t launch_fp4_stream(const Fp4Product& p, const Fp8Device& dev, cudaStr
     a.step = p.tiles ? 1 : p.G;
     a.xs = p.x.scales, a.xs_ld = p.x.lds;
     a.ws = p.w.scales, a.quads = p.w.lds;
-    a.early = p.follows && !p.tiles && pdl_enabled();
+    a.early = p.follows && pdl_enabled();
     a.bias = p.bias;
     a.y = p.y;
     a.o = p.o;
