@@ -770,18 +770,21 @@ def fp4_dequantize(q: Fp4Tensor, dtype: str = "bf16") -> torch.Tensor:
     if q.weight:
         raise ValueError("fp4_dequantize takes activations")
     tdt, code = _DTYPES[dtype]
-    Y = torch.empty(q.shape, dtype=tdt, device=q.device)
-    _lib.rm_fp4_dequantize(q.c, math.prod(q.cs[:-1]), q.cols, Y.data_ptr(), code, q.cols, _raw_stream(d))
+    lead, cols = q.cs[:-1], q.cols
+    Y = torch.empty((*lead, cols), dtype=tdt, device=q.device)
+    _lib.rm_fp4_dequantize(q.c, math.prod(lead), cols, Y.data_ptr(), code, cols, _raw_stream(d))
     return Y
 
 
 def fp4_matmul(x: Fp4Tensor, w: Fp4Tensor, bias: torch.Tensor | None = None, out_dtype: str = "bf16") -> torch.Tensor:
     """Y[b, t, :] = x[b, t, :] w[t] (+ bias[t]): x [B, T, K] and w [T, K, N] in 4 bits, bias float32 [T, N]."""
-    B, T, K = _fp4_activation(x, 3, "x")
-    Tw, Kw, N = _fp4_weight(w, 3, "w")
-    if Tw != T or Kw != K:
+    cs, ws, K, d = x.cs, w.cs, x.cols, x.device_index
+    if x.weight or not w.weight or len(cs) != 3 or len(ws) != 3 or ws[0] != cs[1] or w.cols != K:
+        _fp4_activation(x, 3, "x"), _fp4_weight(w, 3, "w")
         raise ValueError(f"x {x.shape} and w {w.shape} do not fit")
-    d = _fp8_device(x.device_index, w.device_index)
+    if d != w.device_index or d != torch._C._cuda_getDevice():
+        _fp8_device(d, w.device_index)
+    B, T, N = cs[0], cs[1], ws[1]
     tdt, code = _DTYPES[out_dtype]
     b = _bias(bias, (T, N))
     Y = torch.empty((B, T, N), dtype=tdt, device=x.device)
@@ -900,72 +903,80 @@ def expert_sort(G: torch.Tensor) -> ExpertRows:
     return rows
 
 
-def _batch_rows(X: torch.Tensor, rows: ExpertRows, what: str) -> int:
-    shape = X.shape
-    if X.dtype not in _CODE or len(shape) != 3 or shape[0] != rows.B or shape[1] != rows.T:
+# Each of these three checks one argument whole, so that a call takes few Python steps.
+def _batch_rows(X: torch.Tensor, rows: ExpertRows, what: str) -> tuple:
+    """(D, dtype code, pointer) of X [B, T, D]."""
+    shape, code, d = X.shape, _CODE.get(X.dtype), X.get_device()
+    if d != rows.device_index or d != torch._C._cuda_getDevice():
+        _fp8_device(d, rows.device_index)
+    if code is None or len(shape) != 3 or shape[0] != rows.B or shape[1] != rows.T:
         raise ValueError(f"{what} must be a bfloat16 or float32 [{rows.B}, {rows.T}, D], got {X.dtype} {tuple(shape)}")
-    return shape[2]
+    return shape[2], code, _ptr(X)
+
+
+def _sorted_rows(Y: torch.Tensor, rows: ExpertRows, what: str) -> tuple:
+    """(n, D, dtype code, pointer) of Y [n, D]."""
+    shape, code, d = Y.shape, _CODE.get(Y.dtype), Y.get_device()
+    if d != rows.device_index or d != torch._C._cuda_getDevice():
+        _fp8_device(d, rows.device_index)
+    if code is None or len(shape) != 2:
+        raise ValueError(f"{what} must be a bfloat16 or float32 [n, D], got {Y.dtype} {tuple(shape)}")
+    return shape[0], shape[1], code, _ptr(Y)
 
 
 def _gates(G: torch.Tensor, rows: ExpertRows) -> int:
+    """Pointer of G [B, T, E]."""
+    if G.get_device() != rows.device_index:
+        _fp8_device(G.get_device(), rows.device_index)
     if G.dtype != torch.float32 or G.shape != (rows.B, rows.T, rows.E):
         raise ValueError(f"G must be float32 [{rows.B}, {rows.T}, {rows.E}], got {G.dtype} {tuple(G.shape)}")
     return _ptr(G)
 
 
 def _room(rows: ExpertRows, n: int | None) -> int:
-    if n is not None and n < 0:
+    if n is None:
+        return rows.B * rows.T * rows.E
+    if n < 0:
         raise ValueError(f"n must not be negative, got {n}")
-    return rows.B * rows.T * rows.E if n is None else n
+    return n
 
 
 def expert_gather(X: torch.Tensor, rows: ExpertRows, n: int | None = None) -> torch.Tensor:
     """Xs [n, D]: the rows of X [B, T, D] (bf16 or float32), each copied to its slots.  n: room for
     that many rows (default: for all that there can be); slots from n on are left out, rows behind
     the last slot uninitialised."""
-    d = _fp8_device(X.get_device(), rows.device_index)
-    D, n = _batch_rows(X, rows, "X"), _room(rows, n)
+    D, code, x = _batch_rows(X, rows, "X")
+    n = _room(rows, n)
     Xs = torch.empty((n, D), dtype=X.dtype, device=X.device)
-    _lib.rm_expert_gather(_ptr(X), _CODE[X.dtype], rows.c, Xs.data_ptr(), n, D, _raw_stream(d))
+    _lib.rm_expert_gather(x, code, rows.c, Xs.data_ptr(), n, D, _raw_stream(rows.device_index))
     return Xs
 
 
 def fp4_expert_gather(X: torch.Tensor, rows: ExpertRows, n: int | None = None) -> Fp4Tensor:
     """expert_gather and fp4_quantize in one pass: [n, D] in 4 bits."""
-    d = _fp8_device(X.get_device(), rows.device_index)
-    D, n = _batch_rows(X, rows, "X"), _room(rows, n)
-    out = _fp4_new((n,), D, False, X.device, d)
-    _lib.rm_fp4_expert_gather(_ptr(X), _CODE[X.dtype], rows.c, out.c, n, D, _raw_stream(d))
+    D, code, x = _batch_rows(X, rows, "X")
+    n = _room(rows, n)
+    out = _fp4_new((n,), D, False, X.device, rows.device_index)
+    _lib.rm_fp4_expert_gather(x, code, rows.c, out.c, n, D, _raw_stream(rows.device_index))
     return out
-
-
-def _sorted_rows(Y: torch.Tensor, what: str) -> tuple:
-    if Y.dtype not in _CODE or Y.dim() != 2:
-        raise ValueError(f"{what} must be a bfloat16 or float32 [n, D], got {Y.dtype} {tuple(Y.shape)}")
-    return Y.shape
 
 
 def expert_gather_backward(dXs: torch.Tensor, rows: ExpertRows) -> torch.Tensor:
     """dX [B, T, D] for the gradient dXs [n, D] at expert_gather's rows: their sum over a row's slots."""
-    return _combine(dXs, rows, None, "dXs", None)
+    n, D, code, y = _sorted_rows(dXs, rows, "dXs")
+    dX = torch.empty((rows.B, rows.T, D), dtype=dXs.dtype, device=dXs.device)
+    _lib.rm_expert_combine(y, code, rows.c, None, dX.data_ptr(), code, n, D, _raw_stream(rows.device_index))
+    return dX
 
 
 def expert_combine(Y: torch.Tensor, rows: ExpertRows, G: torch.Tensor, out_dtype: str | None = None) -> torch.Tensor:
     """V [B, T, D]: V[b, t] = sum over the open experts e of G[b, t, e] Y[slot of (b, t, e)] (float32
     sums, ascending e; zero where none is open).  Y [n, D]; V in Y's type, or float32 (out_dtype "f32")."""
-    return _combine(Y, rows, G, "Y", out_dtype)
-
-
-def _combine(Y: torch.Tensor, rows: ExpertRows, G: torch.Tensor | None, what: str, out_dtype: str | None) -> torch.Tensor:
-    n, D = _sorted_rows(Y, what)
-    d = _fp8_device(Y.get_device(), rows.device_index)
-    tdt, code = _DTYPES[out_dtype] if out_dtype is not None else (Y.dtype, _CODE[Y.dtype])
-    g = None
-    if G is not None:
-        _fp8_device(G.get_device())
-        g = _gates(G, rows)
+    n, D, code, y = _sorted_rows(Y, rows, "Y")
+    g = _gates(G, rows)
+    tdt, v_code = (Y.dtype, code) if out_dtype is None else _DTYPES[out_dtype]
     V = torch.empty((rows.B, rows.T, D), dtype=tdt, device=Y.device)
-    _lib.rm_expert_combine(_ptr(Y), _CODE[Y.dtype], rows.c, g, V.data_ptr(), code, n, D, _raw_stream(d))
+    _lib.rm_expert_combine(y, code, rows.c, g, V.data_ptr(), v_code, n, D, _raw_stream(rows.device_index))
     return V
 
 
@@ -974,15 +985,15 @@ def expert_combine_backward(dV: torch.Tensor, Y: torch.Tensor, rows: ExpertRows,
     """(dY [n, D], dG [B, T, E] float32) of expert_combine(Y, rows, G) for the gradient dV [B, T, D]
     (of Y's type) at V; dG is zero where an expert is closed, rows of dY behind the last slot
     uninitialised."""
-    d = _fp8_device(dV.get_device(), Y.get_device(), rows.device_index, G.get_device())
-    n, D = _sorted_rows(Y, "Y")
-    if _batch_rows(dV, rows, "dV") != D or dV.dtype != Y.dtype:
+    n, D, code, y = _sorted_rows(Y, rows, "Y")
+    D2, code2, dv = _batch_rows(dV, rows, "dV")
+    if D2 != D or code2 != code:
         raise ValueError(f"dV {dV.dtype} {tuple(dV.shape)} and Y {Y.dtype} {tuple(Y.shape)} do not fit")
     g = _gates(G, rows)
     dY = torch.empty((n, D), dtype=Y.dtype, device=Y.device)
     dG = torch.empty((rows.B, rows.T, rows.E), dtype=torch.float32, device=Y.device)
-    _lib.rm_expert_combine_backward(_ptr(dV), _ptr(Y), _CODE[Y.dtype], rows.c, g, dY.data_ptr(), dG.data_ptr(), n, D,
-                                    _raw_stream(d))
+    _lib.rm_expert_combine_backward(dv, y, code, rows.c, g, dY.data_ptr(), dG.data_ptr(), n, D,
+                                    _raw_stream(rows.device_index))
     return dY, dG
 
 
