@@ -1027,7 +1027,9 @@ class Fp4MoE(_Fp4FFN):
         self.c = _lib.rm_fp4_moe(self.W1.c, self.W2.c, _ptr(self.b1), _ptr(self.b2), self.T, self.E, self.D, self.F)
 
     def forward(self, X: torch.Tensor, G: torch.Tensor, out_dtype: str = "bf16") -> torch.Tensor:
-        """V [B, T, D] of X [B, T, D] and the gates G [B, T, E] (float32)."""
+        """V [B, T, D] of X [B, T, D] and the gates G [B, T, E] (float32; RankMixer.moe_pffn_forward
+        returns such gates, any others will do).  The call's workspace has room for every expert of
+        every row: B T E rows of about D / 2 + F / 2 + 2 D bytes."""
         B = self._rows(X)
         _fp8_device(G.get_device())
         if G.dtype != torch.float32 or G.shape != (B, self.T, self.E):

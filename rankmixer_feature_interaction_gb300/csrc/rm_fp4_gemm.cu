@@ -15,14 +15,14 @@
 //   warps 2, 3   x's exponent bytes (RowScales), every other step of two k-blocks
 //   warps 4-19   epilogue, two groups of eight warps for every other tile, so that one
 //                group's waits and reads lie beside the other's arithmetic (all sixteen
-//                on one tile: layer 1 at B = 2048 290 us).  A warp owns 32 rows and 128
-//                columns, a thread 64 of one row at a time, so that a block of 32 of a
-//                4-bit output is one thread's
+//                on one tile: layer 1 at B = 2048 290 us instead of 270).  A warp owns 32
+//                rows and 128 columns, a thread 32 of one row at a time, which is a block
+//                of a 4-bit output
 // Tensor memory (512 columns): two accumulators of 256 columns that share 64, at
 // columns 0 and 192, so that the next tile's product begins as soon as those 64
-// columns have been read (first), and two slots of exponent bytes from column 448 (8 columns
-// for x, 16 for W).  Copies and MMAs of one thread run in order, so the slots need no
-// barriers of their own.
+// columns have been read (first), and two slots of exponent bytes from column 448 (8
+// columns for x, 16 for W).  Copies and MMAs of one thread run in order, so the slots
+// need no barriers of their own.
 // Measured, T = 32, 4096 samples, bf16 out: 6144 to 1536 340 us (7.3 PFLOP/s), 1536 to
 // 6144 466 us (5.3; float32 out 620, 3.2 GB written); T = 4, 12288 to 6144 315 us (7.9).
 // Bound by what the SMs take in from L2: a k-block of a CTA is 35 KB in 512 cycles of the
@@ -188,8 +188,8 @@ __device__ __forceinline__ void round_block(const float* v, uint32_t (&w)[4], ui
 
 // 128 columns of a warp's rows in 4 bits out of the staging, and their exponent bytes
 // (of this lane's row).  A thread that stored its own 16 bytes and its byte made every
-// store 32 requests of part of a sector: the FFN at B = 2048 took 684 us with that
-// where it takes 510 with rows of 128 bytes by TMA.
+// store 32 requests of part of a sector: the FFN at B = 2048 took 684 us with that, 595
+// once the codes went through shared memory and TMA.
 template <bool EXPERTS>
 __device__ __forceinline__ void save_codes(const Args& a, const CUtensorMap* tmY, const Tile& tl, int m_warp, long long row,
                                            int n, int rows, uint32_t E, int lane, uint32_t stage) {
@@ -528,8 +528,8 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
 }
 
 template <int EPI, bool EXPERTS>
-cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& ms, const CUtensorMap& my, const Args& a, int num_sms,
-                cudaStream_t s) {
+cudaError_t run(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& ms, const CUtensorMap& my, const Args& a,
+                int num_sms, cudaStream_t s) {
     auto k = fp4_product_kernel<EPI, EXPERTS>;
     cudaError_t e = smem_attr_once((const void*)k, SMEM_BYTES);
     if (e != cudaSuccess) return e;
@@ -572,7 +572,8 @@ cudaError_t launch_fp4_product(const Fp4Product& p, const Fp8Device& dev, cudaSt
     a.kblocks = (p.K + BK - 1) / BK;
     a.nb = (int)fp4_blocks(p.K);
     a.table = p.tiles;
-    const long long units = (long long)p.G * a.m_tiles * a.n_tiles;
+    // (by expert: tiles at most)
+    const long long units = (p.tiles ? p.G + p.n / kExpertTile : (long long)p.G * a.m_tiles) * a.n_tiles;
     if (units >= 1ll << 31) return cudaErrorNotSupported;        // more tiles than a device's memory holds outputs for
     a.units = (uint32_t)units;
     a.n = p.n;
@@ -593,7 +594,7 @@ cudaError_t launch_fp4_product(const Fp4Product& p, const Fp8Device& dev, cudaSt
         fp8_tensor_map(&mw, u8t, p.w.codes, wide, p.N, p.G, p.w.ld, p.N * p.w.ld, 128, BN / 2) &&
         fp8_tensor_map(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT32, p.w.scales, p.w.lds * (QUAD_BYTES / 4), tiles, p.G,
                        p.w.lds * QUAD_BYTES, tiles * p.w.lds * QUAD_BYTES, SF_BYTES / 4, 2, true);
-    // what leaves by TMA, in bytes: 64 of 32 rows of Y, or 128 of 32 rows of codes
+    // what leaves by TMA, in bytes: 64 of 32 rows of Y or of the codes
     CUtensorMap my = mx;
     const bool gelu = p.epi == FP4_GELU;
     const long long bytes = gelu ? p.N / 2 : p.N * (p.epi == FP4_OUT_F32 ? 4ll : 2ll), pitch = gelu ? p.o.ld : bytes;
