@@ -143,6 +143,16 @@ def test_quantize_weight_is_the_format_bit_for_bit(shape, dtype):
     ok()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_quantize_weight_of_any_alignment(dtype):
+    """Weights that begin one element off give the same as their copy."""
+    buf = rows((2 * 96 * 130 + 1,), 30).to(DTYPES[dtype]).to(DEV)
+    w = buf[1:].view(2, 96, 130)
+    q, want = fp4_quantize_weight(w), fp4_quantize_weight(w.clone())
+    assert w.data_ptr() % (2 * w.element_size()) and torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
+    ok()
+
+
 def test_four_bits_past_32_bits():
     """More than 2^31 values, and rows behind the 2^31st."""
     n, C = 70001, 32000
