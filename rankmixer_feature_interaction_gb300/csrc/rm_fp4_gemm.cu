@@ -29,7 +29,7 @@
 // tensor core, 68 bytes a cycle, and comes in about 630; with few k-blocks a tile also
 // by the outputs' way through shared memory, which the tensor core's operands share
 // (1536 to 6144 without an epilogue: 366 us), and with Gelu by its instructions beside
-// them (2048 samples: 260 us, 195 without).
+// them (2048 samples: 252 us, 195 without).
 // Every mbarrier wait is bounded in time; on expiry the CTA latches an error
 // word and all roles unwind.
 #include <cudaTypedefs.h>
@@ -152,22 +152,6 @@ __device__ __forceinline__ void save_piece(const float* v, const Args& a, const 
         store_rows<true, E>(stage, dst, pitch, rows, bytes, lane);
     else
         store_rows<false, E>(stage, dst, pitch, rows, bytes, lane);
-}
-
-// fp8_gelu of two values, the polynomial in -|u| so that one constant sign serves both
-// it and the last step: 7 instead of 10 instructions a value.
-__device__ __forceinline__ void gelu2(float& a, float& b) {
-    const uint64_t u = f2_pack(a, b), x = u | 0x8000000080000000ull;
-    uint64_t p = f2_fma(x, f2_splat(9.30538079e-07f), f2_splat(4.20015094e-05f));
-    p = f2_fma(x, p, f2_splat(7.80347327e-04f));
-    p = f2_fma(x, p, f2_splat(8.01421981e-03f));
-    p = f2_fma(x, p, f2_splat(5.32146059e-02f));
-    p = f2_fma(x, p, f2_splat(-4.58957642e-01f));
-    p = f2_fma(x, p, f2_splat(1.15113652f));
-    p = f2_fma(x, p, f2_splat(-9.99999404e-01f));
-    float p0, p1;
-    f2_unpack(p, p0, p1);
-    f2_unpack(f2_fma(x, f2_pack(ex2_approx(p0), ex2_approx(p1)), f2_pack(fmaxf(a, 0.f), fmaxf(b, 0.f))), a, b);
 }
 
 // 32 columns of this thread's row in 4 bits: 16 bytes of codes; E: the exponent byte.
@@ -475,14 +459,14 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                 } else {
                     uint32_t w[4], e;
 #pragma unroll
-                    for (int k = 0; k < CHUNK; k += 2) gelu2(v[k], v[k + 1]);
+                    for (int k = 0; k < CHUNK; k += 2) fp4_gelu2(v[k], v[k + 1]);
                     round_block(v, w, e);
                     st_shared_v4(staged_at(stage, lane, c), w[0], w[1], w[2], w[3]);
                     E |= e << (8 * c);
                 }
             };
             // Two chunks at once, so that the shared columns are free early; the other two
-            // come, one by one, while a chunk is worked on: layer 1 at B = 2048 260 us, 270
+            // come, one by one, while a chunk is worked on: layer 1 at B = 2048 252 us, 262
             // with 64 columns read, worked on and read again.
             uint32_t r0[CHUNK], r1[CHUNK];
             const int c0 = 2 * first, c2 = 2 - c0;
@@ -495,7 +479,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             tc_fence_before();
             __syncwarp();
             if (lane == 0 && owner) mbar_arrive_pair(mapa_shared(shared_bar, 0));
-            if (rows > 0) {                              // (as a loop: 356 us instead of 260, registers in memory)
+            if (rows > 0) {                              // (as a loop: 346 us instead of 252, registers in memory)
                 finish(r0, c0);
                 tmem_ld32_nowait(tcol + CHUNK * c2, r0);
                 finish(r1, c0 + 1);

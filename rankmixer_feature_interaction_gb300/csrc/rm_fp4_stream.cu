@@ -314,11 +314,14 @@ fp4_stream_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                     if (j >= count) break;
                     float q[8];
 #pragma unroll
+                    for (int k = 0; k < 8; ++k) q[k] = __uint_as_float(r[j + k]) + bias;
+#pragma unroll
+                    for (int k = 0; k < 8; k += 2) fp4_gelu2(q[k], q[k + 1]);
+#pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const float a = fp8_gelu(__uint_as_float(r[j + k]) + bias);
-                        const uint32_t E = fp4_exponent(__reduce_max_sync(0xffffffffu, fp4_abs_bits(a)));
+                        const uint32_t E = fp4_exponent(__reduce_max_sync(0xffffffffu, fp4_abs_bits(q[k])));
                         if (lane == j + k) mine = E;
-                        q[k] = a * fp4_inv_scale(E);
+                        q[k] *= fp4_inv_scale(E);
                     }
                     const uint32_t w = turn8(fp4_pack8(q), lane);
                     if (j + (lane & 7) < count)

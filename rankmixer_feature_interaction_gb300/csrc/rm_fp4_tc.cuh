@@ -43,6 +43,24 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint6
             : "memory");
 }
 
+// fp8_gelu of two values, the same bits: the polynomial in x = -|u| = u - 2 relu(u), which
+// is exact, so that one variable serves it and the last step.  6.5 instructions a value
+// instead of 10 (layer 1 of the FFN at B = 2048 252 us instead of 307; with the sign set
+// by a logical instruction a value 262).
+__device__ __forceinline__ void fp4_gelu2(float& a, float& b) {
+    const uint64_t relu = f2_pack(fmaxf(a, 0.f), fmaxf(b, 0.f)), x = f2_fma(relu, f2_splat(-2.f), f2_pack(a, b));
+    uint64_t p = f2_fma(x, f2_splat(9.30538079e-07f), f2_splat(4.20015094e-05f));
+    p = f2_fma(x, p, f2_splat(7.80347327e-04f));
+    p = f2_fma(x, p, f2_splat(8.01421981e-03f));
+    p = f2_fma(x, p, f2_splat(5.32146059e-02f));
+    p = f2_fma(x, p, f2_splat(-4.58957642e-01f));
+    p = f2_fma(x, p, f2_splat(1.15113652f));
+    p = f2_fma(x, p, f2_splat(-9.99999404e-01f));
+    float p0, p1;
+    f2_unpack(p, p0, p1);
+    f2_unpack(f2_fma(x, f2_pack(ex2_approx(p0), ex2_approx(p1)), relu), a, b);
+}
+
 // Bytes of blocks that a row does not have become 127 (its codes there are zero, but
 // an exponent byte of 255 would make them NaN); left: blocks from this word on.
 __device__ __forceinline__ uint32_t existing_blocks(uint32_t w, int left) {
