@@ -720,8 +720,8 @@ RM_API rm_status rm_fp4_expert_gather(const void *X, rm_dtype dtype, const rm_ex
 
 /* V[b][t] = sum over the open e of G[b][t][e] Y[slot of (b, t, e)], in float32 and
  * ascending e; zero where no expert is open.  Y: device [n][D] of y_dtype, V:
- * device [B][T][D] of v_dtype (float32, or bf16 where Y is).  G NULL: without
- * gates, which is the gradient of rm_expert_gather (Y: the gradient at Xs). */
+ * device [B][T][D] of v_dtype.  G NULL: without gates, which is the gradient of
+ * rm_expert_gather (Y: the gradient at Xs). */
 RM_API rm_status rm_expert_combine(const void *Y, rm_dtype y_dtype, const rm_expert_rows *rows, const float *G, void *V,
                                    rm_dtype v_dtype, long long n, int D, void *stream);
 
@@ -750,8 +750,8 @@ typedef struct rm_fp4_moe {
 } rm_fp4_moe;
 
 /* Serving: V[b][t] = sum over the open e of G[b][t][e] FFN_{t,e}(X[b][t]), each
- * expert as in rm_fp4_pffn_forward; an expert's output is rounded to bf16 before
- * its gate is applied.  X: device [B][T][D] of x_dtype; G: device float32
+ * expert as in rm_fp4_pffn_forward; where B T E D is above 2^23 an expert's
+ * output is rounded to bf16 before its gate is applied.  X: device [B][T][D] of x_dtype; G: device float32
  * [B][T][E]; V: device [B][T][D] of v_dtype. */
 RM_API rm_status rm_fp4_moe_workspace(const rm_fp4_moe *p, int B, long long *bytes);
 RM_API rm_status rm_fp4_moe_forward(const rm_fp4_moe *p, const void *X, rm_dtype x_dtype, const float *G, void *V,

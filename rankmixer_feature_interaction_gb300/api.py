@@ -971,7 +971,7 @@ def expert_gather_backward(dXs: torch.Tensor, rows: ExpertRows) -> torch.Tensor:
 
 def expert_combine(Y: torch.Tensor, rows: ExpertRows, G: torch.Tensor, out_dtype: str | None = None) -> torch.Tensor:
     """V [B, T, D]: V[b, t] = sum over the open experts e of G[b, t, e] Y[slot of (b, t, e)] (float32
-    sums, ascending e; zero where none is open).  Y [n, D]; V in Y's type, or float32 (out_dtype "f32")."""
+    sums, ascending e; zero where none is open).  Y [n, D]; V in Y's type, or in out_dtype ("bf16", "f32")."""
     n, D, code, y = _sorted_rows(Y, rows, "Y")
     g = _gates(G, rows)
     tdt, v_code = (Y.dtype, code) if out_dtype is None else _DTYPES[out_dtype]
@@ -1016,7 +1016,7 @@ def fp4_expert_matmul(x: Fp4Tensor, w: Fp4Tensor, rows: ExpertRows, bias: torch.
 class Fp4MoE(_Fp4FFN):
     """The Sparse-MoE per-token FFN with 4-bit experts, for serving: V[b, t] = sum over the experts
     with a gate above zero of G[b, t, e] FFN_{t,e}(X[b, t]), each on 4-bit operands as in Fp4PFFN;
-    an expert's output is rounded to bf16 before its gate is applied.
+    where B T E D is above 2^23 an expert's output is rounded to bf16 before its gate is applied.
 
     W1 [T, E, D, F] and W2 [T, E, F, D]: bf16 or float32 tensors (quantised here, once) or
     Fp4Tensor; b1 [T, E, F], b2 [T, E, D]; D and F multiples of 32."""

@@ -417,11 +417,13 @@ combine_kernel(const T* __restrict__ Y, ExpertRows r, const float* __restrict__ 
                 Piece<TO, VEC> o;
                 o.set(v[i]);
                 o.store(dst);
-            } else if constexpr (VEC) {                 // bf16 rows to float
+            } else if constexpr (!VEC) {
+                *dst = from_f32<TO>(v[i][0]);
+            } else if constexpr (sizeof(TO) == 4) {     // bf16 rows to float
                 reinterpret_cast<float4*>(dst)[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
                 reinterpret_cast<float4*>(dst)[1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
-            } else {
-                *dst = v[i][0];
+            } else {                                    // float rows to bf16
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]));
             }
         }
 }
@@ -613,10 +615,12 @@ cudaError_t launch_fp4_expert_gather(const void* X, bool f32, const ExpertRows& 
 cudaError_t launch_expert_combine(const void* Y, bool y_f32, const ExpertRows& r, const float* G, void* V, bool v_f32,
                                   long long n, int D, cudaStream_t s) {
     RM_HOST_BOUNDS((Y || n == 0) && V && rows_ok(r, n, D));
-    if (y_f32 && !v_f32) return cudaErrorNotSupported;
-    if (y_f32) return combine(static_cast<const float*>(Y), r, G, static_cast<float*>(V), n, D, s);
-    if (v_f32) return combine(static_cast<const __nv_bfloat16*>(Y), r, G, static_cast<float*>(V), n, D, s);
-    return combine(static_cast<const __nv_bfloat16*>(Y), r, G, static_cast<__nv_bfloat16*>(V), n, D, s);
+    using H = __nv_bfloat16;
+    if (y_f32)
+        return v_f32 ? combine(static_cast<const float*>(Y), r, G, static_cast<float*>(V), n, D, s)
+                     : combine(static_cast<const float*>(Y), r, G, static_cast<H*>(V), n, D, s);
+    return v_f32 ? combine(static_cast<const H*>(Y), r, G, static_cast<float*>(V), n, D, s)
+                 : combine(static_cast<const H*>(Y), r, G, static_cast<H*>(V), n, D, s);
 }
 
 cudaError_t launch_expert_combine_backward(const void* dV, const void* Y, bool f32, const ExpertRows& r, const float* G,

@@ -190,7 +190,6 @@ def test_rows_refusals(lib, mem):
         for a in ((None, 0, p, 7, 8), (p, 0, None, 7, 8), (p, 3, p, 7, 8), (p, 0, p, -1, 8), (p, 0, p, 1 << 31, 8),
                   (p, 0, p, 7, 0), (p, 0, p, 7, MAX + 1), (p + 2, 0, p, 7, 8), (p, 0, p + 2, 7, 8), (p + 1, 1, p, 7, 8)):
             assert c(*a) == BAD, a
-    assert lib.rm_expert_combine(p, 0, r, None, p, 1, 7, 8, None) == NO          # float32 rows to bf16
     assert lib.rm_expert_combine(p, 0, r, p + 2, p, 0, 7, 8, None) == BAD
     for G, dY, dG in ((None, p, p), (p, None, p), (p, p, None), (p + 2, p, p), (p, p, p + 2), (p, p + 2, p)):
         assert lib.rm_expert_combine_backward(p, p, 0, r, G, dY, dG, 7, 8, None) == BAD

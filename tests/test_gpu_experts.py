@@ -88,8 +88,8 @@ def test_rows_there_and_back(B, T, D, E, dtype):
     want, bound = (Gd * spread(Y)).sum(2), ref.sum_bound(E, (Gd * spread(Y)).abs().sum(2))
     within(V, want, bound + (want.abs() + bound) * HALF[dtype], "combine")
     assert (V[(slot < 0).all(-1)] == 0).all()
-    if dtype == "bf16":
-        within(expert_combine(Y.to(DEV), r, G.to(DEV), out_dtype="f32").cpu(), want, bound + want.abs() * ref.UNIT_F32, "f32")
+    for out in ("f32", "bf16"):
+        within(expert_combine(Y.to(DEV), r, G.to(DEV), out_dtype=out).cpu(), want, bound + (want.abs() + bound) * HALF[out], out)
     dX = expert_gather_backward(dXs.to(DEV), r).cpu()
     want, bound = spread(dXs).sum(2), ref.sum_bound(E, spread(dXs).abs().sum(2))
     within(dX, want, bound + (want.abs() + bound) * HALF[dtype], "gather's gradient")
@@ -157,8 +157,9 @@ def test_gather_in_4_bits_is_gather_then_quantize(B, T, D, E, dtype):
     ok()
 
 
+# (the last two have more than 2^23 values of experts' outputs)
 EXPERTS = [(1, 1, 1, 32, 32), (2, 2, 3, 64, 96), (8, 4, 8, 256, 160), (30, 2, 5, 320, 288), (100, 3, 2, 96, 64),
-           (128, 1, 3, 128, 256), (129, 2, 4, 256, 96), (300, 2, 3, 512, 288), (700, 1, 2, 64, 544)]
+           (128, 1, 3, 128, 256), (129, 2, 4, 256, 96), (300, 2, 3, 512, 288), (700, 1, 2, 64, 544), (100, 16, 7, 768, 64), (900, 5, 4, 480, 96)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
