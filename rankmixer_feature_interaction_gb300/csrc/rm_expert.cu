@@ -347,7 +347,16 @@ gather_fp4_kernel(const T* __restrict__ X, ExpertRows r, Fp4View out, long long 
     const Run u = run_of<1>(r, runs);
     if (!u.there) return;
     Fp4Raw16<T> v;
-    v.template load<VEC>(X + u.bt * D + 16 * (size_t)u.p, D - 16 * u.p);         // past the row's end: zeros
+    const T* p = X + u.bt * D + 16 * (size_t)u.p;
+    const int left = D - 16 * u.p;                                               // past the row's end: zeros
+    if constexpr (VEC) {
+        v.template load<true>(p, left);
+    } else {
+        const bool in = left <= 0 || Fp4Raw16<T>::inside(p, left, X, X + (size_t)r.B * r.T * D);
+        uint32_t t[Fp4Raw16<T>::AROUND];
+        Fp4Raw16<T>::fetch(p, left, in && left > 0, t);
+        v.take(p, left, in, t);
+    }
     int slot;
     uint32_t m = open_experts(r.slot, u.bt, r.E, 0, n, lane, slot);
     uint32_t E;

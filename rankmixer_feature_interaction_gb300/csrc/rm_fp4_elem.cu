@@ -4,16 +4,18 @@
 // agree on its largest magnitude with one shuffle and write eight bytes of codes each,
 // so a warp reads a kilobyte of bf16 in a row and writes 256 bytes.  What a thread has
 // loaded stays as it came until it is rounded: few registers, so many loads under way.
-// Rows that are not 16-byte aligned are read (or written) an element at a time,
-// neighbouring lanes neighbouring elements, and change their order in shared memory.
 // Measured, 65,536 rows of 6144 in bf16: to 4 bits 147 us (6.9 TB/s; 326 with eight values
 // a lane, unpacked at once), back 154 us (6.6 TB/s): bound by memory, 2.53 bytes a value.
+// Rows that are not 16-byte aligned go by 16-byte pieces of memory too, those around the
+// values, which are then shifted into place: 126,840 bf16 rows of 1547 to 4 bits 114 us
+// (1552 columns, aligned: 79), back 117 us (80).  An element at a time, their order
+// changed in shared memory, they took 262 and 160 us, and 47,720 rows of 33 15.7 us (4.7).
 #include "rm_fp4.cuh"
 
 namespace rm {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256;
 
 // Row and piece of a running number (pieces of a row: n).
 __device__ __forceinline__ void split(unsigned long long id, bool small, unsigned n, unsigned long long& row, int& j) {
@@ -66,47 +68,61 @@ quantize_kernel(const IN* __restrict__ X, unsigned long long pieces, int cols, i
     }
 }
 
-// Other rows: a warp takes 256 values of a row.
+// Other rows: a lane reads the 16-byte pieces around its values and shifts them; end:
+// behind the last row's last value.
 template <typename IN>
 __global__ void __launch_bounds__(kThreads)
-quantize_odd_kernel(const IN* __restrict__ X, unsigned long long chunks, int cols, int nb, int per_row, long long ldx,
-                    Fp4View out) {
-    __shared__ float turn[kWarps][256];
+quantize_odd_kernel(const IN* __restrict__ X, unsigned long long pieces, int cols, int nb, int dq, int dr, long long ldx,
+                    const IN* __restrict__ end, Fp4View out) {
+    constexpr int UNROLL = kInFlight<IN>;
     pdl_wait();
     pdl_launch_next();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned long long id = (unsigned long long)blockIdx.x * kWarps + warp;
-    if (id >= chunks) return;
+    const unsigned long long base = (unsigned long long)blockIdx.x * (kThreads * UNROLL) + threadIdx.x;
     unsigned long long row;
-    int c;
-    split(id, chunks <= 0xffffffffull, per_row, row, c);
-    const IN* p = X + row * ldx + 256 * (long long)c;
-    const int n = cols - 256 * c;
+    int j;
+    split(base, pieces <= 0xffffffffull, 2u * nb, row, j);
+    uint32_t t[UNROLL][Fp4Raw16<IN>::AROUND];
+    unsigned long long at = row;
+    int k = j;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int k = 32 * i + lane;
-        turn[warp][k] = k < n ? to_f32(p[k]) : 0.f;
+    for (int u = 0; u < UNROLL; ++u) {
+        const int n = base + (unsigned long long)u * kThreads < pieces ? cols - 16 * k : 0;
+        const IN* p = X + at * ldx + 16 * k;
+        Fp4Raw16<IN>::fetch(p, n, n > 0 && Fp4Raw16<IN>::inside(p, n, X, end), t[u]);
+        advance(at, k, dq, dr, 2 * nb);
     }
-    __syncwarp();
-    float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = turn[warp][8 * lane + i];
-    uint32_t E;
-    const uint32_t w = fp4_round8(v, E);
-    const int b = 8 * c + (lane >> 2);
-    if (b < nb) {
-        *reinterpret_cast<uint32_t*>(out.codes + row * out.ld + 16 * b + 4 * (lane & 3)) = w;
-        if ((lane & 3) == 0) out.scales[row * out.lds + b] = (uint8_t)E;
+    for (int u = 0; u < UNROLL; ++u) {
+        const bool there = base + (unsigned long long)u * kThreads < pieces;
+        const int n = there ? cols - 16 * j : 0;
+        const IN* p = X + row * ldx + 16 * j;
+        Fp4Raw16<IN> v;
+        v.take(p, n, n <= 0 || Fp4Raw16<IN>::inside(p, n, X, end), t[u]);
+        uint32_t E;
+        const uint2 c = v.round(E);
+        if (there) {
+            *reinterpret_cast<uint2*>(out.codes + row * out.ld + 8 * j) = c;
+            if ((j & 1) == 0) out.scales[row * out.lds + (j >> 1)] = (uint8_t)E;
+        }
+        advance(row, j, dq, dr, 2 * nb);
     }
 }
 
+// 2^(E - 127); 0 stands for 2^-127, 255 for NaN
+__device__ __forceinline__ float fp4_scale(uint32_t E) {
+    return E == 0u ? __uint_as_float(0x00400000u) : E == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(E << 23);
+}
+
+// Eight values to a 16-byte boundary.
 template <typename OUT>
-__device__ __forceinline__ void value8(uint32_t codes, uint32_t E, float (&v)[8]) {
-    fp4_unpack8(codes, v);
-    // 2^(E - 127); 0 stands for 2^-127, 255 for NaN
-    const float s = E == 0u ? __uint_as_float(0x00400000u) : E == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(E << 23);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= s;
+__device__ __forceinline__ void store8(OUT* y, const float (&v)[8]) {
+    if constexpr (sizeof(OUT) == 2) {
+        __stcs(reinterpret_cast<uint4*>(y), make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+    } else {
+        __stcs(reinterpret_cast<float4*>(y), make_float4(v[0], v[1], v[2], v[3]));
+        __stcs(reinterpret_cast<float4*>(y) + 1, make_float4(v[4], v[5], v[6], v[7]));
+    }
 }
 
 template <typename OUT>
@@ -131,17 +147,14 @@ dequantize_kernel(Fp4View in, unsigned long long pieces, int cols, int nb, OUT* 
     for (int u = 0; u < UNROLL; ++u) {
         if (base + (unsigned long long)u * kThreads >= pieces) return;
         float v[8];
-        value8<OUT>(c[u], E[u], v);
+        fp4_unpack8(c[u], v);
+        const float s = fp4_scale(E[u]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= s;
         OUT* y = Y + row[u] * ldy + 8 * j[u];
         const int n = cols - 8 * j[u];
         if (n >= 8) {
-            if constexpr (sizeof(OUT) == 2) {
-                __stcs(reinterpret_cast<uint4*>(y), make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
-            } else {
-                __stcs(reinterpret_cast<float4*>(y), make_float4(v[0], v[1], v[2], v[3]));
-                __stcs(reinterpret_cast<float4*>(y) + 1, make_float4(v[4], v[5], v[6], v[7]));
-            }
+            store8(y, v);
         } else {
 #pragma unroll
             for (int i = 0; i < 7; ++i)
@@ -150,33 +163,51 @@ dequantize_kernel(Fp4View in, unsigned long long pieces, int cols, int nb, OUT* 
     }
 }
 
+// Other rows: a lane writes eight values from a 16-byte boundary of the output on, of
+// which a row's first and last piece may hold fewer; per_row: the most pieces of a row.
 template <typename OUT>
 __global__ void __launch_bounds__(kThreads)
-dequantize_odd_kernel(Fp4View in, unsigned long long chunks, int cols, int nb, int per_row, OUT* __restrict__ Y,
+dequantize_odd_kernel(Fp4View in, unsigned long long pieces, int cols, int nb, int per_row, OUT* __restrict__ Y,
                       long long ldy) {
-    __shared__ float turn[kWarps][256];
+    constexpr int UNROLL = 4;
     pdl_wait();
     pdl_launch_next();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned long long id = (unsigned long long)blockIdx.x * kWarps + warp;
-    if (id >= chunks) return;
-    unsigned long long row;
-    int c;
-    split(id, chunks <= 0xffffffffull, per_row, row, c);
-    const int b = 8 * c + (lane >> 2);
-    float v[8] = {};
-    if (b < nb)
-        value8<OUT>(*reinterpret_cast<const uint32_t*>(in.codes + row * in.ld + 16 * b + 4 * (lane & 3)),
-                    in.scales[row * in.lds + b], v);
+    const unsigned long long base = (unsigned long long)blockIdx.x * (kThreads * UNROLL) + threadIdx.x;
+    const bool small = pieces <= 0xffffffffull;
+    uint32_t w[UNROLL][2], E[UNROLL][2];
+    unsigned long long row[UNROLL];
+    int j[UNROLL];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) turn[warp][8 * lane + i] = v[i];
-    __syncwarp();
-    OUT* y = Y + row * ldy + 256 * (long long)c;
-    const int n = cols - 256 * c;
+    for (int u = 0; u < UNROLL; ++u) {
+        const unsigned long long id = base + (unsigned long long)u * kThreads;
+        split(id < pieces ? id : pieces - 1, small, per_row, row[u], j[u]);
+        // words j - 1 and j of the row's codes, where it has them
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int k = 32 * i + lane;
-        if (k < n) y[k] = from_f32<OUT>(turn[warp][k]);
+        for (int i = 0; i < 2; ++i) {
+            const int k = j[u] - 1 + i;
+            const bool is = k >= 0 && k < 4 * nb;
+            w[u][i] = is ? *reinterpret_cast<const uint32_t*>(in.codes + row[u] * in.ld + 4 * k) : 0u;
+            E[u][i] = is ? in.scales[row[u] * in.lds + (k >> 2)] : 0u;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        if (base + (unsigned long long)u * kThreads >= pieces) return;
+        OUT* y = Y + row[u] * ldy;
+        const int o = (int)(reinterpret_cast<uintptr_t>(y) % 16 / sizeof(OUT));     // values before the row in its first piece
+        const float s0 = fp4_scale(E[u][0]), s1 = fp4_scale(E[u][1]);
+        float v[8];
+        fp4_unpack8(__funnelshift_rc(w[u][0], w[u][1], 4 * (8 - o)), v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= i < o ? s0 : s1;
+        const uint32_t c = 8u * j[u] - o;           // before the row: a column past every other
+        if (cols >= 8 && c <= (uint32_t)cols - 8u) {
+            store8(y + c, v);
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i)
+                if (c + i < (uint32_t)cols) y[c + i] = from_f32<OUT>(v[i]);
+        }
     }
 }
 
@@ -263,19 +294,14 @@ bool rows_aligned(const void* p, long long ld, int esz) { return fp8_on(p, 16) &
 
 template <typename IN>
 cudaError_t quantize(const IN* X, long long rows, int cols, long long ldx, const Fp4View& out, cudaStream_t s) {
-    const int nb = (int)fp4_blocks(cols);
-    if (rows_aligned(X, ldx, sizeof(IN))) {
-        constexpr int PER = kThreads * kInFlight<IN>;
-        const unsigned long long pieces = 2ull * rows * nb, grid = (pieces + PER - 1) / PER;
-        if (grid > 0x7fffffffull) return cudaErrorNotSupported;
-        return launch_k(quantize_kernel<IN>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, pieces, cols, nb,
-                        kThreads / (2 * nb), kThreads % (2 * nb), ldx, out);
-    }
-    const int per_row = (cols + 255) / 256;
-    const unsigned long long chunks = (unsigned long long)rows * per_row, grid = (chunks + kWarps - 1) / kWarps;
+    const int nb = (int)fp4_blocks(cols), dq = kThreads / (2 * nb), dr = kThreads % (2 * nb);
+    constexpr int PER = kThreads * kInFlight<IN>;
+    const unsigned long long pieces = 2ull * rows * nb, grid = (pieces + PER - 1) / PER;
     if (grid > 0x7fffffffull) return cudaErrorNotSupported;
-    return launch_k(quantize_odd_kernel<IN>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, chunks, cols, nb, per_row, ldx,
-                    out);
+    if (rows_aligned(X, ldx, sizeof(IN)))
+        return launch_k(quantize_kernel<IN>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, pieces, cols, nb, dq, dr, ldx, out);
+    return launch_k(quantize_odd_kernel<IN>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, pieces, cols, nb, dq, dr, ldx,
+                    X + (rows - 1) * ldx + cols, out);
 }
 
 template <typename OUT>
@@ -286,11 +312,11 @@ cudaError_t dequantize(const Fp4View& in, long long rows, int cols, OUT* Y, long
         if (grid > 0x7fffffffull) return cudaErrorNotSupported;
         return launch_k(dequantize_kernel<OUT>, dim3((unsigned)grid), dim3(kThreads), 0, s, in, pieces, cols, nb, Y, ldy);
     }
-    const int per_row = (cols + 255) / 256;
-    const unsigned long long chunks = (unsigned long long)rows * per_row, grid = (chunks + kWarps - 1) / kWarps;
+    const int per_row = (int)((cols + 16 / (long long)sizeof(OUT) - 1 + 7) / 8);
+    const unsigned long long pieces = (unsigned long long)rows * per_row, grid = (pieces + 4 * kThreads - 1) / (4 * kThreads);
     if (grid > 0x7fffffffull) return cudaErrorNotSupported;
-    return launch_k(dequantize_odd_kernel<OUT>, dim3((unsigned)grid), dim3(kThreads), 0, s, in, chunks, cols, nb, per_row,
-                    Y, ldy);
+    return launch_k(dequantize_odd_kernel<OUT>, dim3((unsigned)grid), dim3(kThreads), 0, s, in, pieces, cols, nb, per_row, Y,
+                    ldy);
 }
 
 template <typename IN>

@@ -125,6 +125,27 @@ def test_quantize_takes_strided_and_misaligned_rows_and_refuses_others():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cols,gap", [(1, 0), (2, 1), (7, 0), (15, 2), (17, 0), (33, 0), (63, 5), (100, 1), (257, 0), (1003, 4)])
+def test_rows_of_every_alignment(cols, gap, dtype):
+    """Rows from each element of 16 bytes on, `gap` values apart: only they are read and only they are written."""
+    n, ld, tdt, code = 37, cols + gap, DTYPES[dtype], {"bf16": _lib.RM_BF16, "f32": _lib.RM_F32}[dtype]
+    for at in range(17 - 8 * (dtype == "f32")):
+        size = at + (n - 1) * ld + cols
+        flat = torch.full((size + 11,), float("nan"), dtype=tdt, device=DEV)
+        v = flat[at:size].as_strided((n, cols), (ld, 1), at)
+        x = rows((n, cols), 7 + at, 2.0).to(tdt)
+        v.copy_(x)
+        q, (c, E) = fp4_quantize(v), ref.quantise(x)
+        assert torch.equal(q.codes.cpu(), ref.packed(c)) and torch.equal(q.scales.cpu()[..., :E.shape[-1]], E), at
+        y = torch.full_like(flat, 5.0)
+        _lib.rm_fp4_dequantize(q.c, n, cols, y[at:].data_ptr(), code, ld, torch.cuda.current_stream().cuda_stream)
+        want = torch.full((size + 11,), 5.0, dtype=tdt)
+        want.as_strided((n, cols), (ld, 1), at).copy_(ref.value(q).cpu())
+        assert torch.equal(y.cpu(), want), at
+    ok()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shape", [(1, 1, 1), (2, 128, 128), (3, 129, 127), (2, 200, 1001), (1, 400, 16), (5, 64, 256),
                                    (2, 3, 33, 40), (300, 20)])
 def test_quantize_weight_is_the_format_bit_for_bit(shape, dtype):
