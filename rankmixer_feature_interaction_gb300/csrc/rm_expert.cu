@@ -10,15 +10,16 @@
 // before, the slots.  Up to kSmallSort gates of few rows one CTA does both, without
 // the first launch.  No atomics, so the order is always the same.
 //
-// Rows.  A warp takes a run of a row (b, t), reads it once and writes it to (or sums it
-// from) the slots of its open experts, in ascending order of e; two experts' rows are on
-// their way at a time.  For few rows the gates' gradient, which sums over a whole row,
-// takes all four warps of a CTA.  Bound by memory.
-// Measured, T = 32, E = 8, D = 1536 in bf16, 2048 samples, 131,000 sorted rows: sort 10
-// us, gather 89 us (6.8 TB/s), combine 102 (5.9), its gradient 146 (6.9), the gather's
-// gradient 100 (6.0).  8 samples: 4, 3.3, 5.2, 5.6 and 5.2 us, latency; a warp per row and
-// one expert after another took 6.8, 4.4, 10.0, 10.5 and 9.8.  777 samples of T = 5, E = 6,
-// D = 1003 in float32, not 16-byte aligned: 11.5, 10, 12.5, 15 and 12.5 us.
+// Rows.  A warp (for short rows a part of one) takes a run of a row (b, t), reads it once
+// and writes it to (or sums it from) the slots of its open experts, in ascending order of
+// e; two experts' rows are on their way at a time.  For few long rows the gates' gradient,
+// which sums over a whole row, takes all four warps of a CTA.  Bound by memory.
+// Measured, T = 32, E = 8, D = 1536 in bf16, two open, 2048 samples, 131,072 sorted rows:
+// sort 10 us, gather 88 us (6.9 TB/s), combine 94 (6.4), its gradient 147 (6.9), the
+// gather's gradient 92 (6.6).  8 samples: about 2 us each, latency; a warp per row and one
+// expert after another took twice that.  1397 samples of T = 37, E = 11, D = 32 in bf16, three
+// open: 9.9, 5.0, 8.4, 11.5 and 8.4 us (a warp a row: 9.9, 13.6, 19.3, 24 and 19.3).  777
+// samples of T = 5, E = 6, D = 1003 in float32, not 16-byte aligned: 9.6, 6.4, 6.2, 9.2, 6.2.
 #include <initializer_list>
 
 #include "rm_fp4.cuh"
@@ -286,53 +287,79 @@ struct Piece {
         }
     }
 };
-// A warp takes a run of a row: kHeld pieces a lane, held at once.
+// L lanes (a group) take a run of a row: kHeld pieces a lane, held at once.  L is 32, or
+// 16 or 8 where they hold a whole row: a warp then has two or four rows under way.  Rows
+// to 4 bits go by 8 lanes at any length (65,536 rows of 768 to two experts: 26.7 us, by 32
+// lanes 34.7); longer rows otherwise do not: with 8 lanes 1003 floats that are not 16-byte
+// aligned were combined in 8.3 us instead of 6.2, and the gradient of 1536 took 154, not 147.
 template <bool VEC>
 constexpr int kHeld = VEC ? 3 : 8;
+constexpr int kCodeLanes = 8;
 
 struct Run {
     size_t bt;          // the row
     int p;              // this lane's first piece
     bool there;
 };
-template <int HELD>
+template <int L, int HELD>
 __device__ __forceinline__ Run run_of(const ExpertRows& r, int runs) {
-    const unsigned long long id = (unsigned long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    const unsigned long long id = (unsigned long long)blockIdx.x * (32 * kRowWarps / L) + threadIdx.x / L;
     Run u;
     u.bt = id / (unsigned)runs;
-    u.p = (int)(id - u.bt * runs) * 32 * HELD + (threadIdx.x & 31);
+    u.p = (int)(id - u.bt * runs) * L * HELD + threadIdx.x % L;
     u.there = u.bt < (size_t)r.B * r.T;
     return u;
 }
 
-// Open experts e0 .. e0 + 31 of row bt, as a mask; slot: lane e's.
-__device__ __forceinline__ uint32_t open_experts(const int* __restrict__ slots, size_t bt, int E, int e0, long long n,
+// Open experts e0 .. e0 + L - 1 of row bt, as a mask; slot: lane e's.
+template <int L>
+__device__ __forceinline__ uint32_t open_experts(const int* __restrict__ slots, const Run& u, int E, int e0, long long n,
                                                  int lane, int& slot) {
-    slot = e0 + lane < E ? __ldg(slots + bt * E + e0 + lane) : -1;
-    return __ballot_sync(0xffffffffu, slot >= 0 && slot < n);
+    slot = u.there && e0 + lane < E ? __ldg(slots + u.bt * E + e0 + lane) : -1;
+    const uint32_t m = __ballot_sync(0xffffffffu, slot >= 0 && slot < n);
+    return L == 32 ? m : m >> (threadIdx.x & (32 - L)) & ((1u << (L & 31)) - 1u);
+}
+// A group of the warp has experts left.
+template <int L>
+__device__ __forceinline__ bool any_left(uint32_t m) {
+    return L == 32 ? m != 0 : __any_sync(0xffffffffu, m != 0);
+}
+// The next expert of the mask (0 where there is none), which leaves it.
+__device__ __forceinline__ int next_expert(uint32_t& m) {
+    const int e = m ? __ffs(m) - 1 : 0;
+    m &= m - 1;
+    return e;
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+    for (int o = L / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, int L>
 __global__ void __launch_bounds__(32 * kRowWarps)
 gather_kernel(const T* __restrict__ X, ExpertRows r, T* __restrict__ Xs, long long n, int D, int runs) {
     using P = Piece<T, VEC>;
     constexpr int H = kHeld<VEC>;
     pdl_wait();
     pdl_launch_next();
-    const int lane = threadIdx.x & 31, pieces = D / P::N;
-    const Run u = run_of<H>(r, runs);
-    if (!u.there) return;
+    const int lane = threadIdx.x % L;
+    const Run u = run_of<L, H>(r, runs);
+    const int pieces = u.there ? D / P::N : 0;
     P x[H];
 #pragma unroll
     for (int i = 0; i < H; ++i)
-        if (u.p + 32 * i < pieces) x[i].load(X + u.bt * D + (size_t)(u.p + 32 * i) * P::N);
-    for (int e0 = 0; e0 < r.E; e0 += 32) {
+        if (u.p + L * i < pieces) x[i].load(X + u.bt * D + (size_t)(u.p + L * i) * P::N);
+    for (int e0 = 0; e0 < r.E; e0 += L) {
         int slot;
-        for (uint32_t m = open_experts(r.slot, u.bt, r.E, e0, n, lane, slot); m; m &= m - 1) {
-            T* dst = Xs + (size_t)__shfl_sync(0xffffffffu, slot, __ffs(m) - 1) * D;
+        uint32_t m = open_experts<L>(r.slot, u, r.E, e0, n, lane, slot);
+        while (any_left<L>(m)) {
+            const bool is = m != 0;
+            T* dst = Xs + (size_t)__shfl_sync(0xffffffffu, slot, next_expert(m), L) * D;
 #pragma unroll
             for (int i = 0; i < H; ++i)
-                if (u.p + 32 * i < pieces) x[i].store(dst + (size_t)(u.p + 32 * i) * P::N);
+                if (is && u.p + L * i < pieces) x[i].store(dst + (size_t)(u.p + L * i) * P::N);
         }
     }
 }
@@ -341,14 +368,14 @@ gather_kernel(const T* __restrict__ X, ExpertRows r, T* __restrict__ Xs, long lo
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(32 * kRowWarps)
 gather_fp4_kernel(const T* __restrict__ X, ExpertRows r, Fp4View out, long long n, int D, int nb, int runs) {
+    constexpr int L = kCodeLanes;
     pdl_wait();
     pdl_launch_next();
-    const int lane = threadIdx.x & 31;
-    const Run u = run_of<1>(r, runs);
-    if (!u.there) return;
+    const int lane = threadIdx.x % L;
+    const Run u = run_of<L, 1>(r, runs);
     Fp4Raw16<T> v;
     const T* p = X + u.bt * D + 16 * (size_t)u.p;
-    const int left = D - 16 * u.p;                                               // past the row's end: zeros
+    const int left = u.there ? D - 16 * u.p : 0;                                 // past the row's end: zeros
     if constexpr (VEC) {
         v.template load<true>(p, left);
     } else {
@@ -358,24 +385,25 @@ gather_fp4_kernel(const T* __restrict__ X, ExpertRows r, Fp4View out, long long 
         v.take(p, left, in, t);
     }
     int slot;
-    uint32_t m = open_experts(r.slot, u.bt, r.E, 0, n, lane, slot);
+    uint32_t m = open_experts<L>(r.slot, u, r.E, 0, n, lane, slot);
     uint32_t E;
     const uint2 code = v.round(E);
     for (int e0 = 0;;) {
-        for (; m; m &= m - 1) {
-            const size_t row = (size_t)__shfl_sync(0xffffffffu, slot, __ffs(m) - 1);
-            if (u.p < 2 * nb) {
+        while (any_left<L>(m)) {
+            const bool is = m != 0 && u.p < 2 * nb;
+            const size_t row = (size_t)__shfl_sync(0xffffffffu, slot, next_expert(m), L);
+            if (is) {
                 *reinterpret_cast<uint2*>(out.codes + row * out.ld + 8 * u.p) = code;
                 if ((u.p & 1) == 0) out.scales[row * out.lds + (u.p >> 1)] = (uint8_t)E;
             }
         }
-        if ((e0 += 32) >= r.E) break;
-        m = open_experts(r.slot, u.bt, r.E, e0, n, lane, slot);
+        if ((e0 += L) >= r.E) break;
+        m = open_experts<L>(r.slot, u, r.E, e0, n, lane, slot);
     }
 }
 
 // TO: the type of V; sums in float32, ascending e, two experts' rows loaded at a time.
-template <typename T, typename TO, bool VEC>
+template <typename T, typename TO, bool VEC, int L>
 __global__ void __launch_bounds__(32 * kRowWarps)
 combine_kernel(const T* __restrict__ Y, ExpertRows r, const float* __restrict__ G, TO* __restrict__ V, long long n, int D,
                int runs) {
@@ -383,33 +411,32 @@ combine_kernel(const T* __restrict__ Y, ExpertRows r, const float* __restrict__ 
     constexpr int H = kHeld<VEC>, N = P::N;
     pdl_wait();
     pdl_launch_next();
-    const int lane = threadIdx.x & 31, pieces = D / N;
-    const Run u = run_of<H>(r, runs);
-    if (!u.there) return;
+    const int lane = threadIdx.x % L;
+    const Run u = run_of<L, H>(r, runs);
+    const int pieces = u.there ? D / N : 0;
     float v[H][N] = {};
-    for (int e0 = 0; e0 < r.E; e0 += 32) {
-        const float gate = G && e0 + lane < r.E ? __ldg(G + u.bt * r.E + e0 + lane) : 1.f;
+    for (int e0 = 0; e0 < r.E; e0 += L) {
+        const float gate = G && u.there && e0 + lane < r.E ? __ldg(G + u.bt * r.E + e0 + lane) : 1.f;
         int slot;
-        uint32_t m = open_experts(r.slot, u.bt, r.E, e0, n, lane, slot);
-        while (m) {
-            const int e = __ffs(m) - 1;
-            m &= m - 1;
+        uint32_t m = open_experts<L>(r.slot, u, r.E, e0, n, lane, slot);
+        while (any_left<L>(m)) {
+            const bool one = m != 0;
+            const int e = next_expert(m);
             const bool two = m != 0;
-            const int f = two ? __ffs(m) - 1 : e;
-            m &= m - 1;
-            const T* src = Y + (size_t)__shfl_sync(0xffffffffu, slot, e) * D;
-            const T* src2 = Y + (size_t)__shfl_sync(0xffffffffu, slot, f) * D;
-            const float g = __shfl_sync(0xffffffffu, gate, e), g2 = __shfl_sync(0xffffffffu, gate, f);
+            const int f = next_expert(m);
+            const T* src = Y + (size_t)__shfl_sync(0xffffffffu, slot, e, L) * D;
+            const T* src2 = Y + (size_t)__shfl_sync(0xffffffffu, slot, f, L) * D;
+            const float g = __shfl_sync(0xffffffffu, gate, e, L), g2 = __shfl_sync(0xffffffffu, gate, f, L);
             P y[H], z[H];
 #pragma unroll
             for (int i = 0; i < H; ++i)
-                if (u.p + 32 * i < pieces) {
-                    y[i].load(src + (size_t)(u.p + 32 * i) * N);
-                    if (two) z[i].load(src2 + (size_t)(u.p + 32 * i) * N);
+                if (one && u.p + L * i < pieces) {
+                    y[i].load(src + (size_t)(u.p + L * i) * N);
+                    if (two) z[i].load(src2 + (size_t)(u.p + L * i) * N);
                 }
 #pragma unroll
             for (int i = 0; i < H; ++i)
-                if (u.p + 32 * i < pieces) {
+                if (one && u.p + L * i < pieces) {
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
                         v[i][k] = fmaf(g, y[i].get(k), v[i][k]);
@@ -420,8 +447,8 @@ combine_kernel(const T* __restrict__ Y, ExpertRows r, const float* __restrict__ 
     }
 #pragma unroll
     for (int i = 0; i < H; ++i)
-        if (u.p + 32 * i < pieces) {
-            TO* dst = V + u.bt * D + (size_t)(u.p + 32 * i) * N;
+        if (u.p + L * i < pieces) {
+            TO* dst = V + u.bt * D + (size_t)(u.p + L * i) * N;
             if constexpr (sizeof(T) == sizeof(TO)) {
                 Piece<TO, VEC> o;
                 o.set(v[i]);
@@ -437,41 +464,44 @@ combine_kernel(const T* __restrict__ Y, ExpertRows r, const float* __restrict__ 
         }
 }
 
-// WARPS warps a row (where rows are few, all of the CTA's), two experts at a time.
-template <typename T, bool VEC, int WARPS>
+// L lanes a row, or WARPS warps (where rows are few, all of the CTA's); two experts at a time.
+template <typename T, bool VEC, int L, int WARPS>
 __global__ void __launch_bounds__(32 * kRowWarps)
 combine_backward_kernel(const T* __restrict__ dV, const T* __restrict__ Y, ExpertRows r, const float* __restrict__ G,
                         T* __restrict__ dY, float* __restrict__ dG, long long n, int D) {
+    static_assert(L == 32 || WARPS == 1, "warps share a row whole");
     using P = Piece<T, VEC>;
-    constexpr int H = WARPS == 1 || !VEC ? kHeld<VEC> : 2, N = P::N, STEP = 32 * WARPS;
+    constexpr int H = WARPS == 1 || !VEC ? kHeld<VEC> : 2, N = P::N, STEP = L * WARPS;
     __shared__ float sums[2][kRowWarps];
     pdl_wait();
     pdl_launch_next();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pieces = D / N;
-    const size_t bt = (size_t)blockIdx.x * (kRowWarps / WARPS) + (WARPS == 1 ? warp : 0);
-    if (bt >= (size_t)r.B * r.T) return;
-    const int first = WARPS == 1 ? lane : (int)threadIdx.x;
-    for (int e0 = 0; e0 < r.E; e0 += 32) {
-        const float gate = e0 + lane < r.E ? __ldg(G + bt * r.E + e0 + lane) : 0.f;
+    const int lane = threadIdx.x % L, warp = threadIdx.x >> 5;
+    Run u;
+    u.bt = (size_t)blockIdx.x * (32 * kRowWarps / STEP) + threadIdx.x / STEP;
+    u.p = threadIdx.x % STEP;
+    u.there = u.bt < (size_t)r.B * r.T;
+    const int pieces = u.there ? D / N : 0;
+    for (int e0 = 0; e0 < r.E; e0 += L) {
+        const float gate = u.there && e0 + lane < r.E ? __ldg(G + u.bt * r.E + e0 + lane) : 0.f;
         int slot;
-        uint32_t m = open_experts(r.slot, bt, r.E, e0, n, lane, slot);
+        uint32_t m = open_experts<L>(r.slot, u, r.E, e0, n, lane, slot);
         float mine = 0.f;                                   // lane e's dG
-        while (m) {
-            const int e = __ffs(m) - 1;
-            m &= m - 1;
+        while (any_left<L>(m)) {
+            const bool one = m != 0;
+            const int e = next_expert(m);
             const bool two = m != 0;
-            const int f = two ? __ffs(m) - 1 : e;
-            m &= m - 1;
-            const size_t row = (size_t)__shfl_sync(0xffffffffu, slot, e) * D, row2 = (size_t)__shfl_sync(0xffffffffu, slot, f) * D;
-            const float g = __shfl_sync(0xffffffffu, gate, e), g2 = __shfl_sync(0xffffffffu, gate, f);
+            const int f = next_expert(m);
+            const size_t row = (size_t)__shfl_sync(0xffffffffu, slot, e, L) * D;
+            const size_t row2 = (size_t)__shfl_sync(0xffffffffu, slot, f, L) * D;
+            const float g = __shfl_sync(0xffffffffu, gate, e, L), g2 = __shfl_sync(0xffffffffu, gate, f, L);
             float dot = 0.f, dot2 = 0.f;
-            for (int p0 = first; p0 < pieces; p0 += STEP * H) {
+            for (int p0 = u.p; one && p0 < pieces; p0 += STEP * H) {
                 P y[H], z[H], d[H];
 #pragma unroll
                 for (int i = 0; i < H; ++i)
                     if (p0 + STEP * i < pieces) {
                         const size_t at = (size_t)(p0 + STEP * i) * N;
-                        d[i].load(dV + bt * D + at);
+                        d[i].load(dV + u.bt * D + at);
                         y[i].load(Y + row + at);
                         if (two) z[i].load(Y + row2 + at);
                     }
@@ -499,8 +529,8 @@ combine_backward_kernel(const T* __restrict__ dV, const T* __restrict__ Y, Exper
                         }
                     }
             }
-            dot = warp_sum(dot);
-            dot2 = warp_sum(dot2);
+            dot = group_sum<L>(dot);
+            dot2 = group_sum<L>(dot2);
             if constexpr (WARPS > 1) {                      // the same mask in every warp of the CTA
                 __syncthreads();
                 if (lane == 0) sums[0][warp] = dot, sums[1][warp] = dot2;
@@ -509,10 +539,10 @@ combine_backward_kernel(const T* __restrict__ dV, const T* __restrict__ Y, Exper
 #pragma unroll
                 for (int w = 0; w < WARPS; ++w) dot += sums[0][w], dot2 += sums[1][w];
             }
-            if (lane == e) mine = dot;
+            if (one && lane == e) mine = dot;
             if (two && lane == f) mine = dot2;
         }
-        if (e0 + lane < r.E && (WARPS == 1 || warp == 0)) dG[bt * r.E + e0 + lane] = mine;
+        if (u.there && e0 + lane < r.E && (WARPS == 1 || warp == 0)) dG[u.bt * r.E + e0 + lane] = mine;
     }
 }
 
@@ -525,24 +555,29 @@ bool aligned_rows(std::initializer_list<const void*> ps, int D, int esz) {
     return D * (long long)esz % 16 == 0;
 }
 const dim3 kRowBlock(32 * kRowWarps);
-// CTAs for `runs` warps a row.
-bool row_grid(const ExpertRows& r, long long runs, dim3* grid) {
-    const long long ctas = ((long long)r.B * r.T * runs + kRowWarps - 1) / kRowWarps;
+// CTAs for `runs` groups of `lanes` lanes a row.
+bool row_grid(const ExpertRows& r, long long runs, int lanes, dim3* grid) {
+    const int per = 32 * kRowWarps / lanes;
+    const long long ctas = ((long long)r.B * r.T * runs + per - 1) / per;
     *grid = dim3((unsigned)ctas);
     return ctas <= 0x7fffffffll;
 }
-template <bool VEC>
-int runs_of(int D, int esz) {
-    const int per = 32 * kHeld<VEC> * (VEC ? 16 / esz : 1);
-    return (int)(((long long)D + per - 1) / per);
+// Lanes of a group that takes `pieces` pieces a row, `held` a lane at once.
+int lanes_of(long long pieces, int held) { return pieces <= 8 * held ? 8 : pieces <= 16 * held ? 16 : 32; }
+int runs_of(long long pieces, int held, int lanes) { return (int)((pieces + lanes * held - 1) / (lanes * held)); }
+template <typename T, bool VEC>
+long long pieces_of(int D) {
+    return D / (VEC ? 16 / (int)sizeof(T) : 1);
 }
 
 template <typename T, bool VEC>
 cudaError_t gather_v(const T* X, const ExpertRows& r, T* Xs, long long n, int D, cudaStream_t s) {
-    const int runs = runs_of<VEC>(D, sizeof(T));
+    const long long pieces = pieces_of<T, VEC>(D);
+    const int lanes = lanes_of(pieces, kHeld<VEC>), runs = runs_of(pieces, kHeld<VEC>, lanes);
     dim3 grid;
-    if (!row_grid(r, runs, &grid)) return cudaErrorNotSupported;
-    return launch_k(gather_kernel<T, VEC>, grid, kRowBlock, 0, s, X, r, Xs, n, D, runs);
+    if (!row_grid(r, runs, lanes, &grid)) return cudaErrorNotSupported;
+    auto k = lanes == 8 ? gather_kernel<T, VEC, 8> : lanes == 16 ? gather_kernel<T, VEC, 16> : gather_kernel<T, VEC, 32>;
+    return launch_k(k, grid, kRowBlock, 0, s, X, r, Xs, n, D, runs);
 }
 template <typename T>
 cudaError_t gather(const T* X, const ExpertRows& r, T* Xs, long long n, int D, cudaStream_t s) {
@@ -551,17 +586,21 @@ cudaError_t gather(const T* X, const ExpertRows& r, T* Xs, long long n, int D, c
 template <typename T>
 cudaError_t gather_fp4(const T* X, const ExpertRows& r, const Fp4View& out, long long n, int D, cudaStream_t s) {
     auto k = aligned_rows({X}, D, sizeof(T)) ? gather_fp4_kernel<T, true> : gather_fp4_kernel<T, false>;
-    const int nb = (int)fp4_blocks(D), runs = (2 * nb + 31) / 32;
+    const int nb = (int)fp4_blocks(D), runs = runs_of(2ll * nb, 1, kCodeLanes);
     dim3 grid;
-    if (!row_grid(r, runs, &grid)) return cudaErrorNotSupported;
+    if (!row_grid(r, runs, kCodeLanes, &grid)) return cudaErrorNotSupported;
     return launch_k(k, grid, kRowBlock, 0, s, X, r, out, n, D, nb, runs);
 }
 template <typename T, typename TO, bool VEC>
 cudaError_t combine_v(const T* Y, const ExpertRows& r, const float* G, TO* V, long long n, int D, cudaStream_t s) {
-    const int runs = runs_of<VEC>(D, sizeof(T));
+    const long long pieces = pieces_of<T, VEC>(D);
+    const int lanes = lanes_of(pieces, kHeld<VEC>), runs = runs_of(pieces, kHeld<VEC>, lanes);
     dim3 grid;
-    if (!row_grid(r, runs, &grid)) return cudaErrorNotSupported;
-    return launch_k(combine_kernel<T, TO, VEC>, grid, kRowBlock, 0, s, Y, r, G, V, n, D, runs);
+    if (!row_grid(r, runs, lanes, &grid)) return cudaErrorNotSupported;
+    auto k = lanes == 8    ? combine_kernel<T, TO, VEC, 8>
+             : lanes == 16 ? combine_kernel<T, TO, VEC, 16>
+                           : combine_kernel<T, TO, VEC, 32>;
+    return launch_k(k, grid, kRowBlock, 0, s, Y, r, G, V, n, D, runs);
 }
 template <typename T, typename TO>
 cudaError_t combine(const T* Y, const ExpertRows& r, const float* G, TO* V, long long n, int D, cudaStream_t s) {
@@ -571,10 +610,14 @@ cudaError_t combine(const T* Y, const ExpertRows& r, const float* G, TO* V, long
 template <typename T, bool VEC>
 cudaError_t combine_backward_v(const T* dV, const T* Y, const ExpertRows& r, const float* G, T* dY, float* dG, long long n,
                                int D, cudaStream_t s) {
-    const bool few = (long long)r.B * r.T <= kFewRows;
+    const int lanes = lanes_of(pieces_of<T, VEC>(D), kHeld<VEC>);
+    const bool few = lanes == 32 && (long long)r.B * r.T <= kFewRows;
     dim3 grid;
-    if (!row_grid(r, few ? kRowWarps : 1, &grid)) return cudaErrorNotSupported;
-    auto k = few ? combine_backward_kernel<T, VEC, kRowWarps> : combine_backward_kernel<T, VEC, 1>;
+    if (!row_grid(r, few ? kRowWarps : 1, lanes, &grid)) return cudaErrorNotSupported;
+    auto k = few           ? combine_backward_kernel<T, VEC, 32, kRowWarps>
+             : lanes == 8  ? combine_backward_kernel<T, VEC, 8, 1>
+             : lanes == 16 ? combine_backward_kernel<T, VEC, 16, 1>
+                           : combine_backward_kernel<T, VEC, 32, 1>;
     return launch_k(k, grid, kRowBlock, 0, s, dV, Y, r, G, dY, dG, n, D);
 }
 template <typename T>

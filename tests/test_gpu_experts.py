@@ -61,6 +61,8 @@ def test_sort_leaves_the_rest_of_source_alone():
 
 ROWS = [(1, 1, 1, 1), (3, 2, 5, 4), (8, 4, 768, 8), (70, 3, 1003, 6), (5, 2, 40, 40), (130, 5, 264, 3), (9, 1, 2056, 33),
         (2, 1, 4099, 2)]
+# rows that a part of a warp takes, with more and fewer experts than its lanes
+ROWS += [(131, 3, 100, 19), (37, 5, 64, 17), (1201, 7, 24, 11), (333, 3, 320, 9), (1, 3, 192, 8), (59, 1, 65, 5), (23, 3, 128, 65)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -146,7 +148,7 @@ def test_room_for_fewer_rows(D, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("B,T,D,E", [(3, 2, 5, 4), (8, 4, 768, 8), (70, 3, 1003, 6), (5, 2, 40, 40)])
+@pytest.mark.parametrize("B,T,D,E", [(3, 2, 5, 4), (8, 4, 768, 8), (70, 3, 1003, 6), (5, 2, 40, 40), (37, 3, 100, 19), (11, 1, 33, 9)])
 def test_gather_in_4_bits_is_gather_then_quantize(B, T, D, E, dtype):
     r = expert_sort(gates(B, T, E, 0.5, 9).to(DEV))
     n = r.count()
