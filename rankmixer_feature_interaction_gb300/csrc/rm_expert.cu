@@ -376,14 +376,10 @@ gather_fp4_kernel(const T* __restrict__ X, ExpertRows r, Fp4View out, long long 
     Fp4Raw16<T> v;
     const T* p = X + u.bt * D + 16 * (size_t)u.p;
     const int left = u.there ? D - 16 * u.p : 0;                                 // past the row's end: zeros
-    if constexpr (VEC) {
+    if constexpr (VEC)
         v.template load<true>(p, left);
-    } else {
-        const bool in = left <= 0 || Fp4Raw16<T>::inside(p, left, X, X + (size_t)r.B * r.T * D);
-        uint32_t t[Fp4Raw16<T>::AROUND];
-        Fp4Raw16<T>::fetch(p, left, in && left > 0, t);
-        v.take(p, left, in, t);
-    }
+    else
+        v.load_any(p, left, X, X + (size_t)r.B * r.T * D);
     int slot;
     uint32_t m = open_experts<L>(r.slot, u, r.E, 0, n, lane, slot);
     uint32_t E;

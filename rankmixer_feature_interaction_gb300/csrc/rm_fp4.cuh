@@ -90,44 +90,35 @@ struct Fp4Raw16 {
             }
         }
     }
-    // Any p, in two steps: whole 16-byte pieces of memory, and what of them is the row's.
-    // Only pieces inside [lo, hi) are read whole; at its two ends single values are.
-    static constexpr int AROUND = WORDS + 4;
-    __device__ __forceinline__ static bool inside(const IN* p, int n, const IN* lo, const IN* hi) {
+    // Any p: the whole 16-byte pieces of memory around the values, shifted into place,
+    // where they lie inside [lo, hi); single values at its two ends.
+    __device__ __forceinline__ void load_any(const IN* __restrict__ p, int n, const IN* lo, const IN* hi) {
         const uintptr_t a = reinterpret_cast<uintptr_t>(p), end = a + sizeof(IN) * min(n, 16);
-        return (a & ~(uintptr_t)15) >= reinterpret_cast<uintptr_t>(lo) &&
-               ((end + 15) & ~(uintptr_t)15) <= reinterpret_cast<uintptr_t>(hi);
-    }
-    __device__ __forceinline__ static void fetch(const IN* __restrict__ p, int n, bool in, uint32_t (&t)[AROUND]) {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(p);
         const uint4* q = reinterpret_cast<const uint4*>(a & ~(uintptr_t)15);
-        const int bytes = in ? (int)(a & 15) + (int)sizeof(IN) * min(n, 16) : 0;
-#pragma unroll
-        for (int i = 0; i < AROUND / 4; ++i) {
-            const uint4 x = 16 * i < bytes ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
-            t[4 * i] = x.x, t[4 * i + 1] = x.y, t[4 * i + 2] = x.z, t[4 * i + 3] = x.w;
-        }
-    }
-    __device__ __forceinline__ void take(const IN* __restrict__ p, int n, bool in, uint32_t (&t)[AROUND]) {
-        if (!in) {
+        if (n <= 0 || q < reinterpret_cast<const uint4*>(lo) || ((end + 15) & ~(uintptr_t)15) > reinterpret_cast<uintptr_t>(hi)) {
             load<false>(p, n);
             return;
         }
-        const uint32_t o = (uint32_t)reinterpret_cast<uintptr_t>(p);
-        if (o & 8) {
+        uint32_t t[WORDS + 4];
 #pragma unroll
-            for (int i = 0; i + 2 < AROUND; ++i) t[i] = t[i + 2];
+        for (int i = 0; i <= WORDS / 4; ++i) {
+            const uint4 x = reinterpret_cast<uintptr_t>(q + i) < end ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+            t[4 * i] = x.x, t[4 * i + 1] = x.y, t[4 * i + 2] = x.z, t[4 * i + 3] = x.w;
         }
-        if (o & 4) {
+        if (a & 8) {
 #pragma unroll
-            for (int i = 0; i + 1 < AROUND; ++i) t[i] = t[i + 1];
+            for (int i = 0; i + 2 < WORDS + 4; ++i) t[i] = t[i + 2];
+        }
+        if (a & 4) {
+#pragma unroll
+            for (int i = 0; i + 1 < WORDS + 4; ++i) t[i] = t[i + 1];
         }
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) {
             if constexpr (sizeof(IN) == 4) {
                 w[i] = i < n ? t[i] : 0u;
             } else {
-                w[i] = 2 * i < n ? __funnelshift_r(t[i], t[i + 1], 8 * (o & 2)) : 0u;
+                w[i] = 2 * i < n ? __funnelshift_r(t[i], t[i + 1], 8 * (uint32_t)(a & 2)) : 0u;
                 if (2 * i + 1 >= n) w[i] &= 0xffffu;
             }
         }

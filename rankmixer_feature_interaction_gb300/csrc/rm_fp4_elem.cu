@@ -7,9 +7,9 @@
 // Measured, 65,536 rows of 6144 in bf16: to 4 bits 147 us (6.9 TB/s; 326 with eight values
 // a lane, unpacked at once), back 154 us (6.6 TB/s): bound by memory, 2.53 bytes a value.
 // Rows that are not 16-byte aligned go by 16-byte pieces of memory too, those around the
-// values, which are then shifted into place: 126,840 bf16 rows of 1547 to 4 bits 114 us
-// (1552 columns, aligned: 79), back 117 us (80).  An element at a time, their order
-// changed in shared memory, they took 262 and 160 us, and 47,720 rows of 33 15.7 us (4.7).
+// values, which are then shifted into place: 126,840 bf16 rows of 1547 to 4 bits 103 us
+// (1552 columns, aligned: 79), back 119 us (80).  An element at a time, their order
+// changed in shared memory, they took 262 and 160 us, and 47,720 rows of 33 15.7 us (3.8).
 #include "rm_fp4.cuh"
 
 namespace rm {
@@ -68,43 +68,29 @@ quantize_kernel(const IN* __restrict__ X, unsigned long long pieces, int cols, i
     }
 }
 
-// Other rows: a lane reads the 16-byte pieces around its values and shifts them; end:
-// behind the last row's last value.
+// Other rows: a lane reads the 16-byte pieces around its values and shifts them, one
+// block half a thread (four in flight took registers: 114 us where this takes 103).
+// end: behind the last row's last value.
 template <typename IN>
 __global__ void __launch_bounds__(kThreads)
-quantize_odd_kernel(const IN* __restrict__ X, unsigned long long pieces, int cols, int nb, int dq, int dr, long long ldx,
+quantize_odd_kernel(const IN* __restrict__ X, unsigned long long pieces, int cols, int nb, long long ldx,
                     const IN* __restrict__ end, Fp4View out) {
-    constexpr int UNROLL = kInFlight<IN>;
     pdl_wait();
     pdl_launch_next();
-    const unsigned long long base = (unsigned long long)blockIdx.x * (kThreads * UNROLL) + threadIdx.x;
+    const unsigned long long id = (unsigned long long)blockIdx.x * kThreads + threadIdx.x;
+    const bool there = id < pieces;
     unsigned long long row;
     int j;
-    split(base, pieces <= 0xffffffffull, 2u * nb, row, j);
-    uint32_t t[UNROLL][Fp4Raw16<IN>::AROUND];
-    unsigned long long at = row;
-    int k = j;
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-        const int n = base + (unsigned long long)u * kThreads < pieces ? cols - 16 * k : 0;
-        const IN* p = X + at * ldx + 16 * k;
-        Fp4Raw16<IN>::fetch(p, n, n > 0 && Fp4Raw16<IN>::inside(p, n, X, end), t[u]);
-        advance(at, k, dq, dr, 2 * nb);
-    }
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-        const bool there = base + (unsigned long long)u * kThreads < pieces;
-        const int n = there ? cols - 16 * j : 0;
-        const IN* p = X + row * ldx + 16 * j;
-        Fp4Raw16<IN> v;
-        v.take(p, n, n <= 0 || Fp4Raw16<IN>::inside(p, n, X, end), t[u]);
-        uint32_t E;
-        const uint2 c = v.round(E);
-        if (there) {
-            *reinterpret_cast<uint2*>(out.codes + row * out.ld + 8 * j) = c;
-            if ((j & 1) == 0) out.scales[row * out.lds + (j >> 1)] = (uint8_t)E;
-        }
-        advance(row, j, dq, dr, 2 * nb);
+    split(there ? id : pieces - 1, pieces <= 0xffffffffull, 2u * nb, row, j);
+    const int n = cols - 16 * j;
+    const IN* p = X + row * ldx + 16 * j;
+    Fp4Raw16<IN> v;
+    v.load_any(p, n, X, end);
+    uint32_t E;
+    const uint2 c = v.round(E);
+    if (there) {
+        *reinterpret_cast<uint2*>(out.codes + row * out.ld + 8 * j) = c;
+        if ((j & 1) == 0) out.scales[row * out.lds + (j >> 1)] = (uint8_t)E;
     }
 }
 
@@ -294,13 +280,15 @@ bool rows_aligned(const void* p, long long ld, int esz) { return fp8_on(p, 16) &
 
 template <typename IN>
 cudaError_t quantize(const IN* X, long long rows, int cols, long long ldx, const Fp4View& out, cudaStream_t s) {
-    const int nb = (int)fp4_blocks(cols), dq = kThreads / (2 * nb), dr = kThreads % (2 * nb);
-    constexpr int PER = kThreads * kInFlight<IN>;
-    const unsigned long long pieces = 2ull * rows * nb, grid = (pieces + PER - 1) / PER;
+    const int nb = (int)fp4_blocks(cols);
+    const bool aligned = rows_aligned(X, ldx, sizeof(IN));
+    const int per = aligned ? kThreads * kInFlight<IN> : kThreads;
+    const unsigned long long pieces = 2ull * rows * nb, grid = (pieces + per - 1) / per;
     if (grid > 0x7fffffffull) return cudaErrorNotSupported;
-    if (rows_aligned(X, ldx, sizeof(IN)))
-        return launch_k(quantize_kernel<IN>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, pieces, cols, nb, dq, dr, ldx, out);
-    return launch_k(quantize_odd_kernel<IN>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, pieces, cols, nb, dq, dr, ldx,
+    if (aligned)
+        return launch_k(quantize_kernel<IN>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, pieces, cols, nb,
+                        kThreads / (2 * nb), kThreads % (2 * nb), ldx, out);
+    return launch_k(quantize_odd_kernel<IN>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, pieces, cols, nb, ldx,
                     X + (rows - 1) * ldx + cols, out);
 }
 
