@@ -476,7 +476,7 @@ combine_backward_kernel(const T* __restrict__ dV, const T* __restrict__ Y, Exper
     u.bt = (size_t)blockIdx.x * (32 * kRowWarps / STEP) + threadIdx.x / STEP;
     u.p = threadIdx.x % STEP;
     u.there = u.bt < (size_t)r.B * r.T;
-    const int pieces = u.there ? D / N : 0;
+    const uint32_t pieces = u.there ? D / N : 0;
     for (int e0 = 0; e0 < r.E; e0 += L) {
         const float gate = u.there && e0 + lane < r.E ? __ldg(G + u.bt * r.E + e0 + lane) : 0.f;
         int slot;
@@ -491,7 +491,7 @@ combine_backward_kernel(const T* __restrict__ dV, const T* __restrict__ Y, Exper
             const size_t row2 = (size_t)__shfl_sync(0xffffffffu, slot, f, L) * D;
             const float g = __shfl_sync(0xffffffffu, gate, e, L), g2 = __shfl_sync(0xffffffffu, gate, f, L);
             float dot = 0.f, dot2 = 0.f;
-            for (int p0 = u.p; one && p0 < pieces; p0 += STEP * H) {
+            for (uint32_t p0 = u.p; one && p0 < pieces; p0 += STEP * H) {     // (past 2^31 in the last step)
                 P y[H], z[H], d[H];
 #pragma unroll
                 for (int i = 0; i < H; ++i)

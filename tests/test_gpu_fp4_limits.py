@@ -129,6 +129,27 @@ def test_rows_past_32_bits():
     ok()
 
 
+def test_the_longest_rows():
+    """One row of nearly 2^31 values, to two experts and back: steps end past 2^31."""
+    D = 2 ** 31 - 513
+    G = torch.tensor([[[0.5, 2.0]]], device=DEV)
+    r = expert_sort(G)
+    X = torch.zeros((1, 1, D), dtype=torch.bfloat16, device=DEV)
+    at = [0, 1, 12345, 2 ** 30, D - 1200, D - 2, D - 1]
+    value = torch.tensor([1.0, -2.0, 3.0, 5.0, -7.0, 11.0, 13.0])
+    X[0, 0, at] = value.to(DEV, torch.bfloat16)
+    Xs = expert_gather(X, r, 2)
+    assert torch.equal(Xs[0], X[0, 0]) and torch.equal(Xs[1], X[0, 0])
+    V = expert_combine(Xs, r, G)
+    assert V[0, 0, at].float().cpu().tolist() == (2.5 * value).tolist() and int(V.count_nonzero()) == len(at)
+    del V
+    dY, dG = expert_combine_backward(X, Xs, r, G)
+    assert dG.flatten().tolist() == [(value ** 2).sum().item()] * 2
+    for e, g in enumerate((0.5, 2.0)):
+        assert dY[e, at].float().cpu().tolist() == (g * value).tolist() and int(dY[e].count_nonzero()) == len(at)
+    ok()
+
+
 def test_experts_products_past_32_bits():
     """More than 2^31 outputs of sorted rows."""
     B, T, E, K, N = 4096, 32, 8, 64, 2304
