@@ -150,6 +150,23 @@ def test_the_longest_rows():
     ok()
 
 
+@pytest.mark.parametrize("D", [2 ** 31 - 512, 2 ** 31 - 513])
+def test_the_longest_rows_in_4_bits(D):
+    at = torch.tensor([0, 1, 12345, 2 ** 30, D - 1200, D - 2, D - 1])
+    value = torch.tensor([1.0, -2.0, 3.0, 6.0, -1.5, 4.0, 0.5], dtype=torch.bfloat16)     # 4-bit numbers in their blocks
+    X = torch.zeros((1, 1, D), dtype=torch.bfloat16, device=DEV)
+    X[0, 0, at.to(DEV)] = value.to(DEV)
+    q = fp4_quantize(X)
+    y = fp4_dequantize(q)
+    assert y[0, 0, at.to(DEV)].tolist() == value.tolist() and int(y.count_nonzero()) == len(at)
+    del y
+    r = expert_sort(torch.ones((1, 1, 2), device=DEV))
+    x = fp4_expert_gather(X, r, 2)
+    for i in range(2):
+        assert torch.equal(x.codes[i], q.codes[0, 0]) and torch.equal(x.scales[i, :-(-D // 32)], q.scales[0, 0, :-(-D // 32)])
+    ok()
+
+
 def test_experts_products_past_32_bits():
     """More than 2^31 outputs of sorted rows."""
     B, T, E, K, N = 4096, 32, 8, 64, 2304
