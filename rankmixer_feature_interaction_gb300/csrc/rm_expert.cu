@@ -374,12 +374,12 @@ gather_fp4_kernel(const T* __restrict__ X, ExpertRows r, Fp4View out, long long 
     const int lane = threadIdx.x % L;
     const Run u = run_of<L, 1>(r, runs);
     Fp4Raw16<T> v;
-    const T* p = X + u.bt * D + 16 * (size_t)u.p;
+    const size_t at = u.bt * D + 16 * (size_t)u.p;
     const int left = u.there ? D - 16 * u.p : 0;                                 // past the row's end: zeros
     if constexpr (VEC)
-        v.template load<true>(p, left);
+        v.template load<true>(X + at, left);
     else
-        v.load_any(p, left, X, X + (size_t)r.B * r.T * D);
+        v.load_any(X, at, left, (size_t)r.B * r.T * D);
     int slot;
     uint32_t m = open_experts<L>(r.slot, u, r.E, 0, n, lane, slot);
     uint32_t E;

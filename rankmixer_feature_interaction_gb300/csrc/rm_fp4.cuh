@@ -90,36 +90,39 @@ struct Fp4Raw16 {
             }
         }
     }
-    // Any p: the whole 16-byte pieces of memory around the values, shifted into place,
-    // where they lie inside [lo, hi); single values at its two ends.
-    __device__ __forceinline__ void load_any(const IN* __restrict__ p, int n, const IN* lo, const IN* hi) {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(p), end = a + sizeof(IN) * min(n, 16);
-        const uint4* q = reinterpret_cast<const uint4*>(a & ~(uintptr_t)15);
-        if (n <= 0 || q < reinterpret_cast<const uint4*>(lo) || ((end + 15) & ~(uintptr_t)15) > reinterpret_cast<uintptr_t>(hi)) {
+    // Any row, the values from X[at] on: the whole 16-byte pieces of memory around them,
+    // shifted into place; one by one where those might leave X, which has `size` values.
+    __device__ __forceinline__ void load_any(const IN* __restrict__ X, unsigned long long at, int n, unsigned long long size) {
+        constexpr int AROUND = 16 / (int)sizeof(IN);
+        const IN* p = X + at;
+        constexpr int ESZ = sizeof(IN);
+        if (n <= 0 || at < AROUND || at + 16 + AROUND > size) {
             load<false>(p, n);
             return;
         }
+        const uint32_t o = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u, bytes = o + ESZ * min(n, 16);
+        const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) - o);
         uint32_t t[WORDS + 4];
 #pragma unroll
         for (int i = 0; i <= WORDS / 4; ++i) {
-            const uint4 x = reinterpret_cast<uintptr_t>(q + i) < end ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+            const uint4 x = 16u * i < bytes ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
             t[4 * i] = x.x, t[4 * i + 1] = x.y, t[4 * i + 2] = x.z, t[4 * i + 3] = x.w;
         }
-        if (a & 8) {
+        if (o & 8) {
 #pragma unroll
             for (int i = 0; i + 2 < WORDS + 4; ++i) t[i] = t[i + 2];
         }
-        if (a & 4) {
+        if (o & 4) {
 #pragma unroll
             for (int i = 0; i + 1 < WORDS + 4; ++i) t[i] = t[i + 1];
         }
 #pragma unroll
-        for (int i = 0; i < WORDS; ++i) {
-            if constexpr (sizeof(IN) == 4) {
-                w[i] = i < n ? t[i] : 0u;
-            } else {
-                w[i] = 2 * i < n ? __funnelshift_r(t[i], t[i + 1], 8 * (uint32_t)(a & 2)) : 0u;
-                if (2 * i + 1 >= n) w[i] &= 0xffffu;
+        for (int i = 0; i < WORDS; ++i) w[i] = ESZ == 4 ? t[i] : __funnelshift_r(t[i], t[i + 1], 8 * (o & 2));
+        if (n < 16) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                if (4 * i >= ESZ * n) w[i] = 0;
+                if (4 * i + 2 >= ESZ * n) w[i] &= 0xffffu;
             }
         }
     }
@@ -160,19 +163,5 @@ struct Fp4Raw16 {
         return make_uint2(codes(0, s), codes(1, s));
     }
 };
-
-// Eight values of one of a block's four lanes (neighbours) to their codes; E: the block's exponent byte.
-__device__ __forceinline__ uint32_t fp4_round8(float (&v)[8], uint32_t& E) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, fp4_abs_bits(v[i]));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    E = fp4_exponent(m);
-    const float s = fp4_inv_scale(E);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= s;
-    return fp4_pack8(v);
-}
 
 }  // namespace rm

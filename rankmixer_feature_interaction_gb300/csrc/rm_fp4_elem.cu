@@ -7,9 +7,9 @@
 // Measured, 65,536 rows of 6144 in bf16: to 4 bits 147 us (6.9 TB/s; 326 with eight values
 // a lane, unpacked at once), back 154 us (6.6 TB/s): bound by memory, 2.53 bytes a value.
 // Rows that are not 16-byte aligned go by 16-byte pieces of memory too, those around the
-// values, which are then shifted into place: 126,840 bf16 rows of 1547 to 4 bits 103 us
+// values, which are then shifted into place: 126,840 bf16 rows of 1547 to 4 bits 95 us
 // (1552 columns, aligned: 79), back 119 us (80).  An element at a time, their order
-// changed in shared memory, they took 262 and 160 us, and 47,720 rows of 33 15.7 us (3.8).
+// changed in shared memory, they took 262 and 160 us, and 47,720 rows of 33 15.7 us (4).
 #include "rm_fp4.cuh"
 
 namespace rm {
@@ -69,12 +69,12 @@ quantize_kernel(const IN* __restrict__ X, unsigned long long pieces, int cols, i
 }
 
 // Other rows: a lane reads the 16-byte pieces around its values and shifts them, one
-// block half a thread (four in flight took registers: 114 us where this takes 103).
-// end: behind the last row's last value.
+// block half a thread (four in flight took registers: 110 us where one took 103); size:
+// X's values from its first to its last.
 template <typename IN>
 __global__ void __launch_bounds__(kThreads)
 quantize_odd_kernel(const IN* __restrict__ X, unsigned long long pieces, int cols, int nb, long long ldx,
-                    const IN* __restrict__ end, Fp4View out) {
+                    unsigned long long size, Fp4View out) {
     pdl_wait();
     pdl_launch_next();
     const unsigned long long id = (unsigned long long)blockIdx.x * kThreads + threadIdx.x;
@@ -82,10 +82,8 @@ quantize_odd_kernel(const IN* __restrict__ X, unsigned long long pieces, int col
     unsigned long long row;
     int j;
     split(there ? id : pieces - 1, pieces <= 0xffffffffull, 2u * nb, row, j);
-    const int n = cols - 16 * j;
-    const IN* p = X + row * ldx + 16 * j;
     Fp4Raw16<IN> v;
-    v.load_any(p, n, X, end);
+    v.load_any(X, row * ldx + 16 * j, cols - 16 * j, size);
     uint32_t E;
     const uint2 c = v.round(E);
     if (there) {
@@ -289,7 +287,7 @@ cudaError_t quantize(const IN* X, long long rows, int cols, long long ldx, const
         return launch_k(quantize_kernel<IN>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, pieces, cols, nb,
                         kThreads / (2 * nb), kThreads % (2 * nb), ldx, out);
     return launch_k(quantize_odd_kernel<IN>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, pieces, cols, nb, ldx,
-                    X + (rows - 1) * ldx + cols, out);
+                    (unsigned long long)(rows - 1) * ldx + cols, out);
 }
 
 template <typename OUT>
