@@ -162,6 +162,8 @@ def test_gather_in_4_bits_is_gather_then_quantize(B, T, D, E, dtype):
 # (the last two have more than 2^23 values of experts' outputs)
 EXPERTS = [(1, 1, 1, 32, 32), (2, 2, 3, 64, 96), (8, 4, 8, 256, 160), (30, 2, 5, 320, 288), (100, 3, 2, 96, 64),
            (128, 1, 3, 128, 256), (129, 2, 4, 256, 96), (300, 2, 3, 512, 288), (700, 1, 2, 64, 544), (100, 16, 7, 768, 64), (900, 5, 4, 480, 96)]
+# hidden layers that fill part of a tile, more than one tile of rows an expert
+EXPERTS += [(1500, 2, 3, 32, 32), (1300, 2, 2, 160, 32), (700, 2, 4, 32, 288), (1100, 3, 2, 64, 96)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])

@@ -273,7 +273,9 @@ def layer(lead, D, F, seed):
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("x_dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,T,D,F", [(1, 1, 32, 32), (3, 2, 64, 160), (16, 2, 256, 512), (33, 1, 96, 288), (100, 2, 128, 256),
-                                     (130, 3, 320, 1056), (300, 2, 512, 512), (1, 8, 768, 1536)])
+                                     (130, 3, 320, 1056), (300, 2, 512, 512), (1, 8, 768, 1536),
+                                     # many rows by pairs of CTAs, hidden layers that fill part of a tile
+                                     (5000, 4, 64, 32), (2600, 8, 32, 96), (2600, 4, 96, 160), (2600, 4, 224, 288)])
 def test_pffn(B, T, D, F, x_dtype, out):
     w1, b1, w2, b2 = layer((T,), D, F, 20)
     f = Fp4PFFN(w1, b1, w2, b2)
