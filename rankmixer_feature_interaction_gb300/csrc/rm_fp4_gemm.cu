@@ -50,6 +50,7 @@ constexpr int WARP_COLS = 128, CHUNK = 32;      // columns of a warp, and of a t
 constexpr int STAGING = 2048;            // per epilogue warp: 32 rows of 64 bytes
 constexpr int BIAS_BYTES = 2 * CHUNK * 4;       // per epilogue warp
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
+constexpr uint32_t BAND = 8;             // tiles
 constexpr uint32_t ACC1_COL = 192;       // the second accumulator's first column
 constexpr uint32_t SF_COL = 448, SF_COLS = 24;
 // registers: 640 threads launched with 96; 128 x 64 + 512 x 104 = 640 x 96
@@ -62,6 +63,7 @@ static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 struct Args {
     int B, G, K, N;                      // rows of a group (per token), groups
     int m_tiles, n_tiles, kblocks, nb;
+    int band;                            // tiles of columns of a band
     uint32_t units;                      // tiles (per token; experts: the table's length times n_tiles)
     const int4* table;                   // experts: the tiles of rows (null: per token)
     long long n;                         // experts: rows that exist
@@ -80,10 +82,12 @@ struct Args {
 struct Tile {
     int g, m0, rows, n0;
 };
-// Per token, tiles of rows fastest: neighbouring pairs share W's columns, and a
-// token's x (which every tile of columns reads again) stays in L2.  Experts: columns
-// fastest, so that a tile of rows is read from memory once.
-template <bool EXPERTS>
+// Per token by bands of columns, in a band columns fastest: W's columns and a token's x
+// stay in L2, and a row's outputs are written next to each other.  Bands of 8 tiles: 1536
+// to 6144, 4096 samples 446 us, of one 460, of all 448 (and 16,384 to 16,384 686 us, not
+// 530).  Gelu's outputs are few, and its registers too: of one tile.  Experts: columns fastest,
+// so that a tile of rows is read from memory once.
+template <bool EXPERTS, bool GELU>
 __device__ __forceinline__ Tile tile_of(uint32_t i, const Args& a) {
     Tile t;
     if (EXPERTS) {
@@ -92,11 +96,19 @@ __device__ __forceinline__ Tile tile_of(uint32_t i, const Args& a) {
         const int4 e = __ldg(a.table + 1 + l);
         t.g = e.x, t.m0 = e.y;
         t.rows = (int)min((long long)e.z, a.n - e.y);
-    } else {
+    } else if (GELU) {
         const uint32_t column = i / (uint32_t)a.m_tiles;
         t.g = (int)(column / (uint32_t)a.n_tiles);
         t.m0 = (int)(i - column * a.m_tiles) * 2 * BM;
         t.n0 = (int)(column - t.g * a.n_tiles) * BN;
+        t.rows = a.B - t.m0;
+    } else {
+        const uint32_t m = (uint32_t)a.m_tiles, n = (uint32_t)a.n_tiles;
+        const uint32_t g = i / (m * n), in = i - g * m * n, band = in / (BAND * m), j = in - band * BAND * m;
+        const uint32_t wide = min(BAND, n - band * BAND), r = j / wide;
+        t.g = (int)g;
+        t.m0 = (int)r * 2 * BM;
+        t.n0 = (int)(band * BAND + j - r * wide) * BN;
         t.rows = a.B - t.m0;
     }
     return t;
@@ -261,10 +273,10 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             uint32_t phase = 0;
             bool ok = true;
             Tile next{};
-            if (unit < tiles) next = tile_of<EXPERTS>(unit, args);
+            if (unit < tiles) next = tile_of<EXPERTS, EPI == FP4_GELU>(unit, args);
             for (uint32_t i = unit; ok && i < tiles; i += nunits) {
                 const Tile tl = next;
-                if (i + nunits < tiles) next = tile_of<EXPERTS>(i + nunits, args);
+                if (i + nunits < tiles) next = tile_of<EXPERTS, EPI == FP4_GELU>(i + nunits, args);
                 const int xrow = tl.m0 + BM * (int)rank, wrow = tl.n0 + BN / 2 * (int)rank;
                 for (int kb = 0; kb < kblocks; ++kb) {
                     if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.err, args.timeout_ns)) {
@@ -343,7 +355,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             auto skip = [&]() {
                 if (++g == groups) {
                     g = 0, i += nunits;
-                    if (i < tiles) tl = tile_of<EXPERTS>(i, args);
+                    if (i < tiles) tl = tile_of<EXPERTS, EPI == FP4_GELU>(i, args);
                 }
             };
             auto fetch = [&]() {
@@ -354,7 +366,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                 if (i < tiles) skip();
             };
             if (i < tiles) {
-                tl = tile_of<EXPERTS>(i, args);
+                tl = tile_of<EXPERTS, EPI == FP4_GELU>(i, args);
                 if (warp == 3) skip();
             }
 #pragma unroll 1
@@ -403,7 +415,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
         float b[4] = {};
         auto look_ahead = [&](uint32_t i) {
             if (i >= tiles) return;
-            next = tile_of<EXPERTS>(i, args);
+            next = tile_of<EXPERTS, EPI == FP4_GELU>(i, args);
             if (args.bias) {
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
@@ -563,6 +575,7 @@ cudaError_t launch_fp4_product(const Fp4Product& p, const Fp8Device& dev, cudaSt
     a.B = p.B, a.G = p.G, a.K = p.K, a.N = p.N;
     a.m_tiles = (p.B + 2 * BM - 1) / (2 * BM);
     a.n_tiles = (p.N + BN - 1) / BN;
+    a.band = p.epi == FP4_GELU ? 1 : BAND;
     a.kblocks = (p.K + BK - 1) / BK;
     a.nb = (int)fp4_blocks(p.K);
     a.table = p.tiles;
