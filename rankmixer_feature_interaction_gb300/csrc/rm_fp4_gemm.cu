@@ -23,13 +23,15 @@
 // columns have been read (first), and two slots of exponent bytes from column 448 (8
 // columns for x, 16 for W).  Copies and MMAs of one thread run in order, so the slots
 // need no barriers of their own.
-// Measured, T = 32, 4096 samples, bf16 out: 6144 to 1536 340 us (7.3 PFLOP/s), 1536 to
-// 6144 466 us (5.3; float32 out 620, 3.2 GB written); T = 4, 12288 to 6144 315 us (7.9).
-// Bound by what the SMs take in from L2: a k-block of a CTA is 35 KB in 512 cycles of the
-// tensor core, 68 bytes a cycle, and comes in about 630; with few k-blocks a tile also
-// by the outputs' way through shared memory, which the tensor core's operands share
-// (1536 to 6144 without an epilogue: 366 us), and with Gelu by its instructions beside
-// them (2048 samples: 252 us, 195 without).
+// Measured, T = 32, 4096 samples, bf16 out: 6144 to 1536 337 us (7.3 PFLOP/s), 1536 to
+// 6144 446 us (5.5; float32 out 610, 3.2 GB written); T = 4, 12288 to 6144 311 us (7.9).
+// With many k-blocks bound by the tensor core and by what the SMs take in from L2: 35 KB
+// of a CTA in 512 cycles, 68 bytes a cycle (6144 to 1536 303 us without an epilogue, 282
+// with half of the operands too).  With few by the outputs on their way to memory: 1536 to
+// 6144 takes 353 us without their stores and 325 without an epilogue; loads wait behind
+// them, so a stage less costs 10%, and buffers for two pieces of a warp's outputs in its
+// place gain nothing.  With Gelu by its instructions beside the product (2048 samples: 252
+// us, 195 without).
 // Every mbarrier wait is bounded in time; on expiry the CTA latches an error
 // word and all roles unwind.
 #include <cudaTypedefs.h>
