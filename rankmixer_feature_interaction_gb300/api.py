@@ -865,15 +865,15 @@ class ExpertRows:
 
     @property
     def offsets(self) -> torch.Tensor:
-        return self._arena[self._at[0]:self._at[0] + self.T * self.E + 1]
+        return self._arena.as_strided((self.T * self.E + 1,), (1,), self._at[0])
 
     @property
     def source(self) -> torch.Tensor:
-        return self._arena[self._at[1]:self._at[1] + self.B * self.T * self.E]
+        return self._arena.as_strided((self.B * self.T * self.E,), (1,), self._at[1])
 
     @property
     def slot(self) -> torch.Tensor:
-        return self._arena[self._at[2]:self._at[2] + self.B * self.T * self.E].view(self.B, self.T, self.E)
+        return self._arena.as_strided((self.B, self.T, self.E), (self.T * self.E, self.E, 1), self._at[2])
 
     def count(self) -> int:
         """The number of sorted rows (waits for the sort)."""
