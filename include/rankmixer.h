@@ -750,9 +750,9 @@ typedef struct rm_fp4_moe {
 } rm_fp4_moe;
 
 /* Serving: V[b][t] = sum over the open e of G[b][t][e] FFN_{t,e}(X[b][t]), each
- * expert as in rm_fp4_pffn_forward; where B T E D is above 2^23 an expert's
- * output is rounded to bf16 before its gate is applied.  X: device [B][T][D] of x_dtype; G: device float32
- * [B][T][E]; V: device [B][T][D] of v_dtype. */
+ * expert as in rm_fp4_pffn_forward, its output in float32 until the sum is rounded
+ * to v_dtype.  X: device [B][T][D] of x_dtype; G: device float32 [B][T][E]; V:
+ * device [B][T][D] of v_dtype. */
 RM_API rm_status rm_fp4_moe_workspace(const rm_fp4_moe *p, int B, long long *bytes);
 RM_API rm_status rm_fp4_moe_forward(const rm_fp4_moe *p, const void *X, rm_dtype x_dtype, const float *G, void *V,
                                     rm_dtype v_dtype, int B, void *work, long long work_bytes, void *stream);

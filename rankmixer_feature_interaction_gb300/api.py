@@ -1016,7 +1016,7 @@ def fp4_expert_matmul(x: Fp4Tensor, w: Fp4Tensor, rows: ExpertRows, bias: torch.
 class Fp4MoE(_Fp4FFN):
     """The Sparse-MoE per-token FFN with 4-bit experts, for serving: V[b, t] = sum over the experts
     with a gate above zero of G[b, t, e] FFN_{t,e}(X[b, t]), each on 4-bit operands as in Fp4PFFN;
-    where B T E D is above 2^23 an expert's output is rounded to bf16 before its gate is applied.
+    an expert's output stays in float32 until the sum is rounded to V's type.
 
     W1 [T, E, D, F] and W2 [T, E, F, D]: bf16 or float32 tensors (quantised here, once) or
     Fp4Tensor; b1 [T, E, F], b2 [T, E, D]; D and F multiples of 32."""
@@ -1029,7 +1029,7 @@ class Fp4MoE(_Fp4FFN):
     def forward(self, X: torch.Tensor, G: torch.Tensor, out_dtype: str = "bf16") -> torch.Tensor:
         """V [B, T, D] of X [B, T, D] and the gates G [B, T, E] (float32; RankMixer.moe_pffn_forward
         returns such gates, any others will do).  The call's workspace has room for every expert of
-        every row: B T E rows of about D / 2 + F / 2 + 2 D bytes."""
+        every row: B T E rows of about D / 2 + F / 2 + 4 D bytes."""
         B = self._rows(X)
         _fp8_device(G.get_device())
         if G.dtype != torch.float32 or G.shape != (B, self.T, self.E):

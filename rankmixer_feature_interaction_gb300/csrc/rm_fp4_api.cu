@@ -169,17 +169,15 @@ PffnWork pffn_work(const rm_fp4_pffn* p, int B, void* base) {
     w.bytes = c.used;
     return w;
 }
-// The experts' outputs wait for their gates in float32 while all that there can be take
-// no more than this, and stay in L2; in bf16 beyond, where they are the call's largest
-// traffic (1024 samples of T = 32, E = 8, D = 1536, a quarter open: 201 MB written and
-// read, 60 us of 345 more in float32).
-constexpr long long kMoeFloatBytes = 32ll << 20;
+// The experts' outputs wait for their gates in float32 at every size: in bf16 above some
+// size a sample's precision would hang on how many others it is served with (1024 samples
+// of T = 32, E = 8, D = 1536, F = 2048, a quarter open: 417 us, error in norm 0.0017; in bf16
+// 354 and 0.0024).
 struct MoeWork {
     ExpertRows rows;
     int* sort;
     Fp4View x, a;
-    void* y;
-    rm_dtype y_dtype;
+    float* y;
     long long n, bytes;
 };
 MoeWork moe_work(const rm_fp4_moe* p, int B, void* base) {
@@ -195,8 +193,7 @@ MoeWork moe_work(const rm_fp4_moe* p, int B, void* base) {
     w.sort = (int*)c.take(4 * expert_sort_work(B, p->T, p->E));
     w.x = c.rows(w.n, p->D);
     w.a = c.rows(w.n, p->F);
-    w.y_dtype = 4 * w.n * p->D <= kMoeFloatBytes ? RM_F32 : RM_BF16;
-    w.y = c.take((long long)size_of(w.y_dtype) * w.n * p->D);
+    w.y = (float*)c.take(4 * w.n * p->D);
     w.bytes = c.used;
     return w;
 }
@@ -413,11 +410,11 @@ rm_status rm_fp4_moe_forward(const rm_fp4_moe* p, const void* X, rm_dtype x_dtyp
     g.n = w.n;
     g.follows = true;
     RM_LAUNCH(fp4_product, "experts' layer 1", g, dev, s);
-    g = product(w.y_dtype, w.a, view(p->W2), p->b2, w.y, B, groups, F, D);
+    g = product(RM_F32, w.a, view(p->W2), p->b2, w.y, B, groups, F, D);
     g.tiles = w.rows.tiles;
     g.n = w.n;
     g.follows = true;
     RM_LAUNCH(fp4_product, "experts' layer 2", g, dev, s);
-    RM_LAUNCH(expert_combine, "combine", w.y, w.y_dtype == RM_F32, w.rows, G, V, v_dtype == RM_F32, w.n, D, s);
+    RM_LAUNCH(expert_combine, "combine", w.y, true, w.rows, G, V, v_dtype == RM_F32, w.n, D, s);
     return RM_OK;
 }
