@@ -75,6 +75,7 @@ struct Args {
     const float* bias;                   // [G][N] or null
     void* y;
     bool vec;                            // y's rows are 16-byte aligned
+    bool tma;                            // and no longer than 2^31 bytes, TMA's coordinates
     Fp4View o;
     int* err;
     unsigned long long timeout_ns;
@@ -133,7 +134,7 @@ __device__ __forceinline__ void staging_free(int lane) {
 
 // 64 bytes of each row of Y from column n on, through the staging: 32 existing rows by
 // TMA (which clips what lies outside Y), the last rows of an expert, whose neighbours
-// are another's, and unaligned ones by plain stores.  y: the warp's first row in tmY.
+// are another's, unaligned rows and those of more than 2^31 bytes by plain stores.  y: the warp's first row in tmY.
 template <typename OUT, bool EXPERTS>
 __device__ __forceinline__ void save_piece(const float* v, const Args& a, const CUtensorMap* tmY, int y, int plane,
                                            long long row, int n, int rows, int lane, uint32_t stage) {
@@ -150,7 +151,7 @@ __device__ __forceinline__ void save_piece(const float* v, const Args& a, const 
                          __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
     }
     if (n >= a.N) return;
-    if (a.vec && (!EXPERTS || rows >= 32)) {
+    if (a.tma && (!EXPERTS || rows >= 32)) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -608,7 +609,8 @@ cudaError_t launch_fp4_product(const Fp4Product& p, const Fp8Device& dev, cudaSt
     const bool gelu = p.epi == FP4_GELU;
     const long long bytes = gelu ? p.N / 2 : p.N * (p.epi == FP4_OUT_F32 ? 4ll : 2ll), pitch = gelu ? p.o.ld : bytes;
     const void* dst = gelu ? p.o.codes : p.y;
-    if (ok && (gelu || a.vec) &&
+    a.tma = a.vec && bytes <= 1ll << 31;
+    if (ok && (gelu || a.tma) &&
         !(p.tiles ? fp8_tensor_map(&my, u8t, dst, bytes, p.n, 1, pitch, pitch, 64, 32)
                   : fp8_tensor_map(&my, u8t, dst, bytes, p.B, p.G, p.G * pitch, pitch, 64, 32)))
         return cudaErrorInvalidValue;
