@@ -664,14 +664,15 @@ class Fp4Tensor:
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
-            at = self.c.codes - self._arena.data_ptr()
+            # (a tensor of no rows is at address 0, which ctypes reads as None)
+            at = (self.c.codes or 0) - self._arena.data_ptr()
             self._codes = self._arena[at:at + math.prod(self.cs)].view(self.cs)
         return self._codes
 
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is None:
-            at = self.c.scales - self._arena.data_ptr()
+            at = (self.c.scales or 0) - self._arena.data_ptr()
             self._scales = self._arena[at:at + math.prod(self.ss)].view(self.ss)
         return self._scales
 
