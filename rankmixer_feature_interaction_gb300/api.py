@@ -540,6 +540,12 @@ def fp8_wgrad(x: Fp8Tensor, dY: torch.Tensor, grad_dtype: str = "f32") -> tuple[
     return dW, db
 
 
+def _kept_bias(b: torch.Tensor) -> torch.Tensor:
+    """A bias as an FFN keeps it: float32, contiguous, 16-byte aligned; b itself where it is all that."""
+    b = b.to(torch.float32).contiguous()
+    return b if b.data_ptr() % 16 == 0 else b.clone()
+
+
 class Fp8PFFN:
     """The per-token FFN on 8-bit operands: V = Gelu(X W1 + b1) W2 + b2 for every token, with
     X and the hidden activation rounded to 8 bits before their products.
@@ -555,7 +561,7 @@ class Fp8PFFN:
         if _fp8_weight(self.W2, "W2") != (self.T, self.F, self.D):
             raise ValueError(f"W1 {self.W1.shape} and W2 {self.W2.shape} do not fit")
         _lib.too_long("Fp8PFFN", self.T, self.D, self.F)
-        self.b1, self.b2 = b1.to(torch.float32).contiguous(), b2.to(torch.float32).contiguous()
+        self.b1, self.b2 = _kept_bias(b1), _kept_bias(b2)
         if tuple(self.b1.shape) != (self.T, self.F) or tuple(self.b2.shape) != (self.T, self.D):
             raise ValueError(f"b1 must be [{self.T}, {self.F}] and b2 [{self.T}, {self.D}]")
         self.device_index = _fp8_device(self.W1.device_index, self.W2.device_index, self.b1.get_device(),
@@ -804,7 +810,7 @@ class _Fp4FFN:
             raise ValueError(f"W1 {self.W1.shape} and W2 {self.W2.shape} do not fit")
         _lib.too_long(type(self).__name__, *lead, D, F)
         self.lead, self.D, self.F = tuple(lead), D, F
-        self.b1, self.b2 = b1.to(torch.float32).contiguous(), b2.to(torch.float32).contiguous()
+        self.b1, self.b2 = _kept_bias(b1), _kept_bias(b2)
         if tuple(self.b1.shape) != (*lead, F) or tuple(self.b2.shape) != (*lead, D):
             raise ValueError(f"b1 must be {[*lead, F]} and b2 {[*lead, D]}")
         self.device_index = _fp8_device(self.W1.device_index, self.W2.device_index, self.b1.get_device(),

@@ -15,3 +15,16 @@ def test_a_tensor_of_no_rows_has_codes_and_scales(cols):
     assert q.codes.dtype is torch.uint8 and q.scales.dtype is torch.uint8
     again = api.Fp4Tensor(q.codes, q.scales, cols)
     assert again.shape == q.shape and again.codes is q.codes
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_bias_is_kept_aligned(dtype):
+    """Views into a larger buffer among them; a float32 bias that is as it has to be is kept itself."""
+    flat = torch.arange(64, dtype=dtype)
+    for at in range(9):
+        b = flat[at:at + 48].view(3, 16)
+        kept = api._kept_bias(b)
+        assert kept.dtype == torch.float32 and kept.is_contiguous() and kept.data_ptr() % 16 == 0 and torch.equal(kept, b.float())
+        assert (kept.data_ptr() == b.data_ptr()) == (dtype == torch.float32 and b.data_ptr() % 16 == 0)
+    kept = api._kept_bias(flat[:48].view(16, 3).T)
+    assert kept.is_contiguous() and torch.equal(kept, flat[:48].view(16, 3).T.float())
