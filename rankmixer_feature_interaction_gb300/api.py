@@ -567,7 +567,7 @@ class Fp8PFFN:
         self.device_index = _fp8_device(self.W1.device_index, self.W2.device_index, self.b1.get_device(),
                                         self.b2.get_device())
         self.c = _lib.rm_fp8_pffn(self.W1.c, self.W2.c, _ptr(self.b1), _ptr(self.b2), self.T, self.D, self.F)
-        self._bytes = {}
+        self._bytes = functools.lru_cache(maxsize=64)(functools.partial(_lib.rm_fp8_pffn_workspace, self.c))
 
     def _rows(self, X: torch.Tensor, what: str) -> int:
         _fp8_device(X.get_device(), self.device_index)
@@ -577,10 +577,8 @@ class Fp8PFFN:
         return X.shape[0]
 
     def _work(self, B: int, pass_: int, device) -> tuple[torch.Tensor, int]:
-        """This call's workspace (its size is looked up once per batch size)."""
-        n = self._bytes.get((B, pass_))
-        if n is None:
-            n = self._bytes[B, pass_] = _lib.rm_fp8_pffn_workspace(self.c, B, pass_)
+        """This call's workspace (the sizes for the batch sizes of late are kept)."""
+        n = self._bytes(B, pass_)
         return torch.empty(max(n, 16), dtype=torch.uint8, device=device), n
 
     def forward(self, X: torch.Tensor, out_dtype: str = "bf16") -> torch.Tensor:
@@ -815,7 +813,10 @@ class _Fp4FFN:
             raise ValueError(f"b1 must be {[*lead, F]} and b2 {[*lead, D]}")
         self.device_index = _fp8_device(self.W1.device_index, self.W2.device_index, self.b1.get_device(),
                                         self.b2.get_device())
-        self._bytes = {}
+
+    def _sized(self, ask) -> None:
+        """Workspaces of this FFN are as many bytes as ask(self.c, B) says."""
+        self._bytes = functools.lru_cache(maxsize=64)(functools.partial(ask, self.c))
 
     def _rows(self, X: torch.Tensor) -> int:
         _fp8_device(X.get_device(), self.device_index)
@@ -824,11 +825,9 @@ class _Fp4FFN:
                              f"{tuple(X.shape)}")
         return X.shape[0]
 
-    def _work(self, B: int, device, ask) -> tuple[torch.Tensor, int]:
-        """This call's workspace (its size is looked up once per batch size)."""
-        n = self._bytes.get(B)
-        if n is None:
-            n = self._bytes[B] = ask(self.c, B)
+    def _work(self, B: int, device) -> tuple[torch.Tensor, int]:
+        """This call's workspace (the sizes for the batch sizes of late are kept)."""
+        n = self._bytes(B)
         return torch.empty(n, dtype=torch.uint8, device=device), n
 
 
@@ -843,12 +842,13 @@ class Fp4PFFN(_Fp4FFN):
         super().__init__(W1, b1, W2, b2, 3)
         self.T, = self.lead
         self.c = _lib.rm_fp4_pffn(self.W1.c, self.W2.c, _ptr(self.b1), _ptr(self.b2), self.T, self.D, self.F)
+        self._sized(_lib.rm_fp4_pffn_workspace)
 
     def forward(self, X: torch.Tensor, out_dtype: str = "bf16") -> torch.Tensor:
         """V [B, T, D] of X [B, T, D]."""
         B = self._rows(X)
         tdt, code = _DTYPES[out_dtype]
-        work, n = self._work(B, X.device, _lib.rm_fp4_pffn_workspace)
+        work, n = self._work(B, X.device)
         V = torch.empty(X.shape, dtype=tdt, device=X.device)
         _lib.rm_fp4_pffn_forward(self.c, _ptr(X), _CODE[X.dtype], V.data_ptr(), code, B, work.data_ptr(), n,
                                  _raw_stream(self.device_index))
@@ -1032,6 +1032,7 @@ class Fp4MoE(_Fp4FFN):
         super().__init__(W1, b1, W2, b2, 4)
         self.T, self.E = self.lead
         self.c = _lib.rm_fp4_moe(self.W1.c, self.W2.c, _ptr(self.b1), _ptr(self.b2), self.T, self.E, self.D, self.F)
+        self._sized(_lib.rm_fp4_moe_workspace)
 
     def forward(self, X: torch.Tensor, G: torch.Tensor, out_dtype: str = "bf16") -> torch.Tensor:
         """V [B, T, D] of X [B, T, D] and the gates G [B, T, E] (float32; RankMixer.moe_pffn_forward
@@ -1042,7 +1043,7 @@ class Fp4MoE(_Fp4FFN):
         if G.dtype != torch.float32 or G.shape != (B, self.T, self.E):
             raise ValueError(f"G must be float32 [{B}, {self.T}, {self.E}], got {G.dtype} {tuple(G.shape)}")
         tdt, code = _DTYPES[out_dtype]
-        work, n = self._work(B, X.device, _lib.rm_fp4_moe_workspace)
+        work, n = self._work(B, X.device)
         V = torch.empty(X.shape, dtype=tdt, device=X.device)
         _lib.rm_fp4_moe_forward(self.c, _ptr(X), _CODE[X.dtype], _ptr(G), V.data_ptr(), code, B, work.data_ptr(), n,
                                 _raw_stream(self.device_index))
