@@ -63,9 +63,8 @@ constexpr int SMEM_BYTES = 1024 + STAGES * (STAGE_BYTES + SF_BYTES + SFB_BYTES) 
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 
 struct Args {
-    int B, G, K, N;                      // rows of a group (per token), groups
+    int B, G, N;                         // rows of a group (per token), groups
     int m_tiles, n_tiles, kblocks, nb;
-    int band;                            // tiles of columns of a band
     uint32_t units;                      // tiles (per token; experts: the table's length times n_tiles)
     const int4* table;                   // experts: the tiles of rows (null: per token)
     long long n;                         // experts: rows that exist
@@ -575,10 +574,9 @@ cudaError_t launch_fp4_product(const Fp4Product& p, const Fp8Device& dev, cudaSt
     RM_HOST_BOUNDS(p.epi == FP4_GELU ? p.N % 32 == 0 && fp4_holds(p.o, p.N) : fp8_on(p.y, 16));
     if (fp4_streams(p, dev)) return launch_fp4_stream(p, dev, s);
     Args a{};
-    a.B = p.B, a.G = p.G, a.K = p.K, a.N = p.N;
+    a.B = p.B, a.G = p.G, a.N = p.N;
     a.m_tiles = (p.B + 2 * BM - 1) / (2 * BM);
     a.n_tiles = (p.N + BN - 1) / BN;
-    a.band = p.epi == FP4_GELU ? 1 : BAND;
     a.kblocks = (p.K + BK - 1) / BK;
     a.nb = (int)fp4_blocks(p.K);
     a.table = p.tiles;

@@ -55,7 +55,7 @@ struct Cfg {
 };
 
 struct Args {
-    int B, G, K, N;
+    int B, G, N;
     int n_tiles, m_tiles, kblocks, nb;
     uint32_t tiles;                      // per token
     const int4* table;                   // experts: as in rm_fp4_gemm.cu
@@ -379,7 +379,7 @@ bool fp4_streams(const Fp4Product& p, const Fp8Device& dev) {
 cudaError_t launch_fp4_stream(const Fp4Product& p, const Fp8Device& dev, cudaStream_t s) {
     using namespace f4s;
     Args a{};
-    a.B = p.B, a.G = p.G, a.K = p.K, a.N = p.N;
+    a.B = p.B, a.G = p.G, a.N = p.N;
     a.n_tiles = (p.N + BM - 1) / BM;
     a.kblocks = (p.K + BK - 1) / BK;
     a.nb = (int)fp4_blocks(p.K);
