@@ -371,7 +371,7 @@ cudaError_t run_for(const CUtensorMap& mx, const CUtensorMap& mw, const Args& a,
 }  // namespace f4s
 
 bool fp4_streams(const Fp4Product& p, const Fp8Device& dev) {
-    if (p.B <= kFp4StreamMaxB) return true;
+    if (p.B <= (p.epi == FP4_GELU && !p.tiles ? kFp4StreamMaxGeluB : kFp4StreamMaxB)) return true;
     const long long m = (p.B + kFp4StreamMaxB - 1) / kFp4StreamMaxB, n = (p.N + f4s::BM - 1) / f4s::BM;
     return !p.tiles && m * n * p.G <= (p.epi == FP4_GELU ? 1 : 2) * dev.num_sms;
 }

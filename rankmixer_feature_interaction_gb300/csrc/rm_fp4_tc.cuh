@@ -142,13 +142,18 @@ struct RowScales {
 // by pairs: T = 32, K = 1536, N = 6144 27.7 and 39.2 us at 1 sample, 35.0 and 37.4 at 128
 // (of 130 samples, two tiles, 48.9 and 37.4); T = 8, K = 512, N = 2048 2.6 and 5.9, 3.5 and
 // 6.3; the experts of T = 32, E = 8, D = 1536, F = 2048 131 and 161 us at 8 samples, 180
-// and 190 at 128.  (The FFN T = 32, D = 1536, F = 6144 81.1 and 81.4 at 96, but 90.5 and
-// 83.1 at 128: Gelu of 128 rows.)
+// and 190 at 128.  Per token with Gelu, whose epilogue grows with the rows, up to 80.  FFNs
+// with layer 1 streamed and by pairs: T = 32, D = 1536, F = 6144 77 and 73 us at 80, 81 and 74
+// at 96, 91 and 75 at 128; T = 16, D = 512, F = 2048 16.3 and 16.5, 17.2 and 16.6, 18.5 and
+// 16.9; T = 4, D = 2048, F = 8192 25.3 and 26.2, 26.2 and 26.2, 27.9 and 26.7.  What has no
+// more tiles than SMs stays streamed by the rule below: T = 4, D = 512, F = 2048 12.7 and
+// 13.5, 13.2 and 13.6, 13.8 and 13.9.  (Against it: T = 16, D = 512, F = 2432, just two rounds
+// of tiles, 17.1 and 19.4, 18.0 and 19.5, 19.3 and 19.7.)
 // More samples are streamed too, per token, where that makes no more tiles than two rounds
 // of the SMs (one with Gelu): T = 8, K = 512, N = 2048, 256 samples (256 tiles) 4.9 and 6.3
 // us, K = 2048, N = 512, 512 samples (128 tiles) 5.3 and 7.2; 512 samples of the first (512
 // tiles) 7.8 and 7.3; with Gelu the FFN's 256 tiles took 18.4 us where pairs take 15.0.
-constexpr int kFp4StreamMaxB = 128;
+constexpr int kFp4StreamMaxB = 128, kFp4StreamMaxGeluB = 80;
 bool fp4_streams(const Fp4Product& p, const Fp8Device& dev);
 cudaError_t launch_fp4_stream(const Fp4Product& p, const Fp8Device& dev, cudaStream_t s);
 
