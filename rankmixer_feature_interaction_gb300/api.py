@@ -1036,7 +1036,7 @@ class Fp4MoE(_Fp4FFN):
 
     def forward(self, X: torch.Tensor, G: torch.Tensor, out_dtype: str = "bf16") -> torch.Tensor:
         """V [B, T, D] of X [B, T, D] and the gates G [B, T, E] (float32; RankMixer.moe_pffn_forward
-        returns such gates, any others will do).  The call's workspace has room for every expert of
+        returns such gates where asked (return_gates), any others will do).  The call's workspace has room for every expert of
         every row: B T E rows of about D / 2 + F / 2 + 4 D bytes."""
         B = self._rows(X)
         _fp8_device(G.get_device())

@@ -171,8 +171,8 @@ PffnWork pffn_work(const rm_fp4_pffn* p, int B, void* base) {
 }
 // The experts' outputs wait for their gates in float32 at every size: in bf16 above some
 // size a sample's precision would hang on how many others it is served with (1024 samples
-// of T = 32, E = 8, D = 1536, F = 2048, a quarter open: 417 us, error in norm 0.0017; in bf16
-// 354 and 0.0024).
+// of T = 32, E = 8, D = 1536, F = 2048, a quarter open: 409-417 us, error in norm 0.0017; in
+// bf16 354 and 0.0024).
 struct MoeWork {
     ExpertRows rows;
     int* sort;
